@@ -473,6 +473,163 @@ KDA_API kda_status kda_chunk_bwd(const void *q, const void *k, const void *v, co
                                  float *dbeta, float *dS0, void *workspace, size_t workspace_bytes,
                                  int32_t *status, void *stream);
 
+/*
+ * kda_recurrent_step_slots -- kda_recurrent_step on a pool of states: row i of the
+ * batch works on page slots[i] of pool [P, H, K, V], so that sequences come and go
+ * without their states being moved together.
+ *
+ *  slots   [N] device int32.  -1: a padded row, whose row of o is left as it is.  A
+ *          slot outside [0, P), and one that an earlier row of the batch has, are
+ *          refused: the row's state and o are left as they are.
+ *  status  optional device word (4-byte aligned): KDA_OK, or KDA_ERR_RANGE if a row
+ *          was refused.
+ * Everything else as kda_recurrent_step; N * H < 2^31.
+ */
+KDA_API kda_status kda_recurrent_step_slots(const void *q, const void *k, const void *v, const void *g,
+                                    const void *beta, kda_dtype in_dtype, float scale, float *pool,
+                                    const int32_t *slots, int P, int N, int H, int K, int V, void *o,
+                                    kda_dtype o_dtype, int32_t *status, void *stream);
+
+/*
+ * kda_short_conv_fwd -- the layer's short causal convolution as a call of its own
+ * ("kimi-k3-mlx" review, section "Attention is 93 layers ...": kernel size 4 on q, k
+ * and v), with the history carried in and out, for prompts in pieces and for decode
+ * after a prefill.  Depthwise over C channels, W taps; per sequence, with line =
+ * [history | inputs]:
+ *
+ *     p_t = bias + sum_j w[c][j] line_{t-(W-1)+j},   y_t = p_t or p_t sigmoid(p_t)
+ *
+ *  x        [B, T, C], rows ldx >= C elements apart (a slice of a wider projection).
+ *  weight   fp32 [C][W] (tap W-1 multiplies the current token); bias fp32 [C] or NULL.
+ *  conv_act 0: none, 1: SiLU.
+ *  initial  [N, W-1, C], the last inputs before each sequence, oldest first, or NULL
+ *           for zeros.
+ *  cu_seqlens, B, T, N   as kda_chunk_fwd: N sequences packed in B = 1, or B = N of T
+ *           tokens.  Rows before the first offset and behind the last one are left as
+ *           they are.
+ *  y        [B, T, C]; final_history [N, W-1, C] or NULL: the history after each
+ *           sequence (of a sequence without tokens: its initial one).
+ * x, initial, y, final_history have element type dtype; no output may overlap an input.
+ * W in {2, 3, 4}, C <= 2^20, B T < 2^31 - 65536.  Rows whose start, length and stride
+ * are whole 16-byte pieces are read in such pieces, others element by element.
+ */
+KDA_API kda_status kda_short_conv_fwd(const void *x, int64_t ldx, const float *weight, const float *bias,
+                              int conv_act, kda_dtype dtype, const void *initial,
+                              const int32_t *cu_seqlens, int B, int T, int C, int W, int N, void *y,
+                              void *final_history, void *stream);
+
+/*
+ * kda_short_conv_bwd -- gradients of L = <dy, y> + <dfinal, final_history> through
+ * kda_short_conv_fwd, with dp = dy act'(p):
+ *
+ *     dline_i = sum_j w[c][j] dp_{i+(W-1)-j} + dfinal,   dw[c][j] = sum_t dp_t line_{t-(W-1)+j},
+ *     dbias[c] = sum_t dp_t
+ *
+ *  dy [B, T, C], dfinal [N, W-1, C] or NULL, dx [B, T, C], dinitial [N, W-1, C] or
+ *  NULL: element type grad_dtype (KDA_F32, or KDA_BF16 with a KDA_BF16 dtype).
+ *  dweight fp32 [C][W]; dbias fp32 [C] or NULL.  Sums over tokens are fp32, in an
+ *  order fixed by the sizes.
+ *  workspace  at least kda_short_conv_bwd_workspace_size bytes, 16-byte aligned
+ *             (partial sums of dweight and dbias by runs of tokens).
+ * The rest as kda_short_conv_fwd.
+ */
+KDA_API size_t kda_short_conv_bwd_workspace_size(int B, int T, int C, int W);
+KDA_API kda_status kda_short_conv_bwd(const void *x, int64_t ldx, const float *weight, const float *bias,
+                              int conv_act, kda_dtype dtype, const void *initial,
+                              const int32_t *cu_seqlens, int B, int T, int C, int W, int N, const void *dy,
+                              const void *dfinal, kda_dtype grad_dtype, void *dx, float *dweight,
+                              float *dbias, void *dinitial, void *workspace, size_t workspace_bytes,
+                              void *stream);
+
+/*
+ * kda_short_conv_step -- one token of each of N sequences: y [N, C] from x [N, C] (rows
+ * ldx apart) and the histories in the pool `history` [P, W-1, C], which move on by one
+ * token.  slots [N] and status as kda_recurrent_step_slots; slots NULL: row i works on
+ * page i (P >= N).
+ */
+KDA_API kda_status kda_short_conv_step(const void *x, int64_t ldx, const float *weight, const float *bias,
+                               int conv_act, kda_dtype dtype, void *history, const int32_t *slots, int P,
+                               int N, int C, int W, void *y, int32_t *status, void *stream);
+
+/*
+ * kda_ssm_step -- one token of each of N sequences through a selective state space
+ * layer: per row and channel c of group g = c / (C / G), with S states,
+ *
+ *     d = delta + delta_bias, or softplus of it,
+ *     h_s <- exp(d A[c][s]) h_s + d u B[g][s],   y = (sum_s C[g][s] h_s + D u) (z sigmoid(z))
+ *
+ *  u, delta, z [N, C] (z may be NULL: no gate; rows ldu, ldd, ldz apart), Bm, Cm
+ *  [N, G, S] (rows ldb, ldc apart), y [N, C]: element type dtype.
+ *  A fp32 [C][S] (16-byte aligned), D, delta_bias fp32 [C] or NULL.
+ *  softplus 0 or 1.
+ *  state  fp32 pool [P, C, S], 16-byte aligned, updated in place; slots, P, status as
+ *         kda_short_conv_step.
+ * S in {8, 16, 32, 64}; C a multiple of G, C <= 2^20.
+ */
+KDA_API kda_status kda_ssm_step(const void *u, int64_t ldu, const void *delta, int64_t ldd, const float *A,
+                        const void *Bm, int64_t ldb, const void *Cm, int64_t ldc, const float *D,
+                        const void *z, int64_t ldz, const float *delta_bias, int softplus, kda_dtype dtype,
+                        float *state, const int32_t *slots, int P, int N, int C, int G, int S, void *y,
+                        int32_t *status, void *stream);
+
+/*
+ * Pages of a cache.  A pool holds P pages (a sequence's recurrent state, its
+ * convolution history, or page_tokens tokens' rows); several pools (layers) can go by
+ * one set of books:
+ *
+ *   refs   int32 [P]: how many page table entries hold the page; 0: free.
+ *   tables int32 [S, width]: the pages of each sequence in order, -1 behind them.
+ *   lens   int32 [S]: the tokens of each sequence.
+ *
+ * Everything is on the device and stream-ordered, and results are functions of the
+ * arguments alone: the lowest free pages are given out first, requests are served in
+ * order.  status: optional device word, KDA_OK or KDA_ERR_RANGE if a request was
+ * refused; a refused request changes nothing, the others are carried out.
+ *
+ * kda_pages_alloc -- pages[i] = the i-th free page, with refs 1; -1 (refused) where
+ * there are no more.
+ *
+ * kda_pages_free -- one reference less for each of the n pages listed (-1: skipped;
+ * a page may be listed as often as it has references).  Refused: a page out of range
+ * or without references.
+ *
+ * kda_pages_fork -- sequence children[k] becomes a copy of parents[k], k < n <= 65536
+ * (either -1: skipped): its table row shares the parent's full pages (one reference
+ * more each); a last page that is not full is written on by both, so the child gets a
+ * free page for it and (src[k], dst[k]) is the copy to make in every pool with
+ * kda_pages_copy, else (-1, -1).  The child's former pages are the caller's to free
+ * first.  A page that holds a sequence's whole state is never full: page_tokens larger
+ * than any length.  Refused (src = dst = -1): rows out of [0, S), a child that is
+ * another request's child or any request's parent, a length outside [0, width *
+ * page_tokens], a parent's entry that is not a page in use, and no free page left.
+ *
+ * kda_pages_compact -- moves the used pages into the first places of the pools: with
+ * `used` of the P pages in use, the m-th used page at or behind place `used` moves to
+ * the m-th free place before it.  src, dst [P / 2] are the copies to make in every
+ * pool, -1 behind the last; refs and the `entries` table entries (NULL and 0: none)
+ * follow.  workspace: kda_pages_compact_workspace_size bytes.  Refused: an entry that
+ * is neither -1 nor a page in use (those at or behind place `used` are looked at).
+ *
+ * kda_pages_copy -- page dst[i] becomes a copy of page src[i] in pool [P, page_bytes]
+ * (either -1: skipped).  Refused: pages out of range, and a destination that a later
+ * pair writes or another pair reads, so that the order of the copies does not matter.
+ * page_bytes a multiple of 16, pool 16-byte aligned.  workspace:
+ * kda_pages_copy_workspace_size bytes.
+ */
+KDA_API kda_status kda_pages_alloc(int32_t *refs, int P, int n, int32_t *pages, int32_t *status, void *stream);
+KDA_API kda_status kda_pages_free(int32_t *refs, int P, const int32_t *pages, int64_t n, int32_t *status,
+                          void *stream);
+KDA_API kda_status kda_pages_fork(int32_t *tables, int32_t *lens, int S, int width, int page_tokens,
+                          int32_t *refs, int P, const int32_t *parents, const int32_t *children, int n,
+                          int32_t *src, int32_t *dst, int32_t *status, void *stream);
+KDA_API size_t kda_pages_compact_workspace_size(int P);
+KDA_API kda_status kda_pages_compact(int32_t *refs, int P, int32_t *tables, int64_t entries, int32_t *src,
+                             int32_t *dst, void *workspace, size_t workspace_bytes, int32_t *status,
+                             void *stream);
+KDA_API size_t kda_pages_copy_workspace_size(int P, int n);
+KDA_API kda_status kda_pages_copy(void *pool, int P, int64_t page_bytes, const int32_t *src, const int32_t *dst,
+                          int n, void *workspace, size_t workspace_bytes, int32_t *status, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

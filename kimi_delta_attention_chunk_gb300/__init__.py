@@ -22,8 +22,17 @@ from .kda import (  # noqa: F401
     library_path,
     load_library,
     output_gate,
+    pages_alloc,
+    pages_compact,
+    pages_copy,
+    pages_fork,
+    pages_free,
     recurrent_step,
     set_wait_limit,
+    short_conv_bwd,
+    short_conv_fwd,
+    short_conv_step,
+    ssm_step,
     state_compose,
     trace_events,
     workspace_size,

@@ -71,6 +71,22 @@ kda_status check_workspace(kda_dtype in_dtype, int B, int T, int H, int K, int V
     return KDA_OK;
 }
 
+// The decode step's sizes, types and pointers (N = 0: nothing to do, pointers are not looked at).
+kda_status check_step(const void* q, const void* k, const void* v, const void* g, const void* beta,
+                      kda_dtype in_dtype, const float* state, int N, int H, int K, int V, const void* o,
+                      kda_dtype o_dtype) {
+    if (N < 0 || H <= 0) return KDA_ERR_INVALID_ARG;
+    if (!head_size_ok(K) || !head_size_ok(V)) return KDA_ERR_UNSUPPORTED;
+    if (!dtype_ok(in_dtype) || !dtype_ok(o_dtype)) return KDA_ERR_UNSUPPORTED;
+    if (N == 0) return KDA_OK;
+    if (!q || !k || !v || !g || !beta || !state || !o) return KDA_ERR_INVALID_ARG;
+    const void* ptrs[] = {q, k, v, g, state, o};
+    for (const void* p : ptrs)
+        if (!kda_host::aligned16(p)) return KDA_ERR_INVALID_ARG;
+    if ((uintptr_t)beta % (in_dtype == KDA_BF16 ? 2 : 4)) return KDA_ERR_INVALID_ARG;
+    return KDA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -195,18 +211,26 @@ kda_status kda_recurrent_step(const void* q, const void* k, const void* v, const
                               const void* beta, kda_dtype in_dtype, float scale, float* state,
                               int N, int H, int K, int V, void* o, kda_dtype o_dtype,
                               void* stream) {
-    if (N < 0 || H <= 0) return KDA_ERR_INVALID_ARG;
-    if (!head_size_ok(K) || !head_size_ok(V)) return KDA_ERR_UNSUPPORTED;
-    if (!dtype_ok(in_dtype) || !dtype_ok(o_dtype)) return KDA_ERR_UNSUPPORTED;
-    if (N == 0) return KDA_OK;
-    if (!q || !k || !v || !g || !beta || !state || !o) return KDA_ERR_INVALID_ARG;
-    const void* ptrs[] = {q, k, v, g, state, o};
-    for (const void* p : ptrs)
-        if (!kda_host::aligned16(p)) return KDA_ERR_INVALID_ARG;
-    if ((uintptr_t)beta % (in_dtype == KDA_BF16 ? 2 : 4)) return KDA_ERR_INVALID_ARG;
-    cudaStream_t st = (cudaStream_t)stream;
+    const kda_status s = check_step(q, k, v, g, beta, in_dtype, state, N, H, K, V, o, o_dtype);
+    if (s != KDA_OK || N == 0) return s;
     return from_cuda(kda::decode_step(in_dtype, o_dtype, K, V, q, k, v, g, beta,
-                                      resolve_scale(scale, K), state, N, H, o, st));
+                                      resolve_scale(scale, K), state, N, H, o, kda::DecodeSlots{},
+                                      (cudaStream_t)stream));
+}
+
+kda_status kda_recurrent_step_slots(const void* q, const void* k, const void* v, const void* g,
+                                    const void* beta, kda_dtype in_dtype, float scale, float* pool,
+                                    const int32_t* slots, int P, int N, int H, int K, int V, void* o,
+                                    kda_dtype o_dtype, int32_t* status, void* stream) {
+    const kda_status s = check_step(q, k, v, g, beta, in_dtype, pool, N, H, K, V, o, o_dtype);
+    if (s != KDA_OK) return s;
+    if (P < 0 || (N > 0 && (P == 0 || !slots)) || (uintptr_t)slots % 4 || (uintptr_t)status % 4) return KDA_ERR_INVALID_ARG;
+    if ((int64_t)N * H > 0x7fffffffLL) return KDA_ERR_INVALID_ARG;
+    cudaStream_t st = (cudaStream_t)stream;
+    if (status && cudaMemsetAsync(status, 0, sizeof(int32_t), st) != cudaSuccess) return KDA_ERR_CUDA;
+    if (N == 0) return KDA_OK;
+    return from_cuda(kda::decode_step(in_dtype, o_dtype, K, V, q, k, v, g, beta, resolve_scale(scale, K), pool, N,
+                                      H, o, kda::DecodeSlots{slots, P, status}, st));
 }
 
 kda_status kda_output_gate(const float* o, const void* gate, kda_dtype gate_dtype, const float* weight,

@@ -71,10 +71,17 @@ void inject_wait_timeout(int kernel);
 // last kernel (any may be null); the call consumes them.
 void trace_set(void* begin, void* split, void* end);
 
-// Single-token decode.
+// Single-token decode; with slots, state is a pool of P pages and row n works on page slots[n]
+// (status, may be null: KDA_ERR_RANGE set by a row that is refused).
+struct DecodeSlots {
+    const int32_t* slots;
+    int P;
+    int32_t* status;
+};
 cudaError_t decode_step(kda_dtype in_dt, kda_dtype out_dt, int K, int V, const void* q,
                         const void* k, const void* v, const void* g, const void* beta,
-                        float scale, float* state, int N, int H, void* o, cudaStream_t st);
+                        float scale, float* state, int N, int H, void* o, const DecodeSlots& sl,
+                        cudaStream_t st);
 
 // Output gate: out = o / sqrt(mean_V(o^2) + eps) * w * sigmoid(gate), rows of V.
 cudaError_t output_gate(kda_dtype gate_dt, kda_dtype out_dt, int V, const float* o, const void* gate,

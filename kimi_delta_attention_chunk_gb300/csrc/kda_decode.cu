@@ -14,17 +14,22 @@
 // "The A_log shape mismatch ...").
 #include "kda_chunk.h"
 #include "kda_common.cuh"
+#include "kda_slots.cuh"
 
 namespace kda {
 
 constexpr int kDecodeThreads = 256;
 
-template <typename TIn, typename TOut, int K, int V>
+// kSlots: state is a pool of P pages [H, K, V], and row n works on page slots[n] (a row without a
+// page, or refused, leaves its state and its row of o alone).  The page's loads are issued before
+// the slots are looked through for repeats, which they hide.
+template <typename TIn, typename TOut, int K, int V, bool kSlots>
 __global__ void __launch_bounds__(kDecodeThreads, 2)
 decode_step_kernel(const TIn* __restrict__ q, const TIn* __restrict__ k,
                    const TIn* __restrict__ v, const TIn* __restrict__ g,
                    const TIn* __restrict__ beta, float scale, float* __restrict__ state,
-                   TOut* __restrict__ o) {
+                   TOut* __restrict__ o, const int32_t* __restrict__ slots, int H, int P,
+                   int32_t* __restrict__ status) {
     constexpr int NT = kDecodeThreads;
     constexpr int LPR = V / 4;   // threads per state row (one float4 each)
     constexpr int RG = NT / LPR; // row groups
@@ -36,11 +41,20 @@ decode_step_kernel(const TIn* __restrict__ q, const TIn* __restrict__ k,
     const int c4 = tid % LPR;
     const int rg = tid / LPR;
 
-    float4* S = reinterpret_cast<float4*>(state + nh * K * V);
+    int row = 0, page = 0;
+    int64_t at = nh;
+    if constexpr (kSlots) {
+        row = (int)(nh / H);
+        page = page_of_row(slots, row, P);
+        at = (int64_t)max(page, 0) * H + nh % H;
+    }
+    float4* S = reinterpret_cast<float4*>(state + at * K * V);
     float4 s[RPT];
     // Issue every state load first so that the whole slice is in flight.
 #pragma unroll
     for (int i = 0; i < RPT; ++i) s[i] = __ldcs(&S[(rg + i * RG) * LPR + c4]);
+    if constexpr (kSlots)
+        if (row_refused(slots, row, page, status)) return;
 
     __shared__ float eg[K], kk[K], qq[K];
     __shared__ __align__(16) float red_a[RG][V];
@@ -102,34 +116,40 @@ decode_step_kernel(const TIn* __restrict__ q, const TIn* __restrict__ k,
 template <typename TIn, typename TOut, int K, int V>
 static cudaError_t launch_decode(const void* q, const void* k, const void* v, const void* g,
                                  const void* beta, float scale, float* state, int N, int H,
-                                 void* o, cudaStream_t st) {
+                                 void* o, const DecodeSlots& sl, cudaStream_t st) {
     const int64_t blocks = (int64_t)N * H;
     if (blocks == 0) return cudaSuccess;
-    decode_step_kernel<TIn, TOut, K, V><<<(unsigned)blocks, kDecodeThreads, 0, st>>>(
-        (const TIn*)q, (const TIn*)k, (const TIn*)v, (const TIn*)g, (const TIn*)beta, scale,
-        state, (TOut*)o);
+    if (sl.slots)
+        decode_step_kernel<TIn, TOut, K, V, true><<<(unsigned)blocks, kDecodeThreads, 0, st>>>(
+            (const TIn*)q, (const TIn*)k, (const TIn*)v, (const TIn*)g, (const TIn*)beta, scale,
+            state, (TOut*)o, sl.slots, H, sl.P, sl.status);
+    else
+        decode_step_kernel<TIn, TOut, K, V, false><<<(unsigned)blocks, kDecodeThreads, 0, st>>>(
+            (const TIn*)q, (const TIn*)k, (const TIn*)v, (const TIn*)g, (const TIn*)beta, scale,
+            state, (TOut*)o, nullptr, H, 0, nullptr);
     return cudaGetLastError();
 }
 
 template <typename TIn, typename TOut>
 static cudaError_t dispatch_kv(int K, int V, const void* q, const void* k, const void* v,
                                const void* g, const void* beta, float scale, float* state, int N,
-                               int H, void* o, cudaStream_t st) {
-    if (K == 128 && V == 128) return launch_decode<TIn, TOut, 128, 128>(q, k, v, g, beta, scale, state, N, H, o, st);
-    if (K == 128 && V == 64) return launch_decode<TIn, TOut, 128, 64>(q, k, v, g, beta, scale, state, N, H, o, st);
-    if (K == 64 && V == 128) return launch_decode<TIn, TOut, 64, 128>(q, k, v, g, beta, scale, state, N, H, o, st);
-    return launch_decode<TIn, TOut, 64, 64>(q, k, v, g, beta, scale, state, N, H, o, st);
+                               int H, void* o, const DecodeSlots& sl, cudaStream_t st) {
+    if (K == 128 && V == 128) return launch_decode<TIn, TOut, 128, 128>(q, k, v, g, beta, scale, state, N, H, o, sl, st);
+    if (K == 128 && V == 64) return launch_decode<TIn, TOut, 128, 64>(q, k, v, g, beta, scale, state, N, H, o, sl, st);
+    if (K == 64 && V == 128) return launch_decode<TIn, TOut, 64, 128>(q, k, v, g, beta, scale, state, N, H, o, sl, st);
+    return launch_decode<TIn, TOut, 64, 64>(q, k, v, g, beta, scale, state, N, H, o, sl, st);
 }
 
 cudaError_t decode_step(kda_dtype in_dt, kda_dtype out_dt, int K, int V, const void* q,
                         const void* k, const void* v, const void* g, const void* beta,
-                        float scale, float* state, int N, int H, void* o, cudaStream_t st) {
+                        float scale, float* state, int N, int H, void* o, const DecodeSlots& sl,
+                        cudaStream_t st) {
     if (in_dt == KDA_BF16) {
-        if (out_dt == KDA_F32) return dispatch_kv<__nv_bfloat16, float>(K, V, q, k, v, g, beta, scale, state, N, H, o, st);
-        return dispatch_kv<__nv_bfloat16, __nv_bfloat16>(K, V, q, k, v, g, beta, scale, state, N, H, o, st);
+        if (out_dt == KDA_F32) return dispatch_kv<__nv_bfloat16, float>(K, V, q, k, v, g, beta, scale, state, N, H, o, sl, st);
+        return dispatch_kv<__nv_bfloat16, __nv_bfloat16>(K, V, q, k, v, g, beta, scale, state, N, H, o, sl, st);
     }
-    if (out_dt == KDA_F32) return dispatch_kv<float, float>(K, V, q, k, v, g, beta, scale, state, N, H, o, st);
-    return dispatch_kv<float, __nv_bfloat16>(K, V, q, k, v, g, beta, scale, state, N, H, o, st);
+    if (out_dt == KDA_F32) return dispatch_kv<float, float>(K, V, q, k, v, g, beta, scale, state, N, H, o, sl, st);
+    return dispatch_kv<float, __nv_bfloat16>(K, V, q, k, v, g, beta, scale, state, N, H, o, sl, st);
 }
 
 }  // namespace kda

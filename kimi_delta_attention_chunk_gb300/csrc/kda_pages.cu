@@ -1,0 +1,442 @@
+// Pages of a cache: taking, sharing, giving back, copying and closing up the pages of pools that
+// hold sequences' recurrent states, convolution histories or token rows.
+//
+// refs[p] counts the page table entries that hold page p; a page with none is free, and the lowest
+// free pages are given out first, so every result is a function of the arguments alone.  The
+// bookkeeping is integers: one read of refs and of the table rows concerned.  It is bound by
+// latency, so each operation is one kernel of one cluster (eight blocks when there are many pages,
+// else one): the blocks count their share of refs, exchange the counts through distributed shared
+// memory, and place their own pages, with hardware cluster barriers between and no waiting on
+// memory.  The payload moves in kda_pages_copy, bound by HBM.
+#include <cooperative_groups.h>
+
+#include "kda_layer.h"
+#include "kda_segments.cuh"
+
+namespace kda {
+
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kThreads = 1024;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMostBlocks = 8;
+// One block counts this many pages at least as fast as a cluster starts and meets.
+constexpr int kPagesOfOneBlock = 8192;
+
+// Sum of x over the block's threads before this one; *all: over all of them.  `tmp` holds
+// kWarps + 1 ints; the block meets twice.
+__device__ __forceinline__ int block_before(int x, int* tmp, int* all) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int inc = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+    }
+    if (lane == 31) tmp[warp] = inc;
+    __syncthreads();
+    if (warp == 0) {
+        const int w = tmp[lane];
+        int s = w;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += y;
+        }
+        tmp[lane] = s - w;
+        if (lane == 31) tmp[kWarps] = s;
+    }
+    __syncthreads();
+    *all = tmp[kWarps];
+    return tmp[warp] + inc - x;
+}
+
+struct Shared {
+    int tmp[kWarps + 1];
+    int mine[2];  // this block's counts, read by the others
+};
+
+// Sums over the cluster's earlier blocks (base) and over all of them (all) of two counts.
+__device__ __forceinline__ void cluster_sums(Shared& sh, int c0, int c1, int (&base)[2], int (&all)[2]) {
+    cg::cluster_group cl = cg::this_cluster();
+    if (threadIdx.x == 0) {
+        sh.mine[0] = c0;
+        sh.mine[1] = c1;
+    }
+    cl.sync();
+    base[0] = base[1] = all[0] = all[1] = 0;
+    const int rank = cl.block_rank(), blocks = cl.num_blocks();
+    for (int r = 0; r < blocks; ++r) {
+        const int* m = cl.map_shared_rank(sh.mine, r);
+        const int a = m[0], b = m[1];
+        if (r < rank) {
+            base[0] += a;
+            base[1] += b;
+        }
+        all[0] += a;
+        all[1] += b;
+    }
+    cl.sync();  // before anyone writes `mine` again or leaves
+}
+
+// The block's share [lo, hi) of n things, whole tiles of kThreads.
+__device__ __forceinline__ void share(int n, int& lo, int& hi) {
+    cg::cluster_group cl = cg::this_cluster();
+    const int blocks = cl.num_blocks(), tiles = (n - 1) / kThreads + 1;
+    const int per = n > 0 ? (tiles + blocks - 1) / blocks : 0;
+    const int64_t a = (int64_t)cl.block_rank() * per * kThreads;
+    lo = (int)min(a, (int64_t)n);
+    hi = (int)min(a + (int64_t)per * kThreads, (int64_t)n);
+}
+
+// How many of [lo, hi) satisfy f (every thread gets the sum).
+template <typename F>
+__device__ __forceinline__ int count_if(Shared& sh, int lo, int hi, F f) {
+    int c = 0;
+    for (int i = lo + (int)threadIdx.x; i < hi; i += kThreads) c += f(i) ? 1 : 0;
+    int all;
+    block_before(c, sh.tmp, &all);
+    __syncthreads();
+    return all;
+}
+
+// put(rank, i) for every i of [lo, hi) with f(i), rank counting on from `base` in order of i;
+// stops where the ranks reach `most`.
+template <typename F, typename G>
+__device__ __forceinline__ void place_if(Shared& sh, int lo, int hi, int base, int most, F f, G put) {
+    for (int i0 = lo; i0 < hi && base < most; i0 += kThreads) {
+        const int i = i0 + threadIdx.x;
+        const bool is = i < hi && f(i);
+        int all;
+        const int before = block_before(is ? 1 : 0, sh.tmp, &all);
+        if (is && base + before < most) put(base + before, i);
+        base += all;
+        __syncthreads();
+    }
+}
+
+__device__ __forceinline__ void report(int32_t* status) {
+    if (status) *status = KDA_ERR_RANGE;
+}
+
+// ---- taking and giving back ------------------------------------------------------------------
+
+__global__ void __launch_bounds__(kThreads) pages_alloc_kernel(int32_t* refs, int P, int n, int32_t* out,
+                                                               int32_t* status) {
+    __shared__ Shared sh;
+    int lo, hi, base[2], all[2];
+    share(P, lo, hi);
+    const auto is_free = [&](int i) { return refs[i] == 0; };
+    cluster_sums(sh, count_if(sh, lo, hi, is_free), 0, base, all);
+    place_if(sh, lo, hi, base[0], n, is_free, [&](int rank, int i) {
+        out[rank] = i;
+        refs[i] = 1;
+    });
+    if (all[0] < n) {
+        cg::cluster_group cl = cg::this_cluster();
+        for (int i = all[0] + cl.block_rank() * kThreads + threadIdx.x; i < n; i += cl.num_blocks() * kThreads) out[i] = -1;
+        if (threadIdx.x == 0) report(status);
+    }
+}
+
+__global__ void __launch_bounds__(256) pages_free_kernel(int32_t* refs, int P, const int32_t* pages, int64_t n,
+                                                         int32_t* status) {
+    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < n; i += gridDim.x * 256ll) {
+        const int p = pages[i];
+        if (p == -1) continue;
+        bool ok = p >= 0 && p < P;
+        if (ok) {
+            // a count that is 0 already stays so
+            int have = refs[p];
+            for (;;) {
+                if (have <= 0) {
+                    ok = false;
+                    break;
+                }
+                const int was = atomicCAS(refs + p, have, have - 1);
+                if (was == have) break;
+                have = was;
+            }
+        }
+        if (!ok) report(status);
+    }
+}
+
+// ---- forking ---------------------------------------------------------------------------------
+
+// What becomes of request k, kept in dst_out[k] between the phases.
+constexpr int kNeedsPage = 2, kSharesOnly = 1, kNothing = 0;
+constexpr int kRefused = -2;
+
+__global__ void __launch_bounds__(kThreads) pages_fork_kernel(int32_t* tables, int32_t* lens, int S, int width,
+                                                              int page_tokens, int32_t* refs, int P,
+                                                              const int32_t* parents, const int32_t* children, int n,
+                                                              int32_t* src_out, int32_t* dst_out, int32_t* status) {
+    __shared__ Shared sh;
+    cg::cluster_group cl = cg::this_cluster();
+    const int lane = threadIdx.x & 31;
+    const int warp = cl.block_rank() * kWarps + (threadIdx.x >> 5), warps = cl.num_blocks() * kWarps;
+
+    // 1. which requests stand: a warp looks each over
+    for (int k = warp; k < n; k += warps) {
+        const int p = parents[k], c = children[k];
+        int what = kNothing;
+        if (p != -1 && c != -1) {
+            bool bad = p < 0 || p >= S || c < 0 || c >= S;
+            for (int j = lane; j < n && !bad; j += 32) {
+                const int pj = parents[j], cj = children[j];
+                if (pj != -1 && cj != -1 && (pj == c || (j != k && cj == c))) bad = true;
+            }
+            bad = __any_sync(0xffffffffu, bad);
+            int full = 0;
+            bool part = false;
+            if (!bad) {
+                const int len = lens[p];
+                if (len < 0 || len > (int64_t)width * page_tokens) {
+                    bad = true;
+                } else {
+                    full = len / page_tokens;
+                    part = len % page_tokens != 0;
+                }
+            }
+            const int held = full + (part ? 1 : 0);
+            for (int j = lane; j < held && !bad; j += 32) {
+                const int page = tables[(int64_t)p * width + j];
+                if (page < 0 || page >= P || refs[page] <= 0) bad = true;
+            }
+            bad = __any_sync(0xffffffffu, bad);
+            what = bad ? kNothing : part ? kNeedsPage : kSharesOnly;
+            if (bad && lane == 0) report(status);
+        }
+        if (lane == 0) dst_out[k] = what;
+    }
+    cl.sync();
+
+    // 2. the free pages in order (in src_out, for now), and how many requests before each need one
+    int lo, hi, klo, khi, base[2], all[2];
+    share(P, lo, hi);
+    share(n, klo, khi);
+    const auto is_free = [&](int i) { return refs[i] == 0; };
+    const auto needs = [&](int k) { return dst_out[k] == kNeedsPage; };
+    const int free_here = count_if(sh, lo, hi, is_free);
+    const int need_here = count_if(sh, klo, khi, needs);
+    cluster_sums(sh, free_here, need_here, base, all);
+    place_if(sh, lo, hi, base[0], all[1], is_free, [&](int rank, int i) { src_out[rank] = i; });
+    cl.sync();
+
+    // 3. the requests' pages, in order; those that find none are refused
+    for (int k0 = klo, rank = base[1]; k0 < khi; k0 += kThreads) {
+        const int k = k0 + threadIdx.x;
+        const int what = k < khi ? dst_out[k] : kNothing;
+        int here;
+        const int before = block_before(what == kNeedsPage ? 1 : 0, sh.tmp, &here);
+        if (k < khi) {
+            int page = what == kSharesOnly ? -1 : kRefused;
+            if (what == kNeedsPage) {
+                if (rank + before < all[0]) page = src_out[rank + before];
+                else report(status);
+            }
+            dst_out[k] = page;
+        }
+        rank += here;
+        __syncthreads();
+    }
+    cl.sync();
+
+    // 4. the children's rows
+    for (int k = warp; k < n; k += warps) {
+        const int page = dst_out[k];
+        __syncwarp();
+        if (page == kRefused) {
+            if (lane == 0) src_out[k] = dst_out[k] = -1;
+            continue;
+        }
+        const int p = parents[k], c = children[k], len = lens[p], full = len / page_tokens;
+        const int32_t* from = tables + (int64_t)p * width;
+        int32_t* to = tables + (int64_t)c * width;
+        for (int j = lane; j < width; j += 32) {
+            int e = -1;
+            if (j < full) {
+                e = from[j];
+                atomicAdd(refs + e, 1);
+            } else if (j == full && page >= 0) {
+                e = page;
+                refs[e] = 1;
+            }
+            to[j] = e;
+        }
+        if (lane == 0) {
+            src_out[k] = page >= 0 ? from[full] : -1;
+            lens[c] = len;
+        }
+    }
+}
+
+// ---- closing up ------------------------------------------------------------------------------
+
+// remap[0] is the number of used pages; remap[1 + p] the new place of a used page p behind it, -1
+// of a free one.
+__global__ void __launch_bounds__(kThreads) pages_compact_kernel(int32_t* refs, int P, int32_t* src_out,
+                                                                 int32_t* dst_out, int32_t* remap) {
+    __shared__ Shared sh;
+    cg::cluster_group cl = cg::this_cluster();
+    int lo, hi, base[2], all[2];
+    share(P, lo, hi);
+    const int used_here = count_if(sh, lo, hi, [&](int i) { return refs[i] != 0; });
+    cluster_sums(sh, used_here, 0, base, all);
+    const int live = all[0];
+    const auto hole = [&](int i) { return i < live && refs[i] == 0; };
+    const auto tail = [&](int i) { return i >= live && refs[i] != 0; };
+    const int holes = count_if(sh, lo, hi, hole), tails = count_if(sh, lo, hi, tail);
+    cluster_sums(sh, holes, tails, base, all);
+    const int moves = all[0];  // as many used pages behind `live` as holes before it
+    place_if(sh, lo, hi, base[0], moves, hole, [&](int rank, int i) { dst_out[rank] = i; });
+    place_if(sh, lo, hi, base[1], moves, tail, [&](int rank, int i) { src_out[rank] = i; });
+    if (remap) {
+        for (int i = max(lo, live) + (int)threadIdx.x; i < hi; i += kThreads)
+            if (refs[i] == 0) remap[1 + i] = -1;
+        if (cl.block_rank() == 0 && threadIdx.x == 0) remap[0] = live;
+    }
+    cl.sync();
+    const int first = cl.block_rank() * kThreads + threadIdx.x, step = cl.num_blocks() * kThreads;
+    for (int m = first; m < P / 2; m += step) {
+        if (m >= moves) {
+            src_out[m] = dst_out[m] = -1;
+            continue;
+        }
+        const int s = src_out[m], d = dst_out[m];
+        if (remap) remap[1 + s] = d;
+        refs[d] = refs[s];
+        refs[s] = 0;
+    }
+}
+
+__global__ void __launch_bounds__(256) pages_remap_kernel(int32_t* tables, int64_t entries, int P, const int32_t* remap,
+                                                          int32_t* status) {
+    const int live = remap[0];
+    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < entries; i += gridDim.x * 256ll) {
+        const int e = tables[i];
+        if (e == -1 || (e >= 0 && e < live)) continue;
+        const int to = e >= 0 && e < P ? remap[1 + e] : -1;
+        if (to >= 0) tables[i] = to;
+        else report(status);  // an entry that held no used page stays as it is
+    }
+}
+
+// ---- copying ---------------------------------------------------------------------------------
+
+constexpr int kCopyThreads = 256;
+constexpr int kCopyVec = 4;                                  // 16-byte pieces of a thread in one go
+constexpr int kCopyPiece = kCopyThreads * kCopyVec * 16;     // bytes of a block in one go
+
+// marks, all zero before: [0] pairs listed, [1, 1 + P) the last pair (+ 1) that writes a page,
+// [1 + P, 1 + 2 P) whether a pair reads it, then the list.
+__global__ void __launch_bounds__(256) pages_mark_kernel(const int32_t* src, const int32_t* dst, int n, int P,
+                                                         int32_t* marks, int32_t* status) {
+    for (int i = blockIdx.x * 256 + threadIdx.x; i < n; i += gridDim.x * 256) {
+        const int s = src[i], d = dst[i];
+        if (s == -1 || d == -1) continue;
+        if (s < 0 || s >= P || d < 0 || d >= P) {
+            report(status);
+            continue;
+        }
+        if (s == d) continue;
+        atomicMax(marks + 1 + d, i + 1);
+        marks[1 + P + s] = 1;
+        marks[1 + 2 * (int64_t)P + atomicAdd(marks, 1)] = i;
+    }
+}
+
+__global__ void __launch_bounds__(kCopyThreads, 8) pages_copy_kernel(char* pool, int64_t page_bytes, const int32_t* src,
+                                                                     const int32_t* dst, int P, const int32_t* marks,
+                                                                     int32_t* status) {
+    const int pairs = marks[0];
+    const int64_t pieces = (page_bytes + kCopyPiece - 1) / kCopyPiece, items = pairs * pieces;
+    for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+        const int i = marks[1 + 2 * (int64_t)P + it / pieces];
+        const int64_t at = it % pieces * kCopyPiece;
+        const int s = src[i], d = dst[i];
+        // a later pair writes this page, or a pair reads it: left alone
+        if (marks[1 + d] != i + 1 || marks[1 + P + d] != 0) {
+            if (threadIdx.x == 0 && at == 0) report(status);
+            continue;
+        }
+        const uint4* from = reinterpret_cast<const uint4*>(pool + s * page_bytes + at);
+        uint4* to = reinterpret_cast<uint4*>(pool + d * page_bytes + at);
+        const int left = (int)(min((int64_t)kCopyPiece, page_bytes - at) / 16);
+        uint4 r[kCopyVec];
+#pragma unroll
+        for (int v = 0; v < kCopyVec; ++v)
+            if (v * kCopyThreads + (int)threadIdx.x < left) r[v] = __ldcs(from + v * kCopyThreads + threadIdx.x);
+#pragma unroll
+        for (int v = 0; v < kCopyVec; ++v)
+            if (v * kCopyThreads + (int)threadIdx.x < left) __stcs(to + v * kCopyThreads + threadIdx.x, r[v]);
+    }
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch_cluster(void (*kern)(KArgs...), int P, cudaStream_t st, Args... args) {
+    const int blocks = P <= kPagesOfOneBlock ? 1 : kMostBlocks;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = blocks;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
+}
+
+}  // namespace
+
+cudaError_t pages_alloc(int32_t* refs, int P, int n, int32_t* out, int32_t* status, cudaStream_t st) {
+    return launch_cluster(pages_alloc_kernel, P, st, refs, P, n, out, status);
+}
+
+cudaError_t pages_free(int32_t* refs, int P, const int32_t* pages, int64_t n, int32_t* status, cudaStream_t st) {
+    const int64_t blocks = (n + 255) / 256;
+    pages_free_kernel<<<(unsigned)(blocks < 1216 ? blocks : 1216), 256, 0, st>>>(refs, P, pages, n, status);
+    return cudaGetLastError();
+}
+
+cudaError_t pages_fork(int32_t* tables, int32_t* lens, int S, int width, int page_tokens, int32_t* refs, int P,
+                       const int32_t* parents, const int32_t* children, int n, int32_t* src, int32_t* dst,
+                       int32_t* status, cudaStream_t st) {
+    return launch_cluster(pages_fork_kernel, P, st, tables, lens, S, width, page_tokens, refs, P, parents, children, n,
+                          src, dst, status);
+}
+
+size_t pages_compact_workspace(int P) { return ((size_t)P + 1) * 4; }
+
+cudaError_t pages_compact(int32_t* refs, int P, int32_t* tables, int64_t entries, int32_t* src, int32_t* dst, void* ws,
+                          int32_t* status, cudaStream_t st) {
+    int32_t* remap = entries > 0 ? static_cast<int32_t*>(ws) : nullptr;
+    cudaError_t e = launch_cluster(pages_compact_kernel, P, st, refs, P, src, dst, remap);
+    if (e != cudaSuccess || entries == 0) return e;
+    const int64_t blocks = (entries + 255) / 256;
+    pages_remap_kernel<<<(unsigned)(blocks < 1216 ? blocks : 1216), 256, 0, st>>>(tables, entries, P, remap, status);
+    return cudaGetLastError();
+}
+
+size_t pages_copy_workspace(int P, int n) { return (1 + 2 * (size_t)P + n) * 4; }
+
+cudaError_t pages_copy(void* pool, int P, int64_t page_bytes, const int32_t* src, const int32_t* dst, int n, void* ws,
+                       int32_t* status, cudaStream_t st) {
+    int32_t* marks = static_cast<int32_t*>(ws);
+    cudaError_t e = cudaMemsetAsync(marks, 0, (1 + 2 * (size_t)P) * 4, st);
+    if (e != cudaSuccess) return e;
+    const int blocks = (n + 255) / 256;
+    pages_mark_kernel<<<blocks < 1216 ? blocks : 1216, 256, 0, st>>>(src, dst, n, P, marks, status);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    const int64_t items = n * ((page_bytes + kCopyPiece - 1) / kCopyPiece);
+    pages_copy_kernel<<<(unsigned)(items < 152 * 8 ? items : 152 * 8), kCopyThreads, 0, st>>>(
+        static_cast<char*>(pool), page_bytes, src, dst, P, marks, status);
+    return cudaGetLastError();
+}
+
+}  // namespace kda

@@ -1,0 +1,26 @@
+// Scalar pieces of the selective state space scan.
+#pragma once
+
+#include "kda_segments.cuh"
+
+namespace kda {
+
+// log(1 + e) for 0 <= e <= 1 from log(1 + e) = 2 atanh(r), r = e / (2 + e) <= 1/3, by the series
+// r + r^3/3 + r^5/5 + ...: the first term left out is below 2e-8 of the sum.  (A logarithm of the
+// rounded 1 + e would lose the small e that ordinary step sizes have.)
+__device__ __forceinline__ float log1p_unit(float e) {
+    const float r = __fdividef(e, 2.0f + e), q = r * r;
+    float s = 1.0f / 13.0f;
+    s = fmaf(s, q, 1.0f / 11.0f);
+    s = fmaf(s, q, 1.0f / 9.0f);
+    s = fmaf(s, q, 1.0f / 7.0f);
+    s = fmaf(s, q, 1.0f / 5.0f);
+    s = fmaf(s, q, 1.0f / 3.0f);
+    s = fmaf(s * q, r, r);
+    return s + s;
+}
+
+// log(1 + e^x) = max(x, 0) + log(1 + e^-|x|)
+__device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.0f) + log1p_unit(ex2(-kLog2e * fabsf(x))); }
+
+}  // namespace kda

@@ -24,7 +24,7 @@ _STATUS = {0: "KDA_OK", 1: "KDA_ERR_INVALID_ARG", 2: "KDA_ERR_UNSUPPORTED", 3: "
 
 # (name, restype, argtypes) of every exported symbol of include/kda.h
 _vp, _fp, _i32p = ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p
-_i, _f, _sz, _u32 = ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_uint32
+_i, _f, _sz, _u32, _i64 = ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_uint32, ctypes.c_int64
 SIGNATURES = {
     "kda_status_string": (ctypes.c_char_p, [_i]),
     "kda_abi_version": (_i, []),
@@ -52,6 +52,22 @@ SIGNATURES = {
                            _fp, _fp, _fp, _fp, _fp, _fp, _fp, _fp, _vp, _sz, _i32p, _vp]),
     "kda_recurrent_bwd": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _f, _fp, _i32p, _i, _i, _i, _i, _i, _i,
                                _fp, _fp, _fp, _fp, _fp, _fp, _fp, _fp, _vp, _sz, _i32p, _vp]),
+    "kda_recurrent_step_slots": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _f, _fp, _i32p, _i, _i, _i, _i, _i, _vp, _i,
+                                      _i32p, _vp]),
+    "kda_short_conv_fwd": (_i, [_vp, _i64, _fp, _fp, _i, _i, _vp, _i32p, _i, _i, _i, _i, _i, _vp, _vp, _vp]),
+    "kda_short_conv_bwd_workspace_size": (_sz, [_i, _i, _i, _i]),
+    "kda_short_conv_bwd": (_i, [_vp, _i64, _fp, _fp, _i, _i, _vp, _i32p, _i, _i, _i, _i, _i, _vp, _vp, _i, _vp, _fp,
+                                _fp, _vp, _vp, _sz, _vp]),
+    "kda_short_conv_step": (_i, [_vp, _i64, _fp, _fp, _i, _i, _vp, _i32p, _i, _i, _i, _i, _vp, _i32p, _vp]),
+    "kda_ssm_step": (_i, [_vp, _i64, _vp, _i64, _fp, _vp, _i64, _vp, _i64, _fp, _vp, _i64, _fp, _i, _i, _fp, _i32p,
+                          _i, _i, _i, _i, _i, _vp, _i32p, _vp]),
+    "kda_pages_alloc": (_i, [_i32p, _i, _i, _i32p, _i32p, _vp]),
+    "kda_pages_free": (_i, [_i32p, _i, _i32p, _i64, _i32p, _vp]),
+    "kda_pages_fork": (_i, [_i32p, _i32p, _i, _i, _i, _i32p, _i, _i32p, _i32p, _i, _i32p, _i32p, _i32p, _vp]),
+    "kda_pages_compact_workspace_size": (_sz, [_i]),
+    "kda_pages_compact": (_i, [_i32p, _i, _i32p, _i64, _i32p, _i32p, _vp, _sz, _i32p, _vp]),
+    "kda_pages_copy_workspace_size": (_sz, [_i, _i]),
+    "kda_pages_copy": (_i, [_vp, _i, _i64, _i32p, _i32p, _i, _vp, _sz, _i32p, _vp]),
 }
 
 
@@ -118,6 +134,65 @@ def _dt_of(dtype) -> int:
     if dtype == torch.float32:
         return KDA_F32
     raise TypeError(f"unsupported dtype {dtype}")
+
+
+def _here(*tensors):
+    """Every tensor given lies on one CUDA device, the current one."""
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("tensors passed to libkda must be CUDA tensors")
+        if t.device.index != torch.cuda.current_device():
+            raise ValueError(f"a tensor lies on {t.device}, the current device is {torch.cuda.current_device()}")
+
+
+def _int32(*tensors):
+    for t in tensors:
+        if t is not None and t.dtype != torch.int32:
+            raise TypeError(f"expected an int32 tensor, got {t.dtype}")
+
+
+def _f32(*tensors):
+    for t in tensors:
+        if t is not None and t.dtype != torch.float32:
+            raise TypeError(f"expected a float32 tensor, got {t.dtype}")
+
+
+def _like(ref, *tensors):
+    """Every tensor given has ref's element type."""
+    for t in tensors:
+        if t is not None and t.dtype != ref.dtype:
+            raise TypeError(f"expected {ref.dtype}, got {t.dtype}")
+
+
+def _shape(name, t, shape):
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _rows(name, t, lead: int):
+    """(pointer, row stride in elements) of a tensor whose first ``lead`` dimensions number
+    rows a fixed stride apart, each row's elements lying side by side."""
+    if t is None:
+        return None, 0
+    width = 1
+    for d in reversed(range(lead, t.dim())):
+        if t.shape[d] != 1 and t.stride(d) != width:
+            raise ValueError(f"{name}: the elements of a row must lie side by side")
+        width *= t.shape[d]
+    ld, rows = None, 1
+    for d in reversed(range(lead)):
+        if t.shape[d] != 1 and t.numel():
+            if ld is None:
+                ld = t.stride(d)
+            elif t.stride(d) != ld * rows:
+                raise ValueError(f"{name}: rows must lie a fixed stride apart")
+            rows *= t.shape[d]
+    ld = width if ld is None else ld
+    if ld < width:
+        raise ValueError(f"{name}: rows must not overlap")
+    return ctypes.c_void_p(t.data_ptr()), ld
 
 
 def workspace_size(in_dtype, B: int, T: int, H: int, K: int, V: int, N: int, packed: bool) -> int:
@@ -266,16 +341,33 @@ def trace_events(begin=None, split=None, end=None):
     lib.kda_trace_events(*h)
 
 
-def recurrent_step(q, k, v, g, beta, state, scale: float | None = None, o_dtype=torch.float32, o=None):
+def recurrent_step(q, k, v, g, beta, state, scale: float | None = None, o_dtype=torch.float32, o=None,
+                   slots=None, status=None):
     """One decode token per sequence; ``state`` [N,H,K,V] fp32 is updated in place.
 
-    q, k, g: [N,H,K]; v: [N,H,V]; beta: [N,H].  Returns o [N,H,V].
+    q, k, g: [N,H,K]; v: [N,H,V]; beta: [N,H].  Returns o [N,H,V].  With ``slots``
+    (device int32 [N]) ``state`` is a pool [P,H,K,V] and row i works on page
+    ``slots[i]`` (-1: a padded row; its row of o is left as it is, so pass ``o`` to
+    keep its contents).  ``status``: an optional device int32 word, 5 =
+    KDA_ERR_RANGE when a row's slot was out of range or an earlier row's.
     """
     lib = load_library()
     N, H, K = q.shape
     V = v.shape[-1]
     if o is None:
         o = torch.empty((N, H, V), dtype=o_dtype, device=q.device)
+    if slots is not None:
+        _here(q, k, v, g, beta, state, o, slots, status)
+        _int32(slots, status)
+        if tuple(state.shape[1:]) != (H, K, V) or slots.numel() != N:
+            raise ValueError(f"state must be [P, {H}, {K}, {V}] and slots [{N}]")
+        st = lib.kda_recurrent_step_slots(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _dt(q),
+                                          float(scale or 0.0), _ptr(state), _ptr(slots), state.shape[0], N, H,
+                                          K, V, _ptr(o), _dt(o), _ptr(status), _stream(q.device))
+        _check("kda_recurrent_step_slots", st)
+        return o
+    if status is not None:
+        raise ValueError("status goes with slots")
     st = lib.kda_recurrent_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _dt(q),
                                 float(scale or 0.0), _ptr(state), N, H, K, V, _ptr(o), _dt(o),
                                 _stream(q.device))
@@ -404,3 +496,231 @@ def chunk_bwd(q, k, v, g, beta, dO, dS_T=None, scale: float | None = None, initi
                             _stream(dev))
     _check(name, st)
     return out
+
+
+def _conv_check(x, weight, bias, conv_act):
+    C, W = weight.shape
+    _f32(weight, bias)
+    _shape("x", x, tuple(x.shape[:-1]) + (C,))
+    _shape("bias", bias, (C,))
+    if conv_act not in (0, 1):
+        raise ValueError("conv_act is 0 (none) or 1 (SiLU)")
+    return C, W
+
+
+def _sequences(t, cu_seqlens):
+    """N of a [B, T, ...] tensor with or without packed sequences."""
+    if cu_seqlens is None:
+        return t.shape[0]
+    _int32(cu_seqlens)
+    if t.shape[0] != 1:
+        raise ValueError("packed sequences need B == 1")
+    return cu_seqlens.numel() - 1
+
+
+def short_conv_fwd(x, weight, bias=None, conv_act: int = 0, initial=None, cu_seqlens=None,
+                   output_final: bool = True, y=None, final=None):
+    """The short causal convolution as a call of its own: ``y_t = act(bias + sum_j
+    weight[:, j] * line_{t-(W-1)+j})`` per sequence, line = [history | inputs].
+
+    x: [B,T,C] (bf16 or fp32; rows may be slices of wider ones); weight: [C,W] fp32, W in
+    2..4; bias: [C] fp32 or None; conv_act: 0 none, 1 SiLU; initial: [N,W-1,C] the last
+    inputs before each sequence, oldest first (None: zeros); ``cu_seqlens`` as for
+    :func:`chunk_fwd`.  Returns (y [B,T,C], final history [N,W-1,C] or None).  Rows that
+    belong to no sequence are left as they are.
+    """
+    lib = load_library()
+    C, W = _conv_check(x, weight, bias, conv_act)
+    B, T, _ = x.shape
+    N = _sequences(x, cu_seqlens)
+    _here(x, weight, bias, initial, cu_seqlens, y, final)
+    _like(x, initial, y, final)
+    _shape("initial", initial, (N, W - 1, C))
+    _shape("y", y, (B, T, C))
+    _shape("final", final, (N, W - 1, C))
+    if y is None:
+        y = torch.empty((B, T, C), dtype=x.dtype, device=x.device)
+    if final is None and output_final:
+        final = torch.empty((N, W - 1, C), dtype=x.dtype, device=x.device)
+    px, ldx = _rows("x", x, 2)
+    st = lib.kda_short_conv_fwd(px, ldx, _ptr(weight), _ptr(bias), conv_act, _dt(x), _ptr(initial), _ptr(cu_seqlens),
+                                B, T, C, W, N, _ptr(y), _ptr(final), _stream(x.device))
+    _check("kda_short_conv_fwd", st)
+    return y, final
+
+
+def short_conv_bwd(x, weight, dy, bias=None, conv_act: int = 0, initial=None, cu_seqlens=None, dfinal=None,
+                   workspace=None):
+    """Gradients of <dy, y> + <dfinal, final> through :func:`short_conv_fwd` (same
+    arguments).  dy [B,T,C] and dfinal [N,W-1,C] share a type: x's, or fp32.  Returns a
+    dict: dx [B,T,C] and dinitial [N,W-1,C] (None without ``initial``) in dy's type, dweight
+    [C,W] and dbias [C] (None without ``bias``) fp32."""
+    lib = load_library()
+    C, W = _conv_check(x, weight, bias, conv_act)
+    B, T, _ = x.shape
+    N = _sequences(x, cu_seqlens)
+    _here(x, weight, dy, bias, initial, cu_seqlens, dfinal, workspace)
+    _like(x, initial)
+    _like(dy, dfinal)
+    _shape("dy", dy, (B, T, C))
+    _shape("initial", initial, (N, W - 1, C))
+    _shape("dfinal", dfinal, (N, W - 1, C))
+    dev = x.device
+    out = {"dx": torch.empty((B, T, C), dtype=dy.dtype, device=dev),
+           "dweight": torch.empty((C, W), dtype=torch.float32, device=dev),
+           "dbias": torch.empty(C, dtype=torch.float32, device=dev) if bias is not None else None,
+           "dinitial": torch.empty((N, W - 1, C), dtype=dy.dtype, device=dev) if initial is not None else None}
+    ws, ws_bytes = _workspace(int(lib.kda_short_conv_bwd_workspace_size(B, T, C, W)), dev, workspace)
+    px, ldx = _rows("x", x, 2)
+    st = lib.kda_short_conv_bwd(px, ldx, _ptr(weight), _ptr(bias), conv_act, _dt(x), _ptr(initial), _ptr(cu_seqlens),
+                                B, T, C, W, N, _ptr(dy), _ptr(dfinal), _dt(dy), _ptr(out["dx"]), _ptr(out["dweight"]),
+                                _ptr(out["dbias"]), _ptr(out["dinitial"]), _ptr(ws), ws_bytes, _stream(dev))
+    _check("kda_short_conv_bwd", st)
+    return out
+
+
+def short_conv_step(x, history, weight, bias=None, conv_act: int = 0, slots=None, y=None, status=None):
+    """One token of each of N sequences: x [N,C]; ``history`` [P,W-1,C] is updated in place
+    (row i's page is ``slots[i]``, or i without slots; -1 is a padded row).  Returns y
+    [N,C].  ``slots``/``status`` as for :func:`recurrent_step`."""
+    lib = load_library()
+    C, W = _conv_check(x, weight, bias, conv_act)
+    N = x.shape[0]
+    _here(x, history, weight, bias, slots, y, status)
+    _like(x, history, y)
+    _int32(slots, status)
+    _shape("history", history, (history.shape[0], W - 1, C))
+    _shape("slots", slots, (N,))
+    _shape("y", y, (N, C))
+    if y is None:
+        y = torch.empty((N, C), dtype=x.dtype, device=x.device)
+    px, ldx = _rows("x", x, 1)
+    st = lib.kda_short_conv_step(px, ldx, _ptr(weight), _ptr(bias), conv_act, _dt(x), _ptr(history), _ptr(slots),
+                                 history.shape[0], N, C, W, _ptr(y), _ptr(status), _stream(x.device))
+    _check("kda_short_conv_step", st)
+    return y
+
+
+def _ssm_check(u, delta, A, Bm, Cm, D, z, delta_bias):
+    """(C, G, S) of a scan call whose u is [..., C] and Bm, Cm [..., G, S]."""
+    C, S = A.shape
+    lead = tuple(u.shape[:-1])
+    G = Bm.shape[-2]
+    _like(u, delta, Bm, Cm, z)
+    _f32(A, D, delta_bias)
+    _shape("u", u, lead + (C,))
+    _shape("delta", delta, lead + (C,))
+    _shape("z", z, lead + (C,))
+    _shape("Bm", Bm, lead + (G, S))
+    _shape("Cm", Cm, lead + (G, S))
+    _shape("D", D, (C,))
+    _shape("delta_bias", delta_bias, (C,))
+    return C, G, S
+
+
+def ssm_step(u, delta, A, Bm, Cm, state, D=None, z=None, delta_bias=None, softplus: bool = True, slots=None,
+             y=None, status=None):
+    """One token of each of N sequences through a selective state space layer: ``h <-
+    exp(d A) h + d u B``, ``y = (C . h + D u) * silu(z)`` with ``d = softplus(delta +
+    delta_bias)``.
+
+    u, delta, z: [N,C]; A: [C,S] fp32, S in 8, 16, 32, 64; Bm, Cm: [N,G,S], channel c in
+    group c // (C // G); D, delta_bias: [C] fp32; ``state`` fp32 [P,C,S] is updated in place.
+    Returns y [N,C].  ``slots``/``status`` as for :func:`recurrent_step`."""
+    lib = load_library()
+    C, G, S = _ssm_check(u, delta, A, Bm, Cm, D, z, delta_bias)
+    N = u.shape[0]
+    _here(u, delta, A, Bm, Cm, state, D, z, delta_bias, slots, y, status)
+    _like(u, y)
+    _f32(state)
+    _int32(slots, status)
+    _shape("state", state, (state.shape[0], C, S))
+    _shape("slots", slots, (N,))
+    _shape("y", y, (N, C))
+    if y is None:
+        y = torch.empty((N, C), dtype=u.dtype, device=u.device)
+    (pu, ldu), (pd, ldd), (pz, ldz) = _rows("u", u, 1), _rows("delta", delta, 1), _rows("z", z, 1)
+    (pb, ldb), (pc, ldc) = _rows("Bm", Bm, 1), _rows("Cm", Cm, 1)
+    st = lib.kda_ssm_step(pu, ldu, pd, ldd, _ptr(A), pb, ldb, pc, ldc, _ptr(D), pz, ldz, _ptr(delta_bias), int(softplus),
+                          _dt(u), _ptr(state), _ptr(slots), state.shape[0], N, C, G, S, _ptr(y), _ptr(status),
+                          _stream(u.device))
+    _check("kda_ssm_step", st)
+    return y
+
+
+def pages_alloc(refs, n: int, pages=None, status=None):
+    """Take ``n`` free pages, the lowest first: their numbers, int32 [n], -1 where there are
+    no more; ``refs`` [P] (references of each page, 0: free) is updated.  ``status`` of
+    every pages call: an optional device int32 word, 5 = KDA_ERR_RANGE when a request
+    was refused (a refused request changes nothing)."""
+    lib = load_library()
+    _here(refs, pages, status)
+    _int32(refs, pages, status)
+    _shape("pages", pages, (n,))
+    if pages is None:
+        pages = torch.empty(n, dtype=torch.int32, device=refs.device)
+    _check("kda_pages_alloc", lib.kda_pages_alloc(_ptr(refs), refs.numel(), n, _ptr(pages), _ptr(status),
+                                                  _stream(refs.device)))
+    return pages
+
+
+def pages_free(refs, pages, status=None):
+    """Give back one reference of each page listed in ``pages`` (int32, any shape; -1 entries
+    are skipped)."""
+    lib = load_library()
+    _here(refs, pages, status)
+    _int32(refs, pages, status)
+    _check("kda_pages_free", lib.kda_pages_free(_ptr(refs), refs.numel(), _ptr(pages), pages.numel(), _ptr(status),
+                                                _stream(refs.device)))
+
+
+def pages_fork(tables, lens, refs, parents, children, page_tokens: int, status=None):
+    """Sequence ``children[k]`` becomes a copy of ``parents[k]`` in the books: it shares the
+    parent's full pages, and a last page that is not full is to be copied.  tables: int32
+    [S,width] (-1 behind a sequence's pages); lens: int32 [S] tokens.  Returns (src, dst),
+    int32 [n]: the copies to make in every pool with :func:`pages_copy` (-1: none).  Free
+    the child's former pages first."""
+    lib = load_library()
+    n = parents.numel()
+    S, width = tables.shape
+    _here(tables, lens, refs, parents, children, status)
+    _int32(tables, lens, refs, parents, children, status)
+    _shape("lens", lens, (S,))
+    _shape("children", children, parents.shape)
+    src, dst = torch.empty((2, n), dtype=torch.int32, device=refs.device)
+    st = lib.kda_pages_fork(_ptr(tables), _ptr(lens), S, width, int(page_tokens), _ptr(refs), refs.numel(), _ptr(parents),
+                            _ptr(children), n, _ptr(src), _ptr(dst), _ptr(status), _stream(refs.device))
+    _check("kda_pages_fork", st)
+    return src, dst
+
+
+def pages_compact(refs, tables=None, workspace=None, status=None):
+    """Close up the pools: used pages behind the number of used pages move into the free
+    places before it, in order; ``refs`` and the table entries follow.  Returns (src, dst),
+    int32 [P // 2]: the copies to make in every pool with :func:`pages_copy` (-1: none)."""
+    lib = load_library()
+    _here(refs, tables, workspace, status)
+    _int32(refs, tables, status)
+    P = refs.numel()
+    src, dst = torch.empty((2, P // 2), dtype=torch.int32, device=refs.device)
+    ws, ws_bytes = _workspace(int(lib.kda_pages_compact_workspace_size(P)), refs.device, workspace)
+    st = lib.kda_pages_compact(_ptr(refs), P, _ptr(tables), 0 if tables is None else tables.numel(), _ptr(src), _ptr(dst),
+                               _ptr(ws), ws_bytes, _ptr(status), _stream(refs.device))
+    _check("kda_pages_compact", st)
+    return src, dst
+
+
+def pages_copy(pool, src, dst, workspace=None, status=None):
+    """Copy page ``src[i]`` of ``pool`` ([P, ...], any type, a page's bytes a multiple of 16)
+    onto page ``dst[i]``; -1 entries are skipped.  A destination that a later pair writes or
+    another pair reads is refused."""
+    lib = load_library()
+    _here(pool, src, dst, workspace, status)
+    _int32(src, dst, status)
+    _shape("dst", dst, src.shape)
+    P, n = pool.shape[0], src.numel()
+    page_bytes = pool.numel() // P * pool.element_size() if P else 16
+    ws, ws_bytes = _workspace(int(lib.kda_pages_copy_workspace_size(P, n)), pool.device, workspace)
+    st = lib.kda_pages_copy(_ptr(pool), P, page_bytes, _ptr(src), _ptr(dst), n, _ptr(ws), ws_bytes, _ptr(status),
+                            _stream(pool.device))
+    _check("kda_pages_copy", st)
