@@ -573,6 +573,58 @@ KDA_API kda_status kda_ssm_step(const void *u, int64_t ldu, const void *delta, i
                         int32_t *status, void *stream);
 
 /*
+ * kda_ssm_scan_fwd -- kda_ssm_step's recurrence over the tokens of N sequences.
+ *
+ *  u, delta, z [B, T, C] (rows ldu, ldd, ldz >= C apart; z may be NULL), Bm, Cm
+ *  [B, T, G, S] (rows ldb, ldc >= G S apart), y [B, T, C]: element type dtype.
+ *  A fp32 [C][S], D, delta_bias, softplus, S as kda_ssm_step.  The state between tokens
+ *  is fp32; a run of tokens is carried on by exp(A sum d), so A sum d must stay below
+ *  88 over any stretch of a sequence (it does where d >= 0 and A <= 0).
+ *  initial_state fp32 [N, C, S] (16-byte aligned) or NULL for zeros; final_state the
+ *  same or NULL; they must not overlap.
+ *  cu_seqlens, B, T, N   as kda_short_conv_fwd; rows that belong to no sequence are
+ *           left as they are.
+ *  workspace  at least kda_ssm_scan_fwd_workspace_size bytes, 16-byte aligned (the runs
+ *           that the tokens are cut into where channels and sequences alone do not
+ *           fill the machine; 0 where they do).
+ */
+KDA_API size_t kda_ssm_scan_fwd_workspace_size(int B, int T, int C, int G, int S, int N, int packed);
+KDA_API kda_status kda_ssm_scan_fwd(const void *u, int64_t ldu, const void *delta, int64_t ldd, const float *A,
+                            const void *Bm, int64_t ldb, const void *Cm, int64_t ldc, const float *D,
+                            const void *z, int64_t ldz, const float *delta_bias, int softplus,
+                            kda_dtype dtype, const float *initial_state, const int32_t *cu_seqlens, int B,
+                            int T, int C, int G, int S, int N, void *y, float *final_state,
+                            void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * kda_ssm_scan_bwd -- gradients of L = <dy, y> + <dfinal_state, final_state> through
+ * kda_ssm_scan_fwd:
+ *
+ *     yb = dy silu(z),  dh_t = C_t yb_t + a_{t+1} dh_{t+1},  q1 = sum_s dh B,  e = dh a h_{t-1}
+ *     du = d q1 + D yb,  dd = sum_s e A + u q1,  ddelta = dd softplus'(delta + delta_bias)
+ *     dA += d e,  dB_t = sum_c d u dh,  dC_t = sum_c yb h,  dD = sum_t yb u,
+ *     dz = dy (sum_s C h + D u) silu'(z),  ddelta_bias = sum_t ddelta,  dinitial_state = a_0 dh_0
+ *
+ *  dy, du, ddelta, dz [B, T, C], dB, dC [B, T, G, S] (sums over the channels of a group):
+ *  contiguous, element type grad_dtype (KDA_F32, or KDA_BF16 with a KDA_BF16 dtype).
+ *  dz is given exactly if z is.
+ *  dfinal_state, dinitial_state fp32 [N, C, S] or NULL, 16-byte aligned.
+ *  dA fp32 [C][S]; dD, ddelta_bias fp32 [C] or NULL.
+ *  workspace  at least kda_ssm_scan_bwd_workspace_size bytes, 16-byte aligned.
+ * B T <= 4194240.  Sums are fp32, in an order fixed by the sizes.  The rest as
+ * kda_ssm_scan_fwd.
+ */
+KDA_API size_t kda_ssm_scan_bwd_workspace_size(int B, int T, int C, int G, int S, int N, int packed);
+KDA_API kda_status kda_ssm_scan_bwd(const void *u, int64_t ldu, const void *delta, int64_t ldd, const float *A,
+                            const void *Bm, int64_t ldb, const void *Cm, int64_t ldc, const float *D,
+                            const void *z, int64_t ldz, const float *delta_bias, int softplus,
+                            kda_dtype dtype, const float *initial_state, const int32_t *cu_seqlens, int B,
+                            int T, int C, int G, int S, int N, const void *dy, const float *dfinal_state,
+                            kda_dtype grad_dtype, void *du, void *ddelta, float *dA, void *dB, void *dC,
+                            float *dD, void *dz, float *ddelta_bias, float *dinitial_state,
+                            void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * Pages of a cache.  A pool holds P pages (a sequence's recurrent state, its
  * convolution history, or page_tokens tokens' rows); several pools (layers) can go by
  * one set of books:

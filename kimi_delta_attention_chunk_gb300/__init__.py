@@ -32,6 +32,8 @@ from .kda import (  # noqa: F401
     short_conv_bwd,
     short_conv_fwd,
     short_conv_step,
+    ssm_scan_bwd,
+    ssm_scan_fwd,
     ssm_step,
     state_compose,
     trace_events,

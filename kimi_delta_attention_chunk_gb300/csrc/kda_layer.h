@@ -65,6 +65,33 @@ struct SsmStepParams {
 };
 cudaError_t ssm_step(kda_dtype dt, const SsmStepParams& p, cudaStream_t st);
 
+struct SsmScanParams {
+    const void *u, *delta, *z;      // [total][ld*]; z may be null
+    int64_t ldu, ldd, ldz;
+    const void *Bm, *Cm;            // [total][ldb / ldc], G groups of S values a row
+    int64_t ldb, ldc;
+    const float *A, *D, *bias;      // [C][S], [C] or null, [C] or null
+    int softplus;
+    const float* initial;           // [N][C][S] or null
+    const int32_t* cu;
+    int T, N, C, G, S, total;
+    void* y;                        // [total][C]
+    float* final_state;             // [N][C][S] or null
+    // backward
+    const void* dy;                 // [total][C], gradient type
+    const float* dfinal;            // [N][C][S] or null
+    void *du, *ddelta, *dz;         // [total][C], gradient type; dz null with z
+    void *dB, *dC;                  // [total][G][S], gradient type
+    float *dA, *dD, *dbias;         // [C][S], [C] or null, [C] or null
+    float* dinitial;                // [N][C][S] or null
+    void* ws;
+};
+// Device bytes a call needs at p's sizes (p.cu null or not matters, no pointer is followed).
+size_t ssm_scan_workspace(const SsmScanParams& p);
+cudaError_t ssm_scan_fwd(kda_dtype dt, const SsmScanParams& p, cudaStream_t st);
+size_t ssm_scan_bwd_workspace(const SsmScanParams& p);
+cudaError_t ssm_scan_bwd(kda_dtype dt, kda_dtype gdt, const SsmScanParams& p, cudaStream_t st);
+
 cudaError_t pages_alloc(int32_t* refs, int P, int n, int32_t* out, int32_t* status, cudaStream_t st);
 cudaError_t pages_free(int32_t* refs, int P, const int32_t* pages, int64_t n, int32_t* status, cudaStream_t st);
 cudaError_t pages_fork(int32_t* tables, int32_t* lens, int S, int width, int page_tokens, int32_t* refs, int P,

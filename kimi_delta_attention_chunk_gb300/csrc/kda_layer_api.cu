@@ -59,6 +59,40 @@ kda_status check_conv(int64_t ldx, const float* weight, const float* bias, int C
     return KDA_OK;
 }
 
+// Tokens of a scan's backward pass: 65535 chunks of 64.
+constexpr int kMostBwdTokens = 65535 * 64;
+// Stands for offsets where only their presence matters.
+const int32_t* const kPacked = reinterpret_cast<const int32_t*>(16);
+
+kda_status scan_sizes(kda::SsmScanParams& p, int B, int T, int C, int G, int S, int N, const int32_t* cu) {
+    const kda_status s = check_stream(B, T, C, N, cu);
+    if (s != KDA_OK) return s;
+    if (G <= 0 || C % G != 0) return KDA_ERR_INVALID_ARG;
+    if (S != 8 && S != 16 && S != 32 && S != 64) return KDA_ERR_UNSUPPORTED;
+    p.cu = cu; p.T = T; p.N = N; p.C = C; p.G = G; p.S = S; p.total = B * T;
+    return KDA_OK;
+}
+
+// The inputs that the forward and backward scans share.
+kda_status scan_inputs(const kda::SsmScanParams& p, kda_dtype dtype) {
+    if (!dtype_ok(dtype)) return KDA_ERR_UNSUPPORTED;
+    if (p.softplus != 0 && p.softplus != 1) return KDA_ERR_INVALID_ARG;
+    const int64_t vec = (int64_t)p.G * p.S;
+    if (p.ldu < p.C || p.ldd < p.C || (p.z && p.ldz < p.C) || p.ldb < vec || p.ldc < vec) return KDA_ERR_INVALID_ARG;
+    if (!p.A || (p.total > 0 && (!p.u || !p.delta || !p.Bm || !p.Cm))) return KDA_ERR_INVALID_ARG;
+    for (const void* q : {p.u, p.delta, p.Bm, p.Cm, p.z})
+        if (!aligned(q, size_of(dtype))) return KDA_ERR_INVALID_ARG;
+    if (!kda_host::aligned16(p.A) || !kda_host::aligned16(p.initial)) return KDA_ERR_INVALID_ARG;
+    if (!aligned(p.D, 4) || !aligned(p.bias, 4)) return KDA_ERR_INVALID_ARG;
+    return KDA_OK;
+}
+#define SCAN_INPUT_SPANS(in, p, es)                                                                                       \
+    const Span in[] = {rows(p.u, p.total, p.ldu, p.C, es), rows(p.delta, p.total, p.ldd, p.C, es),                        \
+                       rows(p.z, p.total, p.ldz, p.C, es), rows(p.Bm, p.total, p.ldb, (int64_t)p.G * p.S, es),            \
+                       rows(p.Cm, p.total, p.ldc, (int64_t)p.G * p.S, es), {p.A, (size_t)p.C * p.S * 4},                  \
+                       {p.D, (size_t)p.C * 4}, {p.bias, (size_t)p.C * 4}, {p.initial, (size_t)p.N * p.C * p.S * 4},       \
+                       {p.cu, (size_t)(p.N + 1) * 4}}
+
 }  // namespace
 
 extern "C" {
@@ -180,6 +214,79 @@ kda_status kda_ssm_step(const void* u, int64_t ldu, const void* delta, int64_t l
     p.A = A; p.D = D; p.bias = delta_bias; p.softplus = softplus;
     p.state = state; p.slots = slots; p.N = N; p.P = P; p.C = C; p.G = G; p.S = S; p.y = y; p.status = status;
     return from_cuda(kda::ssm_step(dtype, p, st));
+}
+
+size_t kda_ssm_scan_fwd_workspace_size(int B, int T, int C, int G, int S, int N, int packed) {
+    kda::SsmScanParams p{};
+    if (scan_sizes(p, B, T, C, G, S, N, packed ? kPacked : nullptr) != KDA_OK) return 0;
+    return kda::ssm_scan_workspace(p);
+}
+
+kda_status kda_ssm_scan_fwd(const void* u, int64_t ldu, const void* delta, int64_t ldd, const float* A, const void* Bm,
+                            int64_t ldb, const void* Cm, int64_t ldc, const float* D, const void* z, int64_t ldz,
+                            const float* delta_bias, int softplus, kda_dtype dtype, const float* initial_state,
+                            const int32_t* cu_seqlens, int B, int T, int C, int G, int S, int N, void* y,
+                            float* final_state, void* workspace, size_t workspace_bytes, void* stream) {
+    kda::SsmScanParams p{};
+    kda_status s = scan_sizes(p, B, T, C, G, S, N, cu_seqlens);
+    if (s != KDA_OK) return s;
+    p.u = u; p.delta = delta; p.z = z; p.ldu = ldu; p.ldd = ldd; p.ldz = ldz;
+    p.Bm = Bm; p.Cm = Cm; p.ldb = ldb; p.ldc = ldc; p.A = A; p.D = D; p.bias = delta_bias; p.softplus = softplus;
+    p.initial = initial_state; p.y = y; p.final_state = final_state; p.ws = workspace;
+    if ((s = scan_inputs(p, dtype)) != KDA_OK) return s;
+    const size_t es = size_of(dtype), need = kda::ssm_scan_workspace(p), states = (size_t)N * C * S * 4;
+    if (p.total > 0 && !y) return KDA_ERR_INVALID_ARG;
+    if (!aligned(y, es) || !kda_host::aligned16(final_state)) return KDA_ERR_INVALID_ARG;
+    if (workspace_bytes < need || (need > 0 && !workspace)) return KDA_ERR_WORKSPACE;
+    if (!kda_host::aligned16(workspace)) return KDA_ERR_INVALID_ARG;
+    SCAN_INPUT_SPANS(in, p, es);
+    const Span out[] = {{y, (size_t)p.total * C * es}, {final_state, states}, {workspace, need}};
+    if (!apart(in, out)) return KDA_ERR_INVALID_ARG;
+    if (N == 0) return KDA_OK;
+    return from_cuda(kda::ssm_scan_fwd(dtype, p, (cudaStream_t)stream));
+}
+
+size_t kda_ssm_scan_bwd_workspace_size(int B, int T, int C, int G, int S, int N, int packed) {
+    kda::SsmScanParams p{};
+    if (scan_sizes(p, B, T, C, G, S, N, packed ? kPacked : nullptr) != KDA_OK) return 0;
+    return kda::ssm_scan_bwd_workspace(p);
+}
+
+kda_status kda_ssm_scan_bwd(const void* u, int64_t ldu, const void* delta, int64_t ldd, const float* A, const void* Bm,
+                            int64_t ldb, const void* Cm, int64_t ldc, const float* D, const void* z, int64_t ldz,
+                            const float* delta_bias, int softplus, kda_dtype dtype, const float* initial_state,
+                            const int32_t* cu_seqlens, int B, int T, int C, int G, int S, int N, const void* dy,
+                            const float* dfinal_state, kda_dtype grad_dtype, void* du, void* ddelta, float* dA, void* dB,
+                            void* dC, float* dD, void* dz, float* ddelta_bias, float* dinitial_state, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+    kda::SsmScanParams p{};
+    kda_status s = scan_sizes(p, B, T, C, G, S, N, cu_seqlens);
+    if (s != KDA_OK) return s;
+    if (p.total > kMostBwdTokens) return KDA_ERR_UNSUPPORTED;
+    p.u = u; p.delta = delta; p.z = z; p.ldu = ldu; p.ldd = ldd; p.ldz = ldz;
+    p.Bm = Bm; p.Cm = Cm; p.ldb = ldb; p.ldc = ldc; p.A = A; p.D = D; p.bias = delta_bias; p.softplus = softplus;
+    p.initial = initial_state; p.ws = workspace;
+    p.dy = dy; p.dfinal = dfinal_state; p.du = du; p.ddelta = ddelta; p.dz = dz; p.dB = dB; p.dC = dC;
+    p.dA = dA; p.dD = dD; p.dbias = ddelta_bias; p.dinitial = dinitial_state;
+    if (dtype_ok(dtype) && (!dtype_ok(grad_dtype) || (dtype == KDA_F32 && grad_dtype != KDA_F32))) return KDA_ERR_UNSUPPORTED;
+    if ((s = scan_inputs(p, dtype)) != KDA_OK) return s;
+    const size_t es = size_of(dtype), gs = size_of(grad_dtype), need = kda::ssm_scan_bwd_workspace(p);
+    if (!dA || (p.total > 0 && (!dy || !du || !ddelta || !dB || !dC)) || (p.total > 0 && !z != !dz)) return KDA_ERR_INVALID_ARG;
+    for (const void* q : {dy, (const void*)du, (const void*)ddelta, (const void*)dz, (const void*)dB, (const void*)dC})
+        if (!aligned(q, gs)) return KDA_ERR_INVALID_ARG;
+    for (const float* q : {dfinal_state, (const float*)dinitial_state})
+        if (!kda_host::aligned16(q)) return KDA_ERR_INVALID_ARG;
+    for (const float* q : {dA, dD, ddelta_bias})
+        if (!aligned(q, 4)) return KDA_ERR_INVALID_ARG;
+    if (workspace_bytes < need || !workspace) return KDA_ERR_WORKSPACE;
+    if (!kda_host::aligned16(workspace)) return KDA_ERR_INVALID_ARG;
+    const size_t rows_bytes = (size_t)p.total * C * gs, vec = (size_t)p.total * G * S * gs, states = (size_t)N * C * S * 4;
+    SCAN_INPUT_SPANS(in, p, es);
+    const Span more[] = {{dy, rows_bytes}, {dfinal_state, states}};
+    const Span out[] = {{du, rows_bytes}, {ddelta, rows_bytes}, {dz, rows_bytes}, {dB, vec}, {dC, vec}, {dA, (size_t)C * S * 4},
+                        {dD, (size_t)C * 4}, {ddelta_bias, (size_t)C * 4}, {dinitial_state, states}, {workspace, need}};
+    if (!apart(in, out) || !apart(more, out)) return KDA_ERR_INVALID_ARG;
+    return from_cuda(kda::ssm_scan_bwd(dtype, grad_dtype, p, (cudaStream_t)stream));
 }
 
 kda_status kda_pages_alloc(int32_t* refs, int P, int n, int32_t* pages, int32_t* status, void* stream) {

@@ -49,11 +49,12 @@ struct SeqMap {
 
 // The sequences of tokens [t0, t0 + TT): start[i] / end[i] is the sequence that token t0 + i
 // is the first / last of, or -1.  carry: the sequence that token t0 continues (-1: none), which
-// began at carry_start.
+// began at carry_start.  Behind the tile the sequence at hand runs on to token `until`: a tile
+// that ends before it has no boundary and needs no look.
 template <int TT>
 struct TokenTile {
     int start[TT], end[TT];
-    int carry, carry_start, n0;
+    int carry, carry_start, n0, until;
 
     // Every thread of the block calls it; the block has to be past its last use of the tile.
     template <int NTH>
@@ -61,11 +62,12 @@ struct TokenTile {
         const int tid = threadIdx.x;
         for (int i = tid; i < TT; i += NTH) start[i] = end[i] = -1;
         if (tid < 32) {
-            const int n = m.begun_before(t0);
+            const int n = m.begun_before(t0), n1 = m.begun_before(t0 + TT);
             if (tid == 0) {
                 n0 = n;
                 carry = -1;
                 carry_start = t0;
+                until = n1 > 0 ? m.end(n1 - 1) : t0;
             }
         }
         __syncthreads();

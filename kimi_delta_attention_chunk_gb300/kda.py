@@ -61,6 +61,13 @@ SIGNATURES = {
     "kda_short_conv_step": (_i, [_vp, _i64, _fp, _fp, _i, _i, _vp, _i32p, _i, _i, _i, _i, _vp, _i32p, _vp]),
     "kda_ssm_step": (_i, [_vp, _i64, _vp, _i64, _fp, _vp, _i64, _vp, _i64, _fp, _vp, _i64, _fp, _i, _i, _fp, _i32p,
                           _i, _i, _i, _i, _i, _vp, _i32p, _vp]),
+    "kda_ssm_scan_fwd_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
+    "kda_ssm_scan_fwd": (_i, [_vp, _i64, _vp, _i64, _fp, _vp, _i64, _vp, _i64, _fp, _vp, _i64, _fp, _i, _i, _fp,
+                              _i32p, _i, _i, _i, _i, _i, _i, _vp, _fp, _vp, _sz, _vp]),
+    "kda_ssm_scan_bwd_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
+    "kda_ssm_scan_bwd": (_i, [_vp, _i64, _vp, _i64, _fp, _vp, _i64, _vp, _i64, _fp, _vp, _i64, _fp, _i, _i, _fp,
+                              _i32p, _i, _i, _i, _i, _i, _i, _vp, _fp, _i, _vp, _vp, _fp, _vp, _vp, _fp, _vp, _fp,
+                              _fp, _vp, _sz, _vp]),
     "kda_pages_alloc": (_i, [_i32p, _i, _i, _i32p, _i32p, _vp]),
     "kda_pages_free": (_i, [_i32p, _i, _i32p, _i64, _i32p, _vp]),
     "kda_pages_fork": (_i, [_i32p, _i32p, _i, _i, _i, _i32p, _i, _i32p, _i32p, _i, _i32p, _i32p, _i32p, _vp]),
@@ -646,6 +653,76 @@ def ssm_step(u, delta, A, Bm, Cm, state, D=None, z=None, delta_bias=None, softpl
                           _stream(u.device))
     _check("kda_ssm_step", st)
     return y
+
+
+def _ssm_pointers(u, delta, A, Bm, Cm, D, z, delta_bias, softplus):
+    (pu, ldu), (pd, ldd), (pz, ldz) = _rows("u", u, 2), _rows("delta", delta, 2), _rows("z", z, 2)
+    (pb, ldb), (pc, ldc) = _rows("Bm", Bm, 2), _rows("Cm", Cm, 2)
+    return pu, ldu, pd, ldd, _ptr(A), pb, ldb, pc, ldc, _ptr(D), pz, ldz, _ptr(delta_bias), int(softplus), _dt(u)
+
+
+def ssm_scan_fwd(u, delta, A, Bm, Cm, D=None, z=None, delta_bias=None, softplus: bool = True, initial_state=None,
+                 cu_seqlens=None, output_final_state: bool = True, y=None, final_state=None, workspace=None):
+    """:func:`ssm_step`'s recurrence over prompts.
+
+    u, delta, z: [B,T,C] (bf16 or fp32; rows may be slices of wider ones); A: [C,S] fp32, S
+    in 8, 16, 32, 64; Bm, Cm: [B,T,G,S]; D, delta_bias: [C] fp32 or None; ``initial_state``
+    fp32 [N,C,S] (None: zeros); ``cu_seqlens`` as for :func:`chunk_fwd`.  Returns (y
+    [B,T,C], final_state [N,C,S] fp32 or None).  Rows that belong to no sequence are left
+    as they are."""
+    lib = load_library()
+    C, G, S = _ssm_check(u, delta, A, Bm, Cm, D, z, delta_bias)
+    B, T, _ = u.shape
+    N = _sequences(u, cu_seqlens)
+    _here(u, delta, A, Bm, Cm, D, z, delta_bias, initial_state, cu_seqlens, y, final_state, workspace)
+    _like(u, y)
+    _f32(initial_state, final_state)
+    _shape("initial_state", initial_state, (N, C, S))
+    _shape("final_state", final_state, (N, C, S))
+    _shape("y", y, (B, T, C))
+    if y is None:
+        y = torch.empty((B, T, C), dtype=u.dtype, device=u.device)
+    if final_state is None and output_final_state:
+        final_state = torch.empty((N, C, S), dtype=torch.float32, device=u.device)
+    ws, ws_bytes = _workspace(int(lib.kda_ssm_scan_fwd_workspace_size(B, T, C, G, S, N, int(cu_seqlens is not None))),
+                              u.device, workspace)
+    st = lib.kda_ssm_scan_fwd(*_ssm_pointers(u, delta, A, Bm, Cm, D, z, delta_bias, softplus), _ptr(initial_state),
+                              _ptr(cu_seqlens), B, T, C, G, S, N, _ptr(y), _ptr(final_state), _ptr(ws), ws_bytes,
+                              _stream(u.device))
+    _check("kda_ssm_scan_fwd", st)
+    return y, final_state
+
+
+def ssm_scan_bwd(u, delta, A, Bm, Cm, dy, D=None, z=None, delta_bias=None, softplus: bool = True,
+                 initial_state=None, cu_seqlens=None, dfinal_state=None, workspace=None):
+    """Gradients of <dy, y> + <dfinal_state, final_state> through :func:`ssm_scan_fwd` (same
+    arguments).  dy [B,T,C] is of u's type or fp32.  Returns a dict: du, ddelta, dz [B,T,C]
+    and dB, dC [B,T,G,S] in dy's type, dA [C,S], dD, ddelta_bias [C] and dinitial_state
+    [N,C,S] fp32; the gradient of an argument that was not given is None."""
+    lib = load_library()
+    C, G, S = _ssm_check(u, delta, A, Bm, Cm, D, z, delta_bias)
+    B, T, _ = u.shape
+    N = _sequences(u, cu_seqlens)
+    _here(u, delta, A, Bm, Cm, dy, D, z, delta_bias, initial_state, cu_seqlens, dfinal_state, workspace)
+    _f32(initial_state, dfinal_state)
+    _shape("dy", dy, (B, T, C))
+    _shape("initial_state", initial_state, (N, C, S))
+    _shape("dfinal_state", dfinal_state, (N, C, S))
+    new = lambda given, shape, dt: torch.empty(shape, dtype=dt, device=u.device) if given is not None else None  # noqa: E731
+    rows, vecs, f32 = (B, T, C), (B, T, G, S), torch.float32
+    out = {"du": new(u, rows, dy.dtype), "ddelta": new(delta, rows, dy.dtype), "dA": new(A, (C, S), f32),
+           "dB": new(Bm, vecs, dy.dtype), "dC": new(Cm, vecs, dy.dtype), "dD": new(D, C, f32),
+           "dz": new(z, rows, dy.dtype), "ddelta_bias": new(delta_bias, C, f32),
+           "dinitial_state": new(initial_state, (N, C, S), f32)}
+    ws, ws_bytes = _workspace(int(lib.kda_ssm_scan_bwd_workspace_size(B, T, C, G, S, N, int(cu_seqlens is not None))),
+                              u.device, workspace)
+    st = lib.kda_ssm_scan_bwd(*_ssm_pointers(u, delta, A, Bm, Cm, D, z, delta_bias, softplus), _ptr(initial_state),
+                              _ptr(cu_seqlens), B, T, C, G, S, N, _ptr(dy), _ptr(dfinal_state), _dt(dy),
+                              *(_ptr(out[k]) for k in ("du", "ddelta", "dA", "dB", "dC", "dD", "dz", "ddelta_bias",
+                                                       "dinitial_state")),
+                              _ptr(ws), ws_bytes, _stream(u.device))
+    _check("kda_ssm_scan_bwd", st)
+    return out
 
 
 def pages_alloc(refs, n: int, pages=None, status=None):

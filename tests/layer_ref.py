@@ -68,6 +68,75 @@ def conv(x, w, bias, act, initial, cu, dy=None, dfinal=None):
     return (y, final, M) if dy is None else g
 
 
+def scan(u, delta, A, B, C, D, z, bias, sp, initial, cu, dy=None, dfinal=None):
+    """u, delta, z [T, c]; A [c, S]; B, C [T, G, S].  A dict: y, state, and with dy the gradients; every
+    value x with x + "_err", the sum of magnitudes that a relative error of the parts is taken of: of the
+    terms, states and decays, a decay counting (1 + |d A|) times for its exponent's error, which the
+    states behind it inherit."""
+    T, c = u.shape
+    S, G, N = A.shape[1], B.shape[1], len(cu) - 1
+    grp = np.arange(c) // (c // G)
+    raw = delta + (0 if bias is None else bias)
+    d = softplus(raw) if sp else raw
+    D0 = np.zeros(c) if D is None else D
+    sz = np.ones_like(u) if z is None else silu(z)
+    h, eh = np.zeros((T, c, S)), np.zeros((T, c, S))
+    out = {"y": np.zeros_like(u), "y_err": np.zeros_like(u), "state": np.zeros((N, c, S)), "state_err": np.zeros((N, c, S))}
+    lin, elin = np.zeros_like(u), np.zeros_like(u)
+    befores, ebefores, decays = np.zeros((T, c, S)), np.zeros((T, c, S)), np.zeros((T, c, S))
+    for n in range(N):
+        s = np.zeros((c, S)) if initial is None else initial[n]
+        e = np.zeros((c, S))
+        for t in range(cu[n], cu[n + 1]):
+            befores[t], ebefores[t] = s, e
+            a = decays[t] = np.exp(d[t][:, None] * A)
+            b = (d[t] * u[t])[:, None] * B[t][grp]
+            e = a * e + a * np.abs(s) * (1 + np.abs(d[t][:, None] * A)) + np.abs(b)
+            s = a * s + b
+            h[t], eh[t] = s, e
+            lin[t] = (C[t][grp] * s).sum(-1) + D0 * u[t]
+            elin[t] = (np.abs(C[t][grp]) * (e + np.abs(s))).sum(-1) + np.abs(D0 * u[t])
+        out["state"][n], out["state_err"][n] = s, e + np.abs(s)
+    out["y"], out["y_err"] = lin * sz, elin * np.abs(sz) + np.abs(lin * sz) * (1 + (0 if z is None else np.abs(z)))
+    if dy is None:
+        return out
+    yb = dy * sz
+    eyb = np.abs(yb) * (2 + (0 if z is None else np.abs(z)))
+    for k, shape in (("du", u.shape), ("ddelta", u.shape), ("dA", A.shape), ("dB", B.shape), ("dC", B.shape), ("dinitial_state", (N, c, S))):
+        out[k], out[k + "_err"] = np.zeros(shape), np.zeros(shape)
+    slope = 1 / (1 + np.exp(-raw)) if sp else np.ones_like(raw)
+    for n in range(N):
+        g = np.zeros((c, S)) if dfinal is None else dfinal[n]
+        eg = np.zeros((c, S))
+        for t in range(cu[n + 1] - 1, cu[n] - 1, -1):
+            Bt, Ct, dt, ut = B[t][grp], C[t][grp], d[t][:, None], u[t]
+            dh = g + Ct * yb[t][:, None]
+            edh = eg + np.abs(g) + np.abs(Ct) * eyb[t][:, None]
+            a = decays[t]
+            ex = 1 + np.abs(dt * A)
+            through = dh * a * befores[t]
+            ethrough = edh * a * np.abs(befores[t]) + np.abs(dh) * a * (ebefores[t] + np.abs(befores[t]) * ex)
+            q1, eq1 = (dh * Bt).sum(-1), ((edh + np.abs(dh)) * np.abs(Bt)).sum(-1)
+            out["du"][t], out["du_err"][t] = d[t] * q1 + D0 * yb[t], np.abs(d[t]) * (eq1 + np.abs(q1)) + np.abs(D0) * eyb[t]
+            out["ddelta"][t] = ((through * A).sum(-1) + ut * q1) * slope[t]
+            out["ddelta_err"][t] = (((ethrough + np.abs(through)) * np.abs(A)).sum(-1) + np.abs(ut) * (eq1 + np.abs(q1))) * slope[t] * \
+                (2 + np.abs(raw[t]))
+            out["dA"] += through * dt
+            out["dA_err"] += (ethrough + 2 * np.abs(through)) * np.abs(dt)
+            x = (d[t] * ut)[:, None]
+            for i, (v, ev) in (("dB", (dh * x, (edh + 2 * np.abs(dh)) * np.abs(x))),
+                               ("dC", (h[t] * yb[t][:, None], (eh[t] + np.abs(h[t])) * np.abs(yb[t])[:, None] + np.abs(h[t]) * eyb[t][:, None]))):
+                out[i][t], out[i + "_err"][t] = v.reshape(G, c // G, S).sum(1), ev.reshape(G, c // G, S).sum(1)
+            g, eg = a * dh, a * edh + np.abs(a * dh) * ex
+        out["dinitial_state"][n], out["dinitial_state_err"][n] = g, eg + np.abs(g)
+    out["dD"], out["dD_err"] = (yb * u).sum(0), (eyb * np.abs(u)).sum(0)
+    out["ddelta_bias"], out["ddelta_bias_err"] = out["ddelta"].sum(0), out["ddelta_err"].sum(0)
+    if z is not None:
+        out["dz"] = dy * lin * dsilu(z)
+        out["dz_err"] = np.abs(dy) * (elin + np.abs(lin) * (2 + np.abs(z))) * 1.2
+    return out
+
+
 class Books:
     """refs, tables and lens as lists; every operation returns what it gives out and whether a
     request was refused."""

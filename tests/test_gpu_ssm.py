@@ -1,16 +1,22 @@
-"""The selective state space scan (single token) against its plain 64-bit form.
+"""The selective state space scan (prompts, their backward pass, single tokens) against its plain
+64-bit form.
 
 Tolerances, element by element.  The step size d is off by 2^-21 relative (softplus: one exponential,
 2^-22, and a series), and the decay's exponent d A by as much of itself plus a rounding, so the decay is off
 by |d A| 2^-20 + 2^-22 relative; with the products' roundings a state is off by
 2^-19 (|a h| (1 + |d A|) + |d u B|) per step.  y adds S products and D u, each rounded, and the gate's
-relative 2^-20 |z| + 2^-21."""
+relative 2^-20 |z| + 2^-21.
+
+Over a prompt these errors follow the recurrences: `layer_ref.scan` carries along, for every state,
+gradient and sum, the sum of the magnitudes that a relative error of 2^-19 of each part is taken of (the
+decay's part 1 + |d A| times).  Cutting the tokens into runs adds one rounded decay product a run, below what
+the per-token parts already count.  Sums over n terms in fp32 add n 2^-24 of the sum of magnitudes."""
 import numpy as np
 import pytest
 import torch
 
 import kimi_delta_attention_chunk_gb300 as kda
-from tests.layer_ref import f64, half_step, silu, softplus
+from tests.layer_ref import f64, half_step, scan, silu, softplus
 
 pytestmark = pytest.mark.gpu
 
@@ -119,3 +125,225 @@ def test_step_sizes_at_the_ends():
     dl = softplus(f64(raw))
     want = np.exp(-dl) * 2 + dl
     assert np.allclose(f64(pool)[0, :, 0], want, rtol=2e-6, atol=0)
+
+
+# lengths, C, S, G, gate, D, bias, softplus, state, wide
+SCANS = [
+    ([1], 8, 16, 1, True, True, True, True, False),
+    ([64], 40, 16, 1, True, True, True, True, True),
+    ([65, 1, 63], 130, 16, 1, False, True, True, True, True),
+    ([0, 3, 0, 0, 9, 1, 90, 0], 36, 8, 2, True, False, True, True, True),
+    ([31, 33, 129], 70, 32, 2, True, True, False, True, True),
+    ([200], 24, 64, 3, True, True, True, True, False),
+    ([1] * 30 + [17] * 6, 129, 16, 1, True, True, True, True, True),
+    ([300, 5], 260, 16, 1, False, False, False, False, True),
+    ([130], 1, 64, 1, True, True, True, True, True),
+]
+
+
+def scan_inputs(case, dtype, seed):
+    lengths, C, S, G, gate, D, bias, sp, state = SCANS[case]
+    d = make((1, sum(lengths)), C, S, G, dtype, seed, gate, D, bias)
+    if not sp:
+        d["delta"] = (d["delta"].float().abs() * 0.3).to(dtype)
+    g = torch.Generator().manual_seed(seed + 1)
+    N = len(lengths)
+    d["s0"] = torch.randn(N, C, S, generator=g).cuda() if state else None
+    d["cu"] = torch.tensor(np.concatenate([[0], np.cumsum(lengths)]), dtype=torch.int32).cuda()
+    d["dy"] = torch.randn(1, sum(lengths), C, generator=g)
+    d["df"] = torch.randn(N, C, S, generator=g).cuda() if state else None
+    d["sp"] = sp
+    return d
+
+
+def call_args(d):
+    return (d["u"], d["delta"], d["A"], d["B"], d["C"]), dict(D=d["D"], z=d["z"], delta_bias=d["bias"], softplus=d["sp"],
+                                                             initial_state=d["s0"], cu_seqlens=d["cu"])
+
+
+def ref_args(d):
+    one = lambda t: None if t is None else f64(t)[0]  # noqa: E731
+    return (one(d["u"]), one(d["delta"]), f64(d["A"]), one(d["B"]), one(d["C"]), f64(d["D"]), one(d["z"]), f64(d["bias"]), d["sp"],
+            f64(d["s0"]), d["cu"].tolist())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("case", range(len(SCANS)))
+def test_scan(case, dtype):
+    d = scan_inputs(case, dtype, 900 + case)
+    a, kw = call_args(d)
+    y, state = kda.ssm_scan_fwd(*a, **kw)
+    r = scan(*ref_args(d))
+    S = d["A"].shape[1]
+    within(y[0], r["y"], (2.0 ** -19 + S * 2.0 ** -24) * r["y_err"], dtype)
+    within(state, r["state"], 2.0 ** -19 * r["state_err"], F32)
+
+
+@pytest.mark.parametrize("dtype,gdtype", [(BF16, BF16), (BF16, F32), (F32, F32)])
+@pytest.mark.parametrize("case", range(len(SCANS)))
+def test_scan_backward(case, dtype, gdtype):
+    d = scan_inputs(case, dtype, 950 + case)
+    a, kw = call_args(d)
+    dy = d["dy"].to(gdtype).cuda()
+    got = kda.ssm_scan_bwd(*a, dy, dfinal_state=d["df"], **kw)
+    r = scan(*ref_args(d), f64(dy)[0], f64(d["df"]))
+    T, C = dy.shape[1:]
+    S = d["A"].shape[1]
+    for k, dt, n in (("du", gdtype, S), ("ddelta", gdtype, S), ("dz", gdtype, S), ("dB", gdtype, C), ("dC", gdtype, C), ("dA", F32, T),
+                     ("dD", F32, T), ("ddelta_bias", F32, T), ("dinitial_state", F32, 1)):
+        given = {"dz": d["z"], "dD": d["D"], "ddelta_bias": d["bias"], "dinitial_state": d["s0"]}.get(k, d["u"]) is not None
+        assert (got[k] is not None) == given, k
+        if given:
+            within(got[k], r[k], (2.0 ** -19 + n * 2.0 ** -24) * r[k + "_err"], dt)
+
+
+def test_scan_backward_against_differences():
+    """Along random directions of every argument: the loss is smooth, steps of 1e-2 leave a relative truncation
+    of 1e-4 of the magnitudes, and the forward's rounding 2^-18 / 1e-2."""
+    d = scan_inputs(1, F32, 990)
+    a, kw = call_args(d)
+    dy = d["dy"].cuda()
+    got = kda.ssm_scan_bwd(*a, dy, dfinal_state=d["df"], **kw)
+    names = ["u", "delta", "A", "B", "C", "D", "z", "bias", "s0"]
+    grads = ["du", "ddelta", "dA", "dB", "dC", "dD", "dz", "ddelta_bias", "dinitial_state"]
+
+    def loss(v):
+        y, s = kda.ssm_scan_fwd(v["u"], v["delta"], v["A"], v["B"], v["C"], D=v["D"], z=v["z"], delta_bias=v["bias"],
+                                initial_state=v["s0"], cu_seqlens=d["cu"])
+        return float((y.double() * dy.double()).sum() + (s.double() * d["df"].double()).sum())
+    g = torch.Generator().manual_seed(991)
+    for name, grad in zip(names, grads):
+        way = torch.randn(d[name].shape, generator=g).cuda()
+        slope = (loss({**d, name: (d[name] + 1e-2 * way).contiguous()}) - loss({**d, name: (d[name] - 1e-2 * way).contiguous()})) / 2e-2
+        terms = got[grad].reshape(way.shape).double() * way.double()
+        assert abs(slope - float(terms.sum())) <= 2e-3 * (float(terms.abs().sum()) + 1.0), name
+
+
+def test_long_run_of_slow_decay():
+    """Several runs of one sequence, channels that hardly forget: the state in 64 bits on the device."""
+    T, C, S = 5000, 40, 16
+    g = torch.Generator().manual_seed(992)
+    u, delta = torch.randn(1, T, C, generator=g).cuda(), (torch.rand(1, T, C, generator=g) * 0.01).cuda()
+    A = -(torch.arange(S).float() * 0.1).repeat(C, 1).cuda()          # a rate of zero among them
+    B, Cm = torch.randn(1, T, 1, S, generator=g).cuda(), torch.randn(1, T, 1, S, generator=g).cuda()
+    y, state = kda.ssm_scan_fwd(u, delta, A, B, Cm, softplus=False)
+    h = torch.zeros(C, S, dtype=torch.float64, device="cuda")
+    ys, mag, peak = [], torch.zeros_like(h), 0.0
+    for t in range(T):
+        x = delta[0, t].double()[:, None] * A.double()
+        b = (delta[0, t] .double() * u[0, t].double())[:, None] * B[0, t].double()
+        h = torch.exp(x) * h + b
+        mag = torch.exp(x) * mag + b.abs() + h.abs()
+        ys.append((h * Cm[0, t].double()).sum(-1))
+    want = torch.stack(ys)
+    off = (state[0].double() - h).abs() / mag
+    assert float(off.max()) <= 2.0 ** -22      # each step rounds the state once and its decay by 2^-22 of a small exponent
+    assert float((y[0].double() - want).abs().max()) <= 1e-4 * float(want.abs().max())
+
+
+def test_scan_dense_equals_packed_and_leaves_other_rows():
+    d = make((3, 50), 72, 16, 1, BF16, 993, True, True, True)
+    kw = dict(D=d["D"], z=d["z"], delta_bias=d["bias"])
+    y, s = kda.ssm_scan_fwd(d["u"], d["delta"], d["A"], d["B"].contiguous(), d["C"].contiguous(), **kw)
+    flat = lambda t: t.contiguous().reshape(1, 150, *t.shape[2:])  # noqa: E731
+    cu = torch.tensor([0, 50, 100, 150], dtype=torch.int32, device="cuda")
+    args = [flat(d["u"]), flat(d["delta"]), d["A"], flat(d["B"]), flat(d["C"])]
+    y2, s2 = kda.ssm_scan_fwd(*args, D=d["D"], z=flat(d["z"]), delta_bias=d["bias"], cu_seqlens=cu)
+    assert torch.equal(y.view(1, 150, 72), y2) and torch.equal(s, s2)
+    cu = torch.tensor([7, 50, 140], dtype=torch.int32, device="cuda")
+    y3 = torch.full_like(y2, 5.0)
+    kda.ssm_scan_fwd(*args, D=d["D"], z=flat(d["z"]), delta_bias=d["bias"], cu_seqlens=cu, y=y3)
+    assert bool((y3[0, :7] == 5).all()) and bool((y3[0, 140:] == 5).all())
+    assert torch.equal(y3[0, 50:100], y2[0, 50:100])       # a sequence of the same start
+    got = kda.ssm_scan_bwd(*args, y2, D=d["D"], z=flat(d["z"]), delta_bias=d["bias"], cu_seqlens=cu)
+    assert all(bool(got[k].isfinite().all()) for k in ("dA", "dD", "ddelta_bias"))
+
+
+def test_scan_without_tokens():
+    e = torch.empty(1, 0, 24, device="cuda")
+    v = torch.empty(1, 0, 1, 16, device="cuda")
+    A = -torch.ones(24, 16, device="cuda")
+    s0 = torch.randn(2, 24, 16, device="cuda")
+    cu = torch.zeros(3, dtype=torch.int32, device="cuda")
+    y, s = kda.ssm_scan_fwd(e, e, A, v, v, initial_state=s0, cu_seqlens=cu)
+    assert torch.equal(s, s0) and y.numel() == 0
+    got = kda.ssm_scan_bwd(e, e, A, v, v, e, initial_state=s0, cu_seqlens=cu, dfinal_state=s0)
+    assert torch.equal(got["dinitial_state"], s0) and not got["dA"].any()
+
+
+def test_scan_offsets_out_of_order_stay_in_bounds():
+    d = scan_inputs(5, BF16, 994)
+    s0 = torch.randn(4, 24, 64, device="cuda")
+    a, kw = call_args(d)
+    for cu in ([0, 150, 50, 180, 200], [0, -5, 900, 20, 200], [200, 0, 200, 0, 7], [2 ** 31 - 1, -2 ** 31, 5, 6, 2 ** 31 - 1]):
+        kw["initial_state"], kw["cu_seqlens"] = s0, torch.tensor(cu, dtype=torch.int32, device="cuda")
+        y, _ = kda.ssm_scan_fwd(*a, **kw)
+        kda.ssm_scan_bwd(*a, y, dfinal_state=s0, **kw)
+    torch.cuda.synchronize()
+
+
+def test_steps_continue_a_scan():
+    """Prefill into a pool and single tokens from there, as the whole prompt."""
+    d = make((4, 20), 200, 16, 1, F32, 995, True, True, True)
+    kw = dict(D=d["D"], delta_bias=d["bias"])
+    args = lambda sl: [x[:, sl].contiguous() for x in (d["u"], d["delta"], d["B"], d["C"], d["z"])]  # noqa: E731
+    u, dl, B, C, z = args(slice(None))
+    whole, last = kda.ssm_scan_fwd(u, dl, d["A"], B, C, z=z, **kw)
+    u, dl, B, C, z = args(slice(0, 12))
+    _, state = kda.ssm_scan_fwd(u, dl, d["A"], B, C, z=z, **kw)
+    pool = torch.zeros(7, 200, 16, device="cuda")
+    slots = torch.tensor([5, 0, 3, 6], dtype=torch.int32, device="cuda")
+    pool[slots.long()] = state
+    for t in range(12, 20):
+        y = kda.ssm_step(d["u"][:, t], d["delta"][:, t], d["A"], d["B"][:, t], d["C"][:, t], pool, z=d["z"][:, t], slots=slots, **kw)
+        torch.testing.assert_close(y, whole[:, t], rtol=1e-5, atol=1e-5)
+    torch.testing.assert_close(pool[slots.long()], last, rtol=1e-5, atol=1e-5)
+
+
+def test_layer_of_convolution_and_scan():
+    """The convolution's output into the scan and their gradients back through both, packed, against the plain
+    forms chained: bf16 between them, so within the steps of its roundings."""
+    from tests.layer_ref import conv
+    lengths, C = [40, 70, 1], 64
+    d = make((1, 111), C, 16, 1, F32, 996, True, True, True)
+    w = (torch.randn(C, 4, generator=torch.Generator().manual_seed(3)) * 0.5).cuda()
+    cu = torch.tensor([0, 40, 110, 111], dtype=torch.int32, device="cuda")
+    kw = dict(D=d["D"], z=d["z"], delta_bias=d["bias"], cu_seqlens=cu)
+    x, _ = kda.short_conv_fwd(d["u"], w, conv_act=1, cu_seqlens=cu)
+    y, _ = kda.ssm_scan_fwd(x, d["delta"], d["A"], d["B"], d["C"], **kw)
+    dy = torch.randn(1, 111, C, generator=torch.Generator().manual_seed(4)).cuda()
+    back = kda.ssm_scan_bwd(x, d["delta"], d["A"], d["B"], d["C"], dy, **kw)
+    got = kda.short_conv_bwd(d["u"], w, back["du"], conv_act=1, cu_seqlens=cu)
+    rx, _, _ = conv(f64(d["u"])[0], f64(w), None, 1, None, cu.tolist())
+    d2 = dict(d, sp=True, s0=None, cu=cu)
+    args = list(ref_args(d2))
+    args[0] = rx
+    r = scan(*args, f64(dy)[0], None)
+    rg = conv(f64(d["u"])[0], f64(w), None, 1, None, cu.tolist(), r["du"], None)
+    within(y[0], r["y"], 2.0 ** -17 * r["y_err"], F32)
+    scale = np.abs(r["du_err"]).max() * np.abs(f64(w)).sum(1).max()
+    assert np.abs(f64(got["dx"])[0] - rg["dx"]).max() <= 2.0 ** -17 * scale * 2
+    assert np.abs(f64(got["dweight"]) - rg["dweight"]).max() <= 2.0 ** -17 * scale * 111
+
+
+def test_scan_captured_and_replayed_on_another_stream():
+    d = scan_inputs(6, BF16, 997)
+    a, kw = call_args(d)
+    dy = d["dy"].to(BF16).cuda()
+    want, ws = kda.ssm_scan_fwd(*a, **kw)
+    wg = kda.ssm_scan_bwd(*a, dy, dfinal_state=d["df"], **kw)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        y, s = kda.ssm_scan_fwd(*a, **kw)
+        g = kda.ssm_scan_bwd(*a, dy, dfinal_state=d["df"], **kw)
+    side.synchronize()
+    assert torch.equal(y, want) and torch.equal(s, ws) and all(torch.equal(g[k], wg[k]) for k in wg if wg[k] is not None)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, s = kda.ssm_scan_fwd(*a, **kw)
+        g = kda.ssm_scan_bwd(*a, dy, dfinal_state=d["df"], **kw)
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, want) and torch.equal(s, ws) and all(torch.equal(g[k], wg[k]) for k in wg if wg[k] is not None)

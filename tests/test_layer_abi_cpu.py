@@ -103,6 +103,56 @@ def test_ssm_step(lib):
     assert call(N=0, P=0, u=None, s=None) == 0
 
 
+def scan(lib, **kw):
+    a = dict(u=at(1), ldu=256, d=at(2), ldd=256, A=at(3), B=at(4), ldb=32, C=at(5), ldc=32, D=None, z=None, ldz=0, b=None, sp=1, dt=1,
+             s0=None, cu=None, nb=1, T=64, c=256, G=2, S=16, N=1, y=at(8), sT=None, ws=at(9), wsb=1 << 30)
+    a.update(kw)
+    return lib.kda_ssm_scan_fwd(a["u"], a["ldu"], a["d"], a["ldd"], a["A"], a["B"], a["ldb"], a["C"], a["ldc"], a["D"], a["z"],
+                                a["ldz"], a["b"], a["sp"], a["dt"], a["s0"], a["cu"], a["nb"], a["T"], a["c"], a["G"], a["S"],
+                                a["N"], a["y"], a["sT"], a["ws"], a["wsb"], None)
+
+
+def test_scan_fwd(lib):
+    assert scan(lib, S=4) == UNSUPPORTED and scan(lib, dt=9) == UNSUPPORTED and scan(lib, c=(1 << 20) + 2) == UNSUPPORTED
+    assert scan(lib, G=3) == INVALID_ARG and scan(lib, T=-1) == INVALID_ARG and scan(lib, N=2) == INVALID_ARG
+    assert scan(lib, nb=2, N=2, cu=at(7)) == INVALID_ARG
+    assert scan(lib, ldu=255) == INVALID_ARG and scan(lib, ldc=31) == INVALID_ARG and scan(lib, z=at(6), ldz=9) == INVALID_ARG
+    assert scan(lib, A=at(3, 4)) == INVALID_ARG and scan(lib, s0=at(6, 4)) == INVALID_ARG and scan(lib, sT=at(6, 4)) == INVALID_ARG
+    assert scan(lib, A=None) == INVALID_ARG and scan(lib, y=None) == INVALID_ARG and scan(lib, sp=3) == INVALID_ARG
+    assert scan(lib, s0=at(6), sT=at(6)) == INVALID_ARG      # the final state over the initial one
+    assert scan(lib, y=at(1)) == INVALID_ARG
+    need = lib.kda_ssm_scan_fwd_workspace_size(1, 4096, 256, 2, 16, 1, 0)
+    assert need > 0 and scan(lib, T=4096, wsb=need - 1) == WORKSPACE and scan(lib, T=4096, ws=None) == WORKSPACE
+    assert scan(lib, T=4096, ws=at(9, 8)) == INVALID_ARG
+    # one run, or sequences enough: none
+    assert lib.kda_ssm_scan_fwd_workspace_size(1, 64, 256, 2, 16, 1, 0) == 0
+    assert lib.kda_ssm_scan_fwd_workspace_size(1000, 512, 256, 2, 16, 1000, 0) == 0
+    assert lib.kda_ssm_scan_fwd_workspace_size(1, 4096, 256, 3, 16, 1, 0) == 0
+    assert scan(lib, nb=0, N=0, u=None, d=None, B=None, C=None, y=None, ws=None, wsb=0) == 0
+
+
+def test_scan_bwd(lib):
+    need = lib.kda_ssm_scan_bwd_workspace_size(1, 64, 256, 2, 16, 1, 0)
+    # one chunk: states and gradients, sums of d, dD and dbias, four channel blocks' dB and dC, a flag
+    assert need == 2 * 256 * 16 * 4 + 3 * 256 * 4 + 4 * 64 * 32 * 4 + 256
+
+    def call(**kw):
+        a = dict(u=at(1), A=at(3), z=None, ldz=0, dt=1, T=64, c=256, G=2, S=16, N=1, dy=at(10), df=None, gdt=1, du=at(11), dd=at(12),
+                 dA=at(13), dB=at(14), dC=at(15), dD=None, dz=None, db=None, d0=None, ws=at(16), wsb=need)
+        a.update(kw)
+        return lib.kda_ssm_scan_bwd(a["u"], 256, at(2), 256, a["A"], at(4), 32, at(5), 32, None, a["z"], a["ldz"], None, 1, a["dt"],
+                                    None, None, 1, a["T"], a["c"], a["G"], a["S"], a["N"], a["dy"], a["df"], a["gdt"], a["du"],
+                                    a["dd"], a["dA"], a["dB"], a["dC"], a["dD"], a["dz"], a["db"], a["d0"], a["ws"], a["wsb"], None)
+    assert call(S=20) == UNSUPPORTED and call(dt=0, gdt=1) == UNSUPPORTED and call(gdt=2) == UNSUPPORTED
+    assert call(T=65535 * 64 + 1) == UNSUPPORTED
+    assert call(dA=None) == INVALID_ARG and call(du=None) == INVALID_ARG and call(dB=None) == INVALID_ARG
+    assert call(z=at(6), ldz=256) == INVALID_ARG             # z without dz
+    assert call(dz=at(6)) == INVALID_ARG                     # dz without z
+    assert call(d0=at(17, 4)) == INVALID_ARG and call(df=at(17, 8)) == INVALID_ARG
+    assert call(wsb=need - 1) == WORKSPACE and call(ws=None) == WORKSPACE
+    assert call(du=at(10)) == INVALID_ARG and call(dB=at(14), dC=at(14)) == INVALID_ARG
+
+
 def test_recurrent_step_slots(lib):
     def call(**kw):
         a = dict(q=at(1), pool=at(2), sl=at(3), P=8, N=4, H=2, K=128, V=128, dt=1, st=None)
