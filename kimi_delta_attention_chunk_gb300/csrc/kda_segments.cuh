@@ -92,87 +92,132 @@ struct TokenTile {
     }
 };
 
+// ---- two fp32 values in one 64-bit register ------------------------------------------------
+
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pack(float a, float b) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack(f2 x, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x)); }
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ float sum2(f2 x) {
+    float a, b;
+    unpack(x, a, b);
+    return a + b;
+}
+
 // ---- rows of VEC elements ------------------------------------------------------------------
+
+// VEC elements of a row as they lie in memory (VEC = 1, or 8 or 16 bytes).
+template <int BYTES>
+struct Bits;
+template <> struct Bits<16> { typedef uint4 type; };
+template <> struct Bits<8> { typedef uint2 type; };
+template <> struct Bits<4> { typedef uint32_t type; };
+template <> struct Bits<2> { typedef unsigned short type; };
 
 // load() reads data that no thread writes during the kernel, load_rw() any data.
 template <typename T, int VEC>
-struct Row;
-template <>
-struct Row<__nv_bfloat16, 8> {
-    uint4 r;
-    __device__ __forceinline__ void load(const __nv_bfloat16* p) { r = __ldg(reinterpret_cast<const uint4*>(p)); }
-    __device__ __forceinline__ void load_rw(const __nv_bfloat16* p) { r = *reinterpret_cast<const uint4*>(p); }
-    __device__ __forceinline__ void to(float* f) const {
-        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+struct Row {
+    static constexpr int kBytes = VEC * (int)sizeof(T);
+    typedef typename Bits<kBytes>::type Raw;
+    static constexpr int N2 = (VEC + 1) / 2;  // pairs (VEC = 1: one, its upper half zero)
+    Raw r;
+    __device__ __forceinline__ void load(const T* p) { r = __ldg(reinterpret_cast<const Raw*>(p)); }
+    __device__ __forceinline__ void load_rw(const T* p) { r = *reinterpret_cast<const Raw*>(p); }
+    __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<Raw*>(p) = r; }
+    __device__ __forceinline__ void zero() { r = Raw{}; }
+    __device__ __forceinline__ void to(f2 (&v)[N2]) const {
+        if constexpr (VEC == 1) {
+            v[0] = pack(to_f32<T>(*reinterpret_cast<const T*>(&r)), 0.f);
+        } else if constexpr (sizeof(T) == 2) {
+            const uint32_t* w = reinterpret_cast<const uint32_t*>(&r);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[2 * i] = __uint_as_float(w[i] << 16);
-            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            for (int i = 0; i < N2; ++i) v[i] = pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+        } else {
+            const float* w = reinterpret_cast<const float*>(&r);
+#pragma unroll
+            for (int i = 0; i < N2; ++i) v[i] = pack(w[2 * i], w[2 * i + 1]);
         }
     }
-    __device__ __forceinline__ void from(const float* f) {
-        uint32_t w[4];
+    __device__ __forceinline__ void from(const f2 (&v)[N2]) {
+        if constexpr (VEC == 1) {
+            float a, b;
+            unpack(v[0], a, b);
+            const T x = from_f32<T>(a);
+            r = *reinterpret_cast<const Raw*>(&x);
+        } else if constexpr (sizeof(T) == 2) {
+            uint32_t* w = reinterpret_cast<uint32_t*>(&r);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t*>(&v);
+            for (int i = 0; i < N2; ++i) {
+                float a, b;
+                unpack(v[i], a, b);
+                const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
+                w[i] = *reinterpret_cast<const uint32_t*>(&x);
+            }
+        } else {
+            float* w = reinterpret_cast<float*>(&r);
+#pragma unroll
+            for (int i = 0; i < N2; ++i) unpack(v[i], w[2 * i], w[2 * i + 1]);
         }
-        r = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = r; }
-    __device__ __forceinline__ void zero() { r = make_uint4(0, 0, 0, 0); }
+    // Copies a row's piece into shared memory without waiting (two bytes: at once).
+    static __device__ __forceinline__ void copy_async(void* shared, const T* p) {
+        if constexpr (kBytes >= 4) {
+            const uint32_t s = (uint32_t)__cvta_generic_to_shared(shared);
+            if constexpr (kBytes == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(s), "l"(p) : "memory");
+            else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(s), "l"(p), "n"(kBytes) : "memory");
+        } else {
+            *reinterpret_cast<Raw*>(shared) = __ldg(reinterpret_cast<const Raw*>(p));
+        }
+    }
+    __device__ __forceinline__ void from_shared(const void* shared) { r = *reinterpret_cast<const Raw*>(shared); }
 };
-template <>
-struct Row<float, 4> {
-    float4 r;
-    __device__ __forceinline__ void load(const float* p) { r = __ldg(reinterpret_cast<const float4*>(p)); }
-    __device__ __forceinline__ void load_rw(const float* p) { r = *reinterpret_cast<const float4*>(p); }
-    __device__ __forceinline__ void to(float* f) const { f[0] = r.x; f[1] = r.y; f[2] = r.z; f[3] = r.w; }
-    __device__ __forceinline__ void from(const float* f) { r = make_float4(f[0], f[1], f[2], f[3]); }
-    __device__ __forceinline__ void store(float* p) const { *reinterpret_cast<float4*>(p) = r; }
-    __device__ __forceinline__ void zero() { r = make_float4(0.f, 0.f, 0.f, 0.f); }
-};
-template <>
-struct Row<float, 8> {
-    float4 a, b;
-    __device__ __forceinline__ void load(const float* p) {
-        a = __ldg(reinterpret_cast<const float4*>(p));
-        b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-    }
-    __device__ __forceinline__ void to(float* f) const {
-        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-    }
-    __device__ __forceinline__ void from(const float* f) {
-        a = make_float4(f[0], f[1], f[2], f[3]);
-        b = make_float4(f[4], f[5], f[6], f[7]);
-    }
-    __device__ __forceinline__ void store(float* p) const {
-        reinterpret_cast<float4*>(p)[0] = a;
-        reinterpret_cast<float4*>(p)[1] = b;
-    }
-    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-};
-template <typename T>
-struct Row<T, 1> {
-    T r;
-    __device__ __forceinline__ void load(const T* p) { r = __ldg(p); }
-    __device__ __forceinline__ void load_rw(const T* p) { r = *p; }
-    __device__ __forceinline__ void to(float* f) const { f[0] = to_f32<T>(r); }
-    __device__ __forceinline__ void from(const float* f) { r = from_f32<T>(f[0]); }
-    __device__ __forceinline__ void store(T* p) const { *p = r; }
-    __device__ __forceinline__ void zero() { r = from_f32<T>(0.f); }
-};
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// 2^x by the special-function unit (relative error about 2^-22; 0 below the normal range).
+// 2^x and 1 / x by the special-function unit (relative errors about 2^-22 and 2^-23; subnormal
+// numbers count as zero).
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 constexpr float kLog2e = 1.4426950408889634f;
 // 1 / (1 + e^-x).  e^-x may overflow to infinity: the quotient is then 0, as it should be.
-__device__ __forceinline__ float sigmoid(float x) { return __frcp_rn(1.0f + ex2(-kLog2e * x)); }
+__device__ __forceinline__ float sigmoid(float x) { return rcp(1.0f + ex2(-kLog2e * x)); }
+__device__ __forceinline__ f2 ex2_2(f2 x) {
+    float a, b;
+    unpack(x, a, b);
+    return pack(ex2(a), ex2(b));
+}
+__device__ __forceinline__ f2 sigmoid2(f2 x) {
+    float a, b;
+    unpack(x, a, b);
+    return pack(sigmoid(a), sigmoid(b));
+}
 
 }  // namespace kda
 

@@ -7,11 +7,12 @@
 // and backwards, with dp = dy act'(p):
 //     dline_i = sum_j w[c][j] dp_{i+(W-1)-j} (+ the final history's gradient),
 //     dw[c][j] = sum_t dp_t line_{t-(W-1)+j},   dbias = sum_t dp_t.
-// Everything moves W rows through registers, so each direction reads and writes its rows once and
-// HBM bounds it.  A thread owns 16 bytes of channels (or one channel where the rows are not 16-byte
-// pieces) and walks a run of tokens with the last W - 1 inputs (and, backwards, the W - 1 unfinished
-// input gradients) in registers; runs meet at W - 1 rows that both read.  Eight rows are requested
-// before the first is used.
+// Each direction reads and writes its rows once, so HBM bounds it.  A thread owns 16 bytes of channels
+// (8 backwards, where it holds more per channel; one channel where the rows are not such pieces) and
+// walks a run of tokens with the last W - 1 inputs (and, backwards, the W - 1 unfinished input
+// gradients) in registers; runs meet at W - 1 rows that both read.  Rows arrive by asynchronous copies
+// into shared memory, batches ahead of their use; a thread reads back only what it copied itself, so
+// nothing in the walk waits for another thread.
 #include "kda_layer.h"
 #include "kda_segments.cuh"
 #include "kda_slots.cuh"
@@ -21,28 +22,43 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kTile = 64;   // tokens of one look at the sequence boundaries
-constexpr int kBatch = 8;   // rows in flight per thread
+constexpr int kSms = 152;
+constexpr int kResident = 4;  // blocks of an SM that the kernels below are built for
+constexpr int kTile = 64;     // tokens of one look at the sequence boundaries
+constexpr int kStages = 3;    // asynchronous groups of a thread: one in use, two on their way
+
+// Rows of one group: 48 KB of shared memory a block at most, four blocks an SM.
+constexpr int batch_of(int bytes) { return bytes <= 16 ? 8 : 4; }
+
+template <typename T, int VEC>
+struct FwdShared {
+    static constexpr int kBatch = batch_of(Row<T, VEC>::kBytes);
+    typename Row<T, VEC>::Raw ring[kStages][kBatch][kThreads];
+    TokenTile<kTile> tile;
+};
+template <typename T, typename TG, int VEC>
+struct BwdShared {
+    static constexpr int kBatch = batch_of(Row<T, VEC>::kBytes + Row<TG, VEC>::kBytes);
+    typename Row<T, VEC>::Raw ring[kStages][kBatch][kThreads];
+    typename Row<TG, VEC>::Raw gring[kStages][kBatch][kThreads];
+    TokenTile<kTile> tile;
+};
 
 template <typename T, int VEC, int W>
-__device__ __forceinline__ void load_history(const T* hist, int64_t n, int C, int c0, float (&win)[W - 1][VEC]) {
+__device__ __forceinline__ void load_history(const T* hist, int64_t n, int C, int c0, f2 (&win)[W - 1][Row<T, VEC>::N2]) {
 #pragma unroll
     for (int k = 0; k < W - 1; ++k) {
-        if (hist) {
-            Row<T, VEC> r;
-            r.load(hist + (n * (W - 1) + k) * C + c0);
-            r.to(win[k]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) win[k][i] = 0.f;
-        }
+        Row<T, VEC> r;
+        r.zero();
+        if (hist) r.load(hist + (n * (W - 1) + k) * C + c0);
+        r.to(win[k]);
     }
 }
 
 // The W - 1 line entries before token t of sequence n, which began at s <= t.
 template <typename T, int VEC, int W>
 __device__ __forceinline__ void load_window(const T* x, int64_t ldx, const T* hist, int n, int s, int t, int C, int c0,
-                                            float (&win)[W - 1][VEC]) {
+                                            f2 (&win)[W - 1][Row<T, VEC>::N2]) {
 #pragma unroll
     for (int k = 0; k < W - 1; ++k) {
         const int pos = t - (W - 1) + k;
@@ -55,7 +71,7 @@ __device__ __forceinline__ void load_window(const T* x, int64_t ldx, const T* hi
 }
 
 template <typename T, int VEC, int W>
-__device__ __forceinline__ void store_history(T* hist, int64_t n, int C, int c0, const float (&win)[W - 1][VEC]) {
+__device__ __forceinline__ void store_history(T* hist, int64_t n, int C, int c0, const f2 (&win)[W - 1][Row<T, VEC>::N2]) {
 #pragma unroll
     for (int k = 0; k < W - 1; ++k) {
         Row<T, VEC> r;
@@ -65,69 +81,132 @@ __device__ __forceinline__ void store_history(T* hist, int64_t n, int C, int c0,
 }
 
 template <int VEC, int W>
-__device__ __forceinline__ void load_taps(const float* weight, const float* bias, int c0, float (&w)[W][VEC],
-                                          float (&b)[VEC]) {
+__device__ __forceinline__ void load_taps(const float* weight, const float* bias, int c0, f2 (&w)[W][(VEC + 1) / 2],
+                                          f2 (&b)[(VEC + 1) / 2]) {
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
+    for (int i = 0; i < (VEC + 1) / 2; ++i) {
+        const bool two = 2 * i + 1 < VEC;
+        const float* at = weight + (int64_t)(c0 + 2 * i) * W;
 #pragma unroll
-        for (int j = 0; j < W; ++j) w[j][i] = __ldg(weight + (int64_t)(c0 + i) * W + j);
-        b[i] = bias ? __ldg(bias + c0 + i) : 0.f;
+        for (int j = 0; j < W; ++j) w[j][i] = pack(__ldg(at + j), two ? __ldg(at + W + j) : 0.f);
+        b[i] = bias ? pack(__ldg(bias + c0 + 2 * i), two ? __ldg(bias + c0 + 2 * i + 1) : 0.f) : 0ull;
+    }
+}
+
+template <int N2, int W>
+__device__ __forceinline__ void preact(const f2 (&w)[W][N2], const f2 (&b)[N2], const f2 (&win)[W - 1][N2], const f2 (&v)[N2],
+                                       f2 (&p)[N2]) {
+#pragma unroll
+    for (int k = 0; k < N2; ++k) {
+        p[k] = b[k];
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) p[k] = fma2(w[j][k], win[j][k], p[k]);
+        p[k] = fma2(w[W - 1][k], v[k], p[k]);
+    }
+}
+template <int N2, int R>
+__device__ __forceinline__ void shift(f2 (&win)[R][N2], const f2 (&v)[N2]) {
+#pragma unroll
+    for (int k = 0; k < N2; ++k) {
+#pragma unroll
+        for (int j = 0; j + 1 < R; ++j) win[j][k] = win[j + 1][k];
+        win[R - 1][k] = v[k];
     }
 }
 
 template <typename T, int VEC, int W>
-__global__ void __launch_bounds__(kThreads, VEC > 1 ? 4 : 8) conv_fwd_kernel(ConvParams p, SeqMap m, int run) {
-    __shared__ TokenTile<kTile> tile;
-    const int c0 = (blockIdx.x * kThreads + threadIdx.x) * VEC;
+__global__ void __launch_bounds__(kThreads, kResident) conv_fwd_kernel(ConvParams p, SeqMap m, int run) {
+    typedef Row<T, VEC> R;
+    constexpr int N2 = R::N2;
+    typedef FwdShared<T, VEC> Sh;
+    constexpr int kBatch = Sh::kBatch;
+    extern __shared__ __align__(16) char smem[];
+    Sh& sh = *reinterpret_cast<Sh*>(smem);
+    auto& tile = sh.tile;
+    auto& ring = sh.ring;
+    const int tid = threadIdx.x;
+    const int c0 = (blockIdx.x * kThreads + tid) * VEC;
     const bool on = c0 < p.C;
-    const T* x = static_cast<const T*>(p.x);
+    const T* x = static_cast<const T*>(p.x) + (on ? c0 : 0);
     const T* hist = static_cast<const T*>(p.initial);
-    T* y = static_cast<T*>(p.y);
+    T* y = static_cast<T*>(p.y) + c0;
     T* fin = static_cast<T*>(p.final_hist);
-    float w[W][VEC], b[VEC], win[W - 1][VEC] = {};
+    const int r0 = blockIdx.y * run, r1 = min(m.total, r0 + run);
+    auto request = [&](int t) {
+        if (t < r1) {
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+                R::copy_async(&ring[(t - r0) / kBatch % kStages][i][tid], x + (int64_t)min(t + i, r1 - 1) * p.ldx);
+        }
+        copies_commit();
+    };
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) request(r0 + s * kBatch);
+    f2 w[W][N2], b[N2], win[W - 1][N2];
+#pragma unroll
+    for (int k = 0; k < N2; ++k) {
+        b[k] = 0ull;
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) win[j][k] = 0ull;
+    }
     if (on) load_taps<VEC, W>(p.weight, p.bias, c0, w, b);
     // a sequence without tokens hands its history on
     if (fin && on)
         for (int n = blockIdx.y; n < m.N; n += gridDim.y)
             if (m.end(n) <= m.begin(n)) {
-                float h[W - 1][VEC];
+                f2 h[W - 1][N2];
                 load_history<T, VEC, W>(hist, n, p.C, c0, h);
                 store_history<T, VEC, W>(fin, n, p.C, c0, h);
             }
-    const int r0 = blockIdx.y * run, r1 = min(m.total, r0 + run);
-    for (int t0 = r0; t0 < r1; t0 += kTile) {
-        __syncthreads();
-        tile.build<kThreads>(m, t0);
-        if (!on) continue;
-        if (t0 == r0 && tile.carry >= 0)
-            load_window<T, VEC, W>(x, p.ldx, hist, tile.carry, tile.carry_start, t0, p.C, c0, win);
-        const int lo = max(t0, m.first()), hi = min(min(t0 + kTile, r1), m.last());
-        for (int t = lo; t < hi; t += kBatch) {
-            Row<T, VEC> in[kBatch];
+    const int first = m.first(), last = m.last();
+    auto row = [&](int t, const R& in) {
+        f2 v[N2], o[N2];
+        in.to(v);
+        preact<N2, W>(w, b, win, v, o);
+        if (p.act) {
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i)
-                if (t + i < hi) in[i].load(x + (int64_t)(t + i) * p.ldx + c0);
+            for (int k = 0; k < N2; ++k) o[k] = mul2(o[k], sigmoid2(o[k]));
+        }
+        shift<N2, W - 1>(win, v);
+        R out;
+        out.from(o);
+        out.store(y + (int64_t)t * p.C);
+    };
+    int until = r0;  // no boundary before this token
+    bool plain = false;
+    for (int t = r0; t < r1; t += kBatch) {
+        if ((t - r0) % kTile == 0) {
+            plain = t > r0 && t + kTile < until && t >= first;
+            if (!plain) {
+                __syncthreads();
+                tile.build<kThreads>(m, t);
+                until = tile.until;
+                if (t == r0 && tile.carry >= 0 && on)
+                    load_window<T, VEC, W>(x - c0, p.ldx, hist, tile.carry, tile.carry_start, t, p.C, c0, win);
+            }
+        }
+        request(t + (kStages - 1) * kBatch);
+        copies_wait<kStages - 1>();
+        if (!on) continue;
+        const auto& rows = ring[(t - r0) / kBatch % kStages];
+        if (plain && t + kBatch <= r1) {
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
-                if (t + i >= hi) break;
-                const int s = tile.start[t + i - t0], e = tile.end[t + i - t0];
+                R in;
+                in.from_shared(&rows[i][tid]);
+                row(t + i, in);
+            }
+        } else {
+            const int k0 = (t - r0) % kTile;
+#pragma unroll 1
+            for (int i = 0; i < kBatch; ++i) {
+                if (t + i >= r1 || t + i >= last) break;
+                if (t + i < first) continue;
+                const int s = plain ? -1 : tile.start[k0 + i], e = plain ? -1 : tile.end[k0 + i];
                 if (s >= 0) load_history<T, VEC, W>(hist, s, p.C, c0, win);
-                float v[VEC], o[VEC];
-                in[i].to(v);
-#pragma unroll
-                for (int k = 0; k < VEC; ++k) {
-                    float a = b[k];
-#pragma unroll
-                    for (int j = 0; j < W - 1; ++j) a = fmaf(w[j][k], win[j][k], a);
-                    a = fmaf(w[W - 1][k], v[k], a);
-                    o[k] = p.act ? a * sigmoid(a) : a;
-#pragma unroll
-                    for (int j = 0; j < W - 2; ++j) win[j][k] = win[j + 1][k];
-                    win[W - 2][k] = v[k];
-                }
-                Row<T, VEC> out;
-                out.from(o);
-                out.store(y + (int64_t)(t + i) * p.C + c0);
+                R in;
+                in.from_shared(&rows[i][tid]);
+                row(t + i, in);
                 if (e >= 0 && fin) store_history<T, VEC, W>(fin, e, p.C, c0, win);
             }
         }
@@ -135,240 +214,319 @@ __global__ void __launch_bounds__(kThreads, VEC > 1 ? 4 : 8) conv_fwd_kernel(Con
 }
 
 // Backward over tokens [r0, r1) of a run and the W - 1 behind it, whose dp the run's last inputs
-// need.  ring[k] is the unfinished gradient of line entry t - (W - 1) + k.
+// need.  acc[k] is the unfinished gradient of line entry t - (W - 1) + k.
 template <typename T, typename TG, int VEC, int W>
-__global__ void __launch_bounds__(kThreads, VEC > 1 ? 3 : 8) conv_bwd_kernel(ConvParams p, SeqMap m, int run) {
-    __shared__ TokenTile<kTile> tile;
-    const int c0 = (blockIdx.x * kThreads + threadIdx.x) * VEC;
+__global__ void __launch_bounds__(kThreads, kResident) conv_bwd_kernel(ConvParams p, SeqMap m, int run) {
+    typedef Row<T, VEC> R;
+    typedef Row<TG, VEC> RG;
+    constexpr int N2 = R::N2;
+    typedef BwdShared<T, TG, VEC> Sh;
+    constexpr int kBatch = Sh::kBatch;
+    extern __shared__ __align__(16) char smem[];
+    Sh& sh = *reinterpret_cast<Sh*>(smem);
+    auto& tile = sh.tile;
+    auto& ring = sh.ring;
+    auto& gring = sh.gring;
+    const int tid = threadIdx.x;
+    const int c0 = (blockIdx.x * kThreads + tid) * VEC;
     const bool on = c0 < p.C;
-    const T* x = static_cast<const T*>(p.x);
+    const T* x = static_cast<const T*>(p.x) + (on ? c0 : 0);
     const T* hist = static_cast<const T*>(p.initial);
-    const TG* dy = static_cast<const TG*>(p.dy);
+    const TG* dy = static_cast<const TG*>(p.dy) + (on ? c0 : 0);
     const TG* dfin = static_cast<const TG*>(p.dfinal);
-    TG* dx = static_cast<TG*>(p.dx);
+    TG* dx = static_cast<TG*>(p.dx) + c0;
     TG* dinit = static_cast<TG*>(p.dinitial);
-    float w[W][VEC], b[VEC], win[W - 1][VEC] = {}, ring[W][VEC] = {};
-    float dw[W][VEC] = {}, db[VEC] = {};
+    const int r0 = blockIdx.y * run, r1 = min(m.total, r0 + run), stop = min(m.total, r1 + W - 1);
+    auto request = [&](int t) {
+        if (t < stop) {
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int64_t at = min(t + i, stop - 1);
+                const int s = (t - r0) / kBatch % kStages;
+                R::copy_async(&ring[s][i][tid], x + at * p.ldx);
+                RG::copy_async(&gring[s][i][tid], dy + at * p.C);
+            }
+        }
+        copies_commit();
+    };
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) request(r0 + s * kBatch);
+    f2 w[W][N2], b[N2], win[W - 1][N2], acc[W][N2], dw[W][N2], db[N2];
+#pragma unroll
+    for (int k = 0; k < N2; ++k) {
+        b[k] = db[k] = 0ull;
+#pragma unroll
+        for (int j = 0; j < W; ++j) acc[j][k] = dw[j][k] = 0ull;
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) win[j][k] = 0ull;
+    }
     if (on) load_taps<VEC, W>(p.weight, p.bias, c0, w, b);
     // a sequence without tokens hands its history's gradient back
     if (dinit && on)
         for (int n = blockIdx.y; n < m.N; n += gridDim.y)
             if (m.end(n) <= m.begin(n)) {
-                float h[W - 1][VEC];
+                f2 h[W - 1][N2];
                 load_history<TG, VEC, W>(dfin, n, p.C, c0, h);
                 store_history<TG, VEC, W>(dinit, n, p.C, c0, h);
             }
-    const int r0 = blockIdx.y * run, r1 = min(m.total, r0 + run);
-    const int last = m.last();
-    int seq = -1, begin = r0;   // the sequence of the token at hand and its first token
-    bool done = false;          // behind the run: the run's entries are finished
+    const int first = m.first(), last = m.last();
+    int seq = -1, begin = r0;  // the sequence of the token at hand and its first token
     // line entry `pos` of the sequence at hand is finished
-    auto finish = [&](int pos, const float* g) {
+    auto finish = [&](int pos, const f2 (&g)[N2]) {
+        RG r;
+        r.from(g);
         if (pos >= begin) {
-            if (pos < r0 || pos >= r1) return;
-            Row<TG, VEC> r;
-            r.from(g);
-            r.store(dx + (int64_t)pos * p.C + c0);
+            if (pos >= r0 && pos < r1) r.store(dx + (int64_t)pos * p.C);
         } else if (dinit && seq >= 0 && begin >= r0 && begin < r1) {
-            Row<TG, VEC> r;
-            r.from(g);
             r.store(dinit + ((int64_t)seq * (W - 1) + (W - 1) + pos - begin) * p.C + c0);
         }
     };
-    for (int t0 = r0; t0 < min(last, r1 + W - 1); t0 += kTile) {
-        __syncthreads();
-        tile.build<kThreads>(m, t0);
-        if (!on) continue;
-        if (t0 == r0 && tile.carry >= 0) {
-            seq = tile.carry;
-            begin = tile.carry_start;
-            load_window<T, VEC, W>(x, p.ldx, hist, seq, begin, t0, p.C, c0, win);
-        }
-        const int lo = max(t0, m.first()), hi = min(min(t0 + kTile, r1 + W - 1), last);
-        for (int t = lo; t < hi && !done; t += kBatch) {
-            Row<T, VEC> in[kBatch];
-            Row<TG, VEC> gr[kBatch];
+    // token t; `mine`: it lies in the run, so its share of dw and dbias is this run's
+    auto row = [&](const R& in, const RG& gr, bool mine) {
+        f2 v[N2], d[N2];
+        in.to(v);
+        gr.to(d);
+        if (p.act) {
+            f2 a[N2];
+            preact<N2, W>(w, b, win, v, a);
+            const f2 one = pack(1.f, 1.f), minus = pack(-1.f, -1.f);
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i)
-                if (t + i < hi) {
-                    in[i].load(x + (int64_t)(t + i) * p.ldx + c0);
-                    gr[i].load(dy + (int64_t)(t + i) * p.C + c0);
+            for (int k = 0; k < N2; ++k) {
+                const f2 sg = sigmoid2(a[k]);
+                d[k] = mul2(d[k], mul2(sg, fma2(a[k], fma2(minus, sg, one), one)));
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < N2; ++k) {
+#pragma unroll
+            for (int j = 0; j < W; ++j) acc[j][k] = fma2(w[j][k], d[k], acc[j][k]);
+            if (mine) {
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j) dw[j][k] = fma2(d[k], win[j][k], dw[j][k]);
+                dw[W - 1][k] = fma2(d[k], v[k], dw[W - 1][k]);
+                db[k] = add2(db[k], d[k]);
+            }
+        }
+        shift<N2, W - 1>(win, v);
+    };
+    const f2 zero[N2] = {};
+    int until = r0;
+    bool plain = false, done = false;
+    for (int t = r0; t < stop; t += kBatch) {
+        if ((t - r0) % kTile == 0) {
+            plain = t > r0 && t + kTile < until && t >= first;
+            if (!plain) {
+                __syncthreads();
+                tile.build<kThreads>(m, t);
+                until = tile.until;
+                if (t == r0 && tile.carry >= 0 && on) {
+                    seq = tile.carry;
+                    begin = tile.carry_start;
+                    load_window<T, VEC, W>(x - c0, p.ldx, hist, seq, begin, t, p.C, c0, win);
                 }
+            }
+        }
+        request(t + (kStages - 1) * kBatch);
+        copies_wait<kStages - 1>();
+        if (!on || done) continue;
+        const int s = (t - r0) / kBatch % kStages;
+        if (plain && t + kBatch <= r1 && t - (W - 1) >= max(begin, r0)) {
+            // every entry finished here is a token of the run
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
-                if (t + i >= hi || done) break;
-                const int s = tile.start[t + i - t0], e = tile.end[t + i - t0];
-                if (s >= 0) {
-                    if (t + i >= r1) {
-                        done = true;
+                R in;
+                RG gr, out;
+                in.from_shared(&ring[s][i][tid]);
+                gr.from_shared(&gring[s][i][tid]);
+                row(in, gr, true);
+                out.from(acc[0]);
+                out.store(dx + (int64_t)(t + i - (W - 1)) * p.C);
+                shift<N2, W>(acc, zero);
+            }
+        } else {
+            const int k0 = (t - r0) % kTile;
+#pragma unroll 1
+            for (int i = 0; i < kBatch; ++i) {
+                const int at = t + i;
+                if (at >= stop || at >= last) break;
+                if (at < first) continue;
+                const int sb = plain ? -1 : tile.start[k0 + i], se = plain ? -1 : tile.end[k0 + i];
+                if (sb >= 0) {
+                    if (at >= r1) {
+                        done = true;  // the run's entries are finished
                         break;
                     }
-                    seq = s;
-                    begin = t + i;
-                    load_history<T, VEC, W>(hist, s, p.C, c0, win);
+                    seq = sb;
+                    begin = at;
+                    load_history<T, VEC, W>(hist, sb, p.C, c0, win);
 #pragma unroll
                     for (int j = 0; j < W; ++j)
 #pragma unroll
-                        for (int k = 0; k < VEC; ++k) ring[j][k] = 0.f;
+                        for (int k = 0; k < N2; ++k) acc[j][k] = 0ull;
                 }
-                const bool mine = t + i < r1;
-                float v[VEC], d[VEC];
-                in[i].to(v);
-                gr[i].to(d);
-#pragma unroll
-                for (int k = 0; k < VEC; ++k) {
-                    if (p.act) {
-                        float a = b[k];
-#pragma unroll
-                        for (int j = 0; j < W - 1; ++j) a = fmaf(w[j][k], win[j][k], a);
-                        a = fmaf(w[W - 1][k], v[k], a);
-                        const float sg = sigmoid(a);
-                        d[k] *= sg * fmaf(a, 1.f - sg, 1.f);
-                    }
-#pragma unroll
-                    for (int j = 0; j < W; ++j) ring[j][k] = fmaf(w[j][k], d[k], ring[j][k]);
-                    if (mine) {
-#pragma unroll
-                        for (int j = 0; j < W - 1; ++j) dw[j][k] = fmaf(d[k], win[j][k], dw[j][k]);
-                        dw[W - 1][k] = fmaf(d[k], v[k], dw[W - 1][k]);
-                        db[k] += d[k];
-                    }
-#pragma unroll
-                    for (int j = 0; j < W - 2; ++j) win[j][k] = win[j + 1][k];
-                    win[W - 2][k] = v[k];
-                }
-                finish(t + i - (W - 1), ring[0]);
-#pragma unroll
-                for (int j = 0; j < W - 1; ++j)
-#pragma unroll
-                    for (int k = 0; k < VEC; ++k) ring[j][k] = ring[j + 1][k];
-#pragma unroll
-                for (int k = 0; k < VEC; ++k) ring[W - 1][k] = 0.f;
-                if (e >= 0) {
+                R in;
+                RG gr;
+                in.from_shared(&ring[s][i][tid]);
+                gr.from_shared(&gring[s][i][tid]);
+                row(in, gr, at < r1);
+                finish(at - (W - 1), acc[0]);
+                shift<N2, W>(acc, zero);
+                if (se >= 0) {
                     // the sequence's last W - 1 entries: no more dp, but the final history's gradient
 #pragma unroll
                     for (int j = 0; j < W - 1; ++j) {
                         if (dfin) {
-                            float f[VEC];
-                            Row<TG, VEC> r;
-                            r.load(dfin + ((int64_t)e * (W - 1) + j) * p.C + c0);
+                            f2 f[N2];
+                            RG r;
+                            r.load(dfin + ((int64_t)se * (W - 1) + j) * p.C + c0);
                             r.to(f);
 #pragma unroll
-                            for (int k = 0; k < VEC; ++k) ring[j][k] += f[k];
+                            for (int k = 0; k < N2; ++k) acc[j][k] = add2(acc[j][k], f[k]);
                         }
-                        finish(t + i - (W - 2) + j, ring[j]);
+                        finish(at - (W - 2) + j, acc[j]);
                     }
-                    if (!mine) done = true;
+                    if (at >= r1) {
+                        done = true;
+                        break;
+                    }
                 }
             }
         }
     }
     if (on) {
-        float* out = p.partial + ((int64_t)blockIdx.y * p.C + c0) * (W + 1);
+        // [run][tap, and the bias][C]
+        float* out = p.partial + (int64_t)blockIdx.y * (W + 1) * p.C + c0;
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) {
+        for (int j = 0; j <= W; ++j)
 #pragma unroll
-            for (int j = 0; j < W; ++j) out[k * (W + 1) + j] = dw[j][k];
-            out[k * (W + 1) + W] = db[k];
-        }
+            for (int k = 0; k < N2; ++k) {
+                float a, c;
+                unpack(j < W ? dw[j < W ? j : 0][k] : db[k], a, c);
+                out[(int64_t)j * p.C + 2 * k] = a;
+                if (2 * k + 1 < VEC) out[(int64_t)j * p.C + 2 * k + 1] = c;
+            }
     }
 }
 
 // dw and dbias from the runs' partial sums, in the order of the runs.
-__global__ void __launch_bounds__(256) conv_bwd_sum_kernel(const float* partial, int runs, int C, int W, float* dw,
+__global__ void __launch_bounds__(128) conv_bwd_sum_kernel(const float* partial, int runs, int C, int W, float* dw,
                                                            float* db) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, n = (int64_t)C * (W + 1);
+    const int64_t i = (int64_t)blockIdx.x * 128 + threadIdx.x, n = (int64_t)C * (W + 1);
     if (i >= n) return;
     float a = 0.f;
+#pragma unroll 8
     for (int r = 0; r < runs; ++r) a += partial[r * n + i];
-    const int64_t c = i / (W + 1);
-    const int j = (int)(i % (W + 1));
+    const int64_t c = i % C;
+    const int j = (int)(i / C);
     if (j < W) dw[c * W + j] = a;
     else if (db) db[c] = a;
 }
 
-template <typename T, int VEC, int W>
+// kRows rows of the batch a block, so that the taps are fetched once for them: they are as many
+// bytes as two rows' histories.
+template <typename T, int VEC, int W, int kRows>
 __global__ void __launch_bounds__(kThreads) conv_step_kernel(ConvStepParams p) {
-    const int row = blockIdx.x;
-    const int page = page_of_row(p.slots, row, p.P);
-    if (row_refused(p.slots, row, page, p.status)) return;
+    typedef Row<T, VEC> R;
+    constexpr int N2 = R::N2;
+    const int row0 = blockIdx.x * kRows;
     const int c0 = (blockIdx.y * kThreads + threadIdx.x) * VEC;
-    if (c0 >= p.C) return;
+    const bool on = c0 < p.C;
     T* hist = static_cast<T*>(p.history);
-    Row<T, VEC> in;
-    in.load(static_cast<const T*>(p.x) + row * p.ldx + c0);
-    Row<T, VEC> past[W - 1];
+    int page[kRows];
+    R in[kRows], past[kRows][W - 1];
 #pragma unroll
-    for (int k = 0; k < W - 1; ++k) past[k].load_rw(hist + ((int64_t)page * (W - 1) + k) * p.C + c0);
-    float w[W][VEC], b[VEC], v[VEC], o[VEC];
-    load_taps<VEC, W>(p.weight, p.bias, c0, w, b);
-    in.to(v);
+    for (int i = 0; i < kRows; ++i) {
+        page[i] = row0 + i < p.N ? page_of_row(p.slots, row0 + i, p.P) : -1;
+        if (!on || page[i] < 0) continue;
+        in[i].load(static_cast<const T*>(p.x) + (row0 + i) * p.ldx + c0);
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) o[k] = fmaf(w[W - 1][k], v[k], b[k]);
-#pragma unroll
-    for (int j = 0; j < W - 1; ++j) {
-        float h[VEC];
-        past[j].to(h);
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) o[k] = fmaf(w[j][k], h[k], o[k]);
+        for (int k = 0; k < W - 1; ++k) past[i][k].load_rw(hist + ((int64_t)page[i] * (W - 1) + k) * p.C + c0);
     }
-    if (p.act) {
+    f2 w[W][N2], b[N2];
+    if (on) load_taps<VEC, W>(p.weight, p.bias, c0, w, b);
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) o[k] *= sigmoid(o[k]);
+    for (int i = 0; i < kRows; ++i) {
+        if (row0 + i >= p.N) break;
+        if (row_refused(p.slots, row0 + i, page[i], p.status) || !on) continue;
+        f2 win[W - 1][N2], v[N2], o[N2];
+        in[i].to(v);
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k) past[i][k].to(win[k]);
+        preact<N2, W>(w, b, win, v, o);
+        if (p.act) {
+#pragma unroll
+            for (int k = 0; k < N2; ++k) o[k] = mul2(o[k], sigmoid2(o[k]));
+        }
+        R out;
+        out.from(o);
+        out.store(static_cast<T*>(p.y) + (int64_t)(row0 + i) * p.C + c0);
+#pragma unroll
+        for (int k = 0; k + 1 < W - 1; ++k) past[i][k + 1].store(hist + ((int64_t)page[i] * (W - 1) + k) * p.C + c0);
+        in[i].store(hist + ((int64_t)page[i] * (W - 1) + W - 2) * p.C + c0);
     }
-    Row<T, VEC> out;
-    out.from(o);
-    out.store(static_cast<T*>(p.y) + (int64_t)row * p.C + c0);
-#pragma unroll
-    for (int k = 0; k + 1 < W - 1; ++k) past[k + 1].store(hist + ((int64_t)page * (W - 1) + k) * p.C + c0);
-    in.store(hist + ((int64_t)page * (W - 1) + W - 2) * p.C + c0);
 }
 
-// Tokens of one run: enough runs to fill the machine about twice over, at least 32 tokens each
-// so that the W - 1 rows read twice stay below a tenth.
+// Tokens of one run: as many runs as one filling of the machine holds, at least 32 tokens each so
+// that the W - 1 rows read twice stay below a tenth.
 int run_tokens(int total, int C, int vec) {
     const int blocks = (C + kThreads * vec - 1) / (kThreads * vec);
-    const int runs = (152 * 8 + blocks - 1) / blocks;
+    const int runs = kSms * kResident / blocks > 0 ? kSms * kResident / blocks : 1;
     int run = (total + runs - 1) / runs;
-    run = (run + kBatch - 1) / kBatch * kBatch;
+    run = (run + 7) / 8 * 8;
     return run < 32 ? 32 : run;
 }
 int run_count(int total, int run) { return total > 0 ? (total + run - 1) / run : 1; }
 
 SeqMap seq_map(const ConvParams& p) { return SeqMap{p.cu, p.N, p.T, p.total}; }
 
+template <typename K>
+cudaError_t launch_runs(K kern, const ConvParams& p, int vec, int smem, cudaStream_t st) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const int run = run_tokens(p.total, p.C, vec);
+    const dim3 grid((p.C + kThreads * vec - 1) / (kThreads * vec), run_count(p.total, run));
+    kern<<<grid, kThreads, smem, st>>>(p, seq_map(p), run);
+    return cudaGetLastError();
+}
+
 template <typename T, int VEC>
 cudaError_t launch_fwd(const ConvParams& p, cudaStream_t st) {
-    const int run = run_tokens(p.total, p.C, VEC);
-    const dim3 grid((p.C + kThreads * VEC - 1) / (kThreads * VEC), run_count(p.total, run));
-    if (p.W == 4) conv_fwd_kernel<T, VEC, 4><<<grid, kThreads, 0, st>>>(p, seq_map(p), run);
-    else if (p.W == 3) conv_fwd_kernel<T, VEC, 3><<<grid, kThreads, 0, st>>>(p, seq_map(p), run);
-    else conv_fwd_kernel<T, VEC, 2><<<grid, kThreads, 0, st>>>(p, seq_map(p), run);
-    return cudaGetLastError();
+    constexpr int smem = sizeof(FwdShared<T, VEC>);
+    if (p.W == 4) return launch_runs(conv_fwd_kernel<T, VEC, 4>, p, VEC, smem, st);
+    if (p.W == 3) return launch_runs(conv_fwd_kernel<T, VEC, 3>, p, VEC, smem, st);
+    return launch_runs(conv_fwd_kernel<T, VEC, 2>, p, VEC, smem, st);
 }
 
 template <typename T, typename TG, int VEC>
 cudaError_t launch_bwd(const ConvParams& p, cudaStream_t st) {
-    const int run = run_tokens(p.total, p.C, VEC), runs = run_count(p.total, run);
-    const dim3 grid((p.C + kThreads * VEC - 1) / (kThreads * VEC), runs);
-    if (p.W == 4) conv_bwd_kernel<T, TG, VEC, 4><<<grid, kThreads, 0, st>>>(p, seq_map(p), run);
-    else if (p.W == 3) conv_bwd_kernel<T, TG, VEC, 3><<<grid, kThreads, 0, st>>>(p, seq_map(p), run);
-    else conv_bwd_kernel<T, TG, VEC, 2><<<grid, kThreads, 0, st>>>(p, seq_map(p), run);
-    cudaError_t e = cudaGetLastError();
+    constexpr int smem = sizeof(BwdShared<T, TG, VEC>);
+    cudaError_t e = p.W == 4   ? launch_runs(conv_bwd_kernel<T, TG, VEC, 4>, p, VEC, smem, st)
+                    : p.W == 3 ? launch_runs(conv_bwd_kernel<T, TG, VEC, 3>, p, VEC, smem, st)
+                               : launch_runs(conv_bwd_kernel<T, TG, VEC, 2>, p, VEC, smem, st);
     if (e != cudaSuccess) return e;
+    const int runs = run_count(p.total, run_tokens(p.total, p.C, VEC));
     const int64_t n = (int64_t)p.C * (p.W + 1);
-    conv_bwd_sum_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(p.partial, runs, p.C, p.W, p.dweight, p.dbias);
+    conv_bwd_sum_kernel<<<(unsigned)((n + 127) / 128), 128, 0, st>>>(p.partial, runs, p.C, p.W, p.dweight, p.dbias);
     return cudaGetLastError();
 }
 
-template <typename T, int VEC>
-cudaError_t launch_step(const ConvStepParams& p, cudaStream_t st) {
-    const dim3 grid(p.N, (p.C + kThreads * VEC - 1) / (kThreads * VEC));
-    if (p.W == 4) conv_step_kernel<T, VEC, 4><<<grid, kThreads, 0, st>>>(p);
-    else if (p.W == 3) conv_step_kernel<T, VEC, 3><<<grid, kThreads, 0, st>>>(p);
-    else conv_step_kernel<T, VEC, 2><<<grid, kThreads, 0, st>>>(p);
+template <typename T, int VEC, int W>
+cudaError_t launch_step_rows(const ConvStepParams& p, cudaStream_t st) {
+    const int blocks = (p.C + kThreads * VEC - 1) / (kThreads * VEC);
+    // four rows a block once that leaves two blocks an SM, else one
+    if ((int64_t)(p.N + 3) / 4 * blocks >= 2 * kSms) conv_step_kernel<T, VEC, W, 4><<<dim3((p.N + 3) / 4, blocks), kThreads, 0, st>>>(p);
+    else conv_step_kernel<T, VEC, W, 1><<<dim3(p.N, blocks), kThreads, 0, st>>>(p);
     return cudaGetLastError();
 }
+template <typename T, int VEC>
+cudaError_t launch_step(const ConvStepParams& p, cudaStream_t st) {
+    if (p.W == 4) return launch_step_rows<T, VEC, 4>(p, st);
+    if (p.W == 3) return launch_step_rows<T, VEC, 3>(p, st);
+    return launch_step_rows<T, VEC, 2>(p, st);
+}
+
+// Backwards a thread has four channels: 8 bytes of bf16, 16 of fp32.
+constexpr int kBwdVec = 4;
 
 }  // namespace
 
@@ -383,19 +541,18 @@ cudaError_t short_conv_fwd(kda_dtype dt, const ConvParams& p, cudaStream_t st) {
 
 size_t short_conv_bwd_partial(int total, int C, int W) {
     // the narrow variant has the fewer runs: more blocks along the channels
-    return (size_t)run_count(total, run_tokens(total, C, 8)) * C * (W + 1);
+    return (size_t)run_count(total, run_tokens(total, C, kBwdVec)) * C * (W + 1);
 }
 
 cudaError_t short_conv_bwd(kda_dtype dt, kda_dtype gdt, const ConvParams& p, cudaStream_t st) {
     using kda_host::rows_aligned;
-    const int vec = dt == KDA_BF16 ? 8 : 4;
     const void* rows[] = {p.initial, p.dy, p.dfinal, p.dx, p.dinitial};
-    bool wide = rows_aligned(p.x, p.ldx, vec) && p.C % vec == 0;
-    for (const void* r : rows) wide = wide && rows_aligned(r, p.C, vec);
-    if (dt == KDA_F32) return wide ? launch_bwd<float, float, 4>(p, st) : launch_bwd<float, float, 1>(p, st);
+    bool wide = rows_aligned(p.x, p.ldx, kBwdVec) && p.C % kBwdVec == 0;
+    for (const void* r : rows) wide = wide && rows_aligned(r, p.C, kBwdVec);
+    if (dt == KDA_F32) return wide ? launch_bwd<float, float, kBwdVec>(p, st) : launch_bwd<float, float, 1>(p, st);
     if (gdt == KDA_F32)
-        return wide ? launch_bwd<__nv_bfloat16, float, 8>(p, st) : launch_bwd<__nv_bfloat16, float, 1>(p, st);
-    return wide ? launch_bwd<__nv_bfloat16, __nv_bfloat16, 8>(p, st) : launch_bwd<__nv_bfloat16, __nv_bfloat16, 1>(p, st);
+        return wide ? launch_bwd<__nv_bfloat16, float, kBwdVec>(p, st) : launch_bwd<__nv_bfloat16, float, 1>(p, st);
+    return wide ? launch_bwd<__nv_bfloat16, __nv_bfloat16, kBwdVec>(p, st) : launch_bwd<__nv_bfloat16, __nv_bfloat16, 1>(p, st);
 }
 
 cudaError_t short_conv_step(kda_dtype dt, const ConvStepParams& p, cudaStream_t st) {

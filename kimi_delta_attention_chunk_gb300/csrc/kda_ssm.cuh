@@ -23,41 +23,6 @@ __device__ __forceinline__ float log1p_unit(float e) {
 // log(1 + e^x) = max(x, 0) + log(1 + e^-|x|)
 __device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.0f) + log1p_unit(ex2(-kLog2e * fabsf(x))); }
 
-// ---- two fp32 values in one 64-bit register ------------------------------------------------
-
-typedef unsigned long long f2;
-__device__ __forceinline__ f2 pack(float a, float b) {
-    f2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void unpack(f2 x, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x)); }
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-    f2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f2 add2(f2 a, f2 b) {
-    f2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-    f2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ f2 ex2_2(f2 x) {
-    float a, b;
-    unpack(x, a, b);
-    return pack(ex2(a), ex2(b));
-}
-__device__ __forceinline__ float sum2(f2 x) {
-    float a, b;
-    unpack(x, a, b);
-    return a + b;
-}
-
 // ---- which channels and tokens a block works on ------------------------------------------------
 
 // Blocks of CH channels, none across two groups: block x is the (x % per_group)-th of its group.

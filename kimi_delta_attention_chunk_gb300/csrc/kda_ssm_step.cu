@@ -16,54 +16,71 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// CPT channels of a thread: their state loads are all issued before the first is used.
-template <typename T, int S, int CPT>
-__global__ void __launch_bounds__(kThreads) ssm_step_kernel(SsmStepParams p) {
-    constexpr int LP = S / 4, CH = kThreads / LP;
-    const int row = blockIdx.x;
-    const int page = page_of_row(p.slots, row, p.P);
-    const int lane = threadIdx.x % LP;
-    const int c0 = blockIdx.y * (CH * CPT) + threadIdx.x / LP;
-    float4* state = reinterpret_cast<float4*>(p.state + (int64_t)max(page, 0) * p.C * S);
-    float4 h[CPT];
+// Four consecutive elements of a vector, in pairs; `wide`: as one piece.
+template <typename T>
+struct Four {
+    T v[4];
+    __device__ __forceinline__ void load(const T* p, bool wide) {
+        if (wide) {
+            typedef typename Bits<4 * sizeof(T)>::type Raw;
+            *reinterpret_cast<Raw*>(v) = __ldg(reinterpret_cast<const Raw*>(p));
+        } else {
 #pragma unroll
-    for (int i = 0; i < CPT; ++i) {
-        const int c = c0 + i * CH;
-        if (c < p.C) h[i] = __ldcs(state + (int64_t)c * LP + lane);
-    }
-    if (row_refused(p.slots, row, page, p.status)) return;
-    const int per = p.C / p.G;
-    const T* Bm = static_cast<const T*>(p.Bm) + row * p.ldb;
-    const T* Cm = static_cast<const T*>(p.Cm) + row * p.ldc;
-#pragma unroll
-    for (int i = 0; i < CPT; ++i) {
-        const int c = c0 + i * CH;
-        const bool on = c < p.C;
-        float y = 0.f, u = 0.f;
-        if (on) {
-            u = ld(static_cast<const T*>(p.u), row * p.ldu + c);
-            float d = ld(static_cast<const T*>(p.delta), row * p.ldd + c);
-            if (p.bias) d += p.bias[c];
-            if (p.softplus) d = softplus(d);
-            const int g = c / per * S + lane * 4;
-            const float4 A = *reinterpret_cast<const float4*>(p.A + (int64_t)c * S + lane * 4);
-            const float a[4] = {A.x, A.y, A.z, A.w};
-            float v[4] = {h[i].x, h[i].y, h[i].z, h[i].w};
-            const float du = d * u, dl = d * kLog2e;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                v[k] = fmaf(ex2(dl * a[k]), v[k], du * ld(Bm, g + k));
-                y = fmaf(ld(Cm, g + k), v[k], y);
-            }
-            __stcs(state + (int64_t)c * LP + lane, make_float4(v[0], v[1], v[2], v[3]));
+            for (int k = 0; k < 4; ++k) v[k] = __ldg(p + k);
         }
+    }
+};
+
+// kRows rows of the batch a block: A is as many bytes as a row's states, and is fetched once for them.
+// Everything that the rows need is requested before the first is worked on.
+template <typename T, int S, int kRows>
+__global__ void __launch_bounds__(kThreads) ssm_step_kernel(SsmStepParams p, bool wide) {
+    constexpr int LP = S / 4, CH = kThreads / LP;
+    const int row0 = blockIdx.x * kRows;
+    const int lane = threadIdx.x % LP;
+    const int c = blockIdx.y * CH + threadIdx.x / LP;
+    const bool on = c < p.C;
+    const int cc = on ? c : 0, g = cc / (p.C / p.G) * S + lane * 4;
+    int page[kRows];
+    float4 h[kRows];
+    T u[kRows], dl[kRows], z[kRows];
+    Four<T> Bv[kRows], Cv[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const int row = min(row0 + i, p.N - 1);
+        page[i] = page_of_row(p.slots, row, p.P);
+        h[i] = __ldcs(reinterpret_cast<const float4*>(p.state + ((int64_t)max(page[i], 0) * p.C + cc) * S + lane * 4));
+        u[i] = __ldg(static_cast<const T*>(p.u) + row * p.ldu + cc);
+        dl[i] = __ldg(static_cast<const T*>(p.delta) + row * p.ldd + cc);
+        if (p.z) z[i] = __ldg(static_cast<const T*>(p.z) + row * p.ldz + cc);
+        Bv[i].load(static_cast<const T*>(p.Bm) + row * p.ldb + g, wide);
+        Cv[i].load(static_cast<const T*>(p.Cm) + row * p.ldc + g, wide);
+    }
+    const float4 A = *reinterpret_cast<const float4*>(p.A + (int64_t)cc * S + lane * 4);
+    const float a[4] = {A.x, A.y, A.z, A.w};
+    const float bias = p.bias ? __ldg(p.bias + cc) : 0.f, D = p.D ? __ldg(p.D + cc) : 0.f;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const int row = row0 + i;
+        if (row >= p.N) break;
+        if (row_refused(p.slots, row, page[i], p.status)) continue;
+        float d = to_f32<T>(dl[i]) + bias;
+        if (p.softplus) d = softplus(d);
+        const float uv = to_f32<T>(u[i]), du = d * uv, de = d * kLog2e;
+        float v[4] = {h[i].x, h[i].y, h[i].z, h[i].w}, y = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            v[k] = fmaf(ex2(de * a[k]), v[k], du * to_f32<T>(Bv[i].v[k]));
+            y = fmaf(to_f32<T>(Cv[i].v[k]), v[k], y);
+        }
+        if (on) __stcs(reinterpret_cast<float4*>(p.state + ((int64_t)page[i] * p.C + c) * S + lane * 4), make_float4(v[0], v[1], v[2], v[3]));
 #pragma unroll
         for (int o = LP / 2; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
         if (on && lane == 0) {
-            if (p.D) y = fmaf(p.D[c], u, y);
+            y = fmaf(D, uv, y);
             if (p.z) {
-                const float z = ld(static_cast<const T*>(p.z), row * p.ldz + c);
-                y *= z * sigmoid(z);
+                const float zv = to_f32<T>(z[i]);
+                y *= zv * sigmoid(zv);
             }
             static_cast<T*>(p.y)[(int64_t)row * p.C + c] = from_f32<T>(y);
         }
@@ -73,11 +90,14 @@ __global__ void __launch_bounds__(kThreads) ssm_step_kernel(SsmStepParams p) {
 template <typename T, int S>
 cudaError_t launch(const SsmStepParams& p, cudaStream_t st) {
     constexpr int CH = kThreads / (S / 4);
-    // four channels a thread once that still leaves the machine full (152 SMs of 8 blocks), else one
-    if ((int64_t)p.N * ((p.C + 4 * CH - 1) / (4 * CH)) >= 152 * 8)
-        ssm_step_kernel<T, S, 4><<<dim3(p.N, (p.C + 4 * CH - 1) / (4 * CH)), kThreads, 0, st>>>(p);
+    const int blocks = (p.C + CH - 1) / CH;
+    const size_t piece = 4 * sizeof(T);
+    const bool wide = (uintptr_t)p.Bm % piece == 0 && (uintptr_t)p.Cm % piece == 0 && p.ldb % 4 == 0 && p.ldc % 4 == 0;
+    // four rows a block once that leaves the machine four blocks an SM, else one
+    if ((int64_t)(p.N + 3) / 4 * blocks >= 4 * 152)
+        ssm_step_kernel<T, S, 4><<<dim3((p.N + 3) / 4, blocks), kThreads, 0, st>>>(p, wide);
     else
-        ssm_step_kernel<T, S, 1><<<dim3(p.N, (p.C + CH - 1) / CH), kThreads, 0, st>>>(p);
+        ssm_step_kernel<T, S, 1><<<dim3(p.N, blocks), kThreads, 0, st>>>(p, wide);
     return cudaGetLastError();
 }
 

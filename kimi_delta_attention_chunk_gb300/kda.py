@@ -143,20 +143,44 @@ def _dt_of(dtype) -> int:
     raise TypeError(f"unsupported dtype {dtype}")
 
 
-def _here(*tensors):
-    """Every tensor given lies on one CUDA device, the current one."""
+def _lib_now():
+    """The library, without the lock once it is loaded."""
+    return _lib if _lib is not None else load_library()
+
+
+def _here(*tensors) -> int:
+    """Every tensor given lies on one CUDA device, the current one; returns its index."""
+    dev = -1
     for t in tensors:
         if t is None:
             continue
-        if not t.is_cuda:
+        i = t.get_device()
+        if i < 0:
             raise ValueError("tensors passed to libkda must be CUDA tensors")
-        if t.device.index != torch.cuda.current_device():
-            raise ValueError(f"a tensor lies on {t.device}, the current device is {torch.cuda.current_device()}")
+        if i != dev:
+            if i != torch.cuda.current_device():
+                raise ValueError(f"a tensor lies on {t.device}, the current device is {torch.cuda.current_device()}")
+            dev = i
+    return dev
+
+
+def _at(t):
+    """Address of a contiguous tensor that _here has looked at, None for none."""
+    if t is None:
+        return None
+    if not t.is_contiguous():
+        raise ValueError("tensors passed to libkda must be contiguous")
+    return t.data_ptr()
+
+
+def _stream_of(dev: int) -> int:
+    # the raw handle: a torch.cuda.Stream object a call would cost as much as a small kernel
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _int32(*tensors):
     for t in tensors:
-        if t is not None and t.dtype != torch.int32:
+        if t is not None and t.dtype is not torch.int32:
             raise TypeError(f"expected an int32 tensor, got {t.dtype}")
 
 
@@ -174,7 +198,7 @@ def _like(ref, *tensors):
 
 
 def _shape(name, t, shape):
-    if t is not None and tuple(t.shape) != tuple(shape):
+    if t is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
@@ -183,6 +207,8 @@ def _rows(name, t, lead: int):
     rows a fixed stride apart, each row's elements lying side by side."""
     if t is None:
         return None, 0
+    if t.is_contiguous() and t.numel():
+        return t.data_ptr(), t.stride(lead - 1) if t.shape[lead - 1] != 1 else t.shape[lead:].numel()
     width = 1
     for d in reversed(range(lead, t.dim())):
         if t.shape[d] != 1 and t.stride(d) != width:
@@ -199,7 +225,7 @@ def _rows(name, t, lead: int):
     ld = width if ld is None else ld
     if ld < width:
         raise ValueError(f"{name}: rows must not overlap")
-    return ctypes.c_void_p(t.data_ptr()), ld
+    return t.data_ptr(), ld
 
 
 def workspace_size(in_dtype, B: int, T: int, H: int, K: int, V: int, N: int, packed: bool) -> int:
@@ -364,13 +390,16 @@ def recurrent_step(q, k, v, g, beta, state, scale: float | None = None, o_dtype=
     if o is None:
         o = torch.empty((N, H, V), dtype=o_dtype, device=q.device)
     if slots is not None:
-        _here(q, k, v, g, beta, state, o, slots, status)
+        dev = _here(q, k, v, g, beta, state, o, slots, status)
         _int32(slots, status)
-        if tuple(state.shape[1:]) != (H, K, V) or slots.numel() != N:
-            raise ValueError(f"state must be [P, {H}, {K}, {V}] and slots [{N}]")
-        st = lib.kda_recurrent_step_slots(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _dt(q),
-                                          float(scale or 0.0), _ptr(state), _ptr(slots), state.shape[0], N, H,
-                                          K, V, _ptr(o), _dt(o), _ptr(status), _stream(q.device))
+        _like(q, k, v, g, beta)
+        _f32(state)
+        for name, x, shape in (("k", k, (N, H, K)), ("v", v, (N, H, V)), ("g", g, (N, H, K)), ("beta", beta, (N, H)),
+                               ("state", state, (state.shape[0], H, K, V)), ("o", o, (N, H, V)), ("slots", slots, (N,))):
+            _shape(name, x, shape)
+        st = lib.kda_recurrent_step_slots(_at(q), _at(k), _at(v), _at(g), _at(beta), _dt(q), float(scale or 0.0),
+                                          _at(state), _at(slots), state.shape[0], N, H, K, V, _at(o), _dt(o),
+                                          _at(status), _stream_of(dev))
         _check("kda_recurrent_step_slots", st)
         return o
     if status is not None:
@@ -508,7 +537,8 @@ def chunk_bwd(q, k, v, g, beta, dO, dS_T=None, scale: float | None = None, initi
 def _conv_check(x, weight, bias, conv_act):
     C, W = weight.shape
     _f32(weight, bias)
-    _shape("x", x, tuple(x.shape[:-1]) + (C,))
+    if x.shape[-1] != C:
+        raise ValueError(f"x has {x.shape[-1]} channels, expected {C}")
     _shape("bias", bias, (C,))
     if conv_act not in (0, 1):
         raise ValueError("conv_act is 0 (none) or 1 (SiLU)")
@@ -536,11 +566,11 @@ def short_conv_fwd(x, weight, bias=None, conv_act: int = 0, initial=None, cu_seq
     :func:`chunk_fwd`.  Returns (y [B,T,C], final history [N,W-1,C] or None).  Rows that
     belong to no sequence are left as they are.
     """
-    lib = load_library()
+    lib = _lib_now()
     C, W = _conv_check(x, weight, bias, conv_act)
     B, T, _ = x.shape
     N = _sequences(x, cu_seqlens)
-    _here(x, weight, bias, initial, cu_seqlens, y, final)
+    dev = _here(x, weight, bias, initial, cu_seqlens, y, final)
     _like(x, initial, y, final)
     _shape("initial", initial, (N, W - 1, C))
     _shape("y", y, (B, T, C))
@@ -550,8 +580,8 @@ def short_conv_fwd(x, weight, bias=None, conv_act: int = 0, initial=None, cu_seq
     if final is None and output_final:
         final = torch.empty((N, W - 1, C), dtype=x.dtype, device=x.device)
     px, ldx = _rows("x", x, 2)
-    st = lib.kda_short_conv_fwd(px, ldx, _ptr(weight), _ptr(bias), conv_act, _dt(x), _ptr(initial), _ptr(cu_seqlens),
-                                B, T, C, W, N, _ptr(y), _ptr(final), _stream(x.device))
+    st = lib.kda_short_conv_fwd(px, ldx, _at(weight), _at(bias), conv_act, _dt(x), _at(initial), _at(cu_seqlens),
+                                B, T, C, W, N, _at(y), _at(final), _stream_of(dev))
     _check("kda_short_conv_fwd", st)
     return y, final
 
@@ -562,26 +592,26 @@ def short_conv_bwd(x, weight, dy, bias=None, conv_act: int = 0, initial=None, cu
     arguments).  dy [B,T,C] and dfinal [N,W-1,C] share a type: x's, or fp32.  Returns a
     dict: dx [B,T,C] and dinitial [N,W-1,C] (None without ``initial``) in dy's type, dweight
     [C,W] and dbias [C] (None without ``bias``) fp32."""
-    lib = load_library()
+    lib = _lib_now()
     C, W = _conv_check(x, weight, bias, conv_act)
     B, T, _ = x.shape
     N = _sequences(x, cu_seqlens)
-    _here(x, weight, dy, bias, initial, cu_seqlens, dfinal, workspace)
+    dev = _here(x, weight, dy, bias, initial, cu_seqlens, dfinal, workspace)
     _like(x, initial)
     _like(dy, dfinal)
     _shape("dy", dy, (B, T, C))
     _shape("initial", initial, (N, W - 1, C))
     _shape("dfinal", dfinal, (N, W - 1, C))
-    dev = x.device
-    out = {"dx": torch.empty((B, T, C), dtype=dy.dtype, device=dev),
-           "dweight": torch.empty((C, W), dtype=torch.float32, device=dev),
-           "dbias": torch.empty(C, dtype=torch.float32, device=dev) if bias is not None else None,
-           "dinitial": torch.empty((N, W - 1, C), dtype=dy.dtype, device=dev) if initial is not None else None}
-    ws, ws_bytes = _workspace(int(lib.kda_short_conv_bwd_workspace_size(B, T, C, W)), dev, workspace)
+    on = x.device
+    out = {"dx": torch.empty((B, T, C), dtype=dy.dtype, device=on),
+           "dweight": torch.empty((C, W), dtype=torch.float32, device=on),
+           "dbias": torch.empty(C, dtype=torch.float32, device=on) if bias is not None else None,
+           "dinitial": torch.empty((N, W - 1, C), dtype=dy.dtype, device=on) if initial is not None else None}
+    ws, ws_bytes = _workspace(int(lib.kda_short_conv_bwd_workspace_size(B, T, C, W)), on, workspace)
     px, ldx = _rows("x", x, 2)
-    st = lib.kda_short_conv_bwd(px, ldx, _ptr(weight), _ptr(bias), conv_act, _dt(x), _ptr(initial), _ptr(cu_seqlens),
-                                B, T, C, W, N, _ptr(dy), _ptr(dfinal), _dt(dy), _ptr(out["dx"]), _ptr(out["dweight"]),
-                                _ptr(out["dbias"]), _ptr(out["dinitial"]), _ptr(ws), ws_bytes, _stream(dev))
+    st = lib.kda_short_conv_bwd(px, ldx, _at(weight), _at(bias), conv_act, _dt(x), _at(initial), _at(cu_seqlens),
+                                B, T, C, W, N, _at(dy), _at(dfinal), _dt(dy), _at(out["dx"]), _at(out["dweight"]),
+                                _at(out["dbias"]), _at(out["dinitial"]), _at(ws), ws_bytes, _stream_of(dev))
     _check("kda_short_conv_bwd", st)
     return out
 
@@ -590,10 +620,10 @@ def short_conv_step(x, history, weight, bias=None, conv_act: int = 0, slots=None
     """One token of each of N sequences: x [N,C]; ``history`` [P,W-1,C] is updated in place
     (row i's page is ``slots[i]``, or i without slots; -1 is a padded row).  Returns y
     [N,C].  ``slots``/``status`` as for :func:`recurrent_step`."""
-    lib = load_library()
+    lib = _lib_now()
     C, W = _conv_check(x, weight, bias, conv_act)
     N = x.shape[0]
-    _here(x, history, weight, bias, slots, y, status)
+    dev = _here(x, history, weight, bias, slots, y, status)
     _like(x, history, y)
     _int32(slots, status)
     _shape("history", history, (history.shape[0], W - 1, C))
@@ -602,8 +632,8 @@ def short_conv_step(x, history, weight, bias=None, conv_act: int = 0, slots=None
     if y is None:
         y = torch.empty((N, C), dtype=x.dtype, device=x.device)
     px, ldx = _rows("x", x, 1)
-    st = lib.kda_short_conv_step(px, ldx, _ptr(weight), _ptr(bias), conv_act, _dt(x), _ptr(history), _ptr(slots),
-                                 history.shape[0], N, C, W, _ptr(y), _ptr(status), _stream(x.device))
+    st = lib.kda_short_conv_step(px, ldx, _at(weight), _at(bias), conv_act, _dt(x), _at(history), _at(slots),
+                                 history.shape[0], N, C, W, _at(y), _at(status), _stream_of(dev))
     _check("kda_short_conv_step", st)
     return y
 
@@ -634,10 +664,10 @@ def ssm_step(u, delta, A, Bm, Cm, state, D=None, z=None, delta_bias=None, softpl
     u, delta, z: [N,C]; A: [C,S] fp32, S in 8, 16, 32, 64; Bm, Cm: [N,G,S], channel c in
     group c // (C // G); D, delta_bias: [C] fp32; ``state`` fp32 [P,C,S] is updated in place.
     Returns y [N,C].  ``slots``/``status`` as for :func:`recurrent_step`."""
-    lib = load_library()
+    lib = _lib_now()
     C, G, S = _ssm_check(u, delta, A, Bm, Cm, D, z, delta_bias)
     N = u.shape[0]
-    _here(u, delta, A, Bm, Cm, state, D, z, delta_bias, slots, y, status)
+    dev = _here(u, delta, A, Bm, Cm, state, D, z, delta_bias, slots, y, status)
     _like(u, y)
     _f32(state)
     _int32(slots, status)
@@ -648,9 +678,9 @@ def ssm_step(u, delta, A, Bm, Cm, state, D=None, z=None, delta_bias=None, softpl
         y = torch.empty((N, C), dtype=u.dtype, device=u.device)
     (pu, ldu), (pd, ldd), (pz, ldz) = _rows("u", u, 1), _rows("delta", delta, 1), _rows("z", z, 1)
     (pb, ldb), (pc, ldc) = _rows("Bm", Bm, 1), _rows("Cm", Cm, 1)
-    st = lib.kda_ssm_step(pu, ldu, pd, ldd, _ptr(A), pb, ldb, pc, ldc, _ptr(D), pz, ldz, _ptr(delta_bias), int(softplus),
-                          _dt(u), _ptr(state), _ptr(slots), state.shape[0], N, C, G, S, _ptr(y), _ptr(status),
-                          _stream(u.device))
+    st = lib.kda_ssm_step(pu, ldu, pd, ldd, _at(A), pb, ldb, pc, ldc, _at(D), pz, ldz, _at(delta_bias), int(softplus),
+                          _dt(u), _at(state), _at(slots), state.shape[0], N, C, G, S, _at(y), _at(status),
+                          _stream_of(dev))
     _check("kda_ssm_step", st)
     return y
 
@@ -658,7 +688,7 @@ def ssm_step(u, delta, A, Bm, Cm, state, D=None, z=None, delta_bias=None, softpl
 def _ssm_pointers(u, delta, A, Bm, Cm, D, z, delta_bias, softplus):
     (pu, ldu), (pd, ldd), (pz, ldz) = _rows("u", u, 2), _rows("delta", delta, 2), _rows("z", z, 2)
     (pb, ldb), (pc, ldc) = _rows("Bm", Bm, 2), _rows("Cm", Cm, 2)
-    return pu, ldu, pd, ldd, _ptr(A), pb, ldb, pc, ldc, _ptr(D), pz, ldz, _ptr(delta_bias), int(softplus), _dt(u)
+    return pu, ldu, pd, ldd, _at(A), pb, ldb, pc, ldc, _at(D), pz, ldz, _at(delta_bias), int(softplus), _dt(u)
 
 
 def ssm_scan_fwd(u, delta, A, Bm, Cm, D=None, z=None, delta_bias=None, softplus: bool = True, initial_state=None,
@@ -670,11 +700,11 @@ def ssm_scan_fwd(u, delta, A, Bm, Cm, D=None, z=None, delta_bias=None, softplus:
     fp32 [N,C,S] (None: zeros); ``cu_seqlens`` as for :func:`chunk_fwd`.  Returns (y
     [B,T,C], final_state [N,C,S] fp32 or None).  Rows that belong to no sequence are left
     as they are."""
-    lib = load_library()
+    lib = _lib_now()
     C, G, S = _ssm_check(u, delta, A, Bm, Cm, D, z, delta_bias)
     B, T, _ = u.shape
     N = _sequences(u, cu_seqlens)
-    _here(u, delta, A, Bm, Cm, D, z, delta_bias, initial_state, cu_seqlens, y, final_state, workspace)
+    dev = _here(u, delta, A, Bm, Cm, D, z, delta_bias, initial_state, cu_seqlens, y, final_state, workspace)
     _like(u, y)
     _f32(initial_state, final_state)
     _shape("initial_state", initial_state, (N, C, S))
@@ -686,9 +716,9 @@ def ssm_scan_fwd(u, delta, A, Bm, Cm, D=None, z=None, delta_bias=None, softplus:
         final_state = torch.empty((N, C, S), dtype=torch.float32, device=u.device)
     ws, ws_bytes = _workspace(int(lib.kda_ssm_scan_fwd_workspace_size(B, T, C, G, S, N, int(cu_seqlens is not None))),
                               u.device, workspace)
-    st = lib.kda_ssm_scan_fwd(*_ssm_pointers(u, delta, A, Bm, Cm, D, z, delta_bias, softplus), _ptr(initial_state),
-                              _ptr(cu_seqlens), B, T, C, G, S, N, _ptr(y), _ptr(final_state), _ptr(ws), ws_bytes,
-                              _stream(u.device))
+    st = lib.kda_ssm_scan_fwd(*_ssm_pointers(u, delta, A, Bm, Cm, D, z, delta_bias, softplus), _at(initial_state),
+                              _at(cu_seqlens), B, T, C, G, S, N, _at(y), _at(final_state), _at(ws), ws_bytes,
+                              _stream_of(dev))
     _check("kda_ssm_scan_fwd", st)
     return y, final_state
 
@@ -699,11 +729,11 @@ def ssm_scan_bwd(u, delta, A, Bm, Cm, dy, D=None, z=None, delta_bias=None, softp
     arguments).  dy [B,T,C] is of u's type or fp32.  Returns a dict: du, ddelta, dz [B,T,C]
     and dB, dC [B,T,G,S] in dy's type, dA [C,S], dD, ddelta_bias [C] and dinitial_state
     [N,C,S] fp32; the gradient of an argument that was not given is None."""
-    lib = load_library()
+    lib = _lib_now()
     C, G, S = _ssm_check(u, delta, A, Bm, Cm, D, z, delta_bias)
     B, T, _ = u.shape
     N = _sequences(u, cu_seqlens)
-    _here(u, delta, A, Bm, Cm, dy, D, z, delta_bias, initial_state, cu_seqlens, dfinal_state, workspace)
+    dev = _here(u, delta, A, Bm, Cm, dy, D, z, delta_bias, initial_state, cu_seqlens, dfinal_state, workspace)
     _f32(initial_state, dfinal_state)
     _shape("dy", dy, (B, T, C))
     _shape("initial_state", initial_state, (N, C, S))
@@ -716,11 +746,11 @@ def ssm_scan_bwd(u, delta, A, Bm, Cm, dy, D=None, z=None, delta_bias=None, softp
            "dinitial_state": new(initial_state, (N, C, S), f32)}
     ws, ws_bytes = _workspace(int(lib.kda_ssm_scan_bwd_workspace_size(B, T, C, G, S, N, int(cu_seqlens is not None))),
                               u.device, workspace)
-    st = lib.kda_ssm_scan_bwd(*_ssm_pointers(u, delta, A, Bm, Cm, D, z, delta_bias, softplus), _ptr(initial_state),
-                              _ptr(cu_seqlens), B, T, C, G, S, N, _ptr(dy), _ptr(dfinal_state), _dt(dy),
-                              *(_ptr(out[k]) for k in ("du", "ddelta", "dA", "dB", "dC", "dD", "dz", "ddelta_bias",
+    st = lib.kda_ssm_scan_bwd(*_ssm_pointers(u, delta, A, Bm, Cm, D, z, delta_bias, softplus), _at(initial_state),
+                              _at(cu_seqlens), B, T, C, G, S, N, _at(dy), _at(dfinal_state), _dt(dy),
+                              *(_at(out[k]) for k in ("du", "ddelta", "dA", "dB", "dC", "dD", "dz", "ddelta_bias",
                                                        "dinitial_state")),
-                              _ptr(ws), ws_bytes, _stream(u.device))
+                              _at(ws), ws_bytes, _stream_of(dev))
     _check("kda_ssm_scan_bwd", st)
     return out
 
@@ -730,25 +760,24 @@ def pages_alloc(refs, n: int, pages=None, status=None):
     no more; ``refs`` [P] (references of each page, 0: free) is updated.  ``status`` of
     every pages call: an optional device int32 word, 5 = KDA_ERR_RANGE when a request
     was refused (a refused request changes nothing)."""
-    lib = load_library()
-    _here(refs, pages, status)
+    lib = _lib_now()
+    dev = _here(refs, pages, status)
     _int32(refs, pages, status)
     _shape("pages", pages, (n,))
     if pages is None:
         pages = torch.empty(n, dtype=torch.int32, device=refs.device)
-    _check("kda_pages_alloc", lib.kda_pages_alloc(_ptr(refs), refs.numel(), n, _ptr(pages), _ptr(status),
-                                                  _stream(refs.device)))
+    _check("kda_pages_alloc", lib.kda_pages_alloc(_at(refs), refs.numel(), n, _at(pages), _at(status), _stream_of(dev)))
     return pages
 
 
 def pages_free(refs, pages, status=None):
     """Give back one reference of each page listed in ``pages`` (int32, any shape; -1 entries
     are skipped)."""
-    lib = load_library()
-    _here(refs, pages, status)
+    lib = _lib_now()
+    dev = _here(refs, pages, status)
     _int32(refs, pages, status)
-    _check("kda_pages_free", lib.kda_pages_free(_ptr(refs), refs.numel(), _ptr(pages), pages.numel(), _ptr(status),
-                                                _stream(refs.device)))
+    _check("kda_pages_free", lib.kda_pages_free(_at(refs), refs.numel(), _at(pages), pages.numel(), _at(status),
+                                                _stream_of(dev)))
 
 
 def pages_fork(tables, lens, refs, parents, children, page_tokens: int, status=None):
@@ -757,16 +786,16 @@ def pages_fork(tables, lens, refs, parents, children, page_tokens: int, status=N
     [S,width] (-1 behind a sequence's pages); lens: int32 [S] tokens.  Returns (src, dst),
     int32 [n]: the copies to make in every pool with :func:`pages_copy` (-1: none).  Free
     the child's former pages first."""
-    lib = load_library()
+    lib = _lib_now()
     n = parents.numel()
     S, width = tables.shape
-    _here(tables, lens, refs, parents, children, status)
+    dev = _here(tables, lens, refs, parents, children, status)
     _int32(tables, lens, refs, parents, children, status)
     _shape("lens", lens, (S,))
     _shape("children", children, parents.shape)
     src, dst = torch.empty((2, n), dtype=torch.int32, device=refs.device)
-    st = lib.kda_pages_fork(_ptr(tables), _ptr(lens), S, width, int(page_tokens), _ptr(refs), refs.numel(), _ptr(parents),
-                            _ptr(children), n, _ptr(src), _ptr(dst), _ptr(status), _stream(refs.device))
+    st = lib.kda_pages_fork(_at(tables), _at(lens), S, width, int(page_tokens), _at(refs), refs.numel(), _at(parents),
+                            _at(children), n, _at(src), _at(dst), _at(status), _stream_of(dev))
     _check("kda_pages_fork", st)
     return src, dst
 
@@ -775,14 +804,14 @@ def pages_compact(refs, tables=None, workspace=None, status=None):
     """Close up the pools: used pages behind the number of used pages move into the free
     places before it, in order; ``refs`` and the table entries follow.  Returns (src, dst),
     int32 [P // 2]: the copies to make in every pool with :func:`pages_copy` (-1: none)."""
-    lib = load_library()
-    _here(refs, tables, workspace, status)
+    lib = _lib_now()
+    dev = _here(refs, tables, workspace, status)
     _int32(refs, tables, status)
     P = refs.numel()
     src, dst = torch.empty((2, P // 2), dtype=torch.int32, device=refs.device)
     ws, ws_bytes = _workspace(int(lib.kda_pages_compact_workspace_size(P)), refs.device, workspace)
-    st = lib.kda_pages_compact(_ptr(refs), P, _ptr(tables), 0 if tables is None else tables.numel(), _ptr(src), _ptr(dst),
-                               _ptr(ws), ws_bytes, _ptr(status), _stream(refs.device))
+    st = lib.kda_pages_compact(_at(refs), P, _at(tables), 0 if tables is None else tables.numel(), _at(src), _at(dst),
+                               _at(ws), ws_bytes, _at(status), _stream_of(dev))
     _check("kda_pages_compact", st)
     return src, dst
 
@@ -791,13 +820,13 @@ def pages_copy(pool, src, dst, workspace=None, status=None):
     """Copy page ``src[i]`` of ``pool`` ([P, ...], any type, a page's bytes a multiple of 16)
     onto page ``dst[i]``; -1 entries are skipped.  A destination that a later pair writes or
     another pair reads is refused."""
-    lib = load_library()
-    _here(pool, src, dst, workspace, status)
+    lib = _lib_now()
+    dev = _here(pool, src, dst, workspace, status)
     _int32(src, dst, status)
     _shape("dst", dst, src.shape)
     P, n = pool.shape[0], src.numel()
     page_bytes = pool.numel() // P * pool.element_size() if P else 16
     ws, ws_bytes = _workspace(int(lib.kda_pages_copy_workspace_size(P, n)), pool.device, workspace)
-    st = lib.kda_pages_copy(_ptr(pool), P, page_bytes, _ptr(src), _ptr(dst), n, _ptr(ws), ws_bytes, _ptr(status),
-                            _stream(pool.device))
+    st = lib.kda_pages_copy(_at(pool), P, page_bytes, _at(src), _at(dst), n, _at(ws), ws_bytes, _at(status),
+                            _stream_of(dev))
     _check("kda_pages_copy", st)

@@ -2,7 +2,7 @@
 
 Tolerances, element by element.  p is W + 1 fp32 operations, so it is off by at most (W + 1) 2^-24 M with M
 the sum of the magnitudes it adds; SiLU's slope is below 1.1, and sigmoid(p) itself is off by 2^-22
-(the exponential) + |p| log2(e) 2^-24 (its rounded argument, weighted by 1 - sigmoid) + 2^-24, relative:
+(the exponential) + |p| log2(e) 2^-24 (its rounded argument, weighted by 1 - sigmoid) + 2^-23, relative:
 together below 2^-20 M.  Gradients: dp has two such factors of dy, below 2^-19 |dy| (1 + M), and dx is
 a sum of W of them; dw and dbias are sums over tokens in fp32, off by at most T 2^-24 of the sum of
 magnitudes in whatever order they are added.  Rounding to the output type adds half a step."""
