@@ -562,7 +562,7 @@ KDA_API kda_status kda_short_conv_step(const void *x, int64_t ldx, const float *
  *  [N, G, S] (rows ldb, ldc apart), y [N, C]: element type dtype.
  *  A fp32 [C][S] (16-byte aligned), D, delta_bias fp32 [C] or NULL.
  *  softplus 0 or 1.
- *  state  fp32 pool [P, C, S], 16-byte aligned, updated in place; slots, P, status as
+ *  state  fp32 pool [P, C, S], 32-byte aligned, updated in place; slots, P, status as
  *         kda_short_conv_step.
  * S in {8, 16, 32, 64}; C a multiple of G, C <= 2^20.
  */

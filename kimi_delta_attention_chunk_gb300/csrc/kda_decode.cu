@@ -41,12 +41,12 @@ decode_step_kernel(const TIn* __restrict__ q, const TIn* __restrict__ k,
     const int c4 = tid % LPR;
     const int rg = tid / LPR;
 
-    int row = 0, page = 0;
+    int row = 0, page[1] = {0};
     int64_t at = nh;
     if constexpr (kSlots) {
         row = (int)(nh / H);
-        page = page_of_row(slots, row, P);
-        at = (int64_t)max(page, 0) * H + nh % H;
+        page[0] = page_of_row(slots, row, P);
+        at = (int64_t)max(page[0], 0) * H + nh % H;
     }
     float4* S = reinterpret_cast<float4*>(state + at * K * V);
     float4 s[RPT];
@@ -54,7 +54,7 @@ decode_step_kernel(const TIn* __restrict__ q, const TIn* __restrict__ k,
 #pragma unroll
     for (int i = 0; i < RPT; ++i) s[i] = __ldcs(&S[(rg + i * RG) * LPR + c4]);
     if constexpr (kSlots)
-        if (row_refused(slots, row, page, status)) return;
+        if (rows_refused<1>(slots, row, row + 1, page, status)) return;
 
     __shared__ float eg[K], kk[K], qq[K];
     __shared__ __align__(16) float red_a[RG][V];

@@ -198,7 +198,7 @@ kda_status kda_ssm_step(const void* u, int64_t ldu, const void* delta, int64_t l
     const size_t es = size_of(dtype);
     for (const void* p : {u, delta, Bm, Cm, z, (const void*)y})
         if (!aligned(p, es)) return KDA_ERR_INVALID_ARG;
-    if (!kda_host::aligned16(A) || !kda_host::aligned16(state)) return KDA_ERR_INVALID_ARG;
+    if (!kda_host::aligned16(A) || !aligned(state, 32)) return KDA_ERR_INVALID_ARG;
     if (!aligned(D, 4) || !aligned(delta_bias, 4) || !aligned(slots, 4) || !aligned(status, 4)) return KDA_ERR_INVALID_ARG;
     const Span in[] = {rows(u, N, ldu, C, es), rows(delta, N, ldd, C, es), rows(z, N, ldz, C, es), rows(Bm, N, ldb, vec, es),
                        rows(Cm, N, ldc, vec, es), {A, (size_t)C * S * 4}, {D, (size_t)C * 4}, {delta_bias, (size_t)C * 4},

@@ -50,11 +50,13 @@ struct SeqMap {
 // The sequences of tokens [t0, t0 + TT): start[i] / end[i] is the sequence that token t0 + i
 // is the first / last of, or -1.  carry: the sequence that token t0 continues (-1: none), which
 // began at carry_start.  Behind the tile the sequence at hand runs on to token `until`: a tile
-// that ends before it has no boundary and needs no look.
+// that ends before it has no boundary and needs no look.  plain: one sequence runs through the tile
+// and on.
 template <int TT>
 struct TokenTile {
     int start[TT], end[TT];
     int carry, carry_start, n0, until;
+    bool plain;
 
     // Every thread of the block calls it; the block has to be past its last use of the tile.
     template <int NTH>
@@ -68,6 +70,7 @@ struct TokenTile {
                 carry = -1;
                 carry_start = t0;
                 until = n1 > 0 ? m.end(n1 - 1) : t0;
+                plain = n > 0 && n1 == n && until > t0 + TT;
             }
         }
         __syncthreads();

@@ -23,11 +23,15 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kSms = 152;
-constexpr int kResident = 4;  // blocks of an SM that the kernels below are built for
+// Blocks of an SM that the kernels are built for.  Five forwards (70k x 12288 in 565 us, 600 with four);
+// backwards the registers of a fifth would spill (4096 x 12288 in 82 us against 70).
+constexpr int kFwdResident = 5, kBwdResident = 4;
 constexpr int kTile = 64;     // tokens of one look at the sequence boundaries
-constexpr int kStages = 3;    // asynchronous groups of a thread: one in use, two on their way
+// Asynchronous groups of a thread: one in use, one on its way.  (Three groups of eight rows measured 17%
+// slower backwards, two of four and two of sixteen as well.)
+constexpr int kStages = 2;
 
-// Rows of one group: 48 KB of shared memory a block at most, four blocks an SM.
+// Rows of one group: 33 KB of shared memory a block.
 constexpr int batch_of(int bytes) { return bytes <= 16 ? 8 : 4; }
 
 template <typename T, int VEC>
@@ -80,16 +84,29 @@ __device__ __forceinline__ void store_history(T* hist, int64_t n, int C, int c0,
     }
 }
 
+// The taps and biases of VEC channels, which lie side by side; 16-byte pieces for VEC > 1.
 template <int VEC, int W>
 __device__ __forceinline__ void load_taps(const float* weight, const float* bias, int c0, f2 (&w)[W][(VEC + 1) / 2],
                                           f2 (&b)[(VEC + 1) / 2]) {
+    if constexpr (VEC == 1) {
 #pragma unroll
-    for (int i = 0; i < (VEC + 1) / 2; ++i) {
-        const bool two = 2 * i + 1 < VEC;
-        const float* at = weight + (int64_t)(c0 + 2 * i) * W;
+        for (int j = 0; j < W; ++j) w[j][0] = pack(__ldg(weight + (int64_t)c0 * W + j), 0.f);
+        b[0] = bias ? pack(__ldg(bias + c0), 0.f) : 0ull;
+    } else {
+        float raw[VEC * W], rb[VEC] = {};
+        const float4* at = reinterpret_cast<const float4*>(weight + (int64_t)c0 * W);
+        auto put = [](float* to, float4 x) { to[0] = x.x; to[1] = x.y; to[2] = x.z; to[3] = x.w; };
 #pragma unroll
-        for (int j = 0; j < W; ++j) w[j][i] = pack(__ldg(at + j), two ? __ldg(at + W + j) : 0.f);
-        b[i] = bias ? pack(__ldg(bias + c0 + 2 * i), two ? __ldg(bias + c0 + 2 * i + 1) : 0.f) : 0ull;
+        for (int i = 0; i < VEC * W / 4; ++i) put(raw + 4 * i, __ldg(at + i));
+        if (bias)
+#pragma unroll
+            for (int i = 0; i < VEC / 4; ++i) put(rb + 4 * i, __ldg(reinterpret_cast<const float4*>(bias + c0) + i));
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) {
+#pragma unroll
+            for (int j = 0; j < W; ++j) w[j][i] = pack(raw[2 * i * W + j], raw[(2 * i + 1) * W + j]);
+            b[i] = pack(rb[2 * i], rb[2 * i + 1]);
+        }
     }
 }
 
@@ -115,7 +132,7 @@ __device__ __forceinline__ void shift(f2 (&win)[R][N2], const f2 (&v)[N2]) {
 }
 
 template <typename T, int VEC, int W>
-__global__ void __launch_bounds__(kThreads, kResident) conv_fwd_kernel(ConvParams p, SeqMap m, int run) {
+__global__ void __launch_bounds__(kThreads, kFwdResident) conv_fwd_kernel(ConvParams p, SeqMap m, int run) {
     typedef Row<T, VEC> R;
     constexpr int N2 = R::N2;
     typedef FwdShared<T, VEC> Sh;
@@ -134,9 +151,13 @@ __global__ void __launch_bounds__(kThreads, kResident) conv_fwd_kernel(ConvParam
     const int r0 = blockIdx.y * run, r1 = min(m.total, r0 + run);
     auto request = [&](int t) {
         if (t < r1) {
+            const int s = (t - r0) / kBatch % kStages, more = r1 - 1 - t;
+            const T* from = x + t * p.ldx;
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i)
-                R::copy_async(&ring[(t - r0) / kBatch % kStages][i][tid], x + (int64_t)min(t + i, r1 - 1) * p.ldx);
+            for (int i = 0; i < kBatch; ++i) {
+                R::copy_async(&ring[s][i][tid], from);
+                if (i < more) from += p.ldx;  // the last row again behind the run
+            }
         }
         copies_commit();
     };
@@ -179,8 +200,9 @@ __global__ void __launch_bounds__(kThreads, kResident) conv_fwd_kernel(ConvParam
             plain = t > r0 && t + kTile < until && t >= first;
             if (!plain) {
                 __syncthreads();
-                tile.build<kThreads>(m, t);
+                tile.template build<kThreads>(m, t);
                 until = tile.until;
+                plain = tile.plain && t >= first;
                 if (t == r0 && tile.carry >= 0 && on)
                     load_window<T, VEC, W>(x - c0, p.ldx, hist, tile.carry, tile.carry_start, t, p.C, c0, win);
             }
@@ -216,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, kResident) conv_fwd_kernel(ConvParam
 // Backward over tokens [r0, r1) of a run and the W - 1 behind it, whose dp the run's last inputs
 // need.  acc[k] is the unfinished gradient of line entry t - (W - 1) + k.
 template <typename T, typename TG, int VEC, int W>
-__global__ void __launch_bounds__(kThreads, kResident) conv_bwd_kernel(ConvParams p, SeqMap m, int run) {
+__global__ void __launch_bounds__(kThreads, kBwdResident) conv_bwd_kernel(ConvParams p, SeqMap m, int run) {
     typedef Row<T, VEC> R;
     typedef Row<TG, VEC> RG;
     constexpr int N2 = R::N2;
@@ -239,12 +261,17 @@ __global__ void __launch_bounds__(kThreads, kResident) conv_bwd_kernel(ConvParam
     const int r0 = blockIdx.y * run, r1 = min(m.total, r0 + run), stop = min(m.total, r1 + W - 1);
     auto request = [&](int t) {
         if (t < stop) {
+            const int s = (t - r0) / kBatch % kStages, more = stop - 1 - t;
+            const T* from = x + t * p.ldx;
+            const TG* gfrom = dy + (int64_t)t * p.C;
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
-                const int64_t at = min(t + i, stop - 1);
-                const int s = (t - r0) / kBatch % kStages;
-                R::copy_async(&ring[s][i][tid], x + at * p.ldx);
-                RG::copy_async(&gring[s][i][tid], dy + at * p.C);
+                R::copy_async(&ring[s][i][tid], from);
+                RG::copy_async(&gring[s][i][tid], gfrom);
+                if (i < more) {  // the last row again behind the tokens
+                    from += p.ldx;
+                    gfrom += p.C;
+                }
             }
         }
         copies_commit();
@@ -317,8 +344,9 @@ __global__ void __launch_bounds__(kThreads, kResident) conv_bwd_kernel(ConvParam
             plain = t > r0 && t + kTile < until && t >= first;
             if (!plain) {
                 __syncthreads();
-                tile.build<kThreads>(m, t);
+                tile.template build<kThreads>(m, t);
                 until = tile.until;
+                plain = tile.plain && t >= first;
                 if (t == r0 && tile.carry >= 0 && on) {
                     seq = tile.carry;
                     begin = tile.carry_start;
@@ -414,7 +442,7 @@ __global__ void __launch_bounds__(128) conv_bwd_sum_kernel(const float* partial,
     const int64_t i = (int64_t)blockIdx.x * 128 + threadIdx.x, n = (int64_t)C * (W + 1);
     if (i >= n) return;
     float a = 0.f;
-#pragma unroll 8
+#pragma unroll 16
     for (int r = 0; r < runs; ++r) a += partial[r * n + i];
     const int64_t c = i % C;
     const int j = (int)(i / C);
@@ -444,10 +472,10 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(ConvStepParams p) {
     }
     f2 w[W][N2], b[N2];
     if (on) load_taps<VEC, W>(p.weight, p.bias, c0, w, b);
+    const unsigned refused = rows_refused<kRows>(p.slots, row0, p.N, page, p.status);
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-        if (row0 + i >= p.N) break;
-        if (row_refused(p.slots, row0 + i, page[i], p.status) || !on) continue;
+        if (row0 + i >= p.N || (refused >> i & 1) || !on) continue;
         f2 win[W - 1][N2], v[N2], o[N2];
         in[i].to(v);
 #pragma unroll
@@ -468,9 +496,9 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(ConvStepParams p) {
 
 // Tokens of one run: as many runs as one filling of the machine holds, at least 32 tokens each so
 // that the W - 1 rows read twice stay below a tenth.
-int run_tokens(int total, int C, int vec) {
+int run_tokens(int total, int C, int vec, int resident) {
     const int blocks = (C + kThreads * vec - 1) / (kThreads * vec);
-    const int runs = kSms * kResident / blocks > 0 ? kSms * kResident / blocks : 1;
+    const int runs = kSms * resident / blocks > 0 ? kSms * resident / blocks : 1;
     int run = (total + runs - 1) / runs;
     run = (run + 7) / 8 * 8;
     return run < 32 ? 32 : run;
@@ -480,10 +508,10 @@ int run_count(int total, int run) { return total > 0 ? (total + run - 1) / run :
 SeqMap seq_map(const ConvParams& p) { return SeqMap{p.cu, p.N, p.T, p.total}; }
 
 template <typename K>
-cudaError_t launch_runs(K kern, const ConvParams& p, int vec, int smem, cudaStream_t st) {
+cudaError_t launch_runs(K kern, const ConvParams& p, int vec, int resident, int smem, cudaStream_t st) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    const int run = run_tokens(p.total, p.C, vec);
+    const int run = run_tokens(p.total, p.C, vec, resident);
     const dim3 grid((p.C + kThreads * vec - 1) / (kThreads * vec), run_count(p.total, run));
     kern<<<grid, kThreads, smem, st>>>(p, seq_map(p), run);
     return cudaGetLastError();
@@ -492,19 +520,19 @@ cudaError_t launch_runs(K kern, const ConvParams& p, int vec, int smem, cudaStre
 template <typename T, int VEC>
 cudaError_t launch_fwd(const ConvParams& p, cudaStream_t st) {
     constexpr int smem = sizeof(FwdShared<T, VEC>);
-    if (p.W == 4) return launch_runs(conv_fwd_kernel<T, VEC, 4>, p, VEC, smem, st);
-    if (p.W == 3) return launch_runs(conv_fwd_kernel<T, VEC, 3>, p, VEC, smem, st);
-    return launch_runs(conv_fwd_kernel<T, VEC, 2>, p, VEC, smem, st);
+    if (p.W == 4) return launch_runs(conv_fwd_kernel<T, VEC, 4>, p, VEC, kFwdResident, smem, st);
+    if (p.W == 3) return launch_runs(conv_fwd_kernel<T, VEC, 3>, p, VEC, kFwdResident, smem, st);
+    return launch_runs(conv_fwd_kernel<T, VEC, 2>, p, VEC, kFwdResident, smem, st);
 }
 
 template <typename T, typename TG, int VEC>
 cudaError_t launch_bwd(const ConvParams& p, cudaStream_t st) {
     constexpr int smem = sizeof(BwdShared<T, TG, VEC>);
-    cudaError_t e = p.W == 4   ? launch_runs(conv_bwd_kernel<T, TG, VEC, 4>, p, VEC, smem, st)
-                    : p.W == 3 ? launch_runs(conv_bwd_kernel<T, TG, VEC, 3>, p, VEC, smem, st)
-                               : launch_runs(conv_bwd_kernel<T, TG, VEC, 2>, p, VEC, smem, st);
+    cudaError_t e = p.W == 4   ? launch_runs(conv_bwd_kernel<T, TG, VEC, 4>, p, VEC, kBwdResident, smem, st)
+                    : p.W == 3 ? launch_runs(conv_bwd_kernel<T, TG, VEC, 3>, p, VEC, kBwdResident, smem, st)
+                               : launch_runs(conv_bwd_kernel<T, TG, VEC, 2>, p, VEC, kBwdResident, smem, st);
     if (e != cudaSuccess) return e;
-    const int runs = run_count(p.total, run_tokens(p.total, p.C, VEC));
+    const int runs = run_count(p.total, run_tokens(p.total, p.C, VEC, kBwdResident));
     const int64_t n = (int64_t)p.C * (p.W + 1);
     conv_bwd_sum_kernel<<<(unsigned)((n + 127) / 128), 128, 0, st>>>(p.partial, runs, p.C, p.W, p.dweight, p.dbias);
     return cudaGetLastError();
@@ -533,7 +561,7 @@ constexpr int kBwdVec = 4;
 cudaError_t short_conv_fwd(kda_dtype dt, const ConvParams& p, cudaStream_t st) {
     using kda_host::rows_aligned;
     const int vec = dt == KDA_BF16 ? 8 : 4;
-    const bool wide = rows_aligned(p.x, p.ldx, vec) && rows_aligned(p.y, p.C, vec) && rows_aligned(p.initial, p.C, vec) &&
+    const bool wide = rows_aligned(p.x, p.ldx, vec) && rows_aligned(p.weight, 0, 4) && rows_aligned(p.bias, 0, 4) && rows_aligned(p.y, p.C, vec) && rows_aligned(p.initial, p.C, vec) &&
                       rows_aligned(p.final_hist, p.C, vec) && p.C % vec == 0;
     if (dt == KDA_BF16) return wide ? launch_fwd<__nv_bfloat16, 8>(p, st) : launch_fwd<__nv_bfloat16, 1>(p, st);
     return wide ? launch_fwd<float, 4>(p, st) : launch_fwd<float, 1>(p, st);
@@ -541,13 +569,13 @@ cudaError_t short_conv_fwd(kda_dtype dt, const ConvParams& p, cudaStream_t st) {
 
 size_t short_conv_bwd_partial(int total, int C, int W) {
     // the narrow variant has the fewer runs: more blocks along the channels
-    return (size_t)run_count(total, run_tokens(total, C, kBwdVec)) * C * (W + 1);
+    return (size_t)run_count(total, run_tokens(total, C, kBwdVec, kBwdResident)) * C * (W + 1);
 }
 
 cudaError_t short_conv_bwd(kda_dtype dt, kda_dtype gdt, const ConvParams& p, cudaStream_t st) {
     using kda_host::rows_aligned;
     const void* rows[] = {p.initial, p.dy, p.dfinal, p.dx, p.dinitial};
-    bool wide = rows_aligned(p.x, p.ldx, kBwdVec) && p.C % kBwdVec == 0;
+    bool wide = rows_aligned(p.x, p.ldx, kBwdVec) && rows_aligned(p.weight, 0, 4) && rows_aligned(p.bias, 0, 4) && p.C % kBwdVec == 0;
     for (const void* r : rows) wide = wide && rows_aligned(r, p.C, kBwdVec);
     if (dt == KDA_F32) return wide ? launch_bwd<float, float, kBwdVec>(p, st) : launch_bwd<float, float, 1>(p, st);
     if (gdt == KDA_F32)
@@ -558,7 +586,7 @@ cudaError_t short_conv_bwd(kda_dtype dt, kda_dtype gdt, const ConvParams& p, cud
 cudaError_t short_conv_step(kda_dtype dt, const ConvStepParams& p, cudaStream_t st) {
     using kda_host::rows_aligned;
     const int vec = dt == KDA_BF16 ? 8 : 4;
-    const bool wide = rows_aligned(p.x, p.ldx, vec) && rows_aligned(p.y, p.C, vec) && rows_aligned(p.history, p.C, vec) &&
+    const bool wide = rows_aligned(p.x, p.ldx, vec) && rows_aligned(p.weight, 0, 4) && rows_aligned(p.bias, 0, 4) && rows_aligned(p.y, p.C, vec) && rows_aligned(p.history, p.C, vec) &&
                       p.C % vec == 0;
     if (dt == KDA_BF16) return wide ? launch_step<__nv_bfloat16, 8>(p, st) : launch_step<__nv_bfloat16, 1>(p, st);
     return wide ? launch_step<float, 4>(p, st) : launch_step<float, 1>(p, st);

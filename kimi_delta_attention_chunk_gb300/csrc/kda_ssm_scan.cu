@@ -141,10 +141,12 @@ __global__ void __launch_bounds__(kThreads, 4) scan_kernel(SsmScanParams p, SeqM
         }
         __syncthreads();
         if (t0 + kTile < r1) request(t0 + kTile);
-        const bool plain = t0 + kTile < until && t0 > r0;
-        if (!plain) {
+        bool plain = t0 + kTile < until && t0 > r0;
+        const bool looked = !plain;
+        if (looked) {
             tile.template build<kThreads>(m, t0);
             until = tile.until;
+            plain = tile.plain;
             if (t0 == r0 && tile.carry >= 0 && kOutputs && split) load_state(runs.state + (int64_t)blockIdx.y * p.C * S + cs);
         }
         const int lo = max(t0, first), hi = min(min(t0 + kTile, r1), last);
@@ -204,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 4) scan_kernel(SsmScanParams p, SeqM
                 }
             }
         }
-        if (!plain) __syncthreads();  // the tile's boundaries may be looked up anew
+        if (looked) __syncthreads();  // the tile's boundaries may be looked up anew
     }
     if (!kOutputs && on) {
         store_state(runs.state + (int64_t)blockIdx.y * p.C * S + cs);

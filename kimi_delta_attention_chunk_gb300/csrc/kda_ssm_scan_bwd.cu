@@ -16,6 +16,8 @@
 // Sums over channels (dB, dC) go through a shuffle reduction that leaves one value a lane, the block's
 // warps, and partial sums of the channel blocks; sums over tokens through partial sums of the chunks.
 // Every sum has an order fixed by the sizes.  The fp32 units and shuffles bound step 3.
+#include <stddef.h>
+
 #include "kda_layer.h"
 #include "kda_ssm.cuh"
 
@@ -86,7 +88,7 @@ __global__ void __launch_bounds__(kSumThreads, 4) scan_bwd_sum_kernel(SsmScanPar
         }
     }
     tile.template build<kSumThreads>(m, t0);
-    const bool plain = tile.carry >= 0 && tile.until > t0 + kChunk && tile.n0 == m.begun_before(t0 + kChunk);
+    const bool plain = tile.plain;
     f2 A2[H2], h[H2], P[H2], G[H2];
 #pragma unroll
     for (int i = 0; i < H2; ++i) {
@@ -229,14 +231,18 @@ struct BwdShape {
 template <int S>
 struct BwdShared {
     using Sh = BwdShape<S>;
-    TokenTile<kChunk> tile;
+    float4 kept[kBatches][Sh::NT];
+    alignas(16) float vec[2][kChunk][S];  // B, C, read four at a time
     float d[kChunk][Sh::CH];    // step sizes, then dd
     float u[kChunk][Sh::CH];    // inputs, then du
     float yb[kChunk][Sh::CH];   // output gradients behind the gate, then sum_s C h
-    float vec[2][kChunk][S];    // B, C
-    float4 kept[kBatches][Sh::NT];
     float red[Sh::NW][kBatch][2 * S];
+    TokenTile<kChunk> tile;
 };
+
+static_assert(offsetof(BwdShared<8>, vec) % 16 == 0 && offsetof(BwdShared<16>, vec) % 16 == 0 &&
+                  offsetof(BwdShared<32>, vec) % 16 == 0 && offsetof(BwdShared<64>, vec) % 16 == 0,
+              "16-byte reads of B and C");
 
 template <typename T, typename TG, int S>
 __global__ void __launch_bounds__(BwdShape<S>::NT, 512 / BwdShape<S>::NT) scan_bwd_kernel(SsmScanParams p, SeqMap m, Scratch w) {
@@ -294,7 +300,7 @@ __global__ void __launch_bounds__(BwdShape<S>::NT, 512 / BwdShape<S>::NT) scan_b
         }
     }
     sh.tile.template build<NT>(m, t0);
-    const bool plain = sh.tile.carry >= 0 && sh.tile.until > t0 + kChunk && sh.tile.n0 == m.begun_before(t0 + kChunk) && hi - lo == kChunk;
+    const bool plain = sh.tile.plain && hi - lo == kChunk;
 
     auto load4 = [&](const float* from, f2 (&v)[2]) {
         const float4 x = *reinterpret_cast<const float4*>(from);

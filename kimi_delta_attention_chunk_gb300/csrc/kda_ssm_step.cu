@@ -3,8 +3,8 @@
 // Per row and channel c (group g(c)), with S states:
 //     d = softplus(delta + bias),  h <- exp(d A[c]) h + d u B[g],  y = (C[g] . h + D u) (z sigmoid(z))
 // The states are read and written once, 8 S bytes a channel against some ten bytes of the rest, so
-// HBM bounds a full batch and latency a small one.  S / 4 lanes own a channel with four states each
-// (one 16-byte load and store) and sum y with shuffles.
+// HBM bounds a full batch and latency a small one.  S / 8 lanes own a channel with eight states each
+// (one 32-byte load and store) and sum y with shuffles.
 #include "kda_layer.h"
 #include "kda_segments.cuh"
 #include "kda_slots.cuh"
@@ -14,20 +14,37 @@ namespace kda {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 
-// Four consecutive elements of a vector, in pairs; `wide`: as one piece.
+// Eight fp32 in pairs, 32 bytes in one access.
+struct Eight {
+    f2 v[4];
+    __device__ __forceinline__ void load(const float* p) {
+        asm volatile("ld.global.L1::no_allocate.v4.b64 {%0, %1, %2, %3}, [%4];" : "=l"(v[0]), "=l"(v[1]), "=l"(v[2]), "=l"(v[3]) : "l"(p) : "memory");
+    }
+    __device__ __forceinline__ void store(float* p) const {
+        asm volatile("st.global.L1::no_allocate.v4.b64 [%0], {%1, %2, %3, %4};" ::"l"(p), "l"(v[0]), "l"(v[1]), "l"(v[2]), "l"(v[3]) : "memory");
+    }
+};
+
+// Eight consecutive elements of a row of B or C; `wide`: by 16-byte pieces.
 template <typename T>
-struct Four {
-    T v[4];
+struct EightOf {
+    uint4 r[sizeof(T) / 2];
     __device__ __forceinline__ void load(const T* p, bool wide) {
         if (wide) {
-            typedef typename Bits<4 * sizeof(T)>::type Raw;
-            *reinterpret_cast<Raw*>(v) = __ldg(reinterpret_cast<const Raw*>(p));
-        } else {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] = __ldg(p + k);
+            for (int i = 0; i < (int)sizeof(T) / 2; ++i) r[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+        } else {
+            T* v = reinterpret_cast<T*>(r);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = __ldg(p + k);
         }
+    }
+    __device__ __forceinline__ f2 pair(int i) const {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(r);
+        if constexpr (sizeof(T) == 2) return pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+        else return pack(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
     }
 };
 
@@ -35,45 +52,53 @@ struct Four {
 // Everything that the rows need is requested before the first is worked on.
 template <typename T, int S, int kRows>
 __global__ void __launch_bounds__(kThreads) ssm_step_kernel(SsmStepParams p, bool wide) {
-    constexpr int LP = S / 4, CH = kThreads / LP;
+    constexpr int LP = S / 8, CH = kThreads / LP;
     const int row0 = blockIdx.x * kRows;
     const int lane = threadIdx.x % LP;
     const int c = blockIdx.y * CH + threadIdx.x / LP;
     const bool on = c < p.C;
-    const int cc = on ? c : 0, g = cc / (p.C / p.G) * S + lane * 4;
+    const int cc = on ? c : 0, g = cc / (p.C / p.G) * S + lane * 8;
+    const int64_t per_page = (int64_t)p.C * S, at = (int64_t)cc * S + lane * 8;
     int page[kRows];
-    float4 h[kRows];
+    Eight h[kRows];
     T u[kRows], dl[kRows], z[kRows];
-    Four<T> Bv[kRows], Cv[kRows];
+    EightOf<T> Bv[kRows], Cv[kRows];
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
         const int row = min(row0 + i, p.N - 1);
         page[i] = page_of_row(p.slots, row, p.P);
-        h[i] = __ldcs(reinterpret_cast<const float4*>(p.state + ((int64_t)max(page[i], 0) * p.C + cc) * S + lane * 4));
+        h[i].load(p.state + max(page[i], 0) * per_page + at);
         u[i] = __ldg(static_cast<const T*>(p.u) + row * p.ldu + cc);
         dl[i] = __ldg(static_cast<const T*>(p.delta) + row * p.ldd + cc);
         if (p.z) z[i] = __ldg(static_cast<const T*>(p.z) + row * p.ldz + cc);
         Bv[i].load(static_cast<const T*>(p.Bm) + row * p.ldb + g, wide);
         Cv[i].load(static_cast<const T*>(p.Cm) + row * p.ldc + g, wide);
     }
-    const float4 A = *reinterpret_cast<const float4*>(p.A + (int64_t)cc * S + lane * 4);
-    const float a[4] = {A.x, A.y, A.z, A.w};
+    f2 A2[4];
+#pragma unroll
+    for (int k = 0; k < 4; k += 2) {
+        const float4 x = __ldg(reinterpret_cast<const float4*>(p.A + at) + k / 2);
+        A2[k] = pack(kLog2e * x.x, kLog2e * x.y);
+        A2[k + 1] = pack(kLog2e * x.z, kLog2e * x.w);
+    }
     const float bias = p.bias ? __ldg(p.bias + cc) : 0.f, D = p.D ? __ldg(p.D + cc) : 0.f;
+    const unsigned refused = rows_refused<kRows>(p.slots, row0, p.N, page, p.status);
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
         const int row = row0 + i;
-        if (row >= p.N) break;
-        if (row_refused(p.slots, row, page[i], p.status)) continue;
+        if (row >= p.N || (refused >> i & 1)) continue;
         float d = to_f32<T>(dl[i]) + bias;
         if (p.softplus) d = softplus(d);
-        const float uv = to_f32<T>(u[i]), du = d * uv, de = d * kLog2e;
-        float v[4] = {h[i].x, h[i].y, h[i].z, h[i].w}, y = 0.f;
+        const float uv = to_f32<T>(u[i]), du = d * uv;
+        const f2 dd = pack(d, d), du2 = pack(du, du);
+        f2 y2 = 0ull;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            v[k] = fmaf(ex2(de * a[k]), v[k], du * to_f32<T>(Bv[i].v[k]));
-            y = fmaf(to_f32<T>(Cv[i].v[k]), v[k], y);
+            h[i].v[k] = fma2(ex2_2(mul2(dd, A2[k])), h[i].v[k], mul2(du2, Bv[i].pair(k)));
+            y2 = fma2(h[i].v[k], Cv[i].pair(k), y2);
         }
-        if (on) __stcs(reinterpret_cast<float4*>(p.state + ((int64_t)page[i] * p.C + c) * S + lane * 4), make_float4(v[0], v[1], v[2], v[3]));
+        if (on) h[i].store(p.state + page[i] * per_page + at);
+        float y = sum2(y2);
 #pragma unroll
         for (int o = LP / 2; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
         if (on && lane == 0) {
@@ -89,13 +114,13 @@ __global__ void __launch_bounds__(kThreads) ssm_step_kernel(SsmStepParams p, boo
 
 template <typename T, int S>
 cudaError_t launch(const SsmStepParams& p, cudaStream_t st) {
-    constexpr int CH = kThreads / (S / 4);
+    constexpr int CH = kThreads / (S / 8);
     const int blocks = (p.C + CH - 1) / CH;
-    const size_t piece = 4 * sizeof(T);
-    const bool wide = (uintptr_t)p.Bm % piece == 0 && (uintptr_t)p.Cm % piece == 0 && p.ldb % 4 == 0 && p.ldc % 4 == 0;
-    // four rows a block once that leaves the machine four blocks an SM, else one
-    if ((int64_t)(p.N + 3) / 4 * blocks >= 4 * 152)
-        ssm_step_kernel<T, S, 4><<<dim3((p.N + 3) / 4, blocks), kThreads, 0, st>>>(p, wide);
+    const int piece = 16 / (int)sizeof(T);
+    const bool wide = kda_host::rows_aligned(p.Bm, p.ldb, piece) && kda_host::rows_aligned(p.Cm, p.ldc, piece);
+    // two rows a block once that leaves the machine four blocks an SM, else one
+    if ((int64_t)(p.N + 1) / 2 * blocks >= 4 * 152)
+        ssm_step_kernel<T, S, 2><<<dim3((p.N + 1) / 2, blocks), kThreads, 0, st>>>(p, wide);
     else
         ssm_step_kernel<T, S, 1><<<dim3(p.N, blocks), kThreads, 0, st>>>(p, wide);
     return cudaGetLastError();

@@ -96,7 +96,7 @@ def test_ssm_step(lib):
     assert call(G=3) == INVALID_ARG and call(G=0) == INVALID_ARG
     assert call(sp=2) == INVALID_ARG
     assert call(ldu=255) == INVALID_ARG and call(ldb=31) == INVALID_ARG and call(z=at(9), ldz=100) == INVALID_ARG
-    assert call(A=at(3, 4)) == INVALID_ARG and call(s=at(6, 8)) == INVALID_ARG
+    assert call(A=at(3, 4)) == INVALID_ARG and call(s=at(6, 16)) == INVALID_ARG
     assert call(s=None) == INVALID_ARG and call(A=None) == INVALID_ARG
     assert call(sl=None, N=9) == INVALID_ARG
     assert call(y=at(1)) == INVALID_ARG and call(y=at(6)) == INVALID_ARG
