@@ -278,8 +278,20 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(int32_t* tables, i
 
 // remap[0] is the number of used pages; remap[1 + p] the new place of a used page p behind it, -1
 // of a free one.
+__device__ __forceinline__ void remap_entry(int32_t* entry, int live, int P, const int32_t* remap, int32_t* status) {
+    const int e = *entry;
+    if (e == -1 || (e >= 0 && e < live)) return;
+    const int to = e >= 0 && e < P ? remap[1 + e] : -1;
+    if (to >= 0) *entry = to;
+    else report(status);  // an entry that held no used page stays as it is
+}
+
+// Table entries that the cluster itself looks over; more are a launch of their own over the machine.
+constexpr int64_t kEntriesOfCluster = 65536;
+
 __global__ void __launch_bounds__(kThreads) pages_compact_kernel(int32_t* refs, int P, int32_t* src_out,
-                                                                 int32_t* dst_out, int32_t* remap) {
+                                                                 int32_t* dst_out, int32_t* remap, int32_t* tables,
+                                                                 int entries, int32_t* status) {
     __shared__ Shared sh;
     cg::cluster_group cl = cg::this_cluster();
     int lo, hi, base[2], all[2];
@@ -311,25 +323,37 @@ __global__ void __launch_bounds__(kThreads) pages_compact_kernel(int32_t* refs, 
         refs[d] = refs[s];
         refs[s] = 0;
     }
+    if (entries == 0) return;
+    cl.sync();
+    for (int i = first; i < entries; i += step) remap_entry(tables + i, live, P, remap, status);
 }
 
 __global__ void __launch_bounds__(256) pages_remap_kernel(int32_t* tables, int64_t entries, int P, const int32_t* remap,
                                                           int32_t* status) {
     const int live = remap[0];
-    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < entries; i += gridDim.x * 256ll) {
-        const int e = tables[i];
-        if (e == -1 || (e >= 0 && e < live)) continue;
-        const int to = e >= 0 && e < P ? remap[1 + e] : -1;
-        if (to >= 0) tables[i] = to;
-        else report(status);  // an entry that held no used page stays as it is
-    }
+    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < entries; i += gridDim.x * 256ll)
+        remap_entry(tables + i, live, P, remap, status);
 }
 
 // ---- copying ---------------------------------------------------------------------------------
 
-constexpr int kCopyThreads = 256;
+constexpr int kCopyThreads = 256, kCopySms = 152;
 constexpr int kCopyVec = 4;                                  // 16-byte pieces of a thread in one go
 constexpr int kCopyPiece = kCopyThreads * kCopyVec * 16;     // bytes of a block in one go
+
+// Piece `at` of page s onto page d.
+__device__ __forceinline__ void copy_piece(char* pool, int64_t page_bytes, int s, int d, int64_t at) {
+    const uint4* from = reinterpret_cast<const uint4*>(pool + s * page_bytes + at);
+    uint4* to = reinterpret_cast<uint4*>(pool + d * page_bytes + at);
+    const int left = (int)(min((int64_t)kCopyPiece, page_bytes - at) / 16);
+    uint4 r[kCopyVec];
+#pragma unroll
+    for (int v = 0; v < kCopyVec; ++v)
+        if (v * kCopyThreads + (int)threadIdx.x < left) r[v] = __ldcs(from + v * kCopyThreads + threadIdx.x);
+#pragma unroll
+    for (int v = 0; v < kCopyVec; ++v)
+        if (v * kCopyThreads + (int)threadIdx.x < left) __stcs(to + v * kCopyThreads + threadIdx.x, r[v]);
+}
 
 // marks, all zero before: [0] pairs listed, [1, 1 + P) the last pair (+ 1) that writes a page,
 // [1 + P, 1 + 2 P) whether a pair reads it, then the list.
@@ -363,22 +387,60 @@ __global__ void __launch_bounds__(kCopyThreads, 8) pages_copy_kernel(char* pool,
             if (threadIdx.x == 0 && at == 0) report(status);
             continue;
         }
-        const uint4* from = reinterpret_cast<const uint4*>(pool + s * page_bytes + at);
-        uint4* to = reinterpret_cast<uint4*>(pool + d * page_bytes + at);
-        const int left = (int)(min((int64_t)kCopyPiece, page_bytes - at) / 16);
-        uint4 r[kCopyVec];
-#pragma unroll
-        for (int v = 0; v < kCopyVec; ++v)
-            if (v * kCopyThreads + (int)threadIdx.x < left) r[v] = __ldcs(from + v * kCopyThreads + threadIdx.x);
-#pragma unroll
-        for (int v = 0; v < kCopyVec; ++v)
-            if (v * kCopyThreads + (int)threadIdx.x < left) __stcs(to + v * kCopyThreads + threadIdx.x, r[v]);
+        copy_piece(pool, page_bytes, s, d, at);
+    }
+}
+
+// Up to kCopyThreads pairs: every block looks all of them over by itself (a thread holds its pair against
+// the others in shared memory, about a microsecond) and needs no marks.
+__global__ void __launch_bounds__(kCopyThreads, 8) pages_copy_few_kernel(char* pool, int64_t page_bytes, const int32_t* src,
+                                                                         const int32_t* dst, int n, int P, int32_t* status) {
+    __shared__ int2 pairs[kCopyThreads], good[kCopyThreads];
+    __shared__ int counts[kCopyThreads / 32];
+    const int i = threadIdx.x, lane = i & 31, warp = i >> 5;
+    int2 me = i < n ? make_int2(src[i], dst[i]) : make_int2(-1, -1);
+    bool bad = false;
+    if (me.x == -1 || me.y == -1 || me.x == me.y) {
+        bad = me.x == me.y && me.x != -1 && (me.x < 0 || me.x >= P);
+        me = make_int2(-1, -1);
+    } else if (me.x < 0 || me.x >= P || me.y < 0 || me.y >= P) {
+        bad = true;
+        me = make_int2(-1, -1);
+    }
+    pairs[i] = me;
+    __syncthreads();
+    bool ok = me.x != -1;
+    for (int j = 0; j < n && ok; ++j) {
+        const int2 o = pairs[j];
+        // a later pair writes this page, or a pair reads it: left alone
+        if (o.x == me.y || (j > i && o.y == me.y)) ok = false;
+    }
+    if (me.x != -1 && !ok) bad = true;
+    if (bad && blockIdx.x == 0) report(status);
+    const unsigned votes = __ballot_sync(0xffffffffu, ok);
+    if (lane == 0) counts[warp] = __popc(votes);
+    __syncthreads();
+    int before = __popc(votes & ((1u << lane) - 1)), all = 0;
+    for (int w = 0; w < kCopyThreads / 32; ++w) {
+        if (w < warp) before += counts[w];
+        all += counts[w];
+    }
+    if (ok) good[before] = me;
+    __syncthreads();
+    const int64_t pieces = (page_bytes + kCopyPiece - 1) / kCopyPiece, items = all * pieces;
+    for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+        const int2 q = good[it / pieces];
+        copy_piece(pool, page_bytes, q.x, q.y, it % pieces * kCopyPiece);
     }
 }
 
 template <typename... KArgs, typename... Args>
 cudaError_t launch_cluster(void (*kern)(KArgs...), int P, cudaStream_t st, Args... args) {
-    const int blocks = P <= kPagesOfOneBlock ? 1 : kMostBlocks;
+    if (P <= kPagesOfOneBlock) {  // a cluster of one, without the cost of asking for it
+        kern<<<1, kThreads, 0, st>>>(static_cast<KArgs>(args)...);
+        return cudaGetLastError();
+    }
+    constexpr int blocks = kMostBlocks;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(blocks);
     cfg.blockDim = dim3(kThreads);
@@ -416,25 +478,31 @@ size_t pages_compact_workspace(int P) { return ((size_t)P + 1) * 4; }
 cudaError_t pages_compact(int32_t* refs, int P, int32_t* tables, int64_t entries, int32_t* src, int32_t* dst, void* ws,
                           int32_t* status, cudaStream_t st) {
     int32_t* remap = entries > 0 ? static_cast<int32_t*>(ws) : nullptr;
-    cudaError_t e = launch_cluster(pages_compact_kernel, P, st, refs, P, src, dst, remap);
-    if (e != cudaSuccess || entries == 0) return e;
+    const bool one = entries <= kEntriesOfCluster;
+    cudaError_t e = launch_cluster(pages_compact_kernel, P, st, refs, P, src, dst, remap, tables, one ? (int)entries : 0, status);
+    if (e != cudaSuccess || one) return e;
     const int64_t blocks = (entries + 255) / 256;
     pages_remap_kernel<<<(unsigned)(blocks < 1216 ? blocks : 1216), 256, 0, st>>>(tables, entries, P, remap, status);
     return cudaGetLastError();
 }
 
-size_t pages_copy_workspace(int P, int n) { return (1 + 2 * (size_t)P + n) * 4; }
+size_t pages_copy_workspace(int P, int n) { return n <= kCopyThreads ? 0 : (1 + 2 * (size_t)P + n) * 4; }
 
 cudaError_t pages_copy(void* pool, int P, int64_t page_bytes, const int32_t* src, const int32_t* dst, int n, void* ws,
                        int32_t* status, cudaStream_t st) {
+    const int64_t items = n * ((page_bytes + kCopyPiece - 1) / kCopyPiece);
+    const unsigned grid = (unsigned)(items < kCopySms * 8 ? items : kCopySms * 8);
+    if (n <= kCopyThreads) {
+        pages_copy_few_kernel<<<grid, kCopyThreads, 0, st>>>(static_cast<char*>(pool), page_bytes, src, dst, n, P, status);
+        return cudaGetLastError();
+    }
     int32_t* marks = static_cast<int32_t*>(ws);
     cudaError_t e = cudaMemsetAsync(marks, 0, (1 + 2 * (size_t)P) * 4, st);
     if (e != cudaSuccess) return e;
     const int blocks = (n + 255) / 256;
     pages_mark_kernel<<<blocks < 1216 ? blocks : 1216, 256, 0, st>>>(src, dst, n, P, marks, status);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    const int64_t items = n * ((page_bytes + kCopyPiece - 1) / kCopyPiece);
-    pages_copy_kernel<<<(unsigned)(items < 152 * 8 ? items : 152 * 8), kCopyThreads, 0, st>>>(
+    pages_copy_kernel<<<grid, kCopyThreads, 0, st>>>(
         static_cast<char*>(pool), page_bytes, src, dst, P, marks, status);
     return cudaGetLastError();
 }

@@ -143,11 +143,6 @@ def _dt_of(dtype) -> int:
     raise TypeError(f"unsupported dtype {dtype}")
 
 
-def _lib_now():
-    """The library, without the lock once it is loaded."""
-    return _lib if _lib is not None else load_library()
-
-
 def _here(*tensors) -> int:
     """Every tensor given lies on one CUDA device, the current one; returns its index."""
     dev = -1
@@ -207,8 +202,14 @@ def _rows(name, t, lead: int):
     rows a fixed stride apart, each row's elements lying side by side."""
     if t is None:
         return None, 0
-    if t.is_contiguous() and t.numel():
-        return t.data_ptr(), t.stride(lead - 1) if t.shape[lead - 1] != 1 else t.shape[lead:].numel()
+    shape, stride = t.shape, t.stride()
+    if lead == 1:  # the single-token calls: [rows, width], or [rows, groups, width]
+        width = shape[1] if len(shape) == 2 else shape[1] * shape[2]
+        if stride[-1] == 1 and (len(shape) == 2 or shape[1] == 1 or stride[1] == shape[2]):
+            if shape[0] < 2:
+                return t.data_ptr(), width
+            if stride[0] >= width:
+                return t.data_ptr(), stride[0]
     width = 1
     for d in reversed(range(lead, t.dim())):
         if t.shape[d] != 1 and t.stride(d) != width:
@@ -391,12 +392,16 @@ def recurrent_step(q, k, v, g, beta, state, scale: float | None = None, o_dtype=
         o = torch.empty((N, H, V), dtype=o_dtype, device=q.device)
     if slots is not None:
         dev = _here(q, k, v, g, beta, state, o, slots, status)
-        _int32(slots, status)
-        _like(q, k, v, g, beta)
-        _f32(state)
-        for name, x, shape in (("k", k, (N, H, K)), ("v", v, (N, H, V)), ("g", g, (N, H, K)), ("beta", beta, (N, H)),
-                               ("state", state, (state.shape[0], H, K, V)), ("o", o, (N, H, V)), ("slots", slots, (N,))):
-            _shape(name, x, shape)
+        _check_slots(slots, status, N)
+        dt = q.dtype
+        if k.dtype is not dt or v.dtype is not dt or g.dtype is not dt or beta.dtype is not dt:
+            raise TypeError(f"k, v, g and beta must be of q's type, {dt}")
+        if state.dtype is not torch.float32:
+            raise TypeError("state must be float32")
+        if k.shape != (N, H, K) or g.shape != (N, H, K) or v.shape != (N, H, V) or beta.shape != (N, H) or o.shape != (N, H, V):
+            raise ValueError(f"k and g must be [{N}, {H}, {K}], v and o [{N}, {H}, {V}], beta [{N}, {H}]")
+        if state.shape[1:] != (H, K, V):
+            raise ValueError(f"state must be [P, {H}, {K}, {V}]")
         st = lib.kda_recurrent_step_slots(_at(q), _at(k), _at(v), _at(g), _at(beta), _dt(q), float(scale or 0.0),
                                           _at(state), _at(slots), state.shape[0], N, H, K, V, _at(o), _dt(o),
                                           _at(status), _stream_of(dev))
@@ -534,6 +539,13 @@ def chunk_bwd(q, k, v, g, beta, dO, dS_T=None, scale: float | None = None, initi
     return out
 
 
+def _check_slots(slots, status, N):
+    if slots is not None and (slots.dtype is not torch.int32 or slots.shape != (N,)):
+        raise TypeError(f"slots must be int32 [{N}]")
+    if status is not None and status.dtype is not torch.int32:
+        raise TypeError("status must be int32")
+
+
 def _conv_check(x, weight, bias, conv_act):
     C, W = weight.shape
     _f32(weight, bias)
@@ -566,7 +578,7 @@ def short_conv_fwd(x, weight, bias=None, conv_act: int = 0, initial=None, cu_seq
     :func:`chunk_fwd`.  Returns (y [B,T,C], final history [N,W-1,C] or None).  Rows that
     belong to no sequence are left as they are.
     """
-    lib = _lib_now()
+    lib = _lib if _lib is not None else load_library()
     C, W = _conv_check(x, weight, bias, conv_act)
     B, T, _ = x.shape
     N = _sequences(x, cu_seqlens)
@@ -592,7 +604,7 @@ def short_conv_bwd(x, weight, dy, bias=None, conv_act: int = 0, initial=None, cu
     arguments).  dy [B,T,C] and dfinal [N,W-1,C] share a type: x's, or fp32.  Returns a
     dict: dx [B,T,C] and dinitial [N,W-1,C] (None without ``initial``) in dy's type, dweight
     [C,W] and dbias [C] (None without ``bias``) fp32."""
-    lib = _lib_now()
+    lib = _lib if _lib is not None else load_library()
     C, W = _conv_check(x, weight, bias, conv_act)
     B, T, _ = x.shape
     N = _sequences(x, cu_seqlens)
@@ -620,20 +632,21 @@ def short_conv_step(x, history, weight, bias=None, conv_act: int = 0, slots=None
     """One token of each of N sequences: x [N,C]; ``history`` [P,W-1,C] is updated in place
     (row i's page is ``slots[i]``, or i without slots; -1 is a padded row).  Returns y
     [N,C].  ``slots``/``status`` as for :func:`recurrent_step`."""
-    lib = _lib_now()
+    lib = _lib if _lib is not None else load_library()
     C, W = _conv_check(x, weight, bias, conv_act)
     N = x.shape[0]
+    P = history.shape[0]
     dev = _here(x, history, weight, bias, slots, y, status)
-    _like(x, history, y)
-    _int32(slots, status)
-    _shape("history", history, (history.shape[0], W - 1, C))
-    _shape("slots", slots, (N,))
-    _shape("y", y, (N, C))
+    if history.dtype is not x.dtype or history.shape != (P, W - 1, C):
+        raise ValueError(f"history must be [P, {W - 1}, {C}] of {x.dtype}")
     if y is None:
         y = torch.empty((N, C), dtype=x.dtype, device=x.device)
+    elif y.dtype is not x.dtype or y.shape != (N, C):
+        raise ValueError(f"y must be {(N, C)} of {x.dtype}")
+    _check_slots(slots, status, N)
     px, ldx = _rows("x", x, 1)
-    st = lib.kda_short_conv_step(px, ldx, _at(weight), _at(bias), conv_act, _dt(x), _at(history), _at(slots),
-                                 history.shape[0], N, C, W, _at(y), _at(status), _stream_of(dev))
+    st = lib.kda_short_conv_step(px, ldx, _at(weight), _at(bias), conv_act, _dt(x), _at(history), _at(slots), P, N, C, W, _at(y),
+                                 _at(status), _stream_of(dev))
     _check("kda_short_conv_step", st)
     return y
 
@@ -641,18 +654,19 @@ def short_conv_step(x, history, weight, bias=None, conv_act: int = 0, slots=None
 def _ssm_check(u, delta, A, Bm, Cm, D, z, delta_bias):
     """(C, G, S) of a scan call whose u is [..., C] and Bm, Cm [..., G, S]."""
     C, S = A.shape
-    lead = tuple(u.shape[:-1])
-    G = Bm.shape[-2]
-    _like(u, delta, Bm, Cm, z)
-    _f32(A, D, delta_bias)
-    _shape("u", u, lead + (C,))
-    _shape("delta", delta, lead + (C,))
-    _shape("z", z, lead + (C,))
-    _shape("Bm", Bm, lead + (G, S))
-    _shape("Cm", Cm, lead + (G, S))
-    _shape("D", D, (C,))
-    _shape("delta_bias", delta_bias, (C,))
-    return C, G, S
+    rows, vecs, dt = u.shape, Bm.shape, u.dtype
+    if rows[-1] != C or delta.shape != rows or (z is not None and z.shape != rows):
+        raise ValueError(f"u, delta and z must be [..., {C}] alike")
+    if vecs[-1] != S or vecs[:-2] != rows[:-1] or Cm.shape != vecs:
+        raise ValueError(f"Bm and Cm must be {tuple(rows[:-1])} + [G, {S}] alike")
+    if delta.dtype is not dt or Bm.dtype is not dt or Cm.dtype is not dt or (z is not None and z.dtype is not dt):
+        raise TypeError(f"delta, Bm, Cm and z must be of u's type, {dt}")
+    for v in (D, delta_bias):
+        if v is not None and (v.dtype is not torch.float32 or v.shape != (C,)):
+            raise TypeError(f"D and delta_bias must be float32 [{C}]")
+    if A.dtype is not torch.float32:
+        raise TypeError("A must be float32")
+    return C, vecs[-2], S
 
 
 def ssm_step(u, delta, A, Bm, Cm, state, D=None, z=None, delta_bias=None, softplus: bool = True, slots=None,
@@ -664,23 +678,23 @@ def ssm_step(u, delta, A, Bm, Cm, state, D=None, z=None, delta_bias=None, softpl
     u, delta, z: [N,C]; A: [C,S] fp32, S in 8, 16, 32, 64; Bm, Cm: [N,G,S], channel c in
     group c // (C // G); D, delta_bias: [C] fp32; ``state`` fp32 [P,C,S] is updated in place.
     Returns y [N,C].  ``slots``/``status`` as for :func:`recurrent_step`."""
-    lib = _lib_now()
+    lib = _lib if _lib is not None else load_library()
     C, G, S = _ssm_check(u, delta, A, Bm, Cm, D, z, delta_bias)
     N = u.shape[0]
+    P = state.shape[0]
     dev = _here(u, delta, A, Bm, Cm, state, D, z, delta_bias, slots, y, status)
-    _like(u, y)
-    _f32(state)
-    _int32(slots, status)
-    _shape("state", state, (state.shape[0], C, S))
-    _shape("slots", slots, (N,))
-    _shape("y", y, (N, C))
     if y is None:
         y = torch.empty((N, C), dtype=u.dtype, device=u.device)
+    elif y.dtype is not u.dtype or y.shape != (N, C):
+        raise ValueError(f"y must be {(N, C)} of {u.dtype}")
+    if state.dtype is not torch.float32 or state.shape != (P, C, S):
+        raise ValueError(f"state must be fp32 [P, {C}, {S}]")
+    _check_slots(slots, status, N)
     (pu, ldu), (pd, ldd), (pz, ldz) = _rows("u", u, 1), _rows("delta", delta, 1), _rows("z", z, 1)
     (pb, ldb), (pc, ldc) = _rows("Bm", Bm, 1), _rows("Cm", Cm, 1)
     st = lib.kda_ssm_step(pu, ldu, pd, ldd, _at(A), pb, ldb, pc, ldc, _at(D), pz, ldz, _at(delta_bias), int(softplus),
-                          _dt(u), _at(state), _at(slots), state.shape[0], N, C, G, S, _at(y), _at(status),
-                          _stream_of(dev))
+                          KDA_BF16 if u.dtype is torch.bfloat16 else _dt(u), _at(state), _at(slots), P, N, C, G, S, _at(y),
+                          _at(status), _stream_of(dev))
     _check("kda_ssm_step", st)
     return y
 
@@ -700,7 +714,7 @@ def ssm_scan_fwd(u, delta, A, Bm, Cm, D=None, z=None, delta_bias=None, softplus:
     fp32 [N,C,S] (None: zeros); ``cu_seqlens`` as for :func:`chunk_fwd`.  Returns (y
     [B,T,C], final_state [N,C,S] fp32 or None).  Rows that belong to no sequence are left
     as they are."""
-    lib = _lib_now()
+    lib = _lib if _lib is not None else load_library()
     C, G, S = _ssm_check(u, delta, A, Bm, Cm, D, z, delta_bias)
     B, T, _ = u.shape
     N = _sequences(u, cu_seqlens)
@@ -729,7 +743,7 @@ def ssm_scan_bwd(u, delta, A, Bm, Cm, dy, D=None, z=None, delta_bias=None, softp
     arguments).  dy [B,T,C] is of u's type or fp32.  Returns a dict: du, ddelta, dz [B,T,C]
     and dB, dC [B,T,G,S] in dy's type, dA [C,S], dD, ddelta_bias [C] and dinitial_state
     [N,C,S] fp32; the gradient of an argument that was not given is None."""
-    lib = _lib_now()
+    lib = _lib if _lib is not None else load_library()
     C, G, S = _ssm_check(u, delta, A, Bm, Cm, D, z, delta_bias)
     B, T, _ = u.shape
     N = _sequences(u, cu_seqlens)
@@ -760,7 +774,7 @@ def pages_alloc(refs, n: int, pages=None, status=None):
     no more; ``refs`` [P] (references of each page, 0: free) is updated.  ``status`` of
     every pages call: an optional device int32 word, 5 = KDA_ERR_RANGE when a request
     was refused (a refused request changes nothing)."""
-    lib = _lib_now()
+    lib = _lib if _lib is not None else load_library()
     dev = _here(refs, pages, status)
     _int32(refs, pages, status)
     _shape("pages", pages, (n,))
@@ -773,7 +787,7 @@ def pages_alloc(refs, n: int, pages=None, status=None):
 def pages_free(refs, pages, status=None):
     """Give back one reference of each page listed in ``pages`` (int32, any shape; -1 entries
     are skipped)."""
-    lib = _lib_now()
+    lib = _lib if _lib is not None else load_library()
     dev = _here(refs, pages, status)
     _int32(refs, pages, status)
     _check("kda_pages_free", lib.kda_pages_free(_at(refs), refs.numel(), _at(pages), pages.numel(), _at(status),
@@ -786,14 +800,15 @@ def pages_fork(tables, lens, refs, parents, children, page_tokens: int, status=N
     [S,width] (-1 behind a sequence's pages); lens: int32 [S] tokens.  Returns (src, dst),
     int32 [n]: the copies to make in every pool with :func:`pages_copy` (-1: none).  Free
     the child's former pages first."""
-    lib = _lib_now()
+    lib = _lib if _lib is not None else load_library()
     n = parents.numel()
     S, width = tables.shape
     dev = _here(tables, lens, refs, parents, children, status)
     _int32(tables, lens, refs, parents, children, status)
     _shape("lens", lens, (S,))
     _shape("children", children, parents.shape)
-    src, dst = torch.empty((2, n), dtype=torch.int32, device=refs.device)
+    src = torch.empty(n, dtype=torch.int32, device=refs.device)
+    dst = torch.empty(n, dtype=torch.int32, device=refs.device)
     st = lib.kda_pages_fork(_at(tables), _at(lens), S, width, int(page_tokens), _at(refs), refs.numel(), _at(parents),
                             _at(children), n, _at(src), _at(dst), _at(status), _stream_of(dev))
     _check("kda_pages_fork", st)
@@ -804,11 +819,12 @@ def pages_compact(refs, tables=None, workspace=None, status=None):
     """Close up the pools: used pages behind the number of used pages move into the free
     places before it, in order; ``refs`` and the table entries follow.  Returns (src, dst),
     int32 [P // 2]: the copies to make in every pool with :func:`pages_copy` (-1: none)."""
-    lib = _lib_now()
+    lib = _lib if _lib is not None else load_library()
     dev = _here(refs, tables, workspace, status)
     _int32(refs, tables, status)
     P = refs.numel()
-    src, dst = torch.empty((2, P // 2), dtype=torch.int32, device=refs.device)
+    src = torch.empty(P // 2, dtype=torch.int32, device=refs.device)
+    dst = torch.empty(P // 2, dtype=torch.int32, device=refs.device)
     ws, ws_bytes = _workspace(int(lib.kda_pages_compact_workspace_size(P)), refs.device, workspace)
     st = lib.kda_pages_compact(_at(refs), P, _at(tables), 0 if tables is None else tables.numel(), _at(src), _at(dst),
                                _at(ws), ws_bytes, _at(status), _stream_of(dev))
@@ -820,7 +836,7 @@ def pages_copy(pool, src, dst, workspace=None, status=None):
     """Copy page ``src[i]`` of ``pool`` ([P, ...], any type, a page's bytes a multiple of 16)
     onto page ``dst[i]``; -1 entries are skipped.  A destination that a later pair writes or
     another pair reads is refused."""
-    lib = _lib_now()
+    lib = _lib if _lib is not None else load_library()
     dev = _here(pool, src, dst, workspace, status)
     _int32(src, dst, status)
     _shape("dst", dst, src.shape)

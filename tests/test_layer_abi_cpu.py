@@ -203,11 +203,12 @@ def test_pages(lib):
     assert compact(ws=at(5, 4)) == INVALID_ARG and compact(ws=at(1)) == INVALID_ARG
     assert compact(P=0, r=None, s=None, d=None, ws=None, wsb=0) == 0
 
-    need = lib.kda_pages_copy_workspace_size(100, 7)
-    assert need == (1 + 200 + 7) * 4 and lib.kda_pages_copy_workspace_size(100, 0) == 0
+    need = lib.kda_pages_copy_workspace_size(100, 300)
+    assert need == (1 + 200 + 300) * 4 and lib.kda_pages_copy_workspace_size(100, 0) == 0
+    assert lib.kda_pages_copy_workspace_size(100, 256) == 0      # few pairs need none
 
     def copy(**kw):
-        a = dict(p=at(1), P=100, b=64, s=at(2), d=at(3), n=7, ws=at(4), wsb=need, st=None)
+        a = dict(p=at(1), P=100, b=64, s=at(2), d=at(3), n=300, ws=at(4), wsb=need, st=None)
         a.update(kw)
         return lib.kda_pages_copy(a["p"], a["P"], a["b"], a["s"], a["d"], a["n"], a["ws"], a["wsb"], a["st"], None)
     assert copy(b=24) == UNSUPPORTED
