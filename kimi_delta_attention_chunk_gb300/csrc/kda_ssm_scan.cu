@@ -318,39 +318,30 @@ __global__ void __launch_bounds__(kThreads, 4) scan_kernel(SsmScanParams p, SeqM
     }
 }
 
-// Start states of the runs from their end states, in place: one thread carries four states along.
+// Start states of the runs from their end states, in place: one thread carries one state along, with
+// eight runs requested together.
 __global__ void __launch_bounds__(128) scan_prefix_kernel(const float* A, Runs r, int runs, int C, int S) {
-    const int64_t q = blockIdx.x * 128ll + threadIdx.x, quads = (int64_t)C * S / 4;
-    if (q >= quads) return;
-    const int c = (int)(q * 4 / S);
-    float4 a = reinterpret_cast<const float4*>(A)[q];
-    a.x *= kLog2e; a.y *= kLog2e; a.z *= kLog2e; a.w *= kLog2e;
-    float4 h = make_float4(0.f, 0.f, 0.f, 0.f);
-    float4* st = reinterpret_cast<float4*>(r.state) + q;
+    const int64_t i = blockIdx.x * 128ll + threadIdx.x, n = (int64_t)C * S;
+    if (i >= n) return;
+    const int c = (int)(i / S);
+    const float a = kLog2e * __ldg(A + i);
+    float h = 0.f;
     constexpr int kAhead = 8;
     for (int j0 = 0; j0 < runs; j0 += kAhead) {
-        float4 e[kAhead];
-        float d[kAhead];
+        float e[kAhead], d[kAhead];
         int cut[kAhead];
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
-            const int j = min(j0 + k, runs - 1);
-            e[k] = st[j * quads];
+            const int j = min(j0 + k, runs - 2);  // nobody starts from the last run's end
+            e[k] = r.state[j * n + i];
             d[k] = r.sum_d[(int64_t)j * C + c];
             cut[k] = r.cut[j];
         }
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
             if (j0 + k >= runs) break;
-            st[(j0 + k) * quads] = h;
-            if (cut[k]) {
-                h = e[k];
-            } else {
-                h.x = fmaf(ex2(d[k] * a.x), h.x, e[k].x);
-                h.y = fmaf(ex2(d[k] * a.y), h.y, e[k].y);
-                h.z = fmaf(ex2(d[k] * a.z), h.z, e[k].z);
-                h.w = fmaf(ex2(d[k] * a.w), h.w, e[k].w);
-            }
+            r.state[(j0 + k) * n + i] = h;
+            h = cut[k] ? e[k] : fmaf(ex2(d[k] * a), h, e[k]);
         }
     }
 }
@@ -390,11 +381,11 @@ cudaError_t launch_rows(const SsmScanParams& p, cudaStream_t st) {
     Runs r{};
     if (q.split) {
         r = runs_at(p.ws, q.runs, p.C, S);
-        scan_kernel<T, S, false, wide_rows><<<grid, kThreads, 0, st>>>(p, m, q.run, r, true, wide_vecs);
+        scan_kernel<T, S, false, wide_rows><<<dim3(q.blocks, q.runs - 1), kThreads, 0, st>>>(p, m, q.run, r, true, wide_vecs);
         cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
-        const int64_t quads = (int64_t)p.C * S / 4;
-        scan_prefix_kernel<<<(unsigned)((quads + 127) / 128), 128, 0, st>>>(p.A, r, q.runs, p.C, S);
+        const int64_t states = (int64_t)p.C * S;
+        scan_prefix_kernel<<<(unsigned)((states + 127) / 128), 128, 0, st>>>(p.A, r, q.runs, p.C, S);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     scan_kernel<T, S, true, wide_rows><<<grid, kThreads, 0, st>>>(p, m, q.run, r, q.split, wide_vecs);

@@ -17,7 +17,7 @@
 //      recomputed into registers.
 // A lane has eight states of a channel in step 3: fewer lanes share a channel's scalars and shuffles, and
 // twelve warps an SM fit with their states in 168 registers.  (Four states a lane, chunks not halved, and
-// the sums over channels by shuffles took 640 us where this takes SCAN_BWD_US for 2 x 2048 x 4096 x 16.)
+// the sums over channels by shuffles took 640 us where step 3 takes 400 for 2 x 2048 x 4096 x 16.)
 // Sums over channels (dB, dC) go through shared memory, 16 additions a lane and token, then the block's
 // warps, and partial sums of the channel blocks; sums over tokens through partial sums of the chunks.
 // Every sum has an order fixed by the sizes.  Instruction issue bounds steps 1 and 3.
@@ -286,25 +286,25 @@ __global__ void __launch_bounds__(kSumThreads, 4) scan_bwd_sum_kernel(SsmScanPar
 
 // ---- 2. the state before and the gradient behind each chunk -------------------------------------
 
+// One thread carries one state along; blockIdx.y 0: forwards, 1: backwards.  It is bound by the latency of
+// its loads, so sixteen chunks' are requested together.
 __global__ void __launch_bounds__(128) scan_bwd_prefix_kernel(const float* A, Scratch w, int chunks, int C, int S) {
-    const int64_t q = blockIdx.x * 128ll + threadIdx.x, quads = (int64_t)C * S / 4;
-    if (q >= quads) return;
-    const int c = (int)(q * 4 / S);
-    float4 a = reinterpret_cast<const float4*>(A)[q];
-    a.x *= kLog2e; a.y *= kLog2e; a.z *= kLog2e; a.w *= kLog2e;
+    const int64_t i = blockIdx.x * 128ll + threadIdx.x, n = (int64_t)C * S;
+    if (i >= n) return;
+    const int c = (int)(i / S);
+    const float a = kLog2e * __ldg(A + i);
     const bool back = blockIdx.y == 1;
-    float4* io = reinterpret_cast<float4*>(back ? w.grad : w.state) + q;
+    float* io = (back ? w.grad : w.state) + i;
     const int stop = back ? kThrough : kStarts;
-    float4 h = make_float4(0.f, 0.f, 0.f, 0.f);
-    constexpr int kAhead = 8;
+    float h = 0.f;
+    constexpr int kAhead = 16;
     for (int j0 = 0; j0 < chunks; j0 += kAhead) {
-        float4 e[kAhead];
-        float d[kAhead];
+        float e[kAhead], d[kAhead];
         bool on[kAhead];
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
-            const int i = min(j0 + k, chunks - 1), j = back ? chunks - 1 - i : i;
-            e[k] = io[j * quads];
+            const int x = min(j0 + k, chunks - 1), j = back ? chunks - 1 - x : x;
+            e[k] = io[j * n];
             d[k] = w.sum_d[(int64_t)j * C + c];
             on[k] = ((w.flags[j] & stop) != 0) == back;
         }
@@ -312,15 +312,8 @@ __global__ void __launch_bounds__(128) scan_bwd_prefix_kernel(const float* A, Sc
         for (int k = 0; k < kAhead; ++k) {
             if (j0 + k >= chunks) break;
             const int j = back ? chunks - 1 - (j0 + k) : j0 + k;
-            io[j * quads] = h;
-            if (on[k]) {
-                h.x = fmaf(ex2(d[k] * a.x), h.x, e[k].x);
-                h.y = fmaf(ex2(d[k] * a.y), h.y, e[k].y);
-                h.z = fmaf(ex2(d[k] * a.z), h.z, e[k].z);
-                h.w = fmaf(ex2(d[k] * a.w), h.w, e[k].w);
-            } else {
-                h = e[k];
-            }
+            io[j * n] = h;
+            h = on[k] ? fmaf(ex2(d[k] * a), h, e[k]) : e[k];
         }
     }
 }
@@ -730,14 +723,32 @@ __global__ void __launch_bounds__(kThreads, S == 8 ? 2 : 3) scan_bwd_kernel(SsmS
 
 // ---- 4. the partial sums ------------------------------------------------------------------------
 
-// out[i] = sum of the chunks' in[i], chunk by chunk.
-__global__ void __launch_bounds__(128) scan_bwd_chunks_kernel(const float* in, int chunks, int64_t n, float* out) {
-    const int64_t i = blockIdx.x * 128ll + threadIdx.x;
-    if (i >= n) return;
+// dA, dD and dbias: sums over the chunks.  A block has 32 elements (of the three outputs one after the
+// other) in eight threads each; a thread adds up every eighth chunk, and the eight sums are added in order.
+struct ChunkSums {
+    const float* in[3];
+    float* out[3];
+    int64_t n[3];
+};
+__global__ void __launch_bounds__(256) scan_bwd_chunks_kernel(ChunkSums s, int chunks) {
+    __shared__ float part[8][32];
+    const int x = threadIdx.x % 32, y = threadIdx.x / 32;
+    int64_t i = blockIdx.x * 32ll + x;
+    int v = 0;
+    while (v < 2 && i >= s.n[v]) i -= s.n[v++];
+    const bool on = i < s.n[v] && s.out[v];
     float a = 0.f;
+    if (on) {
 #pragma unroll 8
-    for (int j = 0; j < chunks; ++j) a += in[j * n + i];
-    out[i] = a;
+        for (int j = y; j < chunks; j += 8) a += s.in[v][j * s.n[v] + i];
+    }
+    part[y][x] = a;
+    __syncthreads();
+    if (y == 0 && on) {
+#pragma unroll
+        for (int k = 1; k < 8; ++k) a += part[k][x];
+        s.out[v][i] = a;
+    }
 }
 
 // dB and dC from the channel blocks of each group.
@@ -750,7 +761,7 @@ __global__ void __launch_bounds__(256) scan_bwd_vec_kernel(const float* in, SeqM
     const int g = (int)(tg % G), t = (int)(tg / G);
     if (t < m.first() || t >= m.last()) return;
     float a = 0.f;
-#pragma unroll 8
+#pragma unroll 16
     for (int b = 0; b < per_group; ++b) a += in[((int64_t)(g * per_group + b) * m.total + t) * 2 * S + j];
     TG* out = j < S ? dB : dC;
     out[tg * S + j % S] = from_f32<TG>(a);
@@ -784,20 +795,16 @@ cudaError_t launch(const SsmScanParams& p, cudaStream_t st) {
     scan_bwd_sum_kernel<T, TG, S><<<dim3(sum_blocks, chunks), kSumThreads, sizeof(SumShared<T, TG, S>), st>>>(p, m, w, wide_vecs, wide_rows);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    const int64_t quads = (int64_t)p.C * S / 4;
-    scan_bwd_prefix_kernel<<<dim3((unsigned)((quads + 127) / 128), 2), 128, 0, st>>>(p.A, w, chunks, p.C, S);
+    const int64_t states = (int64_t)p.C * S;
+    scan_bwd_prefix_kernel<<<dim3((unsigned)((states + 127) / 128), 2), 128, 0, st>>>(p.A, w, chunks, p.C, S);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     constexpr int smem = sizeof(BwdShared<S>);
     const auto kern = pairs ? scan_bwd_kernel<T, TG, S, true> : scan_bwd_kernel<T, TG, S, false>;
     if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
     kern<<<dim3(blocks, chunks), kThreads, smem, st>>>(p, m, w);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    auto over_chunks = [&](const float* in, int64_t n, float* out) {
-        if (out) scan_bwd_chunks_kernel<<<(unsigned)((n + 127) / 128), 128, 0, st>>>(in, chunks, n, out);
-    };
-    over_chunks(w.state, (int64_t)p.C * S, p.dA);
-    over_chunks(w.dD, p.C, p.dD);
-    over_chunks(w.dbias, p.C, p.dbias);
+    const ChunkSums sums{{w.state, w.dD, w.dbias}, {p.dA, p.dD, p.dbias}, {(int64_t)p.C * S, p.C, p.C}};
+    scan_bwd_chunks_kernel<<<(unsigned)(((int64_t)p.C * (S + 2) + 31) / 32), 256, 0, st>>>(sums, chunks);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const int64_t n = (int64_t)p.total * p.G * 2 * S;
     if (n > 0)
