@@ -195,6 +195,7 @@ kda_status kda_ssm_step(const void* u, int64_t ldu, const void* delta, int64_t l
     if (ldu < C || ldd < C || (z && ldz < C) || ldb < vec || ldc < vec) return KDA_ERR_INVALID_ARG;
     if (N > 0 && (!u || !delta || !A || !Bm || !Cm || !state || !y || P == 0)) return KDA_ERR_INVALID_ARG;
     if (!slots && N > P) return KDA_ERR_INVALID_ARG;
+    if ((int64_t)N * (((int64_t)C * S + 1023) / 1024) > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;  // blocks of one launch
     const size_t es = size_of(dtype);
     for (const void* p : {u, delta, Bm, Cm, z, (const void*)y})
         if (!aligned(p, es)) return KDA_ERR_INVALID_ARG;

@@ -51,11 +51,12 @@ struct EightOf {
 // kRows rows of the batch a block: A is as many bytes as a row's states, and is fetched once for them.
 // Everything that the rows need is requested before the first is worked on.
 template <typename T, int S, int kRows>
-__global__ void __launch_bounds__(kThreads) ssm_step_kernel(SsmStepParams p, bool wide) {
+__global__ void __launch_bounds__(kThreads) ssm_step_kernel(SsmStepParams p, int blocks, bool wide) {
     constexpr int LP = S / 8, CH = kThreads / LP;
-    const int row0 = blockIdx.x * kRows;
+    // (the blocks of one page follow one another)
+    const int row0 = (int)(blockIdx.x / blocks) * kRows;
     const int lane = threadIdx.x % LP;
-    const int c = blockIdx.y * CH + threadIdx.x / LP;
+    const int c = (int)(blockIdx.x % blocks) * CH + threadIdx.x / LP;
     const bool on = c < p.C;
     const int cc = on ? c : 0, g = cc / (p.C / p.G) * S + lane * 8;
     const int64_t per_page = (int64_t)p.C * S, at = (int64_t)cc * S + lane * 8;
@@ -120,9 +121,9 @@ cudaError_t launch(const SsmStepParams& p, cudaStream_t st) {
     const bool wide = kda_host::rows_aligned(p.Bm, p.ldb, piece) && kda_host::rows_aligned(p.Cm, p.ldc, piece);
     // two rows a block once that leaves the machine four blocks an SM, else one
     if ((int64_t)(p.N + 1) / 2 * blocks >= 4 * 152)
-        ssm_step_kernel<T, S, 2><<<dim3((p.N + 1) / 2, blocks), kThreads, 0, st>>>(p, wide);
+        ssm_step_kernel<T, S, 2><<<(unsigned)((int64_t)((p.N + 1) / 2) * blocks), kThreads, 0, st>>>(p, blocks, wide);
     else
-        ssm_step_kernel<T, S, 1><<<dim3(p.N, blocks), kThreads, 0, st>>>(p, wide);
+        ssm_step_kernel<T, S, 1><<<(unsigned)((int64_t)p.N * blocks), kThreads, 0, st>>>(p, blocks, wide);
     return cudaGetLastError();
 }
 
