@@ -38,6 +38,9 @@ bool apart(const Span (&in)[NI], const Span (&out)[NO]) {
     return true;
 }
 
+// Pages and list entries of the pages calls: they are counted in 32 bits.
+constexpr int kMostPages = 1 << 30;
+
 kda_status clear(int32_t* status, cudaStream_t st) {
     if (status && cudaMemsetAsync(status, 0, sizeof(int32_t), st) != cudaSuccess) return KDA_ERR_CUDA;
     return KDA_OK;
@@ -291,7 +294,9 @@ kda_status kda_ssm_scan_bwd(const void* u, int64_t ldu, const void* delta, int64
 }
 
 kda_status kda_pages_alloc(int32_t* refs, int P, int n, int32_t* pages, int32_t* status, void* stream) {
+    if (n > kMostPages) return KDA_ERR_UNSUPPORTED;
     if (P < 0 || n < 0 || (P > 0 && !refs) || (n > 0 && !pages)) return KDA_ERR_INVALID_ARG;
+    if (P > kMostPages) return KDA_ERR_UNSUPPORTED;
     if (!aligned(refs, 4) || !aligned(pages, 4) || !aligned(status, 4)) return KDA_ERR_INVALID_ARG;
     const Span in[] = {{nullptr, 0}};
     const Span out[] = {{refs, (size_t)P * 4}, {pages, (size_t)n * 4}, {status, 4}};
@@ -304,6 +309,7 @@ kda_status kda_pages_alloc(int32_t* refs, int P, int n, int32_t* pages, int32_t*
 
 kda_status kda_pages_free(int32_t* refs, int P, const int32_t* pages, int64_t n, int32_t* status, void* stream) {
     if (P < 0 || n < 0 || (P > 0 && !refs) || (n > 0 && !pages)) return KDA_ERR_INVALID_ARG;
+    if (P > kMostPages) return KDA_ERR_UNSUPPORTED;
     if (!aligned(refs, 4) || !aligned(pages, 4) || !aligned(status, 4)) return KDA_ERR_INVALID_ARG;
     const Span in[] = {{pages, (size_t)n * 4}};
     const Span out[] = {{refs, (size_t)P * 4}, {status, 4}};
@@ -318,7 +324,7 @@ kda_status kda_pages_fork(int32_t* tables, int32_t* lens, int S, int width, int 
                           const int32_t* parents, const int32_t* children, int n, int32_t* src, int32_t* dst,
                           int32_t* status, void* stream) {
     if (S < 0 || width <= 0 || page_tokens <= 0 || P < 0 || n < 0) return KDA_ERR_INVALID_ARG;
-    if (n > 65536) return KDA_ERR_UNSUPPORTED;
+    if (n > 65536 || P > kMostPages) return KDA_ERR_UNSUPPORTED;
     if (n > 0 && (!parents || !children || !src || !dst)) return KDA_ERR_INVALID_ARG;
     if ((S > 0 && (!tables || !lens)) || (P > 0 && !refs)) return KDA_ERR_INVALID_ARG;
     for (const void* p : {(const void*)tables, (const void*)lens, (const void*)refs, (const void*)parents,
@@ -340,6 +346,7 @@ size_t kda_pages_compact_workspace_size(int P) { return P <= 0 ? 0 : kda::pages_
 kda_status kda_pages_compact(int32_t* refs, int P, int32_t* tables, int64_t entries, int32_t* src, int32_t* dst,
                              void* workspace, size_t workspace_bytes, int32_t* status, void* stream) {
     if (P < 0 || entries < 0 || (P > 0 && !refs) || (entries > 0 && !tables) || (P > 1 && (!src || !dst))) return KDA_ERR_INVALID_ARG;
+    if (P > kMostPages) return KDA_ERR_UNSUPPORTED;
     for (const void* p : {(const void*)tables, (const void*)refs, (const void*)src, (const void*)dst, (const void*)status})
         if (!aligned(p, 4)) return KDA_ERR_INVALID_ARG;
     const size_t need = P > 0 ? kda::pages_compact_workspace(P) : 0;
@@ -360,7 +367,7 @@ size_t kda_pages_copy_workspace_size(int P, int n) { return P <= 0 || n <= 0 ? 0
 kda_status kda_pages_copy(void* pool, int P, int64_t page_bytes, const int32_t* src, const int32_t* dst, int n,
                           void* workspace, size_t workspace_bytes, int32_t* status, void* stream) {
     if (P < 0 || n < 0 || page_bytes <= 0 || (P > 0 && !pool) || (n > 0 && (!src || !dst))) return KDA_ERR_INVALID_ARG;
-    if (page_bytes % 16 != 0) return KDA_ERR_UNSUPPORTED;
+    if (page_bytes % 16 != 0 || P > kMostPages || n > kMostPages) return KDA_ERR_UNSUPPORTED;
     if ((double)P * (double)page_bytes > 9.0e18) return KDA_ERR_INVALID_ARG;
     if (!kda_host::aligned16(pool) || !aligned(src, 4) || !aligned(dst, 4) || !aligned(status, 4)) return KDA_ERR_INVALID_ARG;
     const size_t need = P > 0 && n > 0 ? kda::pages_copy_workspace(P, n) : 0;

@@ -516,7 +516,8 @@ __global__ void __launch_bounds__(kThreads, S == 8 ? 2 : 3) scan_bwd_kernel(SsmS
                 load8(w.mid + slot * S + cs, mid);
                 const float sd = w.sum_mid[slot + c];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) h[q] = fma2(ex2_2(mul2(A2[q], pack(sd, sd))), h[q], mid[q]);
+                for (int q = 0; q < 4; ++q)
+                    h[q] = flags & kMidStarts ? mid[q] : fma2(ex2_2(mul2(A2[q], pack(sd, sd))), h[q], mid[q]);
             }
         }
 
@@ -588,8 +589,8 @@ __global__ void __launch_bounds__(kThreads, S == 8 ? 2 : 3) scan_bwd_kernel(SsmS
                         else zero8(carry);
                     }
                     const float d = sh.d[k][ch], u = sh.u[k][ch], yb = sh.yb[k][ch];
-                    const float du = on ? d * u : 0.f, ybo = on ? yb : 0.f;
-                    const f2 yb2 = pack(yb, yb), dd = pack(d, d), du2 = pack(du, du), ybo2 = pack(ybo, ybo);
+                    const float du = d * u;  // (zeros, as yb, in a lane without a channel)
+                    const f2 yb2 = pack(yb, yb), dd = pack(d, d), du2 = pack(du, du);
                     f2 prev[4];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) prev[q] = i > 0 ? hs[i > 0 ? i - 1 : 0][q] : before[q];
@@ -613,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, S == 8 ? 2 : 3) scan_bwd_kernel(SsmS
                             q2 = fma2(ah, A2[x], q2);
                             yv = fma2(hs[i][x], cv, yv);
                             (e ? tb.y : tb.x) = mul2(dh, du2);
-                            (e ? tc.y : tc.x) = mul2(hs[i][x], ybo2);
+                            (e ? tc.y : tc.x) = mul2(hs[i][x], yb2);
                         }
                         *reinterpret_cast<ulonglong2*>(terms + q * LP * 4) = tb;
                         *reinterpret_cast<ulonglong2*>(terms + S + q * LP * 4) = tc;

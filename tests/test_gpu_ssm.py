@@ -347,3 +347,79 @@ def test_scan_captured_and_replayed_on_another_stream():
         graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(y, want) and torch.equal(s, ws) and all(torch.equal(g[k], wg[k]) for k in wg if wg[k] is not None)
+
+
+def test_scan_nan_and_infinity_stay_in_their_sequence():
+    """A sequence with NaN and infinite inputs in one chunk with others: theirs are as without it, bit for bit,
+    forwards and backwards (the sums over everything apart)."""
+    lengths, C = [40, 9, 50, 64, 37], 72
+    d = make((1, 200), C, 16, 1, F32, 998, True, True, True)
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lengths)]), dtype=torch.int32, device="cuda")
+    s0 = torch.randn(5, C, 16, generator=torch.Generator().manual_seed(5)).cuda()
+    dy = torch.randn(1, 200, C, generator=torch.Generator().manual_seed(6)).cuda()
+    kw = dict(D=d["D"], z=d["z"], delta_bias=d["bias"], initial_state=s0, cu_seqlens=cu)
+
+    def run(u, delta, grad):
+        y, s = kda.ssm_scan_fwd(u, delta, d["A"], d["B"], d["C"], **kw)
+        g = kda.ssm_scan_bwd(u, delta, d["A"], d["B"], d["C"], grad, dfinal_state=s0, **kw)
+        return y, s, g
+    y, s, g = run(d["u"], d["delta"], dy)
+    for at in (range(0, 40), range(40, 49), range(99, 163)):
+        u, delta, grad = d["u"].clone(), d["delta"].clone(), dy.clone()
+        t = at[len(at) // 2]
+        u[0, t, 3], delta[0, t, 4], grad[0, t, 5], delta[0, t, 6], u[0, t, 7] = (float("nan"),) * 3 + (float("inf"),) * 2
+        y2, s2, g2 = run(u, delta, grad)
+        n = [0, 40, 49, 99, 163].index(at[0])
+        others = torch.ones(200, dtype=torch.bool)
+        others[list(at)] = False
+        rest = [i for i in range(5) if i != n]
+        assert torch.equal(y[0, others], y2[0, others]) and torch.equal(s[rest], s2[rest])
+        for k in ("du", "ddelta", "dz", "dB", "dC"):
+            assert torch.equal(g[k][0, others], g2[k][0, others]), k
+        assert torch.equal(g["dinitial_state"][rest], g2["dinitial_state"][rest])
+        clean = [c for c in range(C) if c not in (3, 4, 5, 6, 7)]
+        assert torch.equal(y[0][:, clean], y2[0][:, clean]) and torch.equal(g["du"][0][:, clean], g2["du"][0][:, clean])
+
+
+def test_scan_many_short_sequences():
+    """More sequences than one round of the search for boundaries looks at."""
+    rng = np.random.default_rng(9)
+    lengths = rng.integers(0, 4, 3000)
+    T, C = int(lengths.sum()), 24
+    d = make((1, T), C, 8, 1, F32, 999, False, True, True)
+    cu = np.concatenate([[0], np.cumsum(lengths)])
+    s0 = torch.randn(3000, C, 8, generator=torch.Generator().manual_seed(7)).cuda()
+    dy = torch.randn(1, T, C, generator=torch.Generator().manual_seed(8)).cuda()
+    kw = dict(D=d["D"], delta_bias=d["bias"], initial_state=s0, cu_seqlens=torch.tensor(cu, dtype=torch.int32, device="cuda"))
+    y, s = kda.ssm_scan_fwd(d["u"], d["delta"], d["A"], d["B"], d["C"], **kw)
+    got = kda.ssm_scan_bwd(d["u"], d["delta"], d["A"], d["B"], d["C"], dy, **kw)
+    args = ref_args(dict(d, sp=True, s0=s0, cu=torch.tensor(cu)))
+    r = scan(*args, f64(dy)[0], None)
+    within(y[0], r["y"], 2.0 ** -18 * r["y_err"], F32)
+    within(s, r["state"], 2.0 ** -19 * r["state_err"], F32)
+    for k, n in (("du", 8), ("ddelta", 8), ("dB", C), ("dC", C), ("dinitial_state", 1), ("dA", T)):
+        within(got[k], r[k], (2.0 ** -19 + n * 2.0 ** -24) * r[k + "_err"], F32)
+
+
+def test_rows_far_apart():
+    """Rows whose offsets pass 2^31 elements, as slices of one wide buffer."""
+    T, C, wide = 2100, 40, (1 << 20) + 8
+    buf = torch.zeros(1, T, wide, dtype=BF16, device="cuda")
+    d = make((1, T), C, 8, 1, BF16, 1000, True, True, True)
+    v = lambda i: buf[:, :, i * 64:i * 64 + C]  # noqa: E731
+    for i, k in enumerate(("u", "delta", "z")):
+        v(i).copy_(d[k])
+    bc = buf[:, :, 512:528].unflatten(2, (2, 1, 8))
+    bc[:, :, 0].copy_(d["B"])
+    bc[:, :, 1].copy_(d["C"])
+    kw = dict(D=d["D"], delta_bias=d["bias"])
+    want, ws = kda.ssm_scan_fwd(d["u"], d["delta"], d["A"], d["B"].contiguous(), d["C"].contiguous(), z=d["z"], **kw)
+    y, s = kda.ssm_scan_fwd(v(0), v(1), d["A"], bc[:, :, 0], bc[:, :, 1], z=v(2), **kw)
+    assert torch.equal(y, want) and torch.equal(s, ws)
+    wg = kda.ssm_scan_bwd(d["u"], d["delta"], d["A"], d["B"].contiguous(), d["C"].contiguous(), want, z=d["z"], **kw)
+    g = kda.ssm_scan_bwd(v(0), v(1), d["A"], bc[:, :, 0], bc[:, :, 1], want, z=v(2), **kw)
+    assert all(torch.equal(g[k], wg[k]) for k in wg if wg[k] is not None)
+    w = torch.randn(C, 4, device="cuda")
+    assert torch.equal(kda.short_conv_fwd(v(0), w, conv_act=1)[0], kda.short_conv_fwd(d["u"], w, conv_act=1)[0])
+    a, b = kda.short_conv_bwd(v(0), w, want, conv_act=1), kda.short_conv_bwd(d["u"], w, want, conv_act=1)
+    assert torch.equal(a["dx"], b["dx"]) and torch.equal(a["dweight"], b["dweight"])

@@ -94,6 +94,7 @@ def test_ssm_step(lib):
                                 a["y"], a["st"], None)
     assert call(S=12) == UNSUPPORTED and call(S=128, ldb=256, ldc=256) == UNSUPPORTED and call(dt=5) == UNSUPPORTED
     assert call(G=3) == INVALID_ARG and call(G=0) == INVALID_ARG
+    assert call(N=1 << 30, P=1 << 30) == UNSUPPORTED         # more blocks than one launch has
     assert call(sp=2) == INVALID_ARG
     assert call(ldu=255) == INVALID_ARG and call(ldb=31) == INVALID_ARG and call(z=at(9), ldz=100) == INVALID_ARG
     assert call(A=at(3, 4)) == INVALID_ARG and call(s=at(6, 16)) == INVALID_ARG
@@ -174,6 +175,10 @@ def test_pages(lib):
     assert lib.kda_pages_alloc(at(1), 8, 4, at(1), None, None) == INVALID_ARG
     assert lib.kda_pages_alloc(at(1), 8, 4, at(2, 2), None, None) == INVALID_ARG
     assert lib.kda_pages_alloc(at(1), 8, 0, None, None, None) == 0
+    many = (1 << 30) + 1
+    assert lib.kda_pages_alloc(at(1), many, 4, at(9), None, None) == UNSUPPORTED
+    assert lib.kda_pages_alloc(at(1), 8, many, at(9), None, None) == UNSUPPORTED
+    assert lib.kda_pages_free(at(1), many, at(9), 3, None, None) == UNSUPPORTED
     assert lib.kda_pages_free(at(1), 8, None, 3, None, None) == INVALID_ARG
     assert lib.kda_pages_free(at(1), 8, at(1), 3, None, None) == INVALID_ARG
     assert lib.kda_pages_free(at(1), 8, at(2), 3, at(3, 2), None) == INVALID_ARG
@@ -185,7 +190,7 @@ def test_pages(lib):
         return lib.kda_pages_fork(a["t"], a["l"], a["S"], a["w"], a["pt"], a["r"], a["P"], a["p"], a["c"], a["n"], a["s"], a["d"],
                                   a["st"], None)
     assert fork(w=0) == INVALID_ARG and fork(pt=0) == INVALID_ARG and fork(n=-1) == INVALID_ARG
-    assert fork(n=65537) == UNSUPPORTED
+    assert fork(n=65537) == UNSUPPORTED and fork(P=many, r=at(20)) == UNSUPPORTED
     assert fork(t=None) == INVALID_ARG and fork(r=None) == INVALID_ARG and fork(p=None) == INVALID_ARG
     assert fork(s=at(7)) == INVALID_ARG and fork(l=at(2, 1)) == INVALID_ARG
     assert fork(n=0) == 0
@@ -198,7 +203,7 @@ def test_pages(lib):
         a.update(kw)
         return lib.kda_pages_compact(a["r"], a["P"], a["t"], a["e"], a["s"], a["d"], a["ws"], a["wsb"], a["st"], None)
     assert compact(t=None) == INVALID_ARG and compact(r=None) == INVALID_ARG and compact(s=None) == INVALID_ARG
-    assert compact(e=-1) == INVALID_ARG
+    assert compact(e=-1) == INVALID_ARG and compact(P=many) == UNSUPPORTED
     assert compact(wsb=need - 1) == WORKSPACE and compact(ws=None) == WORKSPACE
     assert compact(ws=at(5, 4)) == INVALID_ARG and compact(ws=at(1)) == INVALID_ARG
     assert compact(P=0, r=None, s=None, d=None, ws=None, wsb=0) == 0
@@ -211,7 +216,7 @@ def test_pages(lib):
         a = dict(p=at(1), P=100, b=64, s=at(2), d=at(3), n=300, ws=at(4), wsb=need, st=None)
         a.update(kw)
         return lib.kda_pages_copy(a["p"], a["P"], a["b"], a["s"], a["d"], a["n"], a["ws"], a["wsb"], a["st"], None)
-    assert copy(b=24) == UNSUPPORTED
+    assert copy(b=24) == UNSUPPORTED and copy(n=many) == UNSUPPORTED and copy(P=many) == UNSUPPORTED
     assert copy(b=0) == INVALID_ARG and copy(p=None) == INVALID_ARG and copy(p=at(1, 8)) == INVALID_ARG
     assert copy(s=None) == INVALID_ARG and copy(d=at(3, 1)) == INVALID_ARG
     assert copy(wsb=need - 1) == WORKSPACE and copy(ws=at(2)) == INVALID_ARG
