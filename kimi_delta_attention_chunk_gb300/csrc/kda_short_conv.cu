@@ -24,8 +24,8 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kSms = 152;
 // Blocks of an SM that the kernels are built for.  Five forwards (70k x 12288 in 565 us, 600 with four);
-// backwards the registers of a fifth would spill (4096 x 12288 in 82 us against 70).
-constexpr int kFwdResident = 5, kBwdResident = 4;
+// three backwards, with 168 registers a thread (4096 x 12288 in 68 us, 72 with four, 82 with five, which spill).
+constexpr int kFwdResident = 5, kBwdResident = 3;
 constexpr int kTile = 64;     // tokens of one look at the sequence boundaries
 // Asynchronous groups of a thread: one in use, one on its way.  (Three groups of eight rows measured 17%
 // slower backwards, two of four and two of sixteen as well.)
@@ -495,11 +495,13 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(ConvStepParams p) {
 }
 
 // Tokens of one run: as many runs as one filling of the machine holds, at least 32 tokens each so
-// that the W - 1 rows read twice stay below a tenth.
+// that the W - 1 rows read twice stay below a tenth; three fillings where the runs then still have 128
+// tokens, which evens out what blocks finish early (70k x 12288 forwards: 556 us against 566).
 int run_tokens(int total, int C, int vec, int resident) {
     const int blocks = (C + kThreads * vec - 1) / (kThreads * vec);
     const int runs = kSms * resident / blocks > 0 ? kSms * resident / blocks : 1;
-    int run = (total + runs - 1) / runs;
+    int run = total / runs + (total % runs != 0);
+    if (run >= 3 * 128) run = (run + 2) / 3;
     run = (run + 7) / 8 * 8;
     return run < 32 ? 32 : run;
 }
@@ -568,8 +570,10 @@ cudaError_t short_conv_fwd(kda_dtype dt, const ConvParams& p, cudaStream_t st) {
 }
 
 size_t short_conv_bwd_partial(int total, int C, int W) {
-    // the narrow variant has the fewer runs: more blocks along the channels
-    return (size_t)run_count(total, run_tokens(total, C, kBwdVec, kBwdResident)) * C * (W + 1);
+    // the runs of the wide and of the narrow variant: either may be the more
+    const int wide = run_count(total, run_tokens(total, C, kBwdVec, kBwdResident));
+    const int narrow = run_count(total, run_tokens(total, C, 1, kBwdResident));
+    return (size_t)(wide > narrow ? wide : narrow) * C * (W + 1);
 }
 
 cudaError_t short_conv_bwd(kda_dtype dt, kda_dtype gdt, const ConvParams& p, cudaStream_t st) {

@@ -224,3 +224,16 @@ def test_captured_and_replayed():
     torch.cuda.synchronize()
     assert torch.equal(y, want) and torch.equal(f, wf) and torch.equal(g["dx"], wg["dx"])
     assert torch.equal(g["dweight"], wg["dweight"])
+
+
+def test_many_channels_element_by_element():
+    """A channel count whose narrow runs are more than its wide ones: the workspace holds either."""
+    C, T = 228 * 512 - 1, 700
+    g = torch.Generator().manual_seed(330)
+    x, dy = torch.randn(1, T, C, generator=g).to(BF16).cuda(), torch.randn(1, T, C, generator=g).to(BF16).cuda()
+    w = torch.randn(C, 2, generator=g).cuda()
+    got = kda.short_conv_bwd(x, w, dy, conv_act=0)
+    prev = torch.cat([torch.zeros_like(x[:, :1]), x[:, :-1]], 1).double()
+    want = torch.stack([(dy.double() * prev).sum((0, 1)), (dy.double() * x.double()).sum((0, 1))], 1)
+    size = torch.stack([(dy.double() * prev).abs().sum((0, 1)), (dy.double() * x.double()).abs().sum((0, 1))], 1)
+    assert bool(((got["dweight"].double() - want).abs() <= T * 2.0 ** -24 * size).all())

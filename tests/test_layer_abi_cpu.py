@@ -51,6 +51,8 @@ def test_conv_bwd(lib):
     # two runs of 32 tokens: W + 1 sums a channel each
     assert need == 2 * 256 * 5 * 4
     assert lib.kda_short_conv_bwd_workspace_size(1, 64, 256, 5) == 0
+    # rows in 16-byte pieces: two runs; element by element: three, the more
+    assert lib.kda_short_conv_bwd_workspace_size(1, 700, 228 * 512, 4) == 3 * 228 * 512 * 5 * 4
     assert lib.kda_short_conv_bwd_workspace_size(1, -1, 256, 4) == 0
 
     def call(**kw):
