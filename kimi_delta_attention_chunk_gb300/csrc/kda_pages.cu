@@ -410,10 +410,11 @@ __global__ void __launch_bounds__(kCopyThreads, 8) pages_copy_few_kernel(char* p
     pairs[i] = me;
     __syncthreads();
     bool ok = me.x != -1;
-    for (int j = 0; j < n && ok; ++j) {
+#pragma unroll 8
+    for (int j = 0; j < n; ++j) {
         const int2 o = pairs[j];
         // a later pair writes this page, or a pair reads it: left alone
-        if (o.x == me.y || (j > i && o.y == me.y)) ok = false;
+        ok = ok && !(o.x == me.y || (j > i && o.y == me.y));
     }
     if (me.x != -1 && !ok) bad = true;
     if (bad && blockIdx.x == 0) report(status);

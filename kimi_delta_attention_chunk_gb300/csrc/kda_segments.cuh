@@ -51,12 +51,14 @@ struct SeqMap {
 // is the first / last of, or -1.  carry: the sequence that token t0 continues (-1: none), which
 // began at carry_start.  Behind the tile the sequence at hand runs on to token `until`: a tile
 // that ends before it has no boundary and needs no look.  plain: one sequence runs through the tile
-// and on.
+// and on.  marks: the tokens (bits) that are the first or last of a sequence.
 template <int TT>
 struct TokenTile {
     int start[TT], end[TT];
+    unsigned marks[2];
     int carry, carry_start, n0, until;
     bool plain;
+    static_assert(TT <= 64, "one bit a token");
 
     // Every thread of the block calls it; the block has to be past its last use of the tile.
     template <int NTH>
@@ -92,6 +94,18 @@ struct TokenTile {
             if (e - t0 <= TT) end[e - 1 - t0] = n;
         }
         __syncthreads();
+        if (tid < 64) {
+            const bool mark = tid < TT && (start[tid < TT ? tid : 0] >= 0 || end[tid < TT ? tid : 0] >= 0);
+            const unsigned b = __ballot_sync(0xffffffffu, mark);
+            if (tid % 32 == 0) marks[tid / 32] = b;
+        }
+        __syncthreads();
+    }
+
+    // Whether tokens k ... k + N - 1 of the tile (within a half of it) lie inside one sequence.
+    template <int N>
+    __device__ __forceinline__ bool clear(int k) const {
+        return (marks[k >> 5] >> (k & 31) & ((1u << N) - 1)) == 0;
     }
 };
 

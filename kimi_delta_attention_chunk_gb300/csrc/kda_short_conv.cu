@@ -211,7 +211,8 @@ __global__ void __launch_bounds__(kThreads, kFwdResident) conv_fwd_kernel(ConvPa
         copies_wait<kStages - 1>();
         if (!on) continue;
         const auto& rows = ring[(t - r0) / kBatch % kStages];
-        if (plain && t + kBatch <= r1) {
+        const int k0 = (t - r0) % kTile;
+        if (t + kBatch <= r1 && (plain || (t >= first && t + kBatch <= last && tile.template clear<kBatch>(k0)))) {
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
                 R in;
@@ -219,7 +220,6 @@ __global__ void __launch_bounds__(kThreads, kFwdResident) conv_fwd_kernel(ConvPa
                 row(t + i, in);
             }
         } else {
-            const int k0 = (t - r0) % kTile;
 #pragma unroll 1
             for (int i = 0; i < kBatch; ++i) {
                 if (t + i >= r1 || t + i >= last) break;
@@ -358,7 +358,9 @@ __global__ void __launch_bounds__(kThreads, kBwdResident) conv_bwd_kernel(ConvPa
         copies_wait<kStages - 1>();
         if (!on || done) continue;
         const int s = (t - r0) / kBatch % kStages;
-        if (plain && t + kBatch <= r1 && t - (W - 1) >= max(begin, r0)) {
+        const int k0 = (t - r0) % kTile;
+        if (t + kBatch <= r1 && t - (W - 1) >= max(begin, r0) &&
+            (plain || (seq >= 0 && t + kBatch <= last && tile.template clear<kBatch>(k0)))) {
             // every entry finished here is a token of the run
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
@@ -372,7 +374,6 @@ __global__ void __launch_bounds__(kThreads, kBwdResident) conv_bwd_kernel(ConvPa
                 shift<N2, W>(acc, zero);
             }
         } else {
-            const int k0 = (t - r0) % kTile;
 #pragma unroll 1
             for (int i = 0; i < kBatch; ++i) {
                 const int at = t + i;

@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 4) scan_kernel(SsmScanParams p, SeqM
                 }
             }
         };
-        const bool fast = plain && t + BATCH <= r1;
+        const bool fast = t + BATCH <= r1 && (plain || (t >= first && t + BATCH <= last && tile.template clear<BATCH>(k0)));
         if (fast) tokens(std::true_type{});
         else tokens(std::false_type{});
         if (kOutputs) {

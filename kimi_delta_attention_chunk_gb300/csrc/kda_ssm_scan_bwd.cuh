@@ -223,9 +223,9 @@ __global__ void __launch_bounds__(kSumThreads, 4) scan_bwd_sum_kernel(SsmScanPar
             }
             unpack(y2, yb[j], yb[j + 1]);
         }
-        // the batch's tokens; kAll: one sequence runs through the chunk
-        auto tokens = [&](auto all) {
-            constexpr bool kAll = decltype(all)::value;
+        // the batch's tokens; kAll: they lie inside one sequence, kCarries: the one at the chunk's first token
+        auto tokens = [&](auto all, auto carry) {
+            constexpr bool kAll = decltype(all)::value, kCarries = decltype(carry)::value;
 #pragma unroll
             for (int i = 0; i < BATCH; ++i) {
                 const int k = t - t0 + i;
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kSumThreads, 4) scan_bwd_sum_kernel(SsmScanPar
                     const f2 b = (j & 1) ? Bv[j / 2 * LPC].y : Bv[j / 2 * LPC].x;
                     const f2 a = ex2_2(mul2(dd, A2[j]));
                     h[j] = fma2(a, h[j], mul2(du2, b));
-                    if (kAll || carries) {
+                    if (kAll ? kCarries : carries) {
                         const f2 q = (j & 1) ? Cv[j / 2 * LPC].y : Cv[j / 2 * LPC].x;
                         P[j] = mul2(P[j], a);
                         G[j] = fma2(P[j], mul2(yb2, q), G[j]);
@@ -272,8 +272,10 @@ __global__ void __launch_bounds__(kSumThreads, 4) scan_bwd_sum_kernel(SsmScanPar
                 }
             }
         };
-        if (plain) tokens(std::true_type{});
-        else tokens(std::false_type{});
+        const bool fast = plain || (t >= first && t + BATCH <= min(t1, last) && sh.tile.template clear<BATCH>(t - t0));
+        if (!fast) tokens(std::false_type{}, std::false_type{});
+        else if (carries) tokens(std::true_type{}, std::true_type{});
+        else tokens(std::true_type{}, std::false_type{});
     }
     if (on) {
         store_from(h, w.state + slot * S + cs);
@@ -521,8 +523,7 @@ __global__ void __launch_bounds__(kThreads, S == 8 ? 2 : 3) scan_bwd_kernel(SsmS
             }
         }
 
-        auto walk = [&](auto all) {
-            constexpr bool kAll = decltype(all)::value;
+        {
             // token k forwards: h, and its decays in `a`
             auto forward = [&](int k, f2 (&a)[4]) {
                 const float d = sh.d[k][ch], du = d * sh.u[k][ch];
@@ -536,8 +537,23 @@ __global__ void __launch_bounds__(kThreads, S == 8 ? 2 : 3) scan_bwd_kernel(SsmS
                     h[2 * q + 1] = fma2(a[2 * q + 1], h[2 * q + 1], mul2(du2, B.y));
                 }
             };
-            auto inside = [&](int k) { return kAll || (th + k >= lo && th + k < hi); };
+            // a batch inside one sequence needs no look at its tokens
+            auto fast = [&](int b) {
+                return plain || (th + b * kBatch >= lo && th + (b + 1) * kBatch <= hi && sh.tile.template clear<kBatch>(b * kBatch));
+            };
+            auto inside = [&](int k) { return th + k >= lo && th + k < hi; };
             // forwards: the state before every batch
+            auto sweep = [&](int b, auto all) {
+                constexpr bool kAll = decltype(all)::value;
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const int k = b * kBatch + i;
+                    if (!kAll && !inside(k)) continue;
+                    if (!kAll && sh.tile.start[k] >= 0) initial_of(sh.tile.start[k], h);
+                    f2 a[4];
+                    forward(k, a);
+                }
+            };
 #pragma unroll 1
             for (int b = 0; b < kBatches; ++b) {
 #pragma unroll
@@ -548,19 +564,12 @@ __global__ void __launch_bounds__(kThreads, S == 8 ? 2 : 3) scan_bwd_kernel(SsmS
                     sh.kept[b][q][tid] = x;
                 }
                 if (b + 1 == kBatches) break;
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    const int k = b * kBatch + i;
-                    if (!inside(k)) continue;
-                    if (!kAll && sh.tile.start[k] >= 0) initial_of(sh.tile.start[k], h);
-                    f2 a[4];
-                    forward(k, a);
-                }
+                if (fast(b)) sweep(b, std::true_type{});
+                else sweep(b, std::false_type{});
             }
             // backwards
-#pragma unroll 1
-            for (int b = kBatches - 1; b >= 0; --b) {
-                if (!kAll && (th + b * kBatch >= hi || th + (b + 1) * kBatch <= lo)) continue;
+            auto back = [&](int b, auto all) {
+                constexpr bool kAll = decltype(all)::value;
                 f2 hs[kBatch][4], as[kBatch][4], before[4];
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
@@ -572,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, S == 8 ? 2 : 3) scan_bwd_kernel(SsmS
                 for (int i = 0; i < kBatch; ++i) {
                     const int k = b * kBatch + i;
                     zero8(as[i]);
-                    if (inside(k)) {
+                    if (kAll || inside(k)) {
                         if (!kAll && sh.tile.start[k] >= 0) initial_of(sh.tile.start[k], h);
                         forward(k, as[i]);
                     }
@@ -582,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, S == 8 ? 2 : 3) scan_bwd_kernel(SsmS
 #pragma unroll
                 for (int i = kBatch - 1; i >= 0; --i) {
                     const int k = b * kBatch + i;
-                    if (!inside(k)) continue;
+                    if (!kAll && !inside(k)) continue;
                     const int start = kAll ? -1 : sh.tile.start[k], end = kAll ? -1 : sh.tile.end[k];
                     if (end >= 0) {
                         if (p.dfinal) load8(p.dfinal + (int64_t)end * p.C * S + cs, carry);
@@ -655,6 +664,12 @@ __global__ void __launch_bounds__(kThreads, S == 8 ? 2 : 3) scan_bwd_kernel(SsmS
                     }
                     __syncwarp();
                 }
+            };
+#pragma unroll 1
+            for (int b = kBatches - 1; b >= 0; --b) {
+                if (th + b * kBatch >= hi || th + (b + 1) * kBatch <= lo) continue;
+                if (fast(b)) back(b, std::true_type{});
+                else back(b, std::false_type{});
                 __syncthreads();  // (the other half of `red` takes the next batch meanwhile)
                 for (int e = tid; e < kBatch * 2 * S; e += kThreads) {
                     const int i = e / (2 * S), x = e % (2 * S), t = th + b * kBatch + i;
@@ -665,9 +680,7 @@ __global__ void __launch_bounds__(kThreads, S == 8 ? 2 : 3) scan_bwd_kernel(SsmS
                     w.dBC[((int64_t)blockIdx.x * m.total + t) * 2 * S + x] = a;
                 }
             }
-        };
-        if (plain) walk(std::true_type{});
-        else walk(std::false_type{});
+        }
 
         // outputs of the half, as the inputs came
 #pragma unroll 1
