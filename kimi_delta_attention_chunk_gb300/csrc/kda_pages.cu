@@ -22,7 +22,8 @@ namespace cg = cooperative_groups;
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMostBlocks = 8;
-// One block counts this many pages at least as fast as a cluster starts and meets.
+// One block counts this many pages as fast as a cluster starts and meets: compaction of 8192 pages takes 10 us
+// either way, 16384 take 14 in one block and 10 in a cluster, 32768 take 23 and 10.5.
 constexpr int kPagesOfOneBlock = 8192;
 
 // Sum of x over the block's threads before this one; *all: over all of them.  `tmp` holds
@@ -81,21 +82,34 @@ __device__ __forceinline__ void cluster_sums(Shared& sh, int c0, int c1, int (&b
     cl.sync();  // before anyone writes `mine` again or leaves
 }
 
-// The block's share [lo, hi) of n things, whole tiles of kThreads.
+constexpr int kEach = 4;                  // neighbouring things a thread looks at
+constexpr int kTile = kThreads * kEach;
+
+// The block's share [lo, hi) of n things, whole tiles.
 __device__ __forceinline__ void share(int n, int& lo, int& hi) {
     cg::cluster_group cl = cg::this_cluster();
-    const int blocks = cl.num_blocks(), tiles = (n - 1) / kThreads + 1;
-    const int per = n > 0 ? (tiles + blocks - 1) / blocks : 0;
-    const int64_t a = (int64_t)cl.block_rank() * per * kThreads;
+    const int blocks = cl.num_blocks(), tiles = n > 0 ? (n - 1) / kTile + 1 : 0;
+    const int per = (tiles + blocks - 1) / blocks;
+    const int64_t a = (int64_t)cl.block_rank() * per * kTile;
     lo = (int)min(a, (int64_t)n);
-    hi = (int)min(a + (int64_t)per * kThreads, (int64_t)n);
+    hi = (int)min(a + (int64_t)per * kTile, (int64_t)n);
+}
+
+// Bit k: whether thing i + k of [lo, hi) satisfies f; the loads are independent of one another.
+template <typename F>
+__device__ __forceinline__ int which_of(int i, int hi, F f) {
+    int bits = 0;
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) bits |= (i + k < hi && f(i + k) ? 1 : 0) << k;
+    return bits;
 }
 
 // How many of [lo, hi) satisfy f (every thread gets the sum).
 template <typename F>
 __device__ __forceinline__ int count_if(Shared& sh, int lo, int hi, F f) {
     int c = 0;
-    for (int i = lo + (int)threadIdx.x; i < hi; i += kThreads) c += f(i) ? 1 : 0;
+#pragma unroll 4
+    for (int64_t i = lo + (int)threadIdx.x * kEach; i < hi; i += kTile) c += __popc(which_of((int)i, hi, f));
     int all;
     block_before(c, sh.tmp, &all);
     __syncthreads();
@@ -106,12 +120,11 @@ __device__ __forceinline__ int count_if(Shared& sh, int lo, int hi, F f) {
 // stops where the ranks reach `most`.
 template <typename F, typename G>
 __device__ __forceinline__ void place_if(Shared& sh, int lo, int hi, int base, int most, F f, G put) {
-    for (int i0 = lo; i0 < hi && base < most; i0 += kThreads) {
-        const int i = i0 + threadIdx.x;
-        const bool is = i < hi && f(i);
-        int all;
-        const int before = block_before(is ? 1 : 0, sh.tmp, &all);
-        if (is && base + before < most) put(base + before, i);
+    for (int64_t i0 = lo; i0 < hi && base < most; i0 += kTile) {
+        const int i = (int)i0 + (int)threadIdx.x * kEach;
+        int bits = which_of(i, hi, f), all;
+        int rank = base + block_before(__popc(bits), sh.tmp, &all);
+        for (; bits && rank < most; bits &= bits - 1) put(rank++, i + __ffs(bits) - 1);
         base += all;
         __syncthreads();
     }
@@ -301,11 +314,16 @@ __global__ void __launch_bounds__(kThreads) pages_compact_kernel(int32_t* refs, 
     const int live = all[0];
     const auto hole = [&](int i) { return i < live && refs[i] == 0; };
     const auto tail = [&](int i) { return i >= live && refs[i] != 0; };
-    const int holes = count_if(sh, lo, hi, hole), tails = count_if(sh, lo, hi, tail);
+    // a share on one side of `live` has been counted already
+    int holes = hi <= live ? hi - lo - used_here : 0, tails = lo >= live ? used_here : 0;
+    if (lo < live && live < hi) {
+        holes = count_if(sh, lo, hi, hole);
+        tails = count_if(sh, lo, hi, tail);
+    }
     cluster_sums(sh, holes, tails, base, all);
     const int moves = all[0];  // as many used pages behind `live` as holes before it
-    place_if(sh, lo, hi, base[0], moves, hole, [&](int rank, int i) { dst_out[rank] = i; });
-    place_if(sh, lo, hi, base[1], moves, tail, [&](int rank, int i) { src_out[rank] = i; });
+    place_if(sh, lo, min(hi, live), base[0], moves, hole, [&](int rank, int i) { dst_out[rank] = i; });
+    place_if(sh, max(lo, min(live, hi)), hi, base[1], moves, tail, [&](int rank, int i) { src_out[rank] = i; });
     if (remap) {
         for (int i = max(lo, live) + (int)threadIdx.x; i < hi; i += kThreads)
             if (refs[i] == 0) remap[1 + i] = -1;
@@ -391,13 +409,15 @@ __global__ void __launch_bounds__(kCopyThreads, 8) pages_copy_kernel(char* pool,
     }
 }
 
-// Up to kCopyThreads pairs: every block looks all of them over by itself (a thread holds its pair against
-// the others in shared memory, about a microsecond) and needs no marks.
+// Up to kFewPairs pairs: every block looks all of them over by itself (two threads hold a pair against half of
+// the others each) and needs no marks.  128 pairs take about 3 us this way and 5 with the marks, 256 took 7.
+constexpr int kFewPairs = kCopyThreads / 2;
 __global__ void __launch_bounds__(kCopyThreads, 8) pages_copy_few_kernel(char* pool, int64_t page_bytes, const int32_t* src,
                                                                          const int32_t* dst, int n, int P, int32_t* status) {
-    __shared__ int2 pairs[kCopyThreads], good[kCopyThreads];
-    __shared__ int counts[kCopyThreads / 32];
-    const int i = threadIdx.x, lane = i & 31, warp = i >> 5;
+    __shared__ __align__(16) int2 pairs[kFewPairs];
+    __shared__ int2 good[kFewPairs];
+    __shared__ int counts[kFewPairs / 32], against_first[kFewPairs];
+    const int i = threadIdx.x % kFewPairs, part = threadIdx.x / kFewPairs, lane = i & 31, warp = i >> 5;
     int2 me = i < n ? make_int2(src[i], dst[i]) : make_int2(-1, -1);
     bool bad = false;
     if (me.x == -1 || me.y == -1 || me.x == me.y) {
@@ -407,22 +427,26 @@ __global__ void __launch_bounds__(kCopyThreads, 8) pages_copy_few_kernel(char* p
         bad = true;
         me = make_int2(-1, -1);
     }
-    pairs[i] = me;
+    if (part == 0) pairs[i] = me;
     __syncthreads();
-    bool ok = me.x != -1;
-#pragma unroll 8
-    for (int j = 0; j < n; ++j) {
-        const int2 o = pairs[j];
-        // a later pair writes this page, or a pair reads it: left alone
-        ok = ok && !(o.x == me.y || (j > i && o.y == me.y));
+    // a later pair writes this page, or a pair reads it: left alone
+    int against = 0;
+    const int4* two = reinterpret_cast<const int4*>(pairs);
+#pragma unroll 4
+    for (int j = part * kFewPairs / 4; j < (part + 1) * kFewPairs / 4; ++j) {
+        const int4 o = two[j];
+        against |= (o.x == me.y) | (o.z == me.y) | ((o.y == me.y) & (2 * j > i)) | ((o.w == me.y) & (2 * j + 1 > i));
     }
+    if (part == 0) against_first[i] = against;
+    __syncthreads();
+    const bool ok = part == 1 && me.x != -1 && !(against | against_first[i]);
     if (me.x != -1 && !ok) bad = true;
-    if (bad && blockIdx.x == 0) report(status);
+    if (bad && part == 1 && blockIdx.x == 0) report(status);
     const unsigned votes = __ballot_sync(0xffffffffu, ok);
-    if (lane == 0) counts[warp] = __popc(votes);
+    if (part == 1 && lane == 0) counts[warp] = __popc(votes);
     __syncthreads();
     int before = __popc(votes & ((1u << lane) - 1)), all = 0;
-    for (int w = 0; w < kCopyThreads / 32; ++w) {
+    for (int w = 0; w < kFewPairs / 32; ++w) {
         if (w < warp) before += counts[w];
         all += counts[w];
     }
@@ -487,13 +511,13 @@ cudaError_t pages_compact(int32_t* refs, int P, int32_t* tables, int64_t entries
     return cudaGetLastError();
 }
 
-size_t pages_copy_workspace(int P, int n) { return n <= kCopyThreads ? 0 : (1 + 2 * (size_t)P + n) * 4; }
+size_t pages_copy_workspace(int P, int n) { return n <= kFewPairs ? 0 : (1 + 2 * (size_t)P + n) * 4; }
 
 cudaError_t pages_copy(void* pool, int P, int64_t page_bytes, const int32_t* src, const int32_t* dst, int n, void* ws,
                        int32_t* status, cudaStream_t st) {
     const int64_t items = n * ((page_bytes + kCopyPiece - 1) / kCopyPiece);
     const unsigned grid = (unsigned)(items < kCopySms * 8 ? items : kCopySms * 8);
-    if (n <= kCopyThreads) {
+    if (n <= kFewPairs) {
         pages_copy_few_kernel<<<grid, kCopyThreads, 0, st>>>(static_cast<char*>(pool), page_bytes, src, dst, n, P, status);
         return cudaGetLastError();
     }

@@ -144,7 +144,7 @@ def test_compact_without_tables_and_with_stale_entries():
 
 @pytest.mark.parametrize("dtype,page", [(torch.float32, (4,)), (torch.bfloat16, (3, 8)), (torch.float32, (2, 64, 66)), (torch.uint8, (48,)),
                                         (torch.bfloat16, (5, 4100, 2))])
-@pytest.mark.parametrize("P,n", [(2, 1), (40, 25), (200, 300)])
+@pytest.mark.parametrize("P,n", [(2, 1), (40, 25), (200, 300), (150, 128), (150, 129), (400, 127)])
 def test_copy(P, n, dtype, page):
     rng = np.random.default_rng(P + n)
     pool = torch.randint(0, 100, (P,) + page, generator=torch.Generator().manual_seed(P)).to(dtype)

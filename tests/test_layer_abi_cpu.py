@@ -212,7 +212,7 @@ def test_pages(lib):
 
     need = lib.kda_pages_copy_workspace_size(100, 300)
     assert need == (1 + 200 + 300) * 4 and lib.kda_pages_copy_workspace_size(100, 0) == 0
-    assert lib.kda_pages_copy_workspace_size(100, 256) == 0      # few pairs need none
+    assert lib.kda_pages_copy_workspace_size(100, 128) == 0      # few pairs need none
 
     def copy(**kw):
         a = dict(p=at(1), P=100, b=64, s=at(2), d=at(3), n=300, ws=at(4), wsb=need, st=None)
