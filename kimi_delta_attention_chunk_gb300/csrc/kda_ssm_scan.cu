@@ -364,7 +364,11 @@ Plan plan(const SsmScanParams& p) {
     const int want = 4 * kSms / q.blocks > 0 ? 4 * kSms / q.blocks : 1;
     int run = (p.total + want - 1) / want;
     run = (run + kRunStep - 1) / kRunStep * kRunStep;
-    if (run < 64) run = 64;
+    // A token takes 0.3 us where a block has its SM to itself, and two more launches 10 us: 64 tokens are not cut
+    // (15.5 us; cut in two, 18.5), 65 to 2048 into runs of 32 at least (4096 channels, 128 tokens: 19 us, with runs
+    // of 64 28, of 128 27).  Beyond, the prefix over many runs costs more (4096 tokens of 512 channels: 41 us
+    // with runs of 32, 38 of 64).
+    if (run < 64 && (p.total <= 64 || p.total > 2048)) run = 64;
     q.run = run;
     q.runs = p.total > 0 ? (p.total + run - 1) / run : 1;
     q.split = q.runs > 1;
