@@ -26,7 +26,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kSms = 152;
-constexpr int kRunStep = 32;  // runs are whole steps of tokens
+constexpr int kRunStep = 16;  // runs are whole tiles
 
 // Tokens whose rows are in shared memory at a time: 16 bf16 rows of a warp's 32 channels (32 rows leave fewer
 // blocks an SM: 16384 x 4096 x 16 in 600 us against 547).
@@ -364,11 +364,15 @@ Plan plan(const SsmScanParams& p) {
     const int want = 4 * kSms / q.blocks > 0 ? 4 * kSms / q.blocks : 1;
     int run = (p.total + want - 1) / want;
     run = (run + kRunStep - 1) / kRunStep * kRunStep;
-    // A token takes 0.3 us where a block has its SM to itself, and two more launches 10 us: 64 tokens are not cut
-    // (15.5 us; cut in two, 18.5), 65 to 2048 into runs of 32 at least (4096 channels, 128 tokens: 19 us, with runs
-    // of 64 28, of 128 27).  Beyond, the prefix over many runs costs more (4096 tokens of 512 channels: 41 us
-    // with runs of 32, 38 of 64).
-    if (run < 64 && (p.total <= 64 || p.total > 2048)) run = 64;
+    // The prefix takes longer the more runs there are: 4096 tokens of 128 channels, S = 16, 29 us with 96 runs, 32
+    // with 64 and 37 with 256; 16384 of 512 channels 101, 107 and 90.
+    constexpr int kMostRuns = 96;
+    const int least = (p.total + kMostRuns - 1) / kMostRuns;
+    if (run < least) run = (least + kRunStep - 1) / kRunStep * kRunStep;
+    // A token takes 0.2 us where a block has its SM to itself, and two more launches cost 6: 64 tokens take 15 us uncut
+    // and 13 to 20 cut, 96 of 512 channels 21 and 13.  With more blocks the runs get in one another's way: 96
+    // tokens of 4096 channels, S = 64, 22 us and 26.
+    if (p.total <= 64 || p.total <= 40 + q.blocks / 2) run = (p.total + kRunStep - 1) / kRunStep * kRunStep;
     q.run = run;
     q.runs = p.total > 0 ? (p.total + run - 1) / run : 1;
     q.split = q.runs > 1;
