@@ -545,7 +545,7 @@ KDA_API kda_status kda_short_conv_bwd(const void *x, int64_t ldx, const float *w
  * kda_short_conv_step -- one token of each of N sequences: y [N, C] from x [N, C] (rows
  * ldx apart) and the histories in the pool `history` [P, W-1, C], which move on by one
  * token.  slots [N] and status as kda_recurrent_step_slots; slots NULL: row i works on
- * page i (P >= N).
+ * page i (P >= N).  N <= 2^30.
  */
 KDA_API kda_status kda_short_conv_step(const void *x, int64_t ldx, const float *weight, const float *bias,
                                int conv_act, kda_dtype dtype, void *history, const int32_t *slots, int P,
@@ -564,7 +564,7 @@ KDA_API kda_status kda_short_conv_step(const void *x, int64_t ldx, const float *
  *  softplus 0 or 1.
  *  state  fp32 pool [P, C, S], 32-byte aligned, updated in place; slots, P, status as
  *         kda_short_conv_step.
- * S in {8, 16, 32, 64}; C a multiple of G, C <= 2^20.
+ * S in {8, 16, 32, 64}; C a multiple of G, C <= 2^20; N <= 2^30, and N C S / 1024 < 2^31.
  */
 KDA_API kda_status kda_ssm_step(const void *u, int64_t ldu, const void *delta, int64_t ldd, const float *A,
                         const void *Bm, int64_t ldb, const void *Cm, int64_t ldc, const float *D,

@@ -4,7 +4,7 @@
 // refs[p] counts the page table entries that hold page p; a page with none is free, and the lowest
 // free pages are given out first, so every result is a function of the arguments alone.  The
 // bookkeeping is integers: one read of refs and of the table rows concerned.  It is bound by
-// latency, so each operation is one kernel of one cluster (eight blocks when there are many pages,
+// latency, so each operation is one kernel of one cluster (eight blocks when there are many pages or forks,
 // else one): the blocks count their share of refs, exchange the counts through distributed shared
 // memory, and place their own pages, with hardware cluster barriers between and no waiting on
 // memory.  The payload moves in kda_pages_copy, bound by HBM.
@@ -182,6 +182,45 @@ __global__ void __launch_bounds__(256) pages_free_kernel(int32_t* refs, int P, c
 // What becomes of request k, kept in dst_out[k] between the phases.
 constexpr int kNeedsPage = 2, kSharesOnly = 1, kNothing = 0;
 constexpr int kRefused = -2;
+// One block writes this many children's rows as fast as a cluster: 64 rows of 16 to 256 entries take 9 to 16 us in one
+// block and 10 to 16 in a cluster, 128 rows 14 to 22 and 11 to 15, 65536 rows of 64 entries 4000 and 670.
+constexpr int kForksOfOneBlock = 64;
+// Every pair of this many requests is compared (256 requests take 12 us, 13 by chains); more go by chains (1024 take
+// 63 us by pairs, 23 by chains, 65536 114 ms and 0.7).
+constexpr int kFewForks = 256;
+
+// Sets kConflict in next[k] of every request k whose child is another request's child or any request's parent, in
+// time linear in n: requests are chained by a hash of their child, head[n] holding the first of each chain and
+// next[k] & kNext the one behind k, both plus one.  A look along a chain ends at the first request of the child it
+// looks for, so that many requests of one child cost no more.
+constexpr int kNext = 0xfffff, kConflict = 1 << 30;
+__device__ __forceinline__ void find_conflicts(const int32_t* parents, const int32_t* children, int n, int32_t* head,
+                                               int32_t* next) {
+    cg::cluster_group cl = cg::this_cluster();
+    const int first = cl.block_rank() * kThreads + threadIdx.x, step = cl.num_blocks() * kThreads;
+    const auto chain = [&](int c) { return (int)__umulhi((unsigned)c * 2654435769u, (unsigned)n); };
+    // the first request other than k whose child is c
+    const auto other = [&](int c, int k) {
+        int j = head[chain(c)] - 1;
+        while (j >= 0 && (j == k || children[j] != c)) j = (next[j] & kNext) - 1;
+        return j;
+    };
+    for (int i = first; i < n; i += step) head[i] = 0;
+    cl.sync();
+    for (int k = first; k < n; k += step) {
+        const int c = children[k];
+        next[k] = c != -1 && parents[k] != -1 ? atomicExch(head + chain(c), k + 1) : 0;
+    }
+    cl.sync();
+    for (int k = first; k < n; k += step) {
+        const int p = parents[k], c = children[k];
+        if (p == -1 || c == -1) continue;
+        if (other(c, k) >= 0) atomicOr(next + k, kConflict);
+        const int j = other(p, -1);  // (if it is not the only one of its child, all of them have the flag)
+        if (j >= 0) atomicOr(next + j, kConflict);
+    }
+    cl.sync();
+}
 
 __global__ void __launch_bounds__(kThreads) pages_fork_kernel(int32_t* tables, int32_t* lens, int S, int width,
                                                               int page_tokens, int32_t* refs, int P,
@@ -193,16 +232,23 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(int32_t* tables, i
     const int warp = cl.block_rank() * kWarps + (threadIdx.x >> 5), warps = cl.num_blocks() * kWarps;
 
     // 1. which requests stand: a warp looks each over
+    const bool few = n <= kFewForks;
+    if (!few) find_conflicts(parents, children, n, src_out, dst_out);
     for (int k = warp; k < n; k += warps) {
         const int p = parents[k], c = children[k];
         int what = kNothing;
         if (p != -1 && c != -1) {
             bool bad = p < 0 || p >= S || c < 0 || c >= S;
-            for (int j = lane; j < n && !bad; j += 32) {
-                const int pj = parents[j], cj = children[j];
-                if (pj != -1 && cj != -1 && (pj == c || (j != k && cj == c))) bad = true;
+            if (few) {
+                for (int j = lane; j < n && !bad; j += 32) {
+                    const int pj = parents[j], cj = children[j];
+                    if (pj != -1 && cj != -1 && (pj == c || (j != k && cj == c))) bad = true;
+                }
+                bad = __any_sync(0xffffffffu, bad);
+            } else {
+                bad |= (dst_out[k] & kConflict) != 0;
+                __syncwarp();
             }
-            bad = __any_sync(0xffffffffu, bad);
             int full = 0;
             bool part = false;
             if (!bad) {
@@ -386,7 +432,7 @@ __global__ void __launch_bounds__(256) pages_mark_kernel(const int32_t* src, con
         }
         if (s == d) continue;
         atomicMax(marks + 1 + d, i + 1);
-        marks[1 + P + s] = 1;
+        marks[1 + (int64_t)P + s] = 1;
         marks[1 + 2 * (int64_t)P + atomicAdd(marks, 1)] = i;
     }
 }
@@ -401,7 +447,7 @@ __global__ void __launch_bounds__(kCopyThreads, 8) pages_copy_kernel(char* pool,
         const int64_t at = it % pieces * kCopyPiece;
         const int s = src[i], d = dst[i];
         // a later pair writes this page, or a pair reads it: left alone
-        if (marks[1 + d] != i + 1 || marks[1 + P + d] != 0) {
+        if (marks[1 + d] != i + 1 || marks[1 + (int64_t)P + d] != 0) {
             if (threadIdx.x == 0 && at == 0) report(status);
             continue;
         }
@@ -460,8 +506,8 @@ __global__ void __launch_bounds__(kCopyThreads, 8) pages_copy_few_kernel(char* p
 }
 
 template <typename... KArgs, typename... Args>
-cudaError_t launch_cluster(void (*kern)(KArgs...), int P, cudaStream_t st, Args... args) {
-    if (P <= kPagesOfOneBlock) {  // a cluster of one, without the cost of asking for it
+cudaError_t launch_cluster(void (*kern)(KArgs...), bool many, cudaStream_t st, Args... args) {
+    if (!many) {  // a cluster of one, without the cost of asking for it
         kern<<<1, kThreads, 0, st>>>(static_cast<KArgs>(args)...);
         return cudaGetLastError();
     }
@@ -482,7 +528,7 @@ cudaError_t launch_cluster(void (*kern)(KArgs...), int P, cudaStream_t st, Args.
 }  // namespace
 
 cudaError_t pages_alloc(int32_t* refs, int P, int n, int32_t* out, int32_t* status, cudaStream_t st) {
-    return launch_cluster(pages_alloc_kernel, P, st, refs, P, n, out, status);
+    return launch_cluster(pages_alloc_kernel, P > kPagesOfOneBlock, st, refs, P, n, out, status);
 }
 
 cudaError_t pages_free(int32_t* refs, int P, const int32_t* pages, int64_t n, int32_t* status, cudaStream_t st) {
@@ -494,8 +540,8 @@ cudaError_t pages_free(int32_t* refs, int P, const int32_t* pages, int64_t n, in
 cudaError_t pages_fork(int32_t* tables, int32_t* lens, int S, int width, int page_tokens, int32_t* refs, int P,
                        const int32_t* parents, const int32_t* children, int n, int32_t* src, int32_t* dst,
                        int32_t* status, cudaStream_t st) {
-    return launch_cluster(pages_fork_kernel, P, st, tables, lens, S, width, page_tokens, refs, P, parents, children, n,
-                          src, dst, status);
+    return launch_cluster(pages_fork_kernel, P > kPagesOfOneBlock || n > kForksOfOneBlock, st, tables, lens, S, width,
+                          page_tokens, refs, P, parents, children, n, src, dst, status);
 }
 
 size_t pages_compact_workspace(int P) { return ((size_t)P + 1) * 4; }
@@ -504,7 +550,8 @@ cudaError_t pages_compact(int32_t* refs, int P, int32_t* tables, int64_t entries
                           int32_t* status, cudaStream_t st) {
     int32_t* remap = entries > 0 ? static_cast<int32_t*>(ws) : nullptr;
     const bool one = entries <= kEntriesOfCluster;
-    cudaError_t e = launch_cluster(pages_compact_kernel, P, st, refs, P, src, dst, remap, tables, one ? (int)entries : 0, status);
+    cudaError_t e = launch_cluster(pages_compact_kernel, P > kPagesOfOneBlock, st, refs, P, src, dst, remap, tables,
+                                   one ? (int)entries : 0, status);
     if (e != cudaSuccess || one) return e;
     const int64_t blocks = (entries + 255) / 256;
     pages_remap_kernel<<<(unsigned)(blocks < 1216 ? blocks : 1216), 256, 0, st>>>(tables, entries, P, remap, status);

@@ -81,6 +81,35 @@ def test_fork(S, width, tokens, P, busy, n):
     assert int(st) == (5 if refused else 0)
 
 
+@pytest.mark.parametrize("n", [64, 65, 256, 257, 900])
+@pytest.mark.parametrize("same", [False, True])
+def test_forks_in_conflict(n, same):
+    """Children listed twice, children that are parents, skipped requests and rows out of range among many; `same`: one
+    child for most requests."""
+    rng = np.random.default_rng(n)
+    S, width, tokens, P = 1200, 3, 16, 2000
+    tables, lens, refs = sequences(rng, S, width, tokens, P, 500)
+    order = np.argsort(lens == 0, kind="stable")
+    parents, children = order[rng.integers(0, 500, n)], order[500 + rng.permutation(S - 500)[:n] if n <= S - 500 else 500 + rng.integers(0, S - 500, n)]
+    children[rng.random(n) < (0.6 if same else 0.0)] = order[700]
+    for what, at in (("twice", rng.random(n) < 0.1), ("parent", rng.random(n) < 0.05), ("child", rng.random(n) < 0.05)):
+        other = rng.integers(0, n, n)
+        if what == "twice":
+            children[at] = children[other[at]]
+        elif what == "parent":
+            children[at] = parents[other[at]]
+        else:
+            parents[at] = children[other[at]]
+    parents[rng.random(n) < 0.05], children[rng.random(n) < 0.05] = -1, -1
+    parents[rng.random(n) < 0.02], children[rng.random(n) < 0.02] = S, -7
+    books = Books(refs, tables, lens)
+    t, l, r, st = dev(tables), dev(lens), dev(refs), word()
+    src, dst = kda.pages_fork(t, l, r, dev(parents), dev(children), tokens, status=st)
+    ws, wd, refused = books.fork([int(p) for p in parents], [int(c) for c in children], tokens)
+    assert refused and src.tolist() == ws and dst.tolist() == wd
+    assert t.tolist() == books.tables and l.tolist() == books.lens and r.tolist() == books.refs and int(st) == 5
+
+
 def test_fork_refuses():
     tokens, P = 16, 12
     tables = np.full((8, 3), -1)
@@ -175,6 +204,34 @@ def test_pages_past_four_gigabytes():
     pool[70], pool[1] = 3.0, 1.0
     kda.pages_copy(pool, dev([70, 1]), dev([69, 71]))
     assert bool((pool[69] == 3).all()) and bool((pool[71] == 1).all())
+
+
+def test_copy_in_the_largest_pool():
+    """The last pages of 2^30 pages of 16 bytes, by few pairs and by marks."""
+    P = 2 ** 30
+    pool = torch.empty(P, 4, dtype=torch.int32, device="cuda")
+    for n in (3, 200):
+        pool[-n - 2:] = torch.arange(n + 2, dtype=torch.int32, device="cuda")[:, None]
+        src, dst, st = dev([P - 1] * n), dev(range(P - n - 2, P - 2)), word()
+        kda.pages_copy(pool, src, dst, status=st)
+        assert int(st) == 0 and bool((pool[-n - 2:-2] == n + 1).all()) and int(pool[-2, 0]) == n
+        kda.pages_copy(pool, dev([0] * (n - 1) + [P - 1]), dev([P - 1] * n), status=st)     # written again and again, and onto itself
+        assert int(st) == 5 and bool((pool[-1] == pool[0]).all())          # the last that writes it (its own pair is none)
+
+
+def test_many_forks():
+    """More requests than one block looks over, of a small pool's full pages."""
+    for n in (300, 9000, 65536):
+        tables = torch.full((n + 1, 3), -1, dtype=torch.int32, device="cuda")
+        tables[0] = dev([2, 1, 3])
+        lens, refs, st = torch.zeros(n + 1, dtype=torch.int32, device="cuda"), dev([0, 1, 1, 1]), word()
+        lens[0] = 48
+        children = torch.randperm(n, generator=torch.Generator().manual_seed(n)).to(torch.int32).cuda() + 1
+        children[n // 2] = children[n // 3]
+        src, dst = kda.pages_fork(tables, lens, refs, torch.zeros_like(children), children, 16, status=st)
+        assert int(st) == 5 and bool((src == -1).all()) and bool((dst == -1).all())
+        made = (tables[1:] == tables[0]).all(1)
+        assert int(made.sum()) == n - 2 and refs.tolist() == [0] + [n - 1] * 3 and int((lens == 48).sum()) == n - 1
 
 
 def test_books_in_a_graph():

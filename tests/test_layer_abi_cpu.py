@@ -80,6 +80,7 @@ def test_conv_step(lib):
                                        a["C"], a["W"], a["y"], a["st"], None)
     assert call(dt=7) == UNSUPPORTED and call(W=8) == UNSUPPORTED
     assert call(N=-1) == INVALID_ARG and call(P=0) == INVALID_ARG and call(C=-4) == INVALID_ARG
+    assert call(N=(1 << 30) + 1) == UNSUPPORTED
     assert call(sl=None, N=9) == INVALID_ARG                 # more rows than pages
     assert call(sl=at(4, 1)) == INVALID_ARG and call(st=at(6, 3)) == INVALID_ARG
     assert call(h=None) == INVALID_ARG and call(y=at(3)) == INVALID_ARG
@@ -97,6 +98,7 @@ def test_ssm_step(lib):
     assert call(S=12) == UNSUPPORTED and call(S=128, ldb=256, ldc=256) == UNSUPPORTED and call(dt=5) == UNSUPPORTED
     assert call(G=3) == INVALID_ARG and call(G=0) == INVALID_ARG
     assert call(N=1 << 30, P=1 << 30) == UNSUPPORTED         # more blocks than one launch has
+    assert call(N=(1 << 31) - 1, c=1, G=1) == UNSUPPORTED
     assert call(sp=2) == INVALID_ARG
     assert call(ldu=255) == INVALID_ARG and call(ldb=31) == INVALID_ARG and call(z=at(9), ldz=100) == INVALID_ARG
     assert call(A=at(3, 4)) == INVALID_ARG and call(s=at(6, 16)) == INVALID_ARG
