@@ -7,7 +7,7 @@ cudaError_t ssm_scan_bwd_f32(const SsmScanParams& p, cudaStream_t st);
 
 size_t ssm_scan_bwd_workspace(const SsmScanParams& p) {
     Scratch w;
-    return carve(w, nullptr, chunk_count(p.total), bwd_blocks(p), p);
+    return carve(w, nullptr, chunk_count(p.total, chunk_of(p)), bwd_blocks(p), p);
 }
 
 cudaError_t ssm_scan_bwd(kda_dtype dt, kda_dtype gdt, const SsmScanParams& p, cudaStream_t st) {

@@ -6,13 +6,13 @@
 //     du = d q1 + D yb,  dd = q2 + u q1,  ddelta = dd softplus'(delta + bias),  dbias = sum_t ddelta
 //     dA += d dh a h_{t-1},  dB_t = sum_c d u dh,  dC_t = sum_c yb h,  dD = sum_t yb u
 //     dz = dout (sum_s C h + D u) silu'(z),  dh0 = a_0 dh_0
-// Both recurrences are cut at every 64th token of the stream:
+// Both recurrences are cut at every 64th token of the stream (or 32nd or 16th where there are few):
 //   1. one walk forwards over each chunk gives its end state from a zero start, the sum of its step
 //      sizes, and what the chunk hands to the left (sum over its tokens of the decay since the chunk's
 //      start times C yb), so both directions cost one exponential per token and state; the state at the
 //      chunk's middle is kept too;
 //   2. a prefix in each direction turns them into the state before and the gradient behind each chunk;
-//   3. each chunk's halves, the later one first, are walked forwards once more, keeping the state of every
+//   3. each chunk's halves of 32 tokens, the later one first, are walked forwards once more, keeping the state of every
 //      fourth token in shared memory, then backwards four tokens at a time with their states and decays
 //      recomputed into registers.
 // A lane has eight states of a channel in step 3: fewer lanes share a channel's scalars and shuffles, and
@@ -34,7 +34,7 @@ namespace kda {
 
 namespace {
 
-constexpr int kChunk = 64;
+constexpr int kChunk = 64;  // tokens of a chunk at most
 constexpr int kHalf = 32;
 
 // Device scratch: per chunk and channel and state the end states (then start states, then dA's
@@ -91,7 +91,7 @@ struct SumShared {
 };
 
 template <typename T, typename TG, int S>
-__global__ void __launch_bounds__(kSumThreads, 4) scan_bwd_sum_kernel(SsmScanParams p, SeqMap m, Scratch w, bool wide_vecs,
+__global__ void __launch_bounds__(kSumThreads, 4) scan_bwd_sum_kernel(SsmScanParams p, SeqMap m, Scratch w, int chunk, bool wide_vecs,
                                                                       bool wide_rows) {
     using Sh = SumShape<T, TG, S>;
     constexpr int LPC = Sh::LPC, CH = Sh::CH, CHW = Sh::CHW, H2 = Sh::H2, TILE = Sh::TILE, BATCH = Sh::BATCH, OWN = Sh::OWN;
@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kSumThreads, 4) scan_bwd_sum_kernel(SsmScanPar
     const bool on = in_group < cb.group_size;
     const int c = g * cb.group_size + (on ? in_group : 0);
     const int64_t cs = (int64_t)c * S + lane * 4;  // states 4 (q LPC + lane) ... + 3
-    const int t0 = blockIdx.y * kChunk, t1 = min(m.total, t0 + kChunk);
+    const int t0 = blockIdx.y * chunk, t1 = min(m.total, t0 + chunk);
     const int warp_first = cb.in_group(blockIdx.x, CH) + warp * CHW;
     const int warp_has = max(0, min(CHW, cb.group_size - warp_first));
     const int warp_c = g * cb.group_size + min(warp_first, cb.group_size - 1);
@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kSumThreads, 4) scan_bwd_sum_kernel(SsmScanPar
     const float bias = p.bias ? __ldg(p.bias + c) : 0.f;
     sh.tile.template build<kSumThreads>(m, t0);
     const int first = m.first(), last = m.last();
-    const bool plain = sh.tile.plain && t0 >= first && t1 - t0 == kChunk;
+    const bool plain = sh.tile.plain && t0 >= first && t1 - t0 == chunk;
     bool carries = sh.tile.carry >= 0, starts = false, mid_starts = false;
     float sum_d = 0.f;
     const int64_t slot = (int64_t)blockIdx.y * p.C;
@@ -390,7 +390,7 @@ __device__ __forceinline__ void store_two(T* p, f2 x, bool b) {
 }
 
 template <typename T, typename TG, int S, bool kPairs>
-__global__ void __launch_bounds__(kThreads, S == 8 ? 2 : 3) scan_bwd_kernel(SsmScanParams p, SeqMap m, Scratch w) {
+__global__ void __launch_bounds__(kThreads, S == 8 ? 2 : 3) scan_bwd_kernel(SsmScanParams p, SeqMap m, Scratch w, int chunk) {
     using Sh = BwdShape<S>;
     constexpr int LP = Sh::LP, CH = Sh::CH;
     extern __shared__ __align__(16) char raw_smem[];
@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, S == 8 ? 2 : 3) scan_bwd_kernel(SsmS
     const int c = g * cb.group_size + (on ? base + ch : 0);
     const int64_t cs = (int64_t)c * S + lane * 4;  // states 4 (q LP + lane) ... + 3, q = 0, 1
     const int64_t slot = (int64_t)blockIdx.y * p.C;
-    const int t0 = blockIdx.y * kChunk, t1 = min(m.total, t0 + kChunk);
+    const int t0 = blockIdx.y * chunk, t1 = min(m.total, t0 + chunk);
     const int flags = w.flags[blockIdx.y];
 
     // rows come and go by channel pairs: this thread has one pair, in every kRows-th token, kAtOnce of
@@ -465,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, S == 8 ? 2 : 3) scan_bwd_kernel(SsmS
         }
     };
 
-    for (int half = 1; half >= 0; --half) {
+    for (int half = chunk > kHalf ? 1 : 0; half >= 0; --half) {
         const int th = t0 + half * kHalf;
         if (th >= t1) continue;
         const int lo = max(th, first), hi = min(min(t1, th + kHalf), last);
@@ -785,12 +785,22 @@ int bwd_blocks(const SsmScanParams& p) {
     const int ch = kThreads * 8 / p.S;
     return p.G * ((p.C / p.G + ch - 1) / ch);
 }
-int chunk_count(int total) { return total > 0 ? (total + kChunk - 1) / kChunk : 1; }
+// Tokens of a chunk: 64, less where blocks are few and a chunk's length is what the call takes.  64 tokens of 512
+// channels, S = 16, take 59 us in one chunk and 30 in four of 16; up to two blocks an SM the shorter chunks are
+// faster (512 tokens 32 us by 16, 39 by 32), with four they are not (1024 tokens 47 us by 16, 43 by 32, 60 by
+// 64).  32 against 64: 1024 tokens of 2048 channels (1024 blocks) 91 us and 105, 4096 of them 280 and 276.
+int chunk_of(const SsmScanParams& p) {
+    constexpr int kSms = 152;
+    const int64_t blocks = bwd_blocks(p);
+    if (blocks * ((p.total + 15) / 16) <= 2 * kSms) return 16;
+    return blocks * ((p.total + 31) / 32) <= 15 * kSms ? 32 : kChunk;
+}
+int chunk_count(int total, int chunk) { return total > 0 ? (total + chunk - 1) / chunk : 1; }
 
 template <typename T, typename TG, int S>
 cudaError_t launch(const SsmScanParams& p, cudaStream_t st) {
     const SeqMap m{p.cu, p.N, p.T, p.total};
-    const int chunks = chunk_count(p.total), blocks = bwd_blocks(p);
+    const int chunk = chunk_of(p), chunks = chunk_count(p.total, chunk), blocks = bwd_blocks(p);
     Scratch w;
     carve(w, p.ws, chunks, blocks, p);
     constexpr int kSumChannels = SumShape<T, TG, S>::CH;
@@ -806,7 +816,7 @@ cudaError_t launch(const SsmScanParams& p, cudaStream_t st) {
     cudaError_t e = cudaFuncSetAttribute(scan_bwd_sum_kernel<T, TG, S>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)sizeof(SumShared<T, TG, S>));
     if (e != cudaSuccess) return e;
-    scan_bwd_sum_kernel<T, TG, S><<<dim3(sum_blocks, chunks), kSumThreads, sizeof(SumShared<T, TG, S>), st>>>(p, m, w, wide_vecs, wide_rows);
+    scan_bwd_sum_kernel<T, TG, S><<<dim3(sum_blocks, chunks), kSumThreads, sizeof(SumShared<T, TG, S>), st>>>(p, m, w, chunk, wide_vecs, wide_rows);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const int64_t states = (int64_t)p.C * S;
@@ -815,7 +825,7 @@ cudaError_t launch(const SsmScanParams& p, cudaStream_t st) {
     constexpr int smem = sizeof(BwdShared<S>);
     const auto kern = pairs ? scan_bwd_kernel<T, TG, S, true> : scan_bwd_kernel<T, TG, S, false>;
     if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
-    kern<<<dim3(blocks, chunks), kThreads, smem, st>>>(p, m, w);
+    kern<<<dim3(blocks, chunks), kThreads, smem, st>>>(p, m, w, chunk);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const ChunkSums sums{{w.state, w.dD, w.dbias}, {p.dA, p.dD, p.dbias}, {(int64_t)p.C * S, p.C, p.C}};
     scan_bwd_chunks_kernel<<<(unsigned)(((int64_t)p.C * (S + 2) + 31) / 32), 256, 0, st>>>(sums, chunks);

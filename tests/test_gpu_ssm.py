@@ -138,6 +138,11 @@ SCANS = [
     ([1] * 30 + [17] * 6, 129, 16, 1, True, True, True, True, True),
     ([300, 5], 260, 16, 1, False, False, False, False, True),
     ([130], 1, 64, 1, True, True, True, True, True),
+    # blocks enough that the backward pass takes chunks of 64 tokens (above, 16), and of 32
+    ([130, 70, 1, 64, 35], 600, 16, 300, True, True, True, True, True),
+    ([400], 330, 8, 330, False, True, False, True, False),
+    ([31, 65, 0, 40, 128, 3], 270, 32, 90, True, False, True, True, True),
+    ([200, 64], 1300, 64, 1, True, True, True, True, False),
 ]
 
 
@@ -271,9 +276,10 @@ def test_scan_without_tokens():
     assert torch.equal(got["dinitial_state"], s0) and not got["dA"].any()
 
 
-def test_scan_offsets_out_of_order_stay_in_bounds():
-    d = scan_inputs(5, BF16, 994)
-    s0 = torch.randn(4, 24, 64, device="cuda")
+@pytest.mark.parametrize("case", [5, 9, 11])
+def test_scan_offsets_out_of_order_stay_in_bounds(case):
+    d = scan_inputs(case, BF16, 994)
+    s0 = torch.randn(4, *d["A"].shape, device="cuda")
     a, kw = call_args(d)
     for cu in ([0, 150, 50, 180, 200], [0, -5, 900, 20, 200], [200, 0, 200, 0, 7], [2 ** 31 - 1, -2 ** 31, 5, 6, 2 ** 31 - 1]):
         kw["initial_state"], kw["cu_seqlens"] = s0, torch.tensor(cu, dtype=torch.int32, device="cuda")
@@ -326,8 +332,9 @@ def test_layer_of_convolution_and_scan():
     assert np.abs(f64(got["dweight"]) - rg["dweight"]).max() <= 2.0 ** -17 * scale * 111
 
 
-def test_scan_captured_and_replayed_on_another_stream():
-    d = scan_inputs(6, BF16, 997)
+@pytest.mark.parametrize("case", [6, 9])
+def test_scan_captured_and_replayed_on_another_stream(case):
+    d = scan_inputs(case, BF16, 997)
     a, kw = call_args(d)
     dy = d["dy"].to(BF16).cuda()
     want, ws = kda.ssm_scan_fwd(*a, **kw)
@@ -349,11 +356,12 @@ def test_scan_captured_and_replayed_on_another_stream():
     assert torch.equal(y, want) and torch.equal(s, ws) and all(torch.equal(g[k], wg[k]) for k in wg if wg[k] is not None)
 
 
-def test_scan_nan_and_infinity_stay_in_their_sequence():
+@pytest.mark.parametrize("C,G", [(72, 1), (180, 90), (680, 340)])     # chunks of 16, 32 and 64 tokens backwards
+def test_scan_nan_and_infinity_stay_in_their_sequence(C, G):
     """A sequence with NaN and infinite inputs in one chunk with others: theirs are as without it, bit for bit,
     forwards and backwards (the sums over everything apart)."""
-    lengths, C = [40, 9, 50, 64, 37], 72
-    d = make((1, 200), C, 16, 1, F32, 998, True, True, True)
+    lengths = [40, 9, 50, 64, 37]
+    d = make((1, 200), C, 16, G, F32, 998, True, True, True)
     cu = torch.tensor(np.concatenate([[0], np.cumsum(lengths)]), dtype=torch.int32, device="cuda")
     s0 = torch.randn(5, C, 16, generator=torch.Generator().manual_seed(5)).cuda()
     dy = torch.randn(1, 200, C, generator=torch.Generator().manual_seed(6)).cuda()

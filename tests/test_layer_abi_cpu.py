@@ -138,8 +138,8 @@ def test_scan_fwd(lib):
 
 def test_scan_bwd(lib):
     need = lib.kda_ssm_scan_bwd_workspace_size(1, 64, 256, 2, 16, 1, 0)
-    # one chunk: states, gradients and middle states, two sums of d, dD and dbias, four channel blocks' dB and dC, a flag
-    assert need == 3 * 256 * 16 * 4 + 4 * 256 * 4 + 4 * 64 * 32 * 4 + 256
+    # four chunks: states, gradients and middle states, two sums of d, dD and dbias, four channel blocks' dB and dC, flags
+    assert need == 4 * (3 * 256 * 16 * 4 + 4 * 256 * 4) + 4 * 64 * 32 * 4 + 256
 
     def call(**kw):
         a = dict(u=at(1), A=at(3), z=None, ldz=0, dt=1, T=64, c=256, G=2, S=16, N=1, dy=at(10), df=None, gdt=1, du=at(11), dd=at(12),
