@@ -211,6 +211,10 @@ def _rows(name, t, lead: int):
             if stride[0] >= width:
                 return t.data_ptr(), stride[0]
     width = 1
+    if t.is_contiguous():
+        for d in shape[lead:]:
+            width *= d
+        return t.data_ptr(), width
     for d in reversed(range(lead, t.dim())):
         if t.shape[d] != 1 and t.stride(d) != width:
             raise ValueError(f"{name}: the elements of a row must lie side by side")
@@ -752,12 +756,12 @@ def ssm_scan_bwd(u, delta, A, Bm, Cm, dy, D=None, z=None, delta_bias=None, softp
     _shape("dy", dy, (B, T, C))
     _shape("initial_state", initial_state, (N, C, S))
     _shape("dfinal_state", dfinal_state, (N, C, S))
-    new = lambda given, shape, dt: torch.empty(shape, dtype=dt, device=u.device) if given is not None else None  # noqa: E731
-    rows, vecs, f32 = (B, T, C), (B, T, G, S), torch.float32
-    out = {"du": new(u, rows, dy.dtype), "ddelta": new(delta, rows, dy.dtype), "dA": new(A, (C, S), f32),
-           "dB": new(Bm, vecs, dy.dtype), "dC": new(Cm, vecs, dy.dtype), "dD": new(D, C, f32),
-           "dz": new(z, rows, dy.dtype), "ddelta_bias": new(delta_bias, C, f32),
-           "dinitial_state": new(initial_state, (N, C, S), f32)}
+    rows, vecs = (B, T, C), (B, T, G, S)
+    like, f32 = dy.new_empty, A.new_empty  # of the gradients' type, and fp32
+    out = {"du": like(rows), "ddelta": like(rows), "dA": f32((C, S)), "dB": like(vecs), "dC": like(vecs),
+           "dD": f32(C) if D is not None else None, "dz": like(rows) if z is not None else None,
+           "ddelta_bias": f32(C) if delta_bias is not None else None,
+           "dinitial_state": f32((N, C, S)) if initial_state is not None else None}
     ws, ws_bytes = _workspace(int(lib.kda_ssm_scan_bwd_workspace_size(B, T, C, G, S, N, int(cu_seqlens is not None))),
                               u.device, workspace)
     st = lib.kda_ssm_scan_bwd(*_ssm_pointers(u, delta, A, Bm, Cm, D, z, delta_bias, softplus), _at(initial_state),
