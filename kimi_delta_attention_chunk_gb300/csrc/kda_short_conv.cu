@@ -16,6 +16,7 @@
 #include "kda_layer.h"
 #include "kda_segments.cuh"
 #include "kda_slots.cuh"
+#include "kda_tc.cuh"
 
 namespace kda {
 
@@ -422,6 +423,7 @@ __global__ void __launch_bounds__(kThreads, kBwdResident) conv_bwd_kernel(ConvPa
             }
         }
     }
+    tc::grid_dep_launch();
     if (on) {
         // [run][tap, and the bias][C]
         float* out = p.partial + (int64_t)blockIdx.y * (W + 1) * p.C + c0;
@@ -441,6 +443,7 @@ __global__ void __launch_bounds__(kThreads, kBwdResident) conv_bwd_kernel(ConvPa
 __global__ void __launch_bounds__(128) conv_bwd_sum_kernel(const float* partial, int runs, int C, int W, float* dw,
                                                            float* db) {
     const int64_t i = (int64_t)blockIdx.x * 128 + threadIdx.x, n = (int64_t)C * (W + 1);
+    tc::grid_dep_wait();
     if (i >= n) return;
     float a = 0.f;
 #pragma unroll 16
@@ -537,8 +540,9 @@ cudaError_t launch_bwd(const ConvParams& p, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     const int runs = run_count(p.total, run_tokens(p.total, p.C, VEC, kBwdResident));
     const int64_t n = (int64_t)p.C * (p.W + 1);
-    conv_bwd_sum_kernel<<<(unsigned)((n + 127) / 128), 128, 0, st>>>(p.partial, runs, p.C, p.W, p.dweight, p.dbias);
-    return cudaGetLastError();
+    // (it may start while the runs end: 4096 x 12288 in 65.5 us, 67.7 without)
+    return tc::launch_dependent(conv_bwd_sum_kernel, (unsigned)((n + 127) / 128), 128, 0, st, p.partial, runs, p.C, p.W, p.dweight,
+                                p.dbias);
 }
 
 template <typename T, int VEC, int W>

@@ -19,6 +19,7 @@
 
 #include "kda_layer.h"
 #include "kda_ssm.cuh"
+#include "kda_tc.cuh"
 
 namespace kda {
 
@@ -172,6 +173,7 @@ __global__ void __launch_bounds__(kThreads, 4) scan_kernel(SsmScanParams p, SeqM
         else clear_state();
     };
 
+    if (kOutputs) tc::grid_dep_wait();  // the runs' starts
     // a sequence without tokens hands its state on
     if (kOutputs && p.final_state && on)
         for (int n = blockIdx.y; n < m.N; n += gridDim.y)
@@ -311,6 +313,7 @@ __global__ void __launch_bounds__(kThreads, 4) scan_kernel(SsmScanParams p, SeqM
             }
         }
     }
+    if (!kOutputs) tc::grid_dep_launch();
     if (!kOutputs && on) {
         store_state(runs.state + (int64_t)blockIdx.y * p.C * S + cs);
         if (lane == 0) runs.sum_d[(int64_t)blockIdx.y * p.C + c] = sum_d;
@@ -322,9 +325,10 @@ __global__ void __launch_bounds__(kThreads, 4) scan_kernel(SsmScanParams p, SeqM
 // eight runs requested together.
 __global__ void __launch_bounds__(128) scan_prefix_kernel(const float* A, Runs r, int runs, int C, int S) {
     const int64_t i = blockIdx.x * 128ll + threadIdx.x, n = (int64_t)C * S;
+    const int c = (int)(min(i, n - 1) / S);
+    const float a = kLog2e * __ldg(A + min(i, n - 1));
+    tc::grid_dep_wait();
     if (i >= n) return;
-    const int c = (int)(i / S);
-    const float a = kLog2e * __ldg(A + i);
     float h = 0.f;
     constexpr int kAhead = 8;
     for (int j0 = 0; j0 < runs; j0 += kAhead) {
@@ -344,6 +348,7 @@ __global__ void __launch_bounds__(128) scan_prefix_kernel(const float* A, Runs r
             h = cut[k] ? e[k] : fmaf(ex2(d[k] * a), h, e[k]);
         }
     }
+    tc::grid_dep_launch();
 }
 
 // Tokens of a run, and whether runs depend on one another.
@@ -393,10 +398,14 @@ cudaError_t launch_rows(const SsmScanParams& p, cudaStream_t st) {
         cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
         const int64_t states = (int64_t)p.C * S;
-        scan_prefix_kernel<<<(unsigned)((states + 127) / 128), 128, 0, st>>>(p.A, r, q.runs, p.C, S);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        // Each of the next two may start while the one before it ends (16384 x 4096 x 16 in 532 us, 536 without).  A block asks
+        // for that with its last stores only: blocks that start earlier are spread unevenly over the SMs (16384 x 512 x 16
+        // in 112 us with the prefix asking at its start, 98 at its end, 101 without).
+        if ((e = tc::launch_dependent(scan_prefix_kernel, (unsigned)((states + 127) / 128), 128, 0, st, p.A, r, q.runs, p.C, S)) != cudaSuccess)
+            return e;
+        return tc::launch_dependent(scan_kernel<T, S, true, wide_rows>, grid, kThreads, 0, st, p, m, q.run, r, true, wide_vecs);
     }
-    scan_kernel<T, S, true, wide_rows><<<grid, kThreads, 0, st>>>(p, m, q.run, r, q.split, wide_vecs);
+    scan_kernel<T, S, true, wide_rows><<<grid, kThreads, 0, st>>>(p, m, q.run, r, false, wide_vecs);
     return cudaGetLastError();
 }
 
