@@ -750,12 +750,10 @@ struct ChunkSums {
     float* out[3];
     int64_t n[3];
 };
-__global__ void __launch_bounds__(256) scan_bwd_chunks_kernel(ChunkSums s, int chunks) {
+__device__ __forceinline__ void chunk_sums(const ChunkSums& s, int chunks, int block) {
     __shared__ float part[8][32];
-    tc::grid_dep_launch();
-    tc::grid_dep_wait();
     const int x = threadIdx.x % 32, y = threadIdx.x / 32;
-    int64_t i = blockIdx.x * 32ll + x;
+    int64_t i = block * 32ll + x;
     int v = 0;
     while (v < 2 && i >= s.n[v]) i -= s.n[v++];
     const bool on = i < s.n[v] && s.out[v];
@@ -775,9 +773,8 @@ __global__ void __launch_bounds__(256) scan_bwd_chunks_kernel(ChunkSums s, int c
 
 // dB and dC from the channel blocks of each group.
 template <typename TG, int S>
-__global__ void __launch_bounds__(256) scan_bwd_vec_kernel(const float* in, SeqMap m, int G, int per_group, TG* dB, TG* dC) {
-    const int64_t i = blockIdx.x * 256ll + threadIdx.x;
-    tc::grid_dep_wait();
+__device__ __forceinline__ void vec_sums(const float* in, const SeqMap& m, int G, int per_group, TG* dB, TG* dC, int block) {
+    const int64_t i = block * 256ll + threadIdx.x;
     if (i >= (int64_t)m.total * G * 2 * S) return;
     const int j = (int)(i % (2 * S));
     const int64_t tg = i / (2 * S);
@@ -788,6 +785,15 @@ __global__ void __launch_bounds__(256) scan_bwd_vec_kernel(const float* in, SeqM
     for (int b = 0; b < per_group; ++b) a += in[((int64_t)(g * per_group + b) * m.total + t) * 2 * S + j];
     TG* out = j < S ? dB : dC;
     out[tg * S + j % S] = from_f32<TG>(a);
+}
+
+// Both, by blocks of one launch: the first `chunk_blocks` for the sums over the chunks.
+template <typename TG, int S>
+__global__ void __launch_bounds__(256) scan_bwd_partial_kernel(ChunkSums s, int chunks, int chunk_blocks, const float* in, SeqMap m, int G,
+                                                               int per_group, TG* dB, TG* dC) {
+    tc::grid_dep_wait();
+    if ((int)blockIdx.x < chunk_blocks) chunk_sums(s, chunks, blockIdx.x);
+    else vec_sums<TG, S>(in, m, G, per_group, dB, dC, blockIdx.x - chunk_blocks);
 }
 
 int bwd_blocks(const SsmScanParams& p) {
@@ -829,8 +835,8 @@ cudaError_t launch(const SsmScanParams& p, cudaStream_t st) {
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const int64_t states = (int64_t)p.C * S;
-    // Each of the others may start while the one before it ends, as in the forward scan (2 x 2048 x 4096 x 16 in 538 us,
-    // 546 without; 64 tokens of 512 channels 27.6 and 29.4).
+    // Each of the others may start while the one before it ends, as in the forward scan (2 x 2048 x 4096 x 16 in 534 us,
+    // 542 without; 64 tokens of 512 channels 26 and 28).
     e = tc::launch_dependent(scan_bwd_prefix_kernel, dim3((unsigned)((states + 127) / 128), 2), 128, 0, st, p.A, w, chunks, p.C, S);
     if (e != cudaSuccess) return e;
     constexpr int smem = sizeof(BwdShared<S>);
@@ -838,12 +844,10 @@ cudaError_t launch(const SsmScanParams& p, cudaStream_t st) {
     if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
     if ((e = tc::launch_dependent(kern, dim3(blocks, chunks), kThreads, smem, st, p, m, w, chunk)) != cudaSuccess) return e;
     const ChunkSums sums{{w.state, w.dD, w.dbias}, {p.dA, p.dD, p.dbias}, {(int64_t)p.C * S, p.C, p.C}};
-    e = tc::launch_dependent(scan_bwd_chunks_kernel, (unsigned)(((int64_t)p.C * (S + 2) + 31) / 32), 256, 0, st, sums, chunks);
-    if (e != cudaSuccess) return e;
-    const int64_t n = (int64_t)p.total * p.G * 2 * S;
-    if (n == 0) return cudaSuccess;
-    return tc::launch_dependent(scan_bwd_vec_kernel<TG, S>, (unsigned)((n + 255) / 256), 256, 0, st, w.dBC, m, p.G, blocks / p.G,
-                                static_cast<TG*>(p.dB), static_cast<TG*>(p.dC));
+    const int chunk_blocks = (int)(((int64_t)p.C * (S + 2) + 31) / 32);
+    const int64_t vec_blocks = ((int64_t)p.total * p.G * 2 * S + 255) / 256;
+    return tc::launch_dependent(scan_bwd_partial_kernel<TG, S>, (unsigned)(chunk_blocks + vec_blocks), 256, 0, st, sums, chunks,
+                                chunk_blocks, w.dBC, m, p.G, blocks / p.G, static_cast<TG*>(p.dB), static_cast<TG*>(p.dC));
 }
 
 template <typename T, typename TG>
