@@ -13,6 +13,10 @@
 // gradients) in registers; runs meet at W - 1 rows that both read.  Rows arrive by asynchronous copies
 // into shared memory, batches ahead of their use; a thread reads back only what it copied itself, so
 // nothing in the walk waits for another thread.
+//
+// 70k x 12288 bf16 forwards with histories: 554 us, 6.2 TB/s, 91% of a copy's rate.  4096 x 12288 backwards: 65.5 us, 4.6
+// TB/s, bound by issue (2.05 instructions a cycle and SM) and by one filling's start and end; 32,768 tokens 5.6 TB/s.
+// One token of 256 sequences: 12.3 us, 4.1 TB/s, latency.
 #include "kda_layer.h"
 #include "kda_segments.cuh"
 #include "kda_slots.cuh"
@@ -500,7 +504,7 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(ConvStepParams p) {
 
 // Tokens of one run: as many runs as one filling of the machine holds, at least 32 tokens each so
 // that the W - 1 rows read twice stay below a tenth; three fillings where the runs then still have 128
-// tokens, which evens out what blocks finish early (70k x 12288 forwards: 556 us against 566).
+// tokens, which evens out what blocks finish early (70k x 12288 forwards: 554 us against 566).
 int run_tokens(int total, int C, int vec, int resident) {
     const int blocks = (C + kThreads * vec - 1) / (kThreads * vec);
     const int runs = kSms * resident / blocks > 0 ? kSms * resident / blocks : 1;
