@@ -7,8 +7,8 @@
 // latency, so each operation is one kernel of one cluster (eight blocks when there are many pages or forks,
 // else one): the blocks count their share of refs, exchange the counts through distributed shared
 // memory, and place their own pages, with hardware cluster barriers between and no waiting on
-// memory.  The payload moves in kda_pages_copy, bound by HBM: 24 pages of 6.3 MB in 45 us.  Of the books, taking 8 of
-// 8192 pages takes 5 us, of a million 16; closing up 8192 pages 10, a million 108; 64 forks of rows of 64 entries 10.
+// memory.  The payload moves in kda_pages_copy, bound by HBM: 24 pages of 6.3 MB in 45 us.  Of the books, taking pages
+// of 8192 takes 5 us, of a million 16; closing up 8192 pages 10, a million 108; 64 forks of rows of 64 entries 10.
 #include <cooperative_groups.h>
 
 #include "kda_layer.h"
