@@ -18,9 +18,11 @@
  * ---------------------------------------
  *  - Every tensor pointer is a DEVICE pointer owned by the caller, and so is
  *    every workspace: the library allocates no memory.  kda_chunk_fwd,
- *    kda_chunk_fwd_fused and kda_recurrent_bwd take a caller-owned device
+ *    kda_chunk_fwd_fused and kda_recurrent_bwd, and the convolution, scan and
+ *    pages calls that name one, take a caller-owned device
  *    workspace of at least the size their *_workspace_size query returns
- *    (16-byte aligned; the call owns it until its stream work completes, and
+ *    (16-byte aligned; the call owns it until its stream work completes, so
+ *    calls whose work overlaps, replayed graphs among them, must not share one;
  *    nothing in it needs to be initialised); a smaller one returns
  *    KDA_ERR_WORKSPACE before anything is enqueued.  kda_chunk_fwd_noalloc
  *    keeps its workspace in a fixed array inside the library instead.  Calls
