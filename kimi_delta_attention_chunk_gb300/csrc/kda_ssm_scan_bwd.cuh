@@ -21,7 +21,7 @@
 // Sums over channels (dB, dC) go through shared memory, 16 additions a lane and token, then the block's
 // warps, and partial sums of the channel blocks; sums over tokens through partial sums of the chunks.
 // Every sum has an order fixed by the sizes.  Instruction issue bounds steps 1 and 3 (2.3 and 2.05 a cycle and SM):
-// 2 x 2048 x 4096 x 16 bf16 with every gradient takes 534 us, 118 + 19 + 384 in the steps and 21 in the last sums.
+// 2 x 2048 x 4096 x 16 bf16 with every gradient takes 536 us, 118 + 19 + 384 in the steps and 21 in the last sums.
 #pragma once
 
 #include <stddef.h>
@@ -836,8 +836,8 @@ cudaError_t launch(const SsmScanParams& p, cudaStream_t st) {
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const int64_t states = (int64_t)p.C * S;
-    // Each of the others may start while the one before it ends, as in the forward scan (2 x 2048 x 4096 x 16 in 534 us,
-    // 542 without; 64 tokens of 512 channels 26 and 28).
+    // Each of the others may start while the one before it ends, as in the forward scan (2 x 2048 x 4096 x 16 in 536 us,
+    // 544 without; 64 tokens of 512 channels 26 and 28).
     e = tc::launch_dependent(scan_bwd_prefix_kernel, dim3((unsigned)((states + 127) / 128), 2), 128, 0, st, p.A, w, chunks, p.C, S);
     if (e != cudaSuccess) return e;
     constexpr int smem = sizeof(BwdShared<S>);
