@@ -533,7 +533,8 @@ KDA_API kda_status kda_short_conv_fwd(const void *x, int64_t ldx, const float *w
  *  order fixed by the sizes.
  *  workspace  at least kda_short_conv_bwd_workspace_size bytes, 16-byte aligned
  *             (partial sums of dweight and dbias by runs of tokens).
- * The rest as kda_short_conv_fwd.
+ * The dx of rows that belong to no sequence is zero, whatever they hold: L does not
+ * depend on them.  The rest as kda_short_conv_fwd.
  */
 KDA_API size_t kda_short_conv_bwd_workspace_size(int B, int T, int C, int W);
 KDA_API kda_status kda_short_conv_bwd(const void *x, int64_t ldx, const float *weight, const float *bias,

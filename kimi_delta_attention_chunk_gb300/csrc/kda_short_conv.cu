@@ -427,6 +427,13 @@ __global__ void __launch_bounds__(kThreads, kBwdResident) conv_bwd_kernel(ConvPa
             }
         }
     }
+    if (on) {
+        // the run's rows of no sequence, on which nothing depends
+        RG none;
+        none.zero();
+        for (int t = r0; t < min(r1, first); ++t) none.store(dx + (int64_t)t * p.C);
+        for (int t = max(r0, last); t < r1; ++t) none.store(dx + (int64_t)t * p.C);
+    }
     tc::grid_dep_launch();
     if (on) {
         // [run][tap, and the bias][C]

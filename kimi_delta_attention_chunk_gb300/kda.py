@@ -607,7 +607,8 @@ def short_conv_bwd(x, weight, dy, bias=None, conv_act: int = 0, initial=None, cu
     """Gradients of <dy, y> + <dfinal, final> through :func:`short_conv_fwd` (same
     arguments).  dy [B,T,C] and dfinal [N,W-1,C] share a type: x's, or fp32.  Returns a
     dict: dx [B,T,C] and dinitial [N,W-1,C] (None without ``initial``) in dy's type, dweight
-    [C,W] and dbias [C] (None without ``bias``) fp32."""
+    [C,W] and dbias [C] (None without ``bias``) fp32.  Rows that belong to no sequence have
+    zeros in dx."""
     lib = _lib if _lib is not None else load_library()
     C, W = _conv_check(x, weight, bias, conv_act)
     B, T, _ = x.shape

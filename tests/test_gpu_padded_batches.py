@@ -1,0 +1,58 @@
+"""Packed batches whose offsets leave rows at the front and the back that belong to no sequence: the loss does not
+depend on them, so their gradients are zero, whatever lies in those rows and in the memory that the gradients are
+put into.  Tolerances of the rows in between as in the tests of each operator."""
+import numpy as np
+import pytest
+import torch
+
+import kimi_delta_attention_chunk_gb300 as kda
+from tests import test_gpu_short_conv as short_conv, test_gpu_ssm as ssm
+from tests.layer_ref import conv, f64, scan
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+# tokens, offsets: short of a tile on either side, whole tiles and runs of nobody, sequences without tokens, no sequence
+BATCHES = [(100, [4, 30, 81]), (700, [130, 131, 131, 400]), (300, [0, 5, 7]), (300, [290, 300]), (90, [40, 40, 40]), (64, [64, 64]),
+           (70, [9])]
+
+
+@pytest.fixture
+def dirty_memory():
+    """Fresh tensors are full of NaN."""
+    torch.use_deterministic_algorithms(True, warn_only=True)
+    assert torch.utils.deterministic.fill_uninitialized_memory and bool(torch.empty(3, device="cuda").isnan().all())
+    yield
+    torch.use_deterministic_algorithms(False)
+
+
+def nobody(T, cu):
+    rows = torch.ones(T, dtype=torch.bool)
+    rows[cu[0]:cu[-1]] = False
+    return rows
+
+
+def spoiled(t, rows):
+    t = t.clone()
+    t[0, rows.to(t.device)] = float("nan")
+    return t
+
+
+@pytest.mark.parametrize("dtype,gdtype", [(BF16, BF16), (BF16, F32), (F32, F32)])
+@pytest.mark.parametrize("C,W", [(64, 4), (37, 3), (1032, 2)])
+@pytest.mark.parametrize("batch", range(len(BATCHES)))
+def test_convolution_gradients(batch, C, W, dtype, gdtype, dirty_memory):
+    T, cu = BATCHES[batch]
+    N, rows = len(cu) - 1, nobody(T, cu)
+    g = torch.Generator().manual_seed(2000 + batch)
+    x, dy = torch.randn(1, T, C, generator=g).to(dtype).cuda(), torch.randn(1, T, C, generator=g).to(gdtype).cuda()
+    w, b = (torch.randn(C, W, generator=g) * 0.5).cuda(), torch.randn(C, generator=g).cuda()
+    h, df = torch.randn(N, W - 1, C, generator=g).to(dtype).cuda(), torch.randn(N, W - 1, C, generator=g).to(gdtype).cuda()
+    got = kda.short_conv_bwd(spoiled(x, rows), w, spoiled(dy, rows), bias=b, conv_act=1, initial=h, dfinal=df,
+                             cu_seqlens=torch.tensor(cu, dtype=torch.int32).cuda())
+    assert bool((got["dx"][0, rows.cuda()] == 0).all())
+    ref = conv(f64(x[0]), f64(w), f64(b), 1, f64(h), cu, f64(dy[0]), f64(df))
+    short_conv.within(got["dx"][0], ref["dx"], 2.0 ** -19 * ref["dx_mag"], gdtype)
+    short_conv.within(got["dinitial"], ref["dinitial"], 2.0 ** -19 * ref["di_mag"], gdtype)
+    for k, mag in (("dweight", "dw_mag"), ("dbias", "db_mag")):
+        short_conv.within(got[k], ref[k], (2.0 ** -19 + T * 2.0 ** -24) * ref[mag], F32)
