@@ -614,7 +614,8 @@ KDA_API kda_status kda_ssm_scan_fwd(const void *u, int64_t ldu, const void *delt
  *  dfinal_state, dinitial_state fp32 [N, C, S] or NULL, 16-byte aligned.
  *  dA fp32 [C][S]; dD, ddelta_bias fp32 [C] or NULL.
  *  workspace  at least kda_ssm_scan_bwd_workspace_size bytes, 16-byte aligned.
- * B T <= 4194240.  Sums are fp32, in an order fixed by the sizes.  The rest as
+ * B T <= 4194240.  Sums are fp32, in an order fixed by the sizes.  Rows that belong to
+ * no sequence have zeros in du, ddelta, dz, dB and dC, whatever they hold.  The rest as
  * kda_ssm_scan_fwd.
  */
 KDA_API size_t kda_ssm_scan_bwd_workspace_size(int B, int T, int C, int G, int S, int N, int packed);

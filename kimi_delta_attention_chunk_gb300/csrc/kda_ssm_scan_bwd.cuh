@@ -697,7 +697,13 @@ __global__ void __launch_bounds__(kThreads, S == 8 ? 2 : 3) scan_bwd_kernel(SsmS
             for (int j = 0; j < kAtOnce; ++j) {
                 const int r = r0 + j * kRows;
                 const int64_t t = th + r;
-                if (!e0 || t < lo || t >= hi) continue;
+                if (!e0 || t >= t1) continue;
+                if (t < lo || t >= hi) {  // of no sequence: nothing depends on it
+                    store_two<kPairs>(static_cast<TG*>(p.du) + t * p.C + ec, 0ull, e1);
+                    store_two<kPairs>(static_cast<TG*>(p.ddelta) + t * p.C + ec, 0ull, e1);
+                    if (p.z) store_two<kPairs>(static_cast<TG*>(p.dz) + t * p.C + ec, 0ull, e1);
+                    continue;
+                }
                 f2 dd = *reinterpret_cast<const f2*>(&sh.d[r][ech]);
                 if (p.softplus) dd = mul2(dd, sigmoid2(add2(rd[j].get(e1), ebias)));
                 dbias = add2(dbias, dd);
@@ -780,10 +786,11 @@ __device__ __forceinline__ void vec_sums(const float* in, const SeqMap& m, int G
     const int j = (int)(i % (2 * S));
     const int64_t tg = i / (2 * S);
     const int g = (int)(tg % G), t = (int)(tg / G);
-    if (t < m.first() || t >= m.last()) return;
     float a = 0.f;
+    if (t >= m.first() && t < m.last()) {  // (rows of no sequence: zeros)
 #pragma unroll 16
-    for (int b = 0; b < per_group; ++b) a += in[((int64_t)(g * per_group + b) * m.total + t) * 2 * S + j];
+        for (int b = 0; b < per_group; ++b) a += in[((int64_t)(g * per_group + b) * m.total + t) * 2 * S + j];
+    }
     TG* out = j < S ? dB : dC;
     out[tg * S + j % S] = from_f32<TG>(a);
 }

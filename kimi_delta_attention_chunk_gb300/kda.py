@@ -747,7 +747,8 @@ def ssm_scan_bwd(u, delta, A, Bm, Cm, dy, D=None, z=None, delta_bias=None, softp
     """Gradients of <dy, y> + <dfinal_state, final_state> through :func:`ssm_scan_fwd` (same
     arguments).  dy [B,T,C] is of u's type or fp32.  Returns a dict: du, ddelta, dz [B,T,C]
     and dB, dC [B,T,G,S] in dy's type, dA [C,S], dD, ddelta_bias [C] and dinitial_state
-    [N,C,S] fp32; the gradient of an argument that was not given is None."""
+    [N,C,S] fp32; the gradient of an argument that was not given is None.  Rows that belong
+    to no sequence have zeros."""
     lib = _lib if _lib is not None else load_library()
     C, G, S = _ssm_check(u, delta, A, Bm, Cm, D, z, delta_bias)
     B, T, _ = u.shape

@@ -56,3 +56,29 @@ def test_convolution_gradients(batch, C, W, dtype, gdtype, dirty_memory):
     short_conv.within(got["dinitial"], ref["dinitial"], 2.0 ** -19 * ref["di_mag"], gdtype)
     for k, mag in (("dweight", "dw_mag"), ("dbias", "db_mag")):
         short_conv.within(got[k], ref[k], (2.0 ** -19 + T * 2.0 ** -24) * ref[mag], F32)
+
+
+# channels and groups: chunks of 16, 32 and 64 tokens backwards, and an odd number of channels
+@pytest.mark.parametrize("dtype,gdtype", [(BF16, BF16), (BF16, F32), (F32, F32)])
+@pytest.mark.parametrize("C,G,S", [(72, 1, 16), (180, 90, 16), (680, 340, 8), (37, 1, 32), (24, 2, 64)])
+@pytest.mark.parametrize("batch", range(len(BATCHES)))
+def test_scan_gradients(batch, C, G, S, dtype, gdtype, dirty_memory):
+    T, cu = BATCHES[batch]
+    N, rows = len(cu) - 1, nobody(T, cu)
+    d = ssm.make((1, T), C, S, G, dtype, 2100 + batch, True, True, True)
+    g = torch.Generator().manual_seed(2200 + batch)
+    for k in ("u", "delta", "z", "B", "C"):
+        d[k] = d[k].clone()
+        d[k][0, rows.cuda()] = 0          # (the plain form sums over every row)
+    dy = torch.randn(1, T, C, generator=g).to(gdtype).cuda()
+    dy[0, rows.cuda()] = 0
+    s0, df = torch.randn(N, C, S, generator=g).cuda(), torch.randn(N, C, S, generator=g).cuda()
+    d.update(sp=True, s0=s0, cu=torch.tensor(cu, dtype=torch.int32).cuda())
+    a, kw = ssm.call_args({**d, **{k: spoiled(d[k], rows) for k in ("u", "delta", "z", "B", "C")}})
+    got = kda.ssm_scan_bwd(*a, spoiled(dy, rows), dfinal_state=df, **kw)
+    for k in ("du", "ddelta", "dz", "dB", "dC"):
+        assert bool((got[k][0, rows.cuda()] == 0).all()), k
+    r = scan(*ssm.ref_args(d), f64(dy)[0], f64(df))
+    for k, dt, n in (("du", gdtype, S), ("ddelta", gdtype, S), ("dz", gdtype, S), ("dB", gdtype, C), ("dC", gdtype, C), ("dA", F32, T),
+                     ("dD", F32, T), ("ddelta_bias", F32, T), ("dinitial_state", F32, 1)):
+        ssm.within(got[k], r[k], (2.0 ** -19 + n * 2.0 ** -24) * r[k + "_err"], dt)
