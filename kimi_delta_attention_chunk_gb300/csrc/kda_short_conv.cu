@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, kFwdResident) conv_fwd_kernel(ConvPa
     const T* hist = static_cast<const T*>(p.initial);
     T* y = static_cast<T*>(p.y) + c0;
     T* fin = static_cast<T*>(p.final_hist);
-    const int r0 = blockIdx.y * run, r1 = min(m.total, r0 + run);
+    const int r0 = blockIdx.y * run, r1 = (int)min((int64_t)m.total, (int64_t)r0 + run);
     auto request = [&](int t) {
         if (t < r1) {
             const int s = (t - r0) / kBatch % kStages, more = r1 - 1 - t;
@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, kBwdResident) conv_bwd_kernel(ConvPa
     const TG* dfin = static_cast<const TG*>(p.dfinal);
     TG* dx = static_cast<TG*>(p.dx) + c0;
     TG* dinit = static_cast<TG*>(p.dinitial);
-    const int r0 = blockIdx.y * run, r1 = min(m.total, r0 + run), stop = min(m.total, r1 + W - 1);
+    const int r0 = blockIdx.y * run, r1 = (int)min((int64_t)m.total, (int64_t)r0 + run), stop = min(m.total, r1 + W - 1);
     auto request = [&](int t) {
         if (t < stop) {
             const int s = (t - r0) / kBatch % kStages, more = stop - 1 - t;
@@ -520,7 +520,8 @@ int run_tokens(int total, int C, int vec, int resident) {
     run = (run + 7) / 8 * 8;
     return run < 32 ? 32 : run;
 }
-int run_count(int total, int run) { return total > 0 ? (total + run - 1) / run : 1; }
+// (total + run may pass 2^31)
+int run_count(int total, int run) { return total > 0 ? total / run + (total % run != 0) : 1; }
 
 SeqMap seq_map(const ConvParams& p) { return SeqMap{p.cu, p.N, p.T, p.total}; }
 

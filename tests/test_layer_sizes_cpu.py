@@ -1,0 +1,24 @@
+"""Sizes at the ends of what the recurrent layer's C calls accept: counts that stay within 32 bits, and refusals
+beyond.  Nothing here reaches a launch."""
+import pytest
+
+import kimi_delta_attention_chunk_gb300 as kda
+from kimi_delta_attention_chunk_gb300 import build as kbuild
+
+MOST_TOKENS = 2 ** 31 - 65536 - 1
+
+
+@pytest.fixture(scope="module")
+def lib():
+    kbuild.build()
+    return kda.load_library()
+
+
+def test_convolution_runs_at_the_most_tokens(lib):
+    W, C = 4, 8
+    row = C * (W + 1) * 4                                # a run's partial sums
+    # one block of channels: three fillings of 152 SMs by three blocks, each a run, up to a rounding of their length
+    for T in (2 ** 30, 2 ** 31 - 2 ** 25, MOST_TOKENS - 10 ** 6, MOST_TOKENS):
+        need = lib.kda_short_conv_bwd_workspace_size(1, T, C, W)
+        assert need % row == 0 and 3 * 152 * 3 - 8 <= need // row <= 3 * 152 * 3, T
+    assert lib.kda_short_conv_bwd_workspace_size(1, MOST_TOKENS + 1, C, W) == 0
