@@ -382,7 +382,7 @@ Plan plan(const SsmScanParams& p) {
     // tokens of 4096 channels, S = 64, 22 us and 26.
     if (p.total <= 64 || p.total <= 40 + q.blocks / 2) run = (p.total + kRunStep - 1) / kRunStep * kRunStep;
     q.run = run;
-    q.runs = p.total > 0 ? (p.total + run - 1) / run : 1;
+    q.runs = p.total > 0 ? p.total / run + (p.total % run != 0) : 1;  // (total + run may pass 2^31)
     q.split = q.runs > 1;
     return q;
 }

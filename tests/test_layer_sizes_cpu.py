@@ -22,3 +22,11 @@ def test_convolution_runs_at_the_most_tokens(lib):
         need = lib.kda_short_conv_bwd_workspace_size(1, T, C, W)
         assert need % row == 0 and 3 * 152 * 3 - 8 <= need // row <= 3 * 152 * 3, T
     assert lib.kda_short_conv_bwd_workspace_size(1, MOST_TOKENS + 1, C, W) == 0
+
+
+def test_scan_runs_at_the_most_tokens(lib):
+    C, S = 8, 8
+    for T in (2 ** 30, 2 ** 31 - 2 ** 25, MOST_TOKENS - 10 ** 6, MOST_TOKENS):
+        # 96 runs: their end states, sums of step sizes, and whether a sequence begins inside
+        assert lib.kda_ssm_scan_fwd_workspace_size(1, T, C, 1, S, 1, 0) == 96 * (C * S + C) * 4 + 96 * 4, T
+    assert lib.kda_ssm_scan_fwd_workspace_size(1, MOST_TOKENS + 1, C, 1, S, 1, 0) == 0
