@@ -512,8 +512,9 @@ KDA_API kda_status kda_recurrent_step_slots(const void *q, const void *k, const 
  *  y        [B, T, C]; final_history [N, W-1, C] or NULL: the history after each
  *           sequence (of a sequence without tokens: its initial one).
  * x, initial, y, final_history have element type dtype; no output may overlap an input.
- * W in {2, 3, 4}, C <= 2^20, B T < 2^31 - 65536.  Rows whose start, length and stride
- * are whole 16-byte pieces are read in such pieces, others element by element.
+ * W in {2, 3, 4}, C <= 2^20, B T < 2^31 - 65536, N < 2^31 - 65536.  Rows whose start,
+ * length and stride are whole 16-byte pieces are read in such pieces, others element by
+ * element.
  */
 KDA_API kda_status kda_short_conv_fwd(const void *x, int64_t ldx, const float *weight, const float *bias,
                               int conv_act, kda_dtype dtype, const void *initial,

@@ -49,7 +49,8 @@ kda_status clear(int32_t* status, cudaStream_t st) {
 // Tokens, sequences and channels of a packed or dense call.
 kda_status check_stream(int B, int T, int C, int N, const int32_t* cu) {
     if (B < 0 || T < 0 || C <= 0 || N < 0) return KDA_ERR_INVALID_ARG;
-    if ((int64_t)B * T > 0x7fffffffLL - 65536) return KDA_ERR_INVALID_ARG;
+    // (kernels step past their ends by up to a grid's blocks or a tile)
+    if ((int64_t)B * T > 0x7fffffffLL - 65536 || N > 0x7fffffff - 65536) return KDA_ERR_INVALID_ARG;
     if (cu ? B != 1 : N != B) return KDA_ERR_INVALID_ARG;
     if (!aligned(cu, 4)) return KDA_ERR_INVALID_ARG;
     if (C > kMostChannels) return KDA_ERR_UNSUPPORTED;

@@ -4,6 +4,7 @@ import pytest
 
 import kimi_delta_attention_chunk_gb300 as kda
 from kimi_delta_attention_chunk_gb300 import build as kbuild
+from tests.test_layer_abi_cpu import INVALID_ARG, at, scan
 
 MOST_TOKENS = 2 ** 31 - 65536 - 1
 
@@ -30,3 +31,21 @@ def test_scan_runs_at_the_most_tokens(lib):
         # 96 runs: their end states, sums of step sizes, and whether a sequence begins inside
         assert lib.kda_ssm_scan_fwd_workspace_size(1, T, C, 1, S, 1, 0) == 96 * (C * S + C) * 4 + 96 * 4, T
     assert lib.kda_ssm_scan_fwd_workspace_size(1, MOST_TOKENS + 1, C, 1, S, 1, 0) == 0
+
+
+def test_number_of_sequences(lib):
+    """As many as tokens: offsets and histories are counted past the number in steps of a grid."""
+    many = MOST_TOKENS + 1
+
+    def conv(N, cu=at(4)):
+        return lib.kda_short_conv_fwd(at(1), 8, at(2), None, 0, 1, None, cu, 1 if cu else N, 64 if cu else 0, 8, 4, N, at(3), None, None)
+
+    def conv_bwd(N):
+        return lib.kda_short_conv_bwd(at(1), 8, at(2), None, 0, 1, None, at(4), 1, 64, 8, 4, N, at(5), None, 1, at(6), at(7), None, None,
+                                      at(8), 1 << 30, None)
+    for N in (many, 2 ** 31 - 1):
+        assert conv(N) == INVALID_ARG and conv(N, None) == INVALID_ARG and conv_bwd(N) == INVALID_ARG
+        assert scan(lib, N=N, cu=at(7), G=1, ldb=16, ldc=16) == INVALID_ARG
+        assert lib.kda_ssm_scan_fwd_workspace_size(1, 4096, 256, 2, 16, N, 1) == 0
+        assert lib.kda_ssm_scan_bwd_workspace_size(1, 64, 256, 2, 16, N, 1) == 0
+    assert lib.kda_ssm_scan_fwd_workspace_size(1, 4096, 256, 2, 16, MOST_TOKENS, 1) > 0
