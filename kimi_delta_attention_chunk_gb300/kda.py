@@ -639,6 +639,8 @@ def short_conv_step(x, history, weight, bias=None, conv_act: int = 0, slots=None
     [N,C].  ``slots``/``status`` as for :func:`recurrent_step`."""
     lib = _lib if _lib is not None else load_library()
     C, W = _conv_check(x, weight, bias, conv_act)
+    if x.dim() != 2:
+        raise ValueError(f"x must be [N, {C}], got {tuple(x.shape)}")
     N = x.shape[0]
     P = history.shape[0]
     dev = _here(x, history, weight, bias, slots, y, status)
@@ -685,6 +687,8 @@ def ssm_step(u, delta, A, Bm, Cm, state, D=None, z=None, delta_bias=None, softpl
     Returns y [N,C].  ``slots``/``status`` as for :func:`recurrent_step`."""
     lib = _lib if _lib is not None else load_library()
     C, G, S = _ssm_check(u, delta, A, Bm, Cm, D, z, delta_bias)
+    if u.dim() != 2:
+        raise ValueError(f"u must be [N, {C}], got {tuple(u.shape)}")
     N = u.shape[0]
     P = state.shape[0]
     dev = _here(u, delta, A, Bm, Cm, state, D, z, delta_bias, slots, y, status)
