@@ -179,6 +179,12 @@ def _int32(*tensors):
             raise TypeError(f"expected an int32 tensor, got {t.dtype}")
 
 
+def _ints(*sizes):
+    """Sizes that the library takes as 32-bit integers (ctypes would drop their upper bits)."""
+    if max(sizes) >= 1 << 31:
+        raise ValueError(f"sizes must stay below 2**31, got {max(sizes)}")
+
+
 def _f32(*tensors):
     for t in tensors:
         if t is not None and t.dtype != torch.float32:
@@ -406,6 +412,7 @@ def recurrent_step(q, k, v, g, beta, state, scale: float | None = None, o_dtype=
             raise ValueError(f"k and g must be [{N}, {H}, {K}], v and o [{N}, {H}, {V}], beta [{N}, {H}]")
         if state.shape[1:] != (H, K, V):
             raise ValueError(f"state must be [P, {H}, {K}, {V}]")
+        _ints(state.shape[0], N, H)
         st = lib.kda_recurrent_step_slots(_at(q), _at(k), _at(v), _at(g), _at(beta), _dt(q), float(scale or 0.0),
                                           _at(state), _at(slots), state.shape[0], N, H, K, V, _at(o), _dt(o),
                                           _at(status), _stream_of(dev))
@@ -586,6 +593,7 @@ def short_conv_fwd(x, weight, bias=None, conv_act: int = 0, initial=None, cu_seq
     C, W = _conv_check(x, weight, bias, conv_act)
     B, T, _ = x.shape
     N = _sequences(x, cu_seqlens)
+    _ints(B, T, C, W, N)
     dev = _here(x, weight, bias, initial, cu_seqlens, y, final)
     _like(x, initial, y, final)
     _shape("initial", initial, (N, W - 1, C))
@@ -613,6 +621,7 @@ def short_conv_bwd(x, weight, dy, bias=None, conv_act: int = 0, initial=None, cu
     C, W = _conv_check(x, weight, bias, conv_act)
     B, T, _ = x.shape
     N = _sequences(x, cu_seqlens)
+    _ints(B, T, C, W, N)
     dev = _here(x, weight, dy, bias, initial, cu_seqlens, dfinal, workspace)
     _like(x, initial)
     _like(dy, dfinal)
@@ -643,6 +652,7 @@ def short_conv_step(x, history, weight, bias=None, conv_act: int = 0, slots=None
         raise ValueError(f"x must be [N, {C}], got {tuple(x.shape)}")
     N = x.shape[0]
     P = history.shape[0]
+    _ints(N, P, C, W)
     dev = _here(x, history, weight, bias, slots, y, status)
     if history.dtype is not x.dtype or history.shape != (P, W - 1, C):
         raise ValueError(f"history must be [P, {W - 1}, {C}] of {x.dtype}")
@@ -691,6 +701,7 @@ def ssm_step(u, delta, A, Bm, Cm, state, D=None, z=None, delta_bias=None, softpl
         raise ValueError(f"u must be [N, {C}], got {tuple(u.shape)}")
     N = u.shape[0]
     P = state.shape[0]
+    _ints(N, P, C, G, S)
     dev = _here(u, delta, A, Bm, Cm, state, D, z, delta_bias, slots, y, status)
     if y is None:
         y = torch.empty((N, C), dtype=u.dtype, device=u.device)
@@ -727,6 +738,7 @@ def ssm_scan_fwd(u, delta, A, Bm, Cm, D=None, z=None, delta_bias=None, softplus:
     C, G, S = _ssm_check(u, delta, A, Bm, Cm, D, z, delta_bias)
     B, T, _ = u.shape
     N = _sequences(u, cu_seqlens)
+    _ints(B, T, C, G, S, N)
     dev = _here(u, delta, A, Bm, Cm, D, z, delta_bias, initial_state, cu_seqlens, y, final_state, workspace)
     _like(u, y)
     _f32(initial_state, final_state)
@@ -757,6 +769,7 @@ def ssm_scan_bwd(u, delta, A, Bm, Cm, dy, D=None, z=None, delta_bias=None, softp
     C, G, S = _ssm_check(u, delta, A, Bm, Cm, D, z, delta_bias)
     B, T, _ = u.shape
     N = _sequences(u, cu_seqlens)
+    _ints(B, T, C, G, S, N)
     dev = _here(u, delta, A, Bm, Cm, dy, D, z, delta_bias, initial_state, cu_seqlens, dfinal_state, workspace)
     _f32(initial_state, dfinal_state)
     _shape("dy", dy, (B, T, C))
@@ -785,6 +798,7 @@ def pages_alloc(refs, n: int, pages=None, status=None):
     every pages call: an optional device int32 word, 5 = KDA_ERR_RANGE when a request
     was refused (a refused request changes nothing)."""
     lib = _lib if _lib is not None else load_library()
+    _ints(refs.numel(), n)
     dev = _here(refs, pages, status)
     _int32(refs, pages, status)
     _shape("pages", pages, (n,))
@@ -798,6 +812,7 @@ def pages_free(refs, pages, status=None):
     """Give back one reference of each page listed in ``pages`` (int32, any shape; -1 entries
     are skipped)."""
     lib = _lib if _lib is not None else load_library()
+    _ints(refs.numel())
     dev = _here(refs, pages, status)
     _int32(refs, pages, status)
     _check("kda_pages_free", lib.kda_pages_free(_at(refs), refs.numel(), _at(pages), pages.numel(), _at(status),
@@ -813,6 +828,7 @@ def pages_fork(tables, lens, refs, parents, children, page_tokens: int, status=N
     lib = _lib if _lib is not None else load_library()
     n = parents.numel()
     S, width = tables.shape
+    _ints(S, width, page_tokens, refs.numel(), n)
     dev = _here(tables, lens, refs, parents, children, status)
     _int32(tables, lens, refs, parents, children, status)
     _shape("lens", lens, (S,))
@@ -830,9 +846,10 @@ def pages_compact(refs, tables=None, workspace=None, status=None):
     places before it, in order; ``refs`` and the table entries follow.  Returns (src, dst),
     int32 [P // 2]: the copies to make in every pool with :func:`pages_copy` (-1: none)."""
     lib = _lib if _lib is not None else load_library()
+    P = refs.numel()
+    _ints(P)
     dev = _here(refs, tables, workspace, status)
     _int32(refs, tables, status)
-    P = refs.numel()
     src = torch.empty(P // 2, dtype=torch.int32, device=refs.device)
     dst = torch.empty(P // 2, dtype=torch.int32, device=refs.device)
     ws, ws_bytes = _workspace(int(lib.kda_pages_compact_workspace_size(P)), refs.device, workspace)
@@ -847,10 +864,11 @@ def pages_copy(pool, src, dst, workspace=None, status=None):
     onto page ``dst[i]``; -1 entries are skipped.  A destination that a later pair writes or
     another pair reads is refused."""
     lib = _lib if _lib is not None else load_library()
+    P, n = pool.shape[0], src.numel()
+    _ints(P, n)
     dev = _here(pool, src, dst, workspace, status)
     _int32(src, dst, status)
     _shape("dst", dst, src.shape)
-    P, n = pool.shape[0], src.numel()
     page_bytes = pool.numel() // P * pool.element_size() if P else 16
     ws, ws_bytes = _workspace(int(lib.kda_pages_copy_workspace_size(P, n)), pool.device, workspace)
     st = lib.kda_pages_copy(_at(pool), P, page_bytes, _at(src), _at(dst), n, _at(ws), ws_bytes, _at(status),

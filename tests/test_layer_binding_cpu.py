@@ -74,3 +74,42 @@ def test_prompts_take_batches_of_rows(lib):
         with pytest.raises(ValueError):
             kda.ssm_scan_bwd(u, u, f(C, S), v, v, u)
     assert lib.names() == []
+
+
+MANY = 2 ** 32 + 3      # three, in the library's 32 bits
+
+
+def test_sizes_past_the_librarys_integers(lib):
+    C, S = 1, 8
+    calls = [
+        lambda: kda.short_conv_fwd(t(1, MANY, C), f(C, 4)),
+        lambda: kda.short_conv_fwd(t(MANY, 1, C), f(C, 4)),
+        lambda: kda.short_conv_fwd(t(1, 8, MANY), f(MANY, 4)),
+        lambda: kda.short_conv_fwd(t(1, 8, C), f(C, 4), cu_seqlens=i(MANY)),
+        lambda: kda.short_conv_bwd(t(1, MANY, C), f(C, 4), t(1, MANY, C)),
+        lambda: kda.short_conv_step(t(MANY, C), t(MANY, 3, C), f(C, 4)),
+        lambda: kda.short_conv_step(t(2, C), t(MANY, 3, C), f(C, 4), slots=i(2)),
+        lambda: kda.ssm_step(t(MANY, C), t(MANY, C), f(C, S), t(MANY, 1, S), t(MANY, 1, S), f(MANY, C, S)),
+        lambda: kda.ssm_step(t(2, C), t(2, C), f(C, S), t(2, 1, S), t(2, 1, S), f(MANY, C, S), slots=i(2)),
+        lambda: kda.ssm_scan_fwd(t(1, MANY, C), t(1, MANY, C), f(C, S), t(1, MANY, 1, S), t(1, MANY, 1, S)),
+        lambda: kda.ssm_scan_fwd(t(1, 8, C), t(1, 8, C), f(C, S), t(1, 8, 1, S), t(1, 8, 1, S), cu_seqlens=i(MANY)),
+        lambda: kda.ssm_scan_bwd(t(1, MANY, C), t(1, MANY, C), f(C, S), t(1, MANY, 1, S), t(1, MANY, 1, S), t(1, MANY, C)),
+        lambda: kda.recurrent_step(t(2, 1, 64), t(2, 1, 64), t(2, 1, 64), t(2, 1, 64), t(2, 1), f(MANY, 1, 64, 64), slots=i(2)),
+        lambda: kda.pages_alloc(i(MANY), 5),
+        lambda: kda.pages_alloc(i(8), MANY),
+        lambda: kda.pages_free(i(MANY), i(5)),
+        lambda: kda.pages_fork(i(4, MANY), i(4), i(8), i(2), i(2), 16),
+        lambda: kda.pages_fork(i(MANY, 4), i(MANY), i(8), i(2), i(2), 16),
+        lambda: kda.pages_fork(i(4, 4), i(4), i(MANY), i(2), i(2), 16),
+        lambda: kda.pages_fork(i(4, 4), i(4), i(8), i(MANY), i(MANY), 16),
+        lambda: kda.pages_fork(i(4, 4), i(4), i(8), i(2), i(2), MANY),
+        lambda: kda.pages_compact(i(MANY)),
+        lambda: kda.pages_copy(f(MANY, 4), i(2), i(2)),
+        lambda: kda.pages_copy(f(8, 4), i(MANY), i(MANY)),
+    ]
+    for k, call in enumerate(calls):
+        with pytest.raises(ValueError, match="2\\*\\*31"):
+            call()
+        assert lib.calls == [], k
+    kda.pages_free(i(8), i(MANY))                        # any number of entries: counted in 64 bits
+    assert lib.calls[-1][1][3] == MANY
