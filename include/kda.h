@@ -666,7 +666,7 @@ KDA_API kda_status kda_ssm_scan_bwd(const void *u, int64_t ldu, const void *delt
  * the m-th free place before it.  src, dst [P / 2] are the copies to make in every
  * pool, -1 behind the last; refs and the `entries` table entries (NULL and 0: none)
  * follow.  workspace: kda_pages_compact_workspace_size bytes.  Refused: an entry that
- * is neither -1 nor a page in use (those at or behind place `used` are looked at).
+ * is neither -1 nor a page in use, which stays as it is.
  *
  * kda_pages_copy -- page dst[i] becomes a copy of page src[i] in pool [P, page_bytes]
  * (either -1: skipped).  Refused: pages out of range, and a destination that a later

@@ -336,14 +336,29 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(int32_t* tables, i
 
 // ---- closing up ------------------------------------------------------------------------------
 
-// remap[0] is the number of used pages; remap[1 + p] the new place of a used page p behind it, -1
-// of a free one.
-__device__ __forceinline__ void remap_entry(int32_t* entry, int live, int P, const int32_t* remap, int32_t* status) {
-    const int e = *entry;
-    if (e == -1 || (e >= 0 && e < live)) return;
-    const int to = e >= 0 && e < P ? remap[1 + e] : -1;
-    if (to >= 0) *entry = to;
-    else report(status);  // an entry that held no used page stays as it is
+// remap[0] is the number of used pages; remap[1 + p] the new place of a used page p behind it, -1 of a free one.  Of a
+// free page before it remap[1 + p] is the move that fills its place; of a used one it is whatever was there, so that only
+// as many words are written as there are moves, and dst[] has to confirm it.
+// The entries i, i + step, ... of four, their loads ahead of the looks at them (8192 pages with 65536 entries: 37 us one by
+// one, 25 by fours).
+__device__ __forceinline__ void remap_entries(int32_t* tables, int64_t i, int64_t step, int64_t entries, int live, int P,
+                                              const int32_t* remap, const int32_t* dst, int32_t* status) {
+    int e[kEach], to[kEach];
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) e[k] = i + k * step < entries ? tables[i + k * step] : -1;
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) to[k] = e[k] >= 0 && e[k] < P ? remap[1 + e[k]] : -1;
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+        if (e[k] == -1) continue;
+        if (e[k] >= 0 && e[k] < live) {
+            if (to[k] >= 0 && to[k] < P / 2 && dst[to[k]] == e[k]) report(status);  // it was free: another page lies there now
+        } else if (to[k] >= 0) {
+            tables[i + k * step] = to[k];
+        } else {
+            report(status);  // an entry that held no used page stays as it is
+        }
+    }
 }
 
 // Table entries that the cluster itself looks over; more are a launch of their own over the machine.
@@ -384,20 +399,24 @@ __global__ void __launch_bounds__(kThreads) pages_compact_kernel(int32_t* refs, 
             continue;
         }
         const int s = src_out[m], d = dst_out[m];
-        if (remap) remap[1 + s] = d;
+        if (remap) {
+            remap[1 + s] = d;
+            remap[1 + d] = m;
+        }
         refs[d] = refs[s];
         refs[s] = 0;
     }
     if (entries == 0) return;
     cl.sync();
-    for (int i = first; i < entries; i += step) remap_entry(tables + i, live, P, remap, status);
+    for (int i = first; i < entries; i += kEach * step) remap_entries(tables, i, step, entries, live, P, remap, dst_out, status);
 }
 
 __global__ void __launch_bounds__(256) pages_remap_kernel(int32_t* tables, int64_t entries, int P, const int32_t* remap,
-                                                          int32_t* status) {
+                                                          const int32_t* dst, int32_t* status) {
     const int live = remap[0];
-    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < entries; i += gridDim.x * 256ll)
-        remap_entry(tables + i, live, P, remap, status);
+    const int64_t step = gridDim.x * 256ll;
+    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < entries; i += kEach * step)
+        remap_entries(tables, i, step, entries, live, P, remap, dst, status);
 }
 
 // ---- copying ---------------------------------------------------------------------------------
@@ -555,7 +574,7 @@ cudaError_t pages_compact(int32_t* refs, int P, int32_t* tables, int64_t entries
                                    one ? (int)entries : 0, status);
     if (e != cudaSuccess || one) return e;
     const int64_t blocks = (entries + 255) / 256;
-    pages_remap_kernel<<<(unsigned)(blocks < 1216 ? blocks : 1216), 256, 0, st>>>(tables, entries, P, remap, status);
+    pages_remap_kernel<<<(unsigned)(blocks < 1216 ? blocks : 1216), 256, 0, st>>>(tables, entries, P, remap, dst, status);
     return cudaGetLastError();
 }
 
