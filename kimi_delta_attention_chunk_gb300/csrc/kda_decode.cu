@@ -22,7 +22,7 @@ constexpr int kDecodeThreads = 256;
 
 // kSlots: state is a pool of P pages [H, K, V], and row n works on page slots[n] (a row without a
 // page, or refused, leaves its state and its row of o alone).  The page's loads are issued before
-// the slots are looked through for repeats, which they hide.
+// the slots are looked through for repeats, which they hide; a row without a page loads none.
 template <typename TIn, typename TOut, int K, int V, bool kSlots>
 __global__ void __launch_bounds__(kDecodeThreads, 2)
 decode_step_kernel(const TIn* __restrict__ q, const TIn* __restrict__ k,
@@ -46,7 +46,11 @@ decode_step_kernel(const TIn* __restrict__ q, const TIn* __restrict__ k,
     if constexpr (kSlots) {
         row = (int)(nh / H);
         page[0] = page_of_row(slots, row, P);
-        at = (int64_t)max(page[0], 0) * H + nh % H;
+        if (page[0] < 0) {
+            if (page[0] != -1 && status && tid == 0) *status = KDA_ERR_RANGE;
+            return;
+        }
+        at = (int64_t)page[0] * H + nh % H;
     }
     float4* S = reinterpret_cast<float4*>(state + at * K * V);
     float4 s[RPT];
