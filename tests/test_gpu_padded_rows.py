@@ -51,3 +51,33 @@ def test_recurrent_step(N, H, K, V, dtype):
         o = torch.full((args[0].shape[0], H, V), 3.0, device="cuda")
         return kda.recurrent_step(*args, pages, o=o, slots=slots, status=status)
     check(N, live, slots, P, pool, run)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("N,C,S", [(1, 40, 8), (6, 40, 16), (7, 130, 64), (301, 1024, 16), (300, 600, 32)])
+def test_scan_step(N, C, S, dtype):
+    g, P, slots, live = batch(N, 4100 + N)
+    pool = torch.randn(P, C, S, generator=g).cuda()
+    u, delta, z = (torch.randn(N, C, generator=g).to(dtype).cuda() for _ in range(3))
+    B, Cm = (torch.randn(N, 1, S, generator=g).to(dtype).cuda() for _ in range(2))
+    A, D = -torch.rand(C, S, generator=g).cuda(), torch.randn(C, generator=g).cuda()
+
+    def run(rows, pages, slots, status):
+        x = [a if rows is None else a[rows].contiguous() for a in (u, delta, B, Cm, z)]
+        y = torch.full(x[0].shape, 3.0, dtype=dtype, device="cuda")
+        return kda.ssm_step(x[0], x[1], A, x[2], x[3], pages, D=D, z=x[4], slots=slots, status=status, y=y)
+    check(N, live, slots, P, pool, run)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("N,C,W", [(1, 40, 4), (6, 37, 3), (301, 2048, 4), (998, 600, 2)])
+def test_convolution_step(N, C, W, dtype):
+    g, P, slots, live = batch(N, 4200 + N)
+    pool, x = torch.randn(P, W - 1, C, generator=g).to(dtype).cuda(), torch.randn(N, C, generator=g).to(dtype).cuda()
+    w = torch.randn(C, W, generator=g).cuda()
+
+    def run(rows, pages, slots, status):
+        a = x if rows is None else x[rows].contiguous()
+        y = torch.full(a.shape, 3.0, dtype=dtype, device="cuda")
+        return kda.short_conv_step(a, pages, w, conv_act=1, slots=slots, status=status, y=y)
+    check(N, live, slots, P, pool, run)
