@@ -485,8 +485,10 @@ KDA_API kda_status kda_chunk_bwd(const void *q, const void *k, const void *v, co
  *          refused: the row's state and o are left as they are.
  *  status  optional device word (4-byte aligned): KDA_OK, or KDA_ERR_RANGE if a row
  *          was refused.
- * Everything else as kda_recurrent_step; N * H < 2^31.
+ * Everything else as kda_recurrent_step; N * H < 2^31, N <= KDA_MOST_SLOTS (every row's
+ * slot is compared with those of the rows before it).
  */
+#define KDA_MOST_SLOTS (1 << 18)
 KDA_API kda_status kda_recurrent_step_slots(const void *q, const void *k, const void *v, const void *g,
                                     const void *beta, kda_dtype in_dtype, float scale, float *pool,
                                     const int32_t *slots, int P, int N, int H, int K, int V, void *o,
@@ -549,7 +551,7 @@ KDA_API kda_status kda_short_conv_bwd(const void *x, int64_t ldx, const float *w
  * kda_short_conv_step -- one token of each of N sequences: y [N, C] from x [N, C] (rows
  * ldx apart) and the histories in the pool `history` [P, W-1, C], which move on by one
  * token.  slots [N] and status as kda_recurrent_step_slots; slots NULL: row i works on
- * page i (P >= N).  N <= 2^30.
+ * page i (P >= N).  N <= 2^30, with slots KDA_MOST_SLOTS.
  */
 KDA_API kda_status kda_short_conv_step(const void *x, int64_t ldx, const float *weight, const float *bias,
                                int conv_act, kda_dtype dtype, void *history, const int32_t *slots, int P,
@@ -568,7 +570,8 @@ KDA_API kda_status kda_short_conv_step(const void *x, int64_t ldx, const float *
  *  softplus 0 or 1.
  *  state  fp32 pool [P, C, S], 32-byte aligned, updated in place; slots, P, status as
  *         kda_short_conv_step.
- * S in {8, 16, 32, 64}; C a multiple of G, C <= 2^20; N <= 2^30, and N C S / 1024 < 2^31.
+ * S in {8, 16, 32, 64}; C a multiple of G, C <= 2^20; N <= 2^30, with slots
+ * KDA_MOST_SLOTS, and N C S / 1024 < 2^31.
  */
 KDA_API kda_status kda_ssm_step(const void *u, int64_t ldu, const void *delta, int64_t ldd, const float *A,
                         const void *Bm, int64_t ldb, const void *Cm, int64_t ldc, const float *D,

@@ -226,6 +226,7 @@ kda_status kda_recurrent_step_slots(const void* q, const void* k, const void* v,
     if (s != KDA_OK) return s;
     if (P < 0 || (N > 0 && (P == 0 || !slots)) || (uintptr_t)slots % 4 || (uintptr_t)status % 4) return KDA_ERR_INVALID_ARG;
     if ((int64_t)N * H > 0x7fffffffLL) return KDA_ERR_INVALID_ARG;
+    if (N > KDA_MOST_SLOTS) return KDA_ERR_UNSUPPORTED;
     cudaStream_t st = (cudaStream_t)stream;
     if (status && cudaMemsetAsync(status, 0, sizeof(int32_t), st) != cudaSuccess) return KDA_ERR_CUDA;
     if (N == 0) return KDA_OK;

@@ -169,7 +169,7 @@ kda_status kda_short_conv_step(const void* x, int64_t ldx, const float* weight, 
                                kda_dtype dtype, void* history, const int32_t* slots, int P, int N, int C, int W,
                                void* y, int32_t* status, void* stream) {
     if (N < 0 || P < 0 || C <= 0) return KDA_ERR_INVALID_ARG;
-    if (!dtype_ok(dtype) || C > kMostChannels || N > kMostRows) return KDA_ERR_UNSUPPORTED;
+    if (!dtype_ok(dtype) || C > kMostChannels || N > kMostRows || (slots && N > KDA_MOST_SLOTS)) return KDA_ERR_UNSUPPORTED;
     const kda_status s = check_conv(ldx, weight, bias, C, W, conv_act);
     if (s != KDA_OK) return s;
     const size_t es = size_of(dtype);
@@ -193,7 +193,8 @@ kda_status kda_ssm_step(const void* u, int64_t ldu, const void* delta, int64_t l
                         const float* delta_bias, int softplus, kda_dtype dtype, float* state, const int32_t* slots,
                         int P, int N, int C, int G, int S, void* y, int32_t* status, void* stream) {
     if (N < 0 || P < 0 || C <= 0 || G <= 0 || C % G != 0) return KDA_ERR_INVALID_ARG;
-    if (!dtype_ok(dtype) || (S != 8 && S != 16 && S != 32 && S != 64) || C > kMostChannels || N > kMostRows)
+    if (!dtype_ok(dtype) || (S != 8 && S != 16 && S != 32 && S != 64) || C > kMostChannels || N > kMostRows ||
+        (slots && N > KDA_MOST_SLOTS))
         return KDA_ERR_UNSUPPORTED;
     if (softplus != 0 && softplus != 1) return KDA_ERR_INVALID_ARG;
     const int64_t vec = (int64_t)G * S;

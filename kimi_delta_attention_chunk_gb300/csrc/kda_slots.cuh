@@ -20,8 +20,9 @@ __device__ __forceinline__ int page_of_row(const int32_t* slots, int i, int P) {
 // rows, slots out of range, and slots that an earlier row of the batch has (no two rows may write one
 // page); the last two set *status to KDA_ERR_RANGE.  Every thread of the block calls it, once a
 // kernel.  The repeats are found by reading the slots before the rows, row0 / blockDim loads a thread
-// and one meeting of the block: the blocks of one row all do it, but next to a page's bytes it is
-// little.
+// and one meeting of the block, in all blocks of the row.  That is little next to a page's bytes for some thousand
+// rows and grows with their square: a convolution of 768 channels takes 26 us with slots and 20 without for 4096 rows, 104
+// and 44 for 16384, 1426 and 132 for 65536; 29 ms for the most rows, KDA_MOST_SLOTS, so that every call ends soon.
 template <int kRows>
 __device__ __forceinline__ unsigned rows_refused(const int32_t* slots, int row0, int N, const int (&page)[kRows],
                                                  int32_t* status) {

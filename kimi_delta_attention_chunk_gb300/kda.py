@@ -392,8 +392,8 @@ def recurrent_step(q, k, v, g, beta, state, scale: float | None = None, o_dtype=
     q, k, g: [N,H,K]; v: [N,H,V]; beta: [N,H].  Returns o [N,H,V].  With ``slots``
     (device int32 [N]) ``state`` is a pool [P,H,K,V] and row i works on page
     ``slots[i]`` (-1: a padded row; its row of o is left as it is, so pass ``o`` to
-    keep its contents).  ``status``: an optional device int32 word, 5 =
-    KDA_ERR_RANGE when a row's slot was out of range or an earlier row's.
+    keep its contents); at most 2**18 rows.  ``status``: an optional device int32 word,
+    5 = KDA_ERR_RANGE when a row's slot was out of range or an earlier row's.
     """
     lib = load_library()
     N, H, K = q.shape

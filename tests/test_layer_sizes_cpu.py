@@ -4,7 +4,7 @@ import pytest
 
 import kimi_delta_attention_chunk_gb300 as kda
 from kimi_delta_attention_chunk_gb300 import build as kbuild
-from tests.test_layer_abi_cpu import INVALID_ARG, at, scan
+from tests.test_layer_abi_cpu import INVALID_ARG, UNSUPPORTED, at, scan
 
 MOST_TOKENS = 2 ** 31 - 65536 - 1
 
@@ -49,3 +49,22 @@ def test_number_of_sequences(lib):
         assert lib.kda_ssm_scan_fwd_workspace_size(1, 4096, 256, 2, 16, N, 1) == 0
         assert lib.kda_ssm_scan_bwd_workspace_size(1, 64, 256, 2, 16, N, 1) == 0
     assert lib.kda_ssm_scan_fwd_workspace_size(1, 4096, 256, 2, 16, MOST_TOKENS, 1) > 0
+
+
+def test_rows_with_slots(lib):
+    """Every row's slot is compared with those before it: a number of rows whose square stays small."""
+    most = 1 << 18
+
+    def conv(N, P, slots):
+        return lib.kda_short_conv_step(at(1), 8, at(2), None, 0, 1, at(3), slots, P, N, 8, 4, at(5), None, None)
+
+    def ssm(N, P, slots):
+        return lib.kda_ssm_step(at(1), 8, at(2), 8, at(3), at(4), 8, at(5), 8, None, None, 0, None, 0, 1, at(6), slots, P, N, 8, 1, 8, at(8),
+                                None, None)
+
+    def step(N):
+        return lib.kda_recurrent_step_slots(at(1), at(4), at(5), at(6), at(7), 1, 0.0, at(2), at(3), 8, N, 1, 128, 128, at(8), 0, None, None)
+    for P in (8, 1 << 20):
+        assert conv(most + 1, P, at(4)) == UNSUPPORTED and ssm(most + 1, P, at(7)) == UNSUPPORTED
+    assert step(most + 1) == UNSUPPORTED
+    assert conv(most, 8, at(4, 1)) == INVALID_ARG and ssm(most, 8, at(7, 1)) == INVALID_ARG      # so many are looked at
