@@ -645,7 +645,8 @@ KDA_API kda_status kda_ssm_scan_bwd(const void *u, int64_t ldu, const void *delt
  * arguments alone: the lowest free pages are given out first, requests are served in
  * order.  status: optional device word, KDA_OK or KDA_ERR_RANGE if a request was
  * refused; a refused request changes nothing, the others are carried out.  At most
- * 2^30 pages and list entries (kda_pages_free: any number of entries).
+ * 2^30 pages and list entries (kda_pages_free and the entries of kda_pages_compact: any
+ * number).  With P = 0 kda_pages_compact and kda_pages_copy do nothing.
  *
  * kda_pages_alloc -- pages[i] = the i-th free page, with refs 1; -1 (refused) where
  * there are no more.

@@ -16,7 +16,12 @@
 //
 // 70k x 12288 bf16 forwards with histories: 554 us, 6.2 TB/s, 91% of a copy's rate.  4096 x 12288 backwards: 65.5 us, 4.6
 // TB/s, bound by issue (2.05 instructions a cycle and SM) and by one filling's start and end; 32,768 tokens 5.6 TB/s.
-// One token of 256 sequences: 12.3 us, 4.1 TB/s, latency.
+// One token of 256 sequences: 12.3 us, 4.1 TB/s: 768 blocks in 456 places (142 registers a thread leave three blocks an SM),
+// each a chain of slot, history and store.
+//
+// Rows that are no whole pieces go one channel a thread: 16384 x 12290 forwards in 419 us where 12288 take 139, 4096 x 12290
+// backwards in 186 where 12288 take 63, 256 rows of one token in 16.6 where they take 9.8 (graph replays).  Two bytes have no
+// asynchronous copy, so nothing is on its way while a batch is worked on, and one channel does the work of a pair.
 #include "kda_layer.h"
 #include "kda_segments.cuh"
 #include "kda_slots.cuh"
@@ -28,7 +33,8 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kSms = 152;
-// Blocks of an SM that the kernels are built for.  Five forwards (70k x 12288 in 565 us, 600 with four);
+// Blocks of an SM that the kernels are built for.  Five forwards (70k x 12288 in 565 us, 600 with four, although the
+// instance of eight bf16 channels and four taps then spills 62 bytes, the only one that does);
 // three backwards, with 168 registers a thread (4096 x 12288 in 68 us, 72 with four, 82 with five, which spill).
 constexpr int kFwdResident = 5, kBwdResident = 3;
 constexpr int kTile = 64;     // tokens of one look at the sequence boundaries

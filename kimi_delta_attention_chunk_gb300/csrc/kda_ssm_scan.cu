@@ -373,7 +373,7 @@ Plan plan(const SsmScanParams& p) {
     int run = (p.total + want - 1) / want;
     run = (run + kRunStep - 1) / kRunStep * kRunStep;
     // The prefix takes longer the more runs there are: 4096 tokens of 128 channels, S = 16, 29 us with 96 runs, 32
-    // with 64 and 37 with 256; 16384 of 512 channels 101, 107 and 90.
+    // with 64 and 37 with 256.  Where a run has more blocks the cap costs something: 16384 of 512 channels take 101, 107 and 90.
     constexpr int kMostRuns = 96;
     const int least = (p.total + kMostRuns - 1) / kMostRuns;
     if (run < least) run = (least + kRunStep - 1) / kRunStep * kRunStep;

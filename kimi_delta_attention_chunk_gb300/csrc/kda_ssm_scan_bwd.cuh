@@ -17,11 +17,11 @@
 //      recomputed into registers.
 // A lane has eight states of a channel in step 3: fewer lanes share a channel's scalars and shuffles, and
 // twelve warps an SM fit with their states in 168 registers.  (Four states a lane, chunks not halved, and
-// the sums over channels by shuffles took 640 us where step 3 takes 384 for 2 x 2048 x 4096 x 16.)
+// the sums over channels by shuffles took 640 us where step 3 takes 374 for 2 x 2048 x 4096 x 16.)
 // Sums over channels (dB, dC) go through shared memory, 16 additions a lane and token, then the block's
 // warps, and partial sums of the channel blocks; sums over tokens through partial sums of the chunks.
-// Every sum has an order fixed by the sizes.  Instruction issue bounds steps 1 and 3 (2.3 and 2.05 a cycle and SM):
-// 2 x 2048 x 4096 x 16 bf16 with every gradient takes 536 us, 118 + 19 + 384 in the steps and 21 in the last sums.
+// Every sum has an order fixed by the sizes.  Instruction issue bounds steps 1 and 3 (2.3 and 2.1 a cycle and SM):
+// 2 x 2048 x 4096 x 16 bf16 with every gradient takes 526 us, 119 + 19 + 374 in the steps and 21 in the last sums.
 #pragma once
 
 #include <stddef.h>
@@ -843,8 +843,8 @@ cudaError_t launch(const SsmScanParams& p, cudaStream_t st) {
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const int64_t states = (int64_t)p.C * S;
-    // Each of the others may start while the one before it ends, as in the forward scan (2 x 2048 x 4096 x 16 in 536 us,
-    // 544 without; 64 tokens of 512 channels 26 and 28).
+    // Each of the others may start while the one before it ends, as in the forward scan (2 x 2048 x 4096 x 16 takes 8 us
+    // less so; 64 tokens of 512 channels 26 us, 28 without).
     e = tc::launch_dependent(scan_bwd_prefix_kernel, dim3((unsigned)((states + 127) / 128), 2), 128, 0, st, p.A, w, chunks, p.C, S);
     if (e != cudaSuccess) return e;
     constexpr int smem = sizeof(BwdShared<S>);

@@ -843,8 +843,9 @@ def pages_fork(tables, lens, refs, parents, children, page_tokens: int, status=N
 
 def pages_compact(refs, tables=None, workspace=None, status=None):
     """Close up the pools: used pages behind the number of used pages move into the free
-    places before it, in order; ``refs`` and the table entries follow.  Returns (src, dst),
-    int32 [P // 2]: the copies to make in every pool with :func:`pages_copy` (-1: none)."""
+    places before it, in order; ``refs`` and the table entries follow (an entry that names a
+    free page stays as it is and is reported).  Returns (src, dst), int32 [P // 2]: the
+    copies to make in every pool with :func:`pages_copy` (-1: none)."""
     lib = _lib if _lib is not None else load_library()
     P = refs.numel()
     _ints(P)
