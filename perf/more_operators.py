@@ -13,7 +13,7 @@ own = False
 DTYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
 DECAY = 8.0  # the recurrence's exponent scale
 EPS = 1e-5
-BLOCK = 64   # a forward pass leaves the state before every 64th token to the backward pass
+BLOCK = 32   # a forward pass leaves the state before every 32nd token to the backward pass
 
 
 # ---- cases -------------------------------------------------------------------------------
