@@ -633,6 +633,115 @@ KDA_API kda_status kda_ssm_scan_bwd(const void *u, int64_t ldu, const void *delt
                             void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * kda_gated_scan_fwd -- a gated linear recurrence over the tokens of N sequences, one state a
+ * channel, whose decay and whose input are gated by logits of their own:
+ *
+ *     s = decay softplus(lam) sigmoid(r),   a = e^-s,
+ *     h <- a h + sqrt(1 - a^2) sigmoid(i) x,   y = h (z sigmoid(z))
+ *
+ *  x, r, i, z [B, T, C] (rows ldx, ldr, ldi, ldz >= C apart; z may be NULL: y = h), y [B, T, C]:
+ *           element type dtype.
+ *  lam      fp32 [C]; decay > 0, finite.
+ *  initial_state fp32 [N, C] or NULL for zeros; final_state the same or NULL (of a sequence
+ *           without tokens: its initial state); they must not overlap.
+ *  cu_seqlens, B, T, N   as kda_short_conv_fwd; rows that belong to no sequence are left as
+ *           they are.
+ *  states   fp32 [B, ceil(T / 32), C] or NULL: the state before tokens 0, 32, 64 ... of each
+ *           batch row (zeros where a sequence begins), for kda_gated_scan_bwd.
+ * B ceil(C / 64) <= 2^28 - 1.  sigmoid(i) and sigmoid(z) end at 2^-60.
+ */
+KDA_API kda_status kda_gated_scan_fwd(const void *x, int64_t ldx, const void *r, int64_t ldr, const void *i,
+                              int64_t ldi, const float *lam, const void *z, int64_t ldz, float decay,
+                              kda_dtype dtype, const float *initial_state, const int32_t *cu_seqlens, int B,
+                              int T, int C, int N, void *y, float *final_state, float *states,
+                              void *stream);
+
+/*
+ * kda_gated_scan_bwd -- gradients of L = <dy, y> + <dfinal_state, final_state> through
+ * kda_gated_scan_fwd; with m = sqrt(1 - a^2), sr = sigmoid(r), si = sigmoid(i), yb = dy silu(z):
+ *
+ *     dh_t = yb_t + a_{t+1} dh_{t+1},   ds = dh (si x a^2 / m - a h_{t-1}),
+ *     dx = dh m si,   di = dh m x si (1 - si),   dr = ds s (1 - sr),   dz = dy h silu'(z),
+ *     dlam = decay sigmoid(lam) sum_t ds sr,   dinitial_state = a_0 dh_0
+ *
+ *  dy, dx, dr, di, dz [B, T, C]: contiguous, element type grad_dtype (KDA_F32, or KDA_BF16 with a
+ *  KDA_BF16 dtype).  dz is given exactly if z is.
+ *  dfinal_state, dinitial_state fp32 [N, C] or NULL; dlam fp32 [C].
+ *  states   what the forward call on the same inputs left, or NULL (made again in the workspace:
+ *           x, r and i are then read twice).
+ *  workspace  at least kda_gated_scan_bwd_workspace_size bytes, 16-byte aligned.
+ * Sums are fp32, in an order fixed by the sizes.  Rows that belong to no sequence have zeros in
+ * dx, dr, di and dz, whatever they hold.  Where 1 - a^2 is below 1e-36, 1 / m is taken as 1e18.  The
+ * rest as kda_gated_scan_fwd.
+ */
+KDA_API size_t kda_gated_scan_bwd_workspace_size(int B, int T, int C, int N, int packed, int have_states);
+KDA_API kda_status kda_gated_scan_bwd(const void *x, int64_t ldx, const void *r, int64_t ldr, const void *i,
+                              int64_t ldi, const float *lam, const void *z, int64_t ldz, float decay,
+                              kda_dtype dtype, const float *initial_state, const int32_t *cu_seqlens, int B,
+                              int T, int C, int N, const void *dy, const float *dfinal_state,
+                              kda_dtype grad_dtype, const float *states, void *dx, void *dr, void *di,
+                              float *dlam, void *dz, float *dinitial_state, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
+/*
+ * kda_gated_step -- one token of each of N sequences through kda_gated_scan_fwd's recurrence:
+ * y [N, C] from x, r, i, z [N, C] (rows ldx, ldr, ldi, ldz apart) and the states in the fp32 pool
+ * `state` [P, C], updated in place.  slots, P, N, status as kda_short_conv_step, and
+ * N ceil(C / 128) < 2^31.
+ */
+KDA_API kda_status kda_gated_step(const void *x, int64_t ldx, const void *r, int64_t ldr, const void *i, int64_t ldi,
+                          const float *lam, const void *z, int64_t ldz, float decay, kda_dtype dtype,
+                          float *state, const int32_t *slots, int P, int N, int C, void *y, int32_t *status,
+                          void *stream);
+
+/*
+ * kda_group_norm_fwd -- group norm with an activation, channels last:
+ *
+ *     p = weight (x - mean) / sqrt(var + eps) + bias,   y = p or p sigmoid(p)
+ *
+ * with mean and (biased) variance over the C / G channels of a group: of one token
+ * (over_sequence = 0), or of all tokens of a sequence (over_sequence = 1).
+ *
+ *  x        [B, T, C], rows ldx >= C apart; y [B, T, C]: element type dtype.
+ *  weight, bias  fp32 [C] or NULL for ones and zeros.  eps > 0, finite.
+ *  act      0: none, 1: SiLU.
+ *  cu_seqlens, B, T, N   as kda_short_conv_fwd; over tokens cu_seqlens is NULL (every row is
+ *           normalised).  Rows that belong to no sequence are left as they are.
+ *  stats    over sequences: fp32 [N, G, 2] (8-byte aligned) or NULL, mean and 1 / sqrt(var + eps),
+ *           for kda_group_norm_bwd (of a sequence without tokens: 0 and 1 / sqrt(eps)).
+ *  workspace  at least kda_group_norm_fwd_workspace_size bytes, 16-byte aligned (0 over tokens).
+ * C a multiple of G; over tokens C / G <= 16384.
+ */
+KDA_API size_t kda_group_norm_fwd_workspace_size(int B, int T, int C, int G, int N, int over_sequence, int packed,
+                                                 int have_stats);
+KDA_API kda_status kda_group_norm_fwd(const void *x, int64_t ldx, const float *weight, const float *bias, float eps,
+                              int act, int over_sequence, kda_dtype dtype, const int32_t *cu_seqlens, int B,
+                              int T, int C, int G, int N, void *y, float *stats, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
+/*
+ * kda_group_norm_bwd -- gradients of L = <dy, y> through kda_group_norm_fwd; with dp = dy act'(p),
+ * q = weight dp, xh = (x - mean) / sqrt(var + eps) and means over the group:
+ *
+ *     dx = (q - mean(q) - xh mean(q xh)) / sqrt(var + eps),   dweight = sum dp xh,   dbias = sum dp
+ *
+ *  dy, dx [B, T, C]: contiguous, element type grad_dtype (KDA_F32, or KDA_BF16 with a KDA_BF16
+ *  dtype).  dweight, dbias fp32 [C] or NULL.
+ *  stats    over sequences: what the forward call on the same inputs left, or NULL (x is then read
+ *           once more).
+ *  workspace  at least kda_group_norm_bwd_workspace_size bytes, 16-byte aligned.
+ * Sums are fp32, in an order fixed by the sizes.  The dx of rows that belong to no sequence is
+ * zero, whatever they hold.  The rest as kda_group_norm_fwd.
+ */
+KDA_API size_t kda_group_norm_bwd_workspace_size(int B, int T, int C, int G, int N, int over_sequence, int packed,
+                                                 int have_stats);
+KDA_API kda_status kda_group_norm_bwd(const void *x, int64_t ldx, const float *weight, const float *bias, float eps,
+                              int act, int over_sequence, kda_dtype dtype, const int32_t *cu_seqlens, int B,
+                              int T, int C, int G, int N, const void *dy, kda_dtype grad_dtype,
+                              const float *stats, void *dx, float *dweight, float *dbias, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
+/*
  * Pages of a cache.  A pool holds P pages (a sequence's recurrent state, its
  * convolution history, or page_tokens tokens' rows); several pools (layers) can go by
  * one set of books:

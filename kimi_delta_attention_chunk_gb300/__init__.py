@@ -18,6 +18,12 @@ from .kda import (  # noqa: F401
     chunk_fwd_noalloc,
     gate_proj,
     gate_proj_workspace_size,
+    gated_scan_bwd,
+    gated_scan_fwd,
+    gated_scan_states,
+    gated_step,
+    group_norm_bwd,
+    group_norm_fwd,
     inject_wait_timeout,
     library_path,
     load_library,

@@ -1,0 +1,493 @@
+// Group norm with an activation, channels last, over the tokens of a sequence and a group's channels (the formulas stand in
+// kda_group_norm.cuh).
+//
+// The statistics of a whole sequence come before its first output, so x (and dy) are read twice: by a pass over runs of tokens that
+// leaves partial sums a channel, and by the pass that writes.  Runs are cut at fixed places of the token stream; a run and a sequence that meet
+// make a piece, and piece (run + sequence) has a place of its own in the scratch.  Sums are joined in a fixed order.  Variances:
+// the mean of four rows and the squares around it, joined with those of the rows before (and so on up), so that neither a mean far from zero nor a
+// first token far from the others costs digits.
+#include "kda_group_norm.cuh"
+
+namespace kda {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kPieces = 32;                   // row pieces of a block, side by side
+constexpr int kSubs = kThreads / kPieces;     // rows of a block at a time
+constexpr int kAhead = 4;                     // rows of a thread requested together
+
+struct Cut {
+    int run, runs;
+};
+// Runs of tokens: about `resident` blocks an SM, 64 tokens at least.
+Cut cut_of(const NormParams& p, int blocks, int resident) {
+    Cut q;
+    int want = kSms * resident / blocks;
+    if (want < 1) want = 1;
+    q.run = p.total / want + (p.total % want != 0);
+    q.run = (q.run + 63) / 64 * 64;
+    if (q.run < 64) q.run = 64;
+    q.runs = p.total / q.run + (p.total % q.run != 0);
+    if (q.runs < 1) q.runs = 1;
+    return q;
+}
+
+// The sequences that meet tokens [r0, r1) one after another: f(n, first token, one behind the last).  Whole warps call it.
+template <typename F>
+__device__ __forceinline__ void each_piece(const SeqMap& m, int r0, int r1, F f) {
+    int n = max(m.begun_before(r0 + 1) - 1, 0);
+    for (; n < m.N; ++n) {
+        const int s = m.begin(n);
+        if (s >= r1) break;
+        const int b = max(s, r0), e = min(m.end(n), r1);
+        if (b < e) f(n, b, e);
+    }
+}
+
+template <int VEC>
+struct ChannelSums {
+    static constexpr int N2 = (VEC + 1) / 2;
+    f2 a[N2], b[N2];
+};
+// Adds the block's rows of sums together (in the order of the rows) and stores them, [2][C] at `to`.
+template <int VEC>
+__device__ __forceinline__ void store_sums(const ChannelSums<VEC>& s, f2 (*join)[kThreads], float* to, int C, int c, bool on) {
+    constexpr int N2 = ChannelSums<VEC>::N2;
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < N2; ++e) join[e][threadIdx.x] = v ? s.b[e] : s.a[e];
+        __syncthreads();
+        if (threadIdx.x < kPieces && on) {
+#pragma unroll
+            for (int e = 0; e < N2; ++e) {
+                f2 t = join[e][threadIdx.x];
+                for (int r = 1; r < kSubs; ++r) t = add2(t, join[e][threadIdx.x + r * kPieces]);
+                float x, y;
+                unpack(t, x, y);
+                to[(int64_t)v * C + c + 2 * e] = x;
+                if (2 * e + 1 < VEC) to[(int64_t)v * C + c + 2 * e + 1] = y;
+            }
+        }
+    }
+}
+
+// n, mean and sum of squares around it, joined with those of nb more values (the same counts in both halves).
+struct Moments {
+    f2 mean, m2;
+    __device__ __forceinline__ void join(float n, float nb, const Moments& b) {
+        const float share = nb * rcp(n + nb);
+        const f2 d = add2(b.mean, neg2(mean));
+        mean = fma2(d, both(share), mean);
+        m2 = fma2(mul2(d, d), both(n * share), add2(m2, b.m2));
+    }
+};
+
+// Per piece and channel the mean and the sum of squares around it: pieces[run + n][2][C].
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kThreads) seq_moments_kernel(NormParams p, SeqMap m, int run, float* pieces) {
+    constexpr int N2 = (VEC + 1) / 2;
+    __shared__ Moments join[N2][kThreads];
+    const int piece = threadIdx.x % kPieces, sub = threadIdx.x / kPieces, c = (blockIdx.x * kPieces + piece) * VEC;
+    const bool on = c < p.C;
+    const int r0 = blockIdx.y * run, r1 = (int)min((int64_t)m.total, (int64_t)r0 + run);
+    const T* const x = static_cast<const T*>(p.x) + (on ? c : 0);
+    each_piece(m, r0, r1, [&](int n, int b, int e) {
+        Moments mine[N2];
+#pragma unroll
+        for (int i = 0; i < N2; ++i) mine[i] = Moments{0ull, 0ull};
+        float seen = 0.f;
+        for (int t = b + sub; t < e; t += kSubs * kAhead) {
+            Row<T, VEC> rows[kAhead];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j)
+                if (t + j * kSubs < e) rows[j].load(x + (int64_t)(t + j * kSubs) * p.ldx);
+            const int have = min(kAhead, (e - t + kSubs - 1) / kSubs);
+            const float inv = have == kAhead ? 1.f / kAhead : 1.f / (float)have;
+            f2 v[kAhead][N2];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                if (j >= have) rows[j] = rows[0];  // (counts for nothing)
+                rows[j].to(v[j]);
+            }
+#pragma unroll
+            for (int i = 0; i < N2; ++i) {
+                Moments few{0ull, 0ull};
+#pragma unroll
+                for (int j = 0; j < kAhead; ++j)
+                    if (j < have) few.mean = add2(few.mean, v[j][i]);
+                few.mean = mul2(few.mean, both(inv));
+#pragma unroll
+                for (int j = 0; j < kAhead; ++j) {
+                    const f2 d = add2(v[j][i], neg2(few.mean));
+                    if (j < have) few.m2 = fma2(d, d, few.m2);
+                }
+                mine[i].join(seen, (float)have, few);
+            }
+            seen += (float)have;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < N2; ++i) join[i][threadIdx.x] = mine[i];
+        __syncthreads();
+        if (threadIdx.x >= kPieces || !on) return;
+        float* const to = pieces + (int64_t)(blockIdx.y + n) * 2 * p.C + c;
+        for (int r = 1; r < kSubs && b + r < e; ++r) {
+            const float more = (float)((e - b - r + kSubs - 1) / kSubs);
+#pragma unroll
+            for (int i = 0; i < N2; ++i) mine[i].join(seen, more, join[i][threadIdx.x + r * kPieces]);
+            seen += more;
+        }
+#pragma unroll
+        for (int i = 0; i < N2; ++i) {
+            float x0, x1, q0, q1;
+            unpack(mine[i].mean, x0, x1);
+            unpack(mine[i].m2, q0, q1);
+            to[2 * i] = x0;
+            to[p.C + 2 * i] = q0;
+            if (2 * i + 1 < VEC) {
+                to[2 * i + 1] = x1;
+                to[p.C + 2 * i + 1] = q1;
+            }
+        }
+    });
+}
+
+// Sums of `v` over the block's threads, in a fixed order; everyone gets it.
+__device__ __forceinline__ float block_sum(float v, float* buf) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    __syncthreads();
+    if (threadIdx.x % 32 == 0) buf[threadIdx.x / 32] = v;
+    __syncthreads();
+    v = 0.f;
+    for (int k = 0; k < (int)blockDim.x / 32; ++k) v += buf[k];
+    return v;
+}
+
+// The pieces of a sequence: those of the runs from its first token's to its last one's.
+struct PieceRange {
+    int n, b, e, run, first, count;
+    __device__ __forceinline__ PieceRange(const SeqMap& m, int n, int run) : n(n), b(m.begin(n)), e(m.end(n)), run(run) {
+        first = b / run;
+        count = e > b ? (e - 1) / run - first + 1 : 0;
+    }
+    __device__ __forceinline__ int64_t place(int k) const { return (int64_t)(first + k) + n; }
+    __device__ __forceinline__ int tokens(int k) const {
+        const int64_t r0 = (int64_t)(first + k) * run;
+        return (int)(min((int64_t)e, r0 + run) - max((int64_t)b, r0));
+    }
+};
+
+// mean and 1 / deviation of every sequence and group from the pieces: stats [N][G][2], a block each in turn.
+__global__ void __launch_bounds__(128) seq_stats_kernel(NormParams p, SeqMap m, int run, const float* pieces, float* stats) {
+    __shared__ float buf[4];
+    const int cg = p.C / p.G;
+    tc::grid_dep_wait();
+    for (int64_t i = blockIdx.x; i < (int64_t)p.N * p.G; i += gridDim.x) {
+        const int n = (int)(i / p.G), g = (int)(i % p.G);
+        const PieceRange r(m, n, run);
+        if (r.count == 0) {
+            if (threadIdx.x == 0) stats[2 * i] = 0.f, stats[2 * i + 1] = rsqrtf(p.eps);
+            continue;
+        }
+        const float* const at = pieces + g * cg;
+        const int64_t all = (int64_t)r.count * cg;
+        const float inv = 1.f / ((float)(r.e - r.b) * (float)cg);
+        float s = 0.f, q = 0.f;
+        for (int64_t k = threadIdx.x; k < all; k += blockDim.x)
+            s = fmaf((float)r.tokens((int)(k / cg)), at[r.place((int)(k / cg)) * 2 * p.C + k % cg], s);
+        const float mean = block_sum(s, buf) * inv;
+        for (int64_t k = threadIdx.x; k < all; k += blockDim.x) {
+            const float* const x = at + r.place((int)(k / cg)) * 2 * p.C + k % cg;
+            const float d = x[0] - mean;
+            q += fmaf((float)r.tokens((int)(k / cg)) * d, d, x[p.C]);
+        }
+        const float var = block_sum(q, buf) * inv;
+        if (threadIdx.x == 0) stats[2 * i] = mean, stats[2 * i + 1] = rsqrtf(var + p.eps);
+    }
+    tc::grid_dep_launch();
+}
+
+// Mean (negated) and 1 / deviation of a thread's channels in sequence n.
+template <int VEC>
+__device__ __forceinline__ void stats_of(const NormParams& p, const float* stats, int n, int c, f2 (&mean)[(VEC + 1) / 2], f2 (&rstd)[(VEC + 1) / 2]) {
+    const int cg = p.C / p.G;
+    const float2* const at = reinterpret_cast<const float2*>(stats) + (int64_t)n * p.G;
+#pragma unroll
+    for (int i = 0; i < (VEC + 1) / 2; ++i) {
+        const float2 a = at[(c + 2 * i) / cg], b = VEC > 1 ? at[(c + 2 * i + 1) / cg] : a;
+        mean[i] = pack(-a.x, -b.x);
+        rstd[i] = pack(a.y, b.y);
+    }
+}
+
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kThreads) seq_apply_kernel(NormParams p, SeqMap m, int run, const float* stats) {
+    constexpr int N2 = (VEC + 1) / 2;
+    const int piece = threadIdx.x % kPieces, sub = threadIdx.x / kPieces, c = (blockIdx.x * kPieces + piece) * VEC;
+    const bool on = c < p.C;
+    // the last runs first: they were read last
+    const int r0 = (gridDim.y - 1 - blockIdx.y) * run, r1 = (int)min((int64_t)m.total, (int64_t)r0 + run);
+    f2 w[N2], bias[N2];
+    vec_pairs<VEC>(on && p.weight ? p.weight + c : nullptr, 1.f, w);
+    vec_pairs<VEC>(on && p.bias ? p.bias + c : nullptr, 0.f, bias);
+    tc::grid_dep_wait();
+    each_piece(m, r0, r1, [&](int n, int b, int e) {
+        if (!on) return;
+        f2 mean[N2], scale[N2];
+        stats_of<VEC>(p, stats, n, c, mean, scale);
+#pragma unroll
+        for (int i = 0; i < N2; ++i) scale[i] = mul2(scale[i], w[i]);
+        for (int t = b + sub; t < e; t += kSubs * kAhead) {
+            Row<T, VEC> rows[kAhead];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j)
+                if (t + j * kSubs < e) rows[j].load(static_cast<const T*>(p.x) + (int64_t)(t + j * kSubs) * p.ldx + c);
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                if (t + j * kSubs >= e) break;
+                f2 v[N2];
+                rows[j].to(v);
+#pragma unroll
+                for (int i = 0; i < N2; ++i) {
+                    v[i] = fma2(add2(v[i], mean[i]), scale[i], bias[i]);
+                    if (p.act) v[i] = mul2(v[i], sigmoid2(v[i]));
+                }
+                rows[j].from(v);
+                rows[j].store(static_cast<T*>(p.y) + (int64_t)(t + j * kSubs) * p.C + c);
+            }
+        }
+    });
+}
+
+// Per piece and channel sum dp xh and sum dp, and the same per run: pieces[run + n][2][C], per_run[run][2][C].
+template <typename T, typename TG, int VEC>
+__global__ void __launch_bounds__(kThreads) seq_grads_kernel(NormParams p, SeqMap m, int run, const float* stats, float* pieces, float* per_run) {
+    constexpr int N2 = (VEC + 1) / 2;
+    __shared__ f2 join[N2][kThreads];
+    const int piece = threadIdx.x % kPieces, sub = threadIdx.x / kPieces, c = (blockIdx.x * kPieces + piece) * VEC;
+    const bool on = c < p.C;
+    const int cc = on ? c : 0;
+    const int r0 = blockIdx.y * run, r1 = (int)min((int64_t)m.total, (int64_t)r0 + run);
+    f2 w[N2], bias[N2];
+    vec_pairs<VEC>(p.weight ? p.weight + cc : nullptr, 1.f, w);
+    vec_pairs<VEC>(p.bias ? p.bias + cc : nullptr, 0.f, bias);
+    ChannelSums<VEC> all;
+#pragma unroll
+    for (int i = 0; i < N2; ++i) all.a[i] = all.b[i] = 0ull;
+    tc::grid_dep_wait();
+    each_piece(m, r0, r1, [&](int n, int b, int e) {
+        f2 mean[N2], rstd[N2];
+        stats_of<VEC>(p, stats, n, cc, mean, rstd);
+        ChannelSums<VEC> s;
+#pragma unroll
+        for (int i = 0; i < N2; ++i) s.a[i] = s.b[i] = 0ull;
+        for (int t = b + sub; t < e; t += kSubs * kAhead) {
+            Row<T, VEC> rows[kAhead];
+            Row<TG, VEC> grads[kAhead];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j)
+                if (t + j * kSubs < e) {
+                    rows[j].load(static_cast<const T*>(p.x) + (int64_t)(t + j * kSubs) * p.ldx + cc);
+                    grads[j].load(static_cast<const TG*>(p.dy) + (int64_t)(t + j * kSubs) * p.C + cc);
+                }
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                if (t + j * kSubs >= e) break;
+                f2 v[N2], g[N2];
+                rows[j].to(v);
+                grads[j].to(g);
+#pragma unroll
+                for (int i = 0; i < N2; ++i) {
+                    const f2 xh = mul2(add2(v[i], mean[i]), rstd[i]);
+                    if (p.act) g[i] = mul2(g[i], silu_slope2(fma2(xh, w[i], bias[i])));
+                    s.a[i] = fma2(g[i], xh, s.a[i]);
+                    s.b[i] = add2(s.b[i], g[i]);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < N2; ++i) {
+            all.a[i] = add2(all.a[i], s.a[i]);
+            all.b[i] = add2(all.b[i], s.b[i]);
+        }
+        store_sums<VEC>(s, join, pieces + (int64_t)(blockIdx.y + n) * 2 * p.C, p.C, c, on);
+    });
+    store_sums<VEC>(all, join, per_run + (int64_t)blockIdx.y * 2 * p.C, p.C, c, on);
+    tc::grid_dep_launch();
+}
+
+// Blocks [0, weight_blocks): dweight and dbias.  The others: mean(q xh) and mean(q) of every sequence and group, means [N][G][2].
+__global__ void __launch_bounds__(256) seq_means_kernel(NormParams p, SeqMap m, int run, int runs, const float* pieces, const float* per_run,
+                                                        int weight_blocks, float* means) {
+    __shared__ float buf[8];
+    tc::grid_dep_wait();
+    if ((int)blockIdx.x < weight_blocks) {
+        norm_weight_sums(per_run, runs, p.C, p.dweight, p.dbias, blockIdx.x);
+        tc::grid_dep_launch();
+        return;
+    }
+    const int cg = p.C / p.G;
+    for (int64_t i = blockIdx.x - weight_blocks; i < (int64_t)p.N * p.G; i += gridDim.x - weight_blocks) {
+        const int n = (int)(i / p.G), g = (int)(i % p.G);
+        const PieceRange r(m, n, run);
+        const float* const at = pieces + g * cg;
+        const int64_t all = (int64_t)r.count * cg;
+        float a = 0.f, b = 0.f;
+        for (int64_t k = threadIdx.x; k < all; k += blockDim.x) {
+            const float* const x = at + r.place((int)(k / cg)) * 2 * p.C + k % cg;
+            const float w = p.weight ? __ldg(p.weight + g * cg + k % cg) : 1.f;
+            a = fmaf(w, x[0], a);
+            b = fmaf(w, x[p.C], b);
+        }
+        a = block_sum(a, buf);
+        b = block_sum(b, buf);
+        const float inv = r.count > 0 ? 1.f / ((float)(r.e - r.b) * (float)cg) : 0.f;
+        if (threadIdx.x == 0) means[2 * i] = a * inv, means[2 * i + 1] = b * inv;
+    }
+    tc::grid_dep_launch();
+}
+
+template <typename T, typename TG, int VEC>
+__global__ void __launch_bounds__(kThreads) seq_dx_kernel(NormParams p, SeqMap m, int run, const float* stats, const float* means) {
+    constexpr int N2 = (VEC + 1) / 2;
+    const int piece = threadIdx.x % kPieces, sub = threadIdx.x / kPieces, c = (blockIdx.x * kPieces + piece) * VEC;
+    const bool on = c < p.C;
+    const int r0 = (gridDim.y - 1 - blockIdx.y) * run, r1 = (int)min((int64_t)m.total, (int64_t)r0 + run);
+    f2 w[N2], bias[N2];
+    vec_pairs<VEC>(on && p.weight ? p.weight + c : nullptr, 1.f, w);
+    vec_pairs<VEC>(on && p.bias ? p.bias + c : nullptr, 0.f, bias);
+    tc::grid_dep_wait();
+    if (on) {  // rows of no sequence: zeros
+        const int first = m.first(), last = m.last();
+        Row<TG, VEC> zero;
+        zero.zero();
+        for (int t = r0 + sub; t < r1; t += kSubs)
+            if (t < first || t >= last) zero.store(static_cast<TG*>(p.dx) + (int64_t)t * p.C + c);
+    }
+    each_piece(m, r0, r1, [&](int n, int b, int e) {
+        if (!on) return;
+        f2 mean[N2], rstd[N2], mqx[N2], mq[N2];
+        stats_of<VEC>(p, stats, n, c, mean, rstd);
+        stats_of<VEC>(p, means, n, c, mqx, mq);  // -mean(q xh), mean(q)
+        for (int t = b + sub; t < e; t += kSubs * kAhead) {
+            Row<T, VEC> rows[kAhead];
+            Row<TG, VEC> grads[kAhead];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j)
+                if (t + j * kSubs < e) {
+                    rows[j].load(static_cast<const T*>(p.x) + (int64_t)(t + j * kSubs) * p.ldx + c);
+                    grads[j].load(static_cast<const TG*>(p.dy) + (int64_t)(t + j * kSubs) * p.C + c);
+                }
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                if (t + j * kSubs >= e) break;
+                f2 v[N2], g[N2];
+                rows[j].to(v);
+                grads[j].to(g);
+#pragma unroll
+                for (int i = 0; i < N2; ++i) {
+                    const f2 xh = mul2(add2(v[i], mean[i]), rstd[i]);
+                    if (p.act) g[i] = mul2(g[i], silu_slope2(fma2(xh, w[i], bias[i])));
+                    g[i] = mul2(rstd[i], fma2(xh, mqx[i], fma2(g[i], w[i], neg2(mq[i]))));
+                }
+                grads[j].from(g);
+                grads[j].store(static_cast<TG*>(p.dx) + (int64_t)(t + j * kSubs) * p.C + c);
+            }
+        }
+    });
+}
+
+// ---- launches -------------------------------------------------------------------------------------------
+
+constexpr int kResident = 4;
+int blocks_of(const NormParams& p, int vec) { return (p.C + kPieces * vec - 1) / (kPieces * vec); }
+int64_t groups_grid(const NormParams& p) {
+    const int64_t n = (int64_t)p.N * p.G;
+    return n < 1 ? 1 : n < 8 * kSms ? n : 8 * kSms;
+}
+// Places of pieces at p's sizes, whichever variant runs: the wide ones have the fewest blocks and the most runs.
+int64_t most_runs(const NormParams& p) { return cut_of(p, blocks_of(p, 8), kResident).runs; }
+size_t pieces_bytes(const NormParams& p) { return (size_t)(((most_runs(p) + p.N) * 2 * p.C * 4 + 255) / 256 * 256); }
+size_t stats_bytes(const NormParams& p) { return (size_t)(((int64_t)p.N * p.G * 8 + 255) / 256 * 256); }
+
+template <typename T, int VEC>
+cudaError_t launch_stats(const NormParams& p, const SeqMap& m, const Cut& q, float* pieces, float* stats, cudaStream_t st) {
+    seq_moments_kernel<T, VEC><<<dim3(blocks_of(p, VEC), q.runs), kThreads, 0, st>>>(p, m, q.run, pieces);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return tc::launch_dependent(seq_stats_kernel, (unsigned)groups_grid(p), 128, 0, st, p, m, q.run, (const float*)pieces, stats);
+}
+
+template <typename T, int VEC>
+cudaError_t launch_fwd(const NormParams& p, cudaStream_t st) {
+    const SeqMap m{p.cu, p.N, p.T, p.total};
+    const Cut q = cut_of(p, blocks_of(p, VEC), kResident);
+    char* const ws = static_cast<char*>(p.ws);
+    float* const stats = p.stats ? p.stats : reinterpret_cast<float*>(ws + pieces_bytes(p));
+    const cudaError_t e = launch_stats<T, VEC>(p, m, q, reinterpret_cast<float*>(ws), stats, st);
+    if (e != cudaSuccess) return e;
+    return tc::launch_dependent(seq_apply_kernel<T, VEC>, dim3(blocks_of(p, VEC), q.runs), kThreads, 0, st, p, m, q.run, (const float*)stats);
+}
+
+template <typename T, typename TG, int VEC>
+cudaError_t launch_bwd(const NormParams& p, cudaStream_t st) {
+    const SeqMap m{p.cu, p.N, p.T, p.total};
+    const Cut q = cut_of(p, blocks_of(p, VEC), kResident);
+    char* at = static_cast<char*>(p.ws);
+    float* const pieces = reinterpret_cast<float*>(at);
+    float* const per_run = reinterpret_cast<float*>(at += pieces_bytes(p));
+    float* const means = reinterpret_cast<float*>(at += pieces_bytes(p));
+    float* stats = p.stats;
+    if (!stats) {
+        stats = reinterpret_cast<float*>(at + stats_bytes(p));
+        const cudaError_t e = launch_stats<T, VEC>(p, m, q, pieces, stats, st);
+        if (e != cudaSuccess) return e;
+    }
+    const dim3 grid(blocks_of(p, VEC), q.runs);
+    cudaError_t e;
+    if (p.stats) {  // the call's first kernel: it waits for whatever made its inputs
+        seq_grads_kernel<T, TG, VEC><<<grid, kThreads, 0, st>>>(p, m, q.run, stats, pieces, per_run);
+        e = cudaGetLastError();
+    } else {
+        e = tc::launch_dependent(seq_grads_kernel<T, TG, VEC>, grid, kThreads, 0, st, p, m, q.run, (const float*)stats, pieces, per_run);
+    }
+    if (e != cudaSuccess) return e;
+    const int weight_blocks = p.dweight || p.dbias ? (p.C + 31) / 32 : 0;
+    e = tc::launch_dependent(seq_means_kernel, (unsigned)(weight_blocks + groups_grid(p)), 256, 0, st, p, m, q.run, q.runs, (const float*)pieces,
+                             (const float*)per_run, weight_blocks, means);
+    if (e != cudaSuccess) return e;
+    return tc::launch_dependent(seq_dx_kernel<T, TG, VEC>, grid, kThreads, 0, st, p, m, q.run, (const float*)stats, (const float*)means);
+}
+
+}  // namespace
+
+size_t group_norm_fwd_workspace(const NormParams& p) { return p.over_sequence ? pieces_bytes(p) + (p.stats ? 0 : stats_bytes(p)) : 0; }
+size_t group_norm_bwd_workspace(const NormParams& p) {
+    if (!p.over_sequence) return norm_token_bwd_workspace(p);
+    return 2 * pieces_bytes(p) + (p.stats ? 1 : 2) * stats_bytes(p);
+}
+
+cudaError_t group_norm_fwd(kda_dtype dt, const NormParams& p, cudaStream_t st) {
+    if (!p.over_sequence) return norm_token_fwd(dt, p, st);
+    using kda_host::rows_aligned;
+    const int vec = dt == KDA_BF16 ? 8 : 4;
+    const bool wide = p.C % vec == 0 && rows_aligned(p.x, p.ldx, vec) && rows_aligned(p.y, p.C, vec);
+    if (dt == KDA_BF16) return wide ? launch_fwd<__nv_bfloat16, 8>(p, st) : launch_fwd<__nv_bfloat16, 1>(p, st);
+    return wide ? launch_fwd<float, 4>(p, st) : launch_fwd<float, 1>(p, st);
+}
+
+cudaError_t group_norm_bwd(kda_dtype dt, kda_dtype gdt, const NormParams& p, cudaStream_t st) {
+    if (!p.over_sequence) return norm_token_bwd(dt, gdt, p, st);
+    using kda_host::rows_aligned;
+    const int vec = dt == KDA_BF16 && gdt == KDA_BF16 ? 8 : 4;
+    const bool wide = p.C % vec == 0 && rows_aligned(p.x, p.ldx, dt == KDA_BF16 ? 8 : 4) && rows_aligned(p.dy, p.C, vec) && rows_aligned(p.dx, p.C, vec);
+    if (dt == KDA_F32) return wide ? launch_bwd<float, float, 4>(p, st) : launch_bwd<float, float, 1>(p, st);
+    if (gdt == KDA_F32) return wide ? launch_bwd<__nv_bfloat16, float, 4>(p, st) : launch_bwd<__nv_bfloat16, float, 1>(p, st);
+    return wide ? launch_bwd<__nv_bfloat16, __nv_bfloat16, 8>(p, st) : launch_bwd<__nv_bfloat16, __nv_bfloat16, 1>(p, st);
+}
+
+}  // namespace kda

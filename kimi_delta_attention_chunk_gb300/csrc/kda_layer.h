@@ -92,6 +92,66 @@ cudaError_t ssm_scan_fwd(kda_dtype dt, const SsmScanParams& p, cudaStream_t st);
 size_t ssm_scan_bwd_workspace(const SsmScanParams& p);
 cudaError_t ssm_scan_bwd(kda_dtype dt, kda_dtype gdt, const SsmScanParams& p, cudaStream_t st);
 
+constexpr int kGatedBlock = 32;     // tokens between the states that a forward pass leaves to the backward pass
+
+struct GatedParams {
+    const void *x, *r, *i, *z;      // [B][T][ld*]; z may be null
+    int64_t ldx, ldr, ldi, ldz;
+    const float* lam;               // [C]
+    float decay;
+    const float* initial;           // [N][C] or null
+    const int32_t* cu;              // null: B streams of T tokens, a sequence each; else one of N sequences
+    int B, T, C, N;
+    void* y;                        // [B][T][C]; null: nothing but `states`
+    float* final_state;             // [N][C] or null
+    float* states;                  // [B][ceil(T / kGatedBlock)][C] or null: written forwards, read backwards
+    // backward
+    const void* dy;                 // [B][T][C], gradient type
+    const float* dfinal;            // [N][C] or null
+    void *dx, *dr, *di, *dz;        // [B][T][C], gradient type; dz null with z
+    float* dlam;                    // [C]
+    float* dinitial;                // [N][C] or null
+    void* ws;
+};
+cudaError_t gated_scan_fwd(kda_dtype dt, const GatedParams& p, cudaStream_t st);
+// Device bytes a call needs at p's sizes (p.cu and p.states null or not matters, no pointer is followed).
+size_t gated_scan_bwd_workspace(const GatedParams& p);
+cudaError_t gated_scan_bwd(kda_dtype dt, kda_dtype gdt, const GatedParams& p, cudaStream_t st);
+
+struct GatedStepParams {
+    const void *x, *r, *i, *z;      // [N][ld*]; z may be null
+    int64_t ldx, ldr, ldi, ldz;
+    const float* lam;               // [C]
+    float decay;
+    float* state;                   // [P][C]
+    const int32_t* slots;           // [N] or null
+    int N, P, C;
+    void* y;                        // [N][C]
+    int32_t* status;
+};
+cudaError_t gated_step(kda_dtype dt, const GatedStepParams& p, cudaStream_t st);
+
+struct NormParams {
+    const void* x;                  // [total][ldx]
+    int64_t ldx;
+    const float *weight, *bias;     // [C] or null
+    float eps;
+    int act, over_sequence;
+    const int32_t* cu;              // null: B sequences of T tokens; else N in one stream
+    int T, N, C, G, total;
+    void* y;                        // [total][C]
+    float* stats;                   // [N][G][2] or null, over sequences: mean and 1 / deviation, written forwards, read backwards
+    // backward
+    const void* dy;                 // [total][C], gradient type
+    void* dx;                       // [total][C], gradient type
+    float *dweight, *dbias;         // [C] or null
+    void* ws;
+};
+size_t group_norm_fwd_workspace(const NormParams& p);
+cudaError_t group_norm_fwd(kda_dtype dt, const NormParams& p, cudaStream_t st);
+size_t group_norm_bwd_workspace(const NormParams& p);
+cudaError_t group_norm_bwd(kda_dtype dt, kda_dtype gdt, const NormParams& p, cudaStream_t st);
+
 cudaError_t pages_alloc(int32_t* refs, int P, int n, int32_t* out, int32_t* status, cudaStream_t st);
 cudaError_t pages_free(int32_t* refs, int P, const int32_t* pages, int64_t n, int32_t* status, cudaStream_t st);
 cudaError_t pages_fork(int32_t* tables, int32_t* lens, int S, int width, int page_tokens, int32_t* refs, int P,

@@ -97,6 +97,61 @@ kda_status scan_inputs(const kda::SsmScanParams& p, kda_dtype dtype) {
                        {p.D, (size_t)p.C * 4}, {p.bias, (size_t)p.C * 4}, {p.initial, (size_t)p.N * p.C * p.S * 4},       \
                        {p.cu, (size_t)(p.N + 1) * 4}}
 
+// The inputs that the forward and backward gated scans share.
+kda_status gated_inputs(kda::GatedParams& p, kda_dtype dtype, int B, int T, int C, int N, const int32_t* cu) {
+    const kda_status s = check_stream(B, T, C, N, cu);
+    if (s != KDA_OK) return s;
+    if (!dtype_ok(dtype)) return KDA_ERR_UNSUPPORTED;
+    p.cu = cu; p.B = B; p.T = T; p.C = C; p.N = N;
+    const int64_t total = (int64_t)B * T;
+    if (p.ldx < C || p.ldr < C || p.ldi < C || (p.z && p.ldz < C)) return KDA_ERR_INVALID_ARG;
+    if (!p.lam || (total > 0 && (!p.x || !p.r || !p.i))) return KDA_ERR_INVALID_ARG;
+    if (!(p.decay > 0.f) || !isfinite(p.decay)) return KDA_ERR_INVALID_ARG;
+    for (const void* q : {p.x, p.r, p.i, p.z})
+        if (!aligned(q, size_of(dtype))) return KDA_ERR_INVALID_ARG;
+    for (const void* q : {(const void*)p.lam, (const void*)p.initial, (const void*)p.states})
+        if (!aligned(q, 4)) return KDA_ERR_INVALID_ARG;
+    // blocks of one launch: 64 channels and a batch row each, eight to a cluster
+    if ((int64_t)B * ((C + 63) / 64) * 8 > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+size_t gated_states_bytes(int B, int T, int C) { return (size_t)B * (((size_t)T + kda::kGatedBlock - 1) / kda::kGatedBlock) * C * 4; }
+#define GATED_INPUT_SPANS(in, p, es)                                                                                       \
+    const int64_t total = (int64_t)p.B * p.T;                                                                              \
+    const Span in[] = {rows(p.x, total, p.ldx, p.C, es), rows(p.r, total, p.ldr, p.C, es), rows(p.i, total, p.ldi, p.C, es), \
+                       rows(p.z, total, p.ldz, p.C, es), {p.lam, (size_t)p.C * 4}, {p.initial, (size_t)p.N * p.C * 4},      \
+                       {p.cu, (size_t)(p.N + 1) * 4}}
+
+// The largest group of channels that a token's norm keeps on chip.
+constexpr int kMostGroup = 16384;
+
+kda_status norm_inputs(kda::NormParams& p, kda_dtype dtype, int B, int T, int C, int G, int N, const int32_t* cu) {
+    const kda_status s = check_stream(B, T, C, N, cu);
+    if (s != KDA_OK) return s;
+    if (!dtype_ok(dtype)) return KDA_ERR_UNSUPPORTED;
+    if (G <= 0 || C % G != 0 || (p.act != 0 && p.act != 1) || (p.over_sequence != 0 && p.over_sequence != 1)) return KDA_ERR_INVALID_ARG;
+    if (!p.over_sequence && cu) return KDA_ERR_INVALID_ARG;
+    if (!p.over_sequence && C / G > kMostGroup) return KDA_ERR_UNSUPPORTED;
+    if (!(p.eps > 0.f) || !isfinite(p.eps)) return KDA_ERR_INVALID_ARG;
+    p.cu = cu; p.T = T; p.N = N; p.C = C; p.G = G; p.total = B * T;
+    if (p.ldx < C || (p.total > 0 && !p.x) || !aligned(p.x, size_of(dtype))) return KDA_ERR_INVALID_ARG;
+    for (const float* q : {p.weight, p.bias})
+        if (!aligned(q, 4)) return KDA_ERR_INVALID_ARG;
+    if (!aligned(p.stats, 8) || (p.stats && !p.over_sequence)) return KDA_ERR_INVALID_ARG;
+    return KDA_OK;
+}
+// p at these sizes, for a workspace query.
+bool norm_sizes(kda::NormParams& p, int B, int T, int C, int G, int N, int over_sequence, int packed, int have_stats) {
+    static float none[2];
+    p.over_sequence = over_sequence;
+    p.eps = 1.f;
+    p.x = none;
+    p.ldx = C;
+    if (norm_inputs(p, KDA_F32, B, T, C, G, N, packed ? kPacked : nullptr) != KDA_OK) return false;
+    if (have_stats && over_sequence) p.stats = none;
+    return true;
+}
+
 }  // namespace
 
 extern "C" {
@@ -294,6 +349,146 @@ kda_status kda_ssm_scan_bwd(const void* u, int64_t ldu, const void* delta, int64
                         {dD, (size_t)C * 4}, {ddelta_bias, (size_t)C * 4}, {dinitial_state, states}, {workspace, need}};
     if (!apart(in, out) || !apart(more, out)) return KDA_ERR_INVALID_ARG;
     return from_cuda(kda::ssm_scan_bwd(dtype, grad_dtype, p, (cudaStream_t)stream));
+}
+
+kda_status kda_gated_scan_fwd(const void* x, int64_t ldx, const void* r, int64_t ldr, const void* i, int64_t ldi, const float* lam,
+                              const void* z, int64_t ldz, float decay, kda_dtype dtype, const float* initial_state,
+                              const int32_t* cu_seqlens, int B, int T, int C, int N, void* y, float* final_state,
+                              float* states, void* stream) {
+    kda::GatedParams p{};
+    p.x = x; p.r = r; p.i = i; p.z = z; p.ldx = ldx; p.ldr = ldr; p.ldi = ldi; p.ldz = ldz; p.lam = lam; p.decay = decay;
+    p.initial = initial_state; p.y = y; p.final_state = final_state; p.states = states;
+    const kda_status s = gated_inputs(p, dtype, B, T, C, N, cu_seqlens);
+    if (s != KDA_OK) return s;
+    const size_t es = size_of(dtype);
+    GATED_INPUT_SPANS(in, p, es);
+    if ((total > 0 && !y) || !aligned(y, es) || !aligned(final_state, 4)) return KDA_ERR_INVALID_ARG;
+    const Span out[] = {{y, (size_t)total * C * es}, {final_state, (size_t)N * C * 4}, {states, gated_states_bytes(B, T, C)}};
+    if (!apart(in, out)) return KDA_ERR_INVALID_ARG;
+    if (N == 0) return KDA_OK;
+    return from_cuda(kda::gated_scan_fwd(dtype, p, (cudaStream_t)stream));
+}
+
+size_t kda_gated_scan_bwd_workspace_size(int B, int T, int C, int N, int packed, int have_states) {
+    if (check_stream(B, T, C, N, packed ? kPacked : nullptr) != KDA_OK) return 0;
+    static float none;
+    kda::GatedParams p{};
+    p.B = B; p.T = T; p.C = C; p.N = N;
+    p.states = have_states ? &none : nullptr;
+    return kda::gated_scan_bwd_workspace(p);
+}
+
+kda_status kda_gated_scan_bwd(const void* x, int64_t ldx, const void* r, int64_t ldr, const void* i, int64_t ldi, const float* lam,
+                              const void* z, int64_t ldz, float decay, kda_dtype dtype, const float* initial_state,
+                              const int32_t* cu_seqlens, int B, int T, int C, int N, const void* dy,
+                              const float* dfinal_state, kda_dtype grad_dtype, const float* states, void* dx, void* dr,
+                              void* di, float* dlam, void* dz, float* dinitial_state, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+    kda::GatedParams p{};
+    p.x = x; p.r = r; p.i = i; p.z = z; p.ldx = ldx; p.ldr = ldr; p.ldi = ldi; p.ldz = ldz; p.lam = lam; p.decay = decay;
+    p.initial = initial_state; p.states = const_cast<float*>(states);
+    const kda_status s = gated_inputs(p, dtype, B, T, C, N, cu_seqlens);
+    if (s != KDA_OK) return s;
+    if (!dtype_ok(grad_dtype) || (dtype == KDA_F32 && grad_dtype != KDA_F32)) return KDA_ERR_UNSUPPORTED;
+    const size_t es = size_of(dtype), gs = size_of(grad_dtype);
+    GATED_INPUT_SPANS(in, p, es);
+    if (!dlam || (total > 0 && (!dy || !dx || !dr || !di || !z != !dz))) return KDA_ERR_INVALID_ARG;
+    for (const void* q : {dy, (const void*)dx, (const void*)dr, (const void*)di, (const void*)dz})
+        if (!aligned(q, gs)) return KDA_ERR_INVALID_ARG;
+    for (const float* q : {dfinal_state, (const float*)dlam, (const float*)dinitial_state})
+        if (!aligned(q, 4)) return KDA_ERR_INVALID_ARG;
+    const size_t need = kda::gated_scan_bwd_workspace(p);
+    if (workspace_bytes < need || (need > 0 && !workspace)) return KDA_ERR_WORKSPACE;
+    if (!kda_host::aligned16(workspace)) return KDA_ERR_INVALID_ARG;
+    const size_t row_bytes = (size_t)total * C * gs, state_bytes = (size_t)N * C * 4;
+    const Span more[] = {{dy, row_bytes}, {dfinal_state, state_bytes}, {states, gated_states_bytes(B, T, C)}};
+    const Span out[] = {{dx, row_bytes}, {dr, row_bytes}, {di, row_bytes}, {dz, row_bytes}, {dlam, (size_t)C * 4},
+                        {dinitial_state, state_bytes}, {workspace, need}};
+    if (!apart(in, out) || !apart(more, out)) return KDA_ERR_INVALID_ARG;
+    p.dy = dy; p.dfinal = dfinal_state; p.dx = dx; p.dr = dr; p.di = di; p.dz = dz; p.dlam = dlam; p.dinitial = dinitial_state;
+    p.ws = workspace;
+    return from_cuda(kda::gated_scan_bwd(dtype, grad_dtype, p, (cudaStream_t)stream));
+}
+
+kda_status kda_gated_step(const void* x, int64_t ldx, const void* r, int64_t ldr, const void* i, int64_t ldi, const float* lam,
+                          const void* z, int64_t ldz, float decay, kda_dtype dtype, float* state, const int32_t* slots,
+                          int P, int N, int C, void* y, int32_t* status, void* stream) {
+    if (N < 0 || P < 0 || C <= 0) return KDA_ERR_INVALID_ARG;
+    if (!dtype_ok(dtype) || C > kMostChannels || N > kMostRows || (slots && N > KDA_MOST_SLOTS)) return KDA_ERR_UNSUPPORTED;
+    if (ldx < C || ldr < C || ldi < C || (z && ldz < C)) return KDA_ERR_INVALID_ARG;
+    if (!(decay > 0.f) || !isfinite(decay)) return KDA_ERR_INVALID_ARG;
+    if (!lam || (N > 0 && (!x || !r || !i || !state || !y || P == 0))) return KDA_ERR_INVALID_ARG;
+    if (!slots && N > P) return KDA_ERR_INVALID_ARG;
+    if ((int64_t)N * ((C + 127) / 128) > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;  // blocks of one launch
+    const size_t es = size_of(dtype);
+    for (const void* q : {x, r, i, z, (const void*)y})
+        if (!aligned(q, es)) return KDA_ERR_INVALID_ARG;
+    for (const void* q : {(const void*)lam, (const void*)state, (const void*)slots, (const void*)status})
+        if (!aligned(q, 4)) return KDA_ERR_INVALID_ARG;
+    const Span in[] = {rows(x, N, ldx, C, es), rows(r, N, ldr, C, es), rows(i, N, ldi, C, es), rows(z, N, ldz, C, es),
+                       {lam, (size_t)C * 4}, {slots, (size_t)N * 4}};
+    const Span out[] = {{y, (size_t)N * C * es}, {state, (size_t)P * C * 4}, {status, 4}};
+    if (!apart(in, out)) return KDA_ERR_INVALID_ARG;
+    cudaStream_t st = (cudaStream_t)stream;
+    if (clear(status, st) != KDA_OK) return KDA_ERR_CUDA;
+    if (N == 0) return KDA_OK;
+    kda::GatedStepParams p{x, r, i, z, ldx, ldr, ldi, ldz, lam, decay, state, slots, N, P, C, y, status};
+    return from_cuda(kda::gated_step(dtype, p, st));
+}
+
+size_t kda_group_norm_fwd_workspace_size(int B, int T, int C, int G, int N, int over_sequence, int packed, int have_stats) {
+    kda::NormParams p{};
+    return norm_sizes(p, B, T, C, G, N, over_sequence, packed, have_stats) ? kda::group_norm_fwd_workspace(p) : 0;
+}
+
+kda_status kda_group_norm_fwd(const void* x, int64_t ldx, const float* weight, const float* bias, float eps, int act,
+                              int over_sequence, kda_dtype dtype, const int32_t* cu_seqlens, int B, int T, int C, int G,
+                              int N, void* y, float* stats, void* workspace, size_t workspace_bytes, void* stream) {
+    kda::NormParams p{};
+    p.x = x; p.ldx = ldx; p.weight = weight; p.bias = bias; p.eps = eps; p.act = act; p.over_sequence = over_sequence;
+    p.y = y; p.stats = stats; p.ws = workspace;
+    const kda_status s = norm_inputs(p, dtype, B, T, C, G, N, cu_seqlens);
+    if (s != KDA_OK) return s;
+    const size_t es = size_of(dtype);
+    if ((p.total > 0 && !y) || !aligned(y, es)) return KDA_ERR_INVALID_ARG;
+    const size_t need = kda::group_norm_fwd_workspace(p);
+    if (workspace_bytes < need || (need > 0 && !workspace)) return KDA_ERR_WORKSPACE;
+    if (!kda_host::aligned16(workspace)) return KDA_ERR_INVALID_ARG;
+    const Span in[] = {rows(x, p.total, ldx, C, es), {weight, (size_t)C * 4}, {bias, (size_t)C * 4}, {cu_seqlens, (size_t)(N + 1) * 4}};
+    const Span out[] = {{y, (size_t)p.total * C * es}, {stats, (size_t)N * G * 8}, {workspace, need}};
+    if (!apart(in, out)) return KDA_ERR_INVALID_ARG;
+    if (N == 0 || (p.total == 0 && !stats)) return KDA_OK;
+    return from_cuda(kda::group_norm_fwd(dtype, p, (cudaStream_t)stream));
+}
+
+size_t kda_group_norm_bwd_workspace_size(int B, int T, int C, int G, int N, int over_sequence, int packed, int have_stats) {
+    kda::NormParams p{};
+    return norm_sizes(p, B, T, C, G, N, over_sequence, packed, have_stats) ? kda::group_norm_bwd_workspace(p) : 0;
+}
+
+kda_status kda_group_norm_bwd(const void* x, int64_t ldx, const float* weight, const float* bias, float eps, int act,
+                              int over_sequence, kda_dtype dtype, const int32_t* cu_seqlens, int B, int T, int C, int G,
+                              int N, const void* dy, kda_dtype grad_dtype, const float* stats, void* dx, float* dweight,
+                              float* dbias, void* workspace, size_t workspace_bytes, void* stream) {
+    kda::NormParams p{};
+    p.x = x; p.ldx = ldx; p.weight = weight; p.bias = bias; p.eps = eps; p.act = act; p.over_sequence = over_sequence;
+    p.stats = const_cast<float*>(stats); p.ws = workspace;
+    const kda_status s = norm_inputs(p, dtype, B, T, C, G, N, cu_seqlens);
+    if (s != KDA_OK) return s;
+    if (!dtype_ok(grad_dtype) || (dtype == KDA_F32 && grad_dtype != KDA_F32)) return KDA_ERR_UNSUPPORTED;
+    const size_t es = size_of(dtype), gs = size_of(grad_dtype);
+    if ((p.total > 0 && (!dy || !dx)) || !aligned(dy, gs) || !aligned(dx, gs) || !aligned(dweight, 4) || !aligned(dbias, 4))
+        return KDA_ERR_INVALID_ARG;
+    const size_t need = kda::group_norm_bwd_workspace(p);
+    if (workspace_bytes < need || (need > 0 && !workspace)) return KDA_ERR_WORKSPACE;
+    if (!kda_host::aligned16(workspace)) return KDA_ERR_INVALID_ARG;
+    const size_t row_bytes = (size_t)p.total * C * gs;
+    const Span in[] = {rows(x, p.total, ldx, C, es), {weight, (size_t)C * 4}, {bias, (size_t)C * 4}, {cu_seqlens, (size_t)(N + 1) * 4},
+                       {dy, row_bytes}, {stats, (size_t)N * G * 8}};
+    const Span out[] = {{dx, row_bytes}, {dweight, (size_t)C * 4}, {dbias, (size_t)C * 4}, {workspace, need}};
+    if (!apart(in, out)) return KDA_ERR_INVALID_ARG;
+    p.dy = dy; p.dx = dx; p.dweight = dweight; p.dbias = dbias;
+    return from_cuda(kda::group_norm_bwd(dtype, grad_dtype, p, (cudaStream_t)stream));
 }
 
 kda_status kda_pages_alloc(int32_t* refs, int P, int n, int32_t* pages, int32_t* status, void* stream) {

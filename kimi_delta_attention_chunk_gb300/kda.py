@@ -68,6 +68,18 @@ SIGNATURES = {
     "kda_ssm_scan_bwd": (_i, [_vp, _i64, _vp, _i64, _fp, _vp, _i64, _vp, _i64, _fp, _vp, _i64, _fp, _i, _i, _fp,
                               _i32p, _i, _i, _i, _i, _i, _i, _vp, _fp, _i, _vp, _vp, _fp, _vp, _vp, _fp, _vp, _fp,
                               _fp, _vp, _sz, _vp]),
+    "kda_gated_scan_fwd": (_i, [_vp, _i64, _vp, _i64, _vp, _i64, _fp, _vp, _i64, _f, _i, _fp, _i32p, _i, _i, _i, _i, _vp,
+                                _fp, _fp, _vp]),
+    "kda_gated_scan_bwd_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i]),
+    "kda_gated_scan_bwd": (_i, [_vp, _i64, _vp, _i64, _vp, _i64, _fp, _vp, _i64, _f, _i, _fp, _i32p, _i, _i, _i, _i, _vp,
+                                _fp, _i, _fp, _vp, _vp, _vp, _fp, _vp, _fp, _vp, _sz, _vp]),
+    "kda_gated_step": (_i, [_vp, _i64, _vp, _i64, _vp, _i64, _fp, _vp, _i64, _f, _i, _fp, _i32p, _i, _i, _i, _vp, _i32p,
+                            _vp]),
+    "kda_group_norm_fwd_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i, _i, _i]),
+    "kda_group_norm_fwd": (_i, [_vp, _i64, _fp, _fp, _f, _i, _i, _i, _i32p, _i, _i, _i, _i, _i, _vp, _fp, _vp, _sz, _vp]),
+    "kda_group_norm_bwd_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i, _i, _i]),
+    "kda_group_norm_bwd": (_i, [_vp, _i64, _fp, _fp, _f, _i, _i, _i, _i32p, _i, _i, _i, _i, _i, _vp, _i, _fp, _vp, _fp, _fp,
+                                _vp, _sz, _vp]),
     "kda_pages_alloc": (_i, [_i32p, _i, _i, _i32p, _i32p, _vp]),
     "kda_pages_free": (_i, [_i32p, _i, _i32p, _i64, _i32p, _vp]),
     "kda_pages_fork": (_i, [_i32p, _i32p, _i, _i, _i, _i32p, _i, _i32p, _i32p, _i, _i32p, _i32p, _i32p, _vp]),
@@ -789,6 +801,198 @@ def ssm_scan_bwd(u, delta, A, Bm, Cm, dy, D=None, z=None, delta_bias=None, softp
                                                        "dinitial_state")),
                               _at(ws), ws_bytes, _stream_of(dev))
     _check("kda_ssm_scan_bwd", st)
+    return out
+
+
+def _gated_check(x, r, i, lam, z):
+    """C of a gated call whose x is [..., C]."""
+    if lam.dtype is not torch.float32 or lam.dim() != 1:
+        raise TypeError("lam must be float32 [C]")
+    C, rows, dt = lam.shape[0], x.shape, x.dtype
+    if rows[-1] != C or r.shape != rows or i.shape != rows or (z is not None and z.shape != rows):
+        raise ValueError(f"x, r, i and z must be [..., {C}] alike")
+    if r.dtype is not dt or i.dtype is not dt or (z is not None and z.dtype is not dt):
+        raise TypeError(f"r, i and z must be of x's type, {dt}")
+    return C
+
+
+def gated_scan_states(x) -> tuple:
+    """Shape of the fp32 ``states`` that :func:`gated_scan_fwd` on x [B,T,C] can leave to
+    :func:`gated_scan_bwd`."""
+    B, T, C = x.shape
+    return B, -(-T // 32), C
+
+
+def gated_scan_fwd(x, r, i, lam, z=None, decay: float = 8.0, initial_state=None, cu_seqlens=None,
+                   output_final_state: bool = True, y=None, final_state=None, states=None):
+    """A gated linear recurrence, one state a channel: ``h <- a h + sqrt(1 - a^2) sigmoid(i) x``, ``y = h *
+    silu(z)`` with ``a = exp(-decay * softplus(lam) * sigmoid(r))``.
+
+    x, r, i, z: [B,T,C] (bf16 or fp32; rows may be slices of wider ones; z None: y = h); lam:
+    [C] fp32; ``initial_state`` fp32 [N,C] (None: zeros); ``cu_seqlens`` as for
+    :func:`chunk_fwd`.  ``states``: an fp32 tensor [B, ceil(T / 32), C] (:func:`gated_scan_states`)
+    that receives the state before every 32nd token, for :func:`gated_scan_bwd`.  Returns (y
+    [B,T,C], final_state [N,C] fp32 or None).  Rows that belong to no sequence are left as they
+    are."""
+    lib = _lib if _lib is not None else load_library()
+    C = _gated_check(x, r, i, lam, z)
+    B, T, _ = x.shape
+    N = _sequences(x, cu_seqlens)
+    _ints(B, T, C, N)
+    dev = _here(x, r, i, lam, z, initial_state, cu_seqlens, y, final_state, states)
+    _like(x, y)
+    _f32(initial_state, final_state, states)
+    _shape("initial_state", initial_state, (N, C))
+    _shape("final_state", final_state, (N, C))
+    _shape("y", y, (B, T, C))
+    _shape("states", states, gated_scan_states(x))
+    if y is None:
+        y = torch.empty((B, T, C), dtype=x.dtype, device=x.device)
+    if final_state is None and output_final_state:
+        final_state = torch.empty((N, C), dtype=torch.float32, device=x.device)
+    (px, ldx), (pr, ldr), (pi, ldi), (pz, ldz) = _rows("x", x, 2), _rows("r", r, 2), _rows("i", i, 2), _rows("z", z, 2)
+    st = lib.kda_gated_scan_fwd(px, ldx, pr, ldr, pi, ldi, _at(lam), pz, ldz, decay, _dt(x), _at(initial_state),
+                                _at(cu_seqlens), B, T, C, N, _at(y), _at(final_state), _at(states), _stream_of(dev))
+    _check("kda_gated_scan_fwd", st)
+    return y, final_state
+
+
+def gated_scan_bwd(x, r, i, lam, dy, z=None, decay: float = 8.0, initial_state=None, cu_seqlens=None,
+                   dfinal_state=None, states=None, workspace=None):
+    """Gradients of <dy, y> + <dfinal_state, final_state> through :func:`gated_scan_fwd` (same
+    arguments; ``states`` as that call left them, None: made again).  dy [B,T,C] is of x's type
+    or fp32.  Returns a dict: dx, dr, di, dz [B,T,C] in dy's type, dlam [C] and dinitial_state
+    [N,C] fp32; the gradient of an argument that was not given is None.  Rows that belong to no
+    sequence have zeros."""
+    lib = _lib if _lib is not None else load_library()
+    C = _gated_check(x, r, i, lam, z)
+    B, T, _ = x.shape
+    N = _sequences(x, cu_seqlens)
+    _ints(B, T, C, N)
+    dev = _here(x, r, i, lam, dy, z, initial_state, cu_seqlens, dfinal_state, states, workspace)
+    _f32(initial_state, dfinal_state, states)
+    _shape("dy", dy, (B, T, C))
+    _shape("initial_state", initial_state, (N, C))
+    _shape("dfinal_state", dfinal_state, (N, C))
+    _shape("states", states, gated_scan_states(x))
+    like, f32 = dy.new_empty, lam.new_empty
+    out = {"dx": like((B, T, C)), "dr": like((B, T, C)), "di": like((B, T, C)), "dlam": f32(C),
+           "dz": like((B, T, C)) if z is not None else None,
+           "dinitial_state": f32((N, C)) if initial_state is not None else None}
+    ws, ws_bytes = _workspace(int(lib.kda_gated_scan_bwd_workspace_size(B, T, C, N, int(cu_seqlens is not None),
+                                                                        int(states is not None))), x.device, workspace)
+    (px, ldx), (pr, ldr), (pi, ldi), (pz, ldz) = _rows("x", x, 2), _rows("r", r, 2), _rows("i", i, 2), _rows("z", z, 2)
+    st = lib.kda_gated_scan_bwd(px, ldx, pr, ldr, pi, ldi, _at(lam), pz, ldz, decay, _dt(x), _at(initial_state),
+                                _at(cu_seqlens), B, T, C, N, _at(dy), _at(dfinal_state), _dt(dy), _at(states),
+                                *(_at(out[k]) for k in ("dx", "dr", "di", "dlam", "dz", "dinitial_state")),
+                                _at(ws), ws_bytes, _stream_of(dev))
+    _check("kda_gated_scan_bwd", st)
+    return out
+
+
+def gated_step(x, r, i, lam, state, z=None, decay: float = 8.0, slots=None, y=None, status=None):
+    """One token of each of N sequences through :func:`gated_scan_fwd`'s recurrence: x, r, i, z
+    [N,C]; ``state`` fp32 [P,C] is updated in place.  Returns y [N,C].  ``slots``/``status`` as for
+    :func:`recurrent_step`."""
+    lib = _lib if _lib is not None else load_library()
+    C = _gated_check(x, r, i, lam, z)
+    if x.dim() != 2:
+        raise ValueError(f"x must be [N, {C}], got {tuple(x.shape)}")
+    N = x.shape[0]
+    P = state.shape[0]
+    _ints(N, P, C)
+    dev = _here(x, r, i, lam, state, z, slots, y, status)
+    if state.dtype is not torch.float32 or state.shape != (P, C):
+        raise ValueError(f"state must be fp32 [P, {C}]")
+    if y is None:
+        y = torch.empty((N, C), dtype=x.dtype, device=x.device)
+    elif y.dtype is not x.dtype or y.shape != (N, C):
+        raise ValueError(f"y must be {(N, C)} of {x.dtype}")
+    _check_slots(slots, status, N)
+    (px, ldx), (pr, ldr), (pi, ldi), (pz, ldz) = _rows("x", x, 1), _rows("r", r, 1), _rows("i", i, 1), _rows("z", z, 1)
+    st = lib.kda_gated_step(px, ldx, pr, ldr, pi, ldi, _at(lam), pz, ldz, decay, _dt(x), _at(state), _at(slots), P, N, C,
+                            _at(y), _at(status), _stream_of(dev))
+    _check("kda_gated_step", st)
+    return y
+
+
+_NORM_OVER = {"token": 0, "sequence": 1}
+
+
+def _norm_check(x, groups, weight, bias, over, cu_seqlens):
+    """(B, T, C, N) of a norm call."""
+    if over not in _NORM_OVER:
+        raise ValueError('over is "token" or "sequence"')
+    if x.dim() == 2 and over == "token":
+        (T, C), B = x.shape, 1
+        N = 1
+    else:
+        B, T, C = x.shape
+        N = _sequences(x, cu_seqlens)
+    if cu_seqlens is not None and over == "token":
+        raise ValueError("cu_seqlens goes with norms over sequences")
+    _f32(weight, bias)
+    _shape("weight", weight, (C,))
+    _shape("bias", bias, (C,))
+    _ints(B, T, C, N, groups)
+    return B, T, C, N
+
+
+def group_norm_fwd(x, groups: int, weight=None, bias=None, eps: float = 1e-5, act: int = 0, over: str = "token",
+                   cu_seqlens=None, y=None, stats=None, workspace=None):
+    """Group norm with an activation, channels last: ``act(weight * (x - mean) / sqrt(var + eps) +
+    bias)``, mean and variance over a group's channels of one token (``over="token"``) or of all tokens
+    of a sequence (``over="sequence"``).
+
+    x: [B,T,C] (bf16 or fp32; rows may be slices of wider ones), over tokens also [N,C]; weight,
+    bias: [C] fp32 or None; act: 0 none, 1 SiLU; ``cu_seqlens`` (over sequences) as for
+    :func:`chunk_fwd`.  ``stats``: over sequences an fp32 tensor [N,groups,2] that receives mean and 1 /
+    sqrt(var + eps), for :func:`group_norm_bwd`.  Returns y, of x's shape and type.  Rows that belong to no
+    sequence are left as they are."""
+    lib = _lib if _lib is not None else load_library()
+    B, T, C, N = _norm_check(x, groups, weight, bias, over, cu_seqlens)
+    dev = _here(x, weight, bias, cu_seqlens, y, stats, workspace)
+    _like(x, y)
+    _f32(stats)
+    _shape("y", y, x.shape)
+    _shape("stats", stats, (N, groups, 2))
+    if y is None:
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    seq = _NORM_OVER[over]
+    ws, ws_bytes = None, 0
+    if seq:
+        ws, ws_bytes = _workspace(int(lib.kda_group_norm_fwd_workspace_size(B, T, C, groups, N, seq, int(cu_seqlens is not None),
+                                                                            int(stats is not None))), x.device, workspace)
+    px, ldx = _rows("x", x, x.dim() - 1)
+    st = lib.kda_group_norm_fwd(px, ldx, _at(weight), _at(bias), eps, act, seq, _dt(x), _at(cu_seqlens), B, T, C, groups, N,
+                                _at(y), _at(stats), _at(ws), ws_bytes, _stream_of(dev))
+    _check("kda_group_norm_fwd", st)
+    return y
+
+
+def group_norm_bwd(x, groups: int, dy, weight=None, bias=None, eps: float = 1e-5, act: int = 0, over: str = "token",
+                   cu_seqlens=None, stats=None, workspace=None):
+    """Gradients of <dy, y> through :func:`group_norm_fwd` (same arguments; ``stats`` as that call left
+    them, None: made again).  dy, of x's shape, is of x's type or fp32.  Returns a dict: dx in
+    dy's type, dweight and dbias [C] fp32 (None for an argument that was not given).  Rows that
+    belong to no sequence have zeros in dx."""
+    lib = _lib if _lib is not None else load_library()
+    B, T, C, N = _norm_check(x, groups, weight, bias, over, cu_seqlens)
+    dev = _here(x, dy, weight, bias, cu_seqlens, stats, workspace)
+    _f32(stats)
+    _shape("dy", dy, x.shape)
+    _shape("stats", stats, (N, groups, 2))
+    out = {"dx": dy.new_empty(x.shape),
+           "dweight": torch.empty(C, dtype=torch.float32, device=x.device) if weight is not None else None,
+           "dbias": torch.empty(C, dtype=torch.float32, device=x.device) if bias is not None else None}
+    seq = _NORM_OVER[over]
+    ws, ws_bytes = _workspace(int(lib.kda_group_norm_bwd_workspace_size(B, T, C, groups, N, seq, int(cu_seqlens is not None),
+                                                                        int(stats is not None))), x.device, workspace)
+    px, ldx = _rows("x", x, x.dim() - 1)
+    st = lib.kda_group_norm_bwd(px, ldx, _at(weight), _at(bias), eps, act, seq, _dt(x), _at(cu_seqlens), B, T, C, groups, N,
+                                _at(dy), _dt(dy), _at(stats), _at(out["dx"]), _at(out["dweight"]), _at(out["dbias"]), _at(ws),
+                                ws_bytes, _stream_of(dev))
+    _check("kda_group_norm_bwd", st)
     return out
 
 
