@@ -648,7 +648,7 @@ KDA_API kda_status kda_ssm_scan_bwd(const void *u, int64_t ldu, const void *delt
  *           they are.
  *  states   fp32 [B, ceil(T / 32), C] or NULL: the state before tokens 0, 32, 64 ... of each
  *           batch row (zeros where a sequence begins), for kda_gated_scan_bwd.
- * B ceil(C / 64) <= 2^28 - 1.  sigmoid(i) and sigmoid(z) end at 2^-60.
+ * B ceil(C / 64) <= 2^28 - 1.
  */
 KDA_API kda_status kda_gated_scan_fwd(const void *x, int64_t ldx, const void *r, int64_t ldr, const void *i,
                               int64_t ldi, const float *lam, const void *z, int64_t ldz, float decay,

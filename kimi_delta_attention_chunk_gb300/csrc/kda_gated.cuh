@@ -4,13 +4,14 @@
 //     s = rate sigmoid(r),  a = e^-s,  m = sqrt(1 - e^-2s),  u = m sigmoid(i) x,  h <- a h + u,  y = h silu(z)
 #pragma once
 
+#include <atomic>
+
 #include "kda_layer.h"
 #include "kda_segments.cuh"
 
 namespace kda {
 
 constexpr int kSms = 152;
-constexpr int kGatedThreads = 256, kGatedWarps = kGatedThreads / 32;
 constexpr int kGatedCh = 64;  // channels of a block: a pair a lane, 128 bytes of a bf16 row
 constexpr int kMostCluster = 8;
 
@@ -22,50 +23,57 @@ __device__ __forceinline__ float rsq(float x) {
     return y;
 }
 
-// rate = decay log(1 + e^lam) of one channel (once a kernel: with the accurate functions).
-__device__ __forceinline__ float gated_rate(float lam, float decay) { return decay * (fmaxf(lam, 0.f) + log1pf(expf(-fabsf(lam)))); }
-
-// 1 + e^-x, for sigmoid(x) = 1 / it.  kBound: no more than 2^60, so that the product of two can be inverted; sigmoid then ends at
-// 2^-60 where it would go on to zero.
-template <bool kBound>
-__device__ __forceinline__ f2 one_plus(f2 x) {
-    f2 t = mul2(x, both(-kLog2e));
-    if constexpr (kBound) {
-        float a, b;
-        unpack(t, a, b);
-        t = pack(fminf(a, 60.f), fminf(b, 60.f));
-    }
-    return add2(ex2_2(t), both(1.f));
-}
-__device__ __forceinline__ f2 rcp2(f2 x) {
+// 1 / (1 + e^-x) of a pair, packed but for the special functions.
+__device__ __forceinline__ f2 gate2(f2 x) {
     float a, b;
-    unpack(x, a, b);
+    unpack(add2(ex2_2(mul2(x, both(-kLog2e))), both(1.f)), a, b);
     return pack(rcp(a), rcp(b));
 }
 
-// The decay of a pair of channels from sigmoid(r): a, and a^2 and m^2 = 1 - e^-2s.  Where s < 1/4, 1 - e^-2s would lose its leading bits
-// (layers are initialised with a in 0.9 ... 0.999); it is 2 a sinh(s) there, with sinh(s) / s = 1 + s^2/6 + s^4/120 to 5e-8.
+// rate = decay log(1 + e^lam) of one channel (once a kernel: with the accurate functions).
+__device__ __forceinline__ float gated_rate(float lam, float decay) { return decay * (fmaxf(lam, 0.f) + log1pf(expf(-fabsf(lam)))); }
+
+// The decay of a pair of channels from sr = sigmoid(r): a = e^-s with s = rate sr, and m2 = 1 - a^2.  Where s < 1/4, 1 - a^2 would lose its
+// leading bits (layers are initialised with a in 0.9 ... 0.999); it is 2 a sinh(s) there, with sinh(s) / s = 1 + s^2/6 + s^4/120 to 5e-8.
+// kSmall: rate < 1/4, so every s is (known once a kernel).
 struct Decay {
     f2 a, m2;
-    __device__ __forceinline__ Decay(f2 sr, f2 rate) {
-        const f2 s = mul2(sr, rate);
-        a = ex2_2(mul2(s, both(-kLog2e)));
-        const f2 q = mul2(s, s);
-        const f2 series = fma2(q, fma2(q, both(1.f / 120.f), both(1.f / 6.f)), both(1.f));
-        const f2 small = mul2(mul2(mul2(a, s), both(2.f)), series), large = fma2(neg2(a), a, both(1.f));
-        float s0, s1, x0, x1, y0, y1;
-        unpack(s, s0, s1);
-        unpack(small, x0, x1);
-        unpack(large, y0, y1);
-        m2 = pack(s0 < 0.25f ? x0 : y0, s1 < 0.25f ? x1 : y1);
+    template <bool kSmall>
+    static __device__ __forceinline__ Decay of(f2 sr, f2 rate) {
+        Decay d;
+        const f2 s = mul2(sr, rate), q = mul2(s, s);
+        d.a = ex2_2(mul2(s, both(-kLog2e)));
+        d.m2 = mul2(mul2(d.a, s), fma2(q, fma2(q, both(1.f / 60.f), both(1.f / 3.f)), both(2.f)));
+        if constexpr (!kSmall) {
+            float s0, s1, x0, x1, y0, y1;
+            unpack(s, s0, s1);
+            unpack(d.m2, x0, x1);
+            unpack(fma2(mul2(d.a, d.a), both(-1.f), both(1.f)), y0, y1);
+            d.m2 = pack(s0 < 0.25f ? x0 : y0, s1 < 0.25f ? x1 : y1);
+        }
+        return d;
     }
 };
+__device__ __forceinline__ bool small_rate(f2 rate) {
+    float a, b;
+    unpack(rate, a, b);
+    return fmaxf(a, b) < 0.25f;
+}
 // 1 / m; m = m^2 / m.  (m^2 = 0, a closed gate: m = 0.)
 __device__ __forceinline__ f2 inverse_root(f2 m2) {
     float a, b;
     unpack(m2, a, b);
     return pack(rsq(fmaxf(a, 1e-36f)), rsq(fmaxf(b, 1e-36f)));
 }
+__device__ __forceinline__ f2 root2(f2 m2) {
+    float a, b;
+    unpack(m2, a, b);
+    asm("sqrt.approx.ftz.f32 %0, %0;" : "+f"(a));
+    asm("sqrt.approx.ftz.f32 %0, %0;" : "+f"(b));
+    return pack(a, b);
+}
+// 1 - x
+__device__ __forceinline__ f2 rest2(f2 x) { return fma2(x, both(-1.f), both(1.f)); }
 
 // h -> A h + H.  Where a sequence begins inside (kCuts), A's sign bit is set and h does not reach the end, be it infinite or NaN.
 struct __align__(16) Affine {
@@ -102,7 +110,13 @@ __device__ __forceinline__ unsigned cluster_rank() {
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+// kStores: this thread has stored into another block's shared memory (the fence waits for its stores to global memory too, and
+// is left to the warps that need it).
+template <bool kStores>
+__device__ __forceinline__ void cluster_arrive() {
+    if constexpr (kStores) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+    else asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 // Writes v to the place of `mine` (an address in this block's shared memory) in block `rank` of the cluster.
 __device__ __forceinline__ void store_at(unsigned rank, void* mine, const Affine& v) {
@@ -113,16 +127,42 @@ __device__ __forceinline__ void store_at(unsigned rank, void* mine, const Affine
 
 // ---- tiles -------------------------------------------------------------------------------------------------
 
-// Requests `rows` rows of `has` channels at `from`, ld apart, into a tile [..][kGatedCh], by pieces of VEC elements.
-template <typename T, int TT, int VEC>
-__device__ __forceinline__ void request_rows(T* tile, const T* from, int64_t ld, int rows, int has) {
-    constexpr int PR = kGatedCh / VEC;
+// A lane's share of the rows of one tensor's strips (R rows of kGatedCh channels, copied by the warp that works on them), by pieces of
+// VEC elements.  Strips are asked for in turn, `step` tokens apart.
+template <typename T, int R, int VEC>
+struct Feed {
+    static constexpr int PR = kGatedCh / VEC;           // pieces of a row
+    static constexpr int N = R * PR / 32;               // pieces of a lane
+    static constexpr int ROWS = PR < 32 ? 32 / PR : 1;  // rows between them (one row by several rounds: PR = 64)
+    static_assert(R * PR % 32 == 0 && (PR <= 32 || PR == 64), "whole rounds");
+    const T* at;         // the next strip's piece of this lane
+    int64_t step, more;  // elements to the next strip's, and to the next row's
+    __device__ __forceinline__ Feed(const void* base, int64_t ld, int64_t first_row, int c0, int step)
+        : at(static_cast<const T*>(base) + (first_row + row()) * ld + c0 + col()), step(step * ld), more(ROWS * ld) {}
+    static __device__ __forceinline__ int row() { return threadIdx.x % 32 / PR; }
+    static __device__ __forceinline__ int col() { return threadIdx.x % 32 % PR * VEC; }
+    // The next strip, of which `rows` rows are there (none: <= 0) and `has` channels.
+    __device__ __forceinline__ void request(T* strip, int rows, int has) {
+        T* const to = strip + row() * kGatedCh + col();
+        const T* from = at;
+        if constexpr (PR <= 32) {
+            if (col() < has) {
+                if (rows >= R) {
 #pragma unroll
-    for (int k = 0; k < TT * PR; k += kGatedThreads) {
-        const int e = k + (int)threadIdx.x, r = e / PR, c = e % PR * VEC;
-        if ((TT * PR % kGatedThreads == 0 || e < TT * PR) && r < rows && c < has) Row<T, VEC>::copy_async(tile + r * kGatedCh + c, from + r * ld + c);
+                    for (int k = 0; k < N; ++k, from += more) Row<T, VEC>::copy_async(to + k * ROWS * kGatedCh, from);
+                } else {
+                    for (int r = row(); r < rows; r += ROWS, from += more) Row<T, VEC>::copy_async(strip + r * kGatedCh + col(), from);
+                }
+            }
+        } else {
+            for (int r = 0; r < rows && r < R; ++r, from += more) {
+                if (col() < has) Row<T, VEC>::copy_async(to + r * kGatedCh, from);
+                if (col() + 32 * VEC < has) Row<T, VEC>::copy_async(to + r * kGatedCh + 32 * VEC, from + 32 * VEC);
+            }
+        }
+        at += step;
     }
-}
+};
 template <typename T>
 __device__ __forceinline__ f2 pair_at(const T* shared) {
     Row<T, 2> p;
@@ -157,14 +197,12 @@ __device__ __forceinline__ void store_state(float* p, int64_t at, f2 h, int n) {
     if (n > 1) p[at + 1] = b;
 }
 
-// Launches a kernel in clusters of `cluster` blocks.
+// Launches a kernel (its shared memory set) in clusters of `cluster` blocks.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_clusters(void (*kern)(KArgs...), int64_t grid, int cluster, int smem, cudaStream_t st, Args... args) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
+cudaError_t launch_clusters(void (*kern)(KArgs...), int64_t grid, int cluster, int threads, int smem, cudaStream_t st, Args... args) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = kGatedThreads;
+    cfg.blockDim = threads;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -176,12 +214,45 @@ cudaError_t launch_clusters(void (*kern)(KArgs...), int64_t grid, int cluster, i
     return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
 }
 
-// Blocks of a cluster: as many as bring the call's blocks to about two an SM, no more than there are tiles.
-inline int cluster_size(int64_t groups, int T, int tile) {
-    int k = 1;
-    while (k < kMostCluster && groups * k * 2 <= 2 * kSms && (int64_t)k * tile < T) k *= 2;
-    return k;
+inline int most_blocks(int T, int tile) {
+    const int tiles = T / tile + (T % tile != 0);
+    return tiles < 1 ? 1 : tiles < kMostCluster ? tiles : kMostCluster;
 }
+
+// The launch of one kernel in clusters: how many of each size the machine holds at once, asked for once a process.
+struct ClusterRoom {
+    std::atomic<int> room[kMostCluster + 1];
+    template <typename K>
+    int of(K kern, int size, int threads, int smem) {
+        int n = room[size].load(std::memory_order_relaxed);
+        if (n == 0) {
+            cudaLaunchConfig_t cfg{};
+            cfg.gridDim = dim3(size * 1024);
+            cfg.blockDim = threads;
+            cfg.dynamicSmemBytes = smem;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = size;
+            attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+                cudaGetLastError();
+                n = 0;
+            }
+            n = n > 0 ? n : -1;
+            room[size].store(n, std::memory_order_relaxed);
+        }
+        return n;
+    }
+    // Blocks of a cluster for `groups` clusters of streams of T tokens: as many as run at once, no more than there are tiles.
+    template <typename K>
+    int size_for(K kern, int64_t groups, int T, int tile, int threads, int smem) {
+        for (int k = most_blocks(T, tile); k > 1; --k)
+            if (groups <= of(kern, k, threads, smem)) return k;
+        return 1;
+    }
+};
 
 // Whether rows of p can be read by pieces of `bytes`: every pointer, stride and the row's length.
 inline bool gated_pieces(const GatedParams& p, int es, int bytes) {

@@ -16,59 +16,40 @@ namespace kda {
 
 namespace {
 
+constexpr int kGates = 7, kThreads = 32 * (kGates + 1);  // warps with a strip each, and one that folds their maps
 template <typename T>
-constexpr int kStripOf = sizeof(T) == 2 ? 8 : 4;  // tokens of a warp's strip
+constexpr int kStripOf = sizeof(T) == 2 ? 8 : 4;  // tokens of a strip
 template <typename T>
-constexpr int kTileOf = kGatedWarps * kStripOf<T>;
-constexpr int kStages = 3;
-
+constexpr int kTileOf = kGates * kStripOf<T>;
+// Two stages of x, r and i; z, which is needed last, has one place of its own.
 template <typename T, bool kRows>
-constexpr int kTensors = kRows ? 4 : 3;
-template <typename T, bool kRows>
-constexpr int kSmem = kStages * kTensors<T, kRows> * kTileOf<T> * kGatedCh * (int)sizeof(T);
+constexpr int kSmem = (kRows ? 7 : 6) * kTileOf<T> * kGatedCh * (int)sizeof(T);
 
 // kPacked: sequences by offsets, else a stream for each batch row.  kRows: y and the final states, else only the states that the
-// backward pass starts from.
+// backward pass starts from.  VEC: elements of a piece of x, r, i and z; with more than one, pairs of channels of y are whole and aligned.
 template <typename T, int VEC, bool kPacked, bool kRows>
-__global__ void __launch_bounds__(kGatedThreads, 2) gated_fwd_kernel(GatedParams p, int cluster, int blocks, bool whole_pairs) {
-    constexpr int STRIP = kStripOf<T>, TT = kTileOf<T>, NT = kTensors<T, kRows>, TILE = TT * kGatedCh;
+__global__ void __launch_bounds__(kThreads, 3) gated_fwd_kernel(GatedParams p, int cluster, int blocks) {
+    constexpr int STRIP = kStripOf<T>, TT = kTileOf<T>, PART = STRIP * kGatedCh;
     extern __shared__ __align__(128) char shared[];
-    T* const stage0 = reinterpret_cast<T*>(shared);
-    __shared__ Affine strips[kGatedWarps][32];
+    __shared__ Affine maps[kGates][32];
     __shared__ Affine peers[2][kMostCluster][32];
+    __shared__ f2 starts[kGates][32];
     __shared__ TokenTile<kPacked ? TT : 1> tile;
 
-    const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
+    const int lane = threadIdx.x % 32, w = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0);
     const int rank = cluster > 1 ? (int)cluster_rank() : 0;
     const int group = blockIdx.x / cluster, b = group / blocks, c0 = group % blocks * kGatedCh;
-    const int has = min(kGatedCh, p.C - c0), c = c0 + 2 * lane, n2 = min(2, p.C - c);  // pairs of this lane: 2, 1 or none (<= 0)
+    const int c = c0 + 2 * lane, has = p.C - c0, n2 = min(2, p.C - c);  // channels of this lane: 2, 1 or none (<= 0)
     const SeqMap m{p.cu, p.N, p.T, p.T};
     const int first = kPacked ? m.first() : 0, last = kPacked ? m.last() : p.T;
-    const int steps = (int)(((int64_t)p.T + TT * cluster - 1) / (TT * cluster));
+    const int stride = TT * cluster;  // tokens between a block's tiles
+    const int steps = (int)(((int64_t)p.T + stride - 1) / stride);
     const int64_t row0 = (int64_t)b * p.T;
+    const bool gates = w < kGates;
 
-    auto request = [&](int it) {
-        const int t0 = (it * cluster + rank) * TT;
-        const int rows = it < steps ? min(TT, p.T - t0) : 0;
-        T* const to = stage0 + it % kStages * (NT * TILE);
-        if (rows > 0) {
-#pragma unroll
-            for (int v = 0; v < NT; ++v) {
-                const void* base = v == 0 ? p.x : v == 1 ? p.r : v == 2 ? p.i : p.z;
-                const int64_t ld = v == 0 ? p.ldx : v == 1 ? p.ldr : v == 2 ? p.ldi : p.ldz;
-                if (v == 3 && !base) continue;
-                request_rows<T, TT, VEC>(to + v * TILE, static_cast<const T*>(base) + (row0 + t0) * ld + c0, ld, rows, has);
-            }
-        }
-        copies_commit();
-    };
-#pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) request(s);
-
-    const f2 rate = pack(n2 > 0 ? gated_rate(__ldg(p.lam + c), p.decay) : 0.f, n2 > 1 ? gated_rate(__ldg(p.lam + c + 1), p.decay) : 0.f);
     // sequences without tokens hand their states on
     if (kRows && p.final_state) {
-        const int warps = kGatedWarps * cluster;
+        const int warps = (kGates + 1) * cluster;
         for (int n0 = (w * cluster + rank) * 32; n0 < p.N; n0 += warps * 32) {
             if (!kPacked && p.T > 0) break;
             const int n = n0 + lane;
@@ -79,52 +60,127 @@ __global__ void __launch_bounds__(kGatedThreads, 2) gated_fwd_kernel(GatedParams
             }
         }
     }
-    f2 carry = kPacked ? 0ull : state_pair(p.initial, (int64_t)b * p.C + c, n2);
     if (cluster > 1) {  // everyone's shared memory is there
-        cluster_arrive();
+        cluster_arrive<false>();
         cluster_wait();
     }
-
     int until = 0;  // no boundary before this token
-    for (int it = 0; it < steps; ++it) {
-        const int t0 = (it * cluster + rank) * TT, rows = min(TT, p.T - t0);  // rows <= 0: nothing, behind the end
-        copies_wait<kStages - 2>();
-        __syncthreads();  // the tile is there, and everyone is past the one before
-        request(it + kStages - 1);
-        bool clear = true;  // no boundary in this warp's strip
-        if constexpr (kPacked) {
-            const bool plain = t0 + TT < until;  // (the same in the whole block)
-            if (!plain && rows > 0) {
-                tile.template build<kGatedThreads>(m, t0);
-                until = tile.until;
-                clear = tile.plain || tile.template clear<STRIP>(w * STRIP);
-            }
+    // Looks for boundaries in the tile at t0 (a whole block calls it): whether there are none in the cluster's tiles (wide), in the tile
+    // (plain).
+    auto look = [&](int it, int t0, bool& wide, bool& plain) {
+        // (the sequence at hand covers all of them if it already did at this block's tile before)
+        wide = (int64_t)(it + 1) * stride < until;
+        plain = true;
+        if (t0 < p.T && t0 + TT >= until) {
+            tile.template build<kThreads>(m, t0);
+            until = tile.until;
+            plain = tile.plain;
         }
-        const T* const in = stage0 + it % kStages * (NT * TILE) + w * STRIP * kGatedCh + 2 * lane;
-        f2 a[STRIP], u[STRIP], gate[STRIP];
+    };
+
+    if (!gates) {
+        // The folding warp: from the strips' maps the state before each of them; between the blocks of a cluster the tiles' maps.
+        f2 carry = kPacked ? 0ull : state_pair(p.initial, (int64_t)b * p.C + c, n2);
+        for (int it = 0; it < steps; ++it) {
+            bool wide = true, plain = true;
+            if constexpr (kPacked) look(it, it * stride + rank * TT, wide, plain);
+            __syncthreads();  // the maps are there
+            auto fold = [&](auto cuts) {
+                constexpr bool kCuts = decltype(cuts)::value;
+                Affine map[kGates];
 #pragma unroll
-        for (int j = 0; j < STRIP; ++j) {
-            const f2 x = pair_at(in + j * kGatedCh), r = pair_at(in + TILE + j * kGatedCh), i = pair_at(in + 2 * TILE + j * kGatedCh);
-            const Decay d(rcp2(one_plus<false>(r)), rate);
-            a[j] = d.a;
-            f2 si;
-            if (kRows && p.z) {
-                const f2 z = pair_at(in + 3 * TILE + j * kGatedCh), di = one_plus<true>(i), dz = one_plus<true>(z);
-                const f2 inv = rcp2(mul2(di, dz));
-                si = mul2(inv, dz);
-                gate[j] = mul2(z, mul2(inv, di));
-            } else {
-                si = rcp2(one_plus<false>(i));
-                gate[j] = both(1.f);
-            }
-            u[j] = mul2(mul2(mul2(d.m2, inverse_root(d.m2)), si), x);
+                for (int k = 0; k < kGates; ++k) map[k] = maps[k][lane];
+                f2 h = carry;
+                if (cluster > 1) {
+                    Affine total = map[0];
+#pragma unroll
+                    for (int k = 1; k < kGates; ++k) total = follow<kCuts>(total, map[k]);
+                    const int buf = it & 1;
+                    for (int k = 0; k < cluster; ++k) store_at(k, &peers[buf][rank][lane], total);
+                    cluster_arrive<true>();
+                    cluster_wait();
+                    Affine e[kMostCluster];
+#pragma unroll
+                    for (int k = 0; k < kMostCluster; ++k)
+                        if (k < cluster) e[k] = peers[buf][k][lane];
+#pragma unroll
+                    for (int k = 0; k < kMostCluster; ++k)
+                        if (k < cluster) {
+                            if (k == rank) h = carry;
+                            carry = apply<kCuts>(e[k].A, e[k].H, carry);
+                        }
+                }
+#pragma unroll
+                for (int k = 0; k < kGates; ++k) {
+                    starts[k][lane] = h;
+                    h = apply<kCuts>(map[k].A, map[k].H, h);
+                }
+                if (cluster == 1) carry = h;
+            };
+            if (!kPacked || wide) fold(std::false_type{});
+            else fold(std::true_type{});
+            __syncthreads();  // the states are
         }
-        if (rows < TT) {
+        return;
+    }
+
+    // this warp's rows: x, r and i [2][3][STRIP][64], z [STRIP][64]
+    T* const stage0 = reinterpret_cast<T*>(shared) + w * (kRows ? 7 : 6) * PART;
+    T* const zs = stage0 + 6 * PART;
+    const int64_t mine0 = row0 + rank * TT + w * STRIP;
+    Feed<T, STRIP, VEC> fx(p.x, p.ldx, mine0, c0, stride), fr(p.r, p.ldr, mine0, c0, stride), fi(p.i, p.ldi, mine0, c0, stride);
+    Feed<T, STRIP, VEC> fz(p.z, p.ldz, mine0, c0, stride);
+    int s0 = rank * TT + w * STRIP;  // this strip's first token
+    auto request = [&](int buf, int rows) {
+        T* const to = stage0 + buf * 3 * PART;
+        if (rows > 0) {
+            fx.request(to, rows, has);
+            fr.request(to + PART, rows, has);
+            fi.request(to + 2 * PART, rows, has);
+        }
+        copies_commit();
+    };
+    request(0, p.T - s0);
+    const f2 rate = pack(n2 > 0 ? gated_rate(__ldg(p.lam + c), p.decay) : 0.f, n2 > 1 ? gated_rate(__ldg(p.lam + c + 1), p.decay) : 0.f);
+    const bool small = __all_sync(0xffffffffu, small_rate(rate)) != 0;
+    T* to = static_cast<T*>(p.y) + (row0 + s0) * p.C + c;
+
+    for (int it = 0; it < steps; ++it, s0 += stride, to += (int64_t)stride * p.C) {
+        copies_wait<0>();
+        __syncwarp();  // the strip's rows are there, and every lane is past the strip before
+        if (kRows && p.z && s0 < p.T) fz.request(zs, p.T - s0, has);
+        copies_commit();
+        request((it + 1) & 1, p.T - s0 - stride);
+        bool clear = true;  // no boundary in the strip
+        if constexpr (kPacked) {
+            bool wide, plain;
+            look(it, s0 - w * STRIP, wide, plain);
+            clear = plain || tile.template clear<STRIP>(w * STRIP);
+        }
+        // the first walk: decays and inputs, and the strip's map
+        const T* const in = stage0 + (it & 1) * 3 * PART + 2 * lane;
+        f2 a[STRIP], u[STRIP];
+        auto first_walk = [&](auto small_rates) {
+#pragma unroll
+            for (int j = 0; j < STRIP; ++j) {
+                const f2 x = pair_at(in + j * kGatedCh), r = pair_at(in + PART + j * kGatedCh), i = pair_at(in + 2 * PART + j * kGatedCh);
+                const Decay d = Decay::of<decltype(small_rates)::value>(gate2(r), rate);
+                a[j] = d.a;
+                u[j] = mul2(mul2(root2(d.m2), gate2(i)), x);
+            }
+        };
+        if (small) first_walk(std::true_type{});
+        else first_walk(std::false_type{});
+        if (s0 + STRIP > p.T) {
 #pragma unroll
             for (int j = 0; j < STRIP; ++j)
-                if (w * STRIP + j >= rows) a[j] = both(1.f), u[j] = 0ull;
+                if (s0 + j >= p.T) a[j] = both(1.f), u[j] = 0ull;
         }
-        if (kPacked && !clear) {
+        Affine map{a[0], u[0]};
+        if (!kPacked || clear) {
+#pragma unroll
+            for (int j = 1; j < STRIP; ++j) map = follow<false>(map, Affine{a[j], u[j]});
+        } else {
 #pragma unroll
             for (int j = 0; j < STRIP; ++j) {
                 const int n = tile.start[w * STRIP + j];
@@ -132,53 +188,57 @@ __global__ void __launch_bounds__(kGatedThreads, 2) gated_fwd_kernel(GatedParams
                     if (p.initial) u[j] = fma2(a[j], state_pair(p.initial, (int64_t)n * p.C + c, n2), u[j]);
                     a[j] = both(-1.f);
                 }
+                map = j ? follow<true>(map, Affine{a[j], u[j]}) : Affine{a[j], u[j]};
             }
         }
-        Affine mine{a[0], u[0]};
-#pragma unroll
-        for (int j = 1; j < STRIP; ++j) mine = follow<kPacked>(mine, Affine{a[j], u[j]});
-        strips[w][lane] = mine;
+        maps[w][lane] = map;
         __syncthreads();
-        Affine before = identity(), total = identity();
+        if (cluster > 1) cluster_arrive<false>();
+        // the output gate, while the maps are folded
+        f2 gate[kRows ? STRIP : 1];
+        if constexpr (kRows) {
+            copies_wait<1>();
+            __syncwarp();
+            if (p.z) {
 #pragma unroll
-        for (int k = 0; k < kGatedWarps; ++k) {
-            if (k == w) before = total;
-            total = follow<kPacked>(total, strips[k][lane]);
-        }
-        f2 h = carry;
-        if (cluster > 1) {
-            const int buf = it & 1;
-            if (w < cluster) store_at(w, &peers[buf][rank][lane], total);
-            cluster_arrive();
-            cluster_wait();
-            for (int k = 0; k < cluster; ++k) {
-                if (k == rank) h = carry;
-                const Affine e = peers[buf][k][lane];
-                carry = apply<kPacked>(e.A, e.H, carry);
+                for (int j = 0; j < STRIP; ++j) {
+                    const f2 z = pair_at(zs + 2 * lane + j * kGatedCh);
+                    gate[j] = mul2(z, gate2(z));
+                }
             }
-        } else {
-            carry = apply<kPacked>(total.A, total.H, carry);
         }
-        h = apply<kPacked>(before.A, before.H, h);
-        if (p.states && w * STRIP % kGatedBlock == 0 && w * STRIP < rows) {
-            const bool begins = t0 + w * STRIP == 0 || (kPacked && !clear && tile.start[w * STRIP] >= 0);
-            const int64_t block = (int64_t)b * ((p.T + kGatedBlock - 1) / kGatedBlock) + (t0 + w * STRIP) / kGatedBlock;
+        if (cluster > 1) cluster_wait();
+        __syncthreads();
+        f2 h = starts[w][lane];
+        if (p.states && s0 % kGatedBlock == 0 && s0 < p.T) {
+            const bool begins = s0 == 0 || (kPacked && !clear && tile.start[w * STRIP] >= 0);
+            const int64_t block = (int64_t)b * ((p.T + kGatedBlock - 1) / kGatedBlock) + s0 / kGatedBlock;
             store_state(p.states, block * p.C + c, begins ? 0ull : h, n2);
         }
         if constexpr (kRows) {
-            T* const to = static_cast<T*>(p.y) + (row0 + t0 + w * STRIP) * p.C + c;
+            if (VEC > 1 && (!kPacked || clear) && s0 >= first && s0 + STRIP <= last) {
+                // all of the strip's tokens are of one sequence
+                T* at = to;
+                auto walk = [&](auto gated) {
 #pragma unroll
-            for (int j = 0; j < STRIP; ++j) {
-                h = apply<kPacked>(a[j], u[j], h);
-                const int t = t0 + w * STRIP + j;
-                if (w * STRIP + j < rows && t >= first && t < last) {
-                    const f2 y = mul2(h, gate[j]);
-                    if (whole_pairs) store_pair<T, true>(to + (int64_t)j * p.C, y, n2);
-                    else store_pair<T, false>(to + (int64_t)j * p.C, y, n2);
-                }
-                if (p.final_state) {
-                    const int n = kPacked ? (clear ? -1 : tile.end[w * STRIP + j]) : (t == p.T - 1 ? b : -1);
-                    if (n >= 0) store_state(p.final_state, (int64_t)n * p.C + c, h, n2);
+                    for (int j = 0; j < STRIP; ++j, at += p.C) {
+                        h = fma2(a[j], h, u[j]);
+                        store_pair<T, true>(at, decltype(gated)::value ? mul2(h, gate[j]) : h, n2);
+                    }
+                };
+                if (p.z) walk(std::true_type{});
+                else walk(std::false_type{});
+                if (!kPacked && p.final_state && s0 + STRIP == p.T) store_state(p.final_state, (int64_t)b * p.C + c, h, n2);
+            } else {
+#pragma unroll
+                for (int j = 0; j < STRIP; ++j) {
+                    h = apply<kPacked>(a[j], u[j], h);
+                    const int t = s0 + j;
+                    if (t >= first && t < last) store_pair<T, false>(to + (int64_t)j * p.C, p.z ? mul2(h, gate[j]) : h, n2);
+                    if (p.final_state) {
+                        const int n = kPacked ? (clear ? -1 : tile.end[w * STRIP + j]) : (t == p.T - 1 ? b : -1);
+                        if (n >= 0) store_state(p.final_state, (int64_t)n * p.C + c, h, n2);
+                    }
                 }
             }
         }
@@ -186,34 +246,39 @@ __global__ void __launch_bounds__(kGatedThreads, 2) gated_fwd_kernel(GatedParams
 }
 
 template <typename T, int VEC, bool kPacked, bool kRows>
-cudaError_t launch(const GatedParams& p, bool whole_pairs, cudaStream_t st) {
+cudaError_t launch(const GatedParams& p, cudaStream_t st) {
     const int blocks = (p.C + kGatedCh - 1) / kGatedCh;
     const int64_t groups = (int64_t)blocks * p.B;
-    const int cluster = cluster_size(groups, p.T, kTileOf<T>);
-    return launch_clusters(gated_fwd_kernel<T, VEC, kPacked, kRows>, groups * cluster, cluster, kSmem<T, kRows>, st, p, cluster, blocks,
-                           whole_pairs);
+    const auto kern = gated_fwd_kernel<T, VEC, kPacked, kRows>;
+    constexpr int smem = kSmem<T, kRows>;
+    static ClusterRoom room;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const int cluster = room.size_for(kern, groups, p.T, kTileOf<T>, kThreads, smem);
+    return launch_clusters(kern, groups * cluster, cluster, kThreads, smem, st, p, cluster, blocks);
 }
 template <typename T, int VEC, bool kRows>
-cudaError_t launch_packed(const GatedParams& p, bool whole_pairs, cudaStream_t st) {
-    return p.cu ? launch<T, VEC, true, kRows>(p, whole_pairs, st) : launch<T, VEC, false, kRows>(p, whole_pairs, st);
+cudaError_t launch_packed(const GatedParams& p, cudaStream_t st) {
+    return p.cu ? launch<T, VEC, true, kRows>(p, st) : launch<T, VEC, false, kRows>(p, st);
 }
 template <typename T, int VEC>
-cudaError_t launch_rows(const GatedParams& p, bool whole_pairs, cudaStream_t st) {
-    return p.y || p.final_state ? launch_packed<T, VEC, true>(p, whole_pairs, st) : launch_packed<T, VEC, false>(p, whole_pairs, st);
+cudaError_t launch_rows(const GatedParams& p, cudaStream_t st) {
+    return p.y || p.final_state ? launch_packed<T, VEC, true>(p, st) : launch_packed<T, VEC, false>(p, st);
 }
 
 }  // namespace
 
 cudaError_t gated_scan_fwd(kda_dtype dt, const GatedParams& p, cudaStream_t st) {
     const int es = dt == KDA_BF16 ? 2 : 4;
-    const bool whole_pairs = p.C % 2 == 0 && (uintptr_t)p.y % (2 * es) == 0;
+    const bool pairs = p.C % 2 == 0 && (uintptr_t)p.y % (2 * es) == 0;
     if (dt == KDA_BF16) {
-        if (gated_pieces(p, es, 16)) return launch_rows<__nv_bfloat16, 8>(p, whole_pairs, st);
-        if (gated_pieces(p, es, 4)) return launch_rows<__nv_bfloat16, 2>(p, whole_pairs, st);
-        return launch_rows<__nv_bfloat16, 1>(p, whole_pairs, st);
+        if (pairs && gated_pieces(p, es, 16)) return launch_rows<__nv_bfloat16, 8>(p, st);
+        if (pairs && gated_pieces(p, es, 4)) return launch_rows<__nv_bfloat16, 2>(p, st);
+        return launch_rows<__nv_bfloat16, 1>(p, st);
     }
-    if (gated_pieces(p, es, 16)) return launch_rows<float, 4>(p, whole_pairs, st);
-    return launch_rows<float, 1>(p, whole_pairs, st);
+    if (pairs && gated_pieces(p, es, 16)) return launch_rows<float, 4>(p, st);
+    if (pairs && gated_pieces(p, es, 8)) return launch_rows<float, 2>(p, st);
+    return launch_rows<float, 1>(p, st);
 }
 
 }  // namespace kda

@@ -10,6 +10,8 @@
 // maps folded through shared memory, tiles side by side in a cluster.  What an element needs (a, u, m si, si x a^2 / m, sr, 1 - si, yb, dy
 // silu'(z)) stays in registers between the two walks: 128 a thread, two blocks an SM.  Without those states a first pass of the forward
 // kernel makes them (x, r and i are then read twice).  dlam's sums over tokens: one partial sum a block, added in a fixed order.
+#include <type_traits>
+
 #include "kda_gated.cuh"
 #include "kda_tc.cuh"
 
@@ -17,7 +19,8 @@ namespace kda {
 
 namespace {
 
-constexpr int kStrip = 4, kTile = kGatedWarps * kStrip;
+constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kStrip = 4, kTile = kWarps * kStrip;
 static_assert(kTile == kGatedBlock, "a tile begins at a state that is left to it");
 
 template <typename T>
@@ -26,17 +29,18 @@ template <typename T, typename TG>
 constexpr int kStageBytes = kTile * kGatedCh * (4 * (int)sizeof(T) + (int)sizeof(TG));
 
 template <typename T, typename TG, int VEC, int GVEC, bool kPacked>
-__global__ void __launch_bounds__(kGatedThreads, 2) gated_bwd_kernel(GatedParams p, float* partial, int cluster, int blocks, bool whole_pairs) {
-    constexpr int TILE = kTile * kGatedCh, STAGES = kStages<T>;
+__global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(GatedParams p, float* partial, int cluster, int blocks, bool whole_pairs) {
+    constexpr int STAGES = kStages<T>;
     extern __shared__ __align__(128) char shared[];
-    __shared__ Affine ahead[kGatedWarps][32], back[kGatedWarps][32];
+    __shared__ Affine ahead[kWarps][32], back[kWarps][32];
     __shared__ Affine peers[2][kMostCluster][32];
+    __shared__ f2 ends[32];
     __shared__ TokenTile<kPacked ? kTile : 1> tile;
 
-    const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
+    const int lane = threadIdx.x % 32, w = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0);
     const int rank = cluster > 1 ? (int)cluster_rank() : 0;
     const int group = blockIdx.x / cluster, b = group / blocks, c0 = group % blocks * kGatedCh;
-    const int has = min(kGatedCh, p.C - c0), c = c0 + 2 * lane, n2 = min(2, p.C - c);
+    const int c = c0 + 2 * lane, n2 = min(2, p.C - c);  // channels of this lane: 2, 1 or none (<= 0)
     const SeqMap m{p.cu, p.N, p.T, p.T};
     const int first = kPacked ? m.first() : 0, last = kPacked ? m.last() : p.T;
     const int steps = (int)(((int64_t)p.T + kTile * cluster - 1) / (kTile * cluster));
@@ -44,20 +48,23 @@ __global__ void __launch_bounds__(kGatedThreads, 2) gated_bwd_kernel(GatedParams
 
     // step `it` counts from the stream's end
     auto tile_of = [&](int it) { return ((steps - 1 - it) * cluster + rank) * kTile; };
+    // this warp's rows: a stage holds x, r, i, z [4][kStrip][64] and dy [kStrip][64]
+    constexpr int PART = kStrip * kGatedCh;
+    char* const mine = shared + w * (kStageBytes<T, TG> / kWarps);
+    const int64_t from_row = row0 + tile_of(0) + w * kStrip;
+    Feed<T, kStrip, VEC> fx(p.x, p.ldx, from_row, c0, -kTile * cluster), fr(p.r, p.ldr, from_row, c0, -kTile * cluster);
+    Feed<T, kStrip, VEC> fi(p.i, p.ldi, from_row, c0, -kTile * cluster), fz(p.z, p.ldz, from_row, c0, -kTile * cluster);
+    Feed<TG, kStrip, GVEC> fy(p.dy, p.C, from_row, c0, -kTile * cluster);
+    const int has = p.C - c0;
     auto request = [&](int it) {
-        const int t0 = it < steps ? tile_of(it) : 0;
-        const int rows = it < steps ? min(kTile, p.T - t0) : 0;
-        char* const to = shared + it % STAGES * kStageBytes<T, TG>;
-        if (rows > 0) {
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                const void* base = v == 0 ? p.x : v == 1 ? p.r : v == 2 ? p.i : p.z;
-                const int64_t ld = v == 0 ? p.ldx : v == 1 ? p.ldr : v == 2 ? p.ldi : p.ldz;
-                if (v == 3 && !base) continue;
-                request_rows<T, kTile, VEC>(reinterpret_cast<T*>(to) + v * TILE, static_cast<const T*>(base) + (row0 + t0) * ld + c0, ld, rows, has);
-            }
-            request_rows<TG, kTile, GVEC>(reinterpret_cast<TG*>(to + 4 * TILE * sizeof(T)), static_cast<const TG*>(p.dy) + (row0 + t0) * p.C + c0, p.C,
-                                          rows, has);
+        const int rows = it < steps ? p.T - (tile_of(it) + w * kStrip) : 0;
+        T* const in = reinterpret_cast<T*>(mine + it % STAGES * kStageBytes<T, TG>);
+        if (it < steps) {
+            fx.request(in, rows, has);
+            fr.request(in + PART, rows, has);
+            fi.request(in + 2 * PART, rows, has);
+            if (p.z) fz.request(in + 3 * PART, rows, has);
+            fy.request(reinterpret_cast<TG*>(in + 4 * PART), rows, has);
         }
         copies_commit();
     };
@@ -65,9 +72,10 @@ __global__ void __launch_bounds__(kGatedThreads, 2) gated_bwd_kernel(GatedParams
     for (int s = 0; s < STAGES - 1; ++s) request(s);
 
     const f2 rate = pack(n2 > 0 ? gated_rate(__ldg(p.lam + c), p.decay) : 0.f, n2 > 1 ? gated_rate(__ldg(p.lam + c + 1), p.decay) : 0.f);
+    const bool small = __all_sync(0xffffffffu, small_rate(rate)) != 0;
     // through sequences without tokens the gradient goes as it comes
     if (p.dinitial) {
-        const int warps = kGatedWarps * cluster;
+        const int warps = kWarps * cluster;
         for (int n0 = (w * cluster + rank) * 32; n0 < p.N; n0 += warps * 32) {
             if (!kPacked && p.T > 0) break;
             const int n = n0 + lane;
@@ -79,74 +87,80 @@ __global__ void __launch_bounds__(kGatedThreads, 2) gated_bwd_kernel(GatedParams
         }
     }
     f2 carry = kPacked ? 0ull : state_pair(p.dfinal, (int64_t)b * p.C + c, n2), dlam = 0ull;
+    if (w == 0) ends[lane] = carry;
     if (cluster > 1) {
-        cluster_arrive();
+        cluster_arrive<false>();
         cluster_wait();
     }
 
     int from = 0x7fffffff;  // behind this token, up to the tile before, no boundary
     for (int it = 0; it < steps; ++it) {
-        const int t0 = tile_of(it), rows = min(kTile, p.T - t0);
-        f2 start = 0ull;
+        const int t0 = tile_of(it), rows = min(kTile, p.T - t0), s0 = t0 + w * kStrip;
+        f2 h = 0ull;
         if (rows > 0) {
-            if (!kPacked && t0 == 0) start = state_pair(p.initial, (int64_t)b * p.C + c, n2);
-            else {
+            if (!kPacked && t0 == 0) {
+                h = state_pair(p.initial, (int64_t)b * p.C + c, n2);
+            } else {
                 const float* s = p.states + (block0 + t0 / kTile) * p.C + c;
-                start = pack(n2 > 0 ? s[0] : 0.f, n2 > 1 ? s[1] : 0.f);
+                h = pack(n2 > 0 ? s[0] : 0.f, n2 > 1 ? s[1] : 0.f);
             }
         }
         copies_wait<STAGES - 2>();
         __syncthreads();  // the tile is there, and everyone is past the one before
         request(it + STAGES - 1);
-        bool clear = true;
+        bool plain = true, clear = true;  // no boundary in the tile, in this warp's strip
         if constexpr (kPacked) {
             if (t0 <= from && rows > 0) {
-                tile.template build<kGatedThreads>(m, t0);
+                tile.template build<kThreads>(m, t0);
                 from = tile.carry >= 0 ? tile.carry_start : 0x7fffffff;
-                clear = tile.plain || tile.template clear<kStrip>(w * kStrip);
+                plain = tile.plain;
+                clear = plain || tile.template clear<kStrip>(w * kStrip);
             }
         }
-        const char* const at = shared + it % STAGES * kStageBytes<T, TG>;
-        const T* const in = reinterpret_cast<const T*>(at) + w * kStrip * kGatedCh + 2 * lane;
-        const TG* const dys = reinterpret_cast<const TG*>(at + 4 * TILE * sizeof(T)) + w * kStrip * kGatedCh + 2 * lane;
-        f2 a[kStrip], u[kStrip], wx[kStrip], wm[kStrip], sr[kStrip], ci[kStrip], yb[kStrip], gz[kStrip];
+        const bool inside = s0 >= first && s0 + kStrip <= min(last, t0 + rows);  // all of the strip's tokens are of some sequence
+        const T* const in = reinterpret_cast<const T*>(mine + it % STAGES * kStageBytes<T, TG>) + 2 * lane;
+        const TG* const dys = reinterpret_cast<const TG*>(in - 2 * lane + 4 * PART) + 2 * lane;
+        f2 a[kStrip], u[kStrip], wx[kStrip], wm[kStrip], sr[kStrip], ui[kStrip], yb[kStrip];
+        auto gates = [&](auto small_rates) {
 #pragma unroll
-        for (int j = 0; j < kStrip; ++j) {
-            const f2 x = pair_at(in + j * kGatedCh), r = pair_at(in + TILE + j * kGatedCh), i = pair_at(in + 2 * TILE + j * kGatedCh);
-            yb[j] = pair_at(dys + j * kGatedCh);
-            sr[j] = rcp2(one_plus<false>(r));
-            const Decay d(sr[j], rate);
-            a[j] = d.a;
-            f2 si;
-            if (p.z) {
-                const f2 z = pair_at(in + 3 * TILE + j * kGatedCh), di = one_plus<true>(i), dz = one_plus<true>(z);
-                const f2 inv = rcp2(mul2(di, dz)), sz = mul2(inv, di), silu = mul2(z, sz);
-                si = mul2(inv, dz);
-                gz[j] = mul2(yb[j], fma2(silu, fma2(neg2(sz), both(1.f), both(1.f)), sz));  // silu' = s + z s (1 - s)
-                yb[j] = mul2(yb[j], silu);
-            } else {
-                si = rcp2(one_plus<false>(i));
-                gz[j] = 0ull;
+            for (int j = 0; j < kStrip; ++j) {
+                const f2 x = pair_at(in + j * kGatedCh), r = pair_at(in + PART + j * kGatedCh), i = pair_at(in + 2 * PART + j * kGatedCh);
+                sr[j] = gate2(r);
+                const f2 si = gate2(i);
+                const Decay d = Decay::of<decltype(small_rates)::value>(sr[j], rate);
+                const f2 inv = inverse_root(d.m2), gx = mul2(si, x), m1 = mul2(d.m2, inv);
+                a[j] = d.a;
+                wx[j] = mul2(m1, si);
+                u[j] = mul2(m1, gx);
+                ui[j] = mul2(u[j], rest2(si));
+                wm[j] = mul2(mul2(gx, inv), mul2(d.a, d.a));
+                yb[j] = pair_at(dys + j * kGatedCh);
             }
-            const f2 inv = inverse_root(d.m2), gx = mul2(si, x);
-            wx[j] = mul2(mul2(d.m2, inv), si);
-            u[j] = mul2(wx[j], x);
-            ci[j] = add2(both(1.f), neg2(si));
-            wm[j] = mul2(mul2(gx, inv), mul2(a[j], a[j]));
+        };
+        if (small) gates(std::true_type{});
+        else gates(std::false_type{});
+        if (p.z) {
+#pragma unroll
+            for (int j = 0; j < kStrip; ++j) {
+                const f2 z = pair_at(in + 3 * PART + j * kGatedCh);
+                yb[j] = mul2(yb[j], mul2(z, gate2(z)));
+            }
         }
         if (rows < kTile) {
 #pragma unroll
             for (int j = 0; j < kStrip; ++j)
                 if (w * kStrip + j >= rows) a[j] = both(1.f), u[j] = yb[j] = 0ull;
         }
-        // the strip's maps forwards (af, u: cut where a sequence begins) and backwards (cut where one ends)
+        // the strip's maps forwards (cut where a sequence begins) and backwards (cut where one ends)
         Affine fore = identity(), rear = identity();
         if (!kPacked || clear) {
+            fore = Affine{a[0], u[0]};
 #pragma unroll
-            for (int j = 0; j < kStrip; ++j) fore = follow<false>(fore, Affine{a[j], u[j]});
+            for (int j = 1; j < kStrip; ++j) fore = follow<false>(fore, Affine{a[j], u[j]});
             rear.A = fore.A;
+            rear.H = mul2(a[kStrip - 1], yb[kStrip - 1]);
 #pragma unroll
-            for (int j = kStrip - 1; j >= 0; --j) rear.H = mul2(a[j], add2(yb[j], rear.H));
+            for (int j = kStrip - 2; j >= 0; --j) rear.H = mul2(a[j], add2(yb[j], rear.H));
         } else {
 #pragma unroll
             for (int j = 0; j < kStrip; ++j) {
@@ -167,73 +181,122 @@ __global__ void __launch_bounds__(kGatedThreads, 2) gated_bwd_kernel(GatedParams
         }
         ahead[w][lane] = fore;
         back[w][lane] = rear;
+        f2 g = cluster > 1 ? carry : ends[lane];
         __syncthreads();
-        f2 h = start;
-        for (int k = 0; k < w; ++k) {
-            const Affine e = ahead[k][lane];
-            h = apply<kPacked>(e.A, e.H, h);
-        }
-        Affine behind = identity(), total = identity();
-#pragma unroll
-        for (int k = kGatedWarps - 1; k >= 0; --k) {
-            if (k == w) behind = total;
-            total = follow<kPacked>(total, back[k][lane]);
-        }
-        f2 g = carry;
+        const int buf = it & 1;
         if (cluster > 1) {
-            const int buf = it & 1;
-            if (w < cluster) store_at(w, &peers[buf][rank][lane], total);
-            cluster_arrive();
-            cluster_wait();
-            for (int k = cluster - 1; k >= 0; --k) {
-                if (k == rank) g = carry;
-                const Affine e = peers[buf][k][lane];
-                carry = apply<kPacked>(e.A, e.H, carry);
+            if (w == kWarps - 1) {
+                Affine total = rear;
+                if (!kPacked || plain) {
+#pragma unroll
+                    for (int k = kWarps - 2; k >= 0; --k) total = follow<false>(total, back[k][lane]);
+                } else {
+#pragma unroll
+                    for (int k = kWarps - 2; k >= 0; --k) total = follow<true>(total, back[k][lane]);
+                }
+                for (int k = 0; k < cluster; ++k) store_at(k, &peers[buf][rank][lane], total);
+                cluster_arrive<true>();
+            } else {
+                cluster_arrive<false>();
             }
-        } else {
-            carry = apply<kPacked>(total.A, total.H, carry);
         }
-        g = apply<kPacked>(behind.A, behind.H, g);
-        // the state before each token
-        f2 hp[kStrip];
-        const int64_t row = (row0 + t0 + w * kStrip) * p.C + c;
+        // the state before each token, and with it what dh is multiplied by: e = si x a^2 / m - a h_{t-1}; dz is done
+        if (!kPacked || plain) {
+#pragma unroll
+            for (int k = 0; k < kWarps - 1; ++k)
+                if (k < w) {
+                    const Affine e = ahead[k][lane];
+                    h = fma2(e.A, h, e.H);
+                }
+        } else {
+            for (int k = 0; k < w; ++k) {
+                const Affine e = ahead[k][lane];
+                h = apply<true>(e.A, e.H, h);
+            }
+        }
+        const bool lean = (!kPacked || clear) && inside && whole_pairs;
+        const int64_t row = (row0 + s0) * p.C + c;
 #pragma unroll
         for (int j = 0; j < kStrip; ++j) {
             if (kPacked && !clear) {
                 const int n = tile.start[w * kStrip + j];
                 if (n >= 0) h = state_pair(p.initial, (int64_t)n * p.C + c, n2);
             }
-            hp[j] = h;
-            h = fma2(a[j], h, u[j]);
-            gz[j] = mul2(gz[j], h);
+            const f2 ah = mul2(a[j], h);
+            wm[j] = fma2(ah, both(-1.f), wm[j]);
+            u[j] = add2(ah, u[j]);  // h
+            h = u[j];
         }
+        if (p.z) {
+            TG* to = static_cast<TG*>(p.dz) + row;
 #pragma unroll
-        for (int j = kStrip - 1; j >= 0; --j) {
-            const int t = t0 + w * kStrip + j;
-            if (w * kStrip + j >= rows) continue;
-            const bool in_one = !kPacked || (t >= first && t < last);
-            if (kPacked && !clear && tile.end[w * kStrip + j] >= 0) g = 0ull;
-            const f2 dh = add2(yb[j], g);
-            f2 dx = mul2(dh, wx[j]), di = mul2(mul2(dh, u[j]), ci[j]);
-            const f2 ds = mul2(dh, fma2(neg2(a[j]), hp[j], wm[j])), part = mul2(ds, sr[j]);
-            f2 dr = mul2(mul2(part, rate), fma2(neg2(sr[j]), both(1.f), both(1.f))), dz = gz[j];
-            g = mul2(a[j], dh);
-            if (in_one) dlam = add2(dlam, part);
-            else dx = di = dr = dz = 0ull;
-            const int64_t off = row + (int64_t)j * p.C;
-            auto put = [&](void* to, f2 v) {
-                if (whole_pairs) store_pair<TG, true>(static_cast<TG*>(to) + off, v, n2);
-                else store_pair<TG, false>(static_cast<TG*>(to) + off, v, n2);
-            };
-            put(p.dx, dx);
-            put(p.dr, dr);
-            put(p.di, di);
-            if (p.z) put(p.dz, dz);
-            if (p.dinitial) {
-                const int n = kPacked ? (clear ? -1 : tile.start[w * kStrip + j]) : (t == 0 ? b : -1);
-                if (n >= 0) store_state(p.dinitial, (int64_t)n * p.C + c, g, n2);
+            for (int j = 0; j < kStrip; ++j, to += p.C) {
+                const f2 z = pair_at(in + 3 * PART + j * kGatedCh), s = gate2(z);
+                // silu' = s + z s (1 - s)
+                const f2 dz = mul2(mul2(pair_at(dys + j * kGatedCh), u[j]), fma2(mul2(z, s), rest2(s), s));
+                if (lean) {
+                    store_pair<TG, true>(to, dz, n2);
+                } else if (w * kStrip + j < rows) {
+                    store_pair<TG, false>(to, s0 + j >= first && s0 + j < last ? dz : 0ull, n2);
+                }
             }
         }
+        if (cluster > 1) {
+            cluster_wait();
+#pragma unroll 4
+            for (int k = cluster - 1; k >= 0; --k) {
+                if (k == rank) g = carry;
+                const Affine e = peers[buf][k][lane];
+                carry = apply<kPacked>(e.A, e.H, carry);
+            }
+        }
+        if (!kPacked || plain) {
+#pragma unroll
+            for (int k = kWarps - 1; k > 0; --k)
+                if (k > w) {
+                    const Affine e = back[k][lane];
+                    g = fma2(e.A, g, e.H);
+                }
+        } else {
+            for (int k = kWarps - 1; k > w; --k) {
+                const Affine e = back[k][lane];
+                g = apply<true>(e.A, e.H, g);
+            }
+        }
+        if (lean) {
+            int64_t off = row + (int64_t)(kStrip - 1) * p.C;
+#pragma unroll
+            for (int j = kStrip - 1; j >= 0; --j, off -= p.C) {
+                const f2 dh = add2(yb[j], g), part = mul2(mul2(dh, wm[j]), sr[j]);
+                g = mul2(a[j], dh);
+                dlam = add2(dlam, part);
+                store_pair<TG, true>(static_cast<TG*>(p.dx) + off, mul2(dh, wx[j]), n2);
+                store_pair<TG, true>(static_cast<TG*>(p.dr) + off, mul2(mul2(part, rate), rest2(sr[j])), n2);
+                store_pair<TG, true>(static_cast<TG*>(p.di) + off, mul2(dh, ui[j]), n2);
+            }
+            if (!kPacked && s0 == 0 && p.dinitial) store_state(p.dinitial, (int64_t)b * p.C + c, g, n2);
+        } else {
+#pragma unroll
+            for (int j = kStrip - 1; j >= 0; --j) {
+                const int t = s0 + j;
+                if (w * kStrip + j >= rows) continue;
+                if (kPacked && !clear && tile.end[w * kStrip + j] >= 0) g = 0ull;
+                const f2 dh = add2(yb[j], g);
+                f2 part = mul2(mul2(dh, wm[j]), sr[j]), dx = mul2(dh, wx[j]), dr = mul2(mul2(part, rate), rest2(sr[j])), di = mul2(dh, ui[j]);
+                g = mul2(a[j], dh);
+                if (t >= first && t < last) dlam = add2(dlam, part);
+                else dx = di = dr = 0ull;
+                const int64_t off = row + (int64_t)j * p.C;
+                store_pair<TG, false>(static_cast<TG*>(p.dx) + off, dx, n2);
+                store_pair<TG, false>(static_cast<TG*>(p.dr) + off, dr, n2);
+                store_pair<TG, false>(static_cast<TG*>(p.di) + off, di, n2);
+                if (p.dinitial) {
+                    const int n = kPacked ? (clear ? -1 : tile.start[w * kStrip + j]) : (t == 0 ? b : -1);
+                    if (n >= 0) store_state(p.dinitial, (int64_t)n * p.C + c, g, n2);
+                }
+            }
+        }
+        if (cluster == 1 && w == 0) ends[lane] = g;
     }
     tc::grid_dep_launch();
     __syncthreads();
@@ -242,7 +305,7 @@ __global__ void __launch_bounds__(kGatedThreads, 2) gated_bwd_kernel(GatedParams
     if (w == 0 && steps > 0) {
         f2 sum = 0ull;
 #pragma unroll
-        for (int k = 0; k < kGatedWarps; ++k) sum = add2(sum, ahead[k][lane].A);
+        for (int k = 0; k < kWarps; ++k) sum = add2(sum, ahead[k][lane].A);
         store_state(partial + ((int64_t)b * cluster + rank) * p.C, c, sum, n2);
     }
 }
@@ -258,23 +321,25 @@ __global__ void __launch_bounds__(128) gated_dlam_kernel(const float* partial, i
     dlam[c] = decay * (l >= 0.f ? 1.f : e) / (1.f + e) * sum;
 }
 
-int clusters_of(const GatedParams& p) {
-    return cluster_size((int64_t)((p.C + kGatedCh - 1) / kGatedCh) * p.B, p.T, kTile);
-}
+// (one partial sum a block: as many as the largest clusters have)
 size_t partial_bytes(const GatedParams& p) {
-    return ((size_t)p.B * (p.T > 0 ? clusters_of(p) : 0) * p.C * 4 + 255) / 256 * 256;
+    return ((size_t)p.B * (p.T > 0 ? most_blocks(p.T, kTile) : 0) * p.C * 4 + 255) / 256 * 256;
 }
 
 template <typename T, typename TG, int VEC, int GVEC, bool kPacked>
 cudaError_t launch(const GatedParams& p, bool whole_pairs, cudaStream_t st) {
     const int blocks = (p.C + kGatedCh - 1) / kGatedCh;
     const int64_t groups = (int64_t)blocks * p.B;
-    const int cluster = clusters_of(p);
     float* const partial = static_cast<float*>(p.ws);
     int parts = 0;
     if (groups > 0) {
-        const cudaError_t e = launch_clusters(gated_bwd_kernel<T, TG, VEC, GVEC, kPacked>, groups * cluster, cluster, kStages<T> * kStageBytes<T, TG>, st,
-                                              p, partial, cluster, blocks, whole_pairs);
+        const auto kern = gated_bwd_kernel<T, TG, VEC, GVEC, kPacked>;
+        constexpr int smem = kStages<T> * kStageBytes<T, TG>;
+        static ClusterRoom room;
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        const int cluster = room.size_for(kern, groups, p.T, kTile, kThreads, smem);
+        e = launch_clusters(kern, groups * cluster, cluster, kThreads, smem, st, p, partial, cluster, blocks, whole_pairs);
         if (e != cudaSuccess) return e;
         parts = p.T > 0 ? p.B * cluster : 0;
     }

@@ -46,10 +46,10 @@ __global__ void __launch_bounds__(kThreads) gated_step_kernel(GatedStepParams p,
     for (int k = 0; k < N2; ++k) {
         const int k1 = VEC > 1 ? 2 * k + 1 : 0;
         const f2 rate = pack(gated_rate(lam[2 * k], p.decay), gated_rate(lam[k1], p.decay));
-        const Decay d(rcp2(one_plus<false>(rv[k])), rate);
-        const f2 u = mul2(mul2(mul2(d.m2, inverse_root(d.m2)), rcp2(one_plus<false>(iv[k]))), xv[k]);
+        const Decay d = Decay::of<false>(sigmoid2(rv[k]), rate);
+        const f2 u = mul2(mul2(root2(d.m2), sigmoid2(iv[k])), xv[k]);
         const f2 hn = fma2(d.a, pack(h[2 * k], h[k1]), u);
-        y[k] = p.z ? mul2(hn, mul2(zv[k], rcp2(one_plus<false>(zv[k])))) : hn;
+        y[k] = p.z ? mul2(hn, mul2(zv[k], sigmoid2(zv[k]))) : hn;
         float a, b;
         unpack(hn, a, b);
         h[2 * k] = a;
