@@ -16,24 +16,24 @@ namespace kda {
 
 namespace {
 
-constexpr int kGates = 7, kThreads = 32 * (kGates + 1);  // warps with a strip each, and one that folds their maps
+constexpr int kWarps = 8, kThreads = 32 * kWarps;
 template <typename T>
-constexpr int kStripOf = sizeof(T) == 2 ? 8 : 4;  // tokens of a strip
+constexpr int kStripOf = sizeof(T) == 2 ? 16 : 8;  // tokens of a strip
 template <typename T>
-constexpr int kTileOf = kGates * kStripOf<T>;
-// Two stages of x, r and i; z, which is needed last, has one place of its own.
+constexpr int kTileOf = kWarps * kStripOf<T>;
+// x, r, i and z of every warp's strip.  The next strip's x, r and i are asked for when the first walk is done with this one's, z before it.
 template <typename T, bool kRows>
-constexpr int kSmem = (kRows ? 7 : 6) * kTileOf<T> * kGatedCh * (int)sizeof(T);
+constexpr int kSmem = (kRows ? 4 : 3) * kTileOf<T> * kGatedCh * (int)sizeof(T);
 
 // kPacked: sequences by offsets, else a stream for each batch row.  kRows: y and the final states, else only the states that the
 // backward pass starts from.  VEC: elements of a piece of x, r, i and z; with more than one, pairs of channels of y are whole and aligned.
 template <typename T, int VEC, bool kPacked, bool kRows>
-__global__ void __launch_bounds__(kThreads, 3) gated_fwd_kernel(GatedParams p, int cluster, int blocks) {
+__global__ void __launch_bounds__(kThreads, 2) gated_fwd_kernel(GatedParams p, int cluster, int blocks) {
     constexpr int STRIP = kStripOf<T>, TT = kTileOf<T>, PART = STRIP * kGatedCh;
     extern __shared__ __align__(128) char shared[];
-    __shared__ Affine maps[kGates][32];
+    __shared__ Affine maps[2][kWarps][32];
     __shared__ Affine peers[2][kMostCluster][32];
-    __shared__ f2 starts[kGates][32];
+    __shared__ f2 ends[2][32];
     __shared__ TokenTile<kPacked ? TT : 1> tile;
 
     const int lane = threadIdx.x % 32, w = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0);
@@ -45,11 +45,27 @@ __global__ void __launch_bounds__(kThreads, 3) gated_fwd_kernel(GatedParams p, i
     const int stride = TT * cluster;  // tokens between a block's tiles
     const int steps = (int)(((int64_t)p.T + stride - 1) / stride);
     const int64_t row0 = (int64_t)b * p.T;
-    const bool gates = w < kGates;
+    int s0 = rank * TT + w * STRIP;  // this strip's first token
 
+    // this warp's rows: x, r, i and z [4][STRIP][64]
+    T* const mine = reinterpret_cast<T*>(shared) + w * (kRows ? 4 : 3) * PART;
+    Feed<T, STRIP, VEC> fx(p.x, p.ldx, row0 + s0, c0, stride), fr(p.r, p.ldr, row0 + s0, c0, stride), fi(p.i, p.ldi, row0 + s0, c0, stride);
+    Feed<T, STRIP, VEC> fz(p.z, p.ldz, row0 + s0, c0, stride);
+    auto request = [&](int rows) {
+        if (rows > 0) {
+            fx.request(mine, rows, has);
+            fr.request(mine + PART, rows, has);
+            fi.request(mine + 2 * PART, rows, has);
+        }
+        copies_commit();
+    };
+    request(p.T - s0);
+
+    const f2 rate = pack(n2 > 0 ? gated_rate(__ldg(p.lam + c), p.decay) : 0.f, n2 > 1 ? gated_rate(__ldg(p.lam + c + 1), p.decay) : 0.f);
+    const bool small = __all_sync(0xffffffffu, small_rate(rate)) != 0;
     // sequences without tokens hand their states on
     if (kRows && p.final_state) {
-        const int warps = (kGates + 1) * cluster;
+        const int warps = kWarps * cluster;
         for (int n0 = (w * cluster + rank) * 32; n0 < p.N; n0 += warps * 32) {
             if (!kPacked && p.T > 0) break;
             const int n = n0 + lane;
@@ -60,105 +76,35 @@ __global__ void __launch_bounds__(kThreads, 3) gated_fwd_kernel(GatedParams p, i
             }
         }
     }
+    f2 carry = kPacked ? 0ull : state_pair(p.initial, (int64_t)b * p.C + c, n2);
+    if (w == 0) ends[0][lane] = carry;
     if (cluster > 1) {  // everyone's shared memory is there
         cluster_arrive<false>();
         cluster_wait();
     }
+
     int until = 0;  // no boundary before this token
-    // Looks for boundaries in the tile at t0 (a whole block calls it): whether there are none in the cluster's tiles (wide), in the tile
-    // (plain).
-    auto look = [&](int it, int t0, bool& wide, bool& plain) {
-        // (the sequence at hand covers all of them if it already did at this block's tile before)
-        wide = (int64_t)(it + 1) * stride < until;
-        plain = true;
-        if (t0 < p.T && t0 + TT >= until) {
-            tile.template build<kThreads>(m, t0);
-            until = tile.until;
-            plain = tile.plain;
-        }
-    };
-
-    if (!gates) {
-        // The folding warp: from the strips' maps the state before each of them; between the blocks of a cluster the tiles' maps.
-        f2 carry = kPacked ? 0ull : state_pair(p.initial, (int64_t)b * p.C + c, n2);
-        for (int it = 0; it < steps; ++it) {
-            bool wide = true, plain = true;
-            if constexpr (kPacked) look(it, it * stride + rank * TT, wide, plain);
-            __syncthreads();  // the maps are there
-            auto fold = [&](auto cuts) {
-                constexpr bool kCuts = decltype(cuts)::value;
-                Affine map[kGates];
-#pragma unroll
-                for (int k = 0; k < kGates; ++k) map[k] = maps[k][lane];
-                f2 h = carry;
-                if (cluster > 1) {
-                    Affine total = map[0];
-#pragma unroll
-                    for (int k = 1; k < kGates; ++k) total = follow<kCuts>(total, map[k]);
-                    const int buf = it & 1;
-                    for (int k = 0; k < cluster; ++k) store_at(k, &peers[buf][rank][lane], total);
-                    cluster_arrive<true>();
-                    cluster_wait();
-                    Affine e[kMostCluster];
-#pragma unroll
-                    for (int k = 0; k < kMostCluster; ++k)
-                        if (k < cluster) e[k] = peers[buf][k][lane];
-#pragma unroll
-                    for (int k = 0; k < kMostCluster; ++k)
-                        if (k < cluster) {
-                            if (k == rank) h = carry;
-                            carry = apply<kCuts>(e[k].A, e[k].H, carry);
-                        }
-                }
-#pragma unroll
-                for (int k = 0; k < kGates; ++k) {
-                    starts[k][lane] = h;
-                    h = apply<kCuts>(map[k].A, map[k].H, h);
-                }
-                if (cluster == 1) carry = h;
-            };
-            if (!kPacked || wide) fold(std::false_type{});
-            else fold(std::true_type{});
-            __syncthreads();  // the states are
-        }
-        return;
-    }
-
-    // this warp's rows: x, r and i [2][3][STRIP][64], z [STRIP][64]
-    T* const stage0 = reinterpret_cast<T*>(shared) + w * (kRows ? 7 : 6) * PART;
-    T* const zs = stage0 + 6 * PART;
-    const int64_t mine0 = row0 + rank * TT + w * STRIP;
-    Feed<T, STRIP, VEC> fx(p.x, p.ldx, mine0, c0, stride), fr(p.r, p.ldr, mine0, c0, stride), fi(p.i, p.ldi, mine0, c0, stride);
-    Feed<T, STRIP, VEC> fz(p.z, p.ldz, mine0, c0, stride);
-    int s0 = rank * TT + w * STRIP;  // this strip's first token
-    auto request = [&](int buf, int rows) {
-        T* const to = stage0 + buf * 3 * PART;
-        if (rows > 0) {
-            fx.request(to, rows, has);
-            fr.request(to + PART, rows, has);
-            fi.request(to + 2 * PART, rows, has);
-        }
-        copies_commit();
-    };
-    request(0, p.T - s0);
-    const f2 rate = pack(n2 > 0 ? gated_rate(__ldg(p.lam + c), p.decay) : 0.f, n2 > 1 ? gated_rate(__ldg(p.lam + c + 1), p.decay) : 0.f);
-    const bool small = __all_sync(0xffffffffu, small_rate(rate)) != 0;
     T* to = static_cast<T*>(p.y) + (row0 + s0) * p.C + c;
-
     for (int it = 0; it < steps; ++it, s0 += stride, to += (int64_t)stride * p.C) {
-        copies_wait<0>();
-        __syncwarp();  // the strip's rows are there, and every lane is past the strip before
-        if (kRows && p.z && s0 < p.T) fz.request(zs, p.T - s0, has);
+        const int t0 = s0 - w * STRIP, buf = it & 1;
+        if (kRows && p.z && s0 < p.T) fz.request(mine + 3 * PART, p.T - s0, has);
         copies_commit();
-        request((it + 1) & 1, p.T - s0 - stride);
-        bool clear = true;  // no boundary in the strip
+        bool wide = true, plain = true, clear = true;  // no boundary in the cluster's tiles, in the tile, in the strip
         if constexpr (kPacked) {
-            bool wide, plain;
-            look(it, s0 - w * STRIP, wide, plain);
-            clear = plain || tile.template clear<STRIP>(w * STRIP);
+            // (the sequence at hand covers all of them if it already did at this block's tile before)
+            wide = (int64_t)(it + 1) * stride < until;
+            if (t0 < p.T && t0 + TT >= until) {  // (the same in the whole block)
+                __syncthreads();
+                tile.template build<kThreads>(m, t0);
+                until = tile.until;
+                plain = tile.plain;
+                clear = plain || tile.template clear<STRIP>(w * STRIP);
+            }
         }
         // the first walk: decays and inputs, and the strip's map
-        const T* const in = stage0 + (it & 1) * 3 * PART + 2 * lane;
+        copies_wait<1>();
+        __syncwarp();
+        const T* const in = mine + 2 * lane;
         f2 a[STRIP], u[STRIP];
         auto first_walk = [&](auto small_rates) {
 #pragma unroll
@@ -171,6 +117,8 @@ __global__ void __launch_bounds__(kThreads, 3) gated_fwd_kernel(GatedParams p, i
         };
         if (small) first_walk(std::true_type{});
         else first_walk(std::false_type{});
+        __syncwarp();
+        request(p.T - s0 - stride);
         if (s0 + STRIP > p.T) {
 #pragma unroll
             for (int j = 0; j < STRIP; ++j)
@@ -191,31 +139,52 @@ __global__ void __launch_bounds__(kThreads, 3) gated_fwd_kernel(GatedParams p, i
                 map = j ? follow<true>(map, Affine{a[j], u[j]}) : Affine{a[j], u[j]};
             }
         }
-        maps[w][lane] = map;
+        maps[buf][w][lane] = map;
         __syncthreads();
-        if (cluster > 1) cluster_arrive<false>();
-        // the output gate, while the maps are folded
-        f2 gate[kRows ? STRIP : 1];
-        if constexpr (kRows) {
-            copies_wait<1>();
-            __syncwarp();
-            if (p.z) {
+        // the state before the strip: between the blocks by their tiles' maps, then by the strips before
+        auto fold = [&](auto cuts) {
+            constexpr bool kCuts = decltype(cuts)::value;
+            f2 h;
+            if (cluster > 1) {
+                if (w == 0) {
+                    Affine total = map;
 #pragma unroll
-                for (int j = 0; j < STRIP; ++j) {
-                    const f2 z = pair_at(zs + 2 * lane + j * kGatedCh);
-                    gate[j] = mul2(z, gate2(z));
+                    for (int k = 1; k < kWarps; ++k) total = follow<kCuts>(total, maps[buf][k][lane]);
+                    for (int k = 0; k < cluster; ++k) store_at(k, &peers[buf][rank][lane], total);
+                    cluster_arrive<true>();
+                } else {
+                    cluster_arrive<false>();
                 }
+                cluster_wait();
+#pragma unroll
+                for (int k = 0; k < kMostCluster; ++k)
+                    if (k < cluster) {
+                        if (k == rank) h = carry;
+                        const Affine e = peers[buf][k][lane];
+                        carry = apply<kCuts>(e.A, e.H, carry);
+                    }
+            } else {
+                h = ends[buf][lane];
             }
-        }
-        if (cluster > 1) cluster_wait();
-        __syncthreads();
-        f2 h = starts[w][lane];
+#pragma unroll
+            for (int k = 0; k < kWarps - 1; ++k)
+                if (k < w) {
+                    const Affine e = maps[buf][k][lane];
+                    h = apply<kCuts>(e.A, e.H, h);
+                }
+            return h;
+        };
+        f2 h = !kPacked || wide ? fold(std::false_type{}) : fold(std::true_type{});
+        static_assert(kGatedBlock % STRIP == 0, "blocks begin at strips");
         if (p.states && s0 % kGatedBlock == 0 && s0 < p.T) {
             const bool begins = s0 == 0 || (kPacked && !clear && tile.start[w * STRIP] >= 0);
             const int64_t block = (int64_t)b * ((p.T + kGatedBlock - 1) / kGatedBlock) + s0 / kGatedBlock;
             store_state(p.states, block * p.C + c, begins ? 0ull : h, n2);
         }
         if constexpr (kRows) {
+            copies_wait<1>();  // z
+            __syncwarp();
+            const T* const zin = mine + 3 * PART + 2 * lane;
             if (VEC > 1 && (!kPacked || clear) && s0 >= first && s0 + STRIP <= last) {
                 // all of the strip's tokens are of one sequence
                 T* at = to;
@@ -223,7 +192,12 @@ __global__ void __launch_bounds__(kThreads, 3) gated_fwd_kernel(GatedParams p, i
 #pragma unroll
                     for (int j = 0; j < STRIP; ++j, at += p.C) {
                         h = fma2(a[j], h, u[j]);
-                        store_pair<T, true>(at, decltype(gated)::value ? mul2(h, gate[j]) : h, n2);
+                        f2 y = h;
+                        if constexpr (decltype(gated)::value) {
+                            const f2 z = pair_at(zin + j * kGatedCh);
+                            y = mul2(h, mul2(z, gate2(z)));
+                        }
+                        store_pair<T, true>(at, y, n2);
                     }
                 };
                 if (p.z) walk(std::true_type{});
@@ -234,14 +208,22 @@ __global__ void __launch_bounds__(kThreads, 3) gated_fwd_kernel(GatedParams p, i
                 for (int j = 0; j < STRIP; ++j) {
                     h = apply<kPacked>(a[j], u[j], h);
                     const int t = s0 + j;
-                    if (t >= first && t < last) store_pair<T, false>(to + (int64_t)j * p.C, p.z ? mul2(h, gate[j]) : h, n2);
+                    if (t >= first && t < last) {
+                        const f2 z = pair_at(zin + j * kGatedCh);
+                        store_pair<T, false>(to + (int64_t)j * p.C, p.z ? mul2(h, mul2(z, gate2(z))) : h, n2);
+                    }
                     if (p.final_state) {
                         const int n = kPacked ? (clear ? -1 : tile.end[w * STRIP + j]) : (t == p.T - 1 ? b : -1);
                         if (n >= 0) store_state(p.final_state, (int64_t)n * p.C + c, h, n2);
                     }
                 }
             }
+            __syncwarp();
+        } else {
+#pragma unroll
+            for (int j = 0; j < STRIP; ++j) h = apply<kPacked>(a[j], u[j], h);
         }
+        if (cluster == 1 && w == kWarps - 1) ends[buf ^ 1][lane] = h;
     }
 }
 
