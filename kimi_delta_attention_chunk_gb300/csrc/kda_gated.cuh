@@ -141,25 +141,28 @@ struct Feed {
         : at(static_cast<const T*>(base) + (first_row + row()) * ld + c0 + col()), step(step * ld), more(ROWS * ld) {}
     static __device__ __forceinline__ int row() { return threadIdx.x % 32 / PR; }
     static __device__ __forceinline__ int col() { return threadIdx.x % 32 % PR * VEC; }
+    // The next strip, all of whose rows and channels are there.
+    __device__ __forceinline__ void request(T* strip) {
+        T* const to = strip + row() * kGatedCh + col();
+        if constexpr (PR <= 32) {
+            const T* from = at;
+#pragma unroll
+            for (int k = 0; k < N; ++k, from += more) Row<T, VEC>::copy_async(to + k * ROWS * kGatedCh, from);
+            at += step;
+        } else {
+            request(strip, R, kGatedCh);
+        }
+    }
     // The next strip, of which `rows` rows are there (none: <= 0) and `has` channels.
     __device__ __forceinline__ void request(T* strip, int rows, int has) {
-        T* const to = strip + row() * kGatedCh + col();
         const T* from = at;
-        if constexpr (PR <= 32) {
-            if (col() < has) {
-                if (rows >= R) {
+        const int lines = rows < R ? rows : R;
+        for (int r = row(); r < lines; r += ROWS, from += more)
 #pragma unroll
-                    for (int k = 0; k < N; ++k, from += more) Row<T, VEC>::copy_async(to + k * ROWS * kGatedCh, from);
-                } else {
-                    for (int r = row(); r < rows; r += ROWS, from += more) Row<T, VEC>::copy_async(strip + r * kGatedCh + col(), from);
-                }
+            for (int h = 0; h < (PR + 31) / 32; ++h) {
+                const int c = col() + h * 32 * VEC;
+                if (c < has) Row<T, VEC>::copy_async(strip + r * kGatedCh + c, from + h * 32 * VEC);
             }
-        } else {
-            for (int r = 0; r < rows && r < R; ++r, from += more) {
-                if (col() < has) Row<T, VEC>::copy_async(to + r * kGatedCh, from);
-                if (col() + 32 * VEC < has) Row<T, VEC>::copy_async(to + r * kGatedCh + 32 * VEC, from + 32 * VEC);
-            }
-        }
         at += step;
     }
 };

@@ -52,7 +52,11 @@ __global__ void __launch_bounds__(kThreads, 2) gated_fwd_kernel(GatedParams p, i
     Feed<T, STRIP, VEC> fx(p.x, p.ldx, row0 + s0, c0, stride), fr(p.r, p.ldr, row0 + s0, c0, stride), fi(p.i, p.ldi, row0 + s0, c0, stride);
     Feed<T, STRIP, VEC> fz(p.z, p.ldz, row0 + s0, c0, stride);
     auto request = [&](int rows) {
-        if (rows > 0) {
+        if (rows >= STRIP && has >= kGatedCh) {
+            fx.request(mine);
+            fr.request(mine + PART);
+            fi.request(mine + 2 * PART);
+        } else if (rows > 0) {
             fx.request(mine, rows, has);
             fr.request(mine + PART, rows, has);
             fi.request(mine + 2 * PART, rows, has);
@@ -87,7 +91,10 @@ __global__ void __launch_bounds__(kThreads, 2) gated_fwd_kernel(GatedParams p, i
     T* to = static_cast<T*>(p.y) + (row0 + s0) * p.C + c;
     for (int it = 0; it < steps; ++it, s0 += stride, to += (int64_t)stride * p.C) {
         const int t0 = s0 - w * STRIP, buf = it & 1;
-        if (kRows && p.z && s0 < p.T) fz.request(mine + 3 * PART, p.T - s0, has);
+        if (kRows && p.z) {
+            if (p.T - s0 >= STRIP && has >= kGatedCh) fz.request(mine + 3 * PART);
+            else fz.request(mine + 3 * PART, p.T - s0, has);
+        }
         copies_commit();
         bool wide = true, plain = true, clear = true;  // no boundary in the cluster's tiles, in the tile, in the strip
         if constexpr (kPacked) {

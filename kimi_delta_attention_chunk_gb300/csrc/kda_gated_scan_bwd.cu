@@ -23,53 +23,64 @@ constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kStrip = 4, kTile = kWarps * kStrip;
 static_assert(kTile == kGatedBlock, "a tile begins at a state that is left to it");
 
-template <typename T>
-constexpr int kStages = sizeof(T) == 2 ? 4 : 2;
+// x, r, i, z and dy of every warp's strip, in two stages.
+constexpr int kStages = 2;
 template <typename T, typename TG>
 constexpr int kStageBytes = kTile * kGatedCh * (4 * (int)sizeof(T) + (int)sizeof(TG));
 
+// VEC, GVEC: elements of a piece of x, r, i and z, and of dy; with VEC > 1, pairs of channels of the outputs are whole and aligned.
 template <typename T, typename TG, int VEC, int GVEC, bool kPacked>
-__global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(GatedParams p, float* partial, int cluster, int blocks, bool whole_pairs) {
-    constexpr int STAGES = kStages<T>;
+__global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(GatedParams p, float* partial, int cluster, int blocks) {
+    constexpr int PART = kStrip * kGatedCh;
     extern __shared__ __align__(128) char shared[];
-    __shared__ Affine ahead[kWarps][32], back[kWarps][32];
+    // The strips' maps, backwards [0, kWarps) and forwards [kAhead, kAhead + kWarps), with maps between them that change nothing: every
+    // warp folds kWarps - 1 maps, those behind its own backwards and those before it forwards.
+    constexpr int kAhead = 2 * kWarps - 1;
+    __shared__ Affine maps[2][kAhead + kWarps][32];
     __shared__ Affine peers[2][kMostCluster][32];
-    __shared__ f2 ends[32];
+    __shared__ f2 ends[2][32];
     __shared__ TokenTile<kPacked ? kTile : 1> tile;
 
     const int lane = threadIdx.x % 32, w = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0);
     const int rank = cluster > 1 ? (int)cluster_rank() : 0;
     const int group = blockIdx.x / cluster, b = group / blocks, c0 = group % blocks * kGatedCh;
-    const int c = c0 + 2 * lane, n2 = min(2, p.C - c);  // channels of this lane: 2, 1 or none (<= 0)
+    const int c = c0 + 2 * lane, has = p.C - c0, n2 = min(2, p.C - c);  // channels of this lane: 2, 1 or none (<= 0)
     const SeqMap m{p.cu, p.N, p.T, p.T};
     const int first = kPacked ? m.first() : 0, last = kPacked ? m.last() : p.T;
-    const int steps = (int)(((int64_t)p.T + kTile * cluster - 1) / (kTile * cluster));
-    const int64_t row0 = (int64_t)b * p.T, block0 = (int64_t)b * ((p.T + kTile - 1) / kTile);
+    const int stride = kTile * cluster;  // tokens between a block's tiles
+    const int steps = (int)(((int64_t)p.T + stride - 1) / stride);
+    const int64_t row0 = (int64_t)b * p.T;
+    int s0 = (steps - 1) * stride + rank * kTile + w * kStrip;  // this strip's first token: tiles are taken from the stream's end
 
-    // step `it` counts from the stream's end
-    auto tile_of = [&](int it) { return ((steps - 1 - it) * cluster + rank) * kTile; };
     // this warp's rows: a stage holds x, r, i, z [4][kStrip][64] and dy [kStrip][64]
-    constexpr int PART = kStrip * kGatedCh;
     char* const mine = shared + w * (kStageBytes<T, TG> / kWarps);
-    const int64_t from_row = row0 + tile_of(0) + w * kStrip;
-    Feed<T, kStrip, VEC> fx(p.x, p.ldx, from_row, c0, -kTile * cluster), fr(p.r, p.ldr, from_row, c0, -kTile * cluster);
-    Feed<T, kStrip, VEC> fi(p.i, p.ldi, from_row, c0, -kTile * cluster), fz(p.z, p.ldz, from_row, c0, -kTile * cluster);
-    Feed<TG, kStrip, GVEC> fy(p.dy, p.C, from_row, c0, -kTile * cluster);
-    const int has = p.C - c0;
+    Feed<T, kStrip, VEC> fx(p.x, p.ldx, row0 + s0, c0, -stride), fr(p.r, p.ldr, row0 + s0, c0, -stride), fi(p.i, p.ldi, row0 + s0, c0, -stride);
+    Feed<T, kStrip, VEC> fz(p.z, p.ldz, row0 + s0, c0, -stride);
+    Feed<TG, kStrip, GVEC> fy(p.dy, p.C, row0 + s0, c0, -stride);
     auto request = [&](int it) {
-        const int rows = it < steps ? p.T - (tile_of(it) + w * kStrip) : 0;
-        T* const in = reinterpret_cast<T*>(mine + it % STAGES * kStageBytes<T, TG>);
+        const int rows = p.T - (s0 - stride);
+        T* const in = reinterpret_cast<T*>(mine + (it & 1) * kStageBytes<T, TG>);
         if (it < steps) {
-            fx.request(in, rows, has);
-            fr.request(in + PART, rows, has);
-            fi.request(in + 2 * PART, rows, has);
-            if (p.z) fz.request(in + 3 * PART, rows, has);
-            fy.request(reinterpret_cast<TG*>(in + 4 * PART), rows, has);
+            TG* const dys = reinterpret_cast<TG*>(in + 4 * PART);
+            if (rows >= kStrip && has >= kGatedCh) {
+                fx.request(in);
+                fr.request(in + PART);
+                fi.request(in + 2 * PART);
+                fy.request(dys);
+                if (p.z) fz.request(in + 3 * PART);
+            } else {
+                fx.request(in, rows, has);
+                fr.request(in + PART, rows, has);
+                fi.request(in + 2 * PART, rows, has);
+                fy.request(dys, rows, has);
+                if (p.z) fz.request(in + 3 * PART, rows, has);
+            }
         }
         copies_commit();
     };
-#pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s) request(s);
+    s0 += stride;
+    request(0);
+    s0 -= stride;
 
     const f2 rate = pack(n2 > 0 ? gated_rate(__ldg(p.lam + c), p.decay) : 0.f, n2 > 1 ? gated_rate(__ldg(p.lam + c + 1), p.decay) : 0.f);
     const bool small = __all_sync(0xffffffffu, small_rate(rate)) != 0;
@@ -87,40 +98,43 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(GatedParams p, f
         }
     }
     f2 carry = kPacked ? 0ull : state_pair(p.dfinal, (int64_t)b * p.C + c, n2), dlam = 0ull;
-    if (w == 0) ends[lane] = carry;
+    if (w == 0) ends[0][lane] = carry;
+    if (w < kWarps - 1) maps[0][kWarps + w][lane] = maps[1][kWarps + w][lane] = identity();
     if (cluster > 1) {
         cluster_arrive<false>();
         cluster_wait();
     }
 
+    // where this warp's first row of an output and the tile's state are; all move up by a stride of rows a step
+    int64_t off = (row0 + s0) * p.C + c;
+    const float* before = p.states + ((int64_t)b * ((p.T + kTile - 1) / kTile) + (s0 - w * kStrip) / kTile) * p.C + c;
     int from = 0x7fffffff;  // behind this token, up to the tile before, no boundary
-    for (int it = 0; it < steps; ++it) {
-        const int t0 = tile_of(it), rows = min(kTile, p.T - t0), s0 = t0 + w * kStrip;
+    for (int it = 0; it < steps; ++it, s0 -= stride, off -= (int64_t)stride * p.C, before -= (int64_t)cluster * p.C) {
+        const int t0 = s0 - w * kStrip, buf = it & 1;
         f2 h = 0ull;
-        if (rows > 0) {
-            if (!kPacked && t0 == 0) {
-                h = state_pair(p.initial, (int64_t)b * p.C + c, n2);
-            } else {
-                const float* s = p.states + (block0 + t0 / kTile) * p.C + c;
-                h = pack(n2 > 0 ? s[0] : 0.f, n2 > 1 ? s[1] : 0.f);
-            }
+        if (t0 < p.T) {
+            if (!kPacked && t0 == 0) h = state_pair(p.initial, (int64_t)b * p.C + c, n2);
+            else if (VEC > 1) h = n2 > 0 ? *reinterpret_cast<const f2*>(before) : 0ull;
+            else h = pack(n2 > 0 ? before[0] : 0.f, n2 > 1 ? before[1] : 0.f);
         }
-        copies_wait<STAGES - 2>();
-        __syncthreads();  // the tile is there, and everyone is past the one before
-        request(it + STAGES - 1);
-        bool plain = true, clear = true;  // no boundary in the tile, in this warp's strip
+        // no boundary in the cluster's tiles, in the tile, in this warp's strip
+        bool wide = true, plain = true, clear = true;
         if constexpr (kPacked) {
-            if (t0 <= from && rows > 0) {
+            wide = t0 - rank * kTile > from;
+            if (t0 <= from && t0 < p.T) {  // (the same in the whole block)
+                __syncthreads();
                 tile.template build<kThreads>(m, t0);
                 from = tile.carry >= 0 ? tile.carry_start : 0x7fffffff;
                 plain = tile.plain;
                 clear = plain || tile.template clear<kStrip>(w * kStrip);
             }
         }
-        const bool inside = s0 >= first && s0 + kStrip <= min(last, t0 + rows);  // all of the strip's tokens are of some sequence
-        const T* const in = reinterpret_cast<const T*>(mine + it % STAGES * kStageBytes<T, TG>) + 2 * lane;
+        copies_wait<0>();
+        __syncwarp();  // the strip's rows are there, and every lane is past the strip before
+        request(it + 1);
+        const T* const in = reinterpret_cast<const T*>(mine + buf * kStageBytes<T, TG>) + 2 * lane;
         const TG* const dys = reinterpret_cast<const TG*>(in - 2 * lane + 4 * PART) + 2 * lane;
-        f2 a[kStrip], u[kStrip], wx[kStrip], wm[kStrip], sr[kStrip], ui[kStrip], yb[kStrip];
+        f2 a[kStrip], u[kStrip], wx[kStrip], wm[kStrip], sr[kStrip], ui[kStrip], yb[kStrip], gz[kStrip];
         auto gates = [&](auto small_rates) {
 #pragma unroll
             for (int j = 0; j < kStrip; ++j) {
@@ -142,17 +156,18 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(GatedParams p, f
         if (p.z) {
 #pragma unroll
             for (int j = 0; j < kStrip; ++j) {
-                const f2 z = pair_at(in + 3 * PART + j * kGatedCh);
-                yb[j] = mul2(yb[j], mul2(z, gate2(z)));
+                const f2 z = pair_at(in + 3 * PART + j * kGatedCh), s = gate2(z), silu = mul2(z, s);
+                gz[j] = mul2(yb[j], fma2(silu, rest2(s), s));  // silu' = s + z s (1 - s)
+                yb[j] = mul2(yb[j], silu);
             }
         }
-        if (rows < kTile) {
+        if (s0 + kStrip > p.T) {
 #pragma unroll
             for (int j = 0; j < kStrip; ++j)
-                if (w * kStrip + j >= rows) a[j] = both(1.f), u[j] = yb[j] = 0ull;
+                if (s0 + j >= p.T) a[j] = both(1.f), u[j] = yb[j] = 0ull;
         }
         // the strip's maps forwards (cut where a sequence begins) and backwards (cut where one ends)
-        Affine fore = identity(), rear = identity();
+        Affine fore, rear;
         if (!kPacked || clear) {
             fore = Affine{a[0], u[0]};
 #pragma unroll
@@ -162,6 +177,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(GatedParams p, f
 #pragma unroll
             for (int j = kStrip - 2; j >= 0; --j) rear.H = mul2(a[j], add2(yb[j], rear.H));
         } else {
+            fore = rear = identity();
 #pragma unroll
             for (int j = 0; j < kStrip; ++j) {
                 const int n = tile.start[w * kStrip + j];
@@ -179,43 +195,45 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(GatedParams p, f
                 }
             }
         }
-        ahead[w][lane] = fore;
-        back[w][lane] = rear;
-        f2 g = cluster > 1 ? carry : ends[lane];
+        maps[buf][w][lane] = rear;
+        maps[buf][kAhead + w][lane] = fore;
         __syncthreads();
-        const int buf = it & 1;
-        if (cluster > 1) {
+        f2 g;
+        auto publish = [&](auto cuts) {
             if (w == kWarps - 1) {
                 Affine total = rear;
-                if (!kPacked || plain) {
 #pragma unroll
-                    for (int k = kWarps - 2; k >= 0; --k) total = follow<false>(total, back[k][lane]);
-                } else {
-#pragma unroll
-                    for (int k = kWarps - 2; k >= 0; --k) total = follow<true>(total, back[k][lane]);
-                }
+                for (int k = kWarps - 2; k >= 0; --k) total = follow<decltype(cuts)::value>(total, maps[buf][k][lane]);
                 for (int k = 0; k < cluster; ++k) store_at(k, &peers[buf][rank][lane], total);
                 cluster_arrive<true>();
             } else {
                 cluster_arrive<false>();
             }
-        }
-        // the state before each token, and with it what dh is multiplied by: e = si x a^2 / m - a h_{t-1}; dz is done
-        if (!kPacked || plain) {
-#pragma unroll
-            for (int k = 0; k < kWarps - 1; ++k)
-                if (k < w) {
-                    const Affine e = ahead[k][lane];
-                    h = fma2(e.A, h, e.H);
-                }
-        } else {
-            for (int k = 0; k < w; ++k) {
-                const Affine e = ahead[k][lane];
-                h = apply<true>(e.A, e.H, h);
+        };
+        auto fold = [&](auto cuts) {
+            constexpr bool kCuts = decltype(cuts)::value;
+            if (cluster > 1) {
+                cluster_wait();
+                for (int k = cluster - 1; k > rank; --k) carry = apply<kCuts>(peers[buf][k][lane].A, peers[buf][k][lane].H, carry);
+                g = carry;
+                for (int k = rank; k >= 0; --k) carry = apply<kCuts>(peers[buf][k][lane].A, peers[buf][k][lane].H, carry);
+            } else {
+                g = ends[buf][lane];
             }
+#pragma unroll
+            for (int k = kWarps - 1; k > 0; --k) g = apply<kCuts>(maps[buf][w + k][lane].A, maps[buf][w + k][lane].H, g);
+        };
+        if (!kPacked || wide) {
+            if (cluster > 1) publish(std::false_type{});
+#pragma unroll
+            for (int k = 0; k < kWarps - 1; ++k) h = fma2(maps[buf][kWarps + w + k][lane].A, h, maps[buf][kWarps + w + k][lane].H);
+        } else {
+            if (cluster > 1) publish(std::true_type{});
+#pragma unroll
+            for (int k = 0; k < kWarps - 1; ++k) h = apply<true>(maps[buf][kWarps + w + k][lane].A, maps[buf][kWarps + w + k][lane].H, h);
         }
-        const bool lean = (!kPacked || clear) && inside && whole_pairs;
-        const int64_t row = (row0 + s0) * p.C + c;
+        const bool lean = VEC > 1 && (!kPacked || clear) && s0 >= first && s0 + kStrip <= last;  // the strip's tokens are of one sequence
+        // the state before each token, and with it what dh is multiplied by: wm = si x a^2 / m - a h_{t-1}; dz is done
 #pragma unroll
         for (int j = 0; j < kStrip; ++j) {
             if (kPacked && !clear) {
@@ -224,88 +242,61 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(GatedParams p, f
             }
             const f2 ah = mul2(a[j], h);
             wm[j] = fma2(ah, both(-1.f), wm[j]);
-            u[j] = add2(ah, u[j]);  // h
-            h = u[j];
+            h = add2(ah, u[j]);
+            if (p.z) gz[j] = mul2(gz[j], h);
         }
-        if (p.z) {
-            TG* to = static_cast<TG*>(p.dz) + row;
+        if (p.z && lean) {
+            TG* to = static_cast<TG*>(p.dz) + off;
 #pragma unroll
-            for (int j = 0; j < kStrip; ++j, to += p.C) {
-                const f2 z = pair_at(in + 3 * PART + j * kGatedCh), s = gate2(z);
-                // silu' = s + z s (1 - s)
-                const f2 dz = mul2(mul2(pair_at(dys + j * kGatedCh), u[j]), fma2(mul2(z, s), rest2(s), s));
-                if (lean) {
-                    store_pair<TG, true>(to, dz, n2);
-                } else if (w * kStrip + j < rows) {
-                    store_pair<TG, false>(to, s0 + j >= first && s0 + j < last ? dz : 0ull, n2);
-                }
-            }
+            for (int j = 0; j < kStrip; ++j, to += p.C) store_pair<TG, true>(to, gz[j], n2);
         }
-        if (cluster > 1) {
-            cluster_wait();
-#pragma unroll 4
-            for (int k = cluster - 1; k >= 0; --k) {
-                if (k == rank) g = carry;
-                const Affine e = peers[buf][k][lane];
-                carry = apply<kPacked>(e.A, e.H, carry);
-            }
-        }
-        if (!kPacked || plain) {
-#pragma unroll
-            for (int k = kWarps - 1; k > 0; --k)
-                if (k > w) {
-                    const Affine e = back[k][lane];
-                    g = fma2(e.A, g, e.H);
-                }
-        } else {
-            for (int k = kWarps - 1; k > w; --k) {
-                const Affine e = back[k][lane];
-                g = apply<true>(e.A, e.H, g);
-            }
-        }
+        if (!kPacked || wide) fold(std::false_type{});
+        else fold(std::true_type{});
         if (lean) {
-            int64_t off = row + (int64_t)(kStrip - 1) * p.C;
+            const int64_t up = (int64_t)(kStrip - 1) * p.C;
+            TG *dx = static_cast<TG*>(p.dx) + off + up, *dr = static_cast<TG*>(p.dr) + off + up, *di = static_cast<TG*>(p.di) + off + up;
 #pragma unroll
-            for (int j = kStrip - 1; j >= 0; --j, off -= p.C) {
+            for (int j = kStrip - 1; j >= 0; --j, dx -= p.C, dr -= p.C, di -= p.C) {
                 const f2 dh = add2(yb[j], g), part = mul2(mul2(dh, wm[j]), sr[j]);
                 g = mul2(a[j], dh);
                 dlam = add2(dlam, part);
-                store_pair<TG, true>(static_cast<TG*>(p.dx) + off, mul2(dh, wx[j]), n2);
-                store_pair<TG, true>(static_cast<TG*>(p.dr) + off, mul2(mul2(part, rate), rest2(sr[j])), n2);
-                store_pair<TG, true>(static_cast<TG*>(p.di) + off, mul2(dh, ui[j]), n2);
+                store_pair<TG, true>(dx, mul2(dh, wx[j]), n2);
+                store_pair<TG, true>(dr, mul2(mul2(part, rate), rest2(sr[j])), n2);
+                store_pair<TG, true>(di, mul2(dh, ui[j]), n2);
             }
             if (!kPacked && s0 == 0 && p.dinitial) store_state(p.dinitial, (int64_t)b * p.C + c, g, n2);
         } else {
 #pragma unroll
             for (int j = kStrip - 1; j >= 0; --j) {
                 const int t = s0 + j;
-                if (w * kStrip + j >= rows) continue;
+                if (t >= p.T) continue;
                 if (kPacked && !clear && tile.end[w * kStrip + j] >= 0) g = 0ull;
                 const f2 dh = add2(yb[j], g);
                 f2 part = mul2(mul2(dh, wm[j]), sr[j]), dx = mul2(dh, wx[j]), dr = mul2(mul2(part, rate), rest2(sr[j])), di = mul2(dh, ui[j]);
                 g = mul2(a[j], dh);
                 if (t >= first && t < last) dlam = add2(dlam, part);
-                else dx = di = dr = 0ull;
-                const int64_t off = row + (int64_t)j * p.C;
-                store_pair<TG, false>(static_cast<TG*>(p.dx) + off, dx, n2);
-                store_pair<TG, false>(static_cast<TG*>(p.dr) + off, dr, n2);
-                store_pair<TG, false>(static_cast<TG*>(p.di) + off, di, n2);
+                else dx = di = dr = gz[j] = 0ull;
+                const int64_t o = off + (int64_t)j * p.C;
+                store_pair<TG, false>(static_cast<TG*>(p.dx) + o, dx, n2);
+                store_pair<TG, false>(static_cast<TG*>(p.dr) + o, dr, n2);
+                store_pair<TG, false>(static_cast<TG*>(p.di) + o, di, n2);
+                if (p.z) store_pair<TG, false>(static_cast<TG*>(p.dz) + o, gz[j], n2);
                 if (p.dinitial) {
                     const int n = kPacked ? (clear ? -1 : tile.start[w * kStrip + j]) : (t == 0 ? b : -1);
                     if (n >= 0) store_state(p.dinitial, (int64_t)n * p.C + c, g, n2);
                 }
             }
         }
-        if (cluster == 1 && w == 0) ends[lane] = g;
+        if (cluster == 1 && w == 0) ends[buf ^ 1][lane] = g;
     }
     tc::grid_dep_launch();
     __syncthreads();
-    ahead[w][lane].A = dlam;
+    maps[0][w][lane].A = dlam;
     __syncthreads();
     if (w == 0 && steps > 0) {
         f2 sum = 0ull;
 #pragma unroll
-        for (int k = 0; k < kWarps; ++k) sum = add2(sum, ahead[k][lane].A);
+        for (int k = 0; k < kWarps; ++k) sum = add2(sum, maps[0][k][lane].A);
         store_state(partial + ((int64_t)b * cluster + rank) * p.C, c, sum, n2);
     }
 }
@@ -327,27 +318,27 @@ size_t partial_bytes(const GatedParams& p) {
 }
 
 template <typename T, typename TG, int VEC, int GVEC, bool kPacked>
-cudaError_t launch(const GatedParams& p, bool whole_pairs, cudaStream_t st) {
+cudaError_t launch(const GatedParams& p, cudaStream_t st) {
     const int blocks = (p.C + kGatedCh - 1) / kGatedCh;
     const int64_t groups = (int64_t)blocks * p.B;
     float* const partial = static_cast<float*>(p.ws);
     int parts = 0;
     if (groups > 0) {
         const auto kern = gated_bwd_kernel<T, TG, VEC, GVEC, kPacked>;
-        constexpr int smem = kStages<T> * kStageBytes<T, TG>;
+        constexpr int smem = kStages * kStageBytes<T, TG>;
         static ClusterRoom room;
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         const int cluster = room.size_for(kern, groups, p.T, kTile, kThreads, smem);
-        e = launch_clusters(kern, groups * cluster, cluster, kThreads, smem, st, p, partial, cluster, blocks, whole_pairs);
+        e = launch_clusters(kern, groups * cluster, cluster, kThreads, smem, st, p, partial, cluster, blocks);
         if (e != cudaSuccess) return e;
         parts = p.T > 0 ? p.B * cluster : 0;
     }
     return tc::launch_dependent(gated_dlam_kernel, (unsigned)((p.C + 127) / 128), 128, 0, st, partial, parts, p.lam, p.decay, p.C, p.dlam);
 }
 template <typename T, typename TG, int VEC, int GVEC>
-cudaError_t launch_packed(const GatedParams& p, bool whole_pairs, cudaStream_t st) {
-    return p.cu ? launch<T, TG, VEC, GVEC, true>(p, whole_pairs, st) : launch<T, TG, VEC, GVEC, false>(p, whole_pairs, st);
+cudaError_t launch_packed(const GatedParams& p, cudaStream_t st) {
+    return p.cu ? launch<T, TG, VEC, GVEC, true>(p, st) : launch<T, TG, VEC, GVEC, false>(p, st);
 }
 
 }  // namespace
@@ -368,17 +359,20 @@ cudaError_t gated_scan_bwd(kda_dtype dt, kda_dtype gdt, const GatedParams& given
         if (e != cudaSuccess) return e;
     }
     const int es = dt == KDA_BF16 ? 2 : 4, gs = gdt == KDA_BF16 ? 2 : 4;
-    bool whole_pairs = p.C % 2 == 0, wide = gated_pieces(p, es, 16) && (int64_t)p.C * gs % 16 == 0 && kda_host::aligned16(p.dy);
-    for (const void* q : {(const void*)p.dx, (const void*)p.dr, (const void*)p.di, (const void*)p.dz}) whole_pairs = whole_pairs && (uintptr_t)q % (2 * gs) == 0;
-    const bool narrow = gated_pieces(p, es, 4) && (int64_t)p.C * gs % 4 == 0 && (uintptr_t)p.dy % 4 == 0;
-    if (dt == KDA_F32)
-        return wide ? launch_packed<float, float, 4, 4>(p, whole_pairs, st) : launch_packed<float, float, 1, 1>(p, whole_pairs, st);
-    if (gdt == KDA_F32) {
-        if (wide) return launch_packed<__nv_bfloat16, float, 8, 4>(p, whole_pairs, st);
-        return narrow ? launch_packed<__nv_bfloat16, float, 2, 1>(p, whole_pairs, st) : launch_packed<__nv_bfloat16, float, 1, 1>(p, whole_pairs, st);
+    bool pairs = p.C % 2 == 0 && (uintptr_t)p.states % 8 == 0;
+    for (const void* q : {(const void*)p.dx, (const void*)p.dr, (const void*)p.di, (const void*)p.dz}) pairs = pairs && (uintptr_t)q % (2 * gs) == 0;
+    const bool wide = pairs && gated_pieces(p, es, 16) && (int64_t)p.C * gs % 16 == 0 && kda_host::aligned16(p.dy);
+    const bool narrow = pairs && gated_pieces(p, es, 2 * es) && (uintptr_t)p.dy % (2 * gs) == 0;
+    if (dt == KDA_F32) {
+        if (wide) return launch_packed<float, float, 4, 4>(p, st);
+        return narrow ? launch_packed<float, float, 2, 2>(p, st) : launch_packed<float, float, 1, 1>(p, st);
     }
-    if (wide) return launch_packed<__nv_bfloat16, __nv_bfloat16, 8, 8>(p, whole_pairs, st);
-    return narrow ? launch_packed<__nv_bfloat16, __nv_bfloat16, 2, 2>(p, whole_pairs, st) : launch_packed<__nv_bfloat16, __nv_bfloat16, 1, 1>(p, whole_pairs, st);
+    if (gdt == KDA_F32) {
+        if (wide) return launch_packed<__nv_bfloat16, float, 8, 4>(p, st);
+        return narrow ? launch_packed<__nv_bfloat16, float, 2, 2>(p, st) : launch_packed<__nv_bfloat16, float, 1, 1>(p, st);
+    }
+    if (wide) return launch_packed<__nv_bfloat16, __nv_bfloat16, 8, 8>(p, st);
+    return narrow ? launch_packed<__nv_bfloat16, __nv_bfloat16, 2, 2>(p, st) : launch_packed<__nv_bfloat16, __nv_bfloat16, 1, 1>(p, st);
 }
 
 }  // namespace kda
