@@ -103,6 +103,75 @@ __device__ __forceinline__ Affine follow(const Affine& first, const Affine& then
 }
 __device__ __forceinline__ Affine identity() { return Affine{both(1.f), 0ull}; }
 
+// ---- packed sequences as a warp walks them, strip by strip ------------------------------------------------
+
+// N sequences in a stream of T tokens by their offsets, in shared memory where there are few.
+constexpr int kCachedOffsets = 256;
+struct Offsets {
+    const int32_t* cu;  // (global or shared)
+    int N, T;
+    // Every thread of the block calls it.
+    __device__ __forceinline__ Offsets(const int32_t* cu, int N, int T, int32_t* cache) : cu(cu), N(N), T(T) {
+        if (!cu || N >= kCachedOffsets) return;
+        for (int k = threadIdx.x; k <= N; k += blockDim.x) cache[k] = __ldg(cu + k);
+        __syncthreads();
+        this->cu = cache;
+    }
+    __device__ __forceinline__ int begin(int n) const { return min(max(cu[n], 0), T); }
+    __device__ __forceinline__ int end(int n) const { return begin(n + 1); }
+    // Tokens outside [first, last) belong to no sequence.
+    __device__ __forceinline__ int first() const { return N > 0 ? begin(0) : 0; }
+    __device__ __forceinline__ int last() const { return N > 0 ? begin(N) : 0; }
+    // How many sequences begin before token `key` (a whole warp calls it with one key), by 32 probes a round.  On offsets that are not
+    // sorted it still ends and stays within [0, N].
+    __device__ __forceinline__ int begun_before(int key) const {
+        const int lane = threadIdx.x & 31;
+        int lo = 0, hi = N;
+        while (hi > lo) {
+            const int step = (hi - lo + 31) / 32, at = lo + (lane + 1) * step - 1;
+            const int cnt = __popc(__ballot_sync(0xffffffffu, at < hi && begin(at) < key));
+            const int next = min(hi, lo + (cnt + 1) * step - 1);
+            lo = min(hi, lo + cnt * step);
+            hi = max(lo, next);
+            if (step == 1) break;
+        }
+        return lo;
+    }
+};
+
+// What a warp knows of the sequences at its strip.
+template <int STRIP>
+struct Marks {
+    int start[STRIP], end[STRIP];  // the sequence that a token is the first / last of, or -1
+};
+template <int STRIP>
+struct Walk {
+    int sb = 0, se = 0;        // the sequence at hand: its first token, one behind its last
+    bool wide = true, clear = true;  // no boundary in the cluster's tiles, in the strip; else the marks are set
+    // The strip at s0, the cluster's tiles at [w0, w1).
+    __device__ __forceinline__ void look(const Offsets& m, int s0, int w0, int w1, Marks<STRIP>& marks) {
+        wide = clear = sb < w0 && w1 < se;
+        if (s0 >= m.T) clear = true;
+        if (wide || s0 >= m.T) return;
+        const int n = m.begun_before(s0 + 1) - 1;
+        sb = n >= 0 ? m.begin(n) : 0;
+        se = n >= 0 ? m.end(n) : 0;
+        clear = sb < s0 && s0 + STRIP < se;
+        if (clear) return;
+        const int lane = threadIdx.x & 31, behind = m.begun_before(s0 + STRIP);
+        __syncwarp();
+        for (int j = lane; j < STRIP; j += 32) marks.start[j] = marks.end[j] = -1;
+        __syncwarp();
+        for (int k = max(m.begun_before(s0) - 1, 0) + lane; k < behind; k += 32) {
+            const int s = m.begin(k), e = m.end(k);
+            if (e <= s) continue;
+            if (s >= s0 && s < s0 + STRIP) marks.start[s - s0] = k;
+            if (e > s0 && e <= s0 + STRIP) marks.end[e - 1 - s0] = k;
+        }
+        __syncwarp();
+    }
+};
+
 // ---- clusters: the blocks of one channel block work on consecutive tiles at a time ------------------------
 
 __device__ __forceinline__ unsigned cluster_rank() {

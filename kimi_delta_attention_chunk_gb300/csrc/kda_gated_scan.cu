@@ -34,13 +34,14 @@ __global__ void __launch_bounds__(kThreads, 2) gated_fwd_kernel(GatedParams p, i
     __shared__ Affine maps[2][kWarps][32];
     __shared__ Affine peers[2][kMostCluster][32];
     __shared__ f2 ends[2][32];
-    __shared__ TokenTile<kPacked ? TT : 1> tile;
+    __shared__ Marks<kPacked ? STRIP : 1> all_marks[kWarps];
+    __shared__ int32_t offsets[kPacked ? kCachedOffsets : 1];
 
     const int lane = threadIdx.x % 32, w = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0);
     const int rank = cluster > 1 ? (int)cluster_rank() : 0;
     const int group = blockIdx.x / cluster, b = group / blocks, c0 = group % blocks * kGatedCh;
     const int c = c0 + 2 * lane, has = p.C - c0, n2 = min(2, p.C - c);  // channels of this lane: 2, 1 or none (<= 0)
-    const SeqMap m{p.cu, p.N, p.T, p.T};
+    const Offsets m(p.cu, p.N, p.T, offsets);
     const int first = kPacked ? m.first() : 0, last = kPacked ? m.last() : p.T;
     const int stride = TT * cluster;  // tokens between a block's tiles
     const int steps = (int)(((int64_t)p.T + stride - 1) / stride);
@@ -87,27 +88,18 @@ __global__ void __launch_bounds__(kThreads, 2) gated_fwd_kernel(GatedParams p, i
         cluster_wait();
     }
 
-    int until = 0;  // no boundary before this token
+    Walk<kPacked ? STRIP : 1> walk;
+    const Marks<kPacked ? STRIP : 1>& marks = all_marks[w];
     T* to = static_cast<T*>(p.y) + (row0 + s0) * p.C + c;
     for (int it = 0; it < steps; ++it, s0 += stride, to += (int64_t)stride * p.C) {
-        const int t0 = s0 - w * STRIP, buf = it & 1;
+        const int buf = it & 1;
         if (kRows && p.z) {
             if (p.T - s0 >= STRIP && has >= kGatedCh) fz.request(mine + 3 * PART);
             else fz.request(mine + 3 * PART, p.T - s0, has);
         }
         copies_commit();
-        bool wide = true, plain = true, clear = true;  // no boundary in the cluster's tiles, in the tile, in the strip
-        if constexpr (kPacked) {
-            // (the sequence at hand covers all of them if it already did at this block's tile before)
-            wide = (int64_t)(it + 1) * stride < until;
-            if (t0 < p.T && t0 + TT >= until) {  // (the same in the whole block)
-                __syncthreads();
-                tile.template build<kThreads>(m, t0);
-                until = tile.until;
-                plain = tile.plain;
-                clear = plain || tile.template clear<STRIP>(w * STRIP);
-            }
-        }
+        if constexpr (kPacked) walk.look(m, s0, it * stride, (it + 1) * stride, all_marks[w]);
+        const bool wide = walk.wide, clear = walk.clear;
         // the first walk: decays and inputs, and the strip's map
         copies_wait<1>();
         __syncwarp();
@@ -138,7 +130,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_fwd_kernel(GatedParams p, i
         } else {
 #pragma unroll
             for (int j = 0; j < STRIP; ++j) {
-                const int n = tile.start[w * STRIP + j];
+                const int n = marks.start[j];
                 if (n >= 0) {
                     if (p.initial) u[j] = fma2(a[j], state_pair(p.initial, (int64_t)n * p.C + c, n2), u[j]);
                     a[j] = both(-1.f);
@@ -184,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_fwd_kernel(GatedParams p, i
         f2 h = !kPacked || wide ? fold(std::false_type{}) : fold(std::true_type{});
         static_assert(kGatedBlock % STRIP == 0, "blocks begin at strips");
         if (p.states && s0 % kGatedBlock == 0 && s0 < p.T) {
-            const bool begins = s0 == 0 || (kPacked && !clear && tile.start[w * STRIP] >= 0);
+            const bool begins = s0 == 0 || (kPacked && !clear && marks.start[0] >= 0);
             const int64_t block = (int64_t)b * ((p.T + kGatedBlock - 1) / kGatedBlock) + s0 / kGatedBlock;
             store_state(p.states, block * p.C + c, begins ? 0ull : h, n2);
         }
@@ -195,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_fwd_kernel(GatedParams p, i
             if (VEC > 1 && (!kPacked || clear) && s0 >= first && s0 + STRIP <= last) {
                 // all of the strip's tokens are of one sequence
                 T* at = to;
-                auto walk = [&](auto gated) {
+                auto second_walk = [&](auto gated) {
 #pragma unroll
                     for (int j = 0; j < STRIP; ++j, at += p.C) {
                         h = fma2(a[j], h, u[j]);
@@ -207,8 +199,8 @@ __global__ void __launch_bounds__(kThreads, 2) gated_fwd_kernel(GatedParams p, i
                         store_pair<T, true>(at, y, n2);
                     }
                 };
-                if (p.z) walk(std::true_type{});
-                else walk(std::false_type{});
+                if (p.z) second_walk(std::true_type{});
+                else second_walk(std::false_type{});
                 if (!kPacked && p.final_state && s0 + STRIP == p.T) store_state(p.final_state, (int64_t)b * p.C + c, h, n2);
             } else {
 #pragma unroll
@@ -220,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_fwd_kernel(GatedParams p, i
                         store_pair<T, false>(to + (int64_t)j * p.C, p.z ? mul2(h, mul2(z, gate2(z))) : h, n2);
                     }
                     if (p.final_state) {
-                        const int n = kPacked ? (clear ? -1 : tile.end[w * STRIP + j]) : (t == p.T - 1 ? b : -1);
+                        const int n = kPacked ? (clear ? -1 : marks.end[j]) : (t == p.T - 1 ? b : -1);
                         if (n >= 0) store_state(p.final_state, (int64_t)n * p.C + c, h, n2);
                     }
                 }

@@ -39,13 +39,14 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(GatedParams p, f
     __shared__ Affine maps[2][kAhead + kWarps][32];
     __shared__ Affine peers[2][kMostCluster][32];
     __shared__ f2 ends[2][32];
-    __shared__ TokenTile<kPacked ? kTile : 1> tile;
+    __shared__ Marks<kPacked ? kStrip : 1> all_marks[kWarps];
+    __shared__ int32_t offsets[kPacked ? kCachedOffsets : 1];
 
     const int lane = threadIdx.x % 32, w = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0);
     const int rank = cluster > 1 ? (int)cluster_rank() : 0;
     const int group = blockIdx.x / cluster, b = group / blocks, c0 = group % blocks * kGatedCh;
     const int c = c0 + 2 * lane, has = p.C - c0, n2 = min(2, p.C - c);  // channels of this lane: 2, 1 or none (<= 0)
-    const SeqMap m{p.cu, p.N, p.T, p.T};
+    const Offsets m(p.cu, p.N, p.T, offsets);
     const int first = kPacked ? m.first() : 0, last = kPacked ? m.last() : p.T;
     const int stride = kTile * cluster;  // tokens between a block's tiles
     const int steps = (int)(((int64_t)p.T + stride - 1) / stride);
@@ -108,7 +109,8 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(GatedParams p, f
     // where this warp's first row of an output and the tile's state are; all move up by a stride of rows a step
     int64_t off = (row0 + s0) * p.C + c;
     const float* before = p.states + ((int64_t)b * ((p.T + kTile - 1) / kTile) + (s0 - w * kStrip) / kTile) * p.C + c;
-    int from = 0x7fffffff;  // behind this token, up to the tile before, no boundary
+    Walk<kPacked ? kStrip : 1> walk;
+    const Marks<kPacked ? kStrip : 1>& marks = all_marks[w];
     for (int it = 0; it < steps; ++it, s0 -= stride, off -= (int64_t)stride * p.C, before -= (int64_t)cluster * p.C) {
         const int t0 = s0 - w * kStrip, buf = it & 1;
         f2 h = 0ull;
@@ -117,18 +119,8 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(GatedParams p, f
             else if (VEC > 1) h = n2 > 0 ? *reinterpret_cast<const f2*>(before) : 0ull;
             else h = pack(n2 > 0 ? before[0] : 0.f, n2 > 1 ? before[1] : 0.f);
         }
-        // no boundary in the cluster's tiles, in the tile, in this warp's strip
-        bool wide = true, plain = true, clear = true;
-        if constexpr (kPacked) {
-            wide = t0 - rank * kTile > from;
-            if (t0 <= from && t0 < p.T) {  // (the same in the whole block)
-                __syncthreads();
-                tile.template build<kThreads>(m, t0);
-                from = tile.carry >= 0 ? tile.carry_start : 0x7fffffff;
-                plain = tile.plain;
-                clear = plain || tile.template clear<kStrip>(w * kStrip);
-            }
-        }
+        if constexpr (kPacked) walk.look(m, s0, t0 - rank * kTile, t0 - rank * kTile + stride, all_marks[w]);
+        const bool wide = walk.wide, clear = walk.clear;
         copies_wait<0>();
         __syncwarp();  // the strip's rows are there, and every lane is past the strip before
         request(it + 1);
@@ -180,13 +172,13 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(GatedParams p, f
             fore = rear = identity();
 #pragma unroll
             for (int j = 0; j < kStrip; ++j) {
-                const int n = tile.start[w * kStrip + j];
+                const int n = marks.start[j];
                 if (n >= 0) fore = Affine{both(-1.f), fma2(a[j], state_pair(p.initial, (int64_t)n * p.C + c, n2), u[j])};
                 else fore = follow<true>(fore, Affine{a[j], u[j]});
             }
 #pragma unroll
             for (int j = kStrip - 1; j >= 0; --j) {
-                const int n = tile.end[w * kStrip + j];
+                const int n = marks.end[j];
                 if (n >= 0) {
                     yb[j] = add2(yb[j], state_pair(p.dfinal, (int64_t)n * p.C + c, n2));
                     rear = Affine{both(-1.f), mul2(a[j], yb[j])};
@@ -237,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(GatedParams p, f
 #pragma unroll
         for (int j = 0; j < kStrip; ++j) {
             if (kPacked && !clear) {
-                const int n = tile.start[w * kStrip + j];
+                const int n = marks.start[j];
                 if (n >= 0) h = state_pair(p.initial, (int64_t)n * p.C + c, n2);
             }
             const f2 ah = mul2(a[j], h);
@@ -270,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(GatedParams p, f
             for (int j = kStrip - 1; j >= 0; --j) {
                 const int t = s0 + j;
                 if (t >= p.T) continue;
-                if (kPacked && !clear && tile.end[w * kStrip + j] >= 0) g = 0ull;
+                if (kPacked && !clear && marks.end[j] >= 0) g = 0ull;
                 const f2 dh = add2(yb[j], g);
                 f2 part = mul2(mul2(dh, wm[j]), sr[j]), dx = mul2(dh, wx[j]), dr = mul2(mul2(part, rate), rest2(sr[j])), di = mul2(dh, ui[j]);
                 g = mul2(a[j], dh);
@@ -282,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(GatedParams p, f
                 store_pair<TG, false>(static_cast<TG*>(p.di) + o, di, n2);
                 if (p.z) store_pair<TG, false>(static_cast<TG*>(p.dz) + o, gz[j], n2);
                 if (p.dinitial) {
-                    const int n = kPacked ? (clear ? -1 : tile.start[w * kStrip + j]) : (t == 0 ? b : -1);
+                    const int n = kPacked ? (clear ? -1 : marks.start[j]) : (t == 0 ? b : -1);
                     if (n >= 0) store_state(p.dinitial, (int64_t)n * p.C + c, g, n2);
                 }
             }

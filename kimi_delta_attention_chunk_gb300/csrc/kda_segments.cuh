@@ -54,11 +54,11 @@ struct SeqMap {
 // and on.  marks: the tokens (bits) that are the first or last of a sequence.
 template <int TT>
 struct TokenTile {
-    static constexpr int kWords = TT > 64 ? (TT + 31) / 32 : 2;
     int start[TT], end[TT];
-    unsigned marks[kWords];
+    unsigned marks[2];
     int carry, carry_start, n0, until;
     bool plain;
+    static_assert(TT <= 64, "one bit a token");
 
     // Every thread of the block calls it; the block has to be past its last use of the tile.
     template <int NTH>
@@ -94,8 +94,7 @@ struct TokenTile {
             if (e - t0 <= TT) end[e - 1 - t0] = n;
         }
         __syncthreads();
-        static_assert(NTH >= 32 * kWords, "one bit a token, a thread each");
-        if (tid < 32 * kWords) {
+        if (tid < 64) {
             const bool mark = tid < TT && (start[tid < TT ? tid : 0] >= 0 || end[tid < TT ? tid : 0] >= 0);
             const unsigned b = __ballot_sync(0xffffffffu, mark);
             if (tid % 32 == 0) marks[tid / 32] = b;
@@ -103,7 +102,7 @@ struct TokenTile {
         __syncthreads();
     }
 
-    // Whether tokens k ... k + N - 1 of the tile (within 32 that begin at a multiple) lie inside one sequence.
+    // Whether tokens k ... k + N - 1 of the tile (within a half of it) lie inside one sequence.
     template <int N>
     __device__ __forceinline__ bool clear(int k) const {
         return (marks[k >> 5] >> (k & 31) & ((1u << N) - 1)) == 0;
