@@ -4,6 +4,8 @@
 // of channels (16 lanes of 16 bytes for 128 bf16 channels), teams lie side by side along a row, and a block walks down the rows with its
 // weights, and backwards its share of dw and db, in registers.  Mean, then the sum of squares around it: two sums over a team, by
 // shuffles up to 32 lanes and through shared memory beyond.  Groups of up to 16384 channels fit a block.
+#include <type_traits>
+
 #include "kda_group_norm.cuh"
 
 namespace kda {
@@ -61,14 +63,58 @@ struct Place {
     __device__ __forceinline__ int channel(int k) const { return g * cg + (lane + k * lanes) * VEC; }
 };
 
-template <typename T, int VEC, int R, int U, int NTH>
-__global__ void __launch_bounds__(NTH, NTH == 256 ? 3 : 1) norm_token_fwd_kernel(NormParams p, Teams t) {
+// A thread's own pieces of the next rows, on their way through shared memory: what a thread asks for it alone reads, so that no thread
+// waits for another.  Two-byte pieces have no asynchronous copy: they are loaded when asked for.  Blocks of 1024 threads (groups of
+// more than some thousand channels) load a row when its turn comes: their shared memory would not hold more, or has the sums.
+template <int NTH>
+constexpr int kAhead = NTH == 256 ? 4 : 1;  // rows under way, the one at hand among them
+template <typename T, int VEC, int R, int NTH>
+struct Ring {
+    static constexpr int kRows = kAhead<NTH>;
+    static constexpr int kBytes = kRows > 1 ? kRows * R * NTH * VEC * (int)sizeof(T) : 0;
+    T* mine;
+    Row<T, VEC> now[kRows > 1 ? 1 : R];
+    __device__ __forceinline__ explicit Ring(void* shared) : mine(static_cast<T*>(shared) + threadIdx.x * VEC) {}
+    __device__ __forceinline__ T* at(int row, int k) const { return mine + ((row % kRows) * R + k) * NTH * VEC; }
+    __device__ __forceinline__ void request(int row, int k, const T* from) {
+        if constexpr (kRows > 1) Row<T, VEC>::copy_async(at(row, k), from);
+        else now[k].load(from);
+    }
+    __device__ __forceinline__ void take(int row, int k, f2 (&v)[(VEC + 1) / 2]) const {
+        if constexpr (kRows > 1) {
+            Row<T, VEC> r;
+            r.from_shared(at(row, k));
+            r.to(v);
+        } else {
+            now[k].to(v);
+        }
+    }
+};
+template <int NTH, int E>
+constexpr int kResidentBwd = NTH != 256 ? 1 : E > 8 ? 2 : 3;
+
+template <typename T, int VEC, int R, int NTH>
+__global__ void __launch_bounds__(NTH, NTH == 256 ? 4 : 1) norm_token_fwd_kernel(NormParams p, Teams t) {
     constexpr int N2 = (VEC + 1) / 2;
     constexpr bool kKeep = R * VEC <= 16;
-    __shared__ float buf[2][NTH / 32][U];
-    TeamSum<U, NTH> sum{buf, t.lanes, 0};
+    __shared__ float buf[2][NTH / 32][1];
+    extern __shared__ __align__(16) char shared[];
+    TeamSum<1, NTH> sum{buf, t.lanes, 0};
+    Ring<T, VEC, R, NTH> ring(shared);
     const Place<VEC, R> at(p, t);
     const float inv_n = 1.f / (float)(p.C / p.G);
+    const int64_t step = (int64_t)gridDim.y * t.rows;
+    const int64_t first = (int64_t)blockIdx.y * t.rows + at.rsub;
+    auto request = [&](int i) {
+        const int64_t row = first + i * step;
+        if (row < p.total)
+#pragma unroll
+            for (int k = 0; k < R; ++k)
+                if (at.has(k)) ring.request(i, k, static_cast<const T*>(p.x) + row * p.ldx + at.channel(k));
+        copies_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead<NTH> - 1; ++i) request(i);
     f2 w[kKeep ? R : 1][N2], bias[kKeep ? R : 1][N2];
     if constexpr (kKeep) {
 #pragma unroll
@@ -77,84 +123,109 @@ __global__ void __launch_bounds__(NTH, NTH == 256 ? 3 : 1) norm_token_fwd_kernel
             vec_pairs<VEC>(p.bias && at.has(k) ? p.bias + at.channel(k) : nullptr, 0.f, bias[k]);
         }
     }
-    const int64_t step = (int64_t)t.rows * U;
-    for (int64_t base = blockIdx.y * step; base < p.total; base += gridDim.y * step) {
-        Row<T, VEC> raw[U][R];
+    // (teams of more than a warp meet, so every thread of a block takes as many turns)
+    const int turns = (int)((p.total - (int64_t)blockIdx.y * t.rows + step - 1) / step);
+    T* to = static_cast<T*>(p.y) + first * p.C;
+    for (int i = 0; i < turns; ++i, to += step * p.C) {
+        if constexpr (kAhead<NTH> > 1) copies_wait<kAhead<NTH> - 2>();
+        else request(i);
+        const bool here = first + i * step < p.total;
+        f2 x[R][N2];
+        f2 a = 0ull;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t row = base + u * t.rows + at.rsub;
+        for (int k = 0; k < R; ++k) {
+            if (here && at.has(k)) {
+                ring.take(i, k, x[k]);
 #pragma unroll
-            for (int k = 0; k < R; ++k) {
-                if (row < p.total && at.has(k)) raw[u][k].load(static_cast<const T*>(p.x) + row * p.ldx + at.channel(k));
-                else raw[u][k].zero();
+                for (int e = 0; e < N2; ++e) a = add2(a, x[k][e]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < N2; ++e) x[k][e] = 0ull;
             }
         }
-        f2 x[U][R][N2];
-        float s[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            f2 a = 0ull;
-#pragma unroll
-            for (int k = 0; k < R; ++k) {
-                raw[u][k].to(x[u][k]);
-#pragma unroll
-                for (int e = 0; e < N2; ++e) a = add2(a, x[u][k][e]);
-            }
-            s[u] = sum2(a);
-        }
+        if constexpr (kAhead<NTH> > 1) request(i + kAhead<NTH> - 1);
+        float s[1] = {sum2(a)};
         sum(s);
-        float v[U];
+        const float mean = s[0] * inv_n;
+        a = 0ull;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const float mean = s[u] * inv_n;
-            f2 a = 0ull;
+        for (int k = 0; k < R; ++k)
 #pragma unroll
-            for (int k = 0; k < R; ++k)
-#pragma unroll
-                for (int e = 0; e < N2; ++e) {
-                    const f2 d = add2(x[u][k][e], pack(-mean, VEC == 1 ? 0.f : -mean));
-                    x[u][k][e] = at.has(k) ? d : 0ull;
-                    a = fma2(x[u][k][e], x[u][k][e], a);
-                }
-            v[u] = sum2(a);
-        }
-        sum(v);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t row = base + u * t.rows + at.rsub;
-            const f2 rstd = both(rsqrtf(fmaf(v[u], inv_n, p.eps)));
-#pragma unroll
-            for (int k = 0; k < R; ++k) {
-                if (!(row < p.total && at.has(k))) continue;
-                if constexpr (!kKeep) {
-                    vec_pairs<VEC>(p.weight ? p.weight + at.channel(k) : nullptr, 1.f, w[0]);
-                    vec_pairs<VEC>(p.bias ? p.bias + at.channel(k) : nullptr, 0.f, bias[0]);
-                }
-                f2 y[N2];
-#pragma unroll
-                for (int e = 0; e < N2; ++e) {
-                    y[e] = fma2(mul2(x[u][k][e], rstd), w[kKeep ? k : 0][e], bias[kKeep ? k : 0][e]);
-                    if (p.act) y[e] = mul2(y[e], sigmoid2(y[e]));
-                }
-                Row<T, VEC> out;
-                out.from(y);
-                out.store(static_cast<T*>(p.y) + row * p.C + at.channel(k));
+            for (int e = 0; e < N2; ++e) {
+                const f2 d = add2(x[k][e], pack(-mean, VEC == 1 ? 0.f : -mean));
+                x[k][e] = at.has(k) ? d : 0ull;
+                a = fma2(x[k][e], x[k][e], a);
             }
+        s[0] = sum2(a);
+        sum(s);
+        const f2 rstd = both(rsqrtf(fmaf(s[0], inv_n, p.eps)));
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            if (!(here && at.has(k))) continue;
+            if constexpr (!kKeep) {
+                vec_pairs<VEC>(p.weight ? p.weight + at.channel(k) : nullptr, 1.f, w[0]);
+                vec_pairs<VEC>(p.bias ? p.bias + at.channel(k) : nullptr, 0.f, bias[0]);
+            }
+            f2 y[N2];
+#pragma unroll
+            for (int e = 0; e < N2; ++e) y[e] = fma2(mul2(x[k][e], rstd), w[kKeep ? k : 0][e], bias[kKeep ? k : 0][e]);
+            if (p.act) {
+#pragma unroll
+                for (int e = 0; e < N2; ++e) y[e] = silu2(y[e]);
+            }
+            Row<T, VEC> out;
+            out.from(y);
+            out.store(to + at.channel(k));
         }
     }
 }
 
 // partial: [gridDim.y][2][C].
-template <typename T, typename TG, int VEC, int R, int U, int NTH>
-__global__ void __launch_bounds__(NTH, NTH == 256 ? 2 : 1) norm_token_bwd_kernel(NormParams p, Teams t, float* partial) {
+template <typename T, typename TG, int VEC, int R, int NTH>
+__global__ void __launch_bounds__(NTH, kResidentBwd<NTH, R * VEC>) norm_token_bwd_kernel(NormParams p, Teams t, float* partial) {
     constexpr int N2 = (VEC + 1) / 2;
     constexpr bool kKeep = R * VEC <= 8;
-    __shared__ float buf[2][NTH / 32][2 * U];
-    __shared__ f2 join[NTH * N2];
-    TeamSum<2 * U, NTH> sum{buf, t.lanes, 0};
+    __shared__ float buf[2][NTH / 32][2];
+    extern __shared__ __align__(16) char shared[];
+    f2* const join = reinterpret_cast<f2*>(shared);
+    TeamSum<2, NTH> sum{buf, t.lanes, 0};
+    Ring<T, VEC, R, NTH> ring(shared);
+    Ring<TG, VEC, R, NTH> ring_dy(shared + ring.kBytes);
     const Place<VEC, R> at(p, t);
     const float inv_n = 1.f / (float)(p.C / p.G);
-    f2 w[kKeep ? R : 1][N2], bias[kKeep ? R : 1][N2], dw[R][N2], db[R][N2];
+    const int64_t step = (int64_t)gridDim.y * t.rows;
+    const int64_t first = (int64_t)blockIdx.y * t.rows + at.rsub;
+    auto request = [&](int i) {
+        const int64_t row = first + i * step;
+        if (row < p.total)
+#pragma unroll
+            for (int k = 0; k < R; ++k)
+                if (at.has(k)) {
+                    ring.request(i, k, static_cast<const T*>(p.x) + row * p.ldx + at.channel(k));
+                    ring_dy.request(i, k, static_cast<const TG*>(p.dy) + row * p.C + at.channel(k));
+                }
+        copies_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead<NTH> - 1; ++i) request(i);
+    // dw and db of this thread's channels: in registers, or for large blocks in shared memory [R N2][2][NTH]
+    constexpr bool kShared = NTH != 256;
+    f2 w[kKeep ? R : 1][N2], bias[kKeep ? R : 1][N2], dw[kShared ? 1 : R][N2], db[kShared ? 1 : R][N2];
+    // (a single channel as it is, pairs as pairs)
+    using Sum = typename std::conditional<VEC == 1, float, f2>::type;
+    auto sums_at = [&](int k, int e, int v, int thread) -> Sum& { return reinterpret_cast<Sum*>(shared)[((k * N2 + e) * 2 + v) * NTH + thread]; };
+    auto as_pair = [](Sum s) {
+        if constexpr (VEC == 1) return pack(s, 0.f);
+        else return s;
+    };
+    auto put_sum = [](Sum& to, f2 s) {
+        if constexpr (VEC == 1) {
+            float none;
+            unpack(s, to, none);
+        } else {
+            to = s;
+        }
+    };
 #pragma unroll
     for (int k = 0; k < R; ++k) {
         if constexpr (kKeep) {
@@ -162,107 +233,96 @@ __global__ void __launch_bounds__(NTH, NTH == 256 ? 2 : 1) norm_token_bwd_kernel
             vec_pairs<VEC>(p.bias && at.has(k) ? p.bias + at.channel(k) : nullptr, 0.f, bias[k]);
         }
 #pragma unroll
-        for (int e = 0; e < N2; ++e) dw[k][e] = db[k][e] = 0ull;
+        for (int e = 0; e < N2; ++e) {
+            if constexpr (kShared) sums_at(k, e, 0, threadIdx.x) = sums_at(k, e, 1, threadIdx.x) = Sum(0);
+            else dw[k][e] = db[k][e] = 0ull;
+        }
     }
-    const int64_t step = (int64_t)t.rows * U;
-    for (int64_t base = blockIdx.y * step; base < p.total; base += gridDim.y * step) {
-        Row<T, VEC> raw[U][R];
-        Row<TG, VEC> graw[U][R];
+    const int turns = (int)((p.total - (int64_t)blockIdx.y * t.rows + step - 1) / step);
+    TG* to = static_cast<TG*>(p.dx) + first * p.C;
+    for (int i = 0; i < turns; ++i, to += step * p.C) {
+        if constexpr (kAhead<NTH> > 1) copies_wait<kAhead<NTH> - 2>();
+        else request(i);
+        const bool here = first + i * step < p.total;
+        f2 x[R][N2], q[R][N2];
+        f2 a = 0ull;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t row = base + u * t.rows + at.rsub;
+        for (int k = 0; k < R; ++k) {
+            if (here && at.has(k)) {
+                ring.take(i, k, x[k]);
+                ring_dy.take(i, k, q[k]);
 #pragma unroll
-            for (int k = 0; k < R; ++k) {
-                if (row < p.total && at.has(k)) {
-                    raw[u][k].load(static_cast<const T*>(p.x) + row * p.ldx + at.channel(k));
-                    graw[u][k].load(static_cast<const TG*>(p.dy) + row * p.C + at.channel(k));
+                for (int e = 0; e < N2; ++e) a = add2(a, x[k][e]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < N2; ++e) x[k][e] = q[k][e] = 0ull;
+            }
+        }
+        if constexpr (kAhead<NTH> > 1) request(i + kAhead<NTH> - 1);
+        float s[2] = {sum2(a), 0.f};
+        sum(s);
+        const float mean = s[0] * inv_n;
+        a = 0ull;
+#pragma unroll
+        for (int k = 0; k < R; ++k)
+#pragma unroll
+            for (int e = 0; e < N2; ++e) {
+                const f2 d = add2(x[k][e], pack(-mean, VEC == 1 ? 0.f : -mean));
+                x[k][e] = at.has(k) ? d : 0ull;
+                a = fma2(x[k][e], x[k][e], a);
+            }
+        s[0] = sum2(a);
+        s[1] = 0.f;
+        sum(s);
+        const f2 rstd = both(rsqrtf(fmaf(s[0], inv_n, p.eps)));
+        f2 m1 = 0ull, m2 = 0ull;
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            if constexpr (!kKeep) {
+                vec_pairs<VEC>(p.weight && at.has(k) ? p.weight + at.channel(k) : nullptr, 1.f, w[0]);
+                vec_pairs<VEC>(p.bias && at.has(k) ? p.bias + at.channel(k) : nullptr, 0.f, bias[0]);
+            }
+            const int kk = kKeep ? k : 0;
+#pragma unroll
+            for (int e = 0; e < N2; ++e) x[k][e] = mul2(x[k][e], rstd);
+            if (p.act) {
+#pragma unroll
+                for (int e = 0; e < N2; ++e) q[k][e] = mul2(q[k][e], silu_slope2(fma2(x[k][e], w[kk][e], bias[kk][e])));
+            }
+#pragma unroll
+            for (int e = 0; e < N2; ++e) {
+                if constexpr (kShared) {
+                    Sum &sw = sums_at(k, e, 0, threadIdx.x), &sb = sums_at(k, e, 1, threadIdx.x);
+                    put_sum(sw, fma2(q[k][e], x[k][e], as_pair(sw)));
+                    put_sum(sb, add2(q[k][e], as_pair(sb)));
                 } else {
-                    raw[u][k].zero();
-                    graw[u][k].zero();
+                    dw[k][e] = fma2(q[k][e], x[k][e], dw[k][e]);
+                    db[k][e] = add2(q[k][e], db[k][e]);
                 }
+                q[k][e] = mul2(q[k][e], w[kk][e]);
+                m1 = add2(m1, q[k][e]);
+                m2 = fma2(q[k][e], x[k][e], m2);
             }
         }
-        f2 x[U][R][N2], q[U][R][N2];
-        float s[2 * U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            f2 a = 0ull;
-#pragma unroll
-            for (int k = 0; k < R; ++k) {
-                raw[u][k].to(x[u][k]);
-#pragma unroll
-                for (int e = 0; e < N2; ++e) a = add2(a, x[u][k][e]);
-            }
-            s[u] = sum2(a);
-            s[U + u] = 0.f;
-        }
+        s[0] = sum2(m1);
+        s[1] = sum2(m2);
         sum(s);
+        const f2 n1 = both(-s[0] * inv_n), n2 = both(-s[1] * inv_n);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const float mean = s[u] * inv_n;
-            f2 a = 0ull;
+        for (int k = 0; k < R; ++k) {
+            if (!(here && at.has(k))) continue;
+            f2 dx[N2];
 #pragma unroll
-            for (int k = 0; k < R; ++k)
-#pragma unroll
-                for (int e = 0; e < N2; ++e) {
-                    const f2 d = add2(x[u][k][e], pack(-mean, VEC == 1 ? 0.f : -mean));
-                    x[u][k][e] = at.has(k) ? d : 0ull;
-                    a = fma2(x[u][k][e], x[u][k][e], a);
-                }
-            s[u] = sum2(a);
-        }
-        sum(s);
-        float rstd[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            rstd[u] = rsqrtf(fmaf(s[u], inv_n, p.eps));
-            const f2 r2 = both(rstd[u]);
-            f2 m1 = 0ull, m2 = 0ull;
-#pragma unroll
-            for (int k = 0; k < R; ++k) {
-                graw[u][k].to(q[u][k]);
-                if constexpr (!kKeep) {
-                    vec_pairs<VEC>(p.weight && at.has(k) ? p.weight + at.channel(k) : nullptr, 1.f, w[0]);
-                    vec_pairs<VEC>(p.bias && at.has(k) ? p.bias + at.channel(k) : nullptr, 0.f, bias[0]);
-                }
-#pragma unroll
-                for (int e = 0; e < N2; ++e) {
-                    const int kk = kKeep ? k : 0;
-                    const f2 xh = mul2(x[u][k][e], r2);
-                    x[u][k][e] = xh;
-                    f2 dp = q[u][k][e];
-                    if (p.act) dp = mul2(dp, silu_slope2(fma2(xh, w[kk][e], bias[kk][e])));
-                    dw[k][e] = fma2(dp, xh, dw[k][e]);
-                    db[k][e] = add2(dp, db[k][e]);
-                    const f2 qq = mul2(dp, w[kk][e]);
-                    q[u][k][e] = qq;
-                    m1 = add2(m1, qq);
-                    m2 = fma2(qq, xh, m2);
-                }
-            }
-            s[u] = sum2(m1);
-            s[U + u] = sum2(m2);
-        }
-        sum(s);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t row = base + u * t.rows + at.rsub;
-            const f2 m1 = both(-s[u] * inv_n), m2 = both(-s[U + u] * inv_n), r2 = both(rstd[u]);
-#pragma unroll
-            for (int k = 0; k < R; ++k) {
-                if (!(row < p.total && at.has(k))) continue;
-                f2 dx[N2];
-#pragma unroll
-                for (int e = 0; e < N2; ++e) dx[e] = mul2(r2, fma2(x[u][k][e], m2, add2(q[u][k][e], m1)));
-                Row<TG, VEC> out;
-                out.from(dx);
-                out.store(static_cast<TG*>(p.dx) + row * p.C + at.channel(k));
-            }
+            for (int e = 0; e < N2; ++e) dx[e] = mul2(rstd, fma2(x[k][e], n2, add2(q[k][e], n1)));
+            Row<TG, VEC> out;
+            out.from(dx);
+            out.store(to + at.channel(k));
         }
     }
     tc::grid_dep_launch();
     if (!p.dweight && !p.dbias) return;
-    // the block's rows side by side first
+    // the block's rows side by side first (where the last rows were on their way)
+    copies_wait<0>();
     const int row_threads = t.groups * t.lanes;  // threads of one row
 #pragma unroll
     for (int v = 0; v < 2; ++v) {
@@ -271,16 +331,24 @@ __global__ void __launch_bounds__(NTH, NTH == 256 ? 2 : 1) norm_token_bwd_kernel
         for (int k = 0; k < R; ++k) {
             f2 total[N2];
 #pragma unroll
-            for (int e = 0; e < N2; ++e) total[e] = v ? db[k][e] : dw[k][e];
+            for (int e = 0; e < N2; ++e) {
+                if constexpr (kShared) total[e] = as_pair(sums_at(k, e, v, threadIdx.x));
+                else total[e] = v ? db[k][e] : dw[k][e];
+            }
             if (t.rows > 1) {
                 __syncthreads();
+                if constexpr (!kShared) {
 #pragma unroll
-                for (int e = 0; e < N2; ++e) join[threadIdx.x * N2 + e] = total[e];
-                __syncthreads();
+                    for (int e = 0; e < N2; ++e) join[threadIdx.x * N2 + e] = total[e];
+                    __syncthreads();
+                }
                 if (at.rsub == 0)
                     for (int r = 1; r < t.rows; ++r)
 #pragma unroll
-                        for (int e = 0; e < N2; ++e) total[e] = add2(total[e], join[(threadIdx.x + r * row_threads) * N2 + e]);
+                        for (int e = 0; e < N2; ++e) {
+                            const int from = threadIdx.x + r * row_threads;
+                            total[e] = add2(total[e], kShared ? as_pair(sums_at(k, e, v, from)) : join[from * N2 + e]);
+                        }
             }
             if (at.rsub == 0 && at.has(k)) {
 #pragma unroll
@@ -310,9 +378,9 @@ Teams teams_of(int pieces, int R, int G, int nth) {
     return t;
 }
 // Blocks along the rows: no more than the rows need, about `resident` an SM in all.
-dim3 grid_of(const NormParams& p, const Teams& t, int U, int resident) {
+dim3 grid_of(const NormParams& p, const Teams& t, int resident) {
     const int x = (p.G + t.groups - 1) / t.groups;
-    int64_t y = ((int64_t)p.total + t.rows * U - 1) / (t.rows * U);
+    int64_t y = ((int64_t)p.total + t.rows - 1) / t.rows;
     const int64_t most = (int64_t)kSms * resident / x;
     if (y > most) y = most;
     if (y < 1) y = 1;
@@ -320,50 +388,57 @@ dim3 grid_of(const NormParams& p, const Teams& t, int U, int resident) {
     return dim3(x, (unsigned)y);
 }
 
-// ---- which variant: pieces a lane, rows at a time, threads a block ------------------------------------------
+// ---- which variant: pieces a lane, threads a block ------------------------------------------
 
-// f(R, U, NTH as constants) for groups of `pieces` pieces of VEC elements.
+// f(R, NTH as constants) for groups of `pieces` pieces of VEC elements.
 template <int N>
 struct Int {
     static constexpr int value = N;
 };
 template <int VEC, typename F>
 auto pick_variant(int pieces, F f) {
-    if constexpr (VEC >= 8) {
-        if (pieces <= 32) return f(Int<1>{}, Int<2>{}, Int<256>{});
-        if (pieces <= 512) return f(Int<2>{}, Int<1>{}, Int<256>{});
-        return f(Int<2>{}, Int<1>{}, Int<1024>{});
-    } else if constexpr (VEC == 4) {
-        if (pieces <= 32) return f(Int<1>{}, Int<2>{}, Int<256>{});
-        if (pieces <= 512) return f(Int<2>{}, Int<1>{}, Int<256>{});
-        return f(Int<4>{}, Int<1>{}, Int<1024>{});
+    if constexpr (VEC >= 4) {
+        if (pieces <= 32) return f(Int<1>{}, Int<256>{});
+        if (pieces <= 512) return f(Int<2>{}, Int<256>{});
+        return f(Int<VEC == 4 ? 4 : 2>{}, Int<1024>{});
     } else {
-        if (pieces <= 32) return f(Int<1>{}, Int<4>{}, Int<256>{});
-        if (pieces <= 1024) return f(Int<4>{}, Int<1>{}, Int<256>{});
-        return f(Int<16>{}, Int<1>{}, Int<1024>{});
+        if (pieces <= 32) return f(Int<1>{}, Int<256>{});
+        if (pieces <= 1024) return f(Int<4>{}, Int<256>{});
+        return f(Int<16>{}, Int<1024>{});
     }
 }
+constexpr int resident_fwd(int nth) { return nth == 256 ? 4 : 1; }
 
 template <typename T, int VEC>
 cudaError_t launch_fwd(const NormParams& p, cudaStream_t st) {
     const int pieces = p.C / p.G / VEC;
-    return pick_variant<VEC>(pieces, [&](auto r, auto u, auto nth) {
-        constexpr int R = decltype(r)::value, U = decltype(u)::value, NTH = decltype(nth)::value;
+    return pick_variant<VEC>(pieces, [&](auto r, auto nth) {
+        constexpr int R = decltype(r)::value, NTH = decltype(nth)::value;
+        const auto kern = norm_token_fwd_kernel<T, VEC, R, NTH>;
+        constexpr int smem = Ring<T, VEC, R, NTH>::kBytes;
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
         const Teams t = teams_of(pieces, R, p.G, NTH);
-        norm_token_fwd_kernel<T, VEC, R, U, NTH><<<grid_of(p, t, U, NTH == 256 ? 16 : 4), NTH, 0, st>>>(p, t);
+        kern<<<grid_of(p, t, resident_fwd(NTH)), NTH, smem, st>>>(p, t);
         return cudaGetLastError();
     });
 }
 template <typename T, typename TG, int VEC>
 cudaError_t launch_bwd(const NormParams& p, cudaStream_t st) {
     const int pieces = p.C / p.G / VEC;
-    return pick_variant<VEC>(pieces, [&](auto r, auto u, auto nth) {
-        constexpr int R = decltype(r)::value, U = decltype(u)::value, NTH = decltype(nth)::value;
+    return pick_variant<VEC>(pieces, [&](auto r, auto nth) {
+        constexpr int R = decltype(r)::value, NTH = decltype(nth)::value;
+        const auto kern = norm_token_bwd_kernel<T, TG, VEC, R, NTH>;
+        constexpr int rings = Ring<T, VEC, R, NTH>::kBytes + Ring<TG, VEC, R, NTH>::kBytes;
+        constexpr int joins = NTH == 256 ? NTH * ((VEC + 1) / 2) * 8 : NTH * R * VEC * 8;
+        constexpr int smem = rings > joins ? rings : joins;
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
         const Teams t = teams_of(pieces, R, p.G, NTH);
-        const dim3 grid = grid_of(p, t, U, NTH == 256 ? 2 : 1);
+        const dim3 grid = grid_of(p, t, kResidentBwd<NTH, R * VEC>);
         float* const partial = static_cast<float*>(p.ws);
-        norm_token_bwd_kernel<T, TG, VEC, R, U, NTH><<<grid, NTH, 0, st>>>(p, t, partial);
-        const cudaError_t e = cudaGetLastError();
+        kern<<<grid, NTH, smem, st>>>(p, t, partial);
+        e = cudaGetLastError();
         if (e != cudaSuccess || (!p.dweight && !p.dbias)) return e;
         return tc::launch_dependent(norm_weights_kernel, (unsigned)((p.C + 31) / 32), 256, 0, st, (const float*)partial, (int)grid.y, p.C, p.dweight,
                                     p.dbias);
@@ -387,9 +462,9 @@ size_t norm_token_bwd_workspace(const NormParams& p) {
     auto look = [&](auto vec) {
         constexpr int VEC = decltype(vec)::value;
         if (cg % VEC != 0) return;
-        const size_t y = pick_variant<VEC>(cg / VEC, [&](auto r, auto u, auto nth) {
-            constexpr int R = decltype(r)::value, U = decltype(u)::value, NTH = decltype(nth)::value;
-            return (size_t)grid_of(p, teams_of(cg / VEC, R, p.G, NTH), U, NTH == 256 ? 2 : 1).y;
+        const size_t y = pick_variant<VEC>(cg / VEC, [&](auto r, auto nth) {
+            constexpr int R = decltype(r)::value, NTH = decltype(nth)::value;
+            return (size_t)grid_of(p, teams_of(cg / VEC, R, p.G, NTH), kResidentBwd<NTH, R * VEC>).y;
         });
         if (y > most) most = y;
     };

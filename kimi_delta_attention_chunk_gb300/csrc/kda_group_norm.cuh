@@ -14,10 +14,16 @@ constexpr int kSms = 152;
 
 __device__ __forceinline__ f2 both(float v) { return pack(v, v); }
 __device__ __forceinline__ f2 neg2(f2 x) { return x ^ 0x8000000080000000ull; }
-// act'(p): silu' = s + p s (1 - s)
+// 1 / (1 + e^-x) of a pair, packed but for the special functions; x times it; and the slope of that, s + p s (1 - s).
+__device__ __forceinline__ f2 gate2(f2 x) {
+    float a, b;
+    unpack(add2(ex2_2(mul2(x, both(-kLog2e))), both(1.f)), a, b);
+    return pack(rcp(a), rcp(b));
+}
+__device__ __forceinline__ f2 silu2(f2 p) { return mul2(p, gate2(p)); }
 __device__ __forceinline__ f2 silu_slope2(f2 p) {
-    const f2 s = sigmoid2(p), ps = mul2(p, s);
-    return fma2(ps, add2(both(1.f), neg2(s)), s);
+    const f2 s = gate2(p);
+    return fma2(mul2(p, s), fma2(s, both(-1.f), both(1.f)), s);
 }
 // VEC consecutive fp32 as pairs (of one: its upper half zero), `none` where there are none.
 template <int VEC>

@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(kThreads) seq_apply_kernel(NormParams p, SeqMa
 #pragma unroll
                 for (int i = 0; i < N2; ++i) {
                     v[i] = fma2(add2(v[i], mean[i]), scale[i], bias[i]);
-                    if (p.act) v[i] = mul2(v[i], sigmoid2(v[i]));
+                    if (p.act) v[i] = silu2(v[i]);
                 }
                 rows[j].from(v);
                 rows[j].store(static_cast<T*>(p.y) + (int64_t)(t + j * kSubs) * p.C + c);
