@@ -19,16 +19,37 @@ struct Teams {
     int rows;    // rows that a block has at a time
 };
 
+// A variant: R pieces of VEC elements a lane, NTH threads a block, teams of LANES lanes that the group's pieces fill exactly and that
+// fill the row's groups (0: any team).
+template <int VEC_, int R_, int NTH_, int LANES_>
+struct Variant {
+    static constexpr int VEC = VEC_, R = R_, NTH = NTH_, LANES = LANES_, N2 = (VEC + 1) / 2, E = R * VEC;
+    // Rows of a thread under way in shared memory; where a row is four pieces and more its own loads are enough.
+    static constexpr int kAhead = R <= 2 && NTH == 256 ? 4 : 1;
+    // Backwards, dw and db of a thread's channels: in registers, or where they are many in shared memory.
+    static constexpr bool kSharedSums = E > 16 || NTH != 256;
+    static constexpr int kFwd = NTH != 256 ? 1 : E > 16 ? 3 : 4, kBwd = NTH != 256 ? 1 : E > 8 && !kSharedSums ? 2 : 3;  // blocks an SM
+};
+
 // Sums of `N` values over every team.  Teams of more than a warp meet in shared memory, in a buffer of their own each time.
-template <int N, int NTH>
+template <int LANES, int NTH>
 struct TeamSum {
-    float (*buf)[NTH / 32][N];  // [2]
+    float (*buf)[NTH / 32][2];  // [2]
     int lanes, turn;
+    template <int N>
     __device__ __forceinline__ void operator()(float (&v)[N]) {
-        const int within = min(lanes, 32);
-        for (int o = within / 2; o > 0; o >>= 1)
+        if constexpr (LANES > 0) {
 #pragma unroll
-            for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+            for (int o = LANES / 2; o > 0; o /= 2)
+#pragma unroll
+                for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+            return;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o /= 2)
+            if (o < lanes)
+#pragma unroll
+                for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
         if (lanes <= 32) return;
         const int w = threadIdx.x / 32, team = lanes / 32, w0 = w / team * team;
         if (threadIdx.x % 32 == 0)
@@ -44,45 +65,40 @@ struct TeamSum {
     }
 };
 
-// A thread's place: its group, its row among those that the block has at a time, its first channel in the group and which of its R
-// pieces are there.
-template <int VEC, int R>
+// A thread's place: its group, its row among those that the block has at a time, and its pieces of the group.
+template <typename V>
 struct Place {
     int g, rsub, cg, lane, lanes;
     __device__ __forceinline__ Place(const NormParams& p, const Teams& t) {
-        const int team = threadIdx.x / t.lanes;
-        lane = threadIdx.x % t.lanes;
-        lanes = t.lanes;
+        lanes = V::LANES > 0 ? V::LANES : t.lanes;
+        const int team = threadIdx.x / lanes;
+        lane = threadIdx.x % lanes;
         g = blockIdx.x * t.groups + team % t.groups;
         rsub = team / t.groups;
         cg = p.C / p.G;
-        if (g >= p.G) cg = 0;
+        if (V::LANES == 0 && g >= p.G) cg = 0;
     }
-    __device__ __forceinline__ bool has(int k) const { return (lane + k * lanes) * VEC < cg; }
+    __device__ __forceinline__ bool has(int k) const { return V::LANES > 0 || (lane + k * lanes) * V::VEC < cg; }
     // (of a piece that is there)
-    __device__ __forceinline__ int channel(int k) const { return g * cg + (lane + k * lanes) * VEC; }
+    __device__ __forceinline__ int channel(int k) const { return g * cg + (lane + k * lanes) * V::VEC; }
 };
 
 // A thread's own pieces of the next rows, on their way through shared memory: what a thread asks for it alone reads, so that no thread
-// waits for another.  Two-byte pieces have no asynchronous copy: they are loaded when asked for.  Blocks of 1024 threads (groups of
-// more than some thousand channels) load a row when its turn comes: their shared memory would not hold more, or has the sums.
-template <int NTH>
-constexpr int kAhead = NTH == 256 ? 4 : 1;  // rows under way, the one at hand among them
-template <typename T, int VEC, int R, int NTH>
+// waits for another.  (Two-byte pieces have no asynchronous copy: they are loaded when asked for.)
+template <typename V, typename T>
 struct Ring {
-    static constexpr int kRows = kAhead<NTH>;
-    static constexpr int kBytes = kRows > 1 ? kRows * R * NTH * VEC * (int)sizeof(T) : 0;
+    static constexpr int kBytes = V::kAhead > 1 ? V::kAhead * V::R * V::NTH * V::VEC * (int)sizeof(T) : 0;
     T* mine;
-    Row<T, VEC> now[kRows > 1 ? 1 : R];
-    __device__ __forceinline__ explicit Ring(void* shared) : mine(static_cast<T*>(shared) + threadIdx.x * VEC) {}
-    __device__ __forceinline__ T* at(int row, int k) const { return mine + ((row % kRows) * R + k) * NTH * VEC; }
+    Row<T, V::VEC> now[V::kAhead > 1 ? 1 : V::R];
+    __device__ __forceinline__ explicit Ring(void* shared) : mine(static_cast<T*>(shared) + threadIdx.x * V::VEC) {}
+    __device__ __forceinline__ T* at(int row, int k) const { return mine + ((row % V::kAhead) * V::R + k) * V::NTH * V::VEC; }
     __device__ __forceinline__ void request(int row, int k, const T* from) {
-        if constexpr (kRows > 1) Row<T, VEC>::copy_async(at(row, k), from);
+        if constexpr (V::kAhead > 1) Row<T, V::VEC>::copy_async(at(row, k), from);
         else now[k].load(from);
     }
-    __device__ __forceinline__ void take(int row, int k, f2 (&v)[(VEC + 1) / 2]) const {
-        if constexpr (kRows > 1) {
-            Row<T, VEC> r;
+    __device__ __forceinline__ void take(int row, int k, f2 (&v)[V::N2]) const {
+        if constexpr (V::kAhead > 1) {
+            Row<T, V::VEC> r;
             r.from_shared(at(row, k));
             r.to(v);
         } else {
@@ -90,51 +106,86 @@ struct Ring {
         }
     }
 };
-template <int NTH, int E>
-constexpr int kResidentBwd = NTH != 256 ? 1 : E > 8 ? 2 : 3;
 
-template <typename T, int VEC, int R, int NTH>
-__global__ void __launch_bounds__(NTH, NTH == 256 ? 4 : 1) norm_token_fwd_kernel(NormParams p, Teams t) {
-    constexpr int N2 = (VEC + 1) / 2;
-    constexpr bool kKeep = R * VEC <= 16;
-    __shared__ float buf[2][NTH / 32][1];
+// 1 / sqrt(var + eps)
+__device__ __forceinline__ float inverse_deviation(float m2, float inv_n, float eps) {
+    float r;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaxf(fmaf(m2, inv_n, eps), 1e-37f)));
+    return r;
+}
+
+// The weights of a thread's channels: kept where they are few, else read again for every row.
+template <typename V>
+struct Weights {
+    static constexpr bool kKeep = V::E <= 8;
+    f2 w[kKeep ? V::R : 1][V::N2], b[kKeep ? V::R : 1][V::N2];
+    __device__ __forceinline__ void read(const NormParams& p, const Place<V>& at, int k, int to) {
+        vec_pairs<V::VEC>(p.weight && at.has(k) ? p.weight + at.channel(k) : nullptr, 1.f, w[to]);
+        vec_pairs<V::VEC>(p.bias && at.has(k) ? p.bias + at.channel(k) : nullptr, 0.f, b[to]);
+    }
+    __device__ __forceinline__ Weights(const NormParams& p, const Place<V>& at) {
+        if constexpr (kKeep)
+#pragma unroll
+            for (int k = 0; k < V::R; ++k) read(p, at, k, k);
+    }
+    // Where piece k's are.
+    __device__ __forceinline__ int of(const NormParams& p, const Place<V>& at, int k) {
+        if constexpr (kKeep) return k;
+        read(p, at, k, 0);
+        return 0;
+    }
+};
+
+// x - mean of a thread's pieces, zeros where there are none; the sum of squares.
+template <typename V>
+__device__ __forceinline__ float centre(f2 (&x)[V::R][V::N2], float mean, const Place<V>& at) {
+    f2 a = 0ull;
+#pragma unroll
+    for (int k = 0; k < V::R; ++k)
+#pragma unroll
+        for (int e = 0; e < V::N2; ++e) {
+            const f2 d = add2(x[k][e], pack(-mean, V::VEC == 1 ? 0.f : -mean));
+            x[k][e] = at.has(k) ? d : 0ull;
+            a = fma2(x[k][e], x[k][e], a);
+        }
+    return sum2(a);
+}
+
+template <typename T, typename V>
+__global__ void __launch_bounds__(V::NTH, V::kFwd) norm_token_fwd_kernel(NormParams p, Teams t) {
+    constexpr int R = V::R, N2 = V::N2, A = V::kAhead;
+    __shared__ float buf[2][V::NTH / 32][2];
     extern __shared__ __align__(16) char shared[];
-    TeamSum<1, NTH> sum{buf, t.lanes, 0};
-    Ring<T, VEC, R, NTH> ring(shared);
-    const Place<VEC, R> at(p, t);
+    TeamSum<V::LANES, V::NTH> sum{buf, t.lanes, 0};
+    Ring<V, T> ring(shared);
+    const Place<V> at(p, t);
     const float inv_n = 1.f / (float)(p.C / p.G);
-    const int64_t step = (int64_t)gridDim.y * t.rows;
-    const int64_t first = (int64_t)blockIdx.y * t.rows + at.rsub;
+    // this thread's rows: every step-th from `first`
+    const int64_t step = (int64_t)gridDim.y * t.rows, first = (int64_t)blockIdx.y * t.rows + at.rsub;
+    const int mine = first < p.total ? (int)((p.total - first + step - 1) / step) : 0;
+    const T* from = static_cast<const T*>(p.x) + first * p.ldx;
     auto request = [&](int i) {
-        const int64_t row = first + i * step;
-        if (row < p.total)
+        if (i < mine) {
 #pragma unroll
             for (int k = 0; k < R; ++k)
-                if (at.has(k)) ring.request(i, k, static_cast<const T*>(p.x) + row * p.ldx + at.channel(k));
-        copies_commit();
+                if (at.has(k)) ring.request(i, k, from + at.channel(k));
+            from += step * p.ldx;
+        }
+        if constexpr (A > 1) copies_commit();
     };
 #pragma unroll
-    for (int i = 0; i < kAhead<NTH> - 1; ++i) request(i);
-    f2 w[kKeep ? R : 1][N2], bias[kKeep ? R : 1][N2];
-    if constexpr (kKeep) {
-#pragma unroll
-        for (int k = 0; k < R; ++k) {
-            vec_pairs<VEC>(p.weight && at.has(k) ? p.weight + at.channel(k) : nullptr, 1.f, w[k]);
-            vec_pairs<VEC>(p.bias && at.has(k) ? p.bias + at.channel(k) : nullptr, 0.f, bias[k]);
-        }
-    }
+    for (int i = 0; i < A - 1; ++i) request(i);
+    Weights<V> weights(p, at);
     // (teams of more than a warp meet, so every thread of a block takes as many turns)
     const int turns = (int)((p.total - (int64_t)blockIdx.y * t.rows + step - 1) / step);
     T* to = static_cast<T*>(p.y) + first * p.C;
     for (int i = 0; i < turns; ++i, to += step * p.C) {
-        if constexpr (kAhead<NTH> > 1) copies_wait<kAhead<NTH> - 2>();
+        if constexpr (A > 1) copies_wait<A - 2>();
         else request(i);
-        const bool here = first + i * step < p.total;
-        f2 x[R][N2];
-        f2 a = 0ull;
+        f2 x[R][N2], a = 0ull;
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            if (here && at.has(k)) {
+            if (at.has(k)) {  // (behind the last row: whatever is there)
                 ring.take(i, k, x[k]);
 #pragma unroll
                 for (int e = 0; e < N2; ++e) a = add2(a, x[k][e]);
@@ -143,83 +194,72 @@ __global__ void __launch_bounds__(NTH, NTH == 256 ? 4 : 1) norm_token_fwd_kernel
                 for (int e = 0; e < N2; ++e) x[k][e] = 0ull;
             }
         }
-        if constexpr (kAhead<NTH> > 1) request(i + kAhead<NTH> - 1);
+        if constexpr (A > 1) request(i + A - 1);
         float s[1] = {sum2(a)};
         sum(s);
-        const float mean = s[0] * inv_n;
-        a = 0ull;
-#pragma unroll
-        for (int k = 0; k < R; ++k)
-#pragma unroll
-            for (int e = 0; e < N2; ++e) {
-                const f2 d = add2(x[k][e], pack(-mean, VEC == 1 ? 0.f : -mean));
-                x[k][e] = at.has(k) ? d : 0ull;
-                a = fma2(x[k][e], x[k][e], a);
-            }
-        s[0] = sum2(a);
+        s[0] = centre<V>(x, s[0] * inv_n, at);
         sum(s);
-        const f2 rstd = both(rsqrtf(fmaf(s[0], inv_n, p.eps)));
+        if (i >= mine) continue;
+        const f2 rstd = both(inverse_deviation(s[0], inv_n, p.eps));
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            if (!(here && at.has(k))) continue;
-            if constexpr (!kKeep) {
-                vec_pairs<VEC>(p.weight ? p.weight + at.channel(k) : nullptr, 1.f, w[0]);
-                vec_pairs<VEC>(p.bias ? p.bias + at.channel(k) : nullptr, 0.f, bias[0]);
-            }
+            const int wk = weights.of(p, at, k);
             f2 y[N2];
 #pragma unroll
-            for (int e = 0; e < N2; ++e) y[e] = fma2(mul2(x[k][e], rstd), w[kKeep ? k : 0][e], bias[kKeep ? k : 0][e]);
+            for (int e = 0; e < N2; ++e) y[e] = fma2(mul2(x[k][e], rstd), weights.w[wk][e], weights.b[wk][e]);
             if (p.act) {
 #pragma unroll
                 for (int e = 0; e < N2; ++e) y[e] = silu2(y[e]);
             }
-            Row<T, VEC> out;
+            Row<T, V::VEC> out;
             out.from(y);
-            out.store(to + at.channel(k));
+            if (at.has(k)) out.store(to + at.channel(k));
         }
     }
 }
 
 // partial: [gridDim.y][2][C].
-template <typename T, typename TG, int VEC, int R, int NTH>
-__global__ void __launch_bounds__(NTH, kResidentBwd<NTH, R * VEC>) norm_token_bwd_kernel(NormParams p, Teams t, float* partial) {
-    constexpr int N2 = (VEC + 1) / 2;
-    constexpr bool kKeep = R * VEC <= 8;
+template <typename T, typename TG, typename V>
+__global__ void __launch_bounds__(V::NTH, V::kBwd) norm_token_bwd_kernel(NormParams p, Teams t, float* partial) {
+    constexpr int R = V::R, N2 = V::N2, A = V::kAhead, NTH = V::NTH;
+    constexpr bool kShared = V::kSharedSums;
     __shared__ float buf[2][NTH / 32][2];
     extern __shared__ __align__(16) char shared[];
-    f2* const join = reinterpret_cast<f2*>(shared);
-    TeamSum<2, NTH> sum{buf, t.lanes, 0};
-    Ring<T, VEC, R, NTH> ring(shared);
-    Ring<TG, VEC, R, NTH> ring_dy(shared + ring.kBytes);
-    const Place<VEC, R> at(p, t);
+    TeamSum<V::LANES, NTH> sum{buf, t.lanes, 0};
+    Ring<V, T> ring(shared);
+    Ring<V, TG> ring_dy(shared + ring.kBytes);
+    const Place<V> at(p, t);
     const float inv_n = 1.f / (float)(p.C / p.G);
-    const int64_t step = (int64_t)gridDim.y * t.rows;
-    const int64_t first = (int64_t)blockIdx.y * t.rows + at.rsub;
+    const int64_t step = (int64_t)gridDim.y * t.rows, first = (int64_t)blockIdx.y * t.rows + at.rsub;
+    const int mine = first < p.total ? (int)((p.total - first + step - 1) / step) : 0;
+    const T* from = static_cast<const T*>(p.x) + first * p.ldx;
+    const TG* from_dy = static_cast<const TG*>(p.dy) + first * p.C;
     auto request = [&](int i) {
-        const int64_t row = first + i * step;
-        if (row < p.total)
+        if (i < mine) {
 #pragma unroll
             for (int k = 0; k < R; ++k)
                 if (at.has(k)) {
-                    ring.request(i, k, static_cast<const T*>(p.x) + row * p.ldx + at.channel(k));
-                    ring_dy.request(i, k, static_cast<const TG*>(p.dy) + row * p.C + at.channel(k));
+                    ring.request(i, k, from + at.channel(k));
+                    ring_dy.request(i, k, from_dy + at.channel(k));
                 }
-        copies_commit();
+            from += step * p.ldx;
+            from_dy += step * p.C;
+        }
+        if constexpr (A > 1) copies_commit();
     };
 #pragma unroll
-    for (int i = 0; i < kAhead<NTH> - 1; ++i) request(i);
-    // dw and db of this thread's channels: in registers, or for large blocks in shared memory [R N2][2][NTH]
-    constexpr bool kShared = NTH != 256;
-    f2 w[kKeep ? R : 1][N2], bias[kKeep ? R : 1][N2], dw[kShared ? 1 : R][N2], db[kShared ? 1 : R][N2];
-    // (a single channel as it is, pairs as pairs)
-    using Sum = typename std::conditional<VEC == 1, float, f2>::type;
+    for (int i = 0; i < A - 1; ++i) request(i);
+    Weights<V> weights(p, at);
+    // dw and db of this thread's channels: in registers, or in shared memory [R N2][2][NTH], a single channel as it is, pairs as pairs
+    using Sum = typename std::conditional<V::VEC == 1, float, f2>::type;
+    f2 dw[kShared ? 1 : R][N2], db[kShared ? 1 : R][N2];
     auto sums_at = [&](int k, int e, int v, int thread) -> Sum& { return reinterpret_cast<Sum*>(shared)[((k * N2 + e) * 2 + v) * NTH + thread]; };
     auto as_pair = [](Sum s) {
-        if constexpr (VEC == 1) return pack(s, 0.f);
+        if constexpr (V::VEC == 1) return pack(s, 0.f);
         else return s;
     };
     auto put_sum = [](Sum& to, f2 s) {
-        if constexpr (VEC == 1) {
+        if constexpr (V::VEC == 1) {
             float none;
             unpack(s, to, none);
         } else {
@@ -227,28 +267,21 @@ __global__ void __launch_bounds__(NTH, kResidentBwd<NTH, R * VEC>) norm_token_bw
         }
     };
 #pragma unroll
-    for (int k = 0; k < R; ++k) {
-        if constexpr (kKeep) {
-            vec_pairs<VEC>(p.weight && at.has(k) ? p.weight + at.channel(k) : nullptr, 1.f, w[k]);
-            vec_pairs<VEC>(p.bias && at.has(k) ? p.bias + at.channel(k) : nullptr, 0.f, bias[k]);
-        }
+    for (int k = 0; k < R; ++k)
 #pragma unroll
         for (int e = 0; e < N2; ++e) {
             if constexpr (kShared) sums_at(k, e, 0, threadIdx.x) = sums_at(k, e, 1, threadIdx.x) = Sum(0);
             else dw[k][e] = db[k][e] = 0ull;
         }
-    }
     const int turns = (int)((p.total - (int64_t)blockIdx.y * t.rows + step - 1) / step);
     TG* to = static_cast<TG*>(p.dx) + first * p.C;
     for (int i = 0; i < turns; ++i, to += step * p.C) {
-        if constexpr (kAhead<NTH> > 1) copies_wait<kAhead<NTH> - 2>();
+        if constexpr (A > 1) copies_wait<A - 2>();
         else request(i);
-        const bool here = first + i * step < p.total;
-        f2 x[R][N2], q[R][N2];
-        f2 a = 0ull;
+        f2 x[R][N2], q[R][N2], a = 0ull;
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            if (here && at.has(k)) {
+            if (at.has(k) && i < mine) {
                 ring.take(i, k, x[k]);
                 ring_dy.take(i, k, q[k]);
 #pragma unroll
@@ -258,36 +291,21 @@ __global__ void __launch_bounds__(NTH, kResidentBwd<NTH, R * VEC>) norm_token_bw
                 for (int e = 0; e < N2; ++e) x[k][e] = q[k][e] = 0ull;
             }
         }
-        if constexpr (kAhead<NTH> > 1) request(i + kAhead<NTH> - 1);
-        float s[2] = {sum2(a), 0.f};
-        sum(s);
-        const float mean = s[0] * inv_n;
-        a = 0ull;
-#pragma unroll
-        for (int k = 0; k < R; ++k)
-#pragma unroll
-            for (int e = 0; e < N2; ++e) {
-                const f2 d = add2(x[k][e], pack(-mean, VEC == 1 ? 0.f : -mean));
-                x[k][e] = at.has(k) ? d : 0ull;
-                a = fma2(x[k][e], x[k][e], a);
-            }
-        s[0] = sum2(a);
-        s[1] = 0.f;
-        sum(s);
-        const f2 rstd = both(rsqrtf(fmaf(s[0], inv_n, p.eps)));
+        if constexpr (A > 1) request(i + A - 1);
+        float one[1] = {sum2(a)};
+        sum(one);
+        one[0] = centre<V>(x, one[0] * inv_n, at);
+        sum(one);
+        const f2 rstd = both(inverse_deviation(one[0], inv_n, p.eps));
         f2 m1 = 0ull, m2 = 0ull;
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            if constexpr (!kKeep) {
-                vec_pairs<VEC>(p.weight && at.has(k) ? p.weight + at.channel(k) : nullptr, 1.f, w[0]);
-                vec_pairs<VEC>(p.bias && at.has(k) ? p.bias + at.channel(k) : nullptr, 0.f, bias[0]);
-            }
-            const int kk = kKeep ? k : 0;
+            const int wk = weights.of(p, at, k);
 #pragma unroll
             for (int e = 0; e < N2; ++e) x[k][e] = mul2(x[k][e], rstd);
             if (p.act) {
 #pragma unroll
-                for (int e = 0; e < N2; ++e) q[k][e] = mul2(q[k][e], silu_slope2(fma2(x[k][e], w[kk][e], bias[kk][e])));
+                for (int e = 0; e < N2; ++e) q[k][e] = mul2(q[k][e], silu_slope2(fma2(x[k][e], weights.w[wk][e], weights.b[wk][e])));
             }
 #pragma unroll
             for (int e = 0; e < N2; ++e) {
@@ -299,34 +317,34 @@ __global__ void __launch_bounds__(NTH, kResidentBwd<NTH, R * VEC>) norm_token_bw
                     dw[k][e] = fma2(q[k][e], x[k][e], dw[k][e]);
                     db[k][e] = add2(q[k][e], db[k][e]);
                 }
-                q[k][e] = mul2(q[k][e], w[kk][e]);
+                q[k][e] = mul2(q[k][e], weights.w[wk][e]);
                 m1 = add2(m1, q[k][e]);
                 m2 = fma2(q[k][e], x[k][e], m2);
             }
         }
-        s[0] = sum2(m1);
-        s[1] = sum2(m2);
+        float s[2] = {sum2(m1), sum2(m2)};
         sum(s);
+        if (i >= mine) continue;
         const f2 n1 = both(-s[0] * inv_n), n2 = both(-s[1] * inv_n);
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            if (!(here && at.has(k))) continue;
             f2 dx[N2];
 #pragma unroll
             for (int e = 0; e < N2; ++e) dx[e] = mul2(rstd, fma2(x[k][e], n2, add2(q[k][e], n1)));
-            Row<TG, VEC> out;
+            Row<TG, V::VEC> out;
             out.from(dx);
-            out.store(to + at.channel(k));
+            if (at.has(k)) out.store(to + at.channel(k));
         }
     }
     tc::grid_dep_launch();
     if (!p.dweight && !p.dbias) return;
-    // the block's rows side by side first (where the last rows were on their way)
+    // the block's rows side by side first
     copies_wait<0>();
-    const int row_threads = t.groups * t.lanes;  // threads of one row
+    f2* const join = reinterpret_cast<f2*>(shared);
+    const int row_threads = t.groups * at.lanes;  // threads of one row
 #pragma unroll
     for (int v = 0; v < 2; ++v) {
-        float* const to = partial + ((int64_t)blockIdx.y * 2 + v) * p.C;
+        float* const out = partial + ((int64_t)blockIdx.y * 2 + v) * p.C;
 #pragma unroll
         for (int k = 0; k < R; ++k) {
             f2 total[N2];
@@ -346,17 +364,17 @@ __global__ void __launch_bounds__(NTH, kResidentBwd<NTH, R * VEC>) norm_token_bw
                     for (int r = 1; r < t.rows; ++r)
 #pragma unroll
                         for (int e = 0; e < N2; ++e) {
-                            const int from = threadIdx.x + r * row_threads;
-                            total[e] = add2(total[e], kShared ? as_pair(sums_at(k, e, v, from)) : join[from * N2 + e]);
+                            const int other = threadIdx.x + r * row_threads;
+                            total[e] = add2(total[e], kShared ? as_pair(sums_at(k, e, v, other)) : join[other * N2 + e]);
                         }
             }
             if (at.rsub == 0 && at.has(k)) {
 #pragma unroll
                 for (int e = 0; e < N2; ++e) {
-                    float a, b;
-                    unpack(total[e], a, b);
-                    to[at.channel(k) + 2 * e] = a;
-                    if (2 * e + 1 < VEC) to[at.channel(k) + 2 * e + 1] = b;
+                    float lo, hi;
+                    unpack(total[e], lo, hi);
+                    out[at.channel(k) + 2 * e] = lo;
+                    if (2 * e + 1 < V::VEC) out[at.channel(k) + 2 * e + 1] = hi;
                 }
             }
         }
@@ -368,13 +386,13 @@ int pow2_at_least(int n) {
     while (k < n) k *= 2;
     return k;
 }
-// Teams for groups of `pieces` pieces, R of them a lane, in blocks of nth threads.
-Teams teams_of(int pieces, int R, int G, int nth) {
+template <typename V>
+Teams teams_of(int pieces, int G) {
     Teams t;
-    t.lanes = pow2_at_least((pieces + R - 1) / R);
+    t.lanes = pow2_at_least((pieces + V::R - 1) / V::R);
     t.groups = pow2_at_least(G);
-    if (t.groups > nth / t.lanes) t.groups = nth / t.lanes;
-    t.rows = nth / t.lanes / t.groups;
+    if (t.groups > V::NTH / t.lanes) t.groups = V::NTH / t.lanes;
+    t.rows = V::NTH / t.lanes / t.groups;
     return t;
 }
 // Blocks along the rows: no more than the rows need, about `resident` an SM in all.
@@ -388,56 +406,57 @@ dim3 grid_of(const NormParams& p, const Teams& t, int resident) {
     return dim3(x, (unsigned)y);
 }
 
-// ---- which variant: pieces a lane, threads a block ------------------------------------------
-
-// f(R, NTH as constants) for groups of `pieces` pieces of VEC elements.
-template <int N>
-struct Int {
-    static constexpr int value = N;
-};
+// f(a variant) for groups of `pieces` pieces of VEC elements: a warp has up to 128 pieces, a block of 256 threads up to 1024 (4096
+// single elements), one of 1024 the rest.
 template <int VEC, typename F>
-auto pick_variant(int pieces, F f) {
+auto pick_variant(int pieces, int G, F f) {
     if constexpr (VEC >= 4) {
-        if (pieces <= 32) return f(Int<1>{}, Int<256>{});
-        if (pieces <= 512) return f(Int<2>{}, Int<256>{});
-        return f(Int<VEC == 4 ? 4 : 2>{}, Int<1024>{});
+        // teams that are filled need no tests
+        if (pieces == 16 && G % 16 == 0) return f(Variant<VEC, 1, 256, 16>{});
+        if (pieces == 32 && G % 8 == 0) return f(Variant<VEC, 1, 256, 32>{});
+        if (pieces == 8 && G % 32 == 0) return f(Variant<VEC, 1, 256, 8>{});
+        if (pieces <= 32) return f(Variant<VEC, 1, 256, 0>{});
+        if (pieces <= 64) return f(Variant<VEC, 2, 256, 0>{});
+        if (pieces <= 1024) return f(Variant<VEC, 4, 256, 0>{});
+        return f(Variant<VEC, VEC == 4 ? 4 : 2, 1024, 0>{});
     } else {
-        if (pieces <= 32) return f(Int<1>{}, Int<256>{});
-        if (pieces <= 1024) return f(Int<4>{}, Int<256>{});
-        return f(Int<16>{}, Int<1024>{});
+        if (pieces <= 32) return f(Variant<1, 1, 256, 0>{});
+        if (pieces <= 1024) return f(Variant<1, 4, 256, 0>{});
+        if (pieces <= 4096) return f(Variant<1, 16, 256, 0>{});
+        return f(Variant<1, 16, 1024, 0>{});
     }
 }
-constexpr int resident_fwd(int nth) { return nth == 256 ? 4 : 1; }
 
 template <typename T, int VEC>
 cudaError_t launch_fwd(const NormParams& p, cudaStream_t st) {
     const int pieces = p.C / p.G / VEC;
-    return pick_variant<VEC>(pieces, [&](auto r, auto nth) {
-        constexpr int R = decltype(r)::value, NTH = decltype(nth)::value;
-        const auto kern = norm_token_fwd_kernel<T, VEC, R, NTH>;
-        constexpr int smem = Ring<T, VEC, R, NTH>::kBytes;
+    return pick_variant<VEC>(pieces, p.G, [&](auto variant) {
+        using V = decltype(variant);
+        const auto kern = norm_token_fwd_kernel<T, V>;
+        constexpr int smem = Ring<V, T>::kBytes;
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
-        const Teams t = teams_of(pieces, R, p.G, NTH);
-        kern<<<grid_of(p, t, resident_fwd(NTH)), NTH, smem, st>>>(p, t);
+        const Teams t = teams_of<V>(pieces, p.G);
+        kern<<<grid_of(p, t, V::kFwd), V::NTH, smem, st>>>(p, t);
         return cudaGetLastError();
     });
 }
 template <typename T, typename TG, int VEC>
 cudaError_t launch_bwd(const NormParams& p, cudaStream_t st) {
     const int pieces = p.C / p.G / VEC;
-    return pick_variant<VEC>(pieces, [&](auto r, auto nth) {
-        constexpr int R = decltype(r)::value, NTH = decltype(nth)::value;
-        const auto kern = norm_token_bwd_kernel<T, TG, VEC, R, NTH>;
-        constexpr int rings = Ring<T, VEC, R, NTH>::kBytes + Ring<TG, VEC, R, NTH>::kBytes;
-        constexpr int joins = NTH == 256 ? NTH * ((VEC + 1) / 2) * 8 : NTH * R * VEC * 8;
-        constexpr int smem = rings > joins ? rings : joins;
+    return pick_variant<VEC>(pieces, p.G, [&](auto variant) {
+        using V = decltype(variant);
+        const auto kern = norm_token_bwd_kernel<T, TG, V>;
+        constexpr int rings = Ring<V, T>::kBytes + Ring<V, TG>::kBytes;
+        constexpr int sums = V::kSharedSums ? V::NTH * V::E * 8 : V::NTH * V::N2 * 8;
+        static_assert(!V::kSharedSums || rings == 0, "the sums have the place");
+        constexpr int smem = rings > sums ? rings : sums;
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
-        const Teams t = teams_of(pieces, R, p.G, NTH);
-        const dim3 grid = grid_of(p, t, kResidentBwd<NTH, R * VEC>);
+        const Teams t = teams_of<V>(pieces, p.G);
+        const dim3 grid = grid_of(p, t, V::kBwd);
         float* const partial = static_cast<float*>(p.ws);
-        kern<<<grid, NTH, smem, st>>>(p, t, partial);
+        kern<<<grid, V::NTH, smem, st>>>(p, t, partial);
         e = cudaGetLastError();
         if (e != cudaSuccess || (!p.dweight && !p.dbias)) return e;
         return tc::launch_dependent(norm_weights_kernel, (unsigned)((p.C + 31) / 32), 256, 0, st, (const float*)partial, (int)grid.y, p.C, p.dweight,
@@ -456,21 +475,19 @@ cudaError_t norm_token_fwd(kda_dtype dt, const NormParams& p, cudaStream_t st) {
 }
 
 // The most blocks along the rows of the variants that p's channels allow (which one runs depends on the alignment).
-size_t norm_token_bwd_workspace(const NormParams& p) {
+template <int VEC>
+size_t most_rows(const NormParams& p) {
     const int cg = p.C / p.G;
-    size_t most = 0;
-    auto look = [&](auto vec) {
-        constexpr int VEC = decltype(vec)::value;
-        if (cg % VEC != 0) return;
-        const size_t y = pick_variant<VEC>(cg / VEC, [&](auto r, auto nth) {
-            constexpr int R = decltype(r)::value, NTH = decltype(nth)::value;
-            return (size_t)grid_of(p, teams_of(cg / VEC, R, p.G, NTH), kResidentBwd<NTH, R * VEC>).y;
-        });
-        if (y > most) most = y;
-    };
-    look(Int<8>{});
-    look(Int<4>{});
-    look(Int<1>{});
+    if (cg % VEC != 0) return 0;
+    return pick_variant<VEC>(cg / VEC, p.G, [&](auto variant) {
+        using V = decltype(variant);
+        return (size_t)grid_of(p, teams_of<V>(cg / VEC, p.G), V::kBwd).y;
+    });
+}
+size_t norm_token_bwd_workspace(const NormParams& p) {
+    size_t most = most_rows<1>(p);
+    for (size_t n : {most_rows<8>(p), most_rows<4>(p)})
+        if (n > most) most = n;
     return most * 2 * p.C * 4;
 }
 
