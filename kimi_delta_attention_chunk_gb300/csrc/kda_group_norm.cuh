@@ -4,22 +4,13 @@
 //     dp = dy act'(p),  q = w dp,  xh = (x - mean) rstd:  dx = rstd (q - mean(q) - xh mean(q xh)),  dw = sum dp xh,  db = sum dp
 #pragma once
 
+#include "kda_clusters.cuh"
 #include "kda_layer.h"
-#include "kda_segments.cuh"
 #include "kda_tc.cuh"
 
 namespace kda {
 
-constexpr int kSms = 152;
-
-__device__ __forceinline__ f2 both(float v) { return pack(v, v); }
-__device__ __forceinline__ f2 neg2(f2 x) { return x ^ 0x8000000080000000ull; }
-// 1 / (1 + e^-x) of a pair, packed but for the special functions; x times it; and the slope of that, s + p s (1 - s).
-__device__ __forceinline__ f2 gate2(f2 x) {
-    float a, b;
-    unpack(add2(ex2_2(mul2(x, both(-kLog2e))), both(1.f)), a, b);
-    return pack(rcp(a), rcp(b));
-}
+// x / (1 + e^-x), and the slope of that, s + x s (1 - s).
 __device__ __forceinline__ f2 silu2(f2 p) { return mul2(p, gate2(p)); }
 __device__ __forceinline__ f2 silu_slope2(f2 p) {
     const f2 s = gate2(p);

@@ -15,18 +15,18 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kPieces = 32;                   // row pieces of a block, side by side
 constexpr int kSubs = kThreads / kPieces;     // rows of a block at a time
-constexpr int kAhead = 4;                     // rows of a thread requested together
+constexpr int kBatches = 3;                   // batches of a thread's rows under way, the one at hand among them
 
 struct Cut {
     int run, runs;
 };
-// Runs of tokens: about `resident` blocks an SM, 64 tokens at least.
+// Runs of tokens, whole batches: one filling of the machine by `resident` blocks an SM, 64 tokens at least.
 Cut cut_of(const NormParams& p, int blocks, int resident) {
     Cut q;
     int want = kSms * resident / blocks;
     if (want < 1) want = 1;
     q.run = p.total / want + (p.total % want != 0);
-    q.run = (q.run + 63) / 64 * 64;
+    q.run = (q.run + 31) / 32 * 32;
     if (q.run < 64) q.run = 64;
     q.runs = p.total / q.run + (p.total % q.run != 0);
     if (q.runs < 1) q.runs = 1;
@@ -74,6 +74,44 @@ __device__ __forceinline__ void store_sums(const ChannelSums<VEC>& s, f2 (*join)
     }
 }
 
+// A thread's own pieces of batches of ROWS rows (every kSubs-th token), on their way through shared memory: what a thread asks for it
+// alone reads, so that no thread waits for another.  (Two-byte pieces have no asynchronous copy: they are loaded when asked for.)
+template <typename T, int VEC, int ROWS>
+struct Ring {
+    static constexpr int kBytes = kBatches * ROWS * kThreads * VEC * (int)sizeof(T);
+    T* mine;
+    __device__ __forceinline__ explicit Ring(void* shared) : mine(static_cast<T*>(shared) + threadIdx.x * VEC) {}
+    __device__ __forceinline__ T* at(int batch, int j) const { return mine + ((batch % kBatches) * ROWS + j) * kThreads * VEC; }
+    // `left` rows are there from `from` on, ld apart.
+    __device__ __forceinline__ void request(int batch, int left, const T* from, int64_t ld) const {
+#pragma unroll
+        for (int j = 0; j < ROWS; ++j, from += kSubs * ld)
+            if (j * kSubs < left) Row<T, VEC>::copy_async(at(batch, j), from);
+    }
+    __device__ __forceinline__ void take(int batch, int j, f2 (&v)[(VEC + 1) / 2]) const {
+        Row<T, VEC> r;
+        r.from_shared(at(batch, j));
+        r.to(v);
+    }
+};
+// Walks a thread's rows b + sub, + kSubs ... before e: request(batch, first token of it) asks for a batch, f(batch, first token) has it.
+template <int ROWS, typename Q, typename F>
+__device__ __forceinline__ void each_batch(int b, int e, Q request, F f) {
+    constexpr int STEP = ROWS * kSubs;
+#pragma unroll
+    for (int i = 0; i < kBatches - 1; ++i) {
+        if (b + i * STEP < e) request(i, b + i * STEP);
+        copies_commit();
+    }
+    int i = 0;
+    for (int t = b; t < e; t += STEP, ++i) {
+        copies_wait<kBatches - 2>();
+        f(i, t);
+        if (t + (kBatches - 1) * STEP < e) request(i + kBatches - 1, t + (kBatches - 1) * STEP);
+        copies_commit();
+    }
+}
+
 // n, mean and sum of squares around it, joined with those of nb more values (the same counts in both halves).
 struct Moments {
     f2 mean, m2;
@@ -87,9 +125,12 @@ struct Moments {
 
 // Per piece and channel the mean and the sum of squares around it: pieces[run + n][2][C].
 template <typename T, int VEC>
-__global__ void __launch_bounds__(kThreads) seq_moments_kernel(NormParams p, SeqMap m, int run, float* pieces) {
+__global__ void __launch_bounds__(kThreads, 3) seq_moments_kernel(NormParams p, SeqMap m, int run, float* pieces) {
     constexpr int N2 = (VEC + 1) / 2;
+    constexpr int ROWS = 4;
+    extern __shared__ __align__(16) char shared[];
     __shared__ Moments join[N2][kThreads];
+    const Ring<T, VEC, ROWS> ring(shared);
     const int piece = threadIdx.x % kPieces, sub = threadIdx.x / kPieces, c = (blockIdx.x * kPieces + piece) * VEC;
     const bool on = c < p.C;
     const int r0 = blockIdx.y * run, r1 = (int)min((int64_t)m.total, (int64_t)r0 + run);
@@ -99,57 +140,61 @@ __global__ void __launch_bounds__(kThreads) seq_moments_kernel(NormParams p, Seq
 #pragma unroll
         for (int i = 0; i < N2; ++i) mine[i] = Moments{0ull, 0ull};
         float seen = 0.f;
-        for (int t = b + sub; t < e; t += kSubs * kAhead) {
-            Row<T, VEC> rows[kAhead];
+        each_batch<ROWS>(b + sub, e, [&](int batch, int t) { ring.request(batch, e - t, x + t * p.ldx, p.ldx); }, [&](int batch, int t) {
+            const int have = min(ROWS, (e - t + kSubs - 1) / kSubs);
+            const float inv = have == ROWS ? 1.f / ROWS : 1.f / (float)have;
+            f2 v[ROWS][N2];
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j)
-                if (t + j * kSubs < e) rows[j].load(x + (int64_t)(t + j * kSubs) * p.ldx);
-            const int have = min(kAhead, (e - t + kSubs - 1) / kSubs);
-            const float inv = have == kAhead ? 1.f / kAhead : 1.f / (float)have;
-            f2 v[kAhead][N2];
-#pragma unroll
-            for (int j = 0; j < kAhead; ++j) {
-                if (j >= have) rows[j] = rows[0];  // (counts for nothing)
-                rows[j].to(v[j]);
-            }
+            for (int j = 0; j < ROWS; ++j) ring.take(batch, j < have ? j : 0, v[j]);
 #pragma unroll
             for (int i = 0; i < N2; ++i) {
                 Moments few{0ull, 0ull};
+                if (have == ROWS) {
+                    few.mean = mul2(add2(add2(v[0][i], v[1][i]), add2(v[2][i], v[3][i])), both(inv));
 #pragma unroll
-                for (int j = 0; j < kAhead; ++j)
-                    if (j < have) few.mean = add2(few.mean, v[j][i]);
-                few.mean = mul2(few.mean, both(inv));
+                    for (int j = 0; j < ROWS; ++j) {
+                        const f2 d = add2(v[j][i], neg2(few.mean));
+                        few.m2 = fma2(d, d, few.m2);
+                    }
+                } else {
 #pragma unroll
-                for (int j = 0; j < kAhead; ++j) {
-                    const f2 d = add2(v[j][i], neg2(few.mean));
-                    if (j < have) few.m2 = fma2(d, d, few.m2);
+                    for (int j = 0; j < ROWS; ++j)
+                        if (j < have) few.mean = add2(few.mean, v[j][i]);
+                    few.mean = mul2(few.mean, both(inv));
+#pragma unroll
+                    for (int j = 0; j < ROWS; ++j) {
+                        const f2 d = add2(v[j][i], neg2(few.mean));
+                        if (j < have) few.m2 = fma2(d, d, few.m2);
+                    }
                 }
                 mine[i].join(seen, (float)have, few);
             }
             seen += (float)have;
-        }
+        });
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < N2; ++i) join[i][threadIdx.x] = mine[i];
         __syncthreads();
-        if (threadIdx.x >= kPieces || !on) return;
-        float* const to = pieces + (int64_t)(blockIdx.y + n) * 2 * p.C + c;
-        for (int r = 1; r < kSubs && b + r < e; ++r) {
-            const float more = (float)((e - b - r + kSubs - 1) / kSubs);
-#pragma unroll
-            for (int i = 0; i < N2; ++i) mine[i].join(seen, more, join[i][threadIdx.x + r * kPieces]);
-            seen += more;
-        }
-#pragma unroll
-        for (int i = 0; i < N2; ++i) {
+        // a thread joins the rows of a pair of channels
+        float* const to = pieces + (int64_t)(blockIdx.y + n) * 2 * p.C + blockIdx.x * kPieces * VEC;
+        for (int k = threadIdx.x; k < kPieces * N2; k += kThreads) {
+            const int i = k / kPieces, pc = k % kPieces, at = pc * VEC + 2 * i;
+            if (blockIdx.x * kPieces * VEC + pc * VEC >= p.C) continue;
+            Moments all = join[i][pc];
+            float count = (float)((e - b + kSubs - 1) / kSubs);
+            for (int r = 1; r < kSubs && b + r < e; ++r) {
+                const float more = (float)((e - b - r + kSubs - 1) / kSubs);
+                all.join(count, more, join[i][pc + r * kPieces]);
+                count += more;
+            }
             float x0, x1, q0, q1;
-            unpack(mine[i].mean, x0, x1);
-            unpack(mine[i].m2, q0, q1);
-            to[2 * i] = x0;
-            to[p.C + 2 * i] = q0;
+            unpack(all.mean, x0, x1);
+            unpack(all.m2, q0, q1);
+            to[at] = x0;
+            to[p.C + at] = q0;
             if (2 * i + 1 < VEC) {
-                to[2 * i + 1] = x1;
-                to[p.C + 2 * i + 1] = q1;
+                to[at + 1] = x1;
+                to[p.C + at + 1] = q1;
             }
         }
     });
@@ -183,27 +228,51 @@ struct PieceRange {
 
 // mean and 1 / deviation of every sequence and group from the pieces: stats [N][G][2], a block each in turn.
 __global__ void __launch_bounds__(128) seq_stats_kernel(NormParams p, SeqMap m, int run, const float* pieces, float* stats) {
+    constexpr int kKept = 8;  // pairs of a piece's mean and squares that a thread keeps between the two sums
     __shared__ float buf[4];
     const int cg = p.C / p.G;
     tc::grid_dep_wait();
     for (int64_t i = blockIdx.x; i < (int64_t)p.N * p.G; i += gridDim.x) {
-        const int n = (int)(i / p.G), g = (int)(i % p.G);
+        const int n = (int)(i / p.G), g = (int)(i - (int64_t)n * p.G);
         const PieceRange r(m, n, run);
         if (r.count == 0) {
             if (threadIdx.x == 0) stats[2 * i] = 0.f, stats[2 * i + 1] = rsqrtf(p.eps);
             continue;
         }
         const float* const at = pieces + g * cg;
-        const int64_t all = (int64_t)r.count * cg;
+        const int all = r.count * cg;
         const float inv = 1.f / ((float)(r.e - r.b) * (float)cg);
-        float s = 0.f, q = 0.f;
-        for (int64_t k = threadIdx.x; k < all; k += blockDim.x)
-            s = fmaf((float)r.tokens((int)(k / cg)), at[r.place((int)(k / cg)) * 2 * p.C + k % cg], s);
+        auto entry = [&](int k, float& tokens, float& mean, float& m2) {
+            const int piece = k / cg;
+            const float* const x = at + r.place(piece) * 2 * p.C + (k - piece * cg);
+            tokens = (float)r.tokens(piece);
+            mean = x[0];
+            m2 = x[p.C];
+        };
+        float tk[kKept], mk[kKept], qk[kKept], s = 0.f, q = 0.f;
+#pragma unroll
+        for (int j = 0; j < kKept; ++j) {
+            const int k = threadIdx.x + j * 128;
+            if (k < all) entry(k, tk[j], mk[j], qk[j]);
+            else tk[j] = mk[j] = qk[j] = 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < kKept; ++j) s = fmaf(tk[j], mk[j], s);
+        for (int k = threadIdx.x + kKept * 128; k < all; k += 128) {
+            float t, x, m2;
+            entry(k, t, x, m2);
+            s = fmaf(t, x, s);
+        }
         const float mean = block_sum(s, buf) * inv;
-        for (int64_t k = threadIdx.x; k < all; k += blockDim.x) {
-            const float* const x = at + r.place((int)(k / cg)) * 2 * p.C + k % cg;
-            const float d = x[0] - mean;
-            q += fmaf((float)r.tokens((int)(k / cg)) * d, d, x[p.C]);
+#pragma unroll
+        for (int j = 0; j < kKept; ++j) {
+            const float d = mk[j] - mean;
+            q += fmaf(tk[j] * d, d, qk[j]);
+        }
+        for (int k = threadIdx.x + kKept * 128; k < all; k += 128) {
+            float t, x, m2;
+            entry(k, t, x, m2);
+            q += fmaf(t * (x - mean), x - mean, m2);
         }
         const float var = block_sum(q, buf) * inv;
         if (threadIdx.x == 0) stats[2 * i] = mean, stats[2 * i + 1] = rsqrtf(var + p.eps);
@@ -225,8 +294,10 @@ __device__ __forceinline__ void stats_of(const NormParams& p, const float* stats
 }
 
 template <typename T, int VEC>
-__global__ void __launch_bounds__(kThreads) seq_apply_kernel(NormParams p, SeqMap m, int run, const float* stats) {
-    constexpr int N2 = (VEC + 1) / 2;
+__global__ void __launch_bounds__(kThreads, 3) seq_apply_kernel(NormParams p, SeqMap m, int run, const float* stats) {
+    constexpr int N2 = (VEC + 1) / 2, ROWS = 4;
+    extern __shared__ __align__(16) char shared[];
+    const Ring<T, VEC, ROWS> ring(shared);
     const int piece = threadIdx.x % kPieces, sub = threadIdx.x / kPieces, c = (blockIdx.x * kPieces + piece) * VEC;
     const bool on = c < p.C;
     // the last runs first: they were read last
@@ -241,32 +312,35 @@ __global__ void __launch_bounds__(kThreads) seq_apply_kernel(NormParams p, SeqMa
         stats_of<VEC>(p, stats, n, c, mean, scale);
 #pragma unroll
         for (int i = 0; i < N2; ++i) scale[i] = mul2(scale[i], w[i]);
-        for (int t = b + sub; t < e; t += kSubs * kAhead) {
-            Row<T, VEC> rows[kAhead];
+        const T* const x = static_cast<const T*>(p.x) + c;
+        each_batch<ROWS>(b + sub, e, [&](int batch, int t) { ring.request(batch, e - t, x + t * p.ldx, p.ldx); }, [&](int batch, int t) {
+            T* to = static_cast<T*>(p.y) + (int64_t)t * p.C + c;
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j)
-                if (t + j * kSubs < e) rows[j].load(static_cast<const T*>(p.x) + (int64_t)(t + j * kSubs) * p.ldx + c);
-#pragma unroll
-            for (int j = 0; j < kAhead; ++j) {
+            for (int j = 0; j < ROWS; ++j, to += (int64_t)kSubs * p.C) {
                 if (t + j * kSubs >= e) break;
                 f2 v[N2];
-                rows[j].to(v);
+                ring.take(batch, j, v);
 #pragma unroll
-                for (int i = 0; i < N2; ++i) {
-                    v[i] = fma2(add2(v[i], mean[i]), scale[i], bias[i]);
-                    if (p.act) v[i] = silu2(v[i]);
+                for (int i = 0; i < N2; ++i) v[i] = fma2(add2(v[i], mean[i]), scale[i], bias[i]);
+                if (p.act) {
+#pragma unroll
+                    for (int i = 0; i < N2; ++i) v[i] = silu2(v[i]);
                 }
-                rows[j].from(v);
-                rows[j].store(static_cast<T*>(p.y) + (int64_t)(t + j * kSubs) * p.C + c);
+                Row<T, VEC> out;
+                out.from(v);
+                out.store(to);
             }
-        }
+        });
     });
 }
 
 // Per piece and channel sum dp xh and sum dp, and the same per run: pieces[run + n][2][C], per_run[run][2][C].
 template <typename T, typename TG, int VEC>
-__global__ void __launch_bounds__(kThreads) seq_grads_kernel(NormParams p, SeqMap m, int run, const float* stats, float* pieces, float* per_run) {
-    constexpr int N2 = (VEC + 1) / 2;
+__global__ void __launch_bounds__(kThreads, 2) seq_grads_kernel(NormParams p, SeqMap m, int run, const float* stats, float* pieces, float* per_run) {
+    constexpr int N2 = (VEC + 1) / 2, ROWS = 2;
+    extern __shared__ __align__(16) char shared[];
+    const Ring<T, VEC, ROWS> ring(shared);
+    const Ring<TG, VEC, ROWS> ring_dy(shared + ring.kBytes);
     __shared__ f2 join[N2][kThreads];
     const int piece = threadIdx.x % kPieces, sub = threadIdx.x / kPieces, c = (blockIdx.x * kPieces + piece) * VEC;
     const bool on = c < p.C;
@@ -285,30 +359,31 @@ __global__ void __launch_bounds__(kThreads) seq_grads_kernel(NormParams p, SeqMa
         ChannelSums<VEC> s;
 #pragma unroll
         for (int i = 0; i < N2; ++i) s.a[i] = s.b[i] = 0ull;
-        for (int t = b + sub; t < e; t += kSubs * kAhead) {
-            Row<T, VEC> rows[kAhead];
-            Row<TG, VEC> grads[kAhead];
+        const T* const x = static_cast<const T*>(p.x) + cc;
+        const TG* const dy = static_cast<const TG*>(p.dy) + cc;
+        each_batch<ROWS>(b + sub, e, [&](int batch, int t) {
+            ring.request(batch, e - t, x + t * p.ldx, p.ldx);
+            ring_dy.request(batch, e - t, dy + (int64_t)t * p.C, p.C);
+        }, [&](int batch, int t) {
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j)
-                if (t + j * kSubs < e) {
-                    rows[j].load(static_cast<const T*>(p.x) + (int64_t)(t + j * kSubs) * p.ldx + cc);
-                    grads[j].load(static_cast<const TG*>(p.dy) + (int64_t)(t + j * kSubs) * p.C + cc);
-                }
-#pragma unroll
-            for (int j = 0; j < kAhead; ++j) {
+            for (int j = 0; j < ROWS; ++j) {
                 if (t + j * kSubs >= e) break;
                 f2 v[N2], g[N2];
-                rows[j].to(v);
-                grads[j].to(g);
+                ring.take(batch, j, v);
+                ring_dy.take(batch, j, g);
+#pragma unroll
+                for (int i = 0; i < N2; ++i) v[i] = mul2(add2(v[i], mean[i]), rstd[i]);
+                if (p.act) {
+#pragma unroll
+                    for (int i = 0; i < N2; ++i) g[i] = mul2(g[i], silu_slope2(fma2(v[i], w[i], bias[i])));
+                }
 #pragma unroll
                 for (int i = 0; i < N2; ++i) {
-                    const f2 xh = mul2(add2(v[i], mean[i]), rstd[i]);
-                    if (p.act) g[i] = mul2(g[i], silu_slope2(fma2(xh, w[i], bias[i])));
-                    s.a[i] = fma2(g[i], xh, s.a[i]);
+                    s.a[i] = fma2(g[i], v[i], s.a[i]);
                     s.b[i] = add2(s.b[i], g[i]);
                 }
             }
-        }
+        });
 #pragma unroll
         for (int i = 0; i < N2; ++i) {
             all.a[i] = add2(all.a[i], s.a[i]);
@@ -332,14 +407,16 @@ __global__ void __launch_bounds__(256) seq_means_kernel(NormParams p, SeqMap m, 
     }
     const int cg = p.C / p.G;
     for (int64_t i = blockIdx.x - weight_blocks; i < (int64_t)p.N * p.G; i += gridDim.x - weight_blocks) {
-        const int n = (int)(i / p.G), g = (int)(i % p.G);
+        const int n = (int)(i / p.G), g = (int)(i - (int64_t)n * p.G);
         const PieceRange r(m, n, run);
         const float* const at = pieces + g * cg;
-        const int64_t all = (int64_t)r.count * cg;
+        const int all = r.count * cg;
         float a = 0.f, b = 0.f;
-        for (int64_t k = threadIdx.x; k < all; k += blockDim.x) {
-            const float* const x = at + r.place((int)(k / cg)) * 2 * p.C + k % cg;
-            const float w = p.weight ? __ldg(p.weight + g * cg + k % cg) : 1.f;
+#pragma unroll 4
+        for (int k = threadIdx.x; k < all; k += 256) {
+            const int piece = k / cg, ch = k - piece * cg;
+            const float* const x = at + r.place(piece) * 2 * p.C + ch;
+            const float w = p.weight ? __ldg(p.weight + g * cg + ch) : 1.f;
             a = fmaf(w, x[0], a);
             b = fmaf(w, x[p.C], b);
         }
@@ -352,8 +429,11 @@ __global__ void __launch_bounds__(256) seq_means_kernel(NormParams p, SeqMap m, 
 }
 
 template <typename T, typename TG, int VEC>
-__global__ void __launch_bounds__(kThreads) seq_dx_kernel(NormParams p, SeqMap m, int run, const float* stats, const float* means) {
-    constexpr int N2 = (VEC + 1) / 2;
+__global__ void __launch_bounds__(kThreads, 2) seq_dx_kernel(NormParams p, SeqMap m, int run, const float* stats, const float* means) {
+    constexpr int N2 = (VEC + 1) / 2, ROWS = 2;
+    extern __shared__ __align__(16) char shared[];
+    const Ring<T, VEC, ROWS> ring(shared);
+    const Ring<TG, VEC, ROWS> ring_dy(shared + ring.kBytes);
     const int piece = threadIdx.x % kPieces, sub = threadIdx.x / kPieces, c = (blockIdx.x * kPieces + piece) * VEC;
     const bool on = c < p.C;
     const int r0 = (gridDim.y - 1 - blockIdx.y) * run, r1 = (int)min((int64_t)m.total, (int64_t)r0 + run);
@@ -373,70 +453,77 @@ __global__ void __launch_bounds__(kThreads) seq_dx_kernel(NormParams p, SeqMap m
         f2 mean[N2], rstd[N2], mqx[N2], mq[N2];
         stats_of<VEC>(p, stats, n, c, mean, rstd);
         stats_of<VEC>(p, means, n, c, mqx, mq);  // -mean(q xh), mean(q)
-        for (int t = b + sub; t < e; t += kSubs * kAhead) {
-            Row<T, VEC> rows[kAhead];
-            Row<TG, VEC> grads[kAhead];
+        const T* const x = static_cast<const T*>(p.x) + c;
+        const TG* const dy = static_cast<const TG*>(p.dy) + c;
+        each_batch<ROWS>(b + sub, e, [&](int batch, int t) {
+            ring.request(batch, e - t, x + t * p.ldx, p.ldx);
+            ring_dy.request(batch, e - t, dy + (int64_t)t * p.C, p.C);
+        }, [&](int batch, int t) {
+            TG* to = static_cast<TG*>(p.dx) + (int64_t)t * p.C + c;
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j)
-                if (t + j * kSubs < e) {
-                    rows[j].load(static_cast<const T*>(p.x) + (int64_t)(t + j * kSubs) * p.ldx + c);
-                    grads[j].load(static_cast<const TG*>(p.dy) + (int64_t)(t + j * kSubs) * p.C + c);
-                }
-#pragma unroll
-            for (int j = 0; j < kAhead; ++j) {
+            for (int j = 0; j < ROWS; ++j, to += (int64_t)kSubs * p.C) {
                 if (t + j * kSubs >= e) break;
                 f2 v[N2], g[N2];
-                rows[j].to(v);
-                grads[j].to(g);
+                ring.take(batch, j, v);
+                ring_dy.take(batch, j, g);
 #pragma unroll
-                for (int i = 0; i < N2; ++i) {
-                    const f2 xh = mul2(add2(v[i], mean[i]), rstd[i]);
-                    if (p.act) g[i] = mul2(g[i], silu_slope2(fma2(xh, w[i], bias[i])));
-                    g[i] = mul2(rstd[i], fma2(xh, mqx[i], fma2(g[i], w[i], neg2(mq[i]))));
+                for (int i = 0; i < N2; ++i) v[i] = mul2(add2(v[i], mean[i]), rstd[i]);
+                if (p.act) {
+#pragma unroll
+                    for (int i = 0; i < N2; ++i) g[i] = mul2(g[i], silu_slope2(fma2(v[i], w[i], bias[i])));
                 }
-                grads[j].from(g);
-                grads[j].store(static_cast<TG*>(p.dx) + (int64_t)(t + j * kSubs) * p.C + c);
+#pragma unroll
+                for (int i = 0; i < N2; ++i) g[i] = mul2(rstd[i], fma2(v[i], mqx[i], fma2(g[i], w[i], neg2(mq[i]))));
+                Row<TG, VEC> out;
+                out.from(g);
+                out.store(to);
             }
-        }
+        });
     });
 }
 
 // ---- launches -------------------------------------------------------------------------------------------
 
-constexpr int kResident = 4;
+constexpr int kFwdResident = 3, kBwdResident = 2;
 int blocks_of(const NormParams& p, int vec) { return (p.C + kPieces * vec - 1) / (kPieces * vec); }
 int64_t groups_grid(const NormParams& p) {
     const int64_t n = (int64_t)p.N * p.G;
     return n < 1 ? 1 : n < 8 * kSms ? n : 8 * kSms;
 }
 // Places of pieces at p's sizes, whichever variant runs: the wide ones have the fewest blocks and the most runs.
-int64_t most_runs(const NormParams& p) { return cut_of(p, blocks_of(p, 8), kResident).runs; }
+int64_t most_runs(const NormParams& p) { return cut_of(p, blocks_of(p, 8), kFwdResident).runs; }
 size_t pieces_bytes(const NormParams& p) { return (size_t)(((most_runs(p) + p.N) * 2 * p.C * 4 + 255) / 256 * 256); }
 size_t stats_bytes(const NormParams& p) { return (size_t)(((int64_t)p.N * p.G * 8 + 255) / 256 * 256); }
 
 template <typename T, int VEC>
 cudaError_t launch_stats(const NormParams& p, const SeqMap& m, const Cut& q, float* pieces, float* stats, cudaStream_t st) {
-    seq_moments_kernel<T, VEC><<<dim3(blocks_of(p, VEC), q.runs), kThreads, 0, st>>>(p, m, q.run, pieces);
-    const cudaError_t e = cudaGetLastError();
+    const auto kern = seq_moments_kernel<T, VEC>;
+    constexpr int smem = Ring<T, VEC, 4>::kBytes;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
+    kern<<<dim3(blocks_of(p, VEC), q.runs), kThreads, smem, st>>>(p, m, q.run, pieces);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
     return tc::launch_dependent(seq_stats_kernel, (unsigned)groups_grid(p), 128, 0, st, p, m, q.run, (const float*)pieces, stats);
 }
 
 template <typename T, int VEC>
 cudaError_t launch_fwd(const NormParams& p, cudaStream_t st) {
     const SeqMap m{p.cu, p.N, p.T, p.total};
-    const Cut q = cut_of(p, blocks_of(p, VEC), kResident);
+    const Cut q = cut_of(p, blocks_of(p, VEC), kFwdResident);
     char* const ws = static_cast<char*>(p.ws);
     float* const stats = p.stats ? p.stats : reinterpret_cast<float*>(ws + pieces_bytes(p));
-    const cudaError_t e = launch_stats<T, VEC>(p, m, q, reinterpret_cast<float*>(ws), stats, st);
+    cudaError_t e = launch_stats<T, VEC>(p, m, q, reinterpret_cast<float*>(ws), stats, st);
     if (e != cudaSuccess) return e;
-    return tc::launch_dependent(seq_apply_kernel<T, VEC>, dim3(blocks_of(p, VEC), q.runs), kThreads, 0, st, p, m, q.run, (const float*)stats);
+    const auto kern = seq_apply_kernel<T, VEC>;
+    constexpr int smem = Ring<T, VEC, 4>::kBytes;
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
+    return tc::launch_dependent(kern, dim3(blocks_of(p, VEC), q.runs), kThreads, smem, st, p, m, q.run, (const float*)stats);
 }
 
 template <typename T, typename TG, int VEC>
 cudaError_t launch_bwd(const NormParams& p, cudaStream_t st) {
     const SeqMap m{p.cu, p.N, p.T, p.total};
-    const Cut q = cut_of(p, blocks_of(p, VEC), kResident);
+    const Cut q = cut_of(p, blocks_of(p, VEC), kBwdResident);
     char* at = static_cast<char*>(p.ws);
     float* const pieces = reinterpret_cast<float*>(at);
     float* const per_run = reinterpret_cast<float*>(at += pieces_bytes(p));
@@ -448,19 +535,24 @@ cudaError_t launch_bwd(const NormParams& p, cudaStream_t st) {
         if (e != cudaSuccess) return e;
     }
     const dim3 grid(blocks_of(p, VEC), q.runs);
-    cudaError_t e;
+    const auto grads = seq_grads_kernel<T, TG, VEC>;
+    const auto dx = seq_dx_kernel<T, TG, VEC>;
+    constexpr int smem = Ring<T, VEC, 2>::kBytes + Ring<TG, VEC, 2>::kBytes;
+    cudaError_t e = cudaFuncSetAttribute(grads, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(dx, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
     if (p.stats) {  // the call's first kernel: it waits for whatever made its inputs
-        seq_grads_kernel<T, TG, VEC><<<grid, kThreads, 0, st>>>(p, m, q.run, stats, pieces, per_run);
+        grads<<<grid, kThreads, smem, st>>>(p, m, q.run, stats, pieces, per_run);
         e = cudaGetLastError();
     } else {
-        e = tc::launch_dependent(seq_grads_kernel<T, TG, VEC>, grid, kThreads, 0, st, p, m, q.run, (const float*)stats, pieces, per_run);
+        e = tc::launch_dependent(grads, grid, kThreads, smem, st, p, m, q.run, (const float*)stats, pieces, per_run);
     }
     if (e != cudaSuccess) return e;
     const int weight_blocks = p.dweight || p.dbias ? (p.C + 31) / 32 : 0;
     e = tc::launch_dependent(seq_means_kernel, (unsigned)(weight_blocks + groups_grid(p)), 256, 0, st, p, m, q.run, q.runs, (const float*)pieces,
                              (const float*)per_run, weight_blocks, means);
     if (e != cudaSuccess) return e;
-    return tc::launch_dependent(seq_dx_kernel<T, TG, VEC>, grid, kThreads, 0, st, p, m, q.run, (const float*)stats, (const float*)means);
+    return tc::launch_dependent(dx, grid, kThreads, smem, st, p, m, q.run, (const float*)stats, (const float*)means);
 }
 
 }  // namespace
@@ -476,8 +568,10 @@ cudaError_t group_norm_fwd(kda_dtype dt, const NormParams& p, cudaStream_t st) {
     using kda_host::rows_aligned;
     const int vec = dt == KDA_BF16 ? 8 : 4;
     const bool wide = p.C % vec == 0 && rows_aligned(p.x, p.ldx, vec) && rows_aligned(p.y, p.C, vec);
-    if (dt == KDA_BF16) return wide ? launch_fwd<__nv_bfloat16, 8>(p, st) : launch_fwd<__nv_bfloat16, 1>(p, st);
-    return wide ? launch_fwd<float, 4>(p, st) : launch_fwd<float, 1>(p, st);
+    const int es = dt == KDA_BF16 ? 2 : 4;
+    const bool pairs = p.C % 2 == 0 && p.ldx % 2 == 0 && (uintptr_t)p.x % (2 * es) == 0 && (uintptr_t)p.y % (2 * es) == 0;
+    if (dt == KDA_BF16) return wide ? launch_fwd<__nv_bfloat16, 8>(p, st) : pairs ? launch_fwd<__nv_bfloat16, 2>(p, st) : launch_fwd<__nv_bfloat16, 1>(p, st);
+    return wide ? launch_fwd<float, 4>(p, st) : pairs ? launch_fwd<float, 2>(p, st) : launch_fwd<float, 1>(p, st);
 }
 
 cudaError_t group_norm_bwd(kda_dtype dt, kda_dtype gdt, const NormParams& p, cudaStream_t st) {
@@ -485,9 +579,15 @@ cudaError_t group_norm_bwd(kda_dtype dt, kda_dtype gdt, const NormParams& p, cud
     using kda_host::rows_aligned;
     const int vec = dt == KDA_BF16 && gdt == KDA_BF16 ? 8 : 4;
     const bool wide = p.C % vec == 0 && rows_aligned(p.x, p.ldx, dt == KDA_BF16 ? 8 : 4) && rows_aligned(p.dy, p.C, vec) && rows_aligned(p.dx, p.C, vec);
-    if (dt == KDA_F32) return wide ? launch_bwd<float, float, 4>(p, st) : launch_bwd<float, float, 1>(p, st);
-    if (gdt == KDA_F32) return wide ? launch_bwd<__nv_bfloat16, float, 4>(p, st) : launch_bwd<__nv_bfloat16, float, 1>(p, st);
-    return wide ? launch_bwd<__nv_bfloat16, __nv_bfloat16, 8>(p, st) : launch_bwd<__nv_bfloat16, __nv_bfloat16, 1>(p, st);
+    const int es = dt == KDA_BF16 ? 2 : 4, gs = gdt == KDA_BF16 ? 2 : 4;
+    const bool pairs = p.C % 2 == 0 && p.ldx % 2 == 0 && (uintptr_t)p.x % (2 * es) == 0 && (uintptr_t)p.dy % (2 * gs) == 0 && (uintptr_t)p.dx % (2 * gs) == 0;
+    if (dt == KDA_F32) return wide ? launch_bwd<float, float, 4>(p, st) : pairs ? launch_bwd<float, float, 2>(p, st) : launch_bwd<float, float, 1>(p, st);
+    if (gdt == KDA_F32) {
+        if (wide) return launch_bwd<__nv_bfloat16, float, 4>(p, st);
+        return pairs ? launch_bwd<__nv_bfloat16, float, 2>(p, st) : launch_bwd<__nv_bfloat16, float, 1>(p, st);
+    }
+    if (wide) return launch_bwd<__nv_bfloat16, __nv_bfloat16, 8>(p, st);
+    return pairs ? launch_bwd<__nv_bfloat16, __nv_bfloat16, 2>(p, st) : launch_bwd<__nv_bfloat16, __nv_bfloat16, 1>(p, st);
 }
 
 }  // namespace kda
