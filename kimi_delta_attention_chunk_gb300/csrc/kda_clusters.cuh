@@ -78,6 +78,18 @@ __device__ __forceinline__ uint32_t address_at(unsigned rank, const void* mine) 
     return to;
 }
 
+// Lets a kernel have `bytes` of shared memory, once a device (a mark for each of 64; others every time).  48 KB need no leave.
+template <typename K>
+cudaError_t allow_shared(K kern, int bytes, std::atomic<uint64_t>& done) {
+    if (bytes <= 48 * 1024) return cudaSuccess;
+    int dev = 64;
+    cudaError_t e = cudaGetDevice(&dev);
+    const uint64_t mark = dev < 64 ? 1ull << dev : 0;
+    if (e != cudaSuccess || (done.load(std::memory_order_relaxed) & mark)) return e;
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) == cudaSuccess) done.fetch_or(mark, std::memory_order_relaxed);
+    return e;
+}
+
 // Launches a kernel (its shared memory set) in clusters of `cluster` blocks.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_clusters(void (*kern)(KArgs...), int64_t grid, int cluster, int threads, int smem, cudaStream_t st, Args... args) {

@@ -233,7 +233,8 @@ cudaError_t launch(const GatedParams& p, cudaStream_t st) {
     const auto kern = gated_fwd_kernel<T, VEC, kPacked, kRows>;
     constexpr int smem = kSmem<T, kRows>;
     static ClusterRoom room;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<uint64_t> allowed;
+    const cudaError_t e = allow_shared(kern, smem, allowed);
     if (e != cudaSuccess) return e;
     const int cluster = room.size_for(kern, groups, p.T, kTileOf<T>, kThreads, smem);
     return launch_clusters(kern, groups * cluster, cluster, kThreads, smem, st, p, cluster, blocks);

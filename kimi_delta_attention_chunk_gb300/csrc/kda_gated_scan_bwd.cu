@@ -319,7 +319,8 @@ cudaError_t launch(const GatedParams& p, cudaStream_t st) {
         const auto kern = gated_bwd_kernel<T, TG, VEC, GVEC, kPacked>;
         constexpr int smem = kStages * kStageBytes<T, TG>;
         static ClusterRoom room;
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        static std::atomic<uint64_t> allowed;
+    cudaError_t e = allow_shared(kern, smem, allowed);
         if (e != cudaSuccess) return e;
         const int cluster = room.size_for(kern, groups, p.T, kTile, kThreads, smem);
         e = launch_clusters(kern, groups * cluster, cluster, kThreads, smem, st, p, partial, cluster, blocks);

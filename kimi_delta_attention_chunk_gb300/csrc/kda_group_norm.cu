@@ -434,7 +434,8 @@ cudaError_t launch_fwd(const NormParams& p, cudaStream_t st) {
         using V = decltype(variant);
         const auto kern = norm_token_fwd_kernel<T, V>;
         constexpr int smem = Ring<V, T>::kBytes;
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        static std::atomic<uint64_t> allowed;
+    const cudaError_t e = allow_shared(kern, smem, allowed);
         if (e != cudaSuccess) return e;
         const Teams t = teams_of<V>(pieces, p.G);
         kern<<<grid_of(p, t, V::kFwd), V::NTH, smem, st>>>(p, t);
@@ -451,7 +452,8 @@ cudaError_t launch_bwd(const NormParams& p, cudaStream_t st) {
         constexpr int sums = V::kSharedSums ? V::NTH * V::E * 8 : V::NTH * V::N2 * 8;
         static_assert(!V::kSharedSums || rings == 0, "the sums have the place");
         constexpr int smem = rings > sums ? rings : sums;
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        static std::atomic<uint64_t> allowed;
+    cudaError_t e = allow_shared(kern, smem, allowed);
         if (e != cudaSuccess) return e;
         const Teams t = teams_of<V>(pieces, p.G);
         const dim3 grid = grid_of(p, t, V::kBwd);

@@ -499,7 +499,8 @@ template <typename T, int VEC>
 cudaError_t launch_stats(const NormParams& p, const SeqMap& m, const Cut& q, float* pieces, float* stats, cudaStream_t st) {
     const auto kern = seq_moments_kernel<T, VEC>;
     constexpr int smem = Ring<T, VEC, 4>::kBytes;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<uint64_t> allowed;
+    cudaError_t e = allow_shared(kern, smem, allowed);
     if (e != cudaSuccess) return e;
     kern<<<dim3(blocks_of(p, VEC), q.runs), kThreads, smem, st>>>(p, m, q.run, pieces);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
@@ -516,7 +517,8 @@ cudaError_t launch_fwd(const NormParams& p, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     const auto kern = seq_apply_kernel<T, VEC>;
     constexpr int smem = Ring<T, VEC, 4>::kBytes;
-    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
+    static std::atomic<uint64_t> allowed;
+    if ((e = allow_shared(kern, smem, allowed)) != cudaSuccess) return e;
     return tc::launch_dependent(kern, dim3(blocks_of(p, VEC), q.runs), kThreads, smem, st, p, m, q.run, (const float*)stats);
 }
 
@@ -538,8 +540,9 @@ cudaError_t launch_bwd(const NormParams& p, cudaStream_t st) {
     const auto grads = seq_grads_kernel<T, TG, VEC>;
     const auto dx = seq_dx_kernel<T, TG, VEC>;
     constexpr int smem = Ring<T, VEC, 2>::kBytes + Ring<TG, VEC, 2>::kBytes;
-    cudaError_t e = cudaFuncSetAttribute(grads, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(dx, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<uint64_t> grads_allowed, dx_allowed;
+    cudaError_t e = allow_shared(grads, smem, grads_allowed);
+    if (e == cudaSuccess) e = allow_shared(dx, smem, dx_allowed);
     if (e != cudaSuccess) return e;
     if (p.stats) {  // the call's first kernel: it waits for whatever made its inputs
         grads<<<grid, kThreads, smem, st>>>(p, m, q.run, stats, pieces, per_run);

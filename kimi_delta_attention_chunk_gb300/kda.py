@@ -804,6 +804,18 @@ def ssm_scan_bwd(u, delta, A, Bm, Cm, dy, D=None, z=None, delta_bias=None, softp
     return out
 
 
+def _packed_rows(name, t, width, lead):
+    """_rows, by the short way for a contiguous tensor of rows of ``width`` elements."""
+    if t is None:
+        return None, 0
+    return (t.data_ptr(), width) if t.is_contiguous() else _rows(name, t, lead)
+
+
+def _new_like(t):
+    """A contiguous tensor of t's shape, type and device."""
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+
 def _gated_check(x, r, i, lam, z):
     """C of a gated call whose x is [..., C]."""
     if lam.dtype is not torch.float32 or lam.dim() != 1:
@@ -840,17 +852,20 @@ def gated_scan_fwd(x, r, i, lam, z=None, decay: float = 8.0, initial_state=None,
     N = _sequences(x, cu_seqlens)
     _ints(B, T, C, N)
     dev = _here(x, r, i, lam, z, initial_state, cu_seqlens, y, final_state, states)
-    _like(x, y)
     _f32(initial_state, final_state, states)
     _shape("initial_state", initial_state, (N, C))
     _shape("final_state", final_state, (N, C))
-    _shape("y", y, (B, T, C))
-    _shape("states", states, gated_scan_states(x))
+    if states is not None:
+        _shape("states", states, gated_scan_states(x))
     if y is None:
-        y = torch.empty((B, T, C), dtype=x.dtype, device=x.device)
+        y = _new_like(x)
+    else:
+        _like(x, y)
+        _shape("y", y, (B, T, C))
     if final_state is None and output_final_state:
         final_state = torch.empty((N, C), dtype=torch.float32, device=x.device)
-    (px, ldx), (pr, ldr), (pi, ldi), (pz, ldz) = _rows("x", x, 2), _rows("r", r, 2), _rows("i", i, 2), _rows("z", z, 2)
+    (px, ldx), (pr, ldr) = _packed_rows("x", x, C, 2), _packed_rows("r", r, C, 2)
+    (pi, ldi), (pz, ldz) = _packed_rows("i", i, C, 2), _packed_rows("z", z, C, 2)
     st = lib.kda_gated_scan_fwd(px, ldx, pr, ldr, pi, ldi, _at(lam), pz, ldz, decay, _dt(x), _at(initial_state),
                                 _at(cu_seqlens), B, T, C, N, _at(y), _at(final_state), _at(states), _stream_of(dev))
     _check("kda_gated_scan_fwd", st)
@@ -881,7 +896,8 @@ def gated_scan_bwd(x, r, i, lam, dy, z=None, decay: float = 8.0, initial_state=N
            "dinitial_state": f32((N, C)) if initial_state is not None else None}
     ws, ws_bytes = _workspace(int(lib.kda_gated_scan_bwd_workspace_size(B, T, C, N, int(cu_seqlens is not None),
                                                                         int(states is not None))), x.device, workspace)
-    (px, ldx), (pr, ldr), (pi, ldi), (pz, ldz) = _rows("x", x, 2), _rows("r", r, 2), _rows("i", i, 2), _rows("z", z, 2)
+    (px, ldx), (pr, ldr) = _packed_rows("x", x, C, 2), _packed_rows("r", r, C, 2)
+    (pi, ldi), (pz, ldz) = _packed_rows("i", i, C, 2), _packed_rows("z", z, C, 2)
     st = lib.kda_gated_scan_bwd(px, ldx, pr, ldr, pi, ldi, _at(lam), pz, ldz, decay, _dt(x), _at(initial_state),
                                 _at(cu_seqlens), B, T, C, N, _at(dy), _at(dfinal_state), _dt(dy), _at(states),
                                 *(_at(out[k]) for k in ("dx", "dr", "di", "dlam", "dz", "dinitial_state")),
@@ -905,11 +921,12 @@ def gated_step(x, r, i, lam, state, z=None, decay: float = 8.0, slots=None, y=No
     if state.dtype is not torch.float32 or state.shape != (P, C):
         raise ValueError(f"state must be fp32 [P, {C}]")
     if y is None:
-        y = torch.empty((N, C), dtype=x.dtype, device=x.device)
+        y = _new_like(x)
     elif y.dtype is not x.dtype or y.shape != (N, C):
         raise ValueError(f"y must be {(N, C)} of {x.dtype}")
     _check_slots(slots, status, N)
-    (px, ldx), (pr, ldr), (pi, ldi), (pz, ldz) = _rows("x", x, 1), _rows("r", r, 1), _rows("i", i, 1), _rows("z", z, 1)
+    (px, ldx), (pr, ldr) = _packed_rows("x", x, C, 1), _packed_rows("r", r, C, 1)
+    (pi, ldi), (pz, ldz) = _packed_rows("i", i, C, 1), _packed_rows("z", z, C, 1)
     st = lib.kda_gated_step(px, ldx, pr, ldr, pi, ldi, _at(lam), pz, ldz, decay, _dt(x), _at(state), _at(slots), P, N, C,
                             _at(y), _at(status), _stream_of(dev))
     _check("kda_gated_step", st)
@@ -931,9 +948,10 @@ def _norm_check(x, groups, weight, bias, over, cu_seqlens):
         N = _sequences(x, cu_seqlens)
     if cu_seqlens is not None and over == "token":
         raise ValueError("cu_seqlens goes with norms over sequences")
-    _f32(weight, bias)
-    _shape("weight", weight, (C,))
-    _shape("bias", bias, (C,))
+    for v in (weight, bias):
+        if v is not None and (v.dtype is not torch.float32 or v.shape != (C,)):
+            _f32(v)
+            _shape("weight and bias", v, (C,))
     _ints(B, T, C, N, groups)
     return B, T, C, N
 
@@ -952,18 +970,20 @@ def group_norm_fwd(x, groups: int, weight=None, bias=None, eps: float = 1e-5, ac
     lib = _lib if _lib is not None else load_library()
     B, T, C, N = _norm_check(x, groups, weight, bias, over, cu_seqlens)
     dev = _here(x, weight, bias, cu_seqlens, y, stats, workspace)
-    _like(x, y)
-    _f32(stats)
-    _shape("y", y, x.shape)
-    _shape("stats", stats, (N, groups, 2))
+    if stats is not None:
+        _f32(stats)
+        _shape("stats", stats, (N, groups, 2))
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        y = _new_like(x)
+    else:
+        _like(x, y)
+        _shape("y", y, x.shape)
     seq = _NORM_OVER[over]
     ws, ws_bytes = None, 0
     if seq:
         ws, ws_bytes = _workspace(int(lib.kda_group_norm_fwd_workspace_size(B, T, C, groups, N, seq, int(cu_seqlens is not None),
                                                                             int(stats is not None))), x.device, workspace)
-    px, ldx = _rows("x", x, x.dim() - 1)
+    px, ldx = _packed_rows("x", x, C, x.dim() - 1)
     st = lib.kda_group_norm_fwd(px, ldx, _at(weight), _at(bias), eps, act, seq, _dt(x), _at(cu_seqlens), B, T, C, groups, N,
                                 _at(y), _at(stats), _at(ws), ws_bytes, _stream_of(dev))
     _check("kda_group_norm_fwd", st)
@@ -988,7 +1008,7 @@ def group_norm_bwd(x, groups: int, dy, weight=None, bias=None, eps: float = 1e-5
     seq = _NORM_OVER[over]
     ws, ws_bytes = _workspace(int(lib.kda_group_norm_bwd_workspace_size(B, T, C, groups, N, seq, int(cu_seqlens is not None),
                                                                         int(stats is not None))), x.device, workspace)
-    px, ldx = _rows("x", x, x.dim() - 1)
+    px, ldx = _packed_rows("x", x, C, x.dim() - 1)
     st = lib.kda_group_norm_bwd(px, ldx, _at(weight), _at(bias), eps, act, seq, _dt(x), _at(cu_seqlens), B, T, C, groups, N,
                                 _at(dy), _dt(dy), _at(stats), _at(out["dx"]), _at(out["dweight"]), _at(out["dbias"]), _at(ws),
                                 ws_bytes, _stream_of(dev))
