@@ -78,10 +78,11 @@ __device__ __forceinline__ uint32_t address_at(unsigned rank, const void* mine) 
     return to;
 }
 
-// Lets a kernel have `bytes` of shared memory, once a device (a mark for each of 64; others every time).  48 KB need no leave.
+// Lets a kernel have `bytes` of shared memory, once a device (a mark for each of 64; others every time).  48 KB need no
+// leave, of which the kernel itself may declare half.
 template <typename K>
 cudaError_t allow_shared(K kern, int bytes, std::atomic<uint64_t>& done) {
-    if (bytes <= 48 * 1024) return cudaSuccess;
+    if (bytes <= 24 * 1024) return cudaSuccess;
     int dev = 64;
     cudaError_t e = cudaGetDevice(&dev);
     const uint64_t mark = dev < 64 ? 1ull << dev : 0;

@@ -28,7 +28,7 @@ struct Variant {
     static constexpr int kAhead = R <= 2 && NTH == 256 ? 4 : 1;
     // Backwards, dw and db of a thread's channels: in registers, or where they are many in shared memory.
     static constexpr bool kSharedSums = E > 16 || NTH != 256;
-    static constexpr int kFwd = NTH != 256 ? 1 : E > 16 ? 3 : 4, kBwd = NTH != 256 ? 1 : E > 8 && !kSharedSums ? 2 : 3;  // blocks an SM
+    static constexpr int kFwd = NTH != 256 ? 1 : E > 16 ? 3 : 4, kBwd = NTH != 256 ? 1 : E > 8 ? 2 : 3;  // blocks an SM
 };
 
 // Sums of `N` values over every team.  Teams of more than a warp meet in shared memory, in a buffer of their own each time.
@@ -163,13 +163,15 @@ __global__ void __launch_bounds__(V::NTH, V::kFwd) norm_token_fwd_kernel(NormPar
     // this thread's rows: every step-th from `first`
     const int64_t step = (int64_t)gridDim.y * t.rows, first = (int64_t)blockIdx.y * t.rows + at.rsub;
     const int mine = first < p.total ? (int)((p.total - first + step - 1) / step) : 0;
-    const T* from = static_cast<const T*>(p.x) + first * p.ldx;
+    const int apart = at.lanes * V::VEC;  // channels between a thread's pieces
+    const int64_t next_x = step * p.ldx, next_y = step * p.C;
+    const T* from = static_cast<const T*>(p.x) + first * p.ldx + at.channel(0);
     auto request = [&](int i) {
         if (i < mine) {
 #pragma unroll
             for (int k = 0; k < R; ++k)
-                if (at.has(k)) ring.request(i, k, from + at.channel(k));
-            from += step * p.ldx;
+                if (at.has(k)) ring.request(i, k, from + k * apart);
+            from += next_x;
         }
         if constexpr (A > 1) copies_commit();
     };
@@ -178,8 +180,8 @@ __global__ void __launch_bounds__(V::NTH, V::kFwd) norm_token_fwd_kernel(NormPar
     Weights<V> weights(p, at);
     // (teams of more than a warp meet, so every thread of a block takes as many turns)
     const int turns = (int)((p.total - (int64_t)blockIdx.y * t.rows + step - 1) / step);
-    T* to = static_cast<T*>(p.y) + first * p.C;
-    for (int i = 0; i < turns; ++i, to += step * p.C) {
+    T* to = static_cast<T*>(p.y) + first * p.C + at.channel(0);
+    for (int i = 0; i < turns; ++i, to += next_y) {
         if constexpr (A > 1) copies_wait<A - 2>();
         else request(i);
         f2 x[R][N2], a = 0ull;
@@ -213,7 +215,7 @@ __global__ void __launch_bounds__(V::NTH, V::kFwd) norm_token_fwd_kernel(NormPar
             }
             Row<T, V::VEC> out;
             out.from(y);
-            if (at.has(k)) out.store(to + at.channel(k));
+            if (at.has(k)) out.store(to + k * apart);
         }
     }
 }
@@ -232,18 +234,20 @@ __global__ void __launch_bounds__(V::NTH, V::kBwd) norm_token_bwd_kernel(NormPar
     const float inv_n = 1.f / (float)(p.C / p.G);
     const int64_t step = (int64_t)gridDim.y * t.rows, first = (int64_t)blockIdx.y * t.rows + at.rsub;
     const int mine = first < p.total ? (int)((p.total - first + step - 1) / step) : 0;
-    const T* from = static_cast<const T*>(p.x) + first * p.ldx;
-    const TG* from_dy = static_cast<const TG*>(p.dy) + first * p.C;
+    const int apart = at.lanes * V::VEC;
+    const int64_t next_x = step * p.ldx, next_y = step * p.C;
+    const T* from = static_cast<const T*>(p.x) + first * p.ldx + at.channel(0);
+    const TG* from_dy = static_cast<const TG*>(p.dy) + first * p.C + at.channel(0);
     auto request = [&](int i) {
         if (i < mine) {
 #pragma unroll
             for (int k = 0; k < R; ++k)
                 if (at.has(k)) {
-                    ring.request(i, k, from + at.channel(k));
-                    ring_dy.request(i, k, from_dy + at.channel(k));
+                    ring.request(i, k, from + k * apart);
+                    ring_dy.request(i, k, from_dy + k * apart);
                 }
-            from += step * p.ldx;
-            from_dy += step * p.C;
+            from += next_x;
+            from_dy += next_y;
         }
         if constexpr (A > 1) copies_commit();
     };
@@ -274,14 +278,16 @@ __global__ void __launch_bounds__(V::NTH, V::kBwd) norm_token_bwd_kernel(NormPar
             else dw[k][e] = db[k][e] = 0ull;
         }
     const int turns = (int)((p.total - (int64_t)blockIdx.y * t.rows + step - 1) / step);
-    TG* to = static_cast<TG*>(p.dx) + first * p.C;
-    for (int i = 0; i < turns; ++i, to += step * p.C) {
+    TG* to = static_cast<TG*>(p.dx) + first * p.C + at.channel(0);
+    // kAll: all rows of the block are there
+    auto turn = [&](int i, auto all) {
+        constexpr bool kAll = decltype(all)::value;
         if constexpr (A > 1) copies_wait<A - 2>();
         else request(i);
         f2 x[R][N2], q[R][N2], a = 0ull;
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            if (at.has(k) && i < mine) {
+            if (at.has(k) && (kAll || i < mine)) {
                 ring.take(i, k, x[k]);
                 ring_dy.take(i, k, q[k]);
 #pragma unroll
@@ -324,7 +330,7 @@ __global__ void __launch_bounds__(V::NTH, V::kBwd) norm_token_bwd_kernel(NormPar
         }
         float s[2] = {sum2(m1), sum2(m2)};
         sum(s);
-        if (i >= mine) continue;
+        if (!kAll && i >= mine) return;
         const f2 n1 = both(-s[0] * inv_n), n2 = both(-s[1] * inv_n);
 #pragma unroll
         for (int k = 0; k < R; ++k) {
@@ -333,9 +339,14 @@ __global__ void __launch_bounds__(V::NTH, V::kBwd) norm_token_bwd_kernel(NormPar
             for (int e = 0; e < N2; ++e) dx[e] = mul2(rstd, fma2(x[k][e], n2, add2(q[k][e], n1)));
             Row<TG, V::VEC> out;
             out.from(dx);
-            if (at.has(k)) out.store(to + at.channel(k));
+            if (at.has(k)) out.store(to + k * apart);
         }
-    }
+        to += next_y;
+    };
+    const int64_t behind = p.total - (int64_t)blockIdx.y * t.rows - (t.rows - 1);  // rows from the block's last one on
+    const int full = behind > 0 ? (int)((behind + step - 1) / step) : 0;
+    for (int i = 0; i < full; ++i) turn(i, std::true_type{});
+    for (int i = full; i < turns; ++i) turn(i, std::false_type{});
     tc::grid_dep_launch();
     if (!p.dweight && !p.dbias) return;
     // the block's rows side by side first

@@ -23,7 +23,8 @@ __device__ __forceinline__ void vec_pairs(const float* p, float none, f2 (&v)[(V
     for (int k = 0; k < (VEC + 1) / 2; ++k) v[k] = p ? pack(__ldg(p + 2 * k), 2 * k + 1 < VEC ? __ldg(p + 2 * k + 1) : 0.f) : both(none);
 }
 
-// dweight and dbias from partial sums [parts][2][C] (sum dp xh, then sum dp), 32 channels a block, in a fixed order.
+// dweight and dbias from partial sums [parts][2][C] (sum dp xh, then sum dp), 32 channels a block, in a fixed order.  The first 256 threads
+// of a block call it.
 __device__ __forceinline__ void norm_weight_sums(const float* partial, int parts, int C, float* dweight, float* dbias, int block) {
     __shared__ float sums[8][33];
     const int lane = threadIdx.x % 32, w = threadIdx.x / 32, c = block * 32 + lane;
@@ -32,11 +33,13 @@ __device__ __forceinline__ void norm_weight_sums(const float* partial, int parts
         float* const to = v ? dbias : dweight;
         if (!to) continue;
         float s = 0.f;
-        if (c < C)
+        if (c < C) {
+#pragma unroll 4
             for (int k = w; k < parts; k += 8) s += partial[((int64_t)k * 2 + v) * C + c];
-        __syncthreads();
+        }
+        tc::named_sync(1, 256);  // (the block may have more threads)
         sums[w][lane] = s;
-        __syncthreads();
+        tc::named_sync(1, 256);
         if (w == 0 && c < C) {
             s = 0.f;
 #pragma unroll

@@ -227,9 +227,10 @@ struct PieceRange {
 };
 
 // mean and 1 / deviation of every sequence and group from the pieces: stats [N][G][2], a block each in turn.
-__global__ void __launch_bounds__(128) seq_stats_kernel(NormParams p, SeqMap m, int run, const float* pieces, float* stats) {
+template <int NTH>
+__global__ void __launch_bounds__(NTH) seq_stats_kernel(NormParams p, SeqMap m, int run, const float* pieces, float* stats) {
     constexpr int kKept = 8;  // pairs of a piece's mean and squares that a thread keeps between the two sums
-    __shared__ float buf[4];
+    __shared__ float buf[NTH / 32];
     const int cg = p.C / p.G;
     tc::grid_dep_wait();
     for (int64_t i = blockIdx.x; i < (int64_t)p.N * p.G; i += gridDim.x) {
@@ -252,13 +253,14 @@ __global__ void __launch_bounds__(128) seq_stats_kernel(NormParams p, SeqMap m, 
         float tk[kKept], mk[kKept], qk[kKept], s = 0.f, q = 0.f;
 #pragma unroll
         for (int j = 0; j < kKept; ++j) {
-            const int k = threadIdx.x + j * 128;
+            const int k = threadIdx.x + j * NTH;
             if (k < all) entry(k, tk[j], mk[j], qk[j]);
             else tk[j] = mk[j] = qk[j] = 0.f;
         }
 #pragma unroll
         for (int j = 0; j < kKept; ++j) s = fmaf(tk[j], mk[j], s);
-        for (int k = threadIdx.x + kKept * 128; k < all; k += 128) {
+#pragma unroll 4
+        for (int k = threadIdx.x + kKept * NTH; k < all; k += NTH) {
             float t, x, m2;
             entry(k, t, x, m2);
             s = fmaf(t, x, s);
@@ -269,7 +271,8 @@ __global__ void __launch_bounds__(128) seq_stats_kernel(NormParams p, SeqMap m, 
             const float d = mk[j] - mean;
             q += fmaf(tk[j] * d, d, qk[j]);
         }
-        for (int k = threadIdx.x + kKept * 128; k < all; k += 128) {
+#pragma unroll 4
+        for (int k = threadIdx.x + kKept * NTH; k < all; k += NTH) {
             float t, x, m2;
             entry(k, t, x, m2);
             q += fmaf(t * (x - mean), x - mean, m2);
@@ -396,12 +399,13 @@ __global__ void __launch_bounds__(kThreads, 2) seq_grads_kernel(NormParams p, Se
 }
 
 // Blocks [0, weight_blocks): dweight and dbias.  The others: mean(q xh) and mean(q) of every sequence and group, means [N][G][2].
-__global__ void __launch_bounds__(256) seq_means_kernel(NormParams p, SeqMap m, int run, int runs, const float* pieces, const float* per_run,
+template <int NTH>
+__global__ void __launch_bounds__(NTH) seq_means_kernel(NormParams p, SeqMap m, int run, int runs, const float* pieces, const float* per_run,
                                                         int weight_blocks, float* means) {
-    __shared__ float buf[8];
+    __shared__ float buf[NTH / 32];
     tc::grid_dep_wait();
     if ((int)blockIdx.x < weight_blocks) {
-        norm_weight_sums(per_run, runs, p.C, p.dweight, p.dbias, blockIdx.x);
+        if (threadIdx.x < 256) norm_weight_sums(per_run, runs, p.C, p.dweight, p.dbias, blockIdx.x);
         tc::grid_dep_launch();
         return;
     }
@@ -413,7 +417,7 @@ __global__ void __launch_bounds__(256) seq_means_kernel(NormParams p, SeqMap m, 
         const int all = r.count * cg;
         float a = 0.f, b = 0.f;
 #pragma unroll 4
-        for (int k = threadIdx.x; k < all; k += 256) {
+        for (int k = threadIdx.x; k < all; k += NTH) {
             const int piece = k / cg, ch = k - piece * cg;
             const float* const x = at + r.place(piece) * 2 * p.C + ch;
             const float w = p.weight ? __ldg(p.weight + g * cg + ch) : 1.f;
@@ -490,6 +494,9 @@ int64_t groups_grid(const NormParams& p) {
     const int64_t n = (int64_t)p.N * p.G;
     return n < 1 ? 1 : n < 8 * kSms ? n : 8 * kSms;
 }
+// Whether a sequence's pieces of a group are more than a small block keeps in registers (by the mean length of the sequences: one
+// sequence, one group of 4096 channels in 19 runs takes 78,000 entries, and one block for it 130 us with 128 threads).
+bool large_groups(const NormParams& p, const Cut& q) { return (int64_t)(q.runs / (p.N > 0 ? p.N : 1) + 1) * (p.C / p.G) > 1024; }
 // Places of pieces at p's sizes, whichever variant runs: the wide ones have the fewest blocks and the most runs.
 int64_t most_runs(const NormParams& p) { return cut_of(p, blocks_of(p, 8), kFwdResident).runs; }
 size_t pieces_bytes(const NormParams& p) { return (size_t)(((most_runs(p) + p.N) * 2 * p.C * 4 + 255) / 256 * 256); }
@@ -504,7 +511,8 @@ cudaError_t launch_stats(const NormParams& p, const SeqMap& m, const Cut& q, flo
     if (e != cudaSuccess) return e;
     kern<<<dim3(blocks_of(p, VEC), q.runs), kThreads, smem, st>>>(p, m, q.run, pieces);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    return tc::launch_dependent(seq_stats_kernel, (unsigned)groups_grid(p), 128, 0, st, p, m, q.run, (const float*)pieces, stats);
+    if (large_groups(p, q)) return tc::launch_dependent(seq_stats_kernel<1024>, (unsigned)groups_grid(p), 1024, 0, st, p, m, q.run, (const float*)pieces, stats);
+    return tc::launch_dependent(seq_stats_kernel<128>, (unsigned)groups_grid(p), 128, 0, st, p, m, q.run, (const float*)pieces, stats);
 }
 
 template <typename T, int VEC>
@@ -552,8 +560,9 @@ cudaError_t launch_bwd(const NormParams& p, cudaStream_t st) {
     }
     if (e != cudaSuccess) return e;
     const int weight_blocks = p.dweight || p.dbias ? (p.C + 31) / 32 : 0;
-    e = tc::launch_dependent(seq_means_kernel, (unsigned)(weight_blocks + groups_grid(p)), 256, 0, st, p, m, q.run, q.runs, (const float*)pieces,
-                             (const float*)per_run, weight_blocks, means);
+    const bool large = large_groups(p, q);
+    e = tc::launch_dependent(large ? seq_means_kernel<1024> : seq_means_kernel<256>, (unsigned)(weight_blocks + groups_grid(p)), large ? 1024 : 256, 0, st, p, m,
+                             q.run, q.runs, (const float*)pieces, (const float*)per_run, weight_blocks, means);
     if (e != cudaSuccess) return e;
     return tc::launch_dependent(dx, grid, kThreads, smem, st, p, m, q.run, (const float*)stats, (const float*)means);
 }
