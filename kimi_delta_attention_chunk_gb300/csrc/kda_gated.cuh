@@ -9,8 +9,6 @@
 
 namespace kda {
 
-constexpr int kGatedCh = 64;  // channels of a block: a pair a lane, 128 bytes of a bf16 row
-
 __device__ __forceinline__ float rsq(float x) {
     float y;
     asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -20,23 +18,30 @@ __device__ __forceinline__ float rsq(float x) {
 // rate = decay log(1 + e^lam) of one channel (once a kernel: with the accurate functions).
 __device__ __forceinline__ float gated_rate(float lam, float decay) { return decay * (fmaxf(lam, 0.f) + log1pf(expf(-fabsf(lam)))); }
 
-// The decay of a pair of channels from sr = sigmoid(r): a = e^-s with s = rate sr, and m2 = 1 - a^2.  Where s < 1/4, 1 - a^2 would lose its
-// leading bits (layers are initialised with a in 0.9 ... 0.999); it is 2 a sinh(s) there, with sinh(s) / s = 1 + s^2/6 + s^4/120 to 5e-8.
-// kSmall: rate < 1/4, so every s is (known once a kernel).
+// The decay of a pair of channels from sr = sigmoid(r): a = e^-s with s = rate sr, and m2 = 1 - a^2.  Below s = 1/4 (layers are
+// initialised with a in 0.9 ... 0.999), with S = sinh(s) / s = 1 + s^2/6 + s^4/120 and K = (cosh(s) - 1) / s^2 = 1/2 + s^2/24 + s^4/720
+// (both to 5e-8): a = 1 + (s^2 K - s S), off by its last rounding only, which a state remembers for 1/s tokens, and m2 = 2 a s S, where
+// 1 - a^2 would lose its leading bits.  kSmall: rate < 1/4, so every s is (known once a kernel).
 struct Decay {
     f2 a, m2;
     template <bool kSmall>
     static __device__ __forceinline__ Decay of(f2 sr, f2 rate) {
         Decay d;
         const f2 s = mul2(sr, rate), q = mul2(s, s);
-        d.a = ex2_2(mul2(s, both(-kLog2e)));
-        d.m2 = mul2(mul2(d.a, s), fma2(q, fma2(q, both(1.f / 60.f), both(1.f / 3.f)), both(2.f)));
+        const f2 sinh = mul2(s, fma2(q, fma2(q, both(1.f / 120.f), both(1.f / 6.f)), both(1.f)));
+        const f2 cosh = mul2(q, fma2(q, fma2(q, both(1.f / 720.f), both(1.f / 24.f)), both(0.5f)));
+        d.a = add2(fma2(sinh, both(-1.f), cosh), both(1.f));
+        d.m2 = mul2(mul2(d.a, both(2.f)), sinh);
         if constexpr (!kSmall) {
+            const f2 e = ex2_2(mul2(s, both(-kLog2e)));
             float s0, s1, x0, x1, y0, y1;
             unpack(s, s0, s1);
             unpack(d.m2, x0, x1);
-            unpack(fma2(mul2(d.a, d.a), both(-1.f), both(1.f)), y0, y1);
+            unpack(fma2(mul2(e, e), both(-1.f), both(1.f)), y0, y1);
             d.m2 = pack(s0 < 0.25f ? x0 : y0, s1 < 0.25f ? x1 : y1);
+            unpack(d.a, x0, x1);
+            unpack(e, y0, y1);
+            d.a = pack(s0 < 0.25f ? x0 : y0, s1 < 0.25f ? x1 : y1);
         }
         return d;
     }
@@ -89,6 +94,24 @@ __device__ __forceinline__ Affine follow(const Affine& first, const Affine& then
     return r;
 }
 __device__ __forceinline__ Affine identity() { return Affine{both(1.f), 0ull}; }
+__device__ __forceinline__ f2 shuffle2(f2 x, int with) { return __shfl_xor_sync(0xffffffffu, x, with); }
+// From the maps of a warp's strips: `total` of all of them, and `before`, that of those which are walked before this lane's (forwards the
+// ones in front, backwards those behind).
+template <typename L, bool kCuts, bool kForwards>
+__device__ __forceinline__ void join_strips(const Affine& mine, Affine& total, Affine& before) {
+    total = mine;
+    before = identity();
+#pragma unroll
+    for (int d = 1; d < L::kStrips; d *= 2) {
+        const Affine other{shuffle2(total.A, d * L::kPairs), shuffle2(total.H, d * L::kPairs)};
+        const bool second = ((L::strip() & d) != 0) == kForwards;  // the other strips are walked before these
+        const Affine a = follow<kCuts>(other, total), b = follow<kCuts>(total, other), c = follow<kCuts>(other, before);
+        total.A = second ? a.A : b.A;
+        total.H = second ? a.H : b.H;
+        before.A = second ? c.A : before.A;
+        before.H = second ? c.H : before.H;
+    }
+}
 
 // ---- packed sequences as a warp walks them, strip by strip ------------------------------------------------
 
@@ -135,41 +158,55 @@ __device__ __forceinline__ void store_at(unsigned rank, void* mine, const Affine
 
 // ---- tiles -------------------------------------------------------------------------------------------------
 
-// A lane's share of the rows of one tensor's strips (R rows of kGatedCh channels, copied by the warp that works on them), by pieces of
-// VEC elements.  Strips are asked for in turn, `step` tokens apart.
-template <typename T, int R, int VEC>
+// How a warp's lanes lie on CH channels: a lane has a pair of them, and the warp 64 / CH strips of STRIP tokens, one behind the other.
+// In shared memory a strip's rows are followed by one that is not used, so that the strips of a warp begin in different banks.
+template <int CH, int STRIP>
+struct Lanes {
+    static constexpr int kPairs = CH / 2, kStrips = 64 / CH, kTokens = kStrips * STRIP;  // of a warp
+    static constexpr int kPart = (kStrips == 1 ? STRIP : kStrips * (STRIP + 1)) * CH;    // elements of a warp's rows in shared memory
+    static __device__ __forceinline__ int pair() { return threadIdx.x % kPairs; }
+    static __device__ __forceinline__ int strip() { return threadIdx.x % 32 / kPairs; }
+    static __device__ __forceinline__ int row(int token) { return kStrips == 1 ? token : token + token / STRIP; }
+    // Where this lane's pair of its strip's first token is.
+    static __device__ __forceinline__ int place() { return row(strip() * STRIP) * CH + 2 * pair(); }
+};
+
+// A lane's share of the rows of one tensor's tokens (L::kTokens rows of CH channels, copied by the warp that works on them), by pieces
+// of VEC elements.  Tiles are asked for in turn, `step` tokens apart.
+template <typename T, int CH, int STRIP, int VEC>
 struct Feed {
-    static constexpr int PR = kGatedCh / VEC;           // pieces of a row
+    using L = Lanes<CH, STRIP>;
+    static constexpr int R = L::kTokens;
+    static constexpr int PR = CH / VEC;                 // pieces of a row
     static constexpr int N = R * PR / 32;               // pieces of a lane
     static constexpr int ROWS = PR < 32 ? 32 / PR : 1;  // rows between them (one row by several rounds: PR = 64)
     static_assert(R * PR % 32 == 0 && (PR <= 32 || PR == 64), "whole rounds");
-    const T* at;         // the next strip's piece of this lane
-    int64_t step, more;  // elements to the next strip's, and to the next row's
+    const T* at;         // the next tile's piece of this lane
+    int64_t step, more;  // elements to the next tile's, and to the next row's
     __device__ __forceinline__ Feed(const void* base, int64_t ld, int64_t first_row, int c0, int step)
         : at(static_cast<const T*>(base) + (first_row + row()) * ld + c0 + col()), step(step * ld), more(ROWS * ld) {}
     static __device__ __forceinline__ int row() { return threadIdx.x % 32 / PR; }
     static __device__ __forceinline__ int col() { return threadIdx.x % 32 % PR * VEC; }
-    // The next strip, all of whose rows and channels are there.
-    __device__ __forceinline__ void request(T* strip) {
-        T* const to = strip + row() * kGatedCh + col();
+    // The next tile, all of whose rows and channels are there.
+    __device__ __forceinline__ void request(T* tile) {
         if constexpr (PR <= 32) {
             const T* from = at;
 #pragma unroll
-            for (int k = 0; k < N; ++k, from += more) Row<T, VEC>::copy_async(to + k * ROWS * kGatedCh, from);
+            for (int k = 0; k < N; ++k, from += more) Row<T, VEC>::copy_async(tile + L::row(row() + k * ROWS) * CH + col(), from);
             at += step;
         } else {
-            request(strip, R, kGatedCh);
+            request(tile, R, CH);
         }
     }
-    // The next strip, of which `rows` rows are there (none: <= 0) and `has` channels.
-    __device__ __forceinline__ void request(T* strip, int rows, int has) {
+    // The next tile, of which `rows` rows are there (none: <= 0) and `has` channels.
+    __device__ __forceinline__ void request(T* tile, int rows, int has) {
         const T* from = at;
         const int lines = rows < R ? rows : R;
         for (int r = row(); r < lines; r += ROWS, from += more)
 #pragma unroll
             for (int h = 0; h < (PR + 31) / 32; ++h) {
                 const int c = col() + h * 32 * VEC;
-                if (c < has) Row<T, VEC>::copy_async(strip + r * kGatedCh + c, from + h * 32 * VEC);
+                if (c < has) Row<T, VEC>::copy_async(tile + L::row(r) * CH + c, from + h * 32 * VEC);
             }
         at += step;
     }
@@ -206,6 +243,17 @@ __device__ __forceinline__ void store_state(float* p, int64_t at, f2 h, int n) {
     unpack(h, a, b);
     if (n > 0) p[at] = a;
     if (n > 1) p[at + 1] = b;
+}
+
+// Channels of a block. 64 where blocks of them that take a whole sequence each come to one and a half an SM; else 32 where those do
+// (2 x 8192 x 4096 bf16 forward 148 -> 136 us, backward 2 x 2048 x 4096 86 -> 75); else blocks share a sequence as a cluster whatever
+// their width, and the widest rows cost least (1 x 16384 x 4096: 151, 155 and 171 us with 64, 32 and 16) as long as clusters of eight
+// fill the machine (1 x 65536 x 512: 213, 155, 104).
+inline int gated_channels(const GatedParams& p) {
+    for (const int blocks : {1, kMostCluster})
+        for (const int ch : {64, 32})
+            if ((int64_t)((p.C + ch - 1) / ch) * p.B * blocks >= kSms * 3 / 2) return ch;
+    return 16;
 }
 
 // Whether rows of p can be read by pieces of `bytes`: every pointer, stride and the row's length.

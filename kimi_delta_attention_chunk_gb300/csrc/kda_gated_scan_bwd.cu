@@ -20,50 +20,55 @@ namespace kda {
 namespace {
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kStrip = 4, kTile = kWarps * kStrip;
-static_assert(kTile == kGatedBlock, "a tile begins at a state that is left to it");
+constexpr int kStrip = 4;
+template <int CH>
+constexpr int kTile = kWarps * Lanes<CH, kStrip>::kTokens;
+static_assert(kTile<64> % kGatedBlock == 0 && kTile<32> % kGatedBlock == 0 && kTile<16> % kGatedBlock == 0, "tiles begin at states that are left to them");
 
 // x, r, i, z and dy of every warp's strip, in two stages.
 constexpr int kStages = 2;
-template <typename T, typename TG>
-constexpr int kStageBytes = kTile * kGatedCh * (4 * (int)sizeof(T) + (int)sizeof(TG));
+template <typename T, typename TG, int CH>
+constexpr int kStageBytes = kWarps * Lanes<CH, kStrip>::kPart * (4 * (int)sizeof(T) + (int)sizeof(TG));
 
 // VEC, GVEC: elements of a piece of x, r, i and z, and of dy; with VEC > 1, pairs of channels of the outputs are whole and aligned.
-template <typename T, typename TG, int VEC, int GVEC, bool kPacked>
+template <typename T, typename TG, int CH, int VEC, int GVEC, bool kPacked>
 __global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(GatedParams p, float* partial, int cluster, int blocks) {
-    constexpr int PART = kStrip * kGatedCh;
+    using L = Lanes<CH, kStrip>;
+    constexpr int PART = L::kPart, TT = kTile<CH>, kStage = kStageBytes<T, TG, CH>;
     extern __shared__ __align__(128) char shared[];
     // The strips' maps, backwards [0, kWarps) and forwards [kAhead, kAhead + kWarps), with maps between them that change nothing: every
     // warp folds kWarps - 1 maps, those behind its own backwards and those before it forwards.
     constexpr int kAhead = 2 * kWarps - 1;
-    __shared__ Affine maps[2][kAhead + kWarps][32];
-    __shared__ Affine peers[2][kMostCluster][32];
-    __shared__ f2 ends[2][32];
-    __shared__ Marks<kPacked ? kStrip : 1> all_marks[kWarps];
+    __shared__ Affine maps[2][kAhead + kWarps][L::kPairs];
+    __shared__ Affine peers[2][kMostCluster][L::kPairs];
+    __shared__ f2 ends[2][L::kPairs];
+    __shared__ Marks<kPacked ? L::kTokens : 1> all_marks[kWarps];
     __shared__ int32_t offsets[kPacked ? kCachedOffsets : 1];
 
-    const int lane = threadIdx.x % 32, w = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0);
+    const int pair = L::pair(), strip = L::strip(), w = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0);
     const int rank = cluster > 1 ? (int)cluster_rank() : 0;
-    const int group = blockIdx.x / cluster, b = group / blocks, c0 = group % blocks * kGatedCh;
-    const int c = c0 + 2 * lane, has = p.C - c0, n2 = min(2, p.C - c);  // channels of this lane: 2, 1 or none (<= 0)
+    const int group = blockIdx.x / cluster, b = group / blocks, c0 = group % blocks * CH;
+    const int c = c0 + 2 * pair, has = p.C - c0, n2 = min(2, p.C - c);  // channels of this lane: 2, 1 or none (<= 0)
     const Offsets m(p.cu, p.N, p.T, offsets);
     const int first = kPacked ? m.first() : 0, last = kPacked ? m.last() : p.T;
-    const int stride = kTile * cluster;  // tokens between a block's tiles
+    const int stride = TT * cluster;  // tokens between a block's tiles
     const int steps = (int)(((int64_t)p.T + stride - 1) / stride);
     const int64_t row0 = (int64_t)b * p.T;
-    int s0 = (steps - 1) * stride + rank * kTile + w * kStrip;  // this strip's first token: tiles are taken from the stream's end
+    // this warp's first token and this strip's: tiles are taken from the stream's end
+    int w0 = (steps - 1) * stride + rank * TT + w * L::kTokens, s0 = w0 + strip * kStrip;
 
-    // this warp's rows: a stage holds x, r, i, z [4][kStrip][64] and dy [kStrip][64]
-    char* const mine = shared + w * (kStageBytes<T, TG> / kWarps);
-    Feed<T, kStrip, VEC> fx(p.x, p.ldx, row0 + s0, c0, -stride), fr(p.r, p.ldr, row0 + s0, c0, -stride), fi(p.i, p.ldi, row0 + s0, c0, -stride);
-    Feed<T, kStrip, VEC> fz(p.z, p.ldz, row0 + s0, c0, -stride);
-    Feed<TG, kStrip, GVEC> fy(p.dy, p.C, row0 + s0, c0, -stride);
+    // this warp's rows: a stage holds x, r, i, z and dy
+    char* const mine = shared + w * (kStage / kWarps);
+    using F = Feed<T, CH, kStrip, VEC>;
+    F fx(p.x, p.ldx, row0 + w0, c0, -stride), fr(p.r, p.ldr, row0 + w0, c0, -stride), fi(p.i, p.ldi, row0 + w0, c0, -stride);
+    F fz(p.z, p.ldz, row0 + w0, c0, -stride);
+    Feed<TG, CH, kStrip, GVEC> fy(p.dy, p.C, row0 + w0, c0, -stride);
     auto request = [&](int it) {
-        const int rows = p.T - (s0 - stride);
-        T* const in = reinterpret_cast<T*>(mine + (it & 1) * kStageBytes<T, TG>);
+        const int rows = p.T - (w0 - stride);
+        T* const in = reinterpret_cast<T*>(mine + (it & 1) * kStage);
         if (it < steps) {
             TG* const dys = reinterpret_cast<TG*>(in + 4 * PART);
-            if (rows >= kStrip && has >= kGatedCh) {
+            if (rows >= L::kTokens && has >= CH) {
                 fx.request(in);
                 fr.request(in + PART);
                 fi.request(in + 2 * PART);
@@ -79,9 +84,9 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(GatedParams p, f
         }
         copies_commit();
     };
-    s0 += stride;
+    w0 += stride;
     request(0);
-    s0 -= stride;
+    w0 -= stride;
 
     const f2 rate = pack(n2 > 0 ? gated_rate(__ldg(p.lam + c), p.decay) : 0.f, n2 > 1 ? gated_rate(__ldg(p.lam + c + 1), p.decay) : 0.f);
     const bool small = __all_sync(0xffffffffu, small_rate(rate)) != 0;
@@ -90,7 +95,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(GatedParams p, f
         const int warps = kWarps * cluster;
         for (int n0 = (w * cluster + rank) * 32; n0 < p.N; n0 += warps * 32) {
             if (!kPacked && p.T > 0) break;
-            const int n = n0 + lane;
+            const int n = n0 + (int)threadIdx.x % 32;
             unsigned empty = __ballot_sync(0xffffffffu, n < p.N && (!kPacked || m.end(n) <= m.begin(n)));
             for (; empty; empty &= empty - 1) {
                 const int64_t at = (int64_t)(n0 + __ffs(empty) - 1) * p.C + c;
@@ -99,8 +104,8 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(GatedParams p, f
         }
     }
     f2 carry = kPacked ? 0ull : state_pair(p.dfinal, (int64_t)b * p.C + c, n2), dlam = 0ull;
-    if (w == 0) ends[0][lane] = carry;
-    if (w < kWarps - 1) maps[0][kWarps + w][lane] = maps[1][kWarps + w][lane] = identity();
+    if (w == 0) ends[0][pair] = carry;
+    if (w < kWarps - 1) maps[0][kWarps + w][pair] = maps[1][kWarps + w][pair] = identity();
     if (cluster > 1) {
         cluster_arrive<false>();
         cluster_wait();
@@ -108,29 +113,30 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(GatedParams p, f
 
     // where this warp's first row of an output and the tile's state are; all move up by a stride of rows a step
     int64_t off = (row0 + s0) * p.C + c;
-    const float* before = p.states + ((int64_t)b * ((p.T + kTile - 1) / kTile) + (s0 - w * kStrip) / kTile) * p.C + c;
-    Walk<kPacked ? kStrip : 1> walk;
-    const Marks<kPacked ? kStrip : 1>& marks = all_marks[w];
-    for (int it = 0; it < steps; ++it, s0 -= stride, off -= (int64_t)stride * p.C, before -= (int64_t)cluster * p.C) {
-        const int t0 = s0 - w * kStrip, buf = it & 1;
+    const float* left = p.states + ((int64_t)b * ((p.T + kGatedBlock - 1) / kGatedBlock) + (w0 - w * L::kTokens) / kGatedBlock) * p.C + c;
+    Walk<kPacked ? L::kTokens : 1> walk;
+    const int* const starts = all_marks[w].start + (kPacked ? strip * kStrip : 0);
+    const int* const lasts = all_marks[w].end + (kPacked ? strip * kStrip : 0);
+    for (int it = 0; it < steps; ++it, w0 -= stride, s0 -= stride, off -= (int64_t)stride * p.C, left -= (int64_t)(stride / kGatedBlock) * p.C) {
+        const int t0 = w0 - w * L::kTokens, buf = it & 1;
         f2 h = 0ull;
         if (t0 < p.T) {
             if (!kPacked && t0 == 0) h = state_pair(p.initial, (int64_t)b * p.C + c, n2);
-            else if (VEC > 1) h = n2 > 0 ? *reinterpret_cast<const f2*>(before) : 0ull;
-            else h = pack(n2 > 0 ? before[0] : 0.f, n2 > 1 ? before[1] : 0.f);
+            else if (VEC > 1) h = n2 > 0 ? *reinterpret_cast<const f2*>(left) : 0ull;
+            else h = pack(n2 > 0 ? left[0] : 0.f, n2 > 1 ? left[1] : 0.f);
         }
-        if constexpr (kPacked) walk.look(m, s0, t0 - rank * kTile, t0 - rank * kTile + stride, all_marks[w]);
+        if constexpr (kPacked) walk.look(m, w0, t0 - rank * TT, t0 - rank * TT + stride, all_marks[w]);
         const bool wide = walk.wide, clear = walk.clear;
         copies_wait<0>();
         __syncwarp();  // the strip's rows are there, and every lane is past the strip before
         request(it + 1);
-        const T* const in = reinterpret_cast<const T*>(mine + buf * kStageBytes<T, TG>) + 2 * lane;
-        const TG* const dys = reinterpret_cast<const TG*>(in - 2 * lane + 4 * PART) + 2 * lane;
+        const T* const in = reinterpret_cast<const T*>(mine + buf * kStage) + L::place();
+        const TG* const dys = reinterpret_cast<const TG*>(in - L::place() + 4 * PART) + L::place();
         f2 a[kStrip], u[kStrip], wx[kStrip], wm[kStrip], sr[kStrip], ui[kStrip], yb[kStrip], gz[kStrip];
         auto gates = [&](auto small_rates) {
 #pragma unroll
             for (int j = 0; j < kStrip; ++j) {
-                const f2 x = pair_at(in + j * kGatedCh), r = pair_at(in + PART + j * kGatedCh), i = pair_at(in + 2 * PART + j * kGatedCh);
+                const f2 x = pair_at(in + j * CH), r = pair_at(in + PART + j * CH), i = pair_at(in + 2 * PART + j * CH);
                 sr[j] = gate2(r);
                 const f2 si = gate2(i);
                 const Decay d = Decay::of<decltype(small_rates)::value>(sr[j], rate);
@@ -140,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(GatedParams p, f
                 u[j] = mul2(m1, gx);
                 ui[j] = mul2(u[j], rest2(si));
                 wm[j] = mul2(mul2(gx, inv), mul2(d.a, d.a));
-                yb[j] = pair_at(dys + j * kGatedCh);
+                yb[j] = pair_at(dys + j * CH);
             }
         };
         if (small) gates(std::true_type{});
@@ -148,12 +154,12 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(GatedParams p, f
         if (p.z) {
 #pragma unroll
             for (int j = 0; j < kStrip; ++j) {
-                const f2 z = pair_at(in + 3 * PART + j * kGatedCh), s = gate2(z), silu = mul2(z, s);
+                const f2 z = pair_at(in + 3 * PART + j * CH), s = gate2(z), silu = mul2(z, s);
                 gz[j] = mul2(yb[j], fma2(silu, rest2(s), s));  // silu' = s + z s (1 - s)
                 yb[j] = mul2(yb[j], silu);
             }
         }
-        if (s0 + kStrip > p.T) {
+        if (w0 + L::kTokens > p.T) {
 #pragma unroll
             for (int j = 0; j < kStrip; ++j)
                 if (s0 + j >= p.T) a[j] = both(1.f), u[j] = yb[j] = 0ull;
@@ -172,13 +178,13 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(GatedParams p, f
             fore = rear = identity();
 #pragma unroll
             for (int j = 0; j < kStrip; ++j) {
-                const int n = marks.start[j];
+                const int n = starts[j];
                 if (n >= 0) fore = Affine{both(-1.f), fma2(a[j], state_pair(p.initial, (int64_t)n * p.C + c, n2), u[j])};
                 else fore = follow<true>(fore, Affine{a[j], u[j]});
             }
 #pragma unroll
             for (int j = kStrip - 1; j >= 0; --j) {
-                const int n = marks.end[j];
+                const int n = lasts[j];
                 if (n >= 0) {
                     yb[j] = add2(yb[j], state_pair(p.dfinal, (int64_t)n * p.C + c, n2));
                     rear = Affine{both(-1.f), mul2(a[j], yb[j])};
@@ -187,16 +193,28 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(GatedParams p, f
                 }
             }
         }
-        maps[buf][w][lane] = rear;
-        maps[buf][kAhead + w][lane] = fore;
+        Affine fores, ahead, rears, behind;  // the warp's maps, and those of its strips in front of this one, and behind
+        if (!kPacked || clear) {
+            join_strips<L, false, true>(fore, fores, ahead);
+            join_strips<L, false, false>(rear, rears, behind);
+        } else {
+            join_strips<L, true, true>(fore, fores, ahead);
+            join_strips<L, true, false>(rear, rears, behind);
+        }
+        if (strip == 0) {
+            maps[buf][w][pair] = rears;
+            maps[buf][kAhead + w][pair] = fores;
+        }
         __syncthreads();
         f2 g;
         auto publish = [&](auto cuts) {
             if (w == kWarps - 1) {
-                Affine total = rear;
+                Affine total = rears;
 #pragma unroll
-                for (int k = kWarps - 2; k >= 0; --k) total = follow<decltype(cuts)::value>(total, maps[buf][k][lane]);
-                for (int k = 0; k < cluster; ++k) store_at(k, &peers[buf][rank][lane], total);
+                for (int k = kWarps - 2; k >= 0; --k) total = follow<decltype(cuts)::value>(total, maps[buf][k][pair]);
+                if (strip == 0)
+                    for (int k = 0; k < cluster; ++k) store_at(k, &peers[buf][rank][pair], total);
+                __syncwarp();
                 cluster_arrive<true>();
             } else {
                 cluster_arrive<false>();
@@ -206,30 +224,33 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(GatedParams p, f
             constexpr bool kCuts = decltype(cuts)::value;
             if (cluster > 1) {
                 cluster_wait();
-                for (int k = cluster - 1; k > rank; --k) carry = apply<kCuts>(peers[buf][k][lane].A, peers[buf][k][lane].H, carry);
+                for (int k = cluster - 1; k > rank; --k) carry = apply<kCuts>(peers[buf][k][pair].A, peers[buf][k][pair].H, carry);
                 g = carry;
-                for (int k = rank; k >= 0; --k) carry = apply<kCuts>(peers[buf][k][lane].A, peers[buf][k][lane].H, carry);
+                for (int k = rank; k >= 0; --k) carry = apply<kCuts>(peers[buf][k][pair].A, peers[buf][k][pair].H, carry);
             } else {
-                g = ends[buf][lane];
+                g = ends[buf][pair];
             }
 #pragma unroll
-            for (int k = kWarps - 1; k > 0; --k) g = apply<kCuts>(maps[buf][w + k][lane].A, maps[buf][w + k][lane].H, g);
+            for (int k = kWarps - 1; k > 0; --k) g = apply<kCuts>(maps[buf][w + k][pair].A, maps[buf][w + k][pair].H, g);
+            if constexpr (L::kStrips > 1) g = apply<kCuts>(behind.A, behind.H, g);
         };
         if (!kPacked || wide) {
             if (cluster > 1) publish(std::false_type{});
 #pragma unroll
-            for (int k = 0; k < kWarps - 1; ++k) h = fma2(maps[buf][kWarps + w + k][lane].A, h, maps[buf][kWarps + w + k][lane].H);
+            for (int k = 0; k < kWarps - 1; ++k) h = fma2(maps[buf][kWarps + w + k][pair].A, h, maps[buf][kWarps + w + k][pair].H);
+            if constexpr (L::kStrips > 1) h = fma2(ahead.A, h, ahead.H);
         } else {
             if (cluster > 1) publish(std::true_type{});
 #pragma unroll
-            for (int k = 0; k < kWarps - 1; ++k) h = apply<true>(maps[buf][kWarps + w + k][lane].A, maps[buf][kWarps + w + k][lane].H, h);
+            for (int k = 0; k < kWarps - 1; ++k) h = apply<true>(maps[buf][kWarps + w + k][pair].A, maps[buf][kWarps + w + k][pair].H, h);
+            if constexpr (L::kStrips > 1) h = apply<true>(ahead.A, ahead.H, h);
         }
-        const bool lean = VEC > 1 && (!kPacked || clear) && s0 >= first && s0 + kStrip <= last;  // the strip's tokens are of one sequence
+        const bool lean = VEC > 1 && (!kPacked || clear) && w0 >= first && w0 + L::kTokens <= last;  // the warp's tokens are of one sequence
         // the state before each token, and with it what dh is multiplied by: wm = si x a^2 / m - a h_{t-1}; dz is done
 #pragma unroll
         for (int j = 0; j < kStrip; ++j) {
             if (kPacked && !clear) {
-                const int n = marks.start[j];
+                const int n = starts[j];
                 if (n >= 0) h = state_pair(p.initial, (int64_t)n * p.C + c, n2);
             }
             const f2 ah = mul2(a[j], h);
@@ -262,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(GatedParams p, f
             for (int j = kStrip - 1; j >= 0; --j) {
                 const int t = s0 + j;
                 if (t >= p.T) continue;
-                if (kPacked && !clear && marks.end[j] >= 0) g = 0ull;
+                if (kPacked && !clear && lasts[j] >= 0) g = 0ull;
                 const f2 dh = add2(yb[j], g);
                 f2 part = mul2(mul2(dh, wm[j]), sr[j]), dx = mul2(dh, wx[j]), dr = mul2(mul2(part, rate), rest2(sr[j])), di = mul2(dh, ui[j]);
                 g = mul2(a[j], dh);
@@ -274,21 +295,22 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(GatedParams p, f
                 store_pair<TG, false>(static_cast<TG*>(p.di) + o, di, n2);
                 if (p.z) store_pair<TG, false>(static_cast<TG*>(p.dz) + o, gz[j], n2);
                 if (p.dinitial) {
-                    const int n = kPacked ? (clear ? -1 : marks.start[j]) : (t == 0 ? b : -1);
+                    const int n = kPacked ? (clear ? -1 : starts[j]) : (t == 0 ? b : -1);
                     if (n >= 0) store_state(p.dinitial, (int64_t)n * p.C + c, g, n2);
                 }
             }
         }
-        if (cluster == 1 && w == 0) ends[buf ^ 1][lane] = g;
+        if (cluster == 1 && w == 0 && strip == 0) ends[buf ^ 1][pair] = g;
     }
     tc::grid_dep_launch();
     __syncthreads();
-    maps[0][w][lane].A = dlam;
+    f2* const parts = reinterpret_cast<f2*>(maps);
+    static_assert(sizeof(maps) >= kThreads * sizeof(f2), "a part each thread");
+    parts[w * 32 + threadIdx.x % 32] = dlam;
     __syncthreads();
-    if (w == 0 && steps > 0) {
+    if (w == 0 && strip == 0 && steps > 0) {
         f2 sum = 0ull;
-#pragma unroll
-        for (int k = 0; k < kWarps; ++k) sum = add2(sum, maps[0][k][lane].A);
+        for (int k = 0; k < kWarps * L::kStrips; ++k) sum = add2(sum, parts[k * L::kPairs + pair]);
         store_state(partial + ((int64_t)b * cluster + rank) * p.C, c, sum, n2);
     }
 }
@@ -306,32 +328,37 @@ __global__ void __launch_bounds__(128) gated_dlam_kernel(const float* partial, i
 
 // (one partial sum a block: as many as the largest clusters have)
 size_t partial_bytes(const GatedParams& p) {
-    return ((size_t)p.B * (p.T > 0 ? most_blocks(p.T, kTile) : 0) * p.C * 4 + 255) / 256 * 256;
+    return ((size_t)p.B * (p.T > 0 ? most_blocks(p.T, kTile<64>) : 0) * p.C * 4 + 255) / 256 * 256;
 }
 
-template <typename T, typename TG, int VEC, int GVEC, bool kPacked>
+template <typename T, typename TG, int CH, int VEC, int GVEC, bool kPacked>
 cudaError_t launch(const GatedParams& p, cudaStream_t st) {
-    const int blocks = (p.C + kGatedCh - 1) / kGatedCh;
+    const int blocks = (p.C + CH - 1) / CH;
     const int64_t groups = (int64_t)blocks * p.B;
     float* const partial = static_cast<float*>(p.ws);
     int parts = 0;
     if (groups > 0) {
-        const auto kern = gated_bwd_kernel<T, TG, VEC, GVEC, kPacked>;
-        constexpr int smem = kStages * kStageBytes<T, TG>;
+        const auto kern = gated_bwd_kernel<T, TG, CH, VEC, GVEC, kPacked>;
+        constexpr int smem = kStages * kStageBytes<T, TG, CH>;
         static ClusterRoom room;
         static std::atomic<uint64_t> allowed;
-    cudaError_t e = allow_shared(kern, smem, allowed);
+        cudaError_t e = allow_shared(kern, smem, allowed);
         if (e != cudaSuccess) return e;
-        const int cluster = room.size_for(kern, groups, p.T, kTile, kThreads, smem);
+        const int cluster = room.size_for(kern, groups, p.T, kTile<CH>, kThreads, smem);
         e = launch_clusters(kern, groups * cluster, cluster, kThreads, smem, st, p, partial, cluster, blocks);
         if (e != cudaSuccess) return e;
         parts = p.T > 0 ? p.B * cluster : 0;
     }
     return tc::launch_dependent(gated_dlam_kernel, (unsigned)((p.C + 127) / 128), 128, 0, st, partial, parts, p.lam, p.decay, p.C, p.dlam);
 }
-template <typename T, typename TG, int VEC, int GVEC>
+template <typename T, typename TG, int CH, int VEC, int GVEC>
 cudaError_t launch_packed(const GatedParams& p, cudaStream_t st) {
-    return p.cu ? launch<T, TG, VEC, GVEC, true>(p, st) : launch<T, TG, VEC, GVEC, false>(p, st);
+    return p.cu ? launch<T, TG, CH, VEC, GVEC, true>(p, st) : launch<T, TG, CH, VEC, GVEC, false>(p, st);
+}
+template <typename T, typename TG, int VEC, int GVEC>
+cudaError_t launch_wide(const GatedParams& p, cudaStream_t st) {
+    const int ch = gated_channels(p);
+    return ch == 64 ? launch_packed<T, TG, 64, VEC, GVEC>(p, st) : ch == 32 ? launch_packed<T, TG, 32, VEC, GVEC>(p, st) : launch_packed<T, TG, 16, VEC, GVEC>(p, st);
 }
 
 }  // namespace
@@ -357,15 +384,15 @@ cudaError_t gated_scan_bwd(kda_dtype dt, kda_dtype gdt, const GatedParams& given
     const bool wide = pairs && gated_pieces(p, es, 16) && (int64_t)p.C * gs % 16 == 0 && kda_host::aligned16(p.dy);
     const bool narrow = pairs && gated_pieces(p, es, 2 * es) && (uintptr_t)p.dy % (2 * gs) == 0;
     if (dt == KDA_F32) {
-        if (wide) return launch_packed<float, float, 4, 4>(p, st);
-        return narrow ? launch_packed<float, float, 2, 2>(p, st) : launch_packed<float, float, 1, 1>(p, st);
+        if (wide) return launch_wide<float, float, 4, 4>(p, st);
+        return narrow ? launch_packed<float, float, 64, 2, 2>(p, st) : launch_packed<float, float, 64, 1, 1>(p, st);
     }
     if (gdt == KDA_F32) {
-        if (wide) return launch_packed<__nv_bfloat16, float, 8, 4>(p, st);
-        return narrow ? launch_packed<__nv_bfloat16, float, 2, 2>(p, st) : launch_packed<__nv_bfloat16, float, 1, 1>(p, st);
+        if (wide) return launch_wide<__nv_bfloat16, float, 8, 4>(p, st);
+        return narrow ? launch_packed<__nv_bfloat16, float, 64, 2, 2>(p, st) : launch_packed<__nv_bfloat16, float, 64, 1, 1>(p, st);
     }
-    if (wide) return launch_packed<__nv_bfloat16, __nv_bfloat16, 8, 8>(p, st);
-    return narrow ? launch_packed<__nv_bfloat16, __nv_bfloat16, 2, 2>(p, st) : launch_packed<__nv_bfloat16, __nv_bfloat16, 1, 1>(p, st);
+    if (wide) return launch_wide<__nv_bfloat16, __nv_bfloat16, 8, 8>(p, st);
+    return narrow ? launch_packed<__nv_bfloat16, __nv_bfloat16, 64, 2, 2>(p, st) : launch_packed<__nv_bfloat16, __nv_bfloat16, 64, 1, 1>(p, st);
 }
 
 }  // namespace kda
