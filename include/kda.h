@@ -647,7 +647,8 @@ KDA_API kda_status kda_ssm_scan_bwd(const void *u, int64_t ldu, const void *delt
  *  cu_seqlens, B, T, N   as kda_short_conv_fwd; rows that belong to no sequence are left as
  *           they are.
  *  states   fp32 [B, ceil(T / 32), C] or NULL: the state before tokens 0, 32, 64 ... of each
- *           batch row (zeros where a sequence begins), for kda_gated_scan_bwd.
+ *           batch row (zeros where a sequence begins; left as it is before tokens that belong
+ *           to no sequence), for kda_gated_scan_bwd.
  * B ceil(C / 64) <= 2^28 - 1.
  */
 KDA_API kda_status kda_gated_scan_fwd(const void *x, int64_t ldx, const void *r, int64_t ldr, const void *i,

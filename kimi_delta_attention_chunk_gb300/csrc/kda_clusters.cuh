@@ -91,20 +91,23 @@ cudaError_t allow_shared(K kern, int bytes, std::atomic<uint64_t>& done) {
     return e;
 }
 
-// Launches a kernel (its shared memory set) in clusters of `cluster` blocks.
+// Launches a kernel (its shared memory set) in clusters of `cluster` blocks.  dependent: it may begin while the one before it on the
+// stream still runs.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_clusters(void (*kern)(KArgs...), int64_t grid, int cluster, int threads, int smem, cudaStream_t st, Args... args) {
+cudaError_t launch_clusters(void (*kern)(KArgs...), int64_t grid, int cluster, int threads, int smem, bool dependent, cudaStream_t st, Args... args) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = threads;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = cluster;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = dependent ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
 }
 

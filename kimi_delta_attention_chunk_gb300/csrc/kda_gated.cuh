@@ -245,14 +245,56 @@ __device__ __forceinline__ void store_state(float* p, int64_t at, f2 h, int n) {
     if (n > 1) p[at + 1] = b;
 }
 
+// The rows that a block takes, [row0, row0 + T), and the tokens of them that count, [first, last).
+struct Stretch {
+    int64_t row0;
+    int T, first, last;
+};
+// Sequence n of a stream by itself: from the state that is left to the backward pass before its first token.  kEdges: with the stream's
+// rows that belong to no sequence.  A sequence without tokens has no rows, but for those.
+template <bool kEdges>
+__device__ __forceinline__ Stretch sequence_rows(const GatedParams& p, int n) {
+    const int begin = min(max(__ldg(p.cu + n), 0), p.T), end = min(max(__ldg(p.cu + n + 1), begin), p.T);
+    const int from = kEdges && n == 0 ? 0 : begin / kGatedBlock * kGatedBlock, to = kEdges && n == p.N - 1 ? p.T : end;
+    const bool none = begin == end && !(kEdges && (n == 0 || (n == p.N - 1 && end < p.T)));
+    return {from, none ? 0 : to - from, begin - from, end - from};
+}
+
+// Whether a sequence of the stream has more than `most` tokens (every thread of the block calls it).
+__device__ __forceinline__ bool any_longer(const GatedParams& p, int most) {
+    bool found = false;
+    for (int n = threadIdx.x; n < p.N; n += blockDim.x) {
+        const int begin = min(max(__ldg(p.cu + n), 0), p.T), end = min(max(__ldg(p.cu + n + 1), 0), p.T);
+        found |= end - begin > most;
+    }
+    return __syncthreads_or(found) != 0;
+}
+
+// Sequences that are packed in one stream have blocks of their own, unless they are so short that these would be mostly idle (`mean`
+// tokens), or one of them takes more than two and a half times the share of a machine that works evenly: its blocks would still run when
+// all others are done.  Only the offsets say so, on the device: both kernels are launched, and one of them returns at once.
+// (bf16 with gates, 4096 channels, forward and backward: 16 sequences of 1 to 700 tokens 67 and 108 us with blocks of their own, 80 and 154 as one
+// stream; 128 x 128 151 and 293, 256 and 580; 256 x 64 302 and 336, 278 and 600; 512 x 32 591 and 451, 282 and 606; 1024 x 16 1169 and 817, 287 and
+// 667; one of 16129 among 15 of 17 362 and 1141, 185 and 410)
+inline bool gated_each(const GatedParams& p, int mean) { return p.cu && p.N > 0 && p.N <= p.T / mean; }
+inline int longest_of(const GatedParams& p, int64_t blocks) {
+    const int64_t most = p.T * blocks * 5 / (4 * kSms);
+    return p.N > 1 && most < p.T ? (int)most : p.T;
+}
+// The blocks of a sequence: one where there is one an SM anyway.
+template <typename K>
+int gated_cluster(ClusterRoom& room, K kern, int64_t groups, int T, int tile, int threads, int smem) {
+    return groups > kSms ? 1 : room.size_for(kern, groups, T, tile, threads, smem);
+}
+
 // Channels of a block. 64 where blocks of them that take a whole sequence each come to one and a half an SM; else 32 where those do
 // (2 x 8192 x 4096 bf16 forward 148 -> 136 us, backward 2 x 2048 x 4096 86 -> 75); else blocks share a sequence as a cluster whatever
 // their width, and the widest rows cost least (1 x 16384 x 4096: 151, 155 and 171 us with 64, 32 and 16) as long as clusters of eight
 // fill the machine (1 x 65536 x 512: 213, 155, 104).
-inline int gated_channels(const GatedParams& p) {
+inline int gated_channels(const GatedParams& p, int streams) {
     for (const int blocks : {1, kMostCluster})
         for (const int ch : {64, 32})
-            if ((int64_t)((p.C + ch - 1) / ch) * p.B * blocks >= kSms * 3 / 2) return ch;
+            if ((int64_t)((p.C + ch - 1) / ch) * streams * blocks >= kSms * 3 / 2) return ch;
     return 16;
 }
 

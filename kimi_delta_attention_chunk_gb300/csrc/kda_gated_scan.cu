@@ -17,6 +17,7 @@ namespace kda {
 namespace {
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kMean = 96;  // tokens of a sequence that has its own blocks, on average at least
 template <typename T, int CH>
 using LanesOf = Lanes<CH, sizeof(T) == 2 ? 16 : 8>;  // tokens of a strip
 template <typename T, int CH>
@@ -27,10 +28,10 @@ constexpr int kSmem = (kRows ? 4 : 3) * kWarps * LanesOf<T, CH>::kPart * (int)si
 
 // kPacked: sequences by offsets, else a stream for each batch row.  kRows: y and the final states, else only the states that the
 // backward pass starts from.  VEC: elements of a piece of x, r, i and z; with more than one, pairs of channels of y are whole and aligned.
-template <typename T, int CH, int VEC, bool kPacked, bool kRows>
-__global__ void __launch_bounds__(kThreads, 2) gated_fwd_kernel(GatedParams p, int cluster, int blocks) {
-    using L = LanesOf<T, CH>;
-    constexpr int STRIP = sizeof(T) == 2 ? 16 : 8, TT = kTileOf<T, CH>, PART = L::kPart;
+template <typename E, int CH, int VEC, bool kPacked, bool kRows>
+__global__ void __launch_bounds__(kThreads, 2) gated_fwd_kernel(GatedParams p, int cluster, int blocks, int longest) {
+    using L = LanesOf<E, CH>;
+    constexpr int STRIP = sizeof(E) == 2 ? 16 : 8, TT = kTileOf<E, CH>, PART = L::kPart;
     extern __shared__ __align__(128) char shared[];
     __shared__ Affine maps[2][kWarps][L::kPairs];
     __shared__ Affine peers[2][kMostCluster][L::kPairs];
@@ -38,20 +39,24 @@ __global__ void __launch_bounds__(kThreads, 2) gated_fwd_kernel(GatedParams p, i
     __shared__ Marks<kPacked ? L::kTokens : 1> all_marks[kWarps];
     __shared__ int32_t offsets[kPacked ? kCachedOffsets : 1];
 
+    if constexpr (kPacked) tc::grid_dep_wait();
+    else tc::grid_dep_launch();
+    if (p.cu && longest < p.T && any_longer(p, longest) != kPacked) return;
     const int pair = L::pair(), strip = L::strip(), w = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0);
     const int rank = cluster > 1 ? (int)cluster_rank() : 0;
     const int group = blockIdx.x / cluster, b = group / blocks, c0 = group % blocks * CH;
     const int c = c0 + 2 * pair, has = p.C - c0, n2 = min(2, p.C - c);  // channels of this lane: 2, 1 or none (<= 0)
-    const Offsets m(p.cu, p.N, p.T, offsets);
-    const int first = kPacked ? m.first() : 0, last = kPacked ? m.last() : p.T;
+    const Offsets m(kPacked ? p.cu : nullptr, p.N, p.T, offsets);
+    const Stretch mine_of = kPacked ? Stretch{0, p.T, m.first(), m.last()} : p.cu ? sequence_rows<false>(p, b) : Stretch{(int64_t)b * p.T, p.T, 0, p.T};
+    const int T = mine_of.T, first = mine_of.first, last = mine_of.last;
+    const int64_t row0 = mine_of.row0;
     const int stride = TT * cluster;  // tokens between a block's tiles
-    const int steps = (int)(((int64_t)p.T + stride - 1) / stride);
-    const int64_t row0 = (int64_t)b * p.T;
+    const int steps = (int)(((int64_t)T + stride - 1) / stride);
     int w0 = rank * TT + w * L::kTokens, s0 = w0 + strip * STRIP;  // this warp's first token, this strip's
 
     // this warp's rows: x, r, i and z
-    T* const mine = reinterpret_cast<T*>(shared) + w * (kRows ? 4 : 3) * PART;
-    using F = Feed<T, CH, STRIP, VEC>;
+    E* const mine = reinterpret_cast<E*>(shared) + w * (kRows ? 4 : 3) * PART;
+    using F = Feed<E, CH, STRIP, VEC>;
     F fx(p.x, p.ldx, row0 + w0, c0, stride), fr(p.r, p.ldr, row0 + w0, c0, stride), fi(p.i, p.ldi, row0 + w0, c0, stride);
     F fz(p.z, p.ldz, row0 + w0, c0, stride);
     auto request = [&](int rows) {
@@ -66,21 +71,24 @@ __global__ void __launch_bounds__(kThreads, 2) gated_fwd_kernel(GatedParams p, i
         }
         copies_commit();
     };
-    request(p.T - w0);
+    request(T - w0);
 
     const f2 rate = pack(n2 > 0 ? gated_rate(__ldg(p.lam + c), p.decay) : 0.f, n2 > 1 ? gated_rate(__ldg(p.lam + c + 1), p.decay) : 0.f);
     const bool small = __all_sync(0xffffffffu, small_rate(rate)) != 0;
     // sequences without tokens hand their states on
     if (kRows && p.final_state) {
-        const int warps = kWarps * cluster;
-        for (int n0 = (w * cluster + rank) * 32; n0 < p.N; n0 += warps * 32) {
-            if (!kPacked && p.T > 0) break;
-            const int n = n0 + (int)threadIdx.x % 32;
-            unsigned empty = __ballot_sync(0xffffffffu, n < p.N && (!kPacked || m.end(n) <= m.begin(n)));
-            for (; empty; empty &= empty - 1) {
-                const int64_t at = (int64_t)(n0 + __ffs(empty) - 1) * p.C + c;
-                store_state(p.final_state, at, state_pair(p.initial, at, n2), n2);
+        if constexpr (kPacked) {
+            for (int n0 = (w * cluster + rank) * 32; n0 < p.N; n0 += kWarps * cluster * 32) {
+                const int n = n0 + (int)threadIdx.x % 32;
+                unsigned empty = __ballot_sync(0xffffffffu, n < p.N && m.end(n) <= m.begin(n));
+                for (; empty; empty &= empty - 1) {
+                    const int64_t at = (int64_t)(n0 + __ffs(empty) - 1) * p.C + c;
+                    store_state(p.final_state, at, state_pair(p.initial, at, n2), n2);
+                }
             }
+        } else if (T == 0 && rank == 0 && w == 0) {
+            const int64_t at = (int64_t)b * p.C + c;
+            store_state(p.final_state, at, state_pair(p.initial, at, n2), n2);
         }
     }
     f2 carry = kPacked ? 0ull : state_pair(p.initial, (int64_t)b * p.C + c, n2);
@@ -93,12 +101,13 @@ __global__ void __launch_bounds__(kThreads, 2) gated_fwd_kernel(GatedParams p, i
     Walk<kPacked ? L::kTokens : 1> walk;
     const int* const starts = all_marks[w].start + (kPacked ? strip * STRIP : 0);
     const int* const lasts = all_marks[w].end + (kPacked ? strip * STRIP : 0);
-    T* to = static_cast<T*>(p.y) + (row0 + s0) * p.C + c;
+    const int64_t block0 = p.cu ? row0 / kGatedBlock : (int64_t)b * ((p.T + kGatedBlock - 1) / kGatedBlock);
+    E* to = static_cast<E*>(p.y) + (row0 + s0) * p.C + c;
     for (int it = 0; it < steps; ++it, w0 += stride, s0 += stride, to += (int64_t)stride * p.C) {
         const int buf = it & 1;
         if (kRows && p.z) {
-            if (p.T - w0 >= L::kTokens && has >= CH) fz.request(mine + 3 * PART);
-            else fz.request(mine + 3 * PART, p.T - w0, has);
+            if (T - w0 >= L::kTokens && has >= CH) fz.request(mine + 3 * PART);
+            else fz.request(mine + 3 * PART, T - w0, has);
         }
         copies_commit();
         if constexpr (kPacked) walk.look(m, w0, it * stride, (it + 1) * stride, all_marks[w]);
@@ -106,7 +115,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_fwd_kernel(GatedParams p, i
         // the first walk: decays and inputs, and the strip's map
         copies_wait<1>();
         __syncwarp();
-        const T* const in = mine + L::place();
+        const E* const in = mine + L::place();
         f2 a[STRIP], u[STRIP];
         auto first_walk = [&](auto small_rates) {
 #pragma unroll
@@ -120,11 +129,11 @@ __global__ void __launch_bounds__(kThreads, 2) gated_fwd_kernel(GatedParams p, i
         if (small) first_walk(std::true_type{});
         else first_walk(std::false_type{});
         __syncwarp();
-        request(p.T - w0 - stride);
-        if (w0 + L::kTokens > p.T) {
+        request(T - w0 - stride);
+        if (w0 < first || w0 + L::kTokens > last) {
 #pragma unroll
             for (int j = 0; j < STRIP; ++j)
-                if (s0 + j >= p.T) a[j] = both(1.f), u[j] = 0ull;
+                if (s0 + j < first || s0 + j >= last) a[j] = both(1.f), u[j] = 0ull;
         }
         Affine map{a[0], u[0]};
         if (!kPacked || clear) {
@@ -184,18 +193,18 @@ __global__ void __launch_bounds__(kThreads, 2) gated_fwd_kernel(GatedParams p, i
         };
         f2 h = !kPacked || wide ? fold(std::false_type{}) : fold(std::true_type{});
         static_assert(kGatedBlock % STRIP == 0, "blocks begin at strips");
-        if (p.states && s0 % kGatedBlock == 0 && s0 < p.T) {
-            const bool begins = s0 == 0 || (kPacked && !clear && starts[0] >= 0);
-            const int64_t block = (int64_t)b * ((p.T + kGatedBlock - 1) / kGatedBlock) + s0 / kGatedBlock;
+        if (p.states && s0 % kGatedBlock == 0 && s0 >= first && s0 < last) {
+            const bool begins = s0 == first || (kPacked && !clear && starts[0] >= 0);
+            const int64_t block = block0 + s0 / kGatedBlock;
             store_state(p.states, block * p.C + c, begins ? 0ull : h, n2);
         }
         if constexpr (kRows) {
             copies_wait<1>();  // z
             __syncwarp();
-            const T* const zin = in + 3 * PART;
+            const E* const zin = in + 3 * PART;
             if (VEC > 1 && (!kPacked || clear) && w0 >= first && w0 + L::kTokens <= last) {
                 // all of the warp's tokens are of one sequence
-                T* at = to;
+                E* at = to;
                 auto second_walk = [&](auto gated) {
 #pragma unroll
                     for (int j = 0; j < STRIP; ++j, at += p.C) {
@@ -205,12 +214,12 @@ __global__ void __launch_bounds__(kThreads, 2) gated_fwd_kernel(GatedParams p, i
                             const f2 z = pair_at(zin + j * CH);
                             y = mul2(h, mul2(z, gate2(z)));
                         }
-                        store_pair<T, true>(at, y, n2);
+                        store_pair<E, true>(at, y, n2);
                     }
                 };
                 if (p.z) second_walk(std::true_type{});
                 else second_walk(std::false_type{});
-                if (!kPacked && p.final_state && s0 + STRIP == p.T) store_state(p.final_state, (int64_t)b * p.C + c, h, n2);
+                if (!kPacked && p.final_state && s0 + STRIP == T) store_state(p.final_state, (int64_t)b * p.C + c, h, n2);
             } else {
 #pragma unroll
                 for (int j = 0; j < STRIP; ++j) {
@@ -218,10 +227,10 @@ __global__ void __launch_bounds__(kThreads, 2) gated_fwd_kernel(GatedParams p, i
                     const int t = s0 + j;
                     if (t >= first && t < last) {
                         const f2 z = pair_at(zin + j * CH);
-                        store_pair<T, false>(to + (int64_t)j * p.C, p.z ? mul2(h, mul2(z, gate2(z))) : h, n2);
+                        store_pair<E, false>(to + (int64_t)j * p.C, p.z ? mul2(h, mul2(z, gate2(z))) : h, n2);
                     }
                     if (p.final_state) {
-                        const int n = kPacked ? (clear ? -1 : lasts[j]) : (t == p.T - 1 ? b : -1);
+                        const int n = kPacked ? (clear ? -1 : lasts[j]) : (t == T - 1 ? b : -1);
                         if (n >= 0) store_state(p.final_state, (int64_t)n * p.C + c, h, n2);
                     }
                 }
@@ -235,28 +244,42 @@ __global__ void __launch_bounds__(kThreads, 2) gated_fwd_kernel(GatedParams p, i
     }
 }
 
+// longest: in, of the kernel before, which leaves the work to this one where a sequence is longer (no such kernel: p.T); out, of this one.
 template <typename T, int CH, int VEC, bool kPacked, bool kRows>
-cudaError_t launch(const GatedParams& p, cudaStream_t st) {
+cudaError_t launch(const GatedParams& p, int streams, int& longest, cudaStream_t st) {
     const int blocks = (p.C + CH - 1) / CH;
-    const int64_t groups = (int64_t)blocks * p.B;
+    const int64_t groups = (int64_t)blocks * streams;
     const auto kern = gated_fwd_kernel<T, CH, VEC, kPacked, kRows>;
     constexpr int smem = kSmem<T, CH, kRows>;
     static ClusterRoom room;
     static std::atomic<uint64_t> allowed;
     const cudaError_t e = allow_shared(kern, smem, allowed);
     if (e != cudaSuccess) return e;
-    const int cluster = room.size_for(kern, groups, p.T, kTileOf<T, CH>, kThreads, smem);
-    return launch_clusters(kern, groups * cluster, cluster, kThreads, smem, st, p, cluster, blocks);
+    const int cluster = gated_cluster(room, kern, groups, p.T, kTileOf<T, CH>, kThreads, smem);
+    if (!kPacked) longest = p.cu ? longest_of(p, (int64_t)blocks * cluster) : p.T;
+    return launch_clusters(kern, groups * cluster, cluster, kThreads, smem, kPacked && longest < p.T, st, p, cluster, blocks, longest);
 }
-template <typename T, int CH, int VEC>
-cudaError_t launch_rows(const GatedParams& p, cudaStream_t st) {
-    if (p.y || p.final_state) return p.cu ? launch<T, CH, VEC, true, true>(p, st) : launch<T, CH, VEC, false, true>(p, st);
-    return p.cu ? launch<T, CH, VEC, true, false>(p, st) : launch<T, CH, VEC, false, false>(p, st);
+template <typename T, int VEC, bool kPacked, bool kRows>
+cudaError_t launch_channels(const GatedParams& p, int streams, int& longest, cudaStream_t st) {
+    if constexpr (VEC * sizeof(T) == 16) {
+        const int ch = gated_channels(p, streams);
+        if (ch == 32) return launch<T, 32, VEC, kPacked, kRows>(p, streams, longest, st);
+        if (ch == 16) return launch<T, 16, VEC, kPacked, kRows>(p, streams, longest, st);
+    }
+    return launch<T, 64, VEC, kPacked, kRows>(p, streams, longest, st);
+}
+template <typename T, int VEC, bool kRows>
+cudaError_t launch_streams(const GatedParams& p, cudaStream_t st) {
+    int longest = p.T;
+    if (!p.cu || gated_each(p, kMean)) {
+        const cudaError_t e = launch_channels<T, VEC, false, kRows>(p, p.cu ? p.N : p.B, longest, st);
+        if (e != cudaSuccess || longest == p.T) return e;
+    }
+    return launch_channels<T, VEC, true, kRows>(p, 1, longest, st);
 }
 template <typename T, int VEC>
-cudaError_t launch_wide(const GatedParams& p, cudaStream_t st) {
-    const int ch = gated_channels(p);
-    return ch == 64 ? launch_rows<T, 64, VEC>(p, st) : ch == 32 ? launch_rows<T, 32, VEC>(p, st) : launch_rows<T, 16, VEC>(p, st);
+cudaError_t launch_rows(const GatedParams& p, cudaStream_t st) {
+    return p.y || p.final_state ? launch_streams<T, VEC, true>(p, st) : launch_streams<T, VEC, false>(p, st);
 }
 
 }  // namespace
@@ -265,13 +288,13 @@ cudaError_t gated_scan_fwd(kda_dtype dt, const GatedParams& p, cudaStream_t st) 
     const int es = dt == KDA_BF16 ? 2 : 4;
     const bool pairs = p.C % 2 == 0 && (uintptr_t)p.y % (2 * es) == 0;
     if (dt == KDA_BF16) {
-        if (pairs && gated_pieces(p, es, 16)) return launch_wide<__nv_bfloat16, 8>(p, st);
-        if (pairs && gated_pieces(p, es, 4)) return launch_rows<__nv_bfloat16, 64, 2>(p, st);
-        return launch_rows<__nv_bfloat16, 64, 1>(p, st);
+        if (pairs && gated_pieces(p, es, 16)) return launch_rows<__nv_bfloat16, 8>(p, st);
+        if (pairs && gated_pieces(p, es, 4)) return launch_rows<__nv_bfloat16, 2>(p, st);
+        return launch_rows<__nv_bfloat16, 1>(p, st);
     }
-    if (pairs && gated_pieces(p, es, 16)) return launch_wide<float, 4>(p, st);
-    if (pairs && gated_pieces(p, es, 8)) return launch_rows<float, 64, 2>(p, st);
-    return launch_rows<float, 64, 1>(p, st);
+    if (pairs && gated_pieces(p, es, 16)) return launch_rows<float, 4>(p, st);
+    if (pairs && gated_pieces(p, es, 8)) return launch_rows<float, 2>(p, st);
+    return launch_rows<float, 1>(p, st);
 }
 
 }  // namespace kda

@@ -10,6 +10,7 @@
 // maps folded through shared memory, tiles side by side in a cluster.  What an element needs (a, u, m si, si x a^2 / m, sr, 1 - si, yb, dy
 // silu'(z)) stays in registers between the two walks: 128 a thread, two blocks an SM.  Without those states a first pass of the forward
 // kernel makes them (x, r and i are then read twice).  dlam's sums over tokens: one partial sum a block, added in a fixed order.
+#include <algorithm>
 #include <type_traits>
 
 #include "kda_gated.cuh"
@@ -20,6 +21,7 @@ namespace kda {
 namespace {
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kMean = 32;   // tokens of a sequence that has its own blocks, on average at least
 constexpr int kStrip = 4;
 template <int CH>
 constexpr int kTile = kWarps * Lanes<CH, kStrip>::kTokens;
@@ -32,7 +34,7 @@ constexpr int kStageBytes = kWarps * Lanes<CH, kStrip>::kPart * (4 * (int)sizeof
 
 // VEC, GVEC: elements of a piece of x, r, i and z, and of dy; with VEC > 1, pairs of channels of the outputs are whole and aligned.
 template <typename T, typename TG, int CH, int VEC, int GVEC, bool kPacked>
-__global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(GatedParams p, float* partial, int cluster, int blocks) {
+__global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(GatedParams p, float* partial, int cluster, int blocks, int longest) {
     using L = Lanes<CH, kStrip>;
     constexpr int PART = L::kPart, TT = kTile<CH>, kStage = kStageBytes<T, TG, CH>;
     extern __shared__ __align__(128) char shared[];
@@ -45,15 +47,20 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(GatedParams p, f
     __shared__ Marks<kPacked ? L::kTokens : 1> all_marks[kWarps];
     __shared__ int32_t offsets[kPacked ? kCachedOffsets : 1];
 
+    if constexpr (kPacked) tc::grid_dep_wait();
+    else tc::grid_dep_launch();
+    if (p.cu && longest < p.T && any_longer(p, longest) != kPacked) return;
     const int pair = L::pair(), strip = L::strip(), w = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0);
     const int rank = cluster > 1 ? (int)cluster_rank() : 0;
     const int group = blockIdx.x / cluster, b = group / blocks, c0 = group % blocks * CH;
     const int c = c0 + 2 * pair, has = p.C - c0, n2 = min(2, p.C - c);  // channels of this lane: 2, 1 or none (<= 0)
-    const Offsets m(p.cu, p.N, p.T, offsets);
-    const int first = kPacked ? m.first() : 0, last = kPacked ? m.last() : p.T;
+    const Offsets m(kPacked ? p.cu : nullptr, p.N, p.T, offsets);
+    const Stretch rows_of = kPacked ? Stretch{0, p.T, m.first(), m.last()} : p.cu ? sequence_rows<true>(p, b) : Stretch{(int64_t)b * p.T, p.T, 0, p.T};
+    const int S = rows_of.T, first = rows_of.first, last = rows_of.last;
+    const int from = kPacked || !p.cu || b == 0 ? 0 : first;  // the first row that is this block's to write
+    const int64_t row0 = rows_of.row0;
     const int stride = TT * cluster;  // tokens between a block's tiles
-    const int steps = (int)(((int64_t)p.T + stride - 1) / stride);
-    const int64_t row0 = (int64_t)b * p.T;
+    const int steps = (int)(((int64_t)S + stride - 1) / stride);
     // this warp's first token and this strip's: tiles are taken from the stream's end
     int w0 = (steps - 1) * stride + rank * TT + w * L::kTokens, s0 = w0 + strip * kStrip;
 
@@ -64,7 +71,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(GatedParams p, f
     F fz(p.z, p.ldz, row0 + w0, c0, -stride);
     Feed<TG, CH, kStrip, GVEC> fy(p.dy, p.C, row0 + w0, c0, -stride);
     auto request = [&](int it) {
-        const int rows = p.T - (w0 - stride);
+        const int rows = S - (w0 - stride);
         T* const in = reinterpret_cast<T*>(mine + (it & 1) * kStage);
         if (it < steps) {
             TG* const dys = reinterpret_cast<TG*>(in + 4 * PART);
@@ -92,15 +99,18 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(GatedParams p, f
     const bool small = __all_sync(0xffffffffu, small_rate(rate)) != 0;
     // through sequences without tokens the gradient goes as it comes
     if (p.dinitial) {
-        const int warps = kWarps * cluster;
-        for (int n0 = (w * cluster + rank) * 32; n0 < p.N; n0 += warps * 32) {
-            if (!kPacked && p.T > 0) break;
-            const int n = n0 + (int)threadIdx.x % 32;
-            unsigned empty = __ballot_sync(0xffffffffu, n < p.N && (!kPacked || m.end(n) <= m.begin(n)));
-            for (; empty; empty &= empty - 1) {
-                const int64_t at = (int64_t)(n0 + __ffs(empty) - 1) * p.C + c;
-                store_state(p.dinitial, at, state_pair(p.dfinal, at, n2), n2);
+        if constexpr (kPacked) {
+            for (int n0 = (w * cluster + rank) * 32; n0 < p.N; n0 += kWarps * cluster * 32) {
+                const int n = n0 + (int)threadIdx.x % 32;
+                unsigned empty = __ballot_sync(0xffffffffu, n < p.N && m.end(n) <= m.begin(n));
+                for (; empty; empty &= empty - 1) {
+                    const int64_t at = (int64_t)(n0 + __ffs(empty) - 1) * p.C + c;
+                    store_state(p.dinitial, at, state_pair(p.dfinal, at, n2), n2);
+                }
             }
+        } else if (S == 0 && rank == 0 && w == 0) {
+            const int64_t at = (int64_t)b * p.C + c;
+            store_state(p.dinitial, at, state_pair(p.dfinal, at, n2), n2);
         }
     }
     f2 carry = kPacked ? 0ull : state_pair(p.dfinal, (int64_t)b * p.C + c, n2), dlam = 0ull;
@@ -113,15 +123,15 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(GatedParams p, f
 
     // where this warp's first row of an output and the tile's state are; all move up by a stride of rows a step
     int64_t off = (row0 + s0) * p.C + c;
-    const float* left = p.states + ((int64_t)b * ((p.T + kGatedBlock - 1) / kGatedBlock) + (w0 - w * L::kTokens) / kGatedBlock) * p.C + c;
+    const float* left = p.states + ((p.cu ? row0 / kGatedBlock : (int64_t)b * ((p.T + kGatedBlock - 1) / kGatedBlock)) + (w0 - w * L::kTokens) / kGatedBlock) * p.C + c;
     Walk<kPacked ? L::kTokens : 1> walk;
     const int* const starts = all_marks[w].start + (kPacked ? strip * kStrip : 0);
     const int* const lasts = all_marks[w].end + (kPacked ? strip * kStrip : 0);
     for (int it = 0; it < steps; ++it, w0 -= stride, s0 -= stride, off -= (int64_t)stride * p.C, left -= (int64_t)(stride / kGatedBlock) * p.C) {
         const int t0 = w0 - w * L::kTokens, buf = it & 1;
         f2 h = 0ull;
-        if (t0 < p.T) {
-            if (!kPacked && t0 == 0) h = state_pair(p.initial, (int64_t)b * p.C + c, n2);
+        if (t0 < S) {
+            if (!kPacked && t0 <= first) h = state_pair(p.initial, (int64_t)b * p.C + c, n2);
             else if (VEC > 1) h = n2 > 0 ? *reinterpret_cast<const f2*>(left) : 0ull;
             else h = pack(n2 > 0 ? left[0] : 0.f, n2 > 1 ? left[1] : 0.f);
         }
@@ -149,9 +159,14 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(GatedParams p, f
                 yb[j] = pair_at(dys + j * CH);
             }
         };
-        if (small) gates(std::true_type{});
-        else gates(std::false_type{});
-        if (p.z) {
+        // in a sequence's first and last tile some warps have nothing to do (skipped at this width only: 4 x 4096 x 4096 304 -> 286 us,
+        // but with 32 channels 2 x 2048 x 4096 76 -> 81, by what the compiler keeps in registers)
+        const bool idle = !kPacked && CH == 64 && (w0 + L::kTokens <= from || w0 >= S);
+        if (!idle) {
+            if (small) gates(std::true_type{});
+            else gates(std::false_type{});
+        }
+        if (p.z && !idle) {
 #pragma unroll
             for (int j = 0; j < kStrip; ++j) {
                 const f2 z = pair_at(in + 3 * PART + j * CH), s = gate2(z), silu = mul2(z, s);
@@ -159,10 +174,10 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(GatedParams p, f
                 yb[j] = mul2(yb[j], silu);
             }
         }
-        if (w0 + L::kTokens > p.T) {
+        if (w0 < first || w0 + L::kTokens > last) {
 #pragma unroll
             for (int j = 0; j < kStrip; ++j)
-                if (s0 + j >= p.T) a[j] = both(1.f), u[j] = yb[j] = 0ull;
+                if (s0 + j < first || s0 + j >= last) a[j] = both(1.f), u[j] = yb[j] = 0ull;
         }
         // the strip's maps forwards (cut where a sequence begins) and backwards (cut where one ends)
         Affine fore, rear;
@@ -277,12 +292,12 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(GatedParams p, f
                 store_pair<TG, true>(dr, mul2(mul2(part, rate), rest2(sr[j])), n2);
                 store_pair<TG, true>(di, mul2(dh, ui[j]), n2);
             }
-            if (!kPacked && s0 == 0 && p.dinitial) store_state(p.dinitial, (int64_t)b * p.C + c, g, n2);
-        } else {
+            if (!kPacked && s0 == from && p.dinitial) store_state(p.dinitial, (int64_t)b * p.C + c, g, n2);
+        } else if (!idle) {
 #pragma unroll
             for (int j = kStrip - 1; j >= 0; --j) {
                 const int t = s0 + j;
-                if (t >= p.T) continue;
+                if (t < from || t >= S) continue;
                 if (kPacked && !clear && lasts[j] >= 0) g = 0ull;
                 const f2 dh = add2(yb[j], g);
                 f2 part = mul2(mul2(dh, wm[j]), sr[j]), dx = mul2(dh, wx[j]), dr = mul2(mul2(part, rate), rest2(sr[j])), di = mul2(dh, ui[j]);
@@ -295,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(GatedParams p, f
                 store_pair<TG, false>(static_cast<TG*>(p.di) + o, di, n2);
                 if (p.z) store_pair<TG, false>(static_cast<TG*>(p.dz) + o, gz[j], n2);
                 if (p.dinitial) {
-                    const int n = kPacked ? (clear ? -1 : starts[j]) : (t == 0 ? b : -1);
+                    const int n = kPacked ? (clear ? -1 : starts[j]) : (t == from ? b : -1);
                     if (n >= 0) store_state(p.dinitial, (int64_t)n * p.C + c, g, n2);
                 }
             }
@@ -308,57 +323,75 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(GatedParams p, f
     static_assert(sizeof(maps) >= kThreads * sizeof(f2), "a part each thread");
     parts[w * 32 + threadIdx.x % 32] = dlam;
     __syncthreads();
-    if (w == 0 && strip == 0 && steps > 0) {
+    if (w == 0 && strip == 0 && p.T > 0) {
         f2 sum = 0ull;
         for (int k = 0; k < kWarps * L::kStrips; ++k) sum = add2(sum, parts[k * L::kPairs + pair]);
         store_state(partial + ((int64_t)b * cluster + rank) * p.C, c, sum, n2);
     }
 }
 
-// dlam from the blocks' partial sums.
-__global__ void __launch_bounds__(128) gated_dlam_kernel(const float* partial, int parts, const float* lam, float decay, int C, float* dlam) {
-    const int c = blockIdx.x * 128 + threadIdx.x;
+// dlam from the blocks' partial sums: `parts` of them, or `packed` where a sequence is longer than `longest`.  A block has 32 channels.
+constexpr int kSummers = 8;
+__global__ void __launch_bounds__(32 * kSummers) gated_dlam_kernel(GatedParams p, const float* partial, int parts, int packed, int longest) {
+    __shared__ float sums[kSummers][32];
+    const int c = blockIdx.x * 32 + threadIdx.x % 32, w = threadIdx.x / 32;
+    if (p.cu && longest < p.T && any_longer(p, longest)) parts = packed;
     tc::grid_dep_wait();
-    if (c >= C) return;
     float sum = 0.f;
-    for (int k = 0; k < parts; ++k) sum += partial[(int64_t)k * C + c];
-    const float l = __ldg(lam + c), e = expf(-fabsf(l));
-    dlam[c] = decay * (l >= 0.f ? 1.f : e) / (1.f + e) * sum;
-}
-
-// (one partial sum a block: as many as the largest clusters have)
-size_t partial_bytes(const GatedParams& p) {
-    return ((size_t)p.B * (p.T > 0 ? most_blocks(p.T, kTile<64>) : 0) * p.C * 4 + 255) / 256 * 256;
-}
-
-template <typename T, typename TG, int CH, int VEC, int GVEC, bool kPacked>
-cudaError_t launch(const GatedParams& p, cudaStream_t st) {
-    const int blocks = (p.C + CH - 1) / CH;
-    const int64_t groups = (int64_t)blocks * p.B;
-    float* const partial = static_cast<float*>(p.ws);
-    int parts = 0;
-    if (groups > 0) {
-        const auto kern = gated_bwd_kernel<T, TG, CH, VEC, GVEC, kPacked>;
-        constexpr int smem = kStages * kStageBytes<T, TG, CH>;
-        static ClusterRoom room;
-        static std::atomic<uint64_t> allowed;
-        cudaError_t e = allow_shared(kern, smem, allowed);
-        if (e != cudaSuccess) return e;
-        const int cluster = room.size_for(kern, groups, p.T, kTile<CH>, kThreads, smem);
-        e = launch_clusters(kern, groups * cluster, cluster, kThreads, smem, st, p, partial, cluster, blocks);
-        if (e != cudaSuccess) return e;
-        parts = p.T > 0 ? p.B * cluster : 0;
+    if (c < p.C) {
+#pragma unroll 4
+        for (int k = w; k < parts; k += kSummers) sum += partial[(int64_t)k * p.C + c];
     }
-    return tc::launch_dependent(gated_dlam_kernel, (unsigned)((p.C + 127) / 128), 128, 0, st, partial, parts, p.lam, p.decay, p.C, p.dlam);
+    sums[w][threadIdx.x % 32] = sum;
+    __syncthreads();
+    if (w || c >= p.C) return;
+    for (int k = 1; k < kSummers; ++k) sum += sums[k][threadIdx.x];
+    const float l = __ldg(p.lam + c), e = expf(-fabsf(l));
+    p.dlam[c] = p.decay * (l >= 0.f ? 1.f : e) / (1.f + e) * sum;
 }
-template <typename T, typename TG, int CH, int VEC, int GVEC>
-cudaError_t launch_packed(const GatedParams& p, cudaStream_t st) {
-    return p.cu ? launch<T, TG, CH, VEC, GVEC, true>(p, st) : launch<T, TG, CH, VEC, GVEC, false>(p, st);
+
+// (one partial sum a block)
+size_t partial_bytes(const GatedParams& p) {
+    const int64_t streams = gated_each(p, kMean) ? p.N : p.B;
+    const int64_t blocks = streams * ((p.C + 63) / 64) > kSms ? 1 : most_blocks(p.T, kTile<64>);  // of a stream (narrower ones are more)
+    const int64_t packed = p.cu ? most_blocks(p.T, kTile<64>) : 0;
+    return ((size_t)(p.T > 0 ? std::max(streams * blocks, packed) : 0) * p.C * 4 + 255) / 256 * 256;
+}
+
+// longest: as the forward pass's launch has it.  parts: how many partial sums the kernel leaves.
+template <typename T, typename TG, int CH, int VEC, int GVEC, bool kPacked>
+cudaError_t launch(const GatedParams& p, int streams, int& longest, int& parts, cudaStream_t st) {
+    const int blocks = (p.C + CH - 1) / CH;
+    const int64_t groups = (int64_t)blocks * streams;
+    const auto kern = gated_bwd_kernel<T, TG, CH, VEC, GVEC, kPacked>;
+    constexpr int smem = kStages * kStageBytes<T, TG, CH>;
+    static ClusterRoom room;
+    static std::atomic<uint64_t> allowed;
+    const cudaError_t e = allow_shared(kern, smem, allowed);
+    if (e != cudaSuccess) return e;
+    const int cluster = gated_cluster(room, kern, groups, p.T, kTile<CH>, kThreads, smem);
+    if (!kPacked) longest = p.cu ? longest_of(p, (int64_t)blocks * cluster) : p.T;
+    parts = p.T > 0 ? streams * cluster : 0;
+    return launch_clusters(kern, groups * cluster, cluster, kThreads, smem, kPacked && longest < p.T, st, p, static_cast<float*>(p.ws), cluster, blocks, longest);
+}
+template <typename T, typename TG, int VEC, int GVEC, bool kPacked>
+cudaError_t launch_channels(const GatedParams& p, int streams, int& longest, int& parts, cudaStream_t st) {
+    if constexpr (VEC * sizeof(T) == 16) {
+        const int ch = gated_channels(p, streams);
+        if (ch == 32) return launch<T, TG, 32, VEC, GVEC, kPacked>(p, streams, longest, parts, st);
+        if (ch == 16) return launch<T, TG, 16, VEC, GVEC, kPacked>(p, streams, longest, parts, st);
+    }
+    return launch<T, TG, 64, VEC, GVEC, kPacked>(p, streams, longest, parts, st);
 }
 template <typename T, typename TG, int VEC, int GVEC>
-cudaError_t launch_wide(const GatedParams& p, cudaStream_t st) {
-    const int ch = gated_channels(p);
-    return ch == 64 ? launch_packed<T, TG, 64, VEC, GVEC>(p, st) : ch == 32 ? launch_packed<T, TG, 32, VEC, GVEC>(p, st) : launch_packed<T, TG, 16, VEC, GVEC>(p, st);
+cudaError_t launch_streams(const GatedParams& p, cudaStream_t st) {
+    int longest = p.T, parts = 0, packed = 0;
+    const bool each = !p.cu || gated_each(p, kMean);
+    cudaError_t e = cudaSuccess;
+    if (each && p.B > 0) e = launch_channels<T, TG, VEC, GVEC, false>(p, p.cu ? p.N : p.B, longest, parts, st);
+    if (e == cudaSuccess && p.cu && (!each || longest < p.T)) e = launch_channels<T, TG, VEC, GVEC, true>(p, 1, longest, packed, st);
+    if (e != cudaSuccess) return e;
+    return tc::launch_dependent(gated_dlam_kernel, (unsigned)((p.C + 31) / 32), 32 * kSummers, 0, st, p, static_cast<const float*>(p.ws), each ? parts : packed, packed, longest);
 }
 
 }  // namespace
@@ -384,15 +417,15 @@ cudaError_t gated_scan_bwd(kda_dtype dt, kda_dtype gdt, const GatedParams& given
     const bool wide = pairs && gated_pieces(p, es, 16) && (int64_t)p.C * gs % 16 == 0 && kda_host::aligned16(p.dy);
     const bool narrow = pairs && gated_pieces(p, es, 2 * es) && (uintptr_t)p.dy % (2 * gs) == 0;
     if (dt == KDA_F32) {
-        if (wide) return launch_wide<float, float, 4, 4>(p, st);
-        return narrow ? launch_packed<float, float, 64, 2, 2>(p, st) : launch_packed<float, float, 64, 1, 1>(p, st);
+        if (wide) return launch_streams<float, float, 4, 4>(p, st);
+        return narrow ? launch_streams<float, float, 2, 2>(p, st) : launch_streams<float, float, 1, 1>(p, st);
     }
     if (gdt == KDA_F32) {
-        if (wide) return launch_wide<__nv_bfloat16, float, 8, 4>(p, st);
-        return narrow ? launch_packed<__nv_bfloat16, float, 64, 2, 2>(p, st) : launch_packed<__nv_bfloat16, float, 64, 1, 1>(p, st);
+        if (wide) return launch_streams<__nv_bfloat16, float, 8, 4>(p, st);
+        return narrow ? launch_streams<__nv_bfloat16, float, 2, 2>(p, st) : launch_streams<__nv_bfloat16, float, 1, 1>(p, st);
     }
-    if (wide) return launch_wide<__nv_bfloat16, __nv_bfloat16, 8, 8>(p, st);
-    return narrow ? launch_packed<__nv_bfloat16, __nv_bfloat16, 64, 2, 2>(p, st) : launch_packed<__nv_bfloat16, __nv_bfloat16, 64, 1, 1>(p, st);
+    if (wide) return launch_streams<__nv_bfloat16, __nv_bfloat16, 8, 8>(p, st);
+    return narrow ? launch_streams<__nv_bfloat16, __nv_bfloat16, 2, 2>(p, st) : launch_streams<__nv_bfloat16, __nv_bfloat16, 1, 1>(p, st);
 }
 
 }  // namespace kda

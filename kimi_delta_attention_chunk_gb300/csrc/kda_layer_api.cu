@@ -373,7 +373,7 @@ size_t kda_gated_scan_bwd_workspace_size(int B, int T, int C, int N, int packed,
     if (check_stream(B, T, C, N, packed ? kPacked : nullptr) != KDA_OK) return 0;
     static float none;
     kda::GatedParams p{};
-    p.B = B; p.T = T; p.C = C; p.N = N;
+    p.B = B; p.T = T; p.C = C; p.N = N; p.cu = packed ? kPacked : nullptr;
     p.states = have_states ? &none : nullptr;
     return kda::gated_scan_bwd_workspace(p);
 }
