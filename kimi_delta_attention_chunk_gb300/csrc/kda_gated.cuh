@@ -182,9 +182,9 @@ struct Feed {
     static constexpr int ROWS = PR < 32 ? 32 / PR : 1;  // rows between them (one row by several rounds: PR = 64)
     static_assert(R * PR % 32 == 0 && (PR <= 32 || PR == 64), "whole rounds");
     const T* at;         // the next tile's piece of this lane
-    int64_t step, more;  // elements to the next tile's, and to the next row's
+    int64_t step, more, ld;  // elements to the next tile's, to the lane's next row's, and to the next row's
     __device__ __forceinline__ Feed(const void* base, int64_t ld, int64_t first_row, int c0, int step)
-        : at(static_cast<const T*>(base) + (first_row + row()) * ld + c0 + col()), step(step * ld), more(ROWS * ld) {}
+        : at(static_cast<const T*>(base) + (first_row + row()) * ld + c0 + col()), step(step * ld), more(ROWS * ld), ld(ld) {}
     static __device__ __forceinline__ int row() { return threadIdx.x % 32 / PR; }
     static __device__ __forceinline__ int col() { return threadIdx.x % 32 % PR * VEC; }
     // The next tile, all of whose rows and channels are there.
@@ -202,6 +202,28 @@ struct Feed {
     __device__ __forceinline__ void request(T* tile, int rows, int has) {
         const T* from = at;
         const int lines = rows < R ? rows : R;
+        if constexpr (VEC * sizeof(T) < 4) {
+            // no asynchronous copies of two bytes: sixteen loads of a lane on their way at a time, none of them conditional (what is not
+            // there is copied from where something is)
+            if (lines > 0) {
+                constexpr int H = PR > 32 ? PR / 32 : 1, B = N < 16 ? N : 16;  // elements of a row, and of a batch
+                static_assert(N % B == 0, "whole batches");
+                const int there = has - 1 - col();
+                from += min(0, there);
+                from -= row() * ld;
+#pragma unroll
+                for (int q0 = 0; q0 < N; q0 += B) {
+                    T v[B];
+#pragma unroll
+                    for (int q = 0; q < B; ++q)
+                        v[q] = from[min(row() + (q0 + q) / H * ROWS, lines - 1) * ld + min((q0 + q) % H * 32, max(0, there))];
+#pragma unroll
+                    for (int q = 0; q < B; ++q) tile[L::row(row() + (q0 + q) / H * ROWS) * CH + col() + (q0 + q) % H * 32] = v[q];
+                }
+            }
+            at += step;
+            return;
+        }
         for (int r = row(); r < lines; r += ROWS, from += more)
 #pragma unroll
             for (int h = 0; h < (PR + 31) / 32; ++h) {
@@ -271,14 +293,14 @@ __device__ __forceinline__ bool any_longer(const GatedParams& p, int most) {
 }
 
 // Sequences that are packed in one stream have blocks of their own, unless they are so short that these would be mostly idle (`mean`
-// tokens), or one of them takes more than two and a half times the share of a machine that works evenly: its blocks would still run when
-// all others are done.  Only the offsets say so, on the device: both kernels are launched, and one of them returns at once.
+// tokens), or one of them alone would take them more than twice as many steps as the stream takes as a whole, at `pace` and `stream` tokens a
+// step.  Only the offsets say so, on the device: both kernels are launched, and one of them returns at once.
 // (bf16 with gates, 4096 channels, forward and backward: 16 sequences of 1 to 700 tokens 67 and 108 us with blocks of their own, 80 and 154 as one
 // stream; 128 x 128 151 and 293, 256 and 580; 256 x 64 302 and 336, 278 and 600; 512 x 32 591 and 451, 282 and 606; 1024 x 16 1169 and 817, 287 and
 // 667; one of 16129 among 15 of 17 362 and 1141, 185 and 410)
 inline bool gated_each(const GatedParams& p, int mean) { return p.cu && p.N > 0 && p.N <= p.T / mean; }
-inline int longest_of(const GatedParams& p, int64_t blocks) {
-    const int64_t most = p.T * blocks * 5 / (4 * kSms);
+inline int longest_of(const GatedParams& p, int64_t pace, int64_t stream) {
+    const int64_t most = (p.T + stream - 1) / stream * 2 * pace;
     return p.N > 1 && most < p.T ? (int)most : p.T;
 }
 // The blocks of a sequence: one where there is one an SM anyway.

@@ -244,38 +244,46 @@ __global__ void __launch_bounds__(kThreads, 2) gated_fwd_kernel(GatedParams p, i
     }
 }
 
-// longest: in, of the kernel before, which leaves the work to this one where a sequence is longer (no such kernel: p.T); out, of this one.
+// One kernel's launch.  cluster: blocks of a sequence, 0 where the kernel cannot be set up (error).
 template <typename T, int CH, int VEC, bool kPacked, bool kRows>
-cudaError_t launch(const GatedParams& p, int streams, int& longest, cudaStream_t st) {
-    const int blocks = (p.C + CH - 1) / CH;
-    const int64_t groups = (int64_t)blocks * streams;
-    const auto kern = gated_fwd_kernel<T, CH, VEC, kPacked, kRows>;
-    constexpr int smem = kSmem<T, CH, kRows>;
-    static ClusterRoom room;
-    static std::atomic<uint64_t> allowed;
-    const cudaError_t e = allow_shared(kern, smem, allowed);
-    if (e != cudaSuccess) return e;
-    const int cluster = gated_cluster(room, kern, groups, p.T, kTileOf<T, CH>, kThreads, smem);
-    if (!kPacked) longest = p.cu ? longest_of(p, (int64_t)blocks * cluster) : p.T;
-    return launch_clusters(kern, groups * cluster, cluster, kThreads, smem, kPacked && longest < p.T, st, p, cluster, blocks, longest);
-}
-template <typename T, int VEC, bool kPacked, bool kRows>
-cudaError_t launch_channels(const GatedParams& p, int streams, int& longest, cudaStream_t st) {
-    if constexpr (VEC * sizeof(T) == 16) {
-        const int ch = gated_channels(p, streams);
-        if (ch == 32) return launch<T, 32, VEC, kPacked, kRows>(p, streams, longest, st);
-        if (ch == 16) return launch<T, 16, VEC, kPacked, kRows>(p, streams, longest, st);
+struct Launch {
+    static constexpr int kBytes = kSmem<T, CH, kRows>;
+    const GatedParams& p;
+    const int64_t blocks, groups;
+    cudaError_t error;
+    int cluster = 0;
+    Launch(const GatedParams& p, int streams) : p(p), blocks((p.C + CH - 1) / CH), groups(blocks * streams) {
+        static ClusterRoom room;
+        static std::atomic<uint64_t> allowed;
+        const auto kern = gated_fwd_kernel<T, CH, VEC, kPacked, kRows>;
+        error = allow_shared(kern, kBytes, allowed);
+        if (error == cudaSuccess) cluster = gated_cluster(room, kern, groups, p.T, kTileOf<T, CH>, kThreads, kBytes);
     }
-    return launch<T, 64, VEC, kPacked, kRows>(p, streams, longest, st);
+    int pace() const { return kTileOf<T, CH> * cluster; }  // tokens of a sequence at a time
+    cudaError_t operator()(int longest, bool dependent, cudaStream_t st) const {
+        if (error != cudaSuccess) return error;
+        return launch_clusters(gated_fwd_kernel<T, CH, VEC, kPacked, kRows>, groups * cluster, cluster, kThreads, kBytes, dependent, st, p, cluster, (int)blocks, longest);
+    }
+};
+// Calls f with the launch of the width that fits.
+template <typename T, int VEC, bool kPacked, bool kRows, typename F>
+cudaError_t with_launch(const GatedParams& p, int streams, F f) {
+    const int ch = gated_channels(p, streams);
+    if (VEC * sizeof(T) == 16 && ch == 32) return f(Launch<T, VEC * sizeof(T) == 16 ? 32 : 64, VEC, kPacked, kRows>(p, streams));
+    return ch == 16 ? f(Launch<T, 16, VEC, kPacked, kRows>(p, streams)) : f(Launch<T, 64, VEC, kPacked, kRows>(p, streams));
 }
 template <typename T, int VEC, bool kRows>
 cudaError_t launch_streams(const GatedParams& p, cudaStream_t st) {
-    int longest = p.T;
-    if (!p.cu || gated_each(p, kMean)) {
-        const cudaError_t e = launch_channels<T, VEC, false, kRows>(p, p.cu ? p.N : p.B, longest, st);
-        if (e != cudaSuccess || longest == p.T) return e;
-    }
-    return launch_channels<T, VEC, true, kRows>(p, 1, longest, st);
+    if (!p.cu || (gated_each(p, kMean) && p.N == 1))
+        return with_launch<T, VEC, false, kRows>(p, p.cu ? 1 : p.B, [&](const auto& each) { return each(p.T, false, st); });
+    return with_launch<T, VEC, true, kRows>(p, 1, [&](const auto& stream) {
+        if (!gated_each(p, kMean) || stream.error != cudaSuccess) return stream(p.T, false, st);
+        return with_launch<T, VEC, false, kRows>(p, p.N, [&](const auto& each) {
+            const int longest = longest_of(p, each.pace(), stream.pace());
+            const cudaError_t e = each(longest, false, st);
+            return e != cudaSuccess || longest == p.T ? e : stream(longest, true, st);
+        });
+    });
 }
 template <typename T, int VEC>
 cudaError_t launch_rows(const GatedParams& p, cudaStream_t st) {

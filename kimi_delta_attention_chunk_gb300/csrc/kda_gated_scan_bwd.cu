@@ -358,40 +358,58 @@ size_t partial_bytes(const GatedParams& p) {
     return ((size_t)(p.T > 0 ? std::max(streams * blocks, packed) : 0) * p.C * 4 + 255) / 256 * 256;
 }
 
-// longest: as the forward pass's launch has it.  parts: how many partial sums the kernel leaves.
+// One kernel's launch.  cluster: blocks of a sequence, 0 where the kernel cannot be set up (error).
 template <typename T, typename TG, int CH, int VEC, int GVEC, bool kPacked>
-cudaError_t launch(const GatedParams& p, int streams, int& longest, int& parts, cudaStream_t st) {
-    const int blocks = (p.C + CH - 1) / CH;
-    const int64_t groups = (int64_t)blocks * streams;
-    const auto kern = gated_bwd_kernel<T, TG, CH, VEC, GVEC, kPacked>;
-    constexpr int smem = kStages * kStageBytes<T, TG, CH>;
-    static ClusterRoom room;
-    static std::atomic<uint64_t> allowed;
-    const cudaError_t e = allow_shared(kern, smem, allowed);
-    if (e != cudaSuccess) return e;
-    const int cluster = gated_cluster(room, kern, groups, p.T, kTile<CH>, kThreads, smem);
-    if (!kPacked) longest = p.cu ? longest_of(p, (int64_t)blocks * cluster) : p.T;
-    parts = p.T > 0 ? streams * cluster : 0;
-    return launch_clusters(kern, groups * cluster, cluster, kThreads, smem, kPacked && longest < p.T, st, p, static_cast<float*>(p.ws), cluster, blocks, longest);
-}
-template <typename T, typename TG, int VEC, int GVEC, bool kPacked>
-cudaError_t launch_channels(const GatedParams& p, int streams, int& longest, int& parts, cudaStream_t st) {
-    if constexpr (VEC * sizeof(T) == 16) {
-        const int ch = gated_channels(p, streams);
-        if (ch == 32) return launch<T, TG, 32, VEC, GVEC, kPacked>(p, streams, longest, parts, st);
-        if (ch == 16) return launch<T, TG, 16, VEC, GVEC, kPacked>(p, streams, longest, parts, st);
+struct Launch {
+    static constexpr int kBytes = kStages * kStageBytes<T, TG, CH>;
+    const GatedParams& p;
+    const int64_t blocks, groups;
+    cudaError_t error;
+    int cluster = 0, parts;
+    Launch(const GatedParams& p, int streams) : p(p), blocks((p.C + CH - 1) / CH), groups(blocks * streams) {
+        static ClusterRoom room;
+        static std::atomic<uint64_t> allowed;
+        const auto kern = gated_bwd_kernel<T, TG, CH, VEC, GVEC, kPacked>;
+        error = allow_shared(kern, kBytes, allowed);
+        if (error == cudaSuccess) cluster = gated_cluster(room, kern, groups, p.T, kTile<CH>, kThreads, kBytes);
+        parts = p.T > 0 ? streams * cluster : 0;  // partial sums of dlam
     }
-    return launch<T, TG, 64, VEC, GVEC, kPacked>(p, streams, longest, parts, st);
+    int pace() const { return kTile<CH> * cluster; }  // tokens of a sequence at a time
+    cudaError_t operator()(int longest, bool dependent, cudaStream_t st) const {
+        if (error != cudaSuccess || groups == 0) return error;
+        return launch_clusters(gated_bwd_kernel<T, TG, CH, VEC, GVEC, kPacked>, groups * cluster, cluster, kThreads, kBytes, dependent, st, p, static_cast<float*>(p.ws), cluster,
+                               (int)blocks, longest);
+    }
+};
+// Calls f with the launch of the width that fits.
+template <typename T, typename TG, int VEC, int GVEC, bool kPacked, typename F>
+cudaError_t with_launch(const GatedParams& p, int streams, F f) {
+    const int ch = gated_channels(p, streams);
+    if (VEC * sizeof(T) == 16 && ch == 32) return f(Launch<T, TG, VEC * sizeof(T) == 16 ? 32 : 64, VEC, GVEC, kPacked>(p, streams));
+    return ch == 16 ? f(Launch<T, TG, 16, VEC, GVEC, kPacked>(p, streams)) : f(Launch<T, TG, 64, VEC, GVEC, kPacked>(p, streams));
 }
 template <typename T, typename TG, int VEC, int GVEC>
 cudaError_t launch_streams(const GatedParams& p, cudaStream_t st) {
-    int longest = p.T, parts = 0, packed = 0;
-    const bool each = !p.cu || gated_each(p, kMean);
-    cudaError_t e = cudaSuccess;
-    if (each && p.B > 0) e = launch_channels<T, TG, VEC, GVEC, false>(p, p.cu ? p.N : p.B, longest, parts, st);
-    if (e == cudaSuccess && p.cu && (!each || longest < p.T)) e = launch_channels<T, TG, VEC, GVEC, true>(p, 1, longest, packed, st);
-    if (e != cudaSuccess) return e;
-    return tc::launch_dependent(gated_dlam_kernel, (unsigned)((p.C + 31) / 32), 32 * kSummers, 0, st, p, static_cast<const float*>(p.ws), each ? parts : packed, packed, longest);
+    auto sums = [&](int parts, int packed, int longest) {
+        return tc::launch_dependent(gated_dlam_kernel, (unsigned)((p.C + 31) / 32), 32 * kSummers, 0, st, p, static_cast<const float*>(p.ws), parts, packed, longest);
+    };
+    if (!p.cu || (gated_each(p, kMean) && p.N == 1))
+        return with_launch<T, TG, VEC, GVEC, false>(p, p.cu ? 1 : p.B, [&](const auto& each) {
+            const cudaError_t e = each(p.T, false, st);
+            return e != cudaSuccess ? e : sums(each.parts, 0, p.T);
+        });
+    return with_launch<T, TG, VEC, GVEC, true>(p, 1, [&](const auto& stream) {
+        if (!gated_each(p, kMean) || stream.error != cudaSuccess) {
+            const cudaError_t e = stream(p.T, false, st);
+            return e != cudaSuccess ? e : sums(stream.parts, 0, p.T);
+        }
+        return with_launch<T, TG, VEC, GVEC, false>(p, p.N, [&](const auto& each) {
+            const int longest = longest_of(p, each.pace(), stream.pace());
+            cudaError_t e = each(longest, false, st);
+            if (e == cudaSuccess && longest < p.T) e = stream(longest, true, st);
+            return e != cudaSuccess ? e : sums(each.parts, stream.parts, longest);
+        });
+    });
 }
 
 }  // namespace
