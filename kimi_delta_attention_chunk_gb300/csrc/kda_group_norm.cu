@@ -7,27 +7,27 @@ namespace {
 
 template <typename T, typename V>
 __global__ void __launch_bounds__(V::NTH, V::kFwd) norm_token_fwd_kernel(NormParams p, Teams t) {
-    constexpr int E2 = V::E2, A = V::kAhead;
+    constexpr int E2 = V::E2, A = V::kSlots;
     __shared__ float buf[2][V::NTH / 32][2];
     extern __shared__ __align__(16) char shared[];
     TeamSum<V::LANES, V::NTH> sum{buf, t.lanes, 0};
     const Place<V> at(p, t);
     const float inv_n = 1.f / (float)(p.C / p.G);
     const Turns turns(p, t, at.rsub);
-    Rows<V, T> rows(p.x, turns.first, p.ldx, turns.step, at, shared);
+    Rows<V, T, A> rows(p.x, turns.first, p.ldx, turns.step, at, shared);
     auto request = [&](int i) {
         if (i < turns.full || (i < turns.all && turns.has(p, i))) rows.request(i, at);
         copies_commit();
     };
-    if constexpr (A > 1)
+    if constexpr (A > 0)
 #pragma unroll
-        for (int i = 0; i < A - 1; ++i) request(i);
+        for (int i = 0; i < (A > 1 ? A - 1 : 1); ++i) request(i);
     Weights<V> weights(p, at, t.wide_weights);
     T* to = static_cast<T*>(p.y) + turns.first * p.C + at.first;
     const int64_t next = turns.step * p.C;
     for (int i = 0; i < turns.all; ++i, to += next) {
         const bool here = i < turns.full || turns.has(p, i);
-        if constexpr (A > 1) copies_wait<A - 2>();
+        if constexpr (A > 0) copies_wait<(A > 1 ? A - 2 : 0)>();
         Pieces<V, T> raw;
         if (here) rows.take(i, at, raw);
         else raw.zero();
@@ -38,6 +38,7 @@ __global__ void __launch_bounds__(V::NTH, V::kFwd) norm_token_fwd_kernel(NormPar
         for (int j = 0; j < E2; ++j) a = add2(a, x[j]);
         float s[1] = {sum2(a)};
         sum(s);
+        if constexpr (A == 1) request(i + 1);  // (behind the sum's barrier: the row is in registers)
         const f2 mean = both(-s[0] * inv_n);
         a = 0ull;
 #pragma unroll
@@ -62,10 +63,10 @@ __global__ void __launch_bounds__(V::NTH, V::kFwd) norm_token_fwd_kernel(NormPar
 
 template <typename T, int VEC>
 cudaError_t launch_fwd(const NormParams& p, cudaStream_t st) {
-    return pick_variant<VEC>(p.C / p.G / VEC, p.G, [&](auto variant) {
+    return pick_variant<VEC, false>(p.C / p.G / VEC, p.G, [&](auto variant) {
         using V = decltype(variant);
         const auto kern = norm_token_fwd_kernel<T, V>;
-        constexpr int smem = Rows<V, T>::kBytes;
+        constexpr int smem = Rows<V, T, V::kSlots>::kBytes;
         static std::atomic<uint64_t> allowed;
         const cudaError_t e = allow_shared(kern, smem, allowed);
         if (e != cudaSuccess) return e;

@@ -5,10 +5,21 @@ namespace kda {
 
 namespace {
 
+// The slots of x's and dy's rows (a variant's, or as many as the shared memory of its blocks has room for), and the bytes of these and of
+// the sums that are held there.
+template <typename T, typename TG, typename V>
+struct Room {
+    static constexpr int kSums = V::kSharedSums ? V::NTH * 8 * V::E : 0, kMost = 226 * 1024 / V::kBwd - 1024;
+    static constexpr int slots(int n) { return n > 0 && n * V::E * V::NTH * (int)(sizeof(T) + sizeof(TG)) + kSums > kMost ? slots(n / 2) : n; }
+    static constexpr int kSlots = slots(V::kSlots);
+    static constexpr int kRings = Rows<V, T, kSlots>::kBytes + Rows<V, TG, kSlots>::kBytes;
+};
+
 // partial: [gridDim.y][2][C].
 template <typename T, typename TG, typename V>
 __global__ void __launch_bounds__(V::NTH, V::kBwd) norm_token_bwd_kernel(NormParams p, Teams t, float* partial) {
-    constexpr int E2 = V::E2, A = V::kAhead, NTH = V::NTH;
+    using M = Room<T, TG, V>;
+    constexpr int E2 = V::E2, A = M::kSlots, NTH = V::NTH;
     constexpr bool kShared = V::kSharedSums;
     __shared__ float buf[2][NTH / 32][2];
     extern __shared__ __align__(16) char shared[];
@@ -16,8 +27,8 @@ __global__ void __launch_bounds__(V::NTH, V::kBwd) norm_token_bwd_kernel(NormPar
     const Place<V> at(p, t);
     const float inv_n = 1.f / (float)(p.C / p.G);
     const Turns turns(p, t, at.rsub);
-    Rows<V, T> rows(p.x, turns.first, p.ldx, turns.step, at, shared);
-    Rows<V, TG> grads(p.dy, turns.first, p.C, turns.step, at, shared + rows.kBytes);
+    Rows<V, T, A> rows(p.x, turns.first, p.ldx, turns.step, at, shared);
+    Rows<V, TG, A> grads(p.dy, turns.first, p.C, turns.step, at, shared + rows.kBytes);
     auto request = [&](int i) {
         if (i < turns.full || (i < turns.all && turns.has(p, i))) {
             rows.request(i, at);
@@ -25,13 +36,13 @@ __global__ void __launch_bounds__(V::NTH, V::kBwd) norm_token_bwd_kernel(NormPar
         }
         copies_commit();
     };
-    if constexpr (A > 1)
+    if constexpr (A > 0)
 #pragma unroll
-        for (int i = 0; i < A - 1; ++i) request(i);
+        for (int i = 0; i < (A > 1 ? A - 1 : 1); ++i) request(i);
     Weights<V> weights(p, at, t.wide_weights);
     // dw and db of this thread's channels: in registers, or in shared memory [E2][2][NTH]
     f2 dw[kShared ? 1 : E2], db[kShared ? 1 : E2];
-    f2* const sums = reinterpret_cast<f2*>(shared);
+    f2* const sums = reinterpret_cast<f2*>(shared + (kShared ? M::kRings : 0));
 #pragma unroll
     for (int j = 0; j < E2; ++j) {
         if constexpr (kShared) sums[(2 * j) * NTH + threadIdx.x] = sums[(2 * j + 1) * NTH + threadIdx.x] = 0ull;
@@ -42,7 +53,7 @@ __global__ void __launch_bounds__(V::NTH, V::kBwd) norm_token_bwd_kernel(NormPar
     // kAll: all rows of the block are there
     auto turn = [&](int i, auto all) {
         const bool here = decltype(all)::value || turns.has(p, i);
-        if constexpr (A > 1) copies_wait<A - 2>();
+        if constexpr (A > 0) copies_wait<(A > 1 ? A - 2 : 0)>();
         Pieces<V, T> raw;
         Pieces<V, TG> raw_dy;
         if (here) {
@@ -59,6 +70,7 @@ __global__ void __launch_bounds__(V::NTH, V::kBwd) norm_token_bwd_kernel(NormPar
         for (int j = 0; j < E2; ++j) a = add2(a, x[j]);
         float one[1] = {sum2(a)};
         sum(one);
+        if constexpr (A == 1) request(i + 1);  // (behind the sum's barrier: the row is in registers)
         const f2 mean = both(-one[0] * inv_n);
         a = 0ull;
 #pragma unroll
@@ -140,12 +152,12 @@ __global__ void __launch_bounds__(V::NTH, V::kBwd) norm_token_bwd_kernel(NormPar
 
 template <typename T, typename TG, int VEC>
 cudaError_t launch_bwd(const NormParams& p, cudaStream_t st) {
-    return pick_variant<VEC>(p.C / p.G / VEC, p.G, [&](auto variant) {
+    return pick_variant<VEC, true>(p.C / p.G / VEC, p.G, [&](auto variant) {
         using V = decltype(variant);
         const auto kern = norm_token_bwd_kernel<T, TG, V>;
-        constexpr int rings = Rows<V, T>::kBytes + Rows<V, TG>::kBytes, sums = V::NTH * 8 * (V::kSharedSums ? V::E : 1);
-        static_assert(!V::kSharedSums || rings == 0, "the sums have the place");
-        constexpr int smem = rings > sums ? rings : sums;
+        using M = Room<T, TG, V>;
+        constexpr int join = V::NTH * 8;  // (the joining of the rows' sums, where they are in registers)
+        constexpr int smem = V::kSharedSums ? M::kRings + M::kSums : M::kRings > join ? M::kRings : join;
         static std::atomic<uint64_t> allowed;
         cudaError_t e = allow_shared(kern, smem, allowed);
         if (e != cudaSuccess) return e;
@@ -167,7 +179,7 @@ template <int VEC>
 size_t most_rows(const NormParams& p) {
     const int cg = p.C / p.G;
     if (cg % VEC != 0) return 0;
-    return pick_variant<VEC>(cg / VEC, p.G, [&](auto variant) {
+    return pick_variant<VEC, true>(cg / VEC, p.G, [&](auto variant) {
         using V = decltype(variant);
         return (size_t)grid_of(p, teams_of<V>(p), V::kBwd).y;
     });

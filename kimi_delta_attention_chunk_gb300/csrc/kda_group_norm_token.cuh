@@ -30,13 +30,13 @@ template <int VEC_, int R_, int NTH_, int LANES_>
 struct Variant {
     static constexpr int VEC = VEC_, R = R_, NTH = NTH_, LANES = LANES_, E = R * VEC, E2 = E / 2;
     static_assert(E % 2 == 0, "values go in pairs");
-    // Rows of a thread under way in shared memory; where a row is many pieces its own loads are enough, and two-byte pieces have no
-    // asynchronous copy.
-    static constexpr int kAhead = E <= 16 && VEC > 1 && NTH == 256 ? 4 : 1;
+    // A thread's rows in shared memory, one of them at work and the others under way; with one, the next is asked for when this one is in
+    // registers; two-byte pieces have no asynchronous copy and none.
+    static constexpr int kSlots = VEC == 1 ? 0 : E <= 16 && NTH <= 512 ? 4 : 1;
     static constexpr bool kKeep = E <= 8;  // the weights: kept, or read again for every row
     // Backwards, dw and db of a thread's channels: in registers, or where they are many in shared memory.
-    static constexpr bool kSharedSums = E > 16 || NTH != 256;
-    static constexpr int kFwd = NTH != 256 ? 1 : E > 8 ? 3 : 4, kBwd = NTH != 256 ? 1 : E > 8 ? 2 : 3;  // blocks an SM
+    static constexpr bool kSharedSums = E > 16 || NTH > 512;
+    static constexpr int kFwd = NTH != 256 ? 1 : E > 16 ? 2 : E > 8 ? 3 : 4, kBwd = NTH != 256 ? 1 : E > 8 ? 2 : 3;  // blocks an SM
 };
 
 // Sums of `N` values over every team.  Teams of more than a warp meet in shared memory, in a buffer of their own each time.
@@ -154,15 +154,15 @@ struct Pieces {
 
 // A thread's own rows, every next-th element from `from` on: asked for ahead through shared memory (what a thread asks for it alone
 // reads, so that no thread waits for another), or loaded when their turn comes.
-template <typename V, typename T>
+template <typename V, typename T, int A>
 struct Rows {
-    static constexpr int A = V::kAhead, kBytes = A > 1 ? A * V::R * V::NTH * V::VEC * (int)sizeof(T) : 0;
+    static constexpr int kBytes = A * V::R * V::NTH * V::VEC * (int)sizeof(T);
     const T* from;
     int64_t next;
     T* mine;
     __device__ __forceinline__ Rows(const void* base, int64_t first, int64_t ld, int64_t step, const Place<V>& at, void* shared)
         : from(static_cast<const T*>(base) + first * ld + at.first), next(step * ld), mine(static_cast<T*>(shared) + threadIdx.x * V::VEC) {}
-    __device__ __forceinline__ T* slot(int i, int k) const { return mine + ((i % A) * V::R + k) * V::NTH * V::VEC; }
+    __device__ __forceinline__ T* slot(int i, int k) const { return mine + ((A > 1 ? i % A : 0) * V::R + k) * V::NTH * V::VEC; }
     __device__ __forceinline__ void request(int i, const Place<V>& at) {
 #pragma unroll
         for (int k = 0; k < V::R; ++k)
@@ -170,7 +170,7 @@ struct Rows {
         from += next;
     }
     __device__ __forceinline__ void take(int i, const Place<V>& at, Pieces<V, T>& p) {
-        if constexpr (A > 1) {
+        if constexpr (A > 0) {
 #pragma unroll
             for (int k = 0; k < V::R; ++k)
                 if (at.has(k)) p.r[k].from_shared(slot(i, k));
@@ -262,6 +262,10 @@ Teams teams_of(const NormParams& p) {
     const int teams = t.lanes >= V::NTH ? 1 : V::NTH / t.lanes;  // in a block
     t.groups = teams < p.G ? teams : t.lanes <= 32 ? pow2_at_least(p.G) : p.G;
     if (t.groups > teams) t.groups = teams;
+    if (t.lanes >= 32 && t.groups < p.G) {  // blocks side by side have as many each (17401 x 2575 in 5 groups: 3 and 2 for 4 and 1)
+        const int x = (p.G + t.groups - 1) / t.groups;
+        t.groups = (p.G + x - 1) / x;
+    }
     t.rows = teams / t.groups;
     t.threads = (t.rows * t.groups * t.lanes + 31) / 32 * 32;
     t.wide_weights = kda_host::aligned16(p.weight) && kda_host::aligned16(p.bias);
@@ -280,7 +284,7 @@ dim3 grid_of(const NormParams& p, const Teams& t, int resident) {
 
 // f(a variant) for groups of `pieces` pieces of VEC elements: the fewest values a lane with which a group fits a warp, then a block of
 // 256 threads, then one of 1024.
-template <int VEC, typename F>
+template <int VEC, bool kBackward, typename F>
 auto pick_variant(int pieces, int G, F f) {
     if constexpr (VEC >= 4) {
         // teams that are filled need no tests
@@ -289,7 +293,9 @@ auto pick_variant(int pieces, int G, F f) {
         if (pieces == 8 && G % 32 == 0) return f(Variant<VEC, 1, 256, 8>{});
         if (pieces <= 32) return f(Variant<VEC, 1, 256, 0>{});
         if (pieces <= 512) return f(Variant<VEC, 2, 256, 0>{});
-        if (pieces <= 1024) return f(Variant<VEC, 4, 256, 0>{});
+        // (bf16: forwards two rows an SM, backwards one with its sums in registers)
+        constexpr int R = VEC == 8 && kBackward ? 2 : 4;
+        if (pieces <= 1024) return f(Variant<VEC, R, 1024 / R, 0>{});
         return f(Variant<VEC, 16 / VEC, 1024, 0>{});
     } else if constexpr (VEC == 2) {
         if (pieces <= 32) return f(Variant<2, 1, 256, 0>{});
@@ -298,7 +304,7 @@ auto pick_variant(int pieces, int G, F f) {
         return f(Variant<2, 8, 1024, 0>{});
     } else {
         if (pieces <= 64) return f(Variant<1, 2, 256, 0>{});
-        if (pieces <= 256) return f(Variant<1, 8, 256, 0>{});
+        if (pieces <= 1536) return f(Variant<1, 8, 256, 0>{});
         if (pieces <= 4096) return f(Variant<1, 16, 256, 0>{});
         return f(Variant<1, 16, 1024, 0>{});
     }
