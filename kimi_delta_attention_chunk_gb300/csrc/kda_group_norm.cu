@@ -10,7 +10,7 @@ __global__ void __launch_bounds__(V::NTH, V::kFwd) norm_token_fwd_kernel(NormPar
     constexpr int E2 = V::E2, A = V::kSlots;
     __shared__ float buf[2][V::NTH / 32][2];
     extern __shared__ __align__(16) char shared[];
-    TeamSum<V::LANES, V::NTH> sum{buf, t.lanes, 0};
+    TeamSum<V::LANES, V::NTH> sum(buf, t.lanes);
     const Place<V> at(p, t);
     const float inv_n = 1.f / (float)(p.C / p.G);
     const Turns turns(p, t, at.rsub);
@@ -71,7 +71,7 @@ cudaError_t launch_fwd(const NormParams& p, cudaStream_t st) {
         const cudaError_t e = allow_shared(kern, smem, allowed);
         if (e != cudaSuccess) return e;
         const Teams t = teams_of<V>(p);
-        kern<<<grid_of(p, t, V::kFwd), t.threads, smem, st>>>(p, t);
+        kern<<<grid_of<V>(p, t, V::kFwd), t.threads, smem, st>>>(p, t);
         return cudaGetLastError();
     });
 }

@@ -23,7 +23,7 @@ __global__ void __launch_bounds__(V::NTH, V::kBwd) norm_token_bwd_kernel(NormPar
     constexpr bool kShared = V::kSharedSums;
     __shared__ float buf[2][NTH / 32][2];
     extern __shared__ __align__(16) char shared[];
-    TeamSum<V::LANES, NTH> sum{buf, t.lanes, 0};
+    TeamSum<V::LANES, NTH> sum(buf, t.lanes);
     const Place<V> at(p, t);
     const float inv_n = 1.f / (float)(p.C / p.G);
     const Turns turns(p, t, at.rsub);
@@ -162,7 +162,7 @@ cudaError_t launch_bwd(const NormParams& p, cudaStream_t st) {
         cudaError_t e = allow_shared(kern, smem, allowed);
         if (e != cudaSuccess) return e;
         const Teams t = teams_of<V>(p);
-        const dim3 grid = grid_of(p, t, V::kBwd);
+        const dim3 grid = grid_of<V>(p, t, V::kBwd);
         float* const partial = static_cast<float*>(p.ws);
         kern<<<grid, t.threads, smem, st>>>(p, t, partial);
         e = cudaGetLastError();
@@ -181,7 +181,7 @@ size_t most_rows(const NormParams& p) {
     if (cg % VEC != 0) return 0;
     return pick_variant<VEC, true>(cg / VEC, p.G, [&](auto variant) {
         using V = decltype(variant);
-        return (size_t)grid_of(p, teams_of<V>(p), V::kBwd).y;
+        return (size_t)grid_of<V>(p, teams_of<V>(p), V::kBwd).y;
     });
 }
 size_t norm_token_bwd_workspace(const NormParams& p) {

@@ -42,34 +42,47 @@ struct Variant {
 // Sums of `N` values over every team.  Teams of more than a warp meet in shared memory, in a buffer of their own each time.
 template <int LANES, int NTH>
 struct TeamSum {
-    float (*buf)[NTH / 32][2];  // [2]
-    int lanes, turn;
+    static constexpr int W = NTH / 32;
+    float (*buf)[W][2];  // [2]
+    int lanes, turn = 0, from = 0;
+    bool reads = false;  // of the warps' sums this lane reads one: entry `from`
+    __device__ __forceinline__ TeamSum(float (*buf)[W][2], int lanes) : buf(buf), lanes(lanes) {
+        if (LANES > 0 || lanes <= 32) return;
+        const int w = threadIdx.x / 32, team = lanes / 32;
+        reads = (int)threadIdx.x % W < team;
+        from = w / team * team + threadIdx.x % W;
+    }
     template <int N>
     __device__ __forceinline__ void operator()(float (&v)[N]) {
         if constexpr (LANES > 0) {
-#pragma unroll
-            for (int o = LANES / 2; o > 0; o /= 2)
-#pragma unroll
-                for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+            all<LANES>(v);
         } else {
+            if (lanes >= 32) {
+                all<32>(v);
+            } else {
 #pragma unroll
-            for (int o = 16; o > 0; o /= 2)
-                if (o < lanes)
+                for (int o = 16; o > 0; o /= 2)
+                    if (o < lanes)
 #pragma unroll
-                    for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+                        for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+            }
             if (lanes <= 32) return;
-            const int w = threadIdx.x / 32, team = lanes / 32, w0 = w / team * team;
             if (threadIdx.x % 32 == 0)
 #pragma unroll
-                for (int k = 0; k < N; ++k) buf[turn][w][k] = v[k];
+                for (int k = 0; k < N; ++k) buf[turn][threadIdx.x / 32][k] = v[k];
             __syncthreads();
 #pragma unroll
-            for (int k = 0; k < N; ++k) {
-                v[k] = 0.f;
-                for (int j = 0; j < team; ++j) v[k] += buf[turn][w0 + j][k];
-            }
+            for (int k = 0; k < N; ++k) v[k] = reads ? buf[turn][from][k] : 0.f;
+            all<W>(v);
             turn ^= 1;
         }
+    }
+    template <int L, int N>
+    static __device__ __forceinline__ void all(float (&v)[N]) {
+#pragma unroll
+        for (int o = L / 2; o > 0; o /= 2)
+#pragma unroll
+            for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
     }
 };
 
@@ -271,8 +284,11 @@ Teams teams_of(const NormParams& p) {
     t.wide_weights = kda_host::aligned16(p.weight) && kda_host::aligned16(p.bias);
     return t;
 }
-// Blocks along the rows: no more than the rows need, about `resident` an SM in all.
+// Blocks along the rows: no more than the rows need, about `resident` an SM in all (and more where blocks are smaller and have no rows in
+// shared memory).
+template <typename V>
 dim3 grid_of(const NormParams& p, const Teams& t, int resident) {
+    if (V::kSlots == 0) resident = resident * V::NTH / t.threads;
     const int x = (p.G + t.groups - 1) / t.groups;
     int64_t y = ((int64_t)p.total + t.rows - 1) / t.rows;
     const int64_t most = (int64_t)kSms * resident / x;
