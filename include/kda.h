@@ -18,8 +18,8 @@
  * ---------------------------------------
  *  - Every tensor pointer is a DEVICE pointer owned by the caller, and so is
  *    every workspace: the library allocates no memory.  kda_chunk_fwd,
- *    kda_chunk_fwd_fused and kda_recurrent_bwd, and the convolution, scan and
- *    pages calls that name one, take a caller-owned device
+ *    kda_chunk_fwd_fused and kda_recurrent_bwd, and the convolution, scan, norm
+ *    and pages calls that name one, take a caller-owned device
  *    workspace of at least the size their *_workspace_size query returns
  *    (16-byte aligned; the call owns it until its stream work completes, so
  *    calls whose work overlaps, replayed graphs among them, must not share one;
@@ -671,8 +671,8 @@ KDA_API kda_status kda_gated_scan_fwd(const void *x, int64_t ldx, const void *r,
  *  states   what the forward call on the same inputs left, or NULL (made again in the workspace:
  *           x, r and i are then read twice).
  *  workspace  at least kda_gated_scan_bwd_workspace_size bytes, 16-byte aligned.
- * Sums are fp32, in an order fixed by the sizes.  Rows that belong to no sequence have zeros in
- * dx, dr, di and dz, whatever they hold.  Where 1 - a^2 is below 1e-36, 1 / m is taken as 1e18.  The
+ * Sums are fp32, in an order fixed by the sizes and the offsets.  Rows that belong to no sequence
+ * have zeros in dx, dr, di and dz, whatever they hold.  Where 1 - a^2 is below 1e-36, 1 / m is taken as 1e18.  The
  * rest as kda_gated_scan_fwd.
  */
 KDA_API size_t kda_gated_scan_bwd_workspace_size(int B, int T, int C, int N, int packed, int have_states);

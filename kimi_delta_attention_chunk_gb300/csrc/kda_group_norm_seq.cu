@@ -6,6 +6,8 @@
 // make a piece, and piece (run + sequence) has a place of its own in the scratch.  Sums are joined in a fixed order.  Variances:
 // the mean of four rows and the squares around it, joined with those of the rows before (and so on up), so that neither a mean far from zero nor a
 // first token far from the others costs digits.
+// 8 x 4096 x 512 bf16 in 32 groups: 23 us forwards (44% of the bytes at the copy rate: x is read a second time, most of it from L2, and three
+// kernels follow one another), 2 x 2048 x 4096 in 32 groups 40 us backwards (38%).
 #include "kda_group_norm.cuh"
 
 namespace kda {
