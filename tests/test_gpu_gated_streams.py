@@ -114,3 +114,18 @@ def test_bits_do_not_depend_on_the_others():
     batch = {k: v if k == "lam" else v[:, :256].expand(4, 256, C).contiguous() for k, v in d.items()}
     yb, fb = kda.gated_scan_fwd(*args(batch), z=batch["z"])
     assert torch.equal(yb[0], y[0, :256]) and torch.equal(yb[3], yb[0]) and torch.equal(fb[0], final[0])
+
+
+@pytest.mark.parametrize("lens,lead,tail,C", [([0, 363, 0, 501], 100, 99, 200), ([150, 200], 70, 90, 2048), ([3] * 20, 40, 70, 72)])
+def test_states_before_tokens_of_no_sequence_are_not_used(lens, lead, tail, C):
+    """They are left as they are, whatever was there."""
+    T = lead + sum(lens) + tail
+    cu = torch.tensor(cumulative(lens, lead), dtype=torch.int32, device="cuda")
+    d = make((1, T), C, BF16, T, True)
+    dy = torch.randn(1, T, C, generator=torch.Generator().manual_seed(C)).to(BF16).cuda()
+    out = []
+    for filled in (0.0, float("nan")):
+        states = torch.full(kda.gated_scan_states(d["x"]), filled, device="cuda")
+        kda.gated_scan_fwd(*args(d), z=d["z"], cu_seqlens=cu, states=states)
+        out.append(kda.gated_scan_bwd(*args(d), dy, z=d["z"], cu_seqlens=cu, states=states))
+    assert all(torch.equal(out[0][k], out[1][k]) for k in ("dx", "dr", "di", "dz", "dlam"))
