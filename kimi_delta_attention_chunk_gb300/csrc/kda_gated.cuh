@@ -28,10 +28,10 @@ struct Decay {
     static __device__ __forceinline__ Decay of(f2 sr, f2 rate) {
         Decay d;
         const f2 s = mul2(sr, rate), q = mul2(s, s);
-        const f2 sinh = mul2(s, fma2(q, fma2(q, both(1.f / 120.f), both(1.f / 6.f)), both(1.f)));
+        const f2 sinh2 = mul2(s, fma2(q, fma2(q, both(1.f / 60.f), both(1.f / 3.f)), both(2.f)));  // 2 sinh
         const f2 cosh = mul2(q, fma2(q, fma2(q, both(1.f / 720.f), both(1.f / 24.f)), both(0.5f)));
-        d.a = add2(fma2(sinh, both(-1.f), cosh), both(1.f));
-        d.m2 = mul2(mul2(d.a, both(2.f)), sinh);
+        d.a = add2(fma2(sinh2, both(-0.5f), cosh), both(1.f));
+        d.m2 = mul2(d.a, sinh2);
         if constexpr (!kSmall) {
             const f2 e = ex2_2(mul2(s, both(-kLog2e)));
             float s0, s1, x0, x1, y0, y1;

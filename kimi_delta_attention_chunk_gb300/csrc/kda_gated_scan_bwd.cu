@@ -99,6 +99,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(GatedParams p, f
     w0 -= stride;
 
     const f2 rate = pack(n2 > 0 ? gated_rate(__ldg(p.lam + c), p.decay) : 0.f, n2 > 1 ? gated_rate(__ldg(p.lam + c + 1), p.decay) : 0.f);
+    const f2 down = neg2(rate);
     const bool small = __all_sync(0xffffffffu, small_rate(rate)) != 0;
     // through sequences without tokens the gradient goes as it comes
     if (p.dinitial) {
@@ -292,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(GatedParams p, f
                 g = mul2(a[j], dh);
                 dlam = add2(dlam, part);
                 store_pair<TG, true>(dx, mul2(dh, wx[j]), n2);
-                store_pair<TG, true>(dr, mul2(mul2(part, rate), rest2(sr[j])), n2);
+                store_pair<TG, true>(dr, mul2(part, fma2(sr[j], down, rate)), n2);
                 store_pair<TG, true>(di, mul2(dh, ui[j]), n2);
             }
             if (!kPacked && s0 == from && p.dinitial) store_state(p.dinitial, (int64_t)b * p.C + c, g, n2);
@@ -303,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(GatedParams p, f
                 if (t < from || t >= S) continue;
                 if (kPacked && !clear && lasts[j] >= 0) g = 0ull;
                 const f2 dh = add2(yb[j], g);
-                f2 part = mul2(mul2(dh, wm[j]), sr[j]), dx = mul2(dh, wx[j]), dr = mul2(mul2(part, rate), rest2(sr[j])), di = mul2(dh, ui[j]);
+                f2 part = mul2(mul2(dh, wm[j]), sr[j]), dx = mul2(dh, wx[j]), dr = mul2(part, fma2(sr[j], down, rate)), di = mul2(dh, ui[j]);
                 g = mul2(a[j], dh);
                 if (t >= first && t < last) dlam = add2(dlam, part);
                 else dx = di = dr = gz[j] = 0ull;
