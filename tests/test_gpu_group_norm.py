@@ -193,3 +193,12 @@ def test_nothing_to_do():
     cu = torch.zeros(1, dtype=torch.int32, device="cuda")
     out = kda.group_norm_bwd(x, 2, x, weight=w, over="sequence", cu_seqlens=cu)
     assert not bool(out["dx"].any()) and not bool(out["dweight"].any())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T,C,G", [(700, 6296, 1), (650, 2575, 5), (900, 4096, 1), (700, 4090, 2), (640, 3333, 1), (330, 9002, 1), (330, 12288, 1), (700, 2580, 5),
+                                   (1500, 1032, 3), (700, 2451, 1), (700, 1060, 2), (2000, 600, 6)])
+def test_many_rows_of_large_groups(T, C, G, dtype):
+    """More rows than blocks, so that a block's next rows are under way while it works."""
+    x, w, b, dy = make((1, T), C, dtype, T + C, True, 1 + T % 3)
+    check(x, G, w, b, dy, 1, [(0, T)], "token", 32, dtype)
