@@ -4,7 +4,7 @@
 // The statistics of a whole sequence come before its first output, so x (and dy) are read twice: by a pass over runs of tokens that
 // leaves partial sums a channel, and by the pass that writes.  Runs are cut at fixed places of the token stream; a run and a sequence that meet
 // make a piece, and piece (run + sequence) has a place of its own in the scratch.  Sums are joined in a fixed order.  Variances:
-// the mean of four rows and the squares around it, joined with those of the rows before (and so on up), so that neither a mean far from zero nor a
+// the mean of a batch of 4 to 16 rows and the squares around it, joined with those of the rows before (and so on up), so that neither a mean far from zero nor a
 // first token far from the others costs digits.
 // 8 x 4096 x 512 bf16 in 32 groups: 23 us forwards (44% of the bytes at the copy rate: x is read a second time, most of it from L2, and three
 // kernels follow one another), 2 x 2048 x 4096 in 32 groups 40 us backwards (38%).
@@ -76,8 +76,15 @@ __device__ __forceinline__ void store_sums(const ChannelSums<VEC>& s, f2 (*join)
     }
 }
 
+// Rows of a thread's batch: more where pieces are small.
+template <int VEC>
+constexpr int kFwdRows = VEC == 1 ? 16 : VEC == 2 ? 8 : 4;
+template <int VEC>
+constexpr int kBwdRows = VEC == 1 ? 16 : VEC == 2 ? 8 : 2;
+
 // A thread's own pieces of batches of ROWS rows (every kSubs-th token), on their way through shared memory: what a thread asks for it
-// alone reads, so that no thread waits for another.  (Two-byte pieces have no asynchronous copy: they are loaded when asked for.)
+// alone reads, so that no thread waits for another.  (Two-byte pieces have no asynchronous copy: a batch is loaded when asked for, all of it
+// at once and none of it conditionally.)
 template <typename T, int VEC, int ROWS>
 struct Ring {
     static constexpr int kBytes = kBatches * ROWS * kThreads * VEC * (int)sizeof(T);
@@ -86,6 +93,14 @@ struct Ring {
     __device__ __forceinline__ T* at(int batch, int j) const { return mine + ((batch % kBatches) * ROWS + j) * kThreads * VEC; }
     // `left` rows are there from `from` on, ld apart.
     __device__ __forceinline__ void request(int batch, int left, const T* from, int64_t ld) const {
+        if constexpr (VEC * sizeof(T) < 4) {
+            T v[ROWS];
+#pragma unroll
+            for (int j = 0; j < ROWS; ++j) v[j] = from[min(j, (left - 1) / kSubs) * kSubs * ld];
+#pragma unroll
+            for (int j = 0; j < ROWS; ++j) *at(batch, j) = v[j];
+            return;
+        }
 #pragma unroll
         for (int j = 0; j < ROWS; ++j, from += kSubs * ld)
             if (j * kSubs < left) Row<T, VEC>::copy_async(at(batch, j), from);
@@ -129,7 +144,7 @@ struct Moments {
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kThreads, 3) seq_moments_kernel(NormParams p, SeqMap m, int run, float* pieces) {
     constexpr int N2 = (VEC + 1) / 2;
-    constexpr int ROWS = 4;
+    constexpr int ROWS = kFwdRows<VEC>;
     extern __shared__ __align__(16) char shared[];
     __shared__ Moments join[N2][kThreads];
     const Ring<T, VEC, ROWS> ring(shared);
@@ -152,7 +167,14 @@ __global__ void __launch_bounds__(kThreads, 3) seq_moments_kernel(NormParams p, 
             for (int i = 0; i < N2; ++i) {
                 Moments few{0ull, 0ull};
                 if (have == ROWS) {
-                    few.mean = mul2(add2(add2(v[0][i], v[1][i]), add2(v[2][i], v[3][i])), both(inv));
+                    f2 sum[ROWS / 2];
+#pragma unroll
+                    for (int j = 0; j < ROWS / 2; ++j) sum[j] = add2(v[2 * j][i], v[2 * j + 1][i]);
+#pragma unroll
+                    for (int half = ROWS / 4; half > 0; half /= 2)
+#pragma unroll
+                        for (int j = 0; j < half; ++j) sum[j] = add2(sum[2 * j], sum[2 * j + 1]);
+                    few.mean = mul2(sum[0], both(inv));
 #pragma unroll
                     for (int j = 0; j < ROWS; ++j) {
                         const f2 d = add2(v[j][i], neg2(few.mean));
@@ -300,7 +322,7 @@ __device__ __forceinline__ void stats_of(const NormParams& p, const float* stats
 
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kThreads, 3) seq_apply_kernel(NormParams p, SeqMap m, int run, const float* stats) {
-    constexpr int N2 = (VEC + 1) / 2, ROWS = 4;
+    constexpr int N2 = (VEC + 1) / 2, ROWS = kFwdRows<VEC>;
     extern __shared__ __align__(16) char shared[];
     const Ring<T, VEC, ROWS> ring(shared);
     const int piece = threadIdx.x % kPieces, sub = threadIdx.x / kPieces, c = (blockIdx.x * kPieces + piece) * VEC;
@@ -342,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 3) seq_apply_kernel(NormParams p, Se
 // Per piece and channel sum dp xh and sum dp, and the same per run: pieces[run + n][2][C], per_run[run][2][C].
 template <typename T, typename TG, int VEC>
 __global__ void __launch_bounds__(kThreads, 2) seq_grads_kernel(NormParams p, SeqMap m, int run, const float* stats, float* pieces, float* per_run) {
-    constexpr int N2 = (VEC + 1) / 2, ROWS = 2;
+    constexpr int N2 = (VEC + 1) / 2, ROWS = kBwdRows<VEC>;
     extern __shared__ __align__(16) char shared[];
     const Ring<T, VEC, ROWS> ring(shared);
     const Ring<TG, VEC, ROWS> ring_dy(shared + ring.kBytes);
@@ -436,7 +458,7 @@ __global__ void __launch_bounds__(NTH) seq_means_kernel(NormParams p, SeqMap m, 
 
 template <typename T, typename TG, int VEC>
 __global__ void __launch_bounds__(kThreads, 2) seq_dx_kernel(NormParams p, SeqMap m, int run, const float* stats, const float* means) {
-    constexpr int N2 = (VEC + 1) / 2, ROWS = 2;
+    constexpr int N2 = (VEC + 1) / 2, ROWS = kBwdRows<VEC>;
     extern __shared__ __align__(16) char shared[];
     const Ring<T, VEC, ROWS> ring(shared);
     const Ring<TG, VEC, ROWS> ring_dy(shared + ring.kBytes);
@@ -507,7 +529,7 @@ size_t stats_bytes(const NormParams& p) { return (size_t)(((int64_t)p.N * p.G * 
 template <typename T, int VEC>
 cudaError_t launch_stats(const NormParams& p, const SeqMap& m, const Cut& q, float* pieces, float* stats, cudaStream_t st) {
     const auto kern = seq_moments_kernel<T, VEC>;
-    constexpr int smem = Ring<T, VEC, 4>::kBytes;
+    constexpr int smem = Ring<T, VEC, kFwdRows<VEC>>::kBytes;
     static std::atomic<uint64_t> allowed;
     cudaError_t e = allow_shared(kern, smem, allowed);
     if (e != cudaSuccess) return e;
@@ -526,7 +548,7 @@ cudaError_t launch_fwd(const NormParams& p, cudaStream_t st) {
     cudaError_t e = launch_stats<T, VEC>(p, m, q, reinterpret_cast<float*>(ws), stats, st);
     if (e != cudaSuccess) return e;
     const auto kern = seq_apply_kernel<T, VEC>;
-    constexpr int smem = Ring<T, VEC, 4>::kBytes;
+    constexpr int smem = Ring<T, VEC, kFwdRows<VEC>>::kBytes;
     static std::atomic<uint64_t> allowed;
     if ((e = allow_shared(kern, smem, allowed)) != cudaSuccess) return e;
     return tc::launch_dependent(kern, dim3(blocks_of(p, VEC), q.runs), kThreads, smem, st, p, m, q.run, (const float*)stats);
@@ -549,7 +571,7 @@ cudaError_t launch_bwd(const NormParams& p, cudaStream_t st) {
     const dim3 grid(blocks_of(p, VEC), q.runs);
     const auto grads = seq_grads_kernel<T, TG, VEC>;
     const auto dx = seq_dx_kernel<T, TG, VEC>;
-    constexpr int smem = Ring<T, VEC, 2>::kBytes + Ring<TG, VEC, 2>::kBytes;
+    constexpr int smem = Ring<T, VEC, kBwdRows<VEC>>::kBytes + Ring<TG, VEC, kBwdRows<VEC>>::kBytes;
     static std::atomic<uint64_t> grads_allowed, dx_allowed;
     cudaError_t e = allow_shared(grads, smem, grads_allowed);
     if (e == cudaSuccess) e = allow_shared(dx, smem, dx_allowed);
