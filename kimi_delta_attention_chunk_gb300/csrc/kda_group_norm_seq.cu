@@ -22,11 +22,19 @@ constexpr int kBatches = 3;                   // batches of a thread's rows unde
 struct Cut {
     int run, runs;
 };
-// Runs of tokens, whole batches: one filling of the machine by `resident` blocks an SM, 64 tokens at least.
+// Runs of tokens, whole batches: one filling of the machine by `resident` blocks an SM, 64 tokens at least.  Where channels alone are a
+// third of it or more, up to eight runs in the number of fillings that leaves the least idle (4478 x 4979 backwards, 156 blocks: seven runs in four
+// fillings, one in one).
 Cut cut_of(const NormParams& p, int blocks, int resident) {
     Cut q;
-    int want = kSms * resident / blocks;
+    const int places = kSms * resident;
+    int want = places / blocks;
     if (want < 1) want = 1;
+    if (want < 3) {
+        auto fillings = [&](int n) { return ((int64_t)blocks * n + places - 1) / places; };
+        for (int n = want + 1; n <= 8; ++n)
+            if (fillings(n) * want < fillings(want) * n) want = n;
+    }
     q.run = p.total / want + (p.total % want != 0);
     q.run = (q.run + 31) / 32 * 32;
     if (q.run < 64) q.run = 64;
@@ -76,6 +84,12 @@ __device__ __forceinline__ void store_sums(const ChannelSums<VEC>& s, f2 (*join)
     }
 }
 
+__device__ __forceinline__ f2 low_halves(f2 x, f2 y) {
+    float a, b, none;
+    unpack(x, a, none);
+    unpack(y, b, none);
+    return pack(a, b);
+}
 // Rows of a thread's batch: more where pieces are small.
 template <int VEC>
 constexpr int kFwdRows = VEC == 1 ? 16 : VEC == 2 ? 8 : 4;
@@ -110,7 +124,37 @@ struct Ring {
         r.from_shared(at(batch, j));
         r.to(v);
     }
+    // Row j in pairs of channels, or (VEC = 1) rows j and j + 1 of one channel as a pair, zero where there is no second (two).
+    static constexpr int PER = VEC == 1 ? 2 : 1;
+    __device__ __forceinline__ void take_rows(int batch, int j, bool two, f2 (&v)[(VEC + 1) / 2]) const {
+        take(batch, j, v);
+        if constexpr (VEC == 1) {
+            f2 more[1] = {0ull};
+            if (two) take(batch, j + 1, more);
+            v[0] = low_halves(v[0], more[0]);
+        }
+    }
 };
+// Stores what take_rows' pairs became, the second row `next` elements behind the first.
+template <int VEC, typename T>
+__device__ __forceinline__ void store_rows(T* to, int64_t next, bool two, const f2 (&v)[(VEC + 1) / 2]) {
+    if constexpr (VEC == 1) {
+        float a, b;
+        unpack(v[0], a, b);
+        to[0] = from_f32<T>(a);
+        if (two) to[next] = from_f32<T>(b);
+    } else {
+        Row<T, VEC> out;
+        out.from(v);
+        out.store(to);
+    }
+}
+// One of the weights of a thread's channels for take_rows' pairs.
+template <int VEC>
+__device__ __forceinline__ void weights_of(const float* p, float none, f2 (&v)[(VEC + 1) / 2]) {
+    vec_pairs<VEC>(p, none, v);
+    if constexpr (VEC == 1) v[0] = low_halves(v[0], v[0]);
+}
 // Walks a thread's rows b + sub, + kSubs ... before e: request(batch, first token of it) asks for a batch, f(batch, first token) has it.
 template <int ROWS, typename Q, typename F>
 __device__ __forceinline__ void each_batch(int b, int e, Q request, F f) {
@@ -327,11 +371,12 @@ __global__ void __launch_bounds__(kThreads, 3) seq_apply_kernel(NormParams p, Se
     const Ring<T, VEC, ROWS> ring(shared);
     const int piece = threadIdx.x % kPieces, sub = threadIdx.x / kPieces, c = (blockIdx.x * kPieces + piece) * VEC;
     const bool on = c < p.C;
+    const int64_t next = (int64_t)kSubs * p.C;
     // the last runs first: they were read last
     const int r0 = (gridDim.y - 1 - blockIdx.y) * run, r1 = (int)min((int64_t)m.total, (int64_t)r0 + run);
     f2 w[N2], bias[N2];
-    vec_pairs<VEC>(on && p.weight ? p.weight + c : nullptr, 1.f, w);
-    vec_pairs<VEC>(on && p.bias ? p.bias + c : nullptr, 0.f, bias);
+    weights_of<VEC>(on && p.weight ? p.weight + c : nullptr, 1.f, w);
+    weights_of<VEC>(on && p.bias ? p.bias + c : nullptr, 0.f, bias);
     tc::grid_dep_wait();
     each_piece(m, r0, r1, [&](int n, int b, int e) {
         if (!on) return;
@@ -343,19 +388,18 @@ __global__ void __launch_bounds__(kThreads, 3) seq_apply_kernel(NormParams p, Se
         each_batch<ROWS>(b + sub, e, [&](int batch, int t) { ring.request(batch, e - t, x + t * p.ldx, p.ldx); }, [&](int batch, int t) {
             T* to = static_cast<T*>(p.y) + (int64_t)t * p.C + c;
 #pragma unroll
-            for (int j = 0; j < ROWS; ++j, to += (int64_t)kSubs * p.C) {
+            for (int j = 0; j < ROWS; j += ring.PER, to += ring.PER * next) {
                 if (t + j * kSubs >= e) break;
+                const bool two = t + (j + 1) * kSubs < e;
                 f2 v[N2];
-                ring.take(batch, j, v);
+                ring.take_rows(batch, j, two, v);
 #pragma unroll
                 for (int i = 0; i < N2; ++i) v[i] = fma2(add2(v[i], mean[i]), scale[i], bias[i]);
                 if (p.act) {
 #pragma unroll
                     for (int i = 0; i < N2; ++i) v[i] = silu2(v[i]);
                 }
-                Row<T, VEC> out;
-                out.from(v);
-                out.store(to);
+                store_rows<VEC>(to, next, two, v);
             }
         });
     });
@@ -374,8 +418,8 @@ __global__ void __launch_bounds__(kThreads, 2) seq_grads_kernel(NormParams p, Se
     const int cc = on ? c : 0;
     const int r0 = blockIdx.y * run, r1 = (int)min((int64_t)m.total, (int64_t)r0 + run);
     f2 w[N2], bias[N2];
-    vec_pairs<VEC>(p.weight ? p.weight + cc : nullptr, 1.f, w);
-    vec_pairs<VEC>(p.bias ? p.bias + cc : nullptr, 0.f, bias);
+    weights_of<VEC>(p.weight ? p.weight + cc : nullptr, 1.f, w);
+    weights_of<VEC>(p.bias ? p.bias + cc : nullptr, 0.f, bias);
     ChannelSums<VEC> all;
 #pragma unroll
     for (int i = 0; i < N2; ++i) all.a[i] = all.b[i] = 0ull;
@@ -393,11 +437,12 @@ __global__ void __launch_bounds__(kThreads, 2) seq_grads_kernel(NormParams p, Se
             ring_dy.request(batch, e - t, dy + (int64_t)t * p.C, p.C);
         }, [&](int batch, int t) {
 #pragma unroll
-            for (int j = 0; j < ROWS; ++j) {
+            for (int j = 0; j < ROWS; j += ring.PER) {
                 if (t + j * kSubs >= e) break;
+                const bool two = t + (j + 1) * kSubs < e;
                 f2 v[N2], g[N2];
-                ring.take(batch, j, v);
-                ring_dy.take(batch, j, g);
+                ring.take_rows(batch, j, two, v);
+                ring_dy.take_rows(batch, j, two, g);
 #pragma unroll
                 for (int i = 0; i < N2; ++i) v[i] = mul2(add2(v[i], mean[i]), rstd[i]);
                 if (p.act) {
@@ -411,6 +456,10 @@ __global__ void __launch_bounds__(kThreads, 2) seq_grads_kernel(NormParams p, Se
                 }
             }
         });
+        if constexpr (VEC == 1) {
+            s.a[0] = pack(sum2(s.a[0]), 0.f);
+            s.b[0] = pack(sum2(s.b[0]), 0.f);
+        }
 #pragma unroll
         for (int i = 0; i < N2; ++i) {
             all.a[i] = add2(all.a[i], s.a[i]);
@@ -465,9 +514,10 @@ __global__ void __launch_bounds__(kThreads, 2) seq_dx_kernel(NormParams p, SeqMa
     const int piece = threadIdx.x % kPieces, sub = threadIdx.x / kPieces, c = (blockIdx.x * kPieces + piece) * VEC;
     const bool on = c < p.C;
     const int r0 = (gridDim.y - 1 - blockIdx.y) * run, r1 = (int)min((int64_t)m.total, (int64_t)r0 + run);
+    const int64_t next = (int64_t)kSubs * p.C;
     f2 w[N2], bias[N2];
-    vec_pairs<VEC>(on && p.weight ? p.weight + c : nullptr, 1.f, w);
-    vec_pairs<VEC>(on && p.bias ? p.bias + c : nullptr, 0.f, bias);
+    weights_of<VEC>(on && p.weight ? p.weight + c : nullptr, 1.f, w);
+    weights_of<VEC>(on && p.bias ? p.bias + c : nullptr, 0.f, bias);
     tc::grid_dep_wait();
     if (on) {  // rows of no sequence: zeros
         const int first = m.first(), last = m.last();
@@ -489,11 +539,12 @@ __global__ void __launch_bounds__(kThreads, 2) seq_dx_kernel(NormParams p, SeqMa
         }, [&](int batch, int t) {
             TG* to = static_cast<TG*>(p.dx) + (int64_t)t * p.C + c;
 #pragma unroll
-            for (int j = 0; j < ROWS; ++j, to += (int64_t)kSubs * p.C) {
+            for (int j = 0; j < ROWS; j += ring.PER, to += ring.PER * next) {
                 if (t + j * kSubs >= e) break;
+                const bool two = t + (j + 1) * kSubs < e;
                 f2 v[N2], g[N2];
-                ring.take(batch, j, v);
-                ring_dy.take(batch, j, g);
+                ring.take_rows(batch, j, two, v);
+                ring_dy.take_rows(batch, j, two, g);
 #pragma unroll
                 for (int i = 0; i < N2; ++i) v[i] = mul2(add2(v[i], mean[i]), rstd[i]);
                 if (p.act) {
@@ -502,9 +553,7 @@ __global__ void __launch_bounds__(kThreads, 2) seq_dx_kernel(NormParams p, SeqMa
                 }
 #pragma unroll
                 for (int i = 0; i < N2; ++i) g[i] = mul2(rstd[i], fma2(v[i], mqx[i], fma2(g[i], w[i], neg2(mq[i]))));
-                Row<TG, VEC> out;
-                out.from(g);
-                out.store(to);
+                store_rows<VEC>(to, next, two, g);
             }
         });
     });
@@ -521,8 +570,16 @@ int64_t groups_grid(const NormParams& p) {
 // Whether a sequence's pieces of a group are more than a small block keeps in registers (by the mean length of the sequences: one
 // sequence, one group of 4096 channels in 19 runs takes 78,000 entries, and one block for it 130 us with 128 threads).
 bool large_groups(const NormParams& p, const Cut& q) { return (int64_t)(q.runs / (p.N > 0 ? p.N : 1) + 1) * (p.C / p.G) > 1024; }
-// Places of pieces at p's sizes, whichever variant runs: the wide ones have the fewest blocks and the most runs.
-int64_t most_runs(const NormParams& p) { return cut_of(p, blocks_of(p, 8), kFwdResident).runs; }
+// Places of pieces at p's sizes, whichever variant runs.
+int64_t most_runs(const NormParams& p) {
+    int most = 0;
+    for (const int vec : {1, 2, 4, 8})
+        for (const int resident : {kFwdResident, kBwdResident}) {
+            const int runs = cut_of(p, blocks_of(p, vec), resident).runs;
+            if (runs > most) most = runs;
+        }
+    return most;
+}
 size_t pieces_bytes(const NormParams& p) { return (size_t)(((most_runs(p) + p.N) * 2 * p.C * 4 + 255) / 256 * 256); }
 size_t stats_bytes(const NormParams& p) { return (size_t)(((int64_t)p.N * p.G * 8 + 255) / 256 * 256); }
 
