@@ -189,7 +189,7 @@ struct Feed {
     static __device__ __forceinline__ int col() { return threadIdx.x % 32 % PR * VEC; }
     // The next tile, all of whose rows and channels are there.
     __device__ __forceinline__ void request(T* tile) {
-        if constexpr (PR <= 32) {
+        if constexpr (PR <= 32 && VEC * sizeof(T) >= 4) {
             const T* from = at;
 #pragma unroll
             for (int k = 0; k < N; ++k, from += more) Row<T, VEC>::copy_async(tile + L::row(row() + k * ROWS) * CH + col(), from);
