@@ -81,6 +81,17 @@ struct TeamSum {
     }
     template <int L, int N>
     static __device__ __forceinline__ void all(float (&v)[N]) {
+        if constexpr (N == 2 && L >= 8) {  // half of the lanes sum the one, half the other
+            const bool up = threadIdx.x & (L / 2);
+            float mine = up ? v[1] : v[0];
+            mine += __shfl_xor_sync(0xffffffffu, up ? v[0] : v[1], L / 2);
+#pragma unroll
+            for (int o = L / 4; o > 0; o /= 2) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+            const float other = __shfl_xor_sync(0xffffffffu, mine, L / 2);
+            v[0] = up ? other : mine;
+            v[1] = up ? mine : other;
+            return;
+        }
 #pragma unroll
         for (int o = L / 2; o > 0; o /= 2)
 #pragma unroll
