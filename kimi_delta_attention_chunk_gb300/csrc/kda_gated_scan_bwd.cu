@@ -389,7 +389,7 @@ struct Launch {
 template <typename T, typename TG, int VEC, int GVEC, bool kPacked, typename F>
 cudaError_t with_launch(const GatedParams& p, int streams, F f) {
     const int ch = gated_channels(p, streams);
-    if (VEC * sizeof(T) == 16 && ch == 32) return f(Launch<T, TG, VEC * sizeof(T) == 16 ? 32 : 64, VEC, GVEC, kPacked>(p, streams));
+    if (ch == 32) return f(Launch<T, TG, 32, VEC, GVEC, kPacked>(p, streams));
     return ch == 16 ? f(Launch<T, TG, 16, VEC, GVEC, kPacked>(p, streams)) : f(Launch<T, TG, 64, VEC, GVEC, kPacked>(p, streams));
 }
 template <typename T, typename TG, int VEC, int GVEC>
