@@ -273,7 +273,7 @@ struct Launch {
         return launch_clusters(gated_fwd_kernel<T, CH, VEC, kPacked, kRows>, groups * cluster, cluster, kThreads, kBytes, dependent, st, p, cluster, (int)blocks, longest);
     }
 };
-// Calls f with the launch of the width that fits.
+// Calls f with the launch of the width that fits (32 channels of smaller pieces gain nothing forwards: 7 sequences of 1 to 700 x 1530 fp32 24 and 25 us).
 template <typename T, int VEC, bool kPacked, bool kRows, typename F>
 cudaError_t with_launch(const GatedParams& p, int streams, F f) {
     const int ch = gated_channels(p, streams);
