@@ -285,6 +285,7 @@ __device__ __forceinline__ Stretch sequence_rows(const GatedParams& p, int n) {
 // Whether a sequence of the stream has more than `most` tokens (every thread of the block calls it).
 __device__ __forceinline__ bool any_longer(const GatedParams& p, int most) {
     bool found = false;
+#pragma unroll 4
     for (int n = threadIdx.x; n < p.N; n += blockDim.x) {
         const int begin = min(max(__ldg(p.cu + n), 0), p.T), end = min(max(__ldg(p.cu + n + 1), 0), p.T);
         found |= end - begin > most;
@@ -294,7 +295,8 @@ __device__ __forceinline__ bool any_longer(const GatedParams& p, int most) {
 
 // Sequences that are packed in one stream have blocks of their own, unless they are so short that these would be mostly idle (`mean`
 // tokens), or one of them alone would take them more than twice as many steps as the stream takes as a whole, at `pace` and `stream` tokens a
-// step.  Only the offsets say so, on the device: both kernels are launched, and one of them returns at once.
+// step.  Only the offsets say so, on the device: both kernels are launched.  A long sequence's own blocks return at once, and the stream's kernel,
+// behind them, looks for one and does everything again or nothing (a block that has one sequence does not look at all the others).
 // (bf16 with gates, 4096 channels, forward and backward: 16 sequences of 1 to 700 tokens 67 and 108 us with blocks of their own, 80 and 154 as one
 // stream; 128 x 128 151 and 293, 256 and 580; 256 x 64 302 and 336, 278 and 600; 512 x 32 591 and 451, 282 and 606; 1024 x 16 1169 and 817, 287 and
 // 667; one of 16129 among 15 of 17 362 and 1141, 185 and 410)

@@ -50,9 +50,13 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(GatedParams p, f
     __shared__ Marks<kPacked ? L::kTokens : 1> all_marks[kWarps];
     __shared__ int32_t offsets[kPacked ? kCachedOffsets : 1];
 
-    if constexpr (kPacked) tc::grid_dep_wait();
-    else tc::grid_dep_launch();
-    if (p.cu && longest < p.T && any_longer(p, longest) != kPacked) return;
+    if constexpr (kPacked) {
+        const bool needed = longest >= p.T || any_longer(p, longest);
+        tc::grid_dep_wait();
+        if (!needed) return;
+    } else {
+        tc::grid_dep_launch();
+    }
     const int pair = L::pair(), strip = L::strip(), w = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0);
     const int rank = cluster > 1 ? (int)cluster_rank() : 0;
     const int group = blockIdx.x / cluster, b = group / blocks, c0 = group % blocks * CH;
@@ -60,6 +64,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(GatedParams p, f
     const Offsets m(kPacked ? p.cu : nullptr, p.N, p.T, offsets);
     const Stretch rows_of = kPacked ? Stretch{0, p.T, m.first(), m.last()} : p.cu ? sequence_rows<true>(p, b) : Stretch{(int64_t)b * p.T, p.T, 0, p.T};
     const int S = rows_of.T, first = rows_of.first, last = rows_of.last;
+    if (!kPacked && last - first > longest) return;  // the stream's kernel does it all
     const int from = kPacked || !p.cu || b == 0 ? 0 : first;  // the first row that is this block's to write
     const int64_t row0 = rows_of.row0;
     const int stride = TT * cluster;  // tokens between a block's tiles
