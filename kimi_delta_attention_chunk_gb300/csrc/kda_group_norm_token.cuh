@@ -211,12 +211,9 @@ struct Rows {
     }
 };
 
-// 1 / sqrt(var + eps)
-__device__ __forceinline__ float inverse_deviation(float m2, float inv_n, float eps) {
-    float r;
-    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaxf(fmaf(m2, inv_n, eps), 1e-37f)));
-    return r;
-}
+// 1 / sqrt(var + eps): the accurate function, for which subnormal numbers count and what is not a number (the variance around an infinite
+// mean) stays so.
+__device__ __forceinline__ float inverse_deviation(float m2, float inv_n, float eps) { return rsqrtf(fmaf(m2, inv_n, eps)); }
 
 // One of the weights of a thread's channels in pairs, `none` without weights.
 template <typename V>
