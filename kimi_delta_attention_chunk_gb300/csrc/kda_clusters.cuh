@@ -78,14 +78,16 @@ __device__ __forceinline__ uint32_t address_at(unsigned rank, const void* mine) 
     return to;
 }
 
-// Lets a kernel have `bytes` of shared memory, once a device (a mark for each of 64; others every time).  48 KB need no
-// leave, of which the kernel itself may declare half.
+// Devices for which a launch remembers something; on others it asks every time.
+constexpr int kMostDevices = 64;
+
+// Lets a kernel that declares up to `declared` bytes of shared memory have `bytes` more, once a device.  48 KB in all need no leave.
 template <typename K>
-cudaError_t allow_shared(K kern, int bytes, std::atomic<uint64_t>& done) {
-    if (bytes <= 24 * 1024) return cudaSuccess;
-    int dev = 64;
+cudaError_t allow_shared(K kern, int declared, int bytes, std::atomic<uint64_t>& done) {
+    if (declared + bytes < 48 * 1024) return cudaSuccess;
+    int dev = kMostDevices;
     cudaError_t e = cudaGetDevice(&dev);
-    const uint64_t mark = dev < 64 ? 1ull << dev : 0;
+    const uint64_t mark = dev < kMostDevices ? 1ull << dev : 0;
     if (e != cudaSuccess || (done.load(std::memory_order_relaxed) & mark)) return e;
     if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) == cudaSuccess) done.fetch_or(mark, std::memory_order_relaxed);
     return e;
@@ -116,38 +118,40 @@ inline int most_blocks(int T, int tile) {
     return tiles < 1 ? 1 : tiles < kMostCluster ? tiles : kMostCluster;
 }
 
-// The launch of one kernel in clusters: how many of each size the machine holds at once, asked for once a process.
+// The launch of one kernel in clusters: how many of each size a device holds at once, asked for once a device.  What fails is not
+// remembered: the call has the error.
 struct ClusterRoom {
-    std::atomic<int> room[kMostCluster + 1];
+    std::atomic<int> known[kMostDevices][kMostCluster + 1];  // one more than the answer, 0: not asked yet
     template <typename K>
-    int of(K kern, int size, int threads, int smem) {
-        int n = room[size].load(std::memory_order_relaxed);
-        if (n == 0) {
-            cudaLaunchConfig_t cfg{};
-            cfg.gridDim = dim3(size * 1024);
-            cfg.blockDim = threads;
-            cfg.dynamicSmemBytes = smem;
-            cudaLaunchAttribute attr[1];
-            attr[0].id = cudaLaunchAttributeClusterDimension;
-            attr[0].val.clusterDim.x = size;
-            attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-            cfg.attrs = attr;
-            cfg.numAttrs = 1;
-            if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
-                cudaGetLastError();
-                n = 0;
-            }
-            n = n > 0 ? n : -1;
-            room[size].store(n, std::memory_order_relaxed);
-        }
-        return n;
+    cudaError_t of(K kern, int dev, int size, int threads, int smem, int& n) {
+        n = dev < kMostDevices ? known[dev][size].load(std::memory_order_relaxed) - 1 : -1;
+        if (n >= 0) return cudaSuccess;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(size * 1024);
+        cfg.blockDim = threads;
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = size;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+        if (e != cudaSuccess) return e;
+        n = n > 0 ? n : 0;
+        if (dev < kMostDevices) known[dev][size].store(n + 1, std::memory_order_relaxed);
+        return cudaSuccess;
     }
     // Blocks of a cluster for `groups` clusters of streams of T tokens: as many as run at once, no more than there are tiles.
     template <typename K>
-    int size_for(K kern, int64_t groups, int T, int tile, int threads, int smem) {
-        for (int k = most_blocks(T, tile); k > 1; --k)
-            if (groups <= of(kern, k, threads, smem)) return k;
-        return 1;
+    cudaError_t size_for(K kern, int64_t groups, int T, int tile, int threads, int smem, int& size) {
+        int dev = 0, n = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        for (size = most_blocks(T, tile); e == cudaSuccess && size > 1; --size) {
+            e = of(kern, dev, size, threads, smem, n);
+            if (e == cudaSuccess && groups <= n) break;
+        }
+        return e;
     }
 };
 

@@ -307,8 +307,9 @@ inline int longest_of(const GatedParams& p, int64_t pace, int64_t stream) {
 }
 // The blocks of a sequence: one where there is one an SM anyway.
 template <typename K>
-int gated_cluster(ClusterRoom& room, K kern, int64_t groups, int T, int tile, int threads, int smem) {
-    return groups > kSms ? 1 : room.size_for(kern, groups, T, tile, threads, smem);
+cudaError_t gated_cluster(ClusterRoom& room, K kern, int64_t groups, int T, int tile, int threads, int smem, int& cluster) {
+    cluster = 1;
+    return groups > kSms ? cudaSuccess : room.size_for(kern, groups, T, tile, threads, smem, cluster);
 }
 
 // Channels of a block. 64 where blocks of them that take a whole sequence each come to one and a half an SM; else 32 where those do

@@ -25,6 +25,7 @@ namespace kda {
 namespace {
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kDeclared = 24 * 1024;  // shared memory that the kernel declares, at most
 constexpr int kMean = 96;  // tokens of a sequence that has its own blocks, on average at least
 template <typename T, int CH>
 using LanesOf = Lanes<CH, sizeof(T) == 2 ? 16 : 8>;  // tokens of a strip
@@ -46,6 +47,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_fwd_kernel(GatedParams p, i
     __shared__ f2 ends[2][L::kPairs];
     __shared__ Marks<kPacked ? L::kTokens : 1> all_marks[kWarps];
     __shared__ int32_t offsets[kPacked ? kCachedOffsets : 1];
+    static_assert(sizeof(maps) + sizeof(peers) + sizeof(ends) + sizeof(all_marks) + sizeof(offsets) <= kDeclared, "what a launch allows for");
 
     if constexpr (kPacked) {
         const bool needed = longest >= p.T || any_longer(p, longest);
@@ -257,20 +259,20 @@ __global__ void __launch_bounds__(kThreads, 2) gated_fwd_kernel(GatedParams p, i
     }
 }
 
-// One kernel's launch.  cluster: blocks of a sequence, 0 where the kernel cannot be set up (error).
+// One kernel's launch.  cluster: blocks of a sequence; error: the kernel cannot be set up.
 template <typename T, int CH, int VEC, bool kPacked, bool kRows>
 struct Launch {
     static constexpr int kBytes = kSmem<T, CH, kRows>;
     const GatedParams& p;
     const int64_t blocks, groups;
     cudaError_t error;
-    int cluster = 0;
+    int cluster = 1;
     Launch(const GatedParams& p, int streams) : p(p), blocks((p.C + CH - 1) / CH), groups(blocks * streams) {
         static ClusterRoom room;
         static std::atomic<uint64_t> allowed;
         const auto kern = gated_fwd_kernel<T, CH, VEC, kPacked, kRows>;
-        error = allow_shared(kern, kBytes, allowed);
-        if (error == cudaSuccess) cluster = gated_cluster(room, kern, groups, p.T, kTileOf<T, CH>, kThreads, kBytes);
+        error = allow_shared(kern, kDeclared, kBytes, allowed);
+        if (error == cudaSuccess) error = gated_cluster(room, kern, groups, p.T, kTileOf<T, CH>, kThreads, kBytes, cluster);
     }
     int pace() const { return kTileOf<T, CH> * cluster; }  // tokens of a sequence at a time
     cudaError_t operator()(int longest, bool dependent, cudaStream_t st) const {

@@ -24,6 +24,7 @@ namespace kda {
 namespace {
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kDeclared = 40 * 1024;  // shared memory that the kernel declares, at most
 constexpr int kMean = 32;   // tokens of a sequence that has its own blocks, on average at least
 constexpr int kStrip = 4;
 template <int CH>
@@ -49,6 +50,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(GatedParams p, f
     __shared__ f2 ends[2][L::kPairs];
     __shared__ Marks<kPacked ? L::kTokens : 1> all_marks[kWarps];
     __shared__ int32_t offsets[kPacked ? kCachedOffsets : 1];
+    static_assert(sizeof(maps) + sizeof(peers) + sizeof(ends) + sizeof(all_marks) + sizeof(offsets) <= kDeclared, "what a launch allows for");
 
     if constexpr (kPacked) {
         const bool needed = longest >= p.T || any_longer(p, longest);
@@ -367,20 +369,20 @@ size_t partial_bytes(const GatedParams& p) {
     return ((size_t)(p.T > 0 ? std::max(streams * blocks, packed) : 0) * p.C * 4 + 255) / 256 * 256;
 }
 
-// One kernel's launch.  cluster: blocks of a sequence, 0 where the kernel cannot be set up (error).
+// One kernel's launch.  cluster: blocks of a sequence; error: the kernel cannot be set up.
 template <typename T, typename TG, int CH, int VEC, int GVEC, bool kPacked>
 struct Launch {
     static constexpr int kBytes = kStages * kStageBytes<T, TG, CH>;
     const GatedParams& p;
     const int64_t blocks, groups;
     cudaError_t error;
-    int cluster = 0, parts;
+    int cluster = 1, parts;
     Launch(const GatedParams& p, int streams) : p(p), blocks((p.C + CH - 1) / CH), groups(blocks * streams) {
         static ClusterRoom room;
         static std::atomic<uint64_t> allowed;
         const auto kern = gated_bwd_kernel<T, TG, CH, VEC, GVEC, kPacked>;
-        error = allow_shared(kern, kBytes, allowed);
-        if (error == cudaSuccess) cluster = gated_cluster(room, kern, groups, p.T, kTile<CH>, kThreads, kBytes);
+        error = allow_shared(kern, kDeclared, kBytes, allowed);
+        if (error == cudaSuccess) error = gated_cluster(room, kern, groups, p.T, kTile<CH>, kThreads, kBytes, cluster);
         parts = p.T > 0 ? streams * cluster : 0;  // partial sums of dlam
     }
     int pace() const { return kTile<CH> * cluster; }  // tokens of a sequence at a time

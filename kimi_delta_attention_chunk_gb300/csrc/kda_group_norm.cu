@@ -9,6 +9,7 @@ template <typename T, typename V>
 __global__ void __launch_bounds__(V::NTH, V::kFwd) norm_token_fwd_kernel(NormParams p, Teams t) {
     constexpr int E2 = V::E2, A = V::kSlots;
     __shared__ float buf[2][V::NTH / 32][2];
+    static_assert(sizeof(buf) <= kDeclared, "what a launch allows for");
     extern __shared__ __align__(16) char shared[];
     TeamSum<V::LANES, V::NTH> sum(buf, t.lanes);
     const Place<V> at(p, t);
@@ -68,7 +69,7 @@ cudaError_t launch_fwd(const NormParams& p, cudaStream_t st) {
         const auto kern = norm_token_fwd_kernel<T, V>;
         constexpr int smem = Rows<V, T, V::kSlots>::kBytes;
         static std::atomic<uint64_t> allowed;
-        const cudaError_t e = allow_shared(kern, smem, allowed);
+        const cudaError_t e = allow_shared(kern, kDeclared, smem, allowed);
         if (e != cudaSuccess) return e;
         const Teams t = teams_of<V>(p);
         kern<<<grid_of<V>(p, t, V::kFwd), t.threads, smem, st>>>(p, t);

@@ -22,6 +22,7 @@ __global__ void __launch_bounds__(V::NTH, V::kBwd) norm_token_bwd_kernel(NormPar
     constexpr int E2 = V::E2, A = M::kSlots, NTH = V::NTH;
     constexpr bool kShared = V::kSharedSums;
     __shared__ float buf[2][NTH / 32][2];
+    static_assert(sizeof(buf) <= kDeclared, "what a launch allows for");
     extern __shared__ __align__(16) char shared[];
     TeamSum<V::LANES, NTH> sum(buf, t.lanes);
     const Place<V> at(p, t);
@@ -159,7 +160,7 @@ cudaError_t launch_bwd(const NormParams& p, cudaStream_t st) {
         constexpr int join = V::NTH * 8;  // (the joining of the rows' sums, where they are in registers)
         constexpr int smem = V::kSharedSums ? M::kRings + M::kSums : M::kRings > join ? M::kRings : join;
         static std::atomic<uint64_t> allowed;
-        cudaError_t e = allow_shared(kern, smem, allowed);
+        cudaError_t e = allow_shared(kern, kDeclared, smem, allowed);
         if (e != cudaSuccess) return e;
         const Teams t = teams_of<V>(p);
         const dim3 grid = grid_of<V>(p, t, V::kBwd);

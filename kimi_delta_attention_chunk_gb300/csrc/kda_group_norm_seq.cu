@@ -17,6 +17,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kPieces = 32;                   // row pieces of a block, side by side
 constexpr int kSubs = kThreads / kPieces;     // rows of a block at a time
+constexpr int kDeclared = 16 * 1024;          // shared memory that a kernel declares, at most
 constexpr int kBatches = 3;                   // batches of a thread's rows under way, the one at hand among them
 
 struct Cut {
@@ -191,6 +192,7 @@ __global__ void __launch_bounds__(kThreads, 3) seq_moments_kernel(NormParams p, 
     constexpr int ROWS = kFwdRows<VEC>;
     extern __shared__ __align__(16) char shared[];
     __shared__ Moments join[N2][kThreads];
+    static_assert(sizeof(join) <= kDeclared, "what a launch allows for");
     const Ring<T, VEC, ROWS> ring(shared);
     const int piece = threadIdx.x % kPieces, sub = threadIdx.x / kPieces, c = (blockIdx.x * kPieces + piece) * VEC;
     const bool on = c < p.C;
@@ -413,6 +415,7 @@ __global__ void __launch_bounds__(kThreads, 2) seq_grads_kernel(NormParams p, Se
     const Ring<T, VEC, ROWS> ring(shared);
     const Ring<TG, VEC, ROWS> ring_dy(shared + ring.kBytes);
     __shared__ f2 join[N2][kThreads];
+    static_assert(sizeof(join) <= kDeclared, "what a launch allows for");
     const int piece = threadIdx.x % kPieces, sub = threadIdx.x / kPieces, c = (blockIdx.x * kPieces + piece) * VEC;
     const bool on = c < p.C;
     const int cc = on ? c : 0;
@@ -588,7 +591,7 @@ cudaError_t launch_stats(const NormParams& p, const SeqMap& m, const Cut& q, flo
     const auto kern = seq_moments_kernel<T, VEC>;
     constexpr int smem = Ring<T, VEC, kFwdRows<VEC>>::kBytes;
     static std::atomic<uint64_t> allowed;
-    cudaError_t e = allow_shared(kern, smem, allowed);
+    cudaError_t e = allow_shared(kern, kDeclared, smem, allowed);
     if (e != cudaSuccess) return e;
     kern<<<dim3(blocks_of(p, VEC), q.runs), kThreads, smem, st>>>(p, m, q.run, pieces);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
@@ -607,7 +610,7 @@ cudaError_t launch_fwd(const NormParams& p, cudaStream_t st) {
     const auto kern = seq_apply_kernel<T, VEC>;
     constexpr int smem = Ring<T, VEC, kFwdRows<VEC>>::kBytes;
     static std::atomic<uint64_t> allowed;
-    if ((e = allow_shared(kern, smem, allowed)) != cudaSuccess) return e;
+    if ((e = allow_shared(kern, 0, smem, allowed)) != cudaSuccess) return e;
     return tc::launch_dependent(kern, dim3(blocks_of(p, VEC), q.runs), kThreads, smem, st, p, m, q.run, (const float*)stats);
 }
 
@@ -630,8 +633,8 @@ cudaError_t launch_bwd(const NormParams& p, cudaStream_t st) {
     const auto dx = seq_dx_kernel<T, TG, VEC>;
     constexpr int smem = Ring<T, VEC, kBwdRows<VEC>>::kBytes + Ring<TG, VEC, kBwdRows<VEC>>::kBytes;
     static std::atomic<uint64_t> grads_allowed, dx_allowed;
-    cudaError_t e = allow_shared(grads, smem, grads_allowed);
-    if (e == cudaSuccess) e = allow_shared(dx, smem, dx_allowed);
+    cudaError_t e = allow_shared(grads, kDeclared, smem, grads_allowed);
+    if (e == cudaSuccess) e = allow_shared(dx, 0, smem, dx_allowed);
     if (e != cudaSuccess) return e;
     if (p.stats) {  // the call's first kernel: it waits for whatever made its inputs
         grads<<<grid, kThreads, smem, st>>>(p, m, q.run, stats, pieces, per_run);

@@ -17,6 +17,8 @@ namespace kda {
 
 namespace {
 
+constexpr int kDeclared = 512;  // shared memory that a kernel declares, at most
+
 // Which channels and rows the threads of a block have.
 struct Teams {
     int lanes;    // of a team: a power of two up to 32, or whole warps
