@@ -584,6 +584,7 @@ int64_t most_runs(const NormParams& p) {
     return most;
 }
 size_t pieces_bytes(const NormParams& p) { return (size_t)(((most_runs(p) + p.N) * 2 * p.C * 4 + 255) / 256 * 256); }
+size_t per_run_bytes(const NormParams& p) { return (size_t)((most_runs(p) * 2 * p.C * 4 + 255) / 256 * 256); }
 size_t stats_bytes(const NormParams& p) { return (size_t)(((int64_t)p.N * p.G * 8 + 255) / 256 * 256); }
 
 template <typename T, int VEC>
@@ -621,7 +622,7 @@ cudaError_t launch_bwd(const NormParams& p, cudaStream_t st) {
     char* at = static_cast<char*>(p.ws);
     float* const pieces = reinterpret_cast<float*>(at);
     float* const per_run = reinterpret_cast<float*>(at += pieces_bytes(p));
-    float* const means = reinterpret_cast<float*>(at += pieces_bytes(p));
+    float* const means = reinterpret_cast<float*>(at += per_run_bytes(p));
     float* stats = p.stats;
     if (!stats) {
         stats = reinterpret_cast<float*>(at + stats_bytes(p));
@@ -656,7 +657,7 @@ cudaError_t launch_bwd(const NormParams& p, cudaStream_t st) {
 size_t group_norm_fwd_workspace(const NormParams& p) { return p.over_sequence ? pieces_bytes(p) + (p.stats ? 0 : stats_bytes(p)) : 0; }
 size_t group_norm_bwd_workspace(const NormParams& p) {
     if (!p.over_sequence) return norm_token_bwd_workspace(p);
-    return 2 * pieces_bytes(p) + (p.stats ? 1 : 2) * stats_bytes(p);
+    return pieces_bytes(p) + per_run_bytes(p) + (p.stats ? 1 : 2) * stats_bytes(p);
 }
 
 cudaError_t group_norm_fwd(kda_dtype dt, const NormParams& p, cudaStream_t st) {
