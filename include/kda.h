@@ -671,9 +671,12 @@ KDA_API kda_status kda_gated_scan_fwd(const void *x, int64_t ldx, const void *r,
  *  states   what the forward call on the same inputs left, or NULL (made again in the workspace:
  *           x, r and i are then read twice).
  *  workspace  at least kda_gated_scan_bwd_workspace_size bytes, 16-byte aligned.
- * Sums are fp32, in an order fixed by the sizes and the offsets.  Rows that belong to no sequence
- * have zeros in dx, dr, di and dz, whatever they hold.  Where 1 - a^2 is below 1e-36, 1 / m is taken as 1e18.  The
- * rest as kda_gated_scan_fwd.
+ * Sums are fp32, in an order fixed by the sizes, the offsets, the alignment of the rows (base
+ * addresses and strides) and the device: the same call on the same addresses has the same bits every
+ * time, the same values in rows of another alignment, or on another kind of device, may differ in
+ * their roundings (the outputs of kda_gated_scan_fwd too).  Rows that belong to no sequence have
+ * zeros in dx, dr, di and dz, whatever they hold.  Where 1 - a^2 is below 1e-36, 1 / m is taken as
+ * 1e18.  The rest as kda_gated_scan_fwd.
  */
 KDA_API size_t kda_gated_scan_bwd_workspace_size(int B, int T, int C, int N, int packed, int have_states);
 KDA_API kda_status kda_gated_scan_bwd(const void *x, int64_t ldx, const void *r, int64_t ldr, const void *i,
@@ -731,7 +734,9 @@ KDA_API kda_status kda_group_norm_fwd(const void *x, int64_t ldx, const float *w
  *  stats    over sequences: what the forward call on the same inputs left, or NULL (x is then read
  *           once more).
  *  workspace  at least kda_group_norm_bwd_workspace_size bytes, 16-byte aligned.
- * Sums are fp32, in an order fixed by the sizes.  The dx of rows that belong to no sequence is
+ * Sums are fp32, in an order fixed by the sizes, the offsets and the alignment of the rows (base
+ * addresses and strides), so that the same values in rows of another alignment may differ in their
+ * roundings (the outputs of kda_group_norm_fwd too).  The dx of rows that belong to no sequence is
  * zero, whatever they hold.  The rest as kda_group_norm_fwd.
  */
 KDA_API size_t kda_group_norm_bwd_workspace_size(int B, int T, int C, int G, int N, int over_sequence, int packed,
