@@ -297,9 +297,9 @@ __device__ __forceinline__ bool any_longer(const GatedParams& p, int most) {
 // tokens), or one of them alone would take them more than twice as many steps as the stream takes as a whole, at `pace` and `stream` tokens a
 // step.  Only the offsets say so, on the device: both kernels are launched.  A long sequence's own blocks return at once, and the stream's kernel,
 // behind them, looks for one and does everything again or nothing (a block that has one sequence does not look at all the others).
-// (bf16 with gates, 4096 channels, forward and backward: 16 sequences of 1 to 700 tokens 67 and 108 us with blocks of their own, 80 and 154 as one
-// stream; 128 x 128 151 and 293, 256 and 580; 256 x 64 302 and 336, 278 and 600; 512 x 32 591 and 451, 282 and 606; 1024 x 16 1169 and 817, 287 and
-// 667; one of 16129 among 15 of 17 362 and 1141, 185 and 410)
+// (bf16 with gates, 4096 channels, decays of 0.9 to 0.999, forward and backward: 16 sequences of 1 to 700 tokens 61 and 105 us with blocks of their own,
+// 77 and 156 as one stream; 128 x 128 139 and 266, 242 and 572; 256 x 64 282 and 308, 263 and 595; 512 x 32 574 and 410, 269 and 596; 1024 x 16
+// 1146 and 704, 273 and 659; one of 16129 among 15 of 17 302 and 1051, 172 and 398, and as chosen, with the look for it, 197 and 417)
 inline bool gated_each(const GatedParams& p, int mean) { return p.cu && p.N > 0 && p.N <= p.T / mean; }
 inline int longest_of(const GatedParams& p, int64_t pace, int64_t stream) {
     const int64_t most = (p.T + stream - 1) / stream * 2 * pace;
@@ -312,10 +312,13 @@ cudaError_t gated_cluster(ClusterRoom& room, K kern, int64_t groups, int T, int 
     return groups > kSms ? cudaSuccess : room.size_for(kern, groups, T, tile, threads, smem, cluster);
 }
 
-// Channels of a block. 64 where blocks of them that take a whole sequence each come to one and a half an SM; else 32 where those do
-// (2 x 8192 x 4096 bf16 forward 148 -> 136 us, backward 2 x 2048 x 4096 86 -> 75); else blocks share a sequence as a cluster whatever
-// their width, and the widest rows cost least (1 x 16384 x 4096: 151, 155 and 171 us with 64, 32 and 16) as long as clusters of eight
-// fill the machine (1 x 65536 x 512: 213, 155, 104).
+// Channels of a block. 64 where blocks of them that take a whole sequence each come to one and a half an SM (two run on one); else 32 where
+// those do; else blocks share a sequence as a cluster whatever their width, and the widest rows cost least (1 x 16384 x 4096: 151, 155 and
+// 171 us with 64, 32 and 16) as long as clusters of eight fill the machine (1 x 65536 x 512: 213, 155, 104).
+// bf16 with gates, 4096 channels, B sequences of 2048, forward and backward with 64 | 32 | 16 channels:
+//     2: 41.5 and 91.5 | 37.7 and 74.0 | 48.5 and 87.6      3: 66.8 and 137 | 56.6 and 115 | 68.9 and 127     4: 66.8 and 138 | 71.4 and 144 | 84.2 and 150
+//     5: 98.2 and 216 | 88.3 and 180 | 104 and 189          7: 100 and 219 | 106 and 212 | 140 and 250        9: 127 and 269 | 136 and 279 | 180 and 326
+// (5 sequences come to 320 blocks of 64 channels for 304 places, a second filling for sixteen: there the rule does not choose the best.)
 inline int gated_channels(const GatedParams& p, int streams) {
     for (const int blocks : {1, kMostCluster})
         for (const int ch : {64, 32})

@@ -1,17 +1,22 @@
 // Gated linear recurrence over prompts: forward (the formulas stand in kda_gated.cuh).
 //
-// An element costs 2 bytes of x, r, i, z and y each in bf16, four exponentials, two reciprocals and a root: HBM and instruction issue
-// are near one another.  The recurrence is affine in h, so tokens are taken a tile at a time by a whole block: a lane has a strip
-// of the tile's tokens and a pair of channels, whose decays and inputs stay in registers; the strips' maps h -> A h + H are folded over
-// a warp by shuffles and over the block in shared memory, and every lane walks its tokens once more (one multiply-add each) from the true
-// state.  Every row is read once, by asynchronous copies of the warp that works on it, a tile ahead.
+// An element costs 2 bytes of x, r, i, z and y each in bf16, three exponentials (a fourth where rates are large), three reciprocals and a root
+// (one exponential and one reciprocal fewer without z): HBM, instruction issue and the special functions are near one another.  The
+// recurrence is affine in h, so tokens are taken a tile at a time by a whole block: a lane has a strip of the tile's tokens and a pair of
+// channels, whose decays and inputs stay in registers; the strips' maps h -> A h + H are folded over a warp by shuffles and over the block
+// in shared memory, and every lane walks its tokens once more (one multiply-add each) from the true state.  Every row is read once, by
+// asynchronous copies of the warp that works on it, a tile ahead.
 // A block has 64, 32 or 16 channels of one sequence and the machine is filled with sequences and channels as far as these go (gated_channels);
 // where they do not, up to eight blocks of a cluster take consecutive tiles and hand their tiles' maps to one another through
 // distributed shared memory: one cluster barrier a tile, nothing read twice, sums in a fixed order.  Sequences that are packed have blocks
 // of their own or are walked as one stream with maps that are cut where one begins (gated_each).
-// bf16 with gates, 4096 channels: 7 x 2048 tokens in 100 us (88% of the bytes at the copy rate), 2 x 8192 in 136 (74%), one of 16384, four
-// blocks to a cluster, in 151 (67%; a barrier of the cluster and a fold of four tiles every 512 tokens).  Two blocks of 128 registers a thread fill an SM:
-// 16 warps that issue 2.0 instructions a cycle, waiting on one another's latencies and on the shared-memory queue.
+// bf16 with gates, 4096 channels, decays of 0.9 to 0.999: 7 x 2048 tokens in 100 us (88% of the bytes at the copy rate), 2 x 8192 in 138 (73%),
+// one of 16384, four blocks to a cluster, in 150 (67%; a barrier of the cluster and a fold of four tiles every 512 tokens); with decays of 0.1
+// to 0.7 (rates above 1/4) 115 and 169.  Leaving `states` adds 1 to 2 us.  fp32: 4 x 2048 in 99 (all of the copy rate).
+// Two blocks of 128 registers a thread fill an SM: 16 warps that issue 2.0 instructions a cycle.  They wait on fixed latencies (1.1 cycles an
+// instruction) and on the queue to shared memory and the special functions (1.0): seven special functions an element keep their pipe busy 51%
+// of the time, 60% on the busiest SMs.  And 2 x 4096 tokens come to 256 blocks for 304 places: 104 SMs have two and 48 have one, active for
+// 92,000 to 144,000 cycles, 127,000 on average.
 // Slower when built: a warp of its own that folds while others work ahead (189), the exchange behind the next tile's gates
 // (226: twice the code, and it waits for instructions), strips of 8 tokens with three blocks an SM (180), the output gates computed
 // while the maps travel (160), maps that are padded with identities instead of tested (158).

@@ -11,7 +11,9 @@
 // element needs (a, u, m si, si x a^2 / m, sr, 1 - si, yb, dy silu'(z)) stays in registers between the two walks: 128 a thread, two blocks an
 // SM, whose 16 warps issue 2.2 instructions a cycle: that and their latencies bound it.  Without the states a first pass of the forward kernel makes them (x, r and i are then
 // read twice).  dlam's sums over tokens: one partial sum a block, added in a fixed order.
-// bf16 with gates, 4096 channels: 4 x 2048 tokens in 137 us (67% of the bytes at the copy rate), 2 x 2048 in 74 (61%).
+// bf16 with gates, 4096 channels: 4 x 2048 tokens in 138 us (66% of the bytes at the copy rate), 2 x 2048 in 74 (62%; rates above 1/4: 77), whose
+// 256 blocks for 304 places leave 48 SMs with one: active for 96,000 to 146,000 cycles, 129,000 on average.  4 x 2048 with fp32 gradients
+// 157 (90%), in fp32 206 (88%), with nothing kept 188 (bf16) and 258 (fp32).
 // Slower when built: a tile's map sent before the rest is computed (92 for 89 then), the maps' lengths tested instead of padded with identities (100).
 #include <algorithm>
 #include <type_traits>

@@ -5,7 +5,7 @@
 // along a row, and a block walks down the rows with its weights, and backwards its share of dw and db, in registers.  Mean, then the
 // sum of squares around it: two sums over a team, by shuffles up to 32 lanes and through shared memory beyond.  Groups of up to
 // 16384 channels fit a block.
-// bf16 with SiLU, 4096 x 12288: 96 groups of 128 channels 35 us forwards (86% of the bytes at the copy rate) and 66 backwards (69%: 30
+// bf16 with SiLU, 4096 x 12288: 96 groups of 128 channels 36 us forwards (84% of the bytes at the copy rate) and 66.5 backwards (68%: 30
 // instructions an element at 2.6 a cycle, of 24 warps); one group 88 and 176, where a row's sums wait for one another.
 #pragma once
 
