@@ -645,7 +645,8 @@ KDA_API kda_status kda_ssm_scan_bwd(const void *u, int64_t ldu, const void *delt
  *  initial_state fp32 [N, C] or NULL for zeros; final_state the same or NULL (of a sequence
  *           without tokens: its initial state); they must not overlap.
  *  cu_seqlens, B, T, N   as kda_short_conv_fwd; rows that belong to no sequence are left as
- *           they are.
+ *           they are.  A state that is not finite stays so, infinite or NaN, to the end of its
+ *           sequence, and other sequences are without it.
  *  states   fp32 [B, ceil(T / 32), C] or NULL: the state before tokens 0, 32, 64 ... of each
  *           batch row (zeros where a sequence begins; left as it is before tokens that belong
  *           to no sequence), for kda_gated_scan_bwd.
